@@ -49,8 +49,11 @@ typedef enum {
                        |v| >= 65520: past the fp16 range of its P.V product */
   FS_ERR_SCRATCH_LIMIT = 6, /* fs_prune_cells_static: the shape needs more
                                than its fixed scratch array */
-  FS_ERR_STATE = 7 /* fs_decode_step: the decode state is not at the step's
-                      position t */
+  FS_ERR_STATE = 7, /* fs_decode_step: the decode state is not at the step's
+                       position t */
+  FS_ERR_CACHE = 8 /* a cache call met a position past the page table, a page
+                      number outside the cache or an index outside its list;
+                      the rows concerned were skipped */
 } fs_status;
 
 typedef enum { FS_BF16 = 0, FS_FP32 = 1 } fs_dtype;
@@ -438,6 +441,173 @@ int fs_workspace_view(int batch, int H, int N, int d, const fs_params *p,
                       int dtype, size_t *off_kbar, size_t *off_amax,
                       size_t *off_pool, size_t *off_pool_count,
                       size_t *off_sel);
+
+/* ---------------------------------------------------------------------------
+ * Rotary positions as a call of their own (the window branch of the forward
+ * rotates inside its kernels: paper.rainbus.top summary, 前置知识, RoPE).  The
+ * pages give one form; the layouts, the part of the head and the scalings for
+ * long contexts below are library additions.
+ *
+ * With r = rot rotated elements of a head, pair i (0 <= i < r/2) is
+ *   FS_ROPE_HALF   elements i and i + r/2        FS_ROPE_PAIRS  2i and 2i + 1
+ * and turns by pos * f_i; elements r .. d-1 pass through unchanged:
+ *   y_a = m (x_a cos - x_b sin),  y_b = m (x_b cos + x_a sin).
+ * Frequencies, f_i = base^(-2i/r) before scaling:
+ *   FS_ROPE_PLAIN   f_i
+ *   FS_ROPE_LINEAR  f_i / factor
+ *   FS_ROPE_BASE    f_i with base * factor^(r / (r - 2))          (r > 2)
+ *   FS_ROPE_RAMP    f_i (1 - g_i) + f_i / factor * g_i, where g_i rises from 0
+ *                   to 1 over i = lo .. hi: the pairs that make beta_fast and
+ *                   beta_slow turns in `original` tokens,
+ *                   lo = floor, hi = ceil of r ln(original / (2 pi beta)) /
+ *                   (2 ln base), kept within 0 .. r/2 - 1
+ * m is `amplitude`.  Angles are exact for every 32-bit position: pos * f_i is
+ * taken modulo one turn in 64-bit fixed point. */
+typedef enum { FS_ROPE_HALF = 0, FS_ROPE_PAIRS = 1 } fs_rope_layout;
+typedef enum {
+  FS_ROPE_PLAIN = 0,
+  FS_ROPE_LINEAR = 1,
+  FS_ROPE_BASE = 2,
+  FS_ROPE_RAMP = 3
+} fs_rope_scaling;
+#define FS_ROPE_MAX_ROT 256
+typedef struct {
+  int rot;              /* even, 2 .. 256                                     */
+  int layout, scaling;  /* fs_rope_layout, fs_rope_scaling                    */
+  int original;         /* RAMP: tokens that the model was trained on         */
+  double base, factor;
+  double beta_fast, beta_slow; /* RAMP: turns within `original`               */
+  double amplitude;
+} fs_rope_params;
+/* A model's frequencies, worked out once on the host. */
+typedef struct {
+  int rot, layout;
+  float amplitude;
+  int reserved;
+  uint64_t turns[FS_ROPE_MAX_ROT / 2]; /* f_i / (2 pi) as a fraction of 2^64  */
+} fs_rope_plan;
+/* Host only.  FS_ERR_INVALID_ARG for an odd or non-positive rot, an unknown
+ * layout or scaling, base <= 1, factor < 1, a non-finite or negative
+ * amplitude, RAMP with original < 1 or beta_fast < beta_slow or beta_slow <= 0,
+ * BASE with rot 2; FS_ERR_UNSUPPORTED for rot > 256. */
+int fs_rope_make_plan(const fs_rope_params *p, fs_rope_plan *plan);
+
+/* Rotates q and, in the same launch, k (NULL with Hk = 0 for q alone).
+ *   q, k            [batch, Hq | Hk, N, d] of `dtype` (FS_BF16 or FS_FP32), d
+ *                   even, d >= plan->rot, batch * N * d < 2^32; q_strides, k_strides: elements between
+ *                   batches, heads and tokens (NULL: contiguous); the d values
+ *                   of a head lie together
+ *   q_out, k_out    the same shapes and type, with their own strides; each may
+ *                   be its input with the input's strides (in place); other
+ *                   overlaps give undefined results
+ *   pos             int32 positions: token n of batch b is at
+ *                   pos[b * pos_stride + n] (pos_stride N, or 0 for positions
+ *                   that all batches share); NULL: positions pos0 + n
+ *   inverse         0, or 1 for the transposed rotation: the gradient of q
+ *                   from the gradient of q_out
+ * Computed in fp32, rounded once.  Enqueues one kernel on `stream`. */
+int fs_rope(const void *q, void *q_out, int Hq, const long long *q_strides,
+            const long long *q_out_strides, const void *k, void *k_out, int Hk,
+            const long long *k_strides, const long long *k_out_strides,
+            int dtype, int batch, int N, int d, const int32_t *pos,
+            long long pos_stride, int pos0, const fs_rope_plan *plan,
+            int inverse, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * A paged key/value cache (no counterpart on the pages: it serves layers whose
+ * cache grows, next to the bounded decode state above).
+ *
+ * A row is the d values of one token, one kv head, key or value.  It is held
+ * as bf16, or as codes of 8 or 4 bits with one fp32 scale:
+ *   scale = amax / Q,  code = round(Q x / amax), ties to even,
+ *   amax = max |x| over the row; Q = 448 (e4m3), 127 (int8), 7 (int4)
+ * exactly: the quotient is never rounded across a border between two codes.  A
+ * row of zeros has scale 0.  A row with a NaN or an infinity has codes 0 and
+ * scale NaN and reads back as NaN throughout (bf16 keeps values as they are).
+ *   codes   [pages, 2 (key, value), Hkv, page, fs_cache_row_bytes] bytes; int4
+ *           holds elements 2i and 2i + 1 in the low and high half of byte i
+ *   scales  [pages, 2, Hkv, page] f32 (NULL for FS_CACHE_BF16)
+ *   table   [batch, max_pages] int32: token t of sequence b is row t % page of
+ *           page table[b, t / page]; entries that no position reaches may hold
+ *           anything
+ *   status  device int: a call that meets a position past the table or a page
+ *           outside 0 .. pages-1 skips those rows and records FS_ERR_CACHE
+ *           here (fs_check_status reads it).  The caller zeroes it; no call
+ *           clears it.  May be NULL.
+ * page: 16, 32, 64, 128 or 256; d: 64 or 128; codes 16-byte aligned; other
+ * sizes give FS_ERR_UNSUPPORTED (non-positive ones FS_ERR_INVALID_ARG).
+ * Sequences may share pages to read; two that write one row race. */
+typedef enum {
+  FS_CACHE_BF16 = 0,
+  FS_CACHE_E4M3 = 1,
+  FS_CACHE_INT8 = 2,
+  FS_CACHE_INT4 = 3
+} fs_cache_format;
+typedef struct {
+  void *codes;
+  float *scales;
+  const int32_t *table;
+  int *status;
+  int pages, page, Hkv, d;
+  int format; /* fs_cache_format */
+  int batch, max_pages;
+} fs_cache;
+/* Bytes of one row's codes; 0 for a d or format that the cache does not have. */
+size_t fs_cache_row_bytes(int d, int format);
+
+/* Writes T new tokens of every sequence: token t goes to position start[b] + t.
+ *   k, v          [batch, Hkv, T, d] bf16; strides as fs_rope's (multiples of
+ *                 8 elements and 16-byte aligned pointers, else
+ *                 FS_ERR_UNSUPPORTED)
+ *   start, count  [batch] int32; tokens t >= count[b] are not written (count
+ *                 NULL: all T are) */
+int fs_cache_append(const fs_cache *cache, const void *k, const void *v,
+                    const long long *k_strides, const long long *v_strides,
+                    int T, const int32_t *start, const int32_t *count,
+                    void *stream);
+
+/* Reads T tokens of every sequence from position start[b] on, as code * scale
+ * rounded to `dtype` (FS_BF16 or FS_FP32), into contiguous k, v
+ * [batch, Hkv, T, d], 16-byte aligned: what fs_attention_fwd, fs_cell_summarize
+ * and fs_decode_state_init take.  Rows t >= count[b] are left as they were. */
+int fs_cache_read(const fs_cache *cache, const int32_t *start,
+                  const int32_t *count, int T, int dtype, void *k, void *v,
+                  void *stream);
+
+/* After the verification of drafted tokens that lie at positions start[b] + j:
+ * the row at start[b] + path[b, i] moves to start[b] + i for i < count[b] (all
+ * A without a count).  All sources are read before any row is written, so the
+ * path may hold any indices 0 <= path < 64, also repeated ones.  A <= 64. */
+int fs_cache_accept(const fs_cache *cache, const int32_t *start,
+                    const int32_t *path, const int32_t *count, int A,
+                    void *stream);
+
+/* Attention of T drafted tokens of every sequence over its cache.  The drafted
+ * tokens' keys and values lie in the cache at positions past[b] .. past[b] +
+ * count[b] - 1, behind the past[b] tokens of the prefix.  Row i of sequence b
+ * sees the prefix and the drafted tokens j < count[b] whose bit j of tree[b, i]
+ * is set (itself, if it is to see itself); with T = 1 it is a step of plain
+ * decoding:
+ *   out = sum p v / sum p,  p = exp(scale q . k)  over what the row sees,
+ * zeros where a row sees nothing.
+ *   q, out  [batch, H, T, d] bf16; H a multiple of the cache's Hkv, query head
+ *           h reading kv head h / (H / Hkv)
+ *   past    [batch] int32; count [batch] int32 or NULL (all T); rows
+ *           i >= count[b] of out are left as they were
+ *   tree    [batch, T] 64-bit masks, or NULL: row i sees the drafted 0 .. i
+ *   window  0, or w >= 64: of the prefix, row i sees the positions above
+ *           past[b] + (number of drafted tokens it sees) - 1 - w, so that a
+ *           token whose bits are itself and its ancestors sees the last w
+ *           positions, itself included
+ * T <= 64.  ws: device workspace of fs_tree_workspace_bytes() bytes for one
+ * call at a time.  Rows of a sequence with a position past the table or a page
+ * outside the cache see only what can be read (and the cache's status says
+ * so).  Deterministic. */
+size_t fs_tree_workspace_bytes(const fs_cache *cache, int H, int T);
+int fs_tree_attn(const void *q, const fs_cache *cache, const int32_t *past,
+                 const int32_t *count, const int64_t *tree, int H, int T,
+                 int window, float scale, void *out, void *ws,
+                 size_t ws_bytes, void *stream);
 
 #ifdef __cplusplus
 }

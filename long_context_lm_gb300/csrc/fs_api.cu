@@ -187,6 +187,9 @@ const char *fs_status_string(int status) {
       return "shape needs more scratch than the static array holds "
              "(4 MiB: batch*H*ceil(N/2048) <= 4096)";
     case FS_ERR_STATE: return "the decode state is not at the step's position";
+    case FS_ERR_CACHE:
+      return "a position past the page table, a page outside the cache or an index outside its "
+             "list: the rows concerned were skipped";
     default: return "unknown status";
   }
 }
@@ -811,6 +814,200 @@ extern "C" int fs_decode_step(const void *q_t, const void *k_t, const void *v_t,
   a.out = out_t;
   a.sel_out = sel_t;
   return status_of(launch_decode(a, static_cast<cudaStream_t>(stream)));
+}
+
+// ---------------------------------------------------------------------------
+// Rotary positions, the paged cache and attention of drafted tokens.
+// ---------------------------------------------------------------------------
+extern "C" int fs_rope_make_plan(const fs_rope_params *p, fs_rope_plan *plan) {
+  if (!p || !plan) return FS_ERR_INVALID_ARG;
+  return rope_make_plan(*p, plan);
+}
+
+namespace {
+
+// Strides of [batch, H, N, d], given or contiguous.
+void set_strides(long long (&to)[3], const long long *given, int H, long long N, int d) {
+  if (given) {
+    for (int i = 0; i < 3; ++i) to[i] = given[i];
+    return;
+  }
+  to[0] = H * N * d;
+  to[1] = N * d;
+  to[2] = d;
+}
+
+int check_cache(const fs_cache *c) {
+  if (!c || c->pages < 1 || c->page < 1 || c->Hkv < 1 || c->batch < 1 || c->max_pages < 1)
+    return FS_ERR_INVALID_ARG;
+  if (c->d < 1 || c->format < FS_CACHE_BF16 || c->format > FS_CACHE_INT4) return FS_ERR_INVALID_ARG;
+  if (c->page != 16 && c->page != 32 && c->page != 64 && c->page != 128 && c->page != 256)
+    return FS_ERR_UNSUPPORTED;
+  if (c->d != 64 && c->d != 128) return FS_ERR_UNSUPPORTED;
+  if ((long long)c->batch * c->Hkv > 65535) return FS_ERR_UNSUPPORTED;
+  return FS_OK;
+}
+
+// A cache that a kernel may be handed.
+int check_cache_memory(const fs_cache *c) {
+  FS_TRY(check_cache(c));
+  if (!c->codes || !c->table || (c->format != FS_CACHE_BF16 && !c->scales)) return FS_ERR_INVALID_ARG;
+  return reinterpret_cast<uintptr_t>(c->codes) % 16 ? FS_ERR_UNSUPPORTED : FS_OK;
+}
+
+// T new rows a sequence and head; one thread handles eight elements.
+int check_rows(const fs_cache *c, int T) {
+  if (T < 1) return FS_ERR_INVALID_ARG;
+  return (long long)c->batch * c->Hkv * 2 * T * (c->d / 8) >= (1ll << 32) - 256 ? FS_ERR_UNSUPPORTED
+                                                                               : FS_OK;
+}
+
+}  // namespace
+
+extern "C" int fs_rope(const void *q, void *q_out, int Hq, const long long *q_strides,
+                       const long long *q_out_strides, const void *k, void *k_out, int Hk,
+                       const long long *k_strides, const long long *k_out_strides, int dtype,
+                       int batch, int N, int d, const int32_t *pos, long long pos_stride, int pos0,
+                       const fs_rope_plan *plan, int inverse, void *stream) {
+  FS_TRY(check_dtype(dtype));
+  if (!q || !q_out || !plan || Hq < 1 || Hk < 0 || batch < 1 || N < 1 || d < 2 || d % 2)
+    return FS_ERR_INVALID_ARG;
+  if ((Hk > 0) != (k != nullptr) || (Hk > 0) != (k_out != nullptr)) return FS_ERR_INVALID_ARG;
+  if (plan->rot < 2 || plan->rot % 2 || plan->rot > FS_ROPE_MAX_ROT || plan->rot > d)
+    return FS_ERR_INVALID_ARG;
+  if (plan->layout != FS_ROPE_HALF && plan->layout != FS_ROPE_PAIRS) return FS_ERR_INVALID_ARG;
+  if (pos_stride < 0 || (inverse != 0 && inverse != 1)) return FS_ERR_INVALID_ARG;
+  if ((long long)batch * N >= (1ll << 32) / d || Hq > 65535 || Hk > 65535 - Hq)
+    return FS_ERR_UNSUPPORTED;
+  const size_t align = dtype == FS_FP32 ? 4 : 2;
+  for (const void *p : {q, (const void *)q_out, k, (const void *)k_out})
+    if (reinterpret_cast<uintptr_t>(p) % align) return FS_ERR_INVALID_ARG;
+  RopeArgs a{};
+  a.x[0] = q;
+  a.y[0] = q_out;
+  a.H[0] = Hq;
+  set_strides(a.xs[0], q_strides, Hq, N, d);
+  set_strides(a.ys[0], q_out_strides, Hq, N, d);
+  a.x[1] = k;
+  a.y[1] = k_out;
+  a.H[1] = Hk;
+  set_strides(a.xs[1], k_strides, Hk, N, d);
+  set_strides(a.ys[1], k_out_strides, Hk, N, d);
+  a.f32 = dtype == FS_FP32;
+  a.batch = batch;
+  a.N = N;
+  a.d = d;
+  a.pos = pos;
+  a.pos_stride = pos_stride;
+  a.pos0 = pos0;
+  a.inverse = inverse;
+  a.plan = plan;
+  return status_of(launch_rope(a, static_cast<cudaStream_t>(stream)));
+}
+
+extern "C" size_t fs_cache_row_bytes(int d, int format) {
+  if (d != 64 && d != 128) return 0;
+  switch (format) {
+    case FS_CACHE_BF16: return (size_t)d * 2;
+    case FS_CACHE_E4M3:
+    case FS_CACHE_INT8: return (size_t)d;
+    case FS_CACHE_INT4: return (size_t)d / 2;
+    default: return 0;
+  }
+}
+
+extern "C" int fs_cache_append(const fs_cache *cache, const void *k, const void *v,
+                               const long long *k_strides, const long long *v_strides, int T,
+                               const int32_t *start, const int32_t *count, void *stream) {
+  FS_TRY(check_cache_memory(cache));
+  if (!k || !v || !start) return FS_ERR_INVALID_ARG;
+  FS_TRY(check_rows(cache, T));
+  CacheRowsArgs a{};
+  a.c = *cache;
+  a.k = k;
+  a.v = v;
+  set_strides(a.ks, k_strides, cache->Hkv, T, cache->d);
+  set_strides(a.vs, v_strides, cache->Hkv, T, cache->d);
+  for (int i = 0; i < 3; ++i)
+    if (a.ks[i] % 8 || a.vs[i] % 8) return FS_ERR_UNSUPPORTED;
+  if ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) % 16)
+    return FS_ERR_UNSUPPORTED;
+  a.start = start;
+  a.count = count;
+  a.T = T;
+  return status_of(launch_cache_append(a, static_cast<cudaStream_t>(stream)));
+}
+
+extern "C" int fs_cache_read(const fs_cache *cache, const int32_t *start, const int32_t *count,
+                             int T, int dtype, void *k, void *v, void *stream) {
+  FS_TRY(check_cache_memory(cache));
+  FS_TRY(check_dtype(dtype));
+  if (!k || !v || !start) return FS_ERR_INVALID_ARG;
+  FS_TRY(check_rows(cache, T));
+  if ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) % 16)
+    return FS_ERR_UNSUPPORTED;
+  CacheRowsArgs a{};
+  a.c = *cache;
+  a.k_out = k;
+  a.v_out = v;
+  a.f32 = dtype == FS_FP32;
+  a.start = start;
+  a.count = count;
+  a.T = T;
+  return status_of(launch_cache_read(a, static_cast<cudaStream_t>(stream)));
+}
+
+extern "C" int fs_cache_accept(const fs_cache *cache, const int32_t *start, const int32_t *path,
+                               const int32_t *count, int A, void *stream) {
+  FS_TRY(check_cache_memory(cache));
+  if (!start || !path || A < 1) return FS_ERR_INVALID_ARG;
+  if (A > 64) return FS_ERR_UNSUPPORTED;
+  CacheRowsArgs a{};
+  a.c = *cache;
+  a.start = start;
+  a.count = count;
+  a.path = path;
+  a.T = A;
+  return status_of(launch_cache_accept(a, static_cast<cudaStream_t>(stream)));
+}
+
+namespace {
+int check_tree(const fs_cache *c, int H, int T) {
+  FS_TRY(check_cache(c));
+  if (H < 1 || T < 1 || H % c->Hkv) return FS_ERR_INVALID_ARG;
+  if (T > 64 || H > 65535 || (long long)c->batch * H * T >= (1ll << 31)) return FS_ERR_UNSUPPORTED;
+  return FS_OK;
+}
+}  // namespace
+
+extern "C" size_t fs_tree_workspace_bytes(const fs_cache *cache, int H, int T) {
+  return check_tree(cache, H, T) == FS_OK ? tree_workspace_bytes(*cache, H, T) : 0;
+}
+
+extern "C" int fs_tree_attn(const void *q, const fs_cache *cache, const int32_t *past,
+                            const int32_t *count, const int64_t *tree, int H, int T, int window,
+                            float scale, void *out, void *ws, size_t ws_bytes, void *stream) {
+  FS_TRY(check_cache_memory(cache));
+  FS_TRY(check_tree(cache, H, T));
+  if (!q || !past || !out || !ws || !(scale > 0.f) || !(scale <= 1e30f)) return FS_ERR_INVALID_ARG;
+  if (window < 0 || (window > 0 && window < 64)) return FS_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out) |
+       reinterpret_cast<uintptr_t>(ws)) % 16)
+    return FS_ERR_UNSUPPORTED;
+  if (ws_bytes < tree_workspace_bytes(*cache, H, T)) return FS_ERR_INVALID_ARG;
+  TreeArgs a{};
+  a.c = *cache;
+  a.q = q;
+  a.past = past;
+  a.count = count;
+  a.tree = tree;
+  a.H = H;
+  a.T = T;
+  a.window = window;
+  a.scale = scale;
+  a.out = out;
+  a.ws = ws;
+  return status_of(launch_tree(a, static_cast<cudaStream_t>(stream)));
 }
 
 namespace fs {

@@ -5,6 +5,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "fs.h"
+
 namespace fs {
 
 struct Shape {
@@ -135,5 +137,49 @@ struct BwdArgs {
 size_t backward_workspace_bytes(const Shape &sh);
 cudaError_t launch_backward(const BwdArgs &a, cudaStream_t st);
 cudaError_t launch_qkv(const QkvArgs &a, cudaStream_t st);
+
+// Rotary positions (k10_rope.cu).  Two tensors; H[i] = 0: none.  Strides in
+// elements between batches, heads and tokens.
+struct RopeArgs {
+  const void *x[2];
+  void *y[2];
+  int H[2];
+  long long xs[2][3], ys[2][3];
+  bool f32;
+  int batch, N, d;
+  const int32_t *pos;
+  long long pos_stride;
+  int pos0, inverse;
+  const fs_rope_plan *plan;
+};
+int rope_make_plan(const fs_rope_params &p, fs_rope_plan *plan);
+cudaError_t launch_rope(const RopeArgs &a, cudaStream_t st);
+
+// Paged key/value cache (k11_cache.cu).
+struct CacheRowsArgs {
+  fs_cache c;
+  const void *k, *v;   // append: bf16 rows
+  long long ks[3], vs[3];
+  void *k_out, *v_out; // read
+  bool f32;            // read: fp32 rows
+  const int32_t *start, *count, *path;
+  int T;
+};
+cudaError_t launch_cache_append(const CacheRowsArgs &a, cudaStream_t st);
+cudaError_t launch_cache_read(const CacheRowsArgs &a, cudaStream_t st);
+cudaError_t launch_cache_accept(const CacheRowsArgs &a, cudaStream_t st);
+
+// Attention of drafted tokens over the cache (k12_tree.cu).
+struct TreeArgs {
+  fs_cache c;
+  const void *q;
+  const int32_t *past, *count;
+  const int64_t *tree;
+  int H, T, window;
+  float scale;
+  void *out, *ws;
+};
+size_t tree_workspace_bytes(const fs_cache &c, int H, int T);
+cudaError_t launch_tree(const TreeArgs &a, cudaStream_t st);
 
 }  // namespace fs

@@ -21,7 +21,7 @@ import torch
 from . import build as _build
 
 (FS_OK, FS_ERR_INVALID_ARG, FS_ERR_UNSUPPORTED, FS_ERR_CUDA, FS_ERR_TIMEOUT, FS_ERR_RANGE,
- FS_ERR_SCRATCH_LIMIT, FS_ERR_STATE) = range(8)
+ FS_ERR_SCRATCH_LIMIT, FS_ERR_STATE, FS_ERR_CACHE) = range(9)
 FS_BF16, FS_FP32 = 0, 1
 FS_MODE_FSL, FS_MODE_FS, FS_MODE_FSB = 0, 1, 2
 
@@ -35,7 +35,12 @@ SYMBOLS = ["fs_default_params", "fs_status_string", "fs_last_cuda_error", "fs_wo
            "fs_window_attn_traced", "fs_decode_state_bytes", "fs_decode_state_init",
            "fs_decode_state_view", "fs_qkv_workspace_bytes", "fs_qkv_prologue",
            "fs_backward_workspace_bytes", "fs_attention_bwd",
-           "fs_fsb_workspace_bytes", "fs_fsb_select"]
+           "fs_fsb_workspace_bytes", "fs_fsb_select",
+           "fs_rope_make_plan", "fs_rope", "fs_cache_row_bytes", "fs_cache_append",
+           "fs_cache_read", "fs_cache_accept", "fs_tree_workspace_bytes", "fs_tree_attn"]
+FS_ROPE_LAYOUTS = {"half": 0, "pairs": 1}
+FS_ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "ramp": 3}
+FS_CACHE_FORMATS = {"bf16": 0, "e4m3": 1, "int8": 2, "int4": 3}
 FS_N_STAGES = 4
 STAGE_NAMES = ["cells_prep", "prune", "select", "attention"]
 
@@ -48,6 +53,25 @@ class fs_params(ctypes.Structure):
 
     def as_dict(self):
         return {f: getattr(self, f) for f, _ in self._fields_}
+
+
+class fs_rope_params(ctypes.Structure):
+    _fields_ = [("rot", ctypes.c_int), ("layout", ctypes.c_int), ("scaling", ctypes.c_int),
+                ("original", ctypes.c_int), ("base", ctypes.c_double), ("factor", ctypes.c_double),
+                ("beta_fast", ctypes.c_double), ("beta_slow", ctypes.c_double),
+                ("amplitude", ctypes.c_double)]
+
+
+class fs_rope_plan_t(ctypes.Structure):
+    _fields_ = [("rot", ctypes.c_int), ("layout", ctypes.c_int), ("amplitude", ctypes.c_float),
+                ("reserved", ctypes.c_int), ("turns", ctypes.c_uint64 * 128)]
+
+
+class fs_cache_t(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("table", ctypes.c_void_p),
+                ("status", ctypes.c_void_p), ("pages", ctypes.c_int), ("page", ctypes.c_int),
+                ("Hkv", ctypes.c_int), ("d", ctypes.c_int), ("format", ctypes.c_int),
+                ("batch", ctypes.c_int), ("max_pages", ctypes.c_int)]
 
 
 class FSError(RuntimeError):
@@ -125,8 +149,22 @@ def load(build_if_stale: bool = True):
         L.fs_qkv_prologue.argtypes = [P, P, P, I, I, I, I, F, P, P, P, P, Z, P]
         L.fs_decode_state_init.argtypes = [P, P, I, P, P, P, P, I, I, I, I, I, PP, P, Z, P]
         L.fs_decode_step.argtypes = [P, P, P, I, I, I, I, I, P, P, P, PP, P, Z, P, P, P]
+        PC, S3 = ctypes.POINTER(fs_cache_t), ctypes.POINTER(ctypes.c_longlong)
+        L.fs_rope_make_plan.argtypes = [ctypes.POINTER(fs_rope_params),
+                                        ctypes.POINTER(fs_rope_plan_t)]
+        L.fs_rope.argtypes = [P, P, I, S3, S3, P, P, I, S3, S3, I, I, I, I, P, ctypes.c_longlong, I,
+                              ctypes.POINTER(fs_rope_plan_t), I, P]
+        L.fs_cache_row_bytes.argtypes = [I, I]
+        L.fs_cache_row_bytes.restype = Z
+        L.fs_cache_append.argtypes = [PC, P, P, S3, S3, I, P, P, P]
+        L.fs_cache_read.argtypes = [PC, P, P, I, I, P, P, P]
+        L.fs_cache_accept.argtypes = [PC, P, P, P, I, P]
+        L.fs_tree_workspace_bytes.argtypes = [PC, I, I]
+        L.fs_tree_workspace_bytes.restype = Z
+        L.fs_tree_attn.argtypes = [P, PC, P, P, P, I, I, I, F, P, P, Z, P]
         for name in SYMBOLS:
-            if name not in ("fs_default_params", "fs_status_string", "fs_last_cuda_error",
+            if name not in ("fs_cache_row_bytes", "fs_tree_workspace_bytes",
+                            "fs_default_params", "fs_status_string", "fs_last_cuda_error",
                             "fs_workspace_bytes", "fs_prune_static_scratch_bytes",
                             "fs_prune_workspace_bytes", "fs_window_workspace_bytes",
                             "fs_host_workspace_bytes", "fs_decode_state_bytes",
@@ -634,3 +672,239 @@ def fs_check_status(ws, stream=None):
     """Synchronise the stream and raise FSError if a kernel recorded an error
     (a bounded device wait that timed out) in the workspace header."""
     _check(load().fs_check_status(_ptr(ws), _stream(stream)), "fs_check_status")
+
+
+# ---------------------------------------------------------------------------
+# rotary positions, the paged cache, attention of drafted tokens
+# ---------------------------------------------------------------------------
+
+_Strides = ctypes.c_longlong * 3
+
+
+def _on(t, dev, name, dtype, shape=None):
+    """``t`` is a CUDA tensor of ``dtype`` on ``dev``, contiguous in ``shape`` when given."""
+    if not isinstance(t, torch.Tensor) or t.device != dev:
+        raise ValueError(f"{name} must be a tensor on {dev}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if shape is not None and (tuple(t.shape) != tuple(shape) or not t.is_contiguous()):
+        raise ValueError(f"{name} must be contiguous {list(shape)}, not {list(t.shape)}")
+    return t.data_ptr()
+
+
+def _rows(t, dev, name, dtype, shape=None):
+    """Pointer and strides of a [batch, H, N, d] tensor whose d values lie together."""
+    _on(t, dev, name, dtype)
+    if t.dim() != 4 or (shape is not None and tuple(t.shape) != tuple(shape)):
+        raise ValueError(f"{name} must be {list(shape) if shape else '[batch, H, N, d]'}, "
+                         f"not {list(t.shape)}")
+    a, b, c, e = t.stride()
+    if e != 1 and t.shape[3] > 1:
+        raise ValueError(f"{name}: the values of a head must be contiguous")
+    return t.data_ptr(), _Strides(a, b, c)
+
+
+def _cuda(t, name):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.device
+
+
+def _launch(dev, stream, fn, where, *args):
+    """Calls ``fn`` for device ``dev`` on ``stream`` (default: the device's current one)."""
+    s = stream if stream is not None else torch.cuda.current_stream(dev)
+    if s.device != dev:
+        raise ValueError(f"{where}: the stream is on {s.device}, the tensors on {dev}")
+    if torch.cuda.current_device() == dev.index:
+        rc = fn(*args, s.cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, s.cuda_stream)
+    if rc != FS_OK:
+        raise FSError(rc, where)
+
+
+def fs_rope_plan(rot, layout="half", scaling="none", base=10000.0, factor=1.0, original=4096,
+                 beta_fast=32.0, beta_slow=1.0, amplitude=1.0):
+    """A model's rotary frequencies, worked out once on the host (fs_rope_make_plan):
+    ``rot`` rotated elements of a head, ``layout`` "half" or "pairs", ``scaling`` "none",
+    "linear", "base" or "ramp" by ``factor``."""
+    if layout not in FS_ROPE_LAYOUTS or scaling not in FS_ROPE_SCALINGS:
+        raise ValueError(f"unknown layout {layout!r} or scaling {scaling!r}")
+    p = fs_rope_params(int(rot), FS_ROPE_LAYOUTS[layout], FS_ROPE_SCALINGS[scaling], int(original),
+                       base, factor, beta_fast, beta_slow, amplitude)
+    plan = fs_rope_plan_t()
+    _check(load().fs_rope_make_plan(ctypes.byref(p), ctypes.byref(plan)), "fs_rope_make_plan")
+    return plan
+
+
+def fs_rope(q, k, pos, plan, inverse=False, q_out=None, k_out=None, stream=None):
+    """Rotates q [batch, Hq, N, d] and k [batch, Hk, N, d] (k None: q alone), bf16 or fp32, any
+    strides with the d values together, to the positions ``pos``: int32 [batch, N] or [N], or an
+    int for positions pos, pos + 1, ...  ``inverse`` applies the transposed rotation, which takes
+    the outputs' gradients to the inputs'.  ``q_out`` / ``k_out`` may be the inputs (in place).
+    Returns (q_out, k_out)."""
+    L = load()
+    dev, dt = _cuda(q, "q"), q.dtype
+    if dt not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"q has dtype {dt}, expected bfloat16 or float32")
+    qp, qs = _rows(q, dev, "q", dt)
+    B, Hq, N, d = q.shape
+    q_out = torch.empty_like(q) if q_out is None else q_out
+    qop, qos = _rows(q_out, dev, "q_out", dt, q.shape)
+    kp = ks = kop = kos = None
+    Hk = 0
+    if k is not None:
+        kp, ks = _rows(k, dev, "k", dt)
+        Hk = k.shape[1]
+        if tuple(k.shape) != (B, Hk, N, d):
+            raise ValueError(f"k must be [{B}, Hk, {N}, {d}], not {list(k.shape)}")
+        k_out = torch.empty_like(k) if k_out is None else k_out
+        kop, kos = _rows(k_out, dev, "k_out", dt, k.shape)
+    pp, stride, pos0 = None, 0, 0
+    if isinstance(pos, int):
+        pos0 = pos
+    else:
+        stride = N if pos.dim() == 2 else 0
+        pp = _on(pos, dev, "pos", torch.int32, (B, N) if stride else (N,))
+    _launch(dev, stream, L.fs_rope, "fs_rope", qp, qop, Hq, qs, qos, kp, kop, Hk, ks, kos,
+            FS_BF16 if dt == torch.bfloat16 else FS_FP32, B, N, d, pp, stride, pos0, plan,
+            int(bool(inverse)))
+    return q_out, k_out
+
+
+class fs_cache:
+    """A paged key/value cache: ``codes`` [pages, 2, Hkv, page, row bytes] uint8, ``scales``
+    [pages, 2, Hkv, page] fp32 (ignored for "bf16"), ``table`` [batch, max_pages] int32 and the
+    ``format`` ("bf16", "e4m3", "int8", "int4").  Holds the tensors; ``status`` is its error word
+    (``fs_check_status(cache.status)`` raises if a call met a page or position outside)."""
+
+    def __init__(self, codes, scales, table, format, status=None):
+        if format not in FS_CACHE_FORMATS:
+            raise ValueError(f"unknown cache format {format!r}")
+        dev = _cuda(codes, "codes")
+        if codes.dim() != 5 or codes.shape[1] != 2:
+            raise ValueError("codes must be [pages, 2, Hkv, page, row bytes]")
+        pages, _, Hkv, page, row = codes.shape
+        cp = _on(codes, dev, "codes", torch.uint8, codes.shape)
+        d = {"bf16": row // 2, "int4": row * 2}.get(format, row)
+        if load().fs_cache_row_bytes(d, FS_CACHE_FORMATS[format]) != row:
+            raise FSError(FS_ERR_UNSUPPORTED, "fs_cache")
+        sp = None
+        if format != "bf16":
+            sp = _on(scales, dev, "scales", torch.float32, (pages, 2, Hkv, page))
+        if not isinstance(table, torch.Tensor) or table.dim() != 2:
+            raise ValueError("table must be [batch, max_pages]")
+        tp = _on(table, dev, "table", torch.int32, table.shape)
+        self.status = torch.zeros(64, dtype=torch.int32, device=dev) if status is None else status
+        st = _on(self.status, dev, "status", torch.int32)
+        self.codes, self.scales, self.table, self.format = codes, scales, table, format
+        self.device, self.batch, self.Hkv, self.page, self.d = dev, table.shape[0], Hkv, page, d
+        self.desc = fs_cache_t(cp, sp, tp, st, pages, page, Hkv, d, FS_CACHE_FORMATS[format],
+                               table.shape[0], table.shape[1])
+
+
+def fs_cache_alloc(pages, Hkv, page, d, format, table):
+    """An empty ``fs_cache`` of ``pages`` pages on the device of ``table``."""
+    if format not in FS_CACHE_FORMATS:
+        raise ValueError(f"unknown cache format {format!r}")
+    row = load().fs_cache_row_bytes(d, FS_CACHE_FORMATS[format])
+    if row == 0:
+        raise FSError(FS_ERR_UNSUPPORTED, "fs_cache_alloc")
+    dev = _cuda(table, "table")
+    codes = torch.zeros((pages, 2, Hkv, page, row), dtype=torch.uint8, device=dev)
+    scales = None if format == "bf16" else torch.zeros((pages, 2, Hkv, page), device=dev)
+    return fs_cache(codes, scales, table, format)
+
+
+def _counts(cache, name, t):
+    return None if t is None else _on(t, cache.device, name, torch.int32, (cache.batch,))
+
+
+def fs_cache_append(cache, k, v, start, count=None, stream=None):
+    """Writes k, v [batch, Hkv, T, d] bf16 (any 16-byte aligned strides) at positions
+    start[b] .. start[b] + count[b] - 1 of every sequence (``count`` None: T)."""
+    L = load()
+    T = k.shape[2] if isinstance(k, torch.Tensor) and k.dim() == 4 else 0
+    shape = (cache.batch, cache.Hkv, T, cache.d)
+    kp, ks = _rows(k, cache.device, "k", torch.bfloat16, shape)
+    vp, vs = _rows(v, cache.device, "v", torch.bfloat16, shape)
+    if start is None:
+        raise ValueError("start must be given")
+    _launch(cache.device, stream, L.fs_cache_append, "fs_cache_append", cache.desc, kp, vp, ks, vs,
+            T, _counts(cache, "start", start), _counts(cache, "count", count))
+
+
+def fs_cache_read(cache, start, count=None, k=None, v=None, T=None, dtype=torch.bfloat16,
+                  stream=None):
+    """Reads positions start[b] .. start[b] + count[b] - 1 of every sequence into k, v
+    [batch, Hkv, T, d] (given, or new zeros of ``T`` rows in ``dtype``); rows past count[b] are
+    left as they were.  Returns (k, v)."""
+    L = load()
+    if (k is None) != (v is None) or (k is None and T is None):
+        raise ValueError("give k and v, or T")
+    if k is None:
+        k, v = (torch.zeros((cache.batch, cache.Hkv, T, cache.d), dtype=dtype, device=cache.device)
+                for _ in range(2))
+    if not isinstance(k, torch.Tensor) or k.dim() != 4 or \
+            k.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("k must be [batch, Hkv, T, d], bfloat16 or float32")
+    shape = (cache.batch, cache.Hkv, k.shape[2], cache.d)
+    kp = _on(k, cache.device, "k", k.dtype, shape)
+    vp = _on(v, cache.device, "v", k.dtype, shape)
+    if start is None:
+        raise ValueError("start must be given")
+    _launch(cache.device, stream, L.fs_cache_read, "fs_cache_read", cache.desc,
+            _counts(cache, "start", start), _counts(cache, "count", count), k.shape[2],
+            FS_BF16 if k.dtype == torch.bfloat16 else FS_FP32, kp, vp)
+    return k, v
+
+
+def fs_cache_accept(cache, start, path, count=None, stream=None):
+    """Moves the row at start[b] + path[b, i] to start[b] + i for i < count[b] (``path``
+    [batch, A <= 64] int32), every source read before any row is written."""
+    L = load()
+    if not isinstance(path, torch.Tensor) or path.dim() != 2 or start is None:
+        raise ValueError("path must be [batch, A], start given")
+    pp = _on(path, cache.device, "path", torch.int32, (cache.batch, path.shape[1]))
+    _launch(cache.device, stream, L.fs_cache_accept, "fs_cache_accept", cache.desc,
+            _counts(cache, "start", start), pp, _counts(cache, "count", count), path.shape[1])
+
+
+def fs_tree_workspace(cache, batch, H, T):
+    """A workspace for fs_tree_attn of this shape (one call at a time)."""
+    if batch != cache.batch:
+        raise ValueError(f"batch {batch}, but the cache's table has {cache.batch} sequences")
+    n = load().fs_tree_workspace_bytes(cache.desc, H, T)
+    if n == 0:
+        raise FSError(FS_ERR_INVALID_ARG, "fs_tree_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=cache.device)
+
+
+def fs_tree_attn(q, cache, past, tree=None, count=None, window=0, scale=None, out=None, ws=None,
+                 stream=None):
+    """Attention of drafted tokens q [batch, H, T <= 64, d] bf16, whose keys and values lie behind
+    the past[b] tokens of the prefix in ``cache``.  ``tree`` [batch, T] int64: bit j of row i lets
+    drafted token i see drafted token j (None: every token sees the drafted ones up to itself);
+    ``count`` [batch]: drafted tokens of each sequence (None: T); ``window`` 0 or >= 64 last
+    positions; ``scale`` default d ** -0.5.  Returns out [batch, H, T, d] bf16; rows past count[b]
+    are left as they were (a new ``out`` starts as zeros when ``count`` is given)."""
+    L = load()
+    dev = cache.device
+    if not isinstance(q, torch.Tensor) or q.dim() != 4:
+        raise ValueError("q must be [batch, H, T, d]")
+    B, H, T, d = q.shape
+    qp = _on(q, dev, "q", torch.bfloat16, (cache.batch, H, T, cache.d))
+    if past is None:
+        raise ValueError("past must be given")
+    tp = None if tree is None else _on(tree, dev, "tree", torch.int64, (B, T))
+    if out is None:
+        out = torch.empty_like(q) if count is None else torch.zeros_like(q)
+    op = _on(out, dev, "out", torch.bfloat16, q.shape)
+    if ws is None:
+        ws = fs_tree_workspace(cache, B, H, T)
+    wp = _on(ws, dev, "ws", torch.uint8)
+    _launch(dev, stream, L.fs_tree_attn, "fs_tree_attn", qp, cache.desc,
+            _counts(cache, "past", past), _counts(cache, "count", count), tp, H, T, int(window),
+            d ** -0.5 if scale is None else float(scale), op, wp, ws.numel())
+    return out
