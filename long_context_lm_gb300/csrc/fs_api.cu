@@ -845,6 +845,7 @@ int check_cache(const fs_cache *c) {
     return FS_ERR_UNSUPPORTED;
   if (c->d != 64 && c->d != 128) return FS_ERR_UNSUPPORTED;
   if ((long long)c->batch * c->Hkv > 65535) return FS_ERR_UNSUPPORTED;
+  if ((long long)c->max_pages * c->page > (1ll << 30)) return FS_ERR_UNSUPPORTED;
   return FS_OK;
 }
 

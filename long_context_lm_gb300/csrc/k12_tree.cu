@@ -1,104 +1,914 @@
 // k12_tree.cu -- attention of drafted tokens over the paged cache
-// (fs_tree_attn).
+// (fs_tree_attn): out = sum p v / sum p over the prefix and the drafted tokens
+// that a row's mask lets it see.
+//
+// Rows.  The R = count * G rows of one sequence and kv head (G query heads read
+// one kv head) share its keys; row r is token r / G, query head r % G.  They
+// are taken M at a time.
+//
+// Split.  The work is cut into units of 32 keys of one (sequence, kv head, row
+// tile): a segment.  All units stand in one line and every block takes an
+// equal stretch of it, so that ragged batches and few long sequences alike keep
+// every SM busy.  Lengths are known on the device alone: each block works out
+// the line for itself.  A segment that lies in one block is written by it; of
+// the others each block leaves (m, l, O) in the workspace, and a second kernel
+// adds them in block order (no atomics: the same bits every time).
+//
+// A block's warps take the segment's units in turn, each with all M rows and
+// its own running maximum, sum and output, and a ring of units in flight
+// (asynchronous copies into shared memory); they are joined once a segment.
+//
+// Products are mma.sync m16n8k16 with fp32 sums.  A fragment may hold the
+// elements of a head in any order that q and k share, and the values in any
+// order of columns: so every lane reads whole 16-byte (8, 4) pieces of codes
+// and turns them into fragments in registers.  Codes of 8 and 4 bits are exact
+// in fp16; q is brought into fp16's range by a power of two a row (exact but
+// for elements below 2^-39 of the row's largest).  The key's scale multiplies
+// the score; the value's scale multiplies the probability, relative to a power
+// of two at least as large as every scale seen (exact to follow), which joins
+// the output at the end.
+//
+// Probabilities go into the second product as fp16 (half a step 2^-11) between
+// 0 and 2^15, so that one of 2^-38 of the largest still counts; with bf16
+// values as a bf16 pair (high and low part, 2^-16).  The maximum follows
+// lazily: a row's reference moves only when a score passes it by 8 (log2).
+#include <float.h>
+
 #include "cache.cuh"
+#include "tc05.cuh"
 
 namespace fs {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kUnit = 32;        // keys of a unit
+constexpr float kRaise = 8.f;    // how far a score may pass its reference (log2)
 
-// One block per (row, query head, sequence): tiles of 128 keys, a thread a key
-// for the scores, then a thread a dimension for the values.
-template <int F, int D>
-__global__ void __launch_bounds__(128) k12_simple_kernel(const __grid_constant__ TreeArgs a) {
-  __shared__ float q[D], p[128], red[4];
-  __shared__ long long at[128];
-  const int i = blockIdx.x, h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
-  const int n = a.count ? min(a.count[b], a.T) : a.T;
-  if (i >= n) return;
-  const int G = a.H / a.c.Hkv, kvh = h / G;
-  const long long past = max(a.past[b], 0);
-  uint64_t bits = a.tree ? (uint64_t)a.tree[(size_t)b * a.T + i] : ~0ull >> (63 - i);
-  if (n < 64) bits &= (1ull << n) - 1;
-  long long first = 0;
-  if (a.window) first = max(0ll, past + __popcll(bits) - a.window);
-  const size_t qrow = (((size_t)b * a.H + h) * a.T + i) * D;
-  if (tid < D) q[tid] = __bfloat162float(static_cast<const __nv_bfloat16 *>(a.q)[qrow + tid]) *
-                        (a.scale * kLog2e);
-  float m = -INFINITY, l = 0.f, o = 0.f;
-  for (long long base = first; base < past + n; base += 128) {
-    __syncthreads();
-    const long long key = base + tid;
-    float s = -INFINITY;
-    int off = 0, page = -1;
-    if (key < past + n && (key < past || (bits >> (key - past) & 1)))
-      page = cache_page(a.c, b, key, &off);
-    at[tid] = -1;
-    if (page >= 0) {
-      const size_t row = cache_row(a.c, page, 0, kvh, off);
-      at[tid] = (long long)cache_row(a.c, page, 1, kvh, off);
-      s = 0.f;
-      for (int e = 0; e < D; e += 8) {
-        uint32_t w[4];
-        float x[8];
-        load8<F>(a.c, row, e, w);
-        decode8<F>(w, x);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) s += x[j] * q[e + j];
-      }
-      if constexpr (F != FS_CACHE_BF16) s *= a.c.scales[row];
-    }
-    float t = s;
-    for (int o2 = 16; o2 > 0; o2 >>= 1) t = fmaxf(t, __shfl_xor_sync(~0u, t, o2));
-    if (tid % 32 == 0) red[tid / 32] = t;
-    __syncthreads();
-    const float mt = fmaxf(m, fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])));
-    const float ref = mt == -INFINITY ? 0.f : mt;
-    p[tid] = at[tid] >= 0 ? exp2f(s - ref) : 0.f;
-    const float back = exp2f(m - ref);
-    m = mt;
-    l *= back;
-    o *= back;
-    __syncthreads();
-    for (int j = 0; j < 128; ++j) {
-      const long long row = at[j];
-      if (row < 0) continue;
-      l += p[j];
-      if (tid < D) {
-        uint32_t w[4];
-        float x[8];
-        load8<F>(a.c, row, tid & ~7, w);
-        decode8<F>(w, x);
-        float v = x[0];
-#pragma unroll
-        for (int e = 1; e < 8; ++e) v = (tid & 7) == e ? x[e] : v;
-        if constexpr (F != FS_CACHE_BF16) v *= a.c.scales[row];
-        o += p[j] * v;
-      }
-    }
-  }
-  if (tid < D)
-    static_cast<__nv_bfloat16 *>(a.out)[qrow + tid] = __float2bfloat16_rn(l > 0.f ? o / l : (l == 0.f ? 0.f : l));
+// ---------------------------------------------------------------------------
+// the line of units
+// ---------------------------------------------------------------------------
+struct Seq {
+  int past, n, first, end;  // prefix, drafted tokens, keys [first, end) that any row sees
+  int units, tiles;         // units of a segment, row tiles of a kv head
+};
+
+struct TreeK {
+  TreeArgs a;
+  int G, M, blocks, warps;
+  float *part;  // [blocks][2][M][D + 2]: O, m, l
+};
+
+__device__ __forceinline__ Seq seq_of(const TreeK &k, int b) {
+  Seq s;
+  const int limit = k.a.c.max_pages * k.a.c.page;  // at most 2^30
+  const int past = k.a.past[b];
+  s.n = k.a.count ? min(max(k.a.count[b], 0), k.a.T) : k.a.T;
+  s.past = min(max(past, 0), limit);
+  s.end = min(s.past + s.n, limit);
+  // (a row that sees i drafted tokens begins at past + i - window)
+  s.first = k.a.window ? max(0, s.past - k.a.window) & ~(kUnit - 1) : 0;
+  s.units = (s.end - s.first + kUnit - 1) / kUnit;
+  s.tiles = (s.n * k.G + k.M - 1) / k.M;
+  if (s.n == 0) s.units = 0;
+  return s;
+}
+__device__ __forceinline__ long long seq_units(const TreeK &k, const Seq &s) {
+  return (long long)s.units * s.tiles * k.a.c.Hkv;
+}
+__device__ __forceinline__ bool seq_outside(const TreeK &k, int b) {
+  const int past = k.a.past[b];
+  const int n = k.a.count ? min(max(k.a.count[b], 0), k.a.T) : k.a.T;
+  return n > 0 && (past < 0 || (long long)past + n > (long long)k.a.c.max_pages * k.a.c.page);
 }
 
-template <int D>
-cudaError_t launch_simple(const TreeArgs &a, cudaStream_t st) {
-  const dim3 grid(a.T, a.H, a.c.batch);
-  switch (a.c.format) {
-    case FS_CACHE_BF16: k12_simple_kernel<FS_CACHE_BF16, D><<<grid, 128, 0, st>>>(a); break;
-    case FS_CACHE_E4M3: k12_simple_kernel<FS_CACHE_E4M3, D><<<grid, 128, 0, st>>>(a); break;
-    case FS_CACHE_INT8: k12_simple_kernel<FS_CACHE_INT8, D><<<grid, 128, 0, st>>>(a); break;
-    default: k12_simple_kernel<FS_CACHE_INT4, D><<<grid, 128, 0, st>>>(a); break;
+// Length of the line, and where sequence `want` begins in it (or, with
+// want < 0, the sequence that holds unit `at` and its beginning).  Called by
+// all threads of a block; `sh` is shared memory of 4 long longs a warp.
+struct Line {
+  long long total, begin;
+  int b;
+};
+__device__ Line line_of(const TreeK &k, int want, long long at, long long *sh) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
+  Line out{0, 0, 0};
+  __shared__ long long found[2];
+  for (int b0 = 0; b0 < k.a.c.batch; b0 += blockDim.x) {
+    const int b = b0 + tid;
+    long long u = 0;
+    if (b < k.a.c.batch) u = seq_units(k, seq_of(k, b));
+    long long x = u;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(~0u, x, o);
+      if (lane >= o) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) sh[warp] = x;
+    __syncthreads();
+    long long before = out.total, all = 0;
+    for (int w = 0; w < nw; ++w) {
+      if (w < warp) before += sh[w];
+      all += sh[w];
+    }
+    x += before;  // inclusive
+    if (b < k.a.c.batch && (want >= 0 ? b == want : (at >= x - u && at < x))) {
+      found[0] = b;
+      found[1] = x - u;
+    }
+    out.total += all;
   }
-  return cudaGetLastError();
+  __syncthreads();
+  out.b = (int)found[0];
+  out.begin = found[1];
+  __syncthreads();
+  return out;
+}
+
+// Blocks that share the line: at least a unit for every warp.
+__device__ __forceinline__ int line_blocks(const TreeK &k, long long total) {
+  const long long n = (total + k.warps - 1) / k.warps;
+  return (int)(n < k.blocks ? (n < 1 ? 1 : n) : k.blocks);
+}
+// The block that holds unit u: blocks begin at floor(c total / n).
+__device__ __forceinline__ int block_of(long long u, long long total, int n) {
+  return (int)(((u + 1) * n - 1) / total);
+}
+
+// ---------------------------------------------------------------------------
+// fragments
+// ---------------------------------------------------------------------------
+template <bool BF>
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  if constexpr (BF)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};\n"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};\n"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t h2add(uint32_t a, uint32_t b) {
+  __half2 r = __hadd2(*reinterpret_cast<__half2 *>(&a), *reinterpret_cast<__half2 *>(&b));
+  return *reinterpret_cast<uint32_t *>(&r);
+}
+__device__ __forceinline__ uint32_t h2fma(uint32_t a, uint32_t b, uint32_t c) {
+  __half2 r = __hfma2(*reinterpret_cast<__half2 *>(&a), *reinterpret_cast<__half2 *>(&b),
+                      *reinterpret_cast<__half2 *>(&c));
+  return *reinterpret_cast<uint32_t *>(&r);
+}
+__device__ __forceinline__ uint32_t e4m3_h2(uint32_t two) {
+  const __half2_raw h =
+      __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(two & 0xffffu), __NV_E4M3);
+  return (uint32_t)h.x | ((uint32_t)h.y << 16);
+}
+// fp16 numbers with a code in their lowest bits: 0x6400 is 1024, whose step is 1.
+constexpr uint32_t kMagic = 0x64006400u;
+constexpr uint32_t kSub128 = 0xe480e480u;  // -(1024 + 128)
+constexpr uint32_t kSub8 = 0xe408e408u;    // -(1024 + 8)
+constexpr uint32_t kSixteenth = 0x2c002c00u;
+constexpr uint32_t kSub72 = 0xd480d480u;   // -(64 + 8)
+// Nibbles 0 and 4, or 1 and 5, of codes with their sign bit flipped (code + 8).
+__device__ __forceinline__ uint32_t nib_even(uint32_t x) {
+  return h2add((x & 0x000f000fu) | kMagic, kSub8);
+}
+__device__ __forceinline__ uint32_t nib_odd(uint32_t x) {
+  return h2fma((x & 0x00f000f0u) | kMagic, kSixteenth, kSub72);
+}
+
+template <int F, int D, int MT>
+struct Cfg {
+  static constexpr int kBits = Fmt<F>::kBits;
+  static constexpr int kRow = D * kBits / 8;  // bytes of a row
+  static constexpr int P = kRow / 16;         // 16-byte pieces of a row
+  static constexpr int kM = 16 * MT;
+  static constexpr int kWarps = kRow >= 256 ? 4 : 8;
+  static constexpr int kCodes = kUnit * kRow;  // bytes of a unit's keys
+  // keys, values, 32 + 32 scales, which keys can be read
+  static constexpr int kStage = 2 * kCodes + 8 * kUnit + 16;
+  static constexpr int kCtas = MT == 1 && D == 64 && kStage * kWarps * 3 <= 112 * 1024 ? 2 : 1;
+  static constexpr int kRoom = (kCtas == 2 ? 110 : 220) * 1024;
+  static constexpr int kFit = kRoom / (kStage * kWarps);
+  static constexpr int kStages = kFit > 6 ? 6 : kFit;
+  static constexpr int kJoin = kWarps * kM * (D + 2) * 4;  // the warps' results
+  static constexpr int kRing = kStage * kWarps * kStages;
+  static constexpr int kSmem = kRing > kJoin ? kRing : kJoin;
+  static constexpr bool kBF = F == FS_CACHE_BF16;
+  static_assert(kStages >= 2 && kSmem <= kRoom, "ring");
+};
+
+// Element of a head that lane column c (lane % 4) holds as element e (0..3: low
+// and high half of the first, then the second register) of k step s.
+template <int F, int D>
+__device__ __forceinline__ int k_element(int c, int s, int e) {
+  if constexpr (F == FS_CACHE_BF16) return 8 * (c + 4 * (s / 2)) + (s % 2) * 4 + e;
+  if constexpr (F == FS_CACHE_INT4)
+    return D / 4 * c + 8 * (s / 2) + 2 * (s % 2) + (e / 2) + 4 * (e % 2);
+  return 16 * (c + 4 * (s / 4)) + 4 * (s % 4) + e;
+}
+// Element that column n of value tile i stands for.
+template <int F, int D>
+__device__ __forceinline__ int v_element(int n, int i) {
+  if constexpr (D == 64) return 8 * n + i;
+  if constexpr (F == FS_CACHE_BF16) return 8 * n + i % 8 + 64 * (i / 8);
+  return 16 * n + i;
+}
+// Places of 16-byte pieces, so that the lanes that read at one time hit
+// different banks: keys are read by eight neighbouring rows at once, values by
+// rows two apart.
+template <int P>
+__device__ __forceinline__ int k_place(int r, int piece) {
+  return r * P + (P >= 8 ? piece ^ (4 * (r & 1)) : piece);
+}
+template <int P>
+__device__ __forceinline__ int v_place(int r, int piece) {
+  return (r * P + piece) ^ (P >= 4 ? 2 * ((r >> 1) & 3) : 2 * ((r >> 2) & 1));
+}
+
+// The k step's two key registers from the lane's code words.
+template <int F>
+__device__ __forceinline__ void k_regs(const uint32_t *w, int s, uint32_t &b0, uint32_t &b1) {
+  if constexpr (F == FS_CACHE_BF16) {
+    b0 = w[2 * s];
+    b1 = w[2 * s + 1];
+  } else if constexpr (F == FS_CACHE_E4M3) {
+    b0 = e4m3_h2(w[s]);
+    b1 = e4m3_h2(w[s] >> 16);
+  } else if constexpr (F == FS_CACHE_INT8) {
+    const uint32_t x = w[s] ^ 0x80808080u;
+    b0 = h2add(__byte_perm(x, kMagic, 0x7170), kSub128);
+    b1 = h2add(__byte_perm(x, kMagic, 0x7372), kSub128);
+  } else {
+    const uint32_t x = (w[s / 2] ^ 0x88888888u) >> (8 * (s % 2));
+    b0 = nib_even(x);
+    b1 = nib_odd(x);
+  }
+}
+// Value register(s) of two keys' words: the elements 2 j and 2 j + 1 of the
+// lane's 8 (of word set x, y), each paired over the two keys.
+template <int F>
+__device__ __forceinline__ void v_regs(const uint32_t *x, const uint32_t *y, int j, uint32_t &r0,
+                                       uint32_t &r1) {
+  if constexpr (F == FS_CACHE_BF16) {
+    r0 = __byte_perm(x[j], y[j], 0x5410);
+    r1 = __byte_perm(x[j], y[j], 0x7632);
+  } else if constexpr (F == FS_CACHE_E4M3) {
+    const uint32_t z = __byte_perm(x[j / 2], y[j / 2], j % 2 ? 0x7362 : 0x5140);
+    r0 = e4m3_h2(z);
+    r1 = e4m3_h2(z >> 16);
+  } else if constexpr (F == FS_CACHE_INT8) {
+    const uint32_t z = __byte_perm(x[j / 2], y[j / 2], j % 2 ? 0x7362 : 0x5140) ^ 0x80808080u;
+    r0 = h2add(__byte_perm(z, kMagic, 0x7170), kSub128);
+    r1 = h2add(__byte_perm(z, kMagic, 0x7372), kSub128);
+  } else {
+    // byte j of both keys: its low and high nibble
+    const uint32_t sel = (uint32_t)(j % 4) * 0x0011u + (uint32_t)(4 + j % 4) * 0x1100u;
+    const uint32_t z = __byte_perm(x[j / 4], y[j / 4], sel) ^ 0x88888888u;
+    r0 = nib_even(z);
+    r1 = nib_odd(z);
+  }
+}
+
+__device__ __forceinline__ void cp_async16z(uint32_t dst, const void *src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(bytes));
+}
+__device__ __forceinline__ void cp_async4z(uint32_t dst, const void *src, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(dst), "l"(src), "r"(bytes));
+}
+
+template <int N>
+__device__ __forceinline__ void lds_words(const char *p, uint32_t *w) {
+  if constexpr (N == 1) {
+    w[0] = *reinterpret_cast<const uint32_t *>(p);
+  } else if constexpr (N == 2) {
+    const uint2 u = *reinterpret_cast<const uint2 *>(p);
+    w[0] = u.x, w[1] = u.y;
+  } else {
+    const uint4 u = *reinterpret_cast<const uint4 *>(p);
+    w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// the kernel
+// ---------------------------------------------------------------------------
+template <int F, int D, int MT>
+__global__ void __launch_bounds__(Cfg<F, D, MT>::kWarps * 32, Cfg<F, D, MT>::kCtas)
+k12_tree_kernel(const __grid_constant__ TreeK k) {
+  using C = Cfg<F, D, MT>;
+  constexpr int P = C::P, W = C::kWarps, M = C::kM, NS = C::kStages;
+  constexpr int KS = D / 16, NT = D / 8;  // k steps of a score, value tiles
+  extern __shared__ __align__(128) char smem[];
+  __shared__ long long sh[8];
+  __shared__ uint64_t row_bits[M];
+  __shared__ int row_first[M];
+  const TreeArgs &a = k.a;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
+  const int shift = 31 - __clz(a.c.page);
+  asm volatile("griddepcontrol.launch_dependents;");
+
+  Line line = line_of(k, 0, 0, sh);
+  const long long total = line.total;
+  if (blockIdx.x == 0)
+    for (int b = tid; b < a.c.batch; b += W * 32)
+      if (a.c.status && seq_outside(k, b)) atomicCAS(a.c.status, 0, FS_ERR_CACHE);
+  if (total == 0) return;
+  const int nb = line_blocks(k, total);
+  if ((int)blockIdx.x >= nb) return;
+  const long long u0 = (long long)blockIdx.x * total / nb;
+  const long long u1 = (long long)(blockIdx.x + 1) * total / nb;
+  line = line_of(k, -1, u0, sh);
+  int b = line.b;
+  long long begin = line.begin;  // of sequence b
+  Seq s = seq_of(k, b);
+
+  char *ring = smem + warp * (C::kStage * NS);
+  const uint32_t ring_s = smem_u32(ring);
+  const size_t v_off = (size_t)a.c.Hkv * a.c.page;  // rows from a key to its value
+
+  long long u = u0;
+  while (u < u1) {
+    while (u >= begin + seq_units(k, s) && b + 1 < a.c.batch) {
+      begin += seq_units(k, s);
+      s = seq_of(k, ++b);
+    }
+    if (s.units == 0) break;  // (lengths that changed under the call)
+    const int seg = (int)((u - begin) / s.units);
+    const long long seg0 = begin + (long long)seg * s.units;
+    const int rt = seg % s.tiles, h = seg / s.tiles;
+    const int from = (int)(u - seg0), to = (int)min((long long)s.units, u1 - seg0);
+    const int rows = s.n * k.G;
+
+    // what every row sees: its bits, and its first key of the prefix
+    __syncthreads();
+    if (tid < M) {
+      const int r = rt * M + tid;
+      uint64_t bits = 0;
+      int first = INT_MAX;
+      if (r < rows) {
+        const int t = r / k.G;
+        bits = a.tree ? (uint64_t)a.tree[(size_t)b * a.T + t] : ~0ull >> (63 - t);
+        if (s.n < 64) bits &= (1ull << s.n) - 1;
+        first = a.window ? max(0, s.past + __popcll(bits) - a.window) : 0;
+      }
+      row_bits[tid] = bits;
+      row_first[tid] = first;
+    }
+    __syncthreads();
+
+    // q: fragments of the lane's rows
+    uint32_t q[MT][KS][4];
+    float rf[MT][2];  // score of the fragments' product -> log2 units
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        const int r = rt * M + mt * 16 + hf * 8 + g;
+        const bool live = r < rows;
+        const int t = live ? r / k.G : 0, head = h * k.G + (live ? r % k.G : 0);
+        const uint16_t *src = static_cast<const uint16_t *>(a.q) +
+                              (((size_t)b * a.H + head) * a.T + t) * D;
+        uint32_t raw[KS][2];
+        uint32_t most = 0;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            uint32_t lo = 0, hi = 0;
+            if (live) {
+              lo = src[k_element<F, D>(c, ks, 2 * e)];
+              hi = src[k_element<F, D>(c, ks, 2 * e + 1)];
+            }
+            raw[ks][e] = lo | (hi << 16);
+            most = max(most, max(lo & 0x7fffu, hi & 0x7fffu));
+          }
+        float f = 1.f;
+        if constexpr (!C::kBF) {
+          most = max(most, __shfl_xor_sync(~0u, most, 1));
+          most = max(most, __shfl_xor_sync(~0u, most, 2));
+          // the largest magnitude goes to [2^14, 2^15)
+          f = __uint_as_float((uint32_t)min(254, 268 - (int)(most >> 7)) << 23);
+        }
+        rf[mt][hf] = a.scale * kLog2e * (1.f / f);
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            uint32_t x = raw[ks][e];
+            if constexpr (!C::kBF) x = pack_f16(bf16_lo(x) * f, bf16_hi(x) * f);
+            q[mt][ks][2 * e + hf] = x;
+          }
+      }
+    int lead = 0;  // no row's prefix begins later
+    if (a.window)
+      for (int r = 0; r < M; ++r) lead = max(lead, row_first[r] == INT_MAX ? 0 : row_first[r]);
+
+    float o[MT][NT][4] = {}, m[MT][2], l[MT][2] = {};
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) m[mt][0] = m[mt][1] = -FLT_MAX;
+    float vref = 0x1p-126f;
+
+    // page of keys [16 i, 16 i + 16) of unit x in lane i (i < 2)
+    auto pages_of = [&](int x) -> int {
+      int page = -1;
+      const int key = s.first + x * kUnit + 16 * (lane & 1);
+      if (x < to && key < s.end) {
+        page = a.c.table[(size_t)b * a.c.max_pages + (key >> shift)];
+        if (page < 0 || page >= a.c.pages) {
+          if (a.c.status) atomicCAS(a.c.status, 0, FS_ERR_CACHE);
+          page = -1;
+        }
+      }
+      return page;
+    };
+    auto issue = [&](int x, int stage, int page) {
+      if (x < to) {
+        const int key0 = s.first + x * kUnit;
+        const uint32_t dst = ring_s + stage * C::kStage;
+        size_t row[2];
+        bool ok[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int pg = __shfl_sync(~0u, page, i);
+          ok[i] = pg >= 0;
+          row[i] = cache_row(a.c, ok[i] ? pg : 0, 0, h, (key0 + 16 * i) & (a.c.page - 1));
+        }
+        const char *codes = static_cast<const char *>(a.c.codes);
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+          const int r = (lane + 32 * i) / P, piece = (lane + 32 * i) % P;
+          const int half = i * 2 / P;  // of the unit; the same for all lanes
+          const bool in = ok[half] && key0 + r < s.end;
+          const char *src = codes + (row[half] + (r - 16 * half)) * C::kRow + piece * 16;
+          cp_async16z(dst + k_place<P>(r, piece) * 16, in ? src : codes, in ? 16 : 0);
+          src += v_off * C::kRow;
+          cp_async16z(dst + C::kCodes + v_place<P>(r, piece) * 16, in ? src : codes, in ? 16 : 0);
+        }
+        const int half = lane >> 4;
+        const bool in = (half ? ok[1] : ok[0]) && key0 + lane < s.end;
+        if constexpr (!C::kBF) {
+          const float *src = a.c.scales + (half ? row[1] : row[0]) + (lane & 15);
+          const uint32_t to_s = dst + 2 * C::kCodes + lane * 4;
+          cp_async4z(to_s, in ? src : a.c.scales, in ? 4 : 0);
+          cp_async4z(to_s + 4 * kUnit, in ? src + v_off : a.c.scales, in ? 4 : 0);
+        }
+        const uint32_t valid = __ballot_sync(~0u, in);
+        if (lane == 0)
+          *reinterpret_cast<uint32_t *>(ring + stage * C::kStage + 2 * C::kCodes + 8 * kUnit) = valid;
+      }
+      cp_async_commit();
+    };
+
+    int next = from + warp;  // unit to issue
+    int page = pages_of(next);
+#pragma unroll
+    for (int i = 0; i < NS - 1; ++i) {
+      const int now = page;
+      page = pages_of(next + W);
+      issue(next, i, now);
+      next += W;
+    }
+    int stage = 0;
+    for (int x = from + warp; x < to; x += W) {
+      {
+        const int now = page;
+        page = pages_of(next + W);
+        issue(next, stage == 0 ? NS - 1 : stage - 1, now);
+        next += W;
+      }
+      cp_async_wait<NS - 1>();
+      __syncwarp();
+      const char *st = ring + stage * C::kStage;
+      const uint32_t valid = *reinterpret_cast<const uint32_t *>(st + 2 * C::kCodes + 8 * kUnit);
+      const int key0 = s.first + x * kUnit;
+      const bool whole = valid == ~0u && key0 + kUnit <= s.past && key0 >= lead;
+
+      float sc[MT][4][4] = {};
+#pragma unroll
+      for (int nt = 0; nt < 4; ++nt) {
+        constexpr int KW = D * C::kBits / 128;  // words of a lane: a quarter of the row
+        uint32_t w[KW];
+        const int r = nt * 8 + g;
+        if constexpr (KW <= 4) {
+          lds_words<KW>(st + (KW == 2 ? r * C::kRow + c * 8 : k_place<P>(r, c) * 16), w);
+        } else {
+#pragma unroll
+          for (int j = 0; j < KW / 4; ++j) lds_words<4>(st + k_place<P>(r, c + 4 * j) * 16, w + 4 * j);
+        }
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          uint32_t b0, b1;
+          k_regs<F>(w, ks, b0, b1);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) mma16816<C::kBF>(sc[mt][nt], q[mt][ks], b0, b1);
+        }
+      }
+      // scores in log2 units, masks, the rows' references
+      float vf[4][2];  // value scales over vref
+      const float *kscale = reinterpret_cast<const float *>(st + 2 * C::kCodes);
+      if constexpr (!C::kBF) {
+        const float mine = kscale[kUnit + lane];
+        const float top = __uint_as_float(
+            __reduce_max_sync(~0u, mine <= FLT_MAX ? __float_as_uint(mine) & 0x7fffffffu : 0u));
+        if (top > vref) {  // the same in all lanes
+          const float up = __uint_as_float((__float_as_uint(top) + 0x7fffffu) & 0x7f800000u);
+          const float back = vref / up;
+          vref = up;
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[mt][i][e] *= back;
+        }
+        const float inv = 1.f / vref;
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt) {
+          const float2 ks = *reinterpret_cast<const float2 *>(kscale + nt * 8 + 2 * c);
+          const float2 vs = *reinterpret_cast<const float2 *>(kscale + kUnit + nt * 8 + 2 * c);
+          vf[nt][0] = vs.x * inv;
+          vf[nt][1] = vs.y * inv;
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            sc[mt][nt][0] *= ks.x;
+            sc[mt][nt][1] *= ks.y;
+            sc[mt][nt][2] *= ks.x;
+            sc[mt][nt][3] *= ks.y;
+          }
+        }
+      }
+      bool raise = false;
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          if (!whole) {
+            const uint64_t bits = row_bits[mt * 16 + hf * 8 + g];
+            const int first = row_first[mt * 16 + hf * 8 + g];
+#pragma unroll
+            for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int at = nt * 8 + 2 * c + e, key = key0 + at;
+                const bool see = (valid >> at & 1) &&
+                                 (key < s.past ? key >= first : (bool)(bits >> (key - s.past) & 1));
+                float &y = sc[mt][nt][2 * hf + e];
+                y = see ? y * rf[mt][hf] : -INFINITY;
+              }
+          } else {
+#pragma unroll
+            for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) sc[mt][nt][2 * hf + e] *= rf[mt][hf];
+          }
+          float top = sc[mt][0][2 * hf];
+#pragma unroll
+          for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) top = fmaxf(top, sc[mt][nt][2 * hf + e]);
+          raise = raise || top > m[mt][hf] + kRaise;
+        }
+      if (__any_sync(~0u, raise)) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            float top = m[mt][hf];
+#pragma unroll
+            for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) top = fmaxf(top, sc[mt][nt][2 * hf + e]);
+            top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+            const float back = exp2f(m[mt][hf] - top);
+            m[mt][hf] = top;
+            l[mt][hf] *= back;
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+              o[mt][i][2 * hf] *= back;
+              o[mt][i][2 * hf + 1] *= back;
+            }
+          }
+      }
+      // probabilities, at most 2^15 (fp16) or 1 (bf16)
+      constexpr float kLift = C::kBF ? -kRaise : 15.f - kRaise;
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          const float ref = m[mt][hf] - kLift;
+#pragma unroll
+          for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float &y = sc[mt][nt][2 * hf + e];
+              const float p = tc::ex2(y - ref);
+              l[mt][hf] += p;
+              if constexpr (C::kBF) {
+                y = p;
+              } else {
+                // (a masked key's scale may be NaN)
+                y = whole || y != -INFINITY ? p * vf[nt][e] : 0.f;
+              }
+            }
+        }
+
+      const char *vs = st + C::kCodes;
+      bool plain = true;
+      if constexpr (C::kBF) {
+        // A value that is not finite may reach only the rows that see it: 0 *
+        // inf in the matrix product would reach the others.
+        if (!whole) {
+          bool odd = false;
+          for (int i = lane; i < kUnit * P; i += 32) {
+            uint32_t w[4];
+            lds_words<4>(vs + i * 16, w);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              odd = odd || (w[j] & 0x7f80u) == 0x7f80u || (w[j] & 0x7f800000u) == 0x7f800000u;
+          }
+          plain = !__any_sync(~0u, odd);
+          if (!plain) {
+            __syncwarp();
+            float *pt = reinterpret_cast<float *>(ring + stage * C::kStage);  // [key][row]
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+              for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  pt[(nt * 8 + 2 * c + (e & 1)) * M + mt * 16 + (e >> 1) * 8 + g] = sc[mt][nt][e];
+            __syncwarp();
+            for (int r = 0; r < kUnit; ++r) {
+#pragma unroll
+              for (int i = 0; i < NT; ++i)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const int el = v_element<F, D>(2 * c + e, i);
+                  const uint16_t bits = *reinterpret_cast<const uint16_t *>(
+                      vs + v_place<P>(r, el / 8) * 16 + (el % 8) * 2);
+                  const float v = __uint_as_float((uint32_t)bits << 16);
+#pragma unroll
+                  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+                      const float p = pt[r * M + mt * 16 + hf * 8 + g];
+                      if (p != 0.f) o[mt][i][2 * hf + e] += p * v;
+                    }
+                }
+            }
+          }
+        }
+      }
+      if (plain) {
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+          uint32_t p[MT][4], lo[MT][4];
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float x0 = sc[mt][2 * kk + j / 2][2 * (j % 2)];
+              const float x1 = sc[mt][2 * kk + j / 2][2 * (j % 2) + 1];
+              if constexpr (C::kBF) {
+                p[mt][j] = pack_bf16(x0, x1);
+                lo[mt][j] = pack_bf16(x0 - bf16_lo(p[mt][j]), x1 - bf16_hi(p[mt][j]));
+              } else {
+                p[mt][j] = pack_f16(x0, x1);
+              }
+            }
+          const int r0 = 16 * kk + 2 * c;
+          constexpr int VW = D == 64 ? C::kBits / 4 : (C::kBF ? 4 : C::kBits / 2);  // words at a time
+          constexpr int SETS = C::kBF ? D / 64 : 1;
+#pragma unroll
+          for (int set = 0; set < SETS; ++set) {
+            uint32_t w[4][VW];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int r = r0 + (i & 1) + 8 * (i >> 1);
+              const int byte = g * VW * 4;  // inside the row (its first set)
+              lds_words<VW>(vs + v_place<P>(r, byte / 16 + 8 * set) * 16 + byte % 16, w[i]);
+            }
+#pragma unroll
+            for (int j = 0; j < NT / SETS / 2; ++j) {
+              uint32_t b00, b01, b10, b11;
+              v_regs<F>(w[0], w[1], j, b00, b10);
+              v_regs<F>(w[2], w[3], j, b01, b11);
+              const int i = set * (NT / SETS) + 2 * j;
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt) {
+                mma16816<C::kBF>(o[mt][i], p[mt], b00, b01);
+                mma16816<C::kBF>(o[mt][i + 1], p[mt], b10, b11);
+                if constexpr (C::kBF) {
+                  mma16816<true>(o[mt][i], lo[mt], b00, b01);
+                  mma16816<true>(o[mt][i + 1], lo[mt], b10, b11);
+                }
+              }
+            }
+          }
+        }
+      }
+      __syncwarp();  // before the stage is filled again
+      stage = stage + 1 == NS ? 0 : stage + 1;
+    }
+    cp_async_wait<0>();
+
+    // join the warps
+    __syncthreads();
+    float *jo = reinterpret_cast<float *>(smem);  // [warp][M][D]
+    float *jm = jo + W * M * D, *jl = jm + W * M;  // [warp][M]
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        float sum = l[mt][hf];
+        sum += __shfl_xor_sync(~0u, sum, 1);
+        sum += __shfl_xor_sync(~0u, sum, 2);
+        const int r = warp * M + mt * 16 + hf * 8 + g;
+        if (c == 0) {
+          jm[r] = m[mt][hf];
+          jl[r] = sum;
+        }
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            jo[r * D + v_element<F, D>(2 * c + e, i)] =
+                C::kBF ? o[mt][i][2 * hf + e] : o[mt][i][2 * hf + e] * vref;
+      }
+    __syncthreads();
+    const bool alone = from == 0 && to == s.units;
+    float *part = k.part + ((size_t)blockIdx.x * 2 + (from == 0)) * M * (D + 2);
+    for (int i = tid; i < M * D; i += W * 32) {
+      const int r = i / D, e = i % D, row = rt * M + r;
+      if (row >= rows) break;
+      float top = jm[r];
+#pragma unroll
+      for (int w = 1; w < W; ++w) top = fmaxf(top, jm[w * M + r]);
+      float sum = 0.f, acc = 0.f;
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        const float f = exp2f(jm[w * M + r] - top);
+        sum += f * jl[w * M + r];
+        acc += f * jo[(w * M + r) * D + e];
+      }
+      if (alone) {
+        const int t = row / k.G, head = h * k.G + row % k.G;
+        static_cast<__nv_bfloat16 *>(a.out)[(((size_t)b * a.H + head) * a.T + t) * D + e] =
+            __float2bfloat16_rn(sum == 0.f ? 0.f : acc / sum);
+      } else {
+        part[r * D + e] = acc;
+        if (e == 0) {
+          part[M * D + r] = top;
+          part[M * D + M + r] = sum;
+        }
+      }
+    }
+    u = seg0 + to;
+  }
+}
+
+// A block per (row of a tile, tile, kv head) and sequence: adds what the blocks
+// of the line left of a segment.
+template <int D>
+__global__ void __launch_bounds__(256) k12_join_kernel(const __grid_constant__ TreeK k) {
+  constexpr int L = D / 4, GROUPS = 256 / L;
+  __shared__ long long sh[8];
+  __shared__ float wt[152 * 2 + 1], red[2][8];
+  __shared__ float4 acc_s[256];
+  const TreeArgs &a = k.a;
+  const int b = blockIdx.y, tid = threadIdx.x;
+  const Seq s = seq_of(k, b);
+  const int rows = s.n * k.G;
+  const int row = blockIdx.x % (a.T * k.G), h = blockIdx.x / (a.T * k.G);
+  // What the earlier kernel wrote is read after this; every block waits, so that
+  // the end of this kernel is the end of both.
+  if (row >= rows) {  // also a sequence without units
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
+  }
+  const Line line = line_of(k, b, 0, sh);
+  const int nb = line_blocks(k, line.total);
+  const int rt = row / k.M, r = row % k.M;
+  const long long s0 = line.begin + ((long long)h * s.tiles + rt) * s.units;
+  const int c0 = block_of(s0, line.total, nb), c1 = block_of(s0 + s.units - 1, line.total, nb);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (c0 == c1) return;  // written by its block
+  const int n = c1 - c0 + 1, M = k.M;
+  // the first block left it as its last segment (1), the others as their first (0)
+  auto part = [&](int i) {
+    return k.part + ((size_t)(c0 + i) * 2 + (i == 0)) * M * (D + 2);
+  };
+  float top = -FLT_MAX;
+  for (int i = tid; i < n; i += 256) top = fmaxf(top, part(i)[M * D + r]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+  if (tid % 32 == 0) red[0][tid / 32] = top;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 8; ++w) top = fmaxf(top, red[0][w]);
+  float sum = 0.f;
+  for (int i = tid; i < n; i += 256) {
+    const float *p = part(i);
+    const float f = exp2f(p[M * D + r] - top);
+    wt[i] = f;
+    sum += f * p[M * D + M + r];
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+  if (tid % 32 == 0) red[1][tid / 32] = sum;
+  __syncthreads();
+  sum = 0.f;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) sum += red[1][w];
+  const int e = tid % L, grp = tid / L;
+  float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int i = grp; i < n; i += GROUPS) {
+    const float4 y = *reinterpret_cast<const float4 *>(part(i) + r * D + e * 4);
+    const float f = wt[i];
+    x.x += f * y.x, x.y += f * y.y, x.z += f * y.z, x.w += f * y.w;
+  }
+  acc_s[tid] = x;
+  __syncthreads();
+  if (tid < L) {
+#pragma unroll
+    for (int w = 1; w < GROUPS; ++w) {
+      const float4 y = acc_s[w * L + tid];
+      x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+    }
+    const float inv = 1.f / sum;
+    if (sum == 0.f) x = make_float4(0.f, 0.f, 0.f, 0.f);
+    else x.x *= inv, x.y *= inv, x.z *= inv, x.w *= inv;
+    const int t = row / k.G, head = h * k.G + row % k.G;
+    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) +
+                               (((size_t)b * a.H + head) * a.T + t) * D + e * 4) =
+        make_uint2(pack_bf16(x.x, x.y), pack_bf16(x.z, x.w));
+  }
+}
+
+constexpr int kSMs = 152;
+constexpr int kMaxM = 32;
+
+template <int F, int D, int MT>
+cudaError_t launch_mt(TreeK k, cudaStream_t st) {
+  using C = Cfg<F, D, MT>;
+  k.M = C::kM;
+  k.warps = C::kWarps;
+  k.blocks = kSMs * C::kCtas;
+  // no more blocks than the table has room for units
+  const long long most = (long long)k.a.c.batch * k.a.c.Hkv * ((k.a.T * k.G + k.M - 1) / k.M) *
+                         (((long long)k.a.c.max_pages * k.a.c.page + kUnit - 1) / kUnit);
+  const long long need = (most + k.warps - 1) / k.warps;
+  if (need < k.blocks) k.blocks = (int)need;
+  auto fn = k12_tree_kernel<F, D, MT>;
+  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (e != cudaSuccess) return e;
+  fn<<<k.blocks, C::kWarps * 32, C::kSmem, st>>>(k);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(k.a.T * k.a.H), (unsigned)k.a.c.batch);
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k12_join_kernel<D>, k);
+}
+
+template <int F>
+cudaError_t launch_f(const TreeK &k, cudaStream_t st) {
+  const bool one = k.a.T * k.G <= 16;
+  if (k.a.c.d == 64) return one ? launch_mt<F, 64, 1>(k, st) : launch_mt<F, 64, 2>(k, st);
+  return one ? launch_mt<F, 128, 1>(k, st) : launch_mt<F, 128, 2>(k, st);
 }
 
 }  // namespace
 
-size_t tree_workspace_bytes(const fs_cache &, int, int) { return 256; }
+size_t tree_workspace_bytes(const fs_cache &c, int, int) {
+  return (size_t)kSMs * 2 * 2 * kMaxM * (c.d + 2) * sizeof(float);
+}
 
 cudaError_t launch_tree(const TreeArgs &a, cudaStream_t st) {
-  return a.c.d == 64 ? launch_simple<64>(a, st) : launch_simple<128>(a, st);
+  TreeK k{};
+  k.a = a;
+  k.G = a.H / a.c.Hkv;
+  k.part = static_cast<float *>(a.ws);
+  switch (a.c.format) {
+    case FS_CACHE_BF16: return launch_f<FS_CACHE_BF16>(k, st);
+    case FS_CACHE_E4M3: return launch_f<FS_CACHE_E4M3>(k, st);
+    case FS_CACHE_INT8: return launch_f<FS_CACHE_INT8>(k, st);
+    default: return launch_f<FS_CACHE_INT4>(k, st);
+  }
 }
 
 }  // namespace fs
