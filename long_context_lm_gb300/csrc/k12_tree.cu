@@ -34,6 +34,8 @@
 // lazily: a row's reference moves only when a score passes it by 8 (log2).
 #include <float.h>
 
+#include <type_traits>
+
 #include "cache.cuh"
 #include "tc05.cuh"
 
@@ -137,21 +139,25 @@ __device__ __forceinline__ int block_of(long long u, long long total, int n) {
 // ---------------------------------------------------------------------------
 // fragments
 // ---------------------------------------------------------------------------
+// c = a b, or c += a b (a first product takes zeros in place of c, which costs
+// no moves).
 template <bool BF>
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
-                                         uint32_t b1) {
+                                         uint32_t b1, bool add = true) {
+  const float z0 = add ? c[0] : 0.f, z1 = add ? c[1] : 0.f, z2 = add ? c[2] : 0.f,
+              z3 = add ? c[3] : 0.f;
   if constexpr (BF)
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-        "{%8,%9}, {%0,%1,%2,%3};\n"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%10,%11,%12,%13};\n"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(z0), "f"(z1), "f"(z2),
+          "f"(z3));
   else
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-        "{%8,%9}, {%0,%1,%2,%3};\n"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%10,%11,%12,%13};\n"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(z0), "f"(z1), "f"(z2),
+          "f"(z3));
 }
 
 __device__ __forceinline__ uint32_t h2add(uint32_t a, uint32_t b) {
@@ -163,10 +169,12 @@ __device__ __forceinline__ uint32_t h2fma(uint32_t a, uint32_t b, uint32_t c) {
                       *reinterpret_cast<__half2 *>(&c));
   return *reinterpret_cast<uint32_t *>(&r);
 }
-__device__ __forceinline__ uint32_t e4m3_h2(uint32_t two) {
-  const __half2_raw h =
-      __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(two & 0xffffu), __NV_E4M3);
-  return (uint32_t)h.x | ((uint32_t)h.y << 16);
+// Four e4m3 codes -> two fp16 pairs.
+__device__ __forceinline__ void e4m3_h2(uint32_t w, uint32_t &a, uint32_t &b) {
+  asm("{\n .reg .b16 lo, hi;\n mov.b32 {lo, hi}, %2;\n cvt.rn.f16x2.e4m3x2 %0, lo;\n"
+      " cvt.rn.f16x2.e4m3x2 %1, hi;\n}\n"
+      : "=r"(a), "=r"(b)
+      : "r"(w));
 }
 // fp16 numbers with a code in their lowest bits: 0x6400 is 1024, whose step is 1.
 constexpr uint32_t kMagic = 0x64006400u;
@@ -174,12 +182,21 @@ constexpr uint32_t kSub128 = 0xe480e480u;  // -(1024 + 128)
 constexpr uint32_t kSub8 = 0xe408e408u;    // -(1024 + 8)
 constexpr uint32_t kSixteenth = 0x2c002c00u;
 constexpr uint32_t kSub72 = 0xd480d480u;   // -(64 + 8)
-// Nibbles 0 and 4, or 1 and 5, of codes with their sign bit flipped (code + 8).
+// Nibbles 0 and 4, or 1 and 5, with their sign bits flipped (code + 8) in the
+// same step that puts them into the magic number.
 __device__ __forceinline__ uint32_t nib_even(uint32_t x) {
-  return h2add((x & 0x000f000fu) | kMagic, kSub8);
+  return h2add((x & 0x000f000fu) ^ 0x64086408u, kSub8);
 }
 __device__ __forceinline__ uint32_t nib_odd(uint32_t x) {
-  return h2fma((x & 0x00f000f0u) | kMagic, kSixteenth, kSub72);
+  return h2fma((x & 0x00f000f0u) ^ 0x64806480u, kSixteenth, kSub72);
+}
+
+// (x, y) *= (a, b) and (x, y) = (x, y) * m + c on packed fp32 pairs.
+__device__ __forceinline__ void mul2(float &x, float &y, float a, float b) {
+  unsigned long long r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(f2_bits(x, y)), "l"(f2_bits(a, b)));
+  x = __uint_as_float((uint32_t)r);
+  y = __uint_as_float((uint32_t)(r >> 32));
 }
 
 template <int F, int D, int MT>
@@ -238,14 +255,13 @@ __device__ __forceinline__ void k_regs(const uint32_t *w, int s, uint32_t &b0, u
     b0 = w[2 * s];
     b1 = w[2 * s + 1];
   } else if constexpr (F == FS_CACHE_E4M3) {
-    b0 = e4m3_h2(w[s]);
-    b1 = e4m3_h2(w[s] >> 16);
+    e4m3_h2(w[s], b0, b1);
   } else if constexpr (F == FS_CACHE_INT8) {
     const uint32_t x = w[s] ^ 0x80808080u;
     b0 = h2add(__byte_perm(x, kMagic, 0x7170), kSub128);
     b1 = h2add(__byte_perm(x, kMagic, 0x7372), kSub128);
   } else {
-    const uint32_t x = (w[s / 2] ^ 0x88888888u) >> (8 * (s % 2));
+    const uint32_t x = w[s / 2] >> (8 * (s % 2));
     b0 = nib_even(x);
     b1 = nib_odd(x);
   }
@@ -259,9 +275,7 @@ __device__ __forceinline__ void v_regs(const uint32_t *x, const uint32_t *y, int
     r0 = __byte_perm(x[j], y[j], 0x5410);
     r1 = __byte_perm(x[j], y[j], 0x7632);
   } else if constexpr (F == FS_CACHE_E4M3) {
-    const uint32_t z = __byte_perm(x[j / 2], y[j / 2], j % 2 ? 0x7362 : 0x5140);
-    r0 = e4m3_h2(z);
-    r1 = e4m3_h2(z >> 16);
+    e4m3_h2(__byte_perm(x[j / 2], y[j / 2], j % 2 ? 0x7362 : 0x5140), r0, r1);
   } else if constexpr (F == FS_CACHE_INT8) {
     const uint32_t z = __byte_perm(x[j / 2], y[j / 2], j % 2 ? 0x7362 : 0x5140) ^ 0x80808080u;
     r0 = h2add(__byte_perm(z, kMagic, 0x7170), kSub128);
@@ -269,7 +283,7 @@ __device__ __forceinline__ void v_regs(const uint32_t *x, const uint32_t *y, int
   } else {
     // byte j of both keys: its low and high nibble
     const uint32_t sel = (uint32_t)(j % 4) * 0x0011u + (uint32_t)(4 + j % 4) * 0x1100u;
-    const uint32_t z = __byte_perm(x[j / 4], y[j / 4], sel) ^ 0x88888888u;
+    const uint32_t z = __byte_perm(x[j / 4], y[j / 4], sel);
     r0 = nib_even(z);
     r1 = nib_odd(z);
   }
@@ -395,7 +409,7 @@ k12_tree_kernel(const __grid_constant__ TreeK k) {
           // the largest magnitude goes to [2^14, 2^15)
           f = __uint_as_float((uint32_t)min(254, 268 - (int)(most >> 7)) << 23);
         }
-        rf[mt][hf] = a.scale * kLog2e * (1.f / f);
+        rf[mt][hf] = fmaxf(a.scale * kLog2e * (1.f / f), FLT_MIN);
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
@@ -409,9 +423,13 @@ k12_tree_kernel(const __grid_constant__ TreeK k) {
     if (a.window)
       for (int r = 0; r < M; ++r) lead = max(lead, row_first[r] == INT_MAX ? 0 : row_first[r]);
 
-    float o[MT][NT][4] = {}, m[MT][2], l[MT][2] = {};
+    // reference, the product that passes it too far, sum (of even and odd keys)
+    float o[MT][NT][4] = {}, m[MT][2], thr[MT][2], l[MT][2][2] = {};
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) m[mt][0] = m[mt][1] = -FLT_MAX;
+    for (int mt = 0; mt < MT; ++mt) {
+      m[mt][0] = m[mt][1] = -FLT_MAX;
+      thr[mt][0] = thr[mt][1] = -INFINITY;
+    }
     float vref = 0x1p-126f;
 
     // page of keys [16 i, 16 i + 16) of unit x in lane i (i < 2)
@@ -427,38 +445,56 @@ k12_tree_kernel(const __grid_constant__ TreeK k) {
       }
       return page;
     };
+    // the lane's first row and piece of a unit, in the cache and in the ring
+    const size_t page_bytes = 2 * v_off * C::kRow;
+    const char *lane_src = static_cast<const char *>(a.c.codes) + (size_t)h * a.c.page * C::kRow +
+                           (lane / P) * C::kRow + (lane % P) * 16;
+    const float *lane_scale = C::kBF ? nullptr : a.c.scales + (size_t)h * a.c.page + (lane & 15);
     auto issue = [&](int x, int stage, int page) {
       if (x < to) {
         const int key0 = s.first + x * kUnit;
         const uint32_t dst = ring_s + stage * C::kStage;
-        size_t row[2];
+        const char *src[2];
         bool ok[2];
+        int mine = 0;  // page of the lane's scale
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const int pg = __shfl_sync(~0u, page, i);
+          int pg = __shfl_sync(~0u, page, i);
           ok[i] = pg >= 0;
-          row[i] = cache_row(a.c, ok[i] ? pg : 0, 0, h, (key0 + 16 * i) & (a.c.page - 1));
+          pg = ok[i] ? pg : 0;
+          src[i] = lane_src + pg * page_bytes + ((key0 + 16 * i) & (a.c.page - 1)) * C::kRow;
+          if (i == lane >> 4) mine = pg;
         }
-        const char *codes = static_cast<const char *>(a.c.codes);
-#pragma unroll
-        for (int i = 0; i < P; ++i) {
-          const int r = (lane + 32 * i) / P, piece = (lane + 32 * i) % P;
-          const int half = i * 2 / P;  // of the unit; the same for all lanes
-          const bool in = ok[half] && key0 + r < s.end;
-          const char *src = codes + (row[half] + (r - 16 * half)) * C::kRow + piece * 16;
-          cp_async16z(dst + k_place<P>(r, piece) * 16, in ? src : codes, in ? 16 : 0);
-          src += v_off * C::kRow;
-          cp_async16z(dst + C::kCodes + v_place<P>(r, piece) * 16, in ? src : codes, in ? 16 : 0);
-        }
-        const int half = lane >> 4;
-        const bool in = (half ? ok[1] : ok[0]) && key0 + lane < s.end;
-        if constexpr (!C::kBF) {
-          const float *src = a.c.scales + (half ? row[1] : row[0]) + (lane & 15);
-          const uint32_t to_s = dst + 2 * C::kCodes + lane * 4;
-          cp_async4z(to_s, in ? src : a.c.scales, in ? 4 : 0);
-          cp_async4z(to_s + 4 * kUnit, in ? src + v_off : a.c.scales, in ? 4 : 0);
-        }
+        const bool in = ((lane >> 4) ? ok[1] : ok[0]) && key0 + lane < s.end;
         const uint32_t valid = __ballot_sync(~0u, in);
+        if (valid == ~0u) {
+#pragma unroll
+          for (int i = 0; i < P; ++i) {
+            const int r = lane / P + 32 / P * i;
+            const char *from_k = src[i * 2 / P] + (32 / P * i - 16 * (i * 2 / P)) * C::kRow;
+            cp_async16z(dst + k_place<P>(r, lane % P) * 16, from_k, 16);
+            cp_async16z(dst + C::kCodes + v_place<P>(r, lane % P) * 16, from_k + v_off * C::kRow, 16);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < P; ++i) {
+            const int r = lane / P + 32 / P * i;
+            const bool have = valid >> r & 1;  // else zeros, and nothing is read
+            const char *from_k = have ? src[i * 2 / P] + (32 / P * i - 16 * (i * 2 / P)) * C::kRow
+                                      : static_cast<const char *>(a.c.codes);
+            cp_async16z(dst + k_place<P>(r, lane % P) * 16, from_k, have ? 16 : 0);
+            cp_async16z(dst + C::kCodes + v_place<P>(r, lane % P) * 16,
+                        have ? from_k + v_off * C::kRow : from_k, have ? 16 : 0);
+          }
+        }
+        if constexpr (!C::kBF) {
+          const float *sp = in ? lane_scale + mine * 2 * v_off +
+                                     ((key0 + (lane & 16)) & (a.c.page - 1))
+                               : a.c.scales;
+          const uint32_t to_s = dst + 2 * C::kCodes + lane * 4;
+          cp_async4z(to_s, sp, in ? 4 : 0);
+          cp_async4z(to_s + 4 * kUnit, in ? sp + v_off : sp, in ? 4 : 0);
+        }
         if (lane == 0)
           *reinterpret_cast<uint32_t *>(ring + stage * C::kStage + 2 * C::kCodes + 8 * kUnit) = valid;
       }
@@ -489,7 +525,7 @@ k12_tree_kernel(const __grid_constant__ TreeK k) {
       const int key0 = s.first + x * kUnit;
       const bool whole = valid == ~0u && key0 + kUnit <= s.past && key0 >= lead;
 
-      float sc[MT][4][4] = {};
+      float sc[MT][4][4];
 #pragma unroll
       for (int nt = 0; nt < 4; ++nt) {
         constexpr int KW = D * C::kBits / 128;  // words of a lane: a quarter of the row
@@ -506,10 +542,10 @@ k12_tree_kernel(const __grid_constant__ TreeK k) {
           uint32_t b0, b1;
           k_regs<F>(w, ks, b0, b1);
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) mma16816<C::kBF>(sc[mt][nt], q[mt][ks], b0, b1);
+          for (int mt = 0; mt < MT; ++mt) mma16816<C::kBF>(sc[mt][nt], q[mt][ks], b0, b1, ks > 0);
         }
       }
-      // scores in log2 units, masks, the rows' references
+      // scales, masks, the rows' references
       float vf[4][2];  // value scales over vref
       const float *kscale = reinterpret_cast<const float *>(st + 2 * C::kCodes);
       if constexpr (!C::kBF) {
@@ -527,28 +563,26 @@ k12_tree_kernel(const __grid_constant__ TreeK k) {
 #pragma unroll
               for (int e = 0; e < 4; ++e) o[mt][i][e] *= back;
         }
-        const float inv = 1.f / vref;
+        const float inv = __uint_as_float(0x7f000000u - __float_as_uint(vref));  // a power of two
 #pragma unroll
         for (int nt = 0; nt < 4; ++nt) {
           const float2 ks = *reinterpret_cast<const float2 *>(kscale + nt * 8 + 2 * c);
           const float2 vs = *reinterpret_cast<const float2 *>(kscale + kUnit + nt * 8 + 2 * c);
-          vf[nt][0] = vs.x * inv;
-          vf[nt][1] = vs.y * inv;
+          vf[nt][0] = vs.x;
+          vf[nt][1] = vs.y;
+          mul2(vf[nt][0], vf[nt][1], inv, inv);
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
-            sc[mt][nt][0] *= ks.x;
-            sc[mt][nt][1] *= ks.y;
-            sc[mt][nt][2] *= ks.x;
-            sc[mt][nt][3] *= ks.y;
+            mul2(sc[mt][nt][0], sc[mt][nt][1], ks.x, ks.y);
+            mul2(sc[mt][nt][2], sc[mt][nt][3], ks.x, ks.y);
           }
         }
       }
-      bool raise = false;
+      if (!whole) {
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          if (!whole) {
+          for (int hf = 0; hf < 2; ++hf) {
             const uint64_t bits = row_bits[mt * 16 + hf * 8 + g];
             const int first = row_first[mt * 16 + hf * 8 + g];
 #pragma unroll
@@ -558,37 +592,39 @@ k12_tree_kernel(const __grid_constant__ TreeK k) {
                 const int at = nt * 8 + 2 * c + e, key = key0 + at;
                 const bool see = (valid >> at & 1) &&
                                  (key < s.past ? key >= first : (bool)(bits >> (key - s.past) & 1));
-                float &y = sc[mt][nt][2 * hf + e];
-                y = see ? y * rf[mt][hf] : -INFINITY;
+                if (!see) sc[mt][nt][2 * hf + e] = -INFINITY;
               }
-          } else {
-#pragma unroll
-            for (int nt = 0; nt < 4; ++nt)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) sc[mt][nt][2 * hf + e] *= rf[mt][hf];
           }
-          float top = sc[mt][0][2 * hf];
+      }
+      bool raise = false;
 #pragma unroll
-          for (int nt = 0; nt < 4; ++nt)
+      for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) top = fmaxf(top, sc[mt][nt][2 * hf + e]);
-          raise = raise || top > m[mt][hf] + kRaise;
+        for (int hf = 0; hf < 2; ++hf) {
+          const float *y = &sc[mt][0][2 * hf];
+          float top = fmaxf(y[0], y[1]);
+#pragma unroll
+          for (int nt = 1; nt < 4; ++nt) top = max3f(top, sc[mt][nt][2 * hf], sc[mt][nt][2 * hf + 1]);
+          raise = raise || top > thr[mt][hf];
         }
       if (__any_sync(~0u, raise)) {
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
-            float top = m[mt][hf];
+            float top = -INFINITY;
 #pragma unroll
             for (int nt = 0; nt < 4; ++nt)
 #pragma unroll
               for (int e = 0; e < 2; ++e) top = fmaxf(top, sc[mt][nt][2 * hf + e]);
             top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
             top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+            top = fmaxf(m[mt][hf], top * rf[mt][hf]);
             const float back = exp2f(m[mt][hf] - top);
             m[mt][hf] = top;
-            l[mt][hf] *= back;
+            if (top > -FLT_MAX) thr[mt][hf] = (top + kRaise) / rf[mt][hf];
+            l[mt][hf][0] *= back;
+            l[mt][hf][1] *= back;
 #pragma unroll
             for (int i = 0; i < NT; ++i) {
               o[mt][i][2 * hf] *= back;
@@ -598,26 +634,34 @@ k12_tree_kernel(const __grid_constant__ TreeK k) {
       }
       // probabilities, at most 2^15 (fp16) or 1 (bf16)
       constexpr float kLift = C::kBF ? -kRaise : 15.f - kRaise;
+      auto weigh = [&](auto masked) {
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          const float ref = m[mt][hf] - kLift;
+          for (int hf = 0; hf < 2; ++hf) {
+            const float ref = kLift - m[mt][hf];
 #pragma unroll
-          for (int nt = 0; nt < 4; ++nt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float &y = sc[mt][nt][2 * hf + e];
-              const float p = tc::ex2(y - ref);
-              l[mt][hf] += p;
-              if constexpr (C::kBF) {
-                y = p;
-              } else {
-                // (a masked key's scale may be NaN)
-                y = whole || y != -INFINITY ? p * vf[nt][e] : 0.f;
+            for (int nt = 0; nt < 4; ++nt) {
+              float &x = sc[mt][nt][2 * hf], &y = sc[mt][nt][2 * hf + 1];
+              const bool sx = x != -INFINITY, sy = y != -INFINITY;
+              fma2(x, y, x, y, rf[mt][hf], ref);
+              x = tc::ex2(x);
+              y = tc::ex2(y);
+              add2(l[mt][hf][0], l[mt][hf][1], x, y);
+              if constexpr (!C::kBF) {
+                mul2(x, y, vf[nt][0], vf[nt][1]);
+                if constexpr (masked.value) {  // (a masked key's scale may be NaN)
+                  x = sx ? x : 0.f;
+                  y = sy ? y : 0.f;
+                }
               }
             }
-        }
+          }
+      };
+      if (C::kBF || whole)
+        weigh(std::false_type());
+      else
+        weigh(std::true_type());
 
       const char *vs = st + C::kCodes;
       bool plain = true;
@@ -727,7 +771,7 @@ k12_tree_kernel(const __grid_constant__ TreeK k) {
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
-        float sum = l[mt][hf];
+        float sum = l[mt][hf][0] + l[mt][hf][1];
         sum += __shfl_xor_sync(~0u, sum, 1);
         sum += __shfl_xor_sync(~0u, sum, 2);
         const int r = warp * M + mt * 16 + hf * 8 + g;
