@@ -1,15 +1,6 @@
 // cache.cuh -- the paged cache's formats and addressing, shared by the kernels
 // that write it, read it and attend over it.
-//
-// Codes come from exact quotients.  With bf16 inputs Q x has at most 17
-// significant bits and amax 8, so a quotient Q x / amax that is not exactly on
-// a border between two codes is at least 2^-17 (relative) away from it: any
-// quotient good to 2^-20 falls on the right side, and only an exact border
-// needs an exact quotient, which correctly rounded division gives (the border
-// is representable).
 #pragma once
-
-#include <cuda_fp8.h>
 
 #include "fs_common.cuh"
 
@@ -57,11 +48,12 @@ __device__ __forceinline__ size_t cache_row(const fs_cache &c, int page, int par
   return (((size_t)page * 2 + part) * c.Hkv + h) * (size_t)c.page + row;
 }
 
-// Two codes -> two floats.
-__device__ __forceinline__ float2 e4m3x2(uint32_t two) {
-  const __half2_raw h =
-      __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(two & 0xffffu), __NV_E4M3);
-  return __half22float2(*reinterpret_cast<const __half2 *>(&h));
+// Four e4m3 codes -> two fp16 pairs.
+__device__ __forceinline__ void e4m3_h2(uint32_t w, uint32_t &a, uint32_t &b) {
+  asm("{\n .reg .b16 lo, hi;\n mov.b32 {lo, hi}, %2;\n cvt.rn.f16x2.e4m3x2 %0, lo;\n"
+      " cvt.rn.f16x2.e4m3x2 %1, hi;\n}\n"
+      : "=r"(a), "=r"(b)
+      : "r"(w));
 }
 
 // Eight consecutive elements of a row from their packed codes (16, 8 or 4
@@ -76,33 +68,26 @@ __device__ __forceinline__ void decode8(const uint32_t (&c)[4], float (&x)[8]) {
     }
   } else if constexpr (F == FS_CACHE_E4M3) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = e4m3x2(c[i / 2] >> (16 * (i % 2)));
-      x[2 * i] = f.x;
-      x[2 * i + 1] = f.y;
+    for (int i = 0; i < 2; ++i) {
+      uint32_t h[2];
+      e4m3_h2(c[i], h[0], h[1]);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[j]));
+        x[4 * i + 2 * j] = f.x;
+        x[4 * i + 2 * j + 1] = f.y;
+      }
     }
   } else if constexpr (F == FS_CACHE_INT8) {
+    // 2^23 + (code + 128), an exact fp32 number, less 2^23 + 128
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = (float)(int8_t)(c[i / 4] >> (8 * (i % 4)));
+    for (int i = 0; i < 8; ++i)
+      x[i] = __uint_as_float(__byte_perm(c[i / 4] ^ 0x80808080u, 0x4b000000u, 0x7440 + i % 4)) -
+             8388736.f;
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = (float)((int32_t)(c[0] << (28 - 4 * i)) >> 28);
-  }
-}
-
-// Eight elements' code words of row `index`, element offset e (a multiple of 8).
-template <int F>
-__device__ __forceinline__ void load8(const fs_cache &c, size_t index, int e, uint32_t (&w)[4]) {
-  constexpr int kBits = Fmt<F>::kBits;
-  const char *p = static_cast<const char *>(c.codes) + (index * c.d + e) / 8 * kBits;
-  if constexpr (kBits == 16) {
-    const uint4 u = *reinterpret_cast<const uint4 *>(p);
-    w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
-  } else if constexpr (kBits == 8) {
-    const uint2 u = *reinterpret_cast<const uint2 *>(p);
-    w[0] = u.x, w[1] = u.y;
-  } else {
-    w[0] = *reinterpret_cast<const uint32_t *>(p);
+    for (int i = 0; i < 8; ++i)
+      x[i] = __uint_as_float((c[0] >> (4 * i) & 15u) ^ 0x4b000008u) - 8388616.f;
   }
 }
 

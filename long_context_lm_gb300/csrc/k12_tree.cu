@@ -83,46 +83,61 @@ __device__ __forceinline__ bool seq_outside(const TreeK &k, int b) {
   return n > 0 && (past < 0 || (long long)past + n > (long long)k.a.c.max_pages * k.a.c.page);
 }
 
-// Length of the line, and where sequence `want` begins in it (or, with
-// want < 0, the sequence that holds unit `at` and its beginning).  Called by
-// all threads of a block; `sh` is shared memory of 4 long longs a warp.
+// Length of the line, and of the one sequence that `pick(total, b, begin, end)`
+// chooses (the units [begin, end) are its own) the number, beginning and sizes.
+// Called by all threads of a block.
 struct Line {
   long long total, begin;
   int b;
+  Seq s;
 };
-__device__ Line line_of(const TreeK &k, int want, long long at, long long *sh) {
+template <class Pick>
+__device__ __forceinline__ Line line_of(const TreeK &k, const Pick &pick) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
-  Line out{0, 0, 0};
-  __shared__ long long found[2];
-  for (int b0 = 0; b0 < k.a.c.batch; b0 += blockDim.x) {
-    const int b = b0 + tid;
-    long long u = 0;
-    if (b < k.a.c.batch) u = seq_units(k, seq_of(k, b));
-    long long x = u;
+  __shared__ long long sh[8];
+  __shared__ Line found;
+  const bool once = k.a.c.batch <= (int)blockDim.x;
+  long long total = 0;
+#pragma unroll 1
+  for (int round = once ? 1 : 0; round < 2; ++round) {  // a long batch goes through twice
+    long long before_all = 0;
+#pragma unroll 1
+    for (int b0 = 0; b0 < k.a.c.batch; b0 += blockDim.x) {
+      const int b = b0 + tid;
+      Seq s{};
+      long long u = 0;
+      if (b < k.a.c.batch) {
+        s = seq_of(k, b);
+        u = seq_units(k, s);
+      }
+      long long x = u;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(~0u, x, o);
-      if (lane >= o) x += y;
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(~0u, x, o);
+        if (lane >= o) x += y;
+      }
+      if (b0) __syncthreads();
+      if (lane == 31) sh[warp] = x;
+      __syncthreads();
+      long long all = 0;
+      for (int w = 0; w < nw; ++w) {
+        if (w < warp) x += sh[w];
+        all += sh[w];
+      }
+      x += before_all;
+      before_all += all;
+      if (once) total = all;
+      if (round == 1 && b < k.a.c.batch && pick(total, b, x - u, x)) {
+        found.b = b;
+        found.begin = x - u;
+        found.s = s;
+      }
     }
+    total = before_all;
     __syncthreads();
-    if (lane == 31) sh[warp] = x;
-    __syncthreads();
-    long long before = out.total, all = 0;
-    for (int w = 0; w < nw; ++w) {
-      if (w < warp) before += sh[w];
-      all += sh[w];
-    }
-    x += before;  // inclusive
-    if (b < k.a.c.batch && (want >= 0 ? b == want : (at >= x - u && at < x))) {
-      found[0] = b;
-      found[1] = x - u;
-    }
-    out.total += all;
   }
-  __syncthreads();
-  out.b = (int)found[0];
-  out.begin = found[1];
-  __syncthreads();
+  Line out = found;
+  out.total = total;
   return out;
 }
 
@@ -169,13 +184,6 @@ __device__ __forceinline__ uint32_t h2fma(uint32_t a, uint32_t b, uint32_t c) {
                       *reinterpret_cast<__half2 *>(&c));
   return *reinterpret_cast<uint32_t *>(&r);
 }
-// Four e4m3 codes -> two fp16 pairs.
-__device__ __forceinline__ void e4m3_h2(uint32_t w, uint32_t &a, uint32_t &b) {
-  asm("{\n .reg .b16 lo, hi;\n mov.b32 {lo, hi}, %2;\n cvt.rn.f16x2.e4m3x2 %0, lo;\n"
-      " cvt.rn.f16x2.e4m3x2 %1, hi;\n}\n"
-      : "=r"(a), "=r"(b)
-      : "r"(w));
-}
 // fp16 numbers with a code in their lowest bits: 0x6400 is 1024, whose step is 1.
 constexpr uint32_t kMagic = 0x64006400u;
 constexpr uint32_t kSub128 = 0xe480e480u;  // -(1024 + 128)
@@ -220,14 +228,36 @@ struct Cfg {
   static_assert(kStages >= 2 && kSmem <= kRoom, "ring");
 };
 
-// Element of a head that lane column c (lane % 4) holds as element e (0..3: low
-// and high half of the first, then the second register) of k step s.
+// The lane's registers of one row of q, two for every k step.  Lane column c
+// (lane % 4) holds the elements that its key words hold:
+//   bf16          8-element pieces c, c + 4, ...
+//   8 bits        16-element pieces c, c + 4
+//   4 bits        elements D / 4 c ..., in every eight the pairs (0, 4), (1, 5),
+//                 (2, 6), (3, 7)
 template <int F, int D>
-__device__ __forceinline__ int k_element(int c, int s, int e) {
-  if constexpr (F == FS_CACHE_BF16) return 8 * (c + 4 * (s / 2)) + (s % 2) * 4 + e;
-  if constexpr (F == FS_CACHE_INT4)
-    return D / 4 * c + 8 * (s / 2) + 2 * (s % 2) + (e / 2) + 4 * (e % 2);
-  return 16 * (c + 4 * (s / 4)) + 4 * (s % 4) + e;
+__device__ __forceinline__ void q_words(const uint16_t *row, int c, bool live,
+                                        uint32_t (&raw)[D / 16][2]) {
+  constexpr int N = D / 8;  // words of a lane: a quarter of the row
+  uint32_t w[N];
+#pragma unroll
+  for (int i = 0; i < N / 4; ++i) {
+    const int piece = F == FS_CACHE_BF16   ? c + 4 * i
+                      : F == FS_CACHE_INT4 ? N / 4 * c + i
+                                           : 2 * (c + 4 * (i / 2)) + i % 2;
+    uint4 u = make_uint4(0, 0, 0, 0);
+    if (live) u = *reinterpret_cast<const uint4 *>(row + piece * 8);
+    w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
+  }
+#pragma unroll
+  for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      if constexpr (F == FS_CACHE_INT4)
+        raw[ks][e] = __byte_perm(w[4 * (ks / 2) + ks % 2], w[4 * (ks / 2) + 2 + ks % 2],
+                                 e ? 0x7632 : 0x5410);
+      else
+        raw[ks][e] = w[2 * ks + e];
+    }
 }
 // Element that column n of value tile i stands for.
 template <int F, int D>
@@ -319,7 +349,6 @@ k12_tree_kernel(const __grid_constant__ TreeK k) {
   constexpr int P = C::P, W = C::kWarps, M = C::kM, NS = C::kStages;
   constexpr int KS = D / 16, NT = D / 8;  // k steps of a score, value tiles
   extern __shared__ __align__(128) char smem[];
-  __shared__ long long sh[8];
   __shared__ uint64_t row_bits[M];
   __shared__ int row_first[M];
   const TreeArgs &a = k.a;
@@ -327,20 +356,24 @@ k12_tree_kernel(const __grid_constant__ TreeK k) {
   const int shift = 31 - __clz(a.c.page);
   asm volatile("griddepcontrol.launch_dependents;");
 
-  Line line = line_of(k, 0, 0, sh);
-  const long long total = line.total;
   if (blockIdx.x == 0)
-    for (int b = tid; b < a.c.batch; b += W * 32)
-      if (a.c.status && seq_outside(k, b)) atomicCAS(a.c.status, 0, FS_ERR_CACHE);
+    for (int i = tid; i < a.c.batch; i += W * 32)
+      if (a.c.status && seq_outside(k, i)) atomicCAS(a.c.status, 0, FS_ERR_CACHE);
+  const Line line = line_of(k, [&](long long total, int, long long x, long long y) {
+    if (total == 0) return false;
+    const int n = line_blocks(k, total);
+    const long long at = blockIdx.x * total / n;
+    return (int)blockIdx.x < n && at >= x && at < y;
+  });
+  const long long total = line.total;
   if (total == 0) return;
   const int nb = line_blocks(k, total);
   if ((int)blockIdx.x >= nb) return;
-  const long long u0 = (long long)blockIdx.x * total / nb;
-  const long long u1 = (long long)(blockIdx.x + 1) * total / nb;
-  line = line_of(k, -1, u0, sh);
+  const long long u0 = blockIdx.x * total / nb;
+  const long long u1 = (blockIdx.x + 1) * total / nb;
   int b = line.b;
   long long begin = line.begin;  // of sequence b
-  Seq s = seq_of(k, b);
+  Seq s = line.s;
 
   char *ring = smem + warp * (C::kStage * NS);
   const uint32_t ring_s = smem_u32(ring);
@@ -359,79 +392,7 @@ k12_tree_kernel(const __grid_constant__ TreeK k) {
     const int from = (int)(u - seg0), to = (int)min((long long)s.units, u1 - seg0);
     const int rows = s.n * k.G;
 
-    // what every row sees: its bits, and its first key of the prefix
-    __syncthreads();
-    if (tid < M) {
-      const int r = rt * M + tid;
-      uint64_t bits = 0;
-      int first = INT_MAX;
-      if (r < rows) {
-        const int t = r / k.G;
-        bits = a.tree ? (uint64_t)a.tree[(size_t)b * a.T + t] : ~0ull >> (63 - t);
-        if (s.n < 64) bits &= (1ull << s.n) - 1;
-        first = a.window ? max(0, s.past + __popcll(bits) - a.window) : 0;
-      }
-      row_bits[tid] = bits;
-      row_first[tid] = first;
-    }
-    __syncthreads();
-
-    // q: fragments of the lane's rows
-    uint32_t q[MT][KS][4];
-    float rf[MT][2];  // score of the fragments' product -> log2 units
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        const int r = rt * M + mt * 16 + hf * 8 + g;
-        const bool live = r < rows;
-        const int t = live ? r / k.G : 0, head = h * k.G + (live ? r % k.G : 0);
-        const uint16_t *src = static_cast<const uint16_t *>(a.q) +
-                              (((size_t)b * a.H + head) * a.T + t) * D;
-        uint32_t raw[KS][2];
-        uint32_t most = 0;
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            uint32_t lo = 0, hi = 0;
-            if (live) {
-              lo = src[k_element<F, D>(c, ks, 2 * e)];
-              hi = src[k_element<F, D>(c, ks, 2 * e + 1)];
-            }
-            raw[ks][e] = lo | (hi << 16);
-            most = max(most, max(lo & 0x7fffu, hi & 0x7fffu));
-          }
-        float f = 1.f;
-        if constexpr (!C::kBF) {
-          most = max(most, __shfl_xor_sync(~0u, most, 1));
-          most = max(most, __shfl_xor_sync(~0u, most, 2));
-          // the largest magnitude goes to [2^14, 2^15)
-          f = __uint_as_float((uint32_t)min(254, 268 - (int)(most >> 7)) << 23);
-        }
-        rf[mt][hf] = fmaxf(a.scale * kLog2e * (1.f / f), FLT_MIN);
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            uint32_t x = raw[ks][e];
-            if constexpr (!C::kBF) x = pack_f16(bf16_lo(x) * f, bf16_hi(x) * f);
-            q[mt][ks][2 * e + hf] = x;
-          }
-      }
-    int lead = 0;  // no row's prefix begins later
-    if (a.window)
-      for (int r = 0; r < M; ++r) lead = max(lead, row_first[r] == INT_MAX ? 0 : row_first[r]);
-
-    // reference, the product that passes it too far, sum (of even and odd keys)
-    float o[MT][NT][4] = {}, m[MT][2], thr[MT][2], l[MT][2][2] = {};
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      m[mt][0] = m[mt][1] = -FLT_MAX;
-      thr[mt][0] = thr[mt][1] = -INFINITY;
-    }
-    float vref = 0x1p-126f;
-
+    __syncthreads();  // the ring held the last segment's results
     // page of keys [16 i, 16 i + 16) of unit x in lane i (i < 2)
     auto pages_of = [&](int x) -> int {
       int page = -1;
@@ -510,6 +471,72 @@ k12_tree_kernel(const __grid_constant__ TreeK k) {
       issue(next, i, now);
       next += W;
     }
+    // what every row sees: its bits, and its first key of the prefix
+    if (tid < M) {
+      const int r = rt * M + tid;
+      uint64_t bits = 0;
+      int first = INT_MAX;
+      if (r < rows) {
+        const int t = r / k.G;
+        bits = a.tree ? (uint64_t)a.tree[(size_t)b * a.T + t] : ~0ull >> (63 - t);
+        if (s.n < 64) bits &= (1ull << s.n) - 1;
+        first = a.window ? max(0, s.past + __popcll(bits) - a.window) : 0;
+      }
+      row_bits[tid] = bits;
+      row_first[tid] = first;
+    }
+    __syncthreads();
+
+    // q: fragments of the lane's rows
+    uint32_t q[MT][KS][4];
+    float rf[MT][2];  // score of the fragments' product -> log2 units
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        const int r = rt * M + mt * 16 + hf * 8 + g;
+        const bool live = r < rows;
+        const int t = live ? r / k.G : 0, head = h * k.G + (live ? r % k.G : 0);
+        const uint16_t *src = static_cast<const uint16_t *>(a.q) +
+                              (((size_t)b * a.H + head) * a.T + t) * D;
+        uint32_t raw[KS][2];
+        q_words<F, D>(src, c, live, raw);
+        uint32_t most = 0;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) most = __vmaxu2(most, raw[ks][e] & 0x7fff7fffu);
+        most = max(most & 0xffffu, most >> 16);
+        float f = 1.f;
+        if constexpr (!C::kBF) {
+          most = max(most, __shfl_xor_sync(~0u, most, 1));
+          most = max(most, __shfl_xor_sync(~0u, most, 2));
+          // the largest magnitude goes to [2^14, 2^15)
+          f = __uint_as_float((uint32_t)min(254, 268 - (int)(most >> 7)) << 23);
+        }
+        rf[mt][hf] = fmaxf(a.scale * kLog2e * (1.f / f), FLT_MIN);
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            uint32_t x = raw[ks][e];
+            if constexpr (!C::kBF) x = pack_f16(bf16_lo(x) * f, bf16_hi(x) * f);
+            q[mt][ks][2 * e + hf] = x;
+          }
+      }
+    int lead = 0;  // no row's prefix begins later
+    if (a.window)
+      for (int r = 0; r < M; ++r) lead = max(lead, row_first[r] == INT_MAX ? 0 : row_first[r]);
+
+    // reference, the product that passes it too far, sum (of even and odd keys)
+    float o[MT][NT][4] = {}, m[MT][2], thr[MT][2], l[MT][2][2] = {};
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      m[mt][0] = m[mt][1] = -FLT_MAX;
+      thr[mt][0] = thr[mt][1] = -INFINITY;
+    }
+    float vref = 0x1p-126f;
+
     int stage = 0;
     for (int x = from + warp; x < to; x += W) {
       {
@@ -643,7 +670,7 @@ k12_tree_kernel(const __grid_constant__ TreeK k) {
 #pragma unroll
             for (int nt = 0; nt < 4; ++nt) {
               float &x = sc[mt][nt][2 * hf], &y = sc[mt][nt][2 * hf + 1];
-              const bool sx = x != -INFINITY, sy = y != -INFINITY;
+              [[maybe_unused]] const bool sx = x != -INFINITY, sy = y != -INFINITY;
               fma2(x, y, x, y, rf[mt][hf], ref);
               x = tc::ex2(x);
               y = tc::ex2(y);
@@ -823,26 +850,22 @@ k12_tree_kernel(const __grid_constant__ TreeK k) {
 template <int D>
 __global__ void __launch_bounds__(256) k12_join_kernel(const __grid_constant__ TreeK k) {
   constexpr int L = D / 4, GROUPS = 256 / L;
-  __shared__ long long sh[8];
   __shared__ float wt[152 * 2 + 1], red[2][8];
   __shared__ float4 acc_s[256];
   const TreeArgs &a = k.a;
   const int b = blockIdx.y, tid = threadIdx.x;
-  const Seq s = seq_of(k, b);
-  const int rows = s.n * k.G;
   const int row = blockIdx.x % (a.T * k.G), h = blockIdx.x / (a.T * k.G);
+  const Line line = line_of(k, [&](long long, int i, long long, long long) { return i == b; });
+  const Seq s = line.s;
   // What the earlier kernel wrote is read after this; every block waits, so that
   // the end of this kernel is the end of both.
-  if (row >= rows) {  // also a sequence without units
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    return;
-  }
-  const Line line = line_of(k, b, 0, sh);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int rows = s.n * k.G;
+  if (row >= rows) return;  // also a sequence without units
   const int nb = line_blocks(k, line.total);
   const int rt = row / k.M, r = row % k.M;
   const long long s0 = line.begin + ((long long)h * s.tiles + rt) * s.units;
   const int c0 = block_of(s0, line.total, nb), c1 = block_of(s0 + s.units - 1, line.total, nb);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (c0 == c1) return;  // written by its block
   const int n = c1 - c0 + 1, M = k.M;
   // the first block left it as its last segment (1), the others as their first (0)
