@@ -535,7 +535,8 @@ int fs_rope(const void *q, void *q_out, int Hq, const long long *q_strides,
  *           here (fs_check_status reads it).  The caller zeroes it; no call
  *           clears it.  May be NULL.
  * page: 16, 32, 64, 128 or 256; d: 64 or 128; codes 16-byte aligned; batch *
- * Hkv < 2^16, max_pages * page <= 2^30; other sizes give FS_ERR_UNSUPPORTED (non-positive ones FS_ERR_INVALID_ARG).
+ * Hkv < 2^16, max_pages * page <= 2^30, pages * Hkv * page < 2^34; other sizes
+ * give FS_ERR_UNSUPPORTED (non-positive ones FS_ERR_INVALID_ARG).
  * Sequences may share pages to read; two that write one row race. */
 typedef enum {
   FS_CACHE_BF16 = 0,

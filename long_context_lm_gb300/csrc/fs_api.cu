@@ -846,6 +846,8 @@ int check_cache(const fs_cache *c) {
   if (c->d != 64 && c->d != 128) return FS_ERR_UNSUPPORTED;
   if ((long long)c->batch * c->Hkv > 65535) return FS_ERR_UNSUPPORTED;
   if ((long long)c->max_pages * c->page > (1ll << 30)) return FS_ERR_UNSUPPORTED;
+  // rows in groups of sixteen are counted in 32 bits
+  if ((double)c->pages * 2 * c->Hkv * (c->page / 16) >= 2147483648.0) return FS_ERR_UNSUPPORTED;
   return FS_OK;
 }
 

@@ -33,6 +33,7 @@
 // values as a bf16 pair (high and low part, 2^-16).  The maximum follows
 // lazily: a row's reference moves only when a score passes it by 8 (log2).
 #include <float.h>
+#include <limits.h>
 
 #include <type_traits>
 
@@ -44,6 +45,7 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kUnit = 32;        // keys of a unit
+constexpr uint32_t kNone = ~0u;
 constexpr float kRaise = 8.f;    // how far a score may pass its reference (log2)
 
 // ---------------------------------------------------------------------------
@@ -94,7 +96,34 @@ struct Line {
 template <class Pick>
 __device__ __forceinline__ Line line_of(const TreeK &k, const Pick &pick) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
-  __shared__ long long sh[8];
+  if (k.a.c.batch <= 32) {  // every warp for itself
+    Seq s{};
+    long long u = 0;
+    if (lane < k.a.c.batch) {
+      s = seq_of(k, lane);
+      u = seq_units(k, s);
+    }
+    long long x = u;
+#pragma unroll 1
+    for (int o = 1; o < k.a.c.batch; o <<= 1) {
+      const long long y = __shfl_up_sync(~0u, x, o);
+      if (lane >= o) x += y;
+    }
+    Line out;
+    out.total = __shfl_sync(~0u, x, k.a.c.batch - 1);
+    const uint32_t mine =
+        __ballot_sync(~0u, lane < k.a.c.batch && pick(out.total, lane, x - u, x));
+    out.b = mine ? __ffs(mine) - 1 : 0;
+    out.begin = __shfl_sync(~0u, x - u, out.b);
+    out.s.past = __shfl_sync(~0u, s.past, out.b);
+    out.s.n = __shfl_sync(~0u, s.n, out.b);
+    out.s.first = __shfl_sync(~0u, s.first, out.b);
+    out.s.end = __shfl_sync(~0u, s.end, out.b);
+    out.s.units = __shfl_sync(~0u, s.units, out.b);
+    out.s.tiles = __shfl_sync(~0u, s.tiles, out.b);
+    return out;
+  }
+  __shared__ long long sh[16];
   __shared__ Line found;
   const bool once = k.a.c.batch <= (int)blockDim.x;
   long long total = 0;
@@ -141,15 +170,28 @@ __device__ __forceinline__ Line line_of(const TreeK &k, const Pick &pick) {
   return out;
 }
 
-// Blocks that share the line: at least a unit for every warp.
-__device__ __forceinline__ int line_blocks(const TreeK &k, long long total) {
-  const long long n = (total + k.warps - 1) / k.warps;
-  return (int)(n < k.blocks ? (n < 1 ? 1 : n) : k.blocks);
+// a / b; nearly always both fit 32 bits, whose division is several times faster.
+__device__ __forceinline__ long long quot(long long a, int b) {
+  return a >> 32 ? a / b : (long long)((uint32_t)a / (uint32_t)b);
 }
-// The block that holds unit u: blocks begin at floor(c total / n).
-__device__ __forceinline__ int block_of(long long u, long long total, int n) {
-  return (int)(((u + 1) * n - 1) / total);
-}
+// How the line is shared: at most one block for every W units (one for each
+// warp); the first `more` blocks have a unit more than the others.
+struct Share {
+  int blocks, more;
+  long long each;
+  __device__ __forceinline__ Share(const TreeK &k, long long total) {
+    const long long n = quot(total + k.warps - 1, k.warps);
+    blocks = (int)(n < k.blocks ? (n < 1 ? 1 : n) : k.blocks);
+    each = quot(total, blocks);
+    more = (int)(total - each * blocks);
+  }
+  __device__ __forceinline__ long long begin(int c) const { return c * each + min(c, more); }
+  // the block that holds unit u
+  __device__ __forceinline__ int of(long long u) const {
+    const long long first = more * (each + 1);
+    return (int)(u < first ? u / (each + 1) : more + (u - first) / each);
+  }
+};
 
 // ---------------------------------------------------------------------------
 // fragments
@@ -184,19 +226,31 @@ __device__ __forceinline__ uint32_t h2fma(uint32_t a, uint32_t b, uint32_t c) {
                       *reinterpret_cast<__half2 *>(&c));
   return *reinterpret_cast<uint32_t *>(&r);
 }
-// fp16 numbers with a code in their lowest bits: 0x6400 is 1024, whose step is 1.
-constexpr uint32_t kMagic = 0x64006400u;
+// Constants that stay in registers: the compiler would load one of the two that
+// most of these operations take anew for every one of them.
+struct Magic {
+  uint32_t even, odd;   // nibbles 0 and 4, 1 and 5
+  uint32_t magic;       // fp16 1024, whose step is 1
+  uint32_t sixteenth, sub72;
+};
+__device__ __forceinline__ Magic make_magic() {
+  Magic m;
+  asm volatile("mov.b32 %0, 0x000f000f;" : "=r"(m.even));
+  asm volatile("mov.b32 %0, 0x00f000f0;" : "=r"(m.odd));
+  asm volatile("mov.b32 %0, 0x64006400;" : "=r"(m.magic));
+  asm volatile("mov.b32 %0, 0x2c002c00;" : "=r"(m.sixteenth));
+  asm volatile("mov.b32 %0, 0xd480d480;" : "=r"(m.sub72));  // -(64 + 8)
+  return m;
+}
 constexpr uint32_t kSub128 = 0xe480e480u;  // -(1024 + 128)
 constexpr uint32_t kSub8 = 0xe408e408u;    // -(1024 + 8)
-constexpr uint32_t kSixteenth = 0x2c002c00u;
-constexpr uint32_t kSub72 = 0xd480d480u;   // -(64 + 8)
 // Nibbles 0 and 4, or 1 and 5, with their sign bits flipped (code + 8) in the
 // same step that puts them into the magic number.
-__device__ __forceinline__ uint32_t nib_even(uint32_t x) {
-  return h2add((x & 0x000f000fu) ^ 0x64086408u, kSub8);
+__device__ __forceinline__ uint32_t nib_even(const Magic &m, uint32_t x) {
+  return h2add((x & m.even) ^ 0x64086408u, kSub8);
 }
-__device__ __forceinline__ uint32_t nib_odd(uint32_t x) {
-  return h2fma((x & 0x00f000f0u) ^ 0x64806480u, kSixteenth, kSub72);
+__device__ __forceinline__ uint32_t nib_odd(const Magic &m, uint32_t x) {
+  return h2fma((x & m.odd) ^ 0x64806480u, m.sixteenth, m.sub72);
 }
 
 // (x, y) *= (a, b) and (x, y) = (x, y) * m + c on packed fp32 pairs.
@@ -213,7 +267,7 @@ struct Cfg {
   static constexpr int kRow = D * kBits / 8;  // bytes of a row
   static constexpr int P = kRow / 16;         // 16-byte pieces of a row
   static constexpr int kM = 16 * MT;
-  static constexpr int kWarps = kRow >= 256 ? 4 : 8;
+  static constexpr int kWarps = kRow >= 256 ? 4 : D == 128 && MT == 1 ? 12 : 8;
   static constexpr int kCodes = kUnit * kRow;  // bytes of a unit's keys
   // keys, values, 32 + 32 scales, which keys can be read
   static constexpr int kStage = 2 * kCodes + 8 * kUnit + 16;
@@ -221,7 +275,7 @@ struct Cfg {
   static constexpr int kRoom = (kCtas == 2 ? 110 : 220) * 1024;
   static constexpr int kFit = kRoom / (kStage * kWarps);
   static constexpr int kStages = kFit > 6 ? 6 : kFit;
-  static constexpr int kJoin = kWarps * kM * (D + 2) * 4;  // the warps' results
+  static constexpr int kJoin = kWarps * kM * (D + 6) * 4;  // the warps' results
   static constexpr int kRing = kStage * kWarps * kStages;
   static constexpr int kSmem = kRing > kJoin ? kRing : kJoin;
   static constexpr bool kBF = F == FS_CACHE_BF16;
@@ -278,9 +332,17 @@ __device__ __forceinline__ int v_place(int r, int piece) {
   return (r * P + piece) ^ (P >= 4 ? 2 * ((r >> 1) & 3) : 2 * ((r >> 2) & 1));
 }
 
-// The k step's two key registers from the lane's code words.
+// The k step's two key registers from the lane's code words.  Integer codes go
+// in as code + bias (128 or 8), the bits of an fp16 subnormal: (code + bias)
+// 2^-24, of an odd nibble 16 times that, which its elements of q make up for.
+// The bias is the same for all keys of a row of q and leaves with one addition.
+// (It costs the fp32 sum at most two bits; the values' codes below, whose sum
+// runs over all keys, go in without one.)
 template <int F>
-__device__ __forceinline__ void k_regs(const uint32_t *w, int s, uint32_t &b0, uint32_t &b1) {
+constexpr float kBias = F == FS_CACHE_INT8 ? 128.f : F == FS_CACHE_INT4 ? 8.f : 0.f;
+template <int F>
+__device__ __forceinline__ void k_regs(const Magic &m, const uint32_t *w, int s, uint32_t &b0,
+                                       uint32_t &b1) {
   if constexpr (F == FS_CACHE_BF16) {
     b0 = w[2 * s];
     b1 = w[2 * s + 1];
@@ -288,19 +350,19 @@ __device__ __forceinline__ void k_regs(const uint32_t *w, int s, uint32_t &b0, u
     e4m3_h2(w[s], b0, b1);
   } else if constexpr (F == FS_CACHE_INT8) {
     const uint32_t x = w[s] ^ 0x80808080u;
-    b0 = h2add(__byte_perm(x, kMagic, 0x7170), kSub128);
-    b1 = h2add(__byte_perm(x, kMagic, 0x7372), kSub128);
+    b0 = __byte_perm(x, 0, 0x4140);
+    b1 = __byte_perm(x, 0, 0x4342);
   } else {
     const uint32_t x = w[s / 2] >> (8 * (s % 2));
-    b0 = nib_even(x);
-    b1 = nib_odd(x);
+    b0 = (x & m.even) ^ 0x00080008u;
+    b1 = (x & m.odd) ^ 0x00800080u;
   }
 }
 // Value register(s) of two keys' words: the elements 2 j and 2 j + 1 of the
 // lane's 8 (of word set x, y), each paired over the two keys.
 template <int F>
-__device__ __forceinline__ void v_regs(const uint32_t *x, const uint32_t *y, int j, uint32_t &r0,
-                                       uint32_t &r1) {
+__device__ __forceinline__ void v_regs(const Magic &m, const uint32_t *x, const uint32_t *y, int j,
+                                       uint32_t &r0, uint32_t &r1) {
   if constexpr (F == FS_CACHE_BF16) {
     r0 = __byte_perm(x[j], y[j], 0x5410);
     r1 = __byte_perm(x[j], y[j], 0x7632);
@@ -308,19 +370,25 @@ __device__ __forceinline__ void v_regs(const uint32_t *x, const uint32_t *y, int
     e4m3_h2(__byte_perm(x[j / 2], y[j / 2], j % 2 ? 0x7362 : 0x5140), r0, r1);
   } else if constexpr (F == FS_CACHE_INT8) {
     const uint32_t z = __byte_perm(x[j / 2], y[j / 2], j % 2 ? 0x7362 : 0x5140) ^ 0x80808080u;
-    r0 = h2add(__byte_perm(z, kMagic, 0x7170), kSub128);
-    r1 = h2add(__byte_perm(z, kMagic, 0x7372), kSub128);
+    r0 = h2add(__byte_perm(z, m.magic, 0x7170), kSub128);
+    r1 = h2add(__byte_perm(z, m.magic, 0x7372), kSub128);
   } else {
     // byte j of both keys: its low and high nibble
     const uint32_t sel = (uint32_t)(j % 4) * 0x0011u + (uint32_t)(4 + j % 4) * 0x1100u;
     const uint32_t z = __byte_perm(x[j / 4], y[j / 4], sel);
-    r0 = nib_even(z);
-    r1 = nib_odd(z);
+    r0 = nib_even(m, z);
+    r1 = nib_odd(m, z);
   }
 }
 
 __device__ __forceinline__ void cp_async16z(uint32_t dst, const void *src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(bytes));
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst), "l"(src));
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n" ::"r"(dst), "l"(src));
 }
 __device__ __forceinline__ void cp_async4z(uint32_t dst, const void *src, int bytes) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(dst), "l"(src), "r"(bytes));
@@ -337,6 +405,17 @@ __device__ __forceinline__ void lds_words(const char *p, uint32_t *w) {
     const uint4 u = *reinterpret_cast<const uint4 *>(p);
     w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
   }
+}
+
+// Elements e .. e + 3 of a row's output; zeros where the row sees nothing.
+template <int D>
+__device__ __forceinline__ void put_row(const TreeK &k, int b, int h, int row, int e, float4 x,
+                                        float sum) {
+  const int t = row / k.G, head = h * k.G + row % k.G;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(k.a.out) +
+                             (((size_t)b * k.a.H + head) * k.a.T + t) * D + e) =
+      make_uint2(pack_bf16(x.x * inv, x.y * inv), pack_bf16(x.z * inv, x.w * inv));
 }
 
 // ---------------------------------------------------------------------------
@@ -361,23 +440,25 @@ k12_tree_kernel(const __grid_constant__ TreeK k) {
       if (a.c.status && seq_outside(k, i)) atomicCAS(a.c.status, 0, FS_ERR_CACHE);
   const Line line = line_of(k, [&](long long total, int, long long x, long long y) {
     if (total == 0) return false;
-    const int n = line_blocks(k, total);
-    const long long at = blockIdx.x * total / n;
-    return (int)blockIdx.x < n && at >= x && at < y;
+    const Share share(k, total);
+    const long long at = share.begin(blockIdx.x);
+    return (int)blockIdx.x < share.blocks && at >= x && at < y;
   });
   const long long total = line.total;
   if (total == 0) return;
-  const int nb = line_blocks(k, total);
-  if ((int)blockIdx.x >= nb) return;
-  const long long u0 = blockIdx.x * total / nb;
-  const long long u1 = (blockIdx.x + 1) * total / nb;
+  const Share share(k, total);
+  if ((int)blockIdx.x >= share.blocks) return;
+  const long long u0 = share.begin(blockIdx.x), u1 = share.begin(blockIdx.x + 1);
   int b = line.b;
   long long begin = line.begin;  // of sequence b
   Seq s = line.s;
 
+  const Magic magic = make_magic();
   char *ring = smem + warp * (C::kStage * NS);
   const uint32_t ring_s = smem_u32(ring);
-  const size_t v_off = (size_t)a.c.Hkv * a.c.page;  // rows from a key to its value
+  const int v_off = a.c.Hkv * a.c.page;  // rows from a key to its value
+
+  uint32_t whole_units = 0;  // stages whose 32 keys can all be read
 
   long long u = u0;
   while (u < u1) {
@@ -393,84 +474,91 @@ k12_tree_kernel(const __grid_constant__ TreeK k) {
     const int rows = s.n * k.G;
 
     __syncthreads();  // the ring held the last segment's results
-    // page of keys [16 i, 16 i + 16) of unit x in lane i (i < 2)
-    auto pages_of = [&](int x) -> int {
-      int page = -1;
-      const int key = s.first + x * kUnit + 16 * (lane & 1);
-      if (x < to && key < s.end) {
-        page = a.c.table[(size_t)b * a.c.max_pages + (key >> shift)];
-        if (page < 0 || page >= a.c.pages) {
-          if (a.c.status) atomicCAS(a.c.status, 0, FS_ERR_CACHE);
-          page = -1;
-        }
-      }
-      return page;
+    // Where sixteen of the warp's units lie, two halves of sixteen rows to a unit:
+    // lane 2 i + j holds half j of unit x + W i, as its place among all groups of
+    // sixteen rows (kNone: nothing to read).  The table is read sixteen units
+    // ahead: a load behind the units in flight waits for them.
+    const int groups = a.c.page >> 4;
+    auto page_of = [&](int x) -> int {
+      const int key = s.first + (x + W * (lane >> 1)) * kUnit + 16 * (lane & 1);
+      return x + W * (lane >> 1) < to && key < s.end
+                 ? a.c.table[(size_t)b * a.c.max_pages + (key >> shift)]
+                 : INT_MIN;
     };
-    // the lane's first row and piece of a unit, in the cache and in the ring
-    const size_t page_bytes = 2 * v_off * C::kRow;
-    const char *lane_src = static_cast<const char *>(a.c.codes) + (size_t)h * a.c.page * C::kRow +
-                           (lane / P) * C::kRow + (lane % P) * 16;
-    const float *lane_scale = C::kBF ? nullptr : a.c.scales + (size_t)h * a.c.page + (lane & 15);
-    auto issue = [&](int x, int stage, int page) {
+    auto place_of = [&](int x, int page) -> uint32_t {
+      if ((unsigned)page >= (unsigned)a.c.pages) {
+        if (page != INT_MIN && a.c.status) atomicCAS(a.c.status, 0, FS_ERR_CACHE);
+        return kNone;
+      }
+      const int key = s.first + (x + W * (lane >> 1)) * kUnit + 16 * (lane & 1);
+      return (uint32_t)(page * 2 * a.c.Hkv + h) * groups + ((key & (a.c.page - 1)) >> 4);
+    };
+    // the lane's first row and piece of a half, and its scale
+    const char *lane_src =
+        static_cast<const char *>(a.c.codes) + (lane / P) * C::kRow + (lane % P) * 16;
+    const float *lane_scale = C::kBF ? nullptr : a.c.scales + (lane & 15);
+    auto issue = [&](int x, int stage, uint32_t place, int at) {
       if (x < to) {
-        const int key0 = s.first + x * kUnit;
         const uint32_t dst = ring_s + stage * C::kStage;
-        const char *src[2];
-        bool ok[2];
-        int mine = 0;  // page of the lane's scale
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          int pg = __shfl_sync(~0u, page, i);
-          ok[i] = pg >= 0;
-          pg = ok[i] ? pg : 0;
-          src[i] = lane_src + pg * page_bytes + ((key0 + 16 * i) & (a.c.page - 1)) * C::kRow;
-          if (i == lane >> 4) mine = pg;
-        }
-        const bool in = ((lane >> 4) ? ok[1] : ok[0]) && key0 + lane < s.end;
-        const uint32_t valid = __ballot_sync(~0u, in);
-        if (valid == ~0u) {
+        const uint32_t g0 = __shfl_sync(~0u, place, 2 * at), g1 = __shfl_sync(~0u, place, 2 * at + 1);
+        const char *src[2] = {lane_src + (size_t)g0 * (16 * C::kRow),
+                              lane_src + (size_t)g1 * (16 * C::kRow)};
+        const float *sp = nullptr;
+        const uint32_t to_s = dst + 2 * C::kCodes + lane * 4;
+        if constexpr (!C::kBF) sp = lane_scale + (size_t)(lane >> 4 ? g1 : g0) * 16;
+        if (g0 != kNone && g1 != kNone && s.first + (x + 1) * kUnit <= s.end) {
 #pragma unroll
           for (int i = 0; i < P; ++i) {
             const int r = lane / P + 32 / P * i;
             const char *from_k = src[i * 2 / P] + (32 / P * i - 16 * (i * 2 / P)) * C::kRow;
-            cp_async16z(dst + k_place<P>(r, lane % P) * 16, from_k, 16);
-            cp_async16z(dst + C::kCodes + v_place<P>(r, lane % P) * 16, from_k + v_off * C::kRow, 16);
+            cp_async16(dst + k_place<P>(r, lane % P) * 16, from_k);
+            cp_async16(dst + C::kCodes + v_place<P>(r, lane % P) * 16, from_k + v_off * C::kRow);
           }
-        } else {
+          if constexpr (!C::kBF) {
+            cp_async4(to_s, sp);
+            cp_async4(to_s + 4 * kUnit, sp + v_off);
+          }
+          whole_units |= 1u << stage;
+        } else {  // zeros for what cannot be read
+          const bool in = (lane >> 4 ? g1 : g0) != kNone && s.first + x * kUnit + lane < s.end;
+          const uint32_t valid = __ballot_sync(~0u, in);
 #pragma unroll
           for (int i = 0; i < P; ++i) {
             const int r = lane / P + 32 / P * i;
-            const bool have = valid >> r & 1;  // else zeros, and nothing is read
+            const bool have = valid >> r & 1;
             const char *from_k = have ? src[i * 2 / P] + (32 / P * i - 16 * (i * 2 / P)) * C::kRow
                                       : static_cast<const char *>(a.c.codes);
             cp_async16z(dst + k_place<P>(r, lane % P) * 16, from_k, have ? 16 : 0);
             cp_async16z(dst + C::kCodes + v_place<P>(r, lane % P) * 16,
                         have ? from_k + v_off * C::kRow : from_k, have ? 16 : 0);
           }
+          if constexpr (!C::kBF) {
+            cp_async4z(to_s, in ? sp : a.c.scales, in ? 4 : 0);
+            cp_async4z(to_s + 4 * kUnit, in ? sp + v_off : a.c.scales, in ? 4 : 0);
+          }
+          whole_units &= ~(1u << stage);
+          if (lane == 0)
+            *reinterpret_cast<uint32_t *>(ring + stage * C::kStage + 2 * C::kCodes + 8 * kUnit) =
+                valid;
         }
-        if constexpr (!C::kBF) {
-          const float *sp = in ? lane_scale + mine * 2 * v_off +
-                                     ((key0 + (lane & 16)) & (a.c.page - 1))
-                               : a.c.scales;
-          const uint32_t to_s = dst + 2 * C::kCodes + lane * 4;
-          cp_async4z(to_s, sp, in ? 4 : 0);
-          cp_async4z(to_s + 4 * kUnit, in ? sp + v_off : sp, in ? 4 : 0);
-        }
-        if (lane == 0)
-          *reinterpret_cast<uint32_t *>(ring + stage * C::kStage + 2 * C::kCodes + 8 * kUnit) = valid;
       }
       cp_async_commit();
     };
 
-    int next = from + warp;  // unit to issue
-    int page = pages_of(next);
-#pragma unroll
-    for (int i = 0; i < NS - 1; ++i) {
-      const int now = page;
-      page = pages_of(next + W);
-      issue(next, i, now);
+    int next = from + warp, at = 0;  // unit to issue, its place among sixteen
+    uint32_t place = place_of(next, page_of(next));
+    int later = page_of(next + 16 * W);
+    auto issue_next = [&](int stage) {
+      issue(next, stage, place, at);
       next += W;
-    }
+      if (++at == 16) {
+        at = 0;
+        place = place_of(next, later);
+        later = page_of(next + 16 * W);
+      }
+    };
+#pragma unroll 1
+    for (int i = 0; i < NS - 1; ++i) issue_next(i);
     // what every row sees: its bits, and its first key of the prefix
     if (tid < M) {
       const int r = rt * M + tid;
@@ -490,6 +578,7 @@ k12_tree_kernel(const __grid_constant__ TreeK k) {
     // q: fragments of the lane's rows
     uint32_t q[MT][KS][4];
     float rf[MT][2];  // score of the fragments' product -> log2 units
+    [[maybe_unused]] float bias[MT][2];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -515,14 +604,29 @@ k12_tree_kernel(const __grid_constant__ TreeK k) {
           f = __uint_as_float((uint32_t)min(254, 268 - (int)(most >> 7)) << 23);
         }
         rf[mt][hf] = fmaxf(a.scale * kLog2e * (1.f / f), FLT_MIN);
+        float sum = 0.f;
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             uint32_t x = raw[ks][e];
-            if constexpr (!C::kBF) x = pack_f16(bf16_lo(x) * f, bf16_hi(x) * f);
+            if constexpr (!C::kBF) {
+              x = pack_f16(bf16_lo(x) * f, bf16_hi(x) * f);
+              if constexpr (kBias<F> != 0.f) {
+                const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&x));
+                sum += y.x + y.y;
+              }
+              if constexpr (F == FS_CACHE_INT4)
+                if (e) x = h2fma(x, magic.sixteenth, 0u);
+            }
             q[mt][ks][2 * e + hf] = x;
           }
+        if constexpr (kBias<F> != 0.f) {
+          sum += __shfl_xor_sync(~0u, sum, 1);
+          sum += __shfl_xor_sync(~0u, sum, 2);
+          bias[mt][hf] = -0x1p-24f * kBias<F> * sum;
+          rf[mt][hf] *= 0x1p24f;
+        }
       }
     int lead = 0;  // no row's prefix begins later
     if (a.window)
@@ -539,18 +643,12 @@ k12_tree_kernel(const __grid_constant__ TreeK k) {
 
     int stage = 0;
     for (int x = from + warp; x < to; x += W) {
-      {
-        const int now = page;
-        page = pages_of(next + W);
-        issue(next, stage == 0 ? NS - 1 : stage - 1, now);
-        next += W;
-      }
+      issue_next(stage == 0 ? NS - 1 : stage - 1);
       cp_async_wait<NS - 1>();
       __syncwarp();
       const char *st = ring + stage * C::kStage;
-      const uint32_t valid = *reinterpret_cast<const uint32_t *>(st + 2 * C::kCodes + 8 * kUnit);
       const int key0 = s.first + x * kUnit;
-      const bool whole = valid == ~0u && key0 + kUnit <= s.past && key0 >= lead;
+      const bool whole = (whole_units >> stage & 1) && key0 + kUnit <= s.past && key0 >= lead;
 
       float sc[MT][4][4];
 #pragma unroll
@@ -567,7 +665,7 @@ k12_tree_kernel(const __grid_constant__ TreeK k) {
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
           uint32_t b0, b1;
-          k_regs<F>(w, ks, b0, b1);
+          k_regs<F>(magic, w, ks, b0, b1);
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) mma16816<C::kBF>(sc[mt][nt], q[mt][ks], b0, b1, ks > 0);
         }
@@ -577,10 +675,10 @@ k12_tree_kernel(const __grid_constant__ TreeK k) {
       const float *kscale = reinterpret_cast<const float *>(st + 2 * C::kCodes);
       if constexpr (!C::kBF) {
         const float mine = kscale[kUnit + lane];
-        const float top = __uint_as_float(
-            __reduce_max_sync(~0u, mine <= FLT_MAX ? __float_as_uint(mine) & 0x7fffffffu : 0u));
-        if (top > vref) {  // the same in all lanes
-          const float up = __uint_as_float((__float_as_uint(top) + 0x7fffffu) & 0x7f800000u);
+        if (__any_sync(~0u, mine > vref && mine <= FLT_MAX)) {
+          const uint32_t top =
+              __reduce_max_sync(~0u, mine <= FLT_MAX ? __float_as_uint(fmaxf(mine, 0.f)) : 0u);
+          const float up = __uint_as_float((top + 0x7fffffu) & 0x7f800000u);
           const float back = vref / up;
           vref = up;
 #pragma unroll
@@ -599,13 +697,20 @@ k12_tree_kernel(const __grid_constant__ TreeK k) {
           vf[nt][1] = vs.y;
           mul2(vf[nt][0], vf[nt][1], inv, inv);
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            mul2(sc[mt][nt][0], sc[mt][nt][1], ks.x, ks.y);
-            mul2(sc[mt][nt][2], sc[mt][nt][3], ks.x, ks.y);
-          }
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+              float &x = sc[mt][nt][2 * hf], &y = sc[mt][nt][2 * hf + 1];
+              if constexpr (kBias<F> != 0.f) add2(x, y, bias[mt][hf], bias[mt][hf]);
+              mul2(x, y, ks.x, ks.y);
+            }
         }
       }
       if (!whole) {
+        const uint32_t valid =
+            whole_units >> stage & 1
+                ? ~0u
+                : *reinterpret_cast<const uint32_t *>(st + 2 * C::kCodes + 8 * kUnit);
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -769,8 +874,8 @@ k12_tree_kernel(const __grid_constant__ TreeK k) {
 #pragma unroll
             for (int j = 0; j < NT / SETS / 2; ++j) {
               uint32_t b00, b01, b10, b11;
-              v_regs<F>(w[0], w[1], j, b00, b10);
-              v_regs<F>(w[2], w[3], j, b01, b11);
+              v_regs<F>(magic, w[0], w[1], j, b00, b10);
+              v_regs<F>(magic, w[2], w[3], j, b01, b11);
               const int i = set * (NT / SETS) + 2 * j;
 #pragma unroll
               for (int mt = 0; mt < MT; ++mt) {
@@ -792,8 +897,10 @@ k12_tree_kernel(const __grid_constant__ TreeK k) {
 
     // join the warps
     __syncthreads();
-    float *jo = reinterpret_cast<float *>(smem);  // [warp][M][D]
-    float *jm = jo + W * M * D, *jl = jm + W * M;  // [warp][M]
+    constexpr int SD = D + 4;  // (rows in different banks)
+    float *jo = reinterpret_cast<float *>(smem);  // [warp][M][SD]
+    float *jm = jo + W * M * SD, *jl = jm + W * M;  // [warp][M]
+    const int live = min(M, rows - rt * M);
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -801,45 +908,54 @@ k12_tree_kernel(const __grid_constant__ TreeK k) {
         float sum = l[mt][hf][0] + l[mt][hf][1];
         sum += __shfl_xor_sync(~0u, sum, 1);
         sum += __shfl_xor_sync(~0u, sum, 2);
-        const int r = warp * M + mt * 16 + hf * 8 + g;
+        const int row = mt * 16 + hf * 8 + g, r = warp * M + row;
+        if (row >= live) continue;
         if (c == 0) {
           jm[r] = m[mt][hf];
           jl[r] = sum;
         }
+        const float unit = C::kBF ? 1.f : vref;
 #pragma unroll
-        for (int i = 0; i < NT; ++i)
+        for (int i = 0; i < NT; i += 4)
 #pragma unroll
           for (int e = 0; e < 2; ++e)
-            jo[r * D + v_element<F, D>(2 * c + e, i)] =
-                C::kBF ? o[mt][i][2 * hf + e] : o[mt][i][2 * hf + e] * vref;
+            *reinterpret_cast<float4 *>(jo + r * SD + v_element<F, D>(2 * c + e, i)) =
+                make_float4(o[mt][i][2 * hf + e] * unit, o[mt][i + 1][2 * hf + e] * unit,
+                            o[mt][i + 2][2 * hf + e] * unit, o[mt][i + 3][2 * hf + e] * unit);
       }
     __syncthreads();
     const bool alone = from == 0 && to == s.units;
     float *part = k.part + ((size_t)blockIdx.x * 2 + (from == 0)) * M * (D + 2);
-    for (int i = tid; i < M * D; i += W * 32) {
-      const int r = i / D, e = i % D, row = rt * M + r;
-      if (row >= rows) break;
-      float top = jm[r];
+    if (tid < live) {  // a row: the warps' weights in place of their references
+      float top = jm[tid], sum = 0.f;
 #pragma unroll
-      for (int w = 1; w < W; ++w) top = fmaxf(top, jm[w * M + r]);
-      float sum = 0.f, acc = 0.f;
+      for (int w = 1; w < W; ++w) top = fmaxf(top, jm[w * M + tid]);
 #pragma unroll
       for (int w = 0; w < W; ++w) {
-        const float f = exp2f(jm[w * M + r] - top);
-        sum += f * jl[w * M + r];
-        acc += f * jo[(w * M + r) * D + e];
+        const float f = exp2f(jm[w * M + tid] - top);
+        jm[w * M + tid] = f;
+        sum += f * jl[w * M + tid];
       }
-      if (alone) {
-        const int t = row / k.G, head = h * k.G + row % k.G;
-        static_cast<__nv_bfloat16 *>(a.out)[(((size_t)b * a.H + head) * a.T + t) * D + e] =
-            __float2bfloat16_rn(sum == 0.f ? 0.f : acc / sum);
-      } else {
-        part[r * D + e] = acc;
-        if (e == 0) {
-          part[M * D + r] = top;
-          part[M * D + M + r] = sum;
-        }
+      if (!alone) {
+        part[M * D + tid] = top;
+        part[M * D + M + tid] = sum;
       }
+      jl[tid] = sum;
+    }
+    __syncthreads();
+    for (int i = tid; i < live * (D / 4); i += W * 32) {
+      const int r = i / (D / 4), e = i % (D / 4) * 4, row = rt * M + r;
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        const float f = jm[w * M + r];
+        const float4 y = *reinterpret_cast<const float4 *>(jo + (w * M + r) * SD + e);
+        x.x += f * y.x, x.y += f * y.y, x.z += f * y.z, x.w += f * y.w;
+      }
+      if (alone)
+        put_row<D>(k, b, h, row, e, x, jl[r]);
+      else
+        *reinterpret_cast<float4 *>(part + r * D + e) = x;
     }
     u = seg0 + to;
   }
@@ -862,10 +978,10 @@ __global__ void __launch_bounds__(256) k12_join_kernel(const __grid_constant__ T
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int rows = s.n * k.G;
   if (row >= rows) return;  // also a sequence without units
-  const int nb = line_blocks(k, line.total);
+  const Share share(k, line.total);
   const int rt = row / k.M, r = row % k.M;
   const long long s0 = line.begin + ((long long)h * s.tiles + rt) * s.units;
-  const int c0 = block_of(s0, line.total, nb), c1 = block_of(s0 + s.units - 1, line.total, nb);
+  const int c0 = share.of(s0), c1 = share.of(s0 + s.units - 1);
   if (c0 == c1) return;  // written by its block
   const int n = c1 - c0 + 1, M = k.M;
   // the first block left it as its last segment (1), the others as their first (0)
@@ -910,13 +1026,7 @@ __global__ void __launch_bounds__(256) k12_join_kernel(const __grid_constant__ T
       const float4 y = acc_s[w * L + tid];
       x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
     }
-    const float inv = 1.f / sum;
-    if (sum == 0.f) x = make_float4(0.f, 0.f, 0.f, 0.f);
-    else x.x *= inv, x.y *= inv, x.z *= inv, x.w *= inv;
-    const int t = row / k.G, head = h * k.G + row % k.G;
-    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) +
-                               (((size_t)b * a.H + head) * a.T + t) * D + e * 4) =
-        make_uint2(pack_bf16(x.x, x.y), pack_bf16(x.z, x.w));
+    put_row<D>(k, b, h, row, e * 4, x, sum);
   }
 }
 
