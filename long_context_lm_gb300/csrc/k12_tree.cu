@@ -32,166 +32,15 @@
 // 0 and 2^15, so that one of 2^-38 of the largest still counts; with bf16
 // values as a bf16 pair (high and low part, 2^-16).  The maximum follows
 // lazily: a row's reference moves only when a score passes it by 8 (log2).
-#include <float.h>
-#include <limits.h>
-
 #include <type_traits>
 
-#include "cache.cuh"
-#include "tc05.cuh"
+#include "tree.cuh"
 
 namespace fs {
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kUnit = 32;        // keys of a unit
+constexpr int kUnit = 32;  // keys of a unit
 constexpr uint32_t kNone = ~0u;
-constexpr float kRaise = 8.f;    // how far a score may pass its reference (log2)
-
-// ---------------------------------------------------------------------------
-// the line of units
-// ---------------------------------------------------------------------------
-struct Seq {
-  int past, n, first, end;  // prefix, drafted tokens, keys [first, end) that any row sees
-  int units, tiles;         // units of a segment, row tiles of a kv head
-};
-
-struct TreeK {
-  TreeArgs a;
-  int G, M, blocks, warps;
-  float *part;  // [blocks][2][M][D + 2]: O, m, l
-};
-
-__device__ __forceinline__ Seq seq_of(const TreeK &k, int b) {
-  Seq s;
-  const int limit = k.a.c.max_pages * k.a.c.page;  // at most 2^30
-  const int past = k.a.past[b];
-  s.n = k.a.count ? min(max(k.a.count[b], 0), k.a.T) : k.a.T;
-  s.past = min(max(past, 0), limit);
-  s.end = min(s.past + s.n, limit);
-  // (a row that sees i drafted tokens begins at past + i - window)
-  s.first = k.a.window ? max(0, s.past - k.a.window) & ~(kUnit - 1) : 0;
-  s.units = (s.end - s.first + kUnit - 1) / kUnit;
-  s.tiles = (s.n * k.G + k.M - 1) / k.M;
-  if (s.n == 0) s.units = 0;
-  return s;
-}
-__device__ __forceinline__ long long seq_units(const TreeK &k, const Seq &s) {
-  return (long long)s.units * s.tiles * k.a.c.Hkv;
-}
-__device__ __forceinline__ bool seq_outside(const TreeK &k, int b) {
-  const int past = k.a.past[b];
-  const int n = k.a.count ? min(max(k.a.count[b], 0), k.a.T) : k.a.T;
-  return n > 0 && (past < 0 || (long long)past + n > (long long)k.a.c.max_pages * k.a.c.page);
-}
-
-// Length of the line, and of the one sequence that `pick(total, b, begin, end)`
-// chooses (the units [begin, end) are its own) the number, beginning and sizes.
-// Called by all threads of a block.
-struct Line {
-  long long total, begin;
-  int b;
-  Seq s;
-};
-template <class Pick>
-__device__ __forceinline__ Line line_of(const TreeK &k, const Pick &pick) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
-  if (k.a.c.batch <= 32) {  // every warp for itself
-    Seq s{};
-    long long u = 0;
-    if (lane < k.a.c.batch) {
-      s = seq_of(k, lane);
-      u = seq_units(k, s);
-    }
-    long long x = u;
-#pragma unroll 1
-    for (int o = 1; o < k.a.c.batch; o <<= 1) {
-      const long long y = __shfl_up_sync(~0u, x, o);
-      if (lane >= o) x += y;
-    }
-    Line out;
-    out.total = __shfl_sync(~0u, x, k.a.c.batch - 1);
-    const uint32_t mine =
-        __ballot_sync(~0u, lane < k.a.c.batch && pick(out.total, lane, x - u, x));
-    out.b = mine ? __ffs(mine) - 1 : 0;
-    out.begin = __shfl_sync(~0u, x - u, out.b);
-    out.s.past = __shfl_sync(~0u, s.past, out.b);
-    out.s.n = __shfl_sync(~0u, s.n, out.b);
-    out.s.first = __shfl_sync(~0u, s.first, out.b);
-    out.s.end = __shfl_sync(~0u, s.end, out.b);
-    out.s.units = __shfl_sync(~0u, s.units, out.b);
-    out.s.tiles = __shfl_sync(~0u, s.tiles, out.b);
-    return out;
-  }
-  __shared__ long long sh[16];
-  __shared__ Line found;
-  const bool once = k.a.c.batch <= (int)blockDim.x;
-  long long total = 0;
-#pragma unroll 1
-  for (int round = once ? 1 : 0; round < 2; ++round) {  // a long batch goes through twice
-    long long before_all = 0;
-#pragma unroll 1
-    for (int b0 = 0; b0 < k.a.c.batch; b0 += blockDim.x) {
-      const int b = b0 + tid;
-      Seq s{};
-      long long u = 0;
-      if (b < k.a.c.batch) {
-        s = seq_of(k, b);
-        u = seq_units(k, s);
-      }
-      long long x = u;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(~0u, x, o);
-        if (lane >= o) x += y;
-      }
-      if (b0) __syncthreads();
-      if (lane == 31) sh[warp] = x;
-      __syncthreads();
-      long long all = 0;
-      for (int w = 0; w < nw; ++w) {
-        if (w < warp) x += sh[w];
-        all += sh[w];
-      }
-      x += before_all;
-      before_all += all;
-      if (once) total = all;
-      if (round == 1 && b < k.a.c.batch && pick(total, b, x - u, x)) {
-        found.b = b;
-        found.begin = x - u;
-        found.s = s;
-      }
-    }
-    total = before_all;
-    __syncthreads();
-  }
-  Line out = found;
-  out.total = total;
-  return out;
-}
-
-// a / b; nearly always both fit 32 bits, whose division is several times faster.
-__device__ __forceinline__ long long quot(long long a, int b) {
-  return a >> 32 ? a / b : (long long)((uint32_t)a / (uint32_t)b);
-}
-// How the line is shared: at most one block for every W units (one for each
-// warp); the first `more` blocks have a unit more than the others.
-struct Share {
-  int blocks, more;
-  long long each;
-  __device__ __forceinline__ Share(const TreeK &k, long long total) {
-    const long long n = quot(total + k.warps - 1, k.warps);
-    blocks = (int)(n < k.blocks ? (n < 1 ? 1 : n) : k.blocks);
-    each = quot(total, blocks);
-    more = (int)(total - each * blocks);
-  }
-  __device__ __forceinline__ long long begin(int c) const { return c * each + min(c, more); }
-  // the block that holds unit u
-  __device__ __forceinline__ int of(long long u) const {
-    const long long first = more * (each + 1);
-    return (int)(u < first ? u / (each + 1) : more + (u - first) / each);
-  }
-};
 
 // ---------------------------------------------------------------------------
 // fragments
@@ -215,50 +64,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
         : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(z0), "f"(z1), "f"(z2),
           "f"(z3));
-}
-
-__device__ __forceinline__ uint32_t h2add(uint32_t a, uint32_t b) {
-  __half2 r = __hadd2(*reinterpret_cast<__half2 *>(&a), *reinterpret_cast<__half2 *>(&b));
-  return *reinterpret_cast<uint32_t *>(&r);
-}
-__device__ __forceinline__ uint32_t h2fma(uint32_t a, uint32_t b, uint32_t c) {
-  __half2 r = __hfma2(*reinterpret_cast<__half2 *>(&a), *reinterpret_cast<__half2 *>(&b),
-                      *reinterpret_cast<__half2 *>(&c));
-  return *reinterpret_cast<uint32_t *>(&r);
-}
-// Constants that stay in registers: the compiler would load one of the two that
-// most of these operations take anew for every one of them.
-struct Magic {
-  uint32_t even, odd;   // nibbles 0 and 4, 1 and 5
-  uint32_t magic;       // fp16 1024, whose step is 1
-  uint32_t sixteenth, sub72;
-};
-__device__ __forceinline__ Magic make_magic() {
-  Magic m;
-  asm volatile("mov.b32 %0, 0x000f000f;" : "=r"(m.even));
-  asm volatile("mov.b32 %0, 0x00f000f0;" : "=r"(m.odd));
-  asm volatile("mov.b32 %0, 0x64006400;" : "=r"(m.magic));
-  asm volatile("mov.b32 %0, 0x2c002c00;" : "=r"(m.sixteenth));
-  asm volatile("mov.b32 %0, 0xd480d480;" : "=r"(m.sub72));  // -(64 + 8)
-  return m;
-}
-constexpr uint32_t kSub128 = 0xe480e480u;  // -(1024 + 128)
-constexpr uint32_t kSub8 = 0xe408e408u;    // -(1024 + 8)
-// Nibbles 0 and 4, or 1 and 5, with their sign bits flipped (code + 8) in the
-// same step that puts them into the magic number.
-__device__ __forceinline__ uint32_t nib_even(const Magic &m, uint32_t x) {
-  return h2add((x & m.even) ^ 0x64086408u, kSub8);
-}
-__device__ __forceinline__ uint32_t nib_odd(const Magic &m, uint32_t x) {
-  return h2fma((x & m.odd) ^ 0x64806480u, m.sixteenth, m.sub72);
-}
-
-// (x, y) *= (a, b) and (x, y) = (x, y) * m + c on packed fp32 pairs.
-__device__ __forceinline__ void mul2(float &x, float &y, float a, float b) {
-  unsigned long long r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(f2_bits(x, y)), "l"(f2_bits(a, b)));
-  x = __uint_as_float((uint32_t)r);
-  y = __uint_as_float((uint32_t)(r >> 32));
 }
 
 template <int F, int D, int MT>
@@ -405,17 +210,6 @@ __device__ __forceinline__ void lds_words(const char *p, uint32_t *w) {
     const uint4 u = *reinterpret_cast<const uint4 *>(p);
     w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
   }
-}
-
-// Elements e .. e + 3 of a row's output; zeros where the row sees nothing.
-template <int D>
-__device__ __forceinline__ void put_row(const TreeK &k, int b, int h, int row, int e, float4 x,
-                                        float sum) {
-  const int t = row / k.G, head = h * k.G + row % k.G;
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(k.a.out) +
-                             (((size_t)b * k.a.H + head) * k.a.T + t) * D + e) =
-      make_uint2(pack_bf16(x.x * inv, x.y * inv), pack_bf16(x.z * inv, x.w * inv));
 }
 
 // ---------------------------------------------------------------------------
@@ -1030,36 +824,24 @@ __global__ void __launch_bounds__(256) k12_join_kernel(const __grid_constant__ T
   }
 }
 
-constexpr int kSMs = 152;
-constexpr int kMaxM = 32;
-
 template <int F, int D, int MT>
 cudaError_t launch_mt(TreeK k, cudaStream_t st) {
   using C = Cfg<F, D, MT>;
   k.M = C::kM;
-  k.warps = C::kWarps;
-  k.blocks = kSMs * C::kCtas;
+  k.unit = kUnit;
+  k.least = C::kWarps;
+  k.blocks = kTreeSMs * C::kCtas;
   // no more blocks than the table has room for units
   const long long most = (long long)k.a.c.batch * k.a.c.Hkv * ((k.a.T * k.G + k.M - 1) / k.M) *
                          (((long long)k.a.c.max_pages * k.a.c.page + kUnit - 1) / kUnit);
-  const long long need = (most + k.warps - 1) / k.warps;
+  const long long need = (most + k.least - 1) / k.least;
   if (need < k.blocks) k.blocks = (int)need;
   auto fn = k12_tree_kernel<F, D, MT>;
   cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
   fn<<<k.blocks, C::kWarps * 32, C::kSmem, st>>>(k);
   e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(k.a.T * k.a.H), (unsigned)k.a.c.batch);
-  cfg.blockDim = dim3(256);
-  cfg.stream = st;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k12_join_kernel<D>, k);
+  return e != cudaSuccess ? e : launch_tree_join(k, st);
 }
 
 template <int F>
@@ -1071,8 +853,31 @@ cudaError_t launch_f(const TreeK &k, cudaStream_t st) {
 
 }  // namespace
 
-size_t tree_workspace_bytes(const fs_cache &c, int, int) {
-  return (size_t)kSMs * 2 * 2 * kMaxM * (c.d + 2) * sizeof(float);
+// From how many rows to a kv head on 128 of them are taken at a time.
+constexpr int kWideRows = 33;
+bool wide(const fs_cache &c, int H, int T) {
+  return c.format != FS_CACHE_BF16 && H / c.Hkv * T >= kWideRows;
+}
+
+cudaError_t launch_tree_join(const TreeK &k, cudaStream_t st) {
+  // its blocks may start, and look up their rows, while the last ones of the
+  // kernel before run
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(k.a.T * k.a.H), (unsigned)k.a.c.batch);
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return k.a.c.d == 64 ? cudaLaunchKernelEx(&cfg, k12_join_kernel<64>, k)
+                       : cudaLaunchKernelEx(&cfg, k12_join_kernel<128>, k);
+}
+
+size_t tree_workspace_bytes(const fs_cache &c, int H, int T) {
+  const int rows = wide(c, H, T) ? kTreeSMs * 128 : kTreeSMs * 2 * 32;
+  return (size_t)rows * 2 * (c.d + 2) * sizeof(float);
 }
 
 cudaError_t launch_tree(const TreeArgs &a, cudaStream_t st) {
@@ -1080,6 +885,7 @@ cudaError_t launch_tree(const TreeArgs &a, cudaStream_t st) {
   k.a = a;
   k.G = a.H / a.c.Hkv;
   k.part = static_cast<float *>(a.ws);
+  if (wide(a.c, a.H, a.T)) return launch_tree_wide(k, st);
   switch (a.c.format) {
     case FS_CACHE_BF16: return launch_f<FS_CACHE_BF16>(k, st);
     case FS_CACHE_E4M3: return launch_f<FS_CACHE_E4M3>(k, st);

@@ -1,0 +1,636 @@
+// k13_tree_wide.cu -- fs_tree_attn where many rows share their keys (a wide
+// tree, or grouped heads): 128 rows a block on the tensor cores (tcgen05).
+//
+// The line of units, its sharing and the joining of the blocks' results are
+// k12_tree.cu's; a unit here is a tile of KT keys.  A block works on one
+// segment at a time:
+//   * warps 8-11 turn codes into fp16 tiles in shared memory (exact: codes have
+//     at most 8 bits), a ring of them, with the scales beside them;
+//   * two streams of four warps take the tiles in turn, a thread a row, each
+//     stream with its own scores, probabilities, output (TMEM), running
+//     reference and sum, so that neither waits for the other;
+//   * one thread of warp 12 (13) issues the first (second) stream's products:
+//     S = Q K^T, then O += P V with P from TMEM, in two halves of the tile's
+//     keys, so that the next tile's S and the second half of P are made while
+//     the first half is multiplied.
+// The streams are joined through shared memory at the end of a segment.
+//
+// Scores, scales, references and probabilities are as in k12_tree.cu (q by a
+// power of two a row, fp16 probabilities up to 2^15, value scales relative to a
+// power of two).  A half whose scores pass their reference by more than 8 (log2)
+// raises it, multiplies the row's O by the difference once no product is under
+// way, and is done again.
+//
+// Bound by: the exponentials and the roughly five operations around each
+// (128 x KT a tile), then the products' issue.
+#include "tree.cuh"
+
+namespace fs {
+namespace {
+
+template <int F, int D>
+struct Wide {
+  static constexpr int kBits = Fmt<F>::kBits;
+  static constexpr int kRow = D * kBits / 8, P = kRow / 16;
+  static constexpr int KT = D == 64 ? 128 : 64;  // keys of a tile
+  static constexpr int kCols = D / 64;           // 64-element column blocks
+  static constexpr int kBlock = KT * 128;        // bytes of one of them
+  static constexpr int kStage = 2 * kCols * kBlock;
+  static constexpr int kStages = D == 64 ? 5 : 3;
+  static constexpr int kQ = 128 * 128 * kCols;
+  static constexpr int kMerge = 128 * (D + 2) * 4;
+  static constexpr int kSide = KT * 8 + 64;  // scales, valid words, largest value scales
+  static constexpr int kSmem =
+      1024 + kStage * kStages + kQ + kMerge + kSide * kStages + 256;
+  // TMEM columns of a stream: S, P, O
+  static constexpr int kS = 0, kP = KT, kO = KT + KT / 2, kTmem = 256;
+  static_assert(kO + D <= kTmem && kSmem <= 227 * 1024, "sizes");
+  static constexpr int NP = KT * P / 128;  // pieces of a thread, keys or values
+};
+
+// Element of a head at position i of the tiles' rows: int4 codes leave a word
+// in the order 0 4 1 5 2 6 3 7.
+template <int F>
+__device__ __forceinline__ constexpr int element_of(int i) {
+  return F == FS_CACHE_INT4 ? (i & ~7) | ((i & 7) >> 1) | ((i & 1) << 2) : i;
+}
+
+// The segments of a block, one after the other.
+struct Walk {
+  long long u, u1, begin;
+  int b;
+  Seq s;
+  int h, rt, from, to;
+  __device__ __forceinline__ bool next(const TreeK &k) {
+    if (u >= u1) return false;
+    while (u >= begin + seq_units(k, s) && b + 1 < k.a.c.batch) {
+      begin += seq_units(k, s);
+      s = seq_of(k, ++b);
+    }
+    if (s.units == 0) return false;  // (lengths that changed under the call)
+    const int seg = (int)((u - begin) / s.units);
+    const long long seg0 = begin + (long long)seg * s.units;
+    rt = seg % s.tiles;
+    h = seg / s.tiles;
+    from = (int)(u - seg0);
+    to = (int)min((long long)s.units, u1 - seg0);
+    u = seg0 + to;
+    return true;
+  }
+};
+
+struct Bars {
+  uint64_t full[5], empty[5];        // tiles
+  uint64_t s_full[2], s_free[2];     // a stream's scores
+  uint64_t p_full[2][2], p_free[2][2];  // a stream's halves of probabilities
+  uint64_t q_full, merge;
+};
+
+// Sixteen bytes of codes -> fp16, eight elements to a 16-byte chunk.
+template <int F>
+__device__ __forceinline__ void to_chunk(const Magic &m, const uint32_t *w, uint4 &x) {
+  if constexpr (F == FS_CACHE_E4M3) {
+    e4m3_h2(w[0], x.x, x.y);
+    e4m3_h2(w[1], x.z, x.w);
+  } else if constexpr (F == FS_CACHE_INT8) {
+    const uint32_t a = w[0] ^ 0x80808080u, b = w[1] ^ 0x80808080u;
+    x.x = h2add(__byte_perm(a, m.magic, 0x7170), kSub128);
+    x.y = h2add(__byte_perm(a, m.magic, 0x7372), kSub128);
+    x.z = h2add(__byte_perm(b, m.magic, 0x7170), kSub128);
+    x.w = h2add(__byte_perm(b, m.magic, 0x7372), kSub128);
+  } else {
+    x.x = nib_even(m, w[0]);
+    x.y = nib_odd(m, w[0]);
+    x.z = nib_even(m, w[0] >> 8);
+    x.w = nib_odd(m, w[0] >> 8);
+  }
+}
+
+template <int F, int D>
+__global__ void __launch_bounds__(512, 1) k13_tree_wide_kernel(const __grid_constant__ TreeK k) {
+  using C = Wide<F, D>;
+  constexpr int KT = C::KT, P = C::P, NS = C::kStages, NP = C::NP, HALF = KT / 2;
+  extern __shared__ char smem_raw[];
+  char *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  char *qs = smem + NS * C::kStage;
+  float *mo = reinterpret_cast<float *>(qs + C::kQ);  // the second stream's O [D][128]
+  float *mm = mo + 128 * D, *ml = mm + 128;
+  char *side = reinterpret_cast<char *>(ml + 128);
+  Bars &bar = *reinterpret_cast<Bars *>(side + NS * C::kSide);
+  __shared__ uint32_t tmem_base;
+  __shared__ int fail;
+  const TreeArgs &a = k.a;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  asm volatile("griddepcontrol.launch_dependents;");
+
+  if (blockIdx.x == 0)
+    for (int i = tid; i < a.c.batch; i += 512)
+      if (a.c.status && seq_outside(k, i)) atomicCAS(a.c.status, 0, FS_ERR_CACHE);
+  const Line line = line_of(k, [&](long long total, int, long long x, long long y) {
+    if (total == 0) return false;
+    const Share share(k, total);
+    const long long at = share.begin(blockIdx.x);
+    return (int)blockIdx.x < share.blocks && at >= x && at < y;
+  });
+  if (line.total == 0) return;
+  const Share share(k, line.total);
+  if ((int)blockIdx.x >= share.blocks) return;
+
+  if (tid == 0) {
+    fail = 0;
+    for (int i = 0; i < NS; ++i) {
+      tc::mbar_init(&bar.full[i], 128);
+      tc::mbar_init(&bar.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&bar.s_full[i], 1);
+      tc::mbar_init(&bar.s_free[i], 128);
+      for (int j = 0; j < 2; ++j) {
+        tc::mbar_init(&bar.p_full[i][j], 128);
+        tc::mbar_init(&bar.p_free[i][j], 1);
+      }
+    }
+    tc::mbar_init(&bar.q_full, 128);
+    tc::mbar_init(&bar.merge, 128);
+    tc::mbar_fence_init();
+  }
+  if (warp == 12) {
+    tc::tmem_alloc(&tmem_base, 512);
+    tc::tmem_relinquish();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+
+  Walk w{share.begin(blockIdx.x), share.begin(blockIdx.x + 1), line.begin, line.b, line.s, 0, 0, 0, 0};
+  // Waits give up after a limit and say so in `fail`; every role then leaves its
+  // loops for the barrier at the end.
+  auto wait_one = [&](uint64_t *b, uint32_t phase) { return tc::mbar_wait(b, phase & 1, &fail); };
+  auto wait = [&](uint64_t *b, uint32_t phase) {  // the same answer in a warp
+    return (bool)__all_sync(~0u, wait_one(b, phase));
+  };
+  int it = 0;  // tiles of the block before the current segment
+  uint32_t seg = 0;
+
+  if (warp < 8) {
+    // ------------------------------------------------------------- a stream
+    const int st = warp >> 2, row = tid & 127;
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's quarter of the lanes
+    const uint32_t tm = tmem_base + st * C::kTmem + lanes;
+    uint32_t jt = 0;  // tiles of the stream before the current one
+    bool ok = true;
+    for (; ok && w.next(k); ++seg) {
+      const int n = w.to - w.from, rows = w.s.n * k.G, r = w.rt * 128 + row;
+      const bool live = r < rows;
+      const int t = live ? r / k.G : 0, head = w.h * k.G + (live ? r % k.G : 0);
+      const size_t at = (((size_t)w.b * a.H + head) * a.T + t) * D;
+      uint64_t bits = 0;
+      int first = 0;
+      if (live) {
+        bits = a.tree ? (uint64_t)a.tree[(size_t)w.b * a.T + t] : ~0ull >> (63 - t);
+        if (w.s.n < 64) bits &= (1ull << w.s.n) - 1;
+        if (a.window) first = max(0, w.s.past + __popcll(bits) - a.window);
+      }
+      // the row's power of two; the first stream writes q
+      const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q) + at);
+      uint4 x[D / 8];
+      uint32_t most = 0;
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {
+        x[i] = live ? src[i] : make_uint4(0, 0, 0, 0);
+        most = __vmaxu2(most, x[i].x & 0x7fff7fffu);
+        most = __vmaxu2(most, x[i].y & 0x7fff7fffu);
+        most = __vmaxu2(most, x[i].z & 0x7fff7fffu);
+        most = __vmaxu2(most, x[i].w & 0x7fff7fffu);
+      }
+      most = max(most & 0xffffu, most >> 16);
+      const float f = __uint_as_float((uint32_t)min(254, 268 - (int)(most >> 7)) << 23);
+      const float rf = fmaxf(a.scale * kLog2e * (1.f / f), FLT_MIN);
+      if (st == 0) {
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          const uint32_t y[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+          uint32_t z[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int e0 = element_of<F>(2 * j), e1 = element_of<F>(2 * j + 1);
+            const float v0 = e0 % 2 ? bf16_hi(y[e0 / 2]) : bf16_lo(y[e0 / 2]);
+            const float v1 = e1 % 2 ? bf16_hi(y[e1 / 2]) : bf16_lo(y[e1 / 2]);
+            z[j] = pack_f16(v0 * f, v1 * f);
+          }
+          *reinterpret_cast<uint4 *>(qs + i / 8 * (128 * 128) + swz128(row, i % 8)) =
+              make_uint4(z[0], z[1], z[2], z[3]);
+        }
+        tc::fence_async_smem();
+        tc::mbar_arrive(&bar.q_full);
+      } else if (!(ok = wait(&bar.q_full, seg))) {  // (the last segment's results have been taken)
+        break;
+      }
+
+      float m = -FLT_MAX, thr = -INFINITY, l0 = 0.f, l1 = 0.f, vref = 0x1p-126f;
+      bool begun = false;  // O holds something
+      // O *= by, once no product is under way: those of this tile's first half
+      // and of the last tile
+      auto rescale = [&](float by, int half) -> bool {
+        if (jt > 0 || half)
+          if (!wait(&bar.p_free[st][0], half ? jt : jt - 1)) return false;
+        if (jt > 0)
+          if (!wait(&bar.p_free[st][1], jt - 1)) return false;
+        tc::fence_after_sync();
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[32];
+          tc::tmem_ld32(tm + C::kO + c, o);
+          tc::tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * by);
+          tc::tmem_st32(tm + C::kO + c, o);
+        }
+        tc::tmem_wait_st();
+        return true;
+      };
+
+      for (int i = st; ok && i < n; i += 2, ++jt) {
+        const int tile = it + i, stage = tile % NS;
+        const char *sd = side + stage * C::kSide;
+        const float *ks = reinterpret_cast<const float *>(sd), *vs = ks + KT;
+        const uint32_t *valid = reinterpret_cast<const uint32_t *>(vs + KT);
+        if (!(ok = wait(&bar.full[stage], tile / NS) && wait(&bar.s_full[st], jt))) break;
+        tc::fence_after_sync();
+        const int key0 = w.s.first + (w.from + i) * KT;
+        uint32_t all = ~0u;
+        float top_v = 0.f;
+#pragma unroll
+        for (int j = 0; j < KT / 32; ++j) {
+          all &= valid[j];
+          top_v = fmaxf(top_v, __uint_as_float(valid[KT / 32 + j]));
+        }
+        const bool whole =
+            all == ~0u && __all_sync(~0u, key0 + KT <= w.s.past && key0 >= first);
+        if (top_v > vref) {  // the same for all rows
+          const float up =
+              __uint_as_float((__float_as_uint(top_v) + 0x7fffffu) & 0x7f800000u);
+          if (begun && !(ok = rescale(vref / up, 0))) break;
+          vref = up;
+        }
+        const float inv = __uint_as_float(0x7f000000u - __float_as_uint(vref));
+
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          uint32_t p[HALF / 2];
+          float s0 = 0.f, s1 = 0.f;
+#pragma unroll 1
+          for (int tries = 0; tries < 2; ++tries) {
+            float top = -INFINITY;
+            const float ref = 15.f - kRaise - m;
+            s0 = s1 = 0.f;
+#pragma unroll
+            for (int ch = 0; ch < HALF / 32; ++ch) {
+              const int c0 = half * HALF + ch * 32;
+              uint32_t u[32];
+              tc::tmem_ld32(tm + C::kS + c0, u);
+              tc::tmem_wait_ld();
+              uint32_t seen = ~0u;  // of these 32 keys
+              if (!whole) {
+                const int key = key0 + c0;
+                seen = valid[c0 / 32];
+                const int before = min(max(w.s.past - key, 0), 32);  // keys of the prefix
+                const int skip = min(max(first - key, 0), before);   // outside the window
+                uint32_t see = before - skip == 32 ? ~0u
+                               : before > skip    ? ((1u << (before - skip)) - 1) << skip
+                                                  : 0u;
+                if (before < 32) {  // drafted: bit (key + i - past)
+                  const int j = key - w.s.past;  // of key 0; negative inside the prefix
+                  const uint64_t x = j >= 64 ? 0 : j >= 0 ? bits >> j : bits << -j;
+                  see |= (uint32_t)x & (before ? ~0u << before : ~0u);
+                }
+                seen &= see;
+              }
+              auto weigh = [&](auto masked) {
+#pragma unroll
+                for (int j = 0; j < 32; j += 4) {
+                  const float4 kk = *reinterpret_cast<const float4 *>(ks + c0 + j);
+                  const float4 vv = *reinterpret_cast<const float4 *>(vs + c0 + j);
+                  float y[4] = {__uint_as_float(u[j]), __uint_as_float(u[j + 1]),
+                                __uint_as_float(u[j + 2]), __uint_as_float(u[j + 3])};
+                  mul2(y[0], y[1], kk.x, kk.y);
+                  mul2(y[2], y[3], kk.z, kk.w);
+                  if constexpr (masked.value) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) y[e] = seen >> (j + e) & 1 ? y[e] : -INFINITY;
+                  }
+                  top = max3f(max3f(top, y[0], y[1]), y[2], y[3]);
+                  fma2(y[0], y[1], y[0], y[1], rf, ref);
+                  fma2(y[2], y[3], y[2], y[3], rf, ref);
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) y[e] = tc::ex2(y[e]);
+                  add2(s0, s1, y[0], y[1]);
+                  add2(s0, s1, y[2], y[3]);
+                  float z[4] = {vv.x, vv.y, vv.z, vv.w};
+                  mul2(z[0], z[1], inv, inv);
+                  mul2(z[2], z[3], inv, inv);
+                  mul2(y[0], y[1], z[0], z[1]);
+                  mul2(y[2], y[3], z[2], z[3]);
+                  if constexpr (masked.value) {  // (a masked key's scale may be NaN)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) y[e] = seen >> (j + e) & 1 ? y[e] : 0.f;
+                  }
+                  p[ch * 16 + j / 2] = pack_f16(y[0], y[1]);
+                  p[ch * 16 + j / 2 + 1] = pack_f16(y[2], y[3]);
+                }
+              };
+              if (whole)
+                weigh(std::false_type());
+              else
+                weigh(std::true_type());
+            }
+            if (tries || !__any_sync(~0u, top > thr)) break;
+            const float up = fmaxf(m, top * rf);
+            const float back = exp2f(m - up);
+            m = up;
+            if (up > -FLT_MAX) thr = (up + kRaise) / rf;
+            l0 *= back;
+            l1 *= back;
+            if (begun && !(ok = rescale(back, half))) break;
+          }
+          if (!ok) break;
+          l0 += s0;
+          l1 += s1;
+          if (half) {
+            tc::fence_before_sync();
+            tc::mbar_arrive(&bar.s_free[st]);
+          }
+          if (jt > 0 && !(ok = wait(&bar.p_free[st][half], jt - 1))) break;
+          tc::fence_after_sync();
+          if constexpr (HALF == 64)
+            tc::tmem_st32(tm + C::kP + half * 32, p);
+          else
+            tc::tmem_st16(tm + C::kP + half * 16, p);
+          tc::tmem_wait_st();
+          tc::fence_before_sync();
+          tc::mbar_arrive(&bar.p_full[st][half]);
+          begun = true;
+        }
+      }
+      if (!ok) break;
+      // the segment's end: all products of the stream
+      if (begun) {
+        if (!(ok = wait(&bar.p_free[st][0], jt - 1) && wait(&bar.p_free[st][1], jt - 1))) break;
+        tc::fence_after_sync();
+      }
+      const float l = l0 + l1;
+      if (st == 1) {
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[32];
+          if (begun) {
+            tc::tmem_ld32(tm + C::kO + c, o);
+            tc::tmem_wait_ld();
+          }
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            mo[(c + i) * 128 + row] = begun ? __uint_as_float(o[i]) * vref : 0.f;
+        }
+        mm[row] = m;
+        ml[row] = l;
+        tc::fence_before_sync();
+        tc::mbar_arrive(&bar.merge);
+      } else {
+        if (!(ok = wait(&bar.merge, seg))) break;
+        const float m1 = mm[row], l1_ = ml[row], top = fmaxf(m, m1);
+        const float f0 = exp2f(m - top), f1 = exp2f(m1 - top), sum = f0 * l + f1 * l1_;
+        const bool alone = w.from == 0 && w.to == w.s.units;
+        float *part = k.part + ((size_t)blockIdx.x * 2 + (w.from == 0)) * 128 * (D + 2);
+        const float unit = f0 * vref, inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[32];
+          tc::tmem_ld32(tm + C::kO + c, o);  // (the first stream has a tile of every segment)
+          tc::tmem_wait_ld();
+          float y[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            y[element_of<F>(i)] = __uint_as_float(o[i]) * unit + mo[(c + i) * 128 + row] * f1;
+          if (live && alone) {
+            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + at + c);
+#pragma unroll
+            for (int i = 0; i < 32; i += 8)
+              dst[i / 8] = make_uint4(pack_bf16(y[i] * inv, y[i + 1] * inv),
+                                      pack_bf16(y[i + 2] * inv, y[i + 3] * inv),
+                                      pack_bf16(y[i + 4] * inv, y[i + 5] * inv),
+                                      pack_bf16(y[i + 6] * inv, y[i + 7] * inv));
+          } else if (live) {
+            float4 *dst = reinterpret_cast<float4 *>(part + row * D + c);
+#pragma unroll
+            for (int i = 0; i < 32; i += 4)
+              dst[i / 4] = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
+          }
+          __syncwarp();
+        }
+        if (live && !alone) {
+          part[128 * D + row] = top;
+          part[128 * D + 128 + row] = sum;
+        }
+        tc::fence_before_sync();
+      }
+      it += n;
+    }
+  } else if (warp < 12) {
+    // -------------------------------------------------- codes -> fp16 tiles
+    const int t = tid - 256, shift = 31 - __clz(a.c.page);
+    const Magic magic = make_magic();
+    const size_t v_off = (size_t)a.c.Hkv * a.c.page;  // rows from a key to its value
+    bool ok = true;
+    while (ok && w.next(k)) {
+      // A thread's pieces lie in rows t / P + i (128 / P); its scale belongs to
+      // key t % KT (threads past KT: none, with KT = 64 the upper 64 take the
+      // values' scales).  Pages are looked up two tiles ahead of the codes,
+      // codes loaded two tiles ahead of their use.
+      struct Ahead {
+        int page[NP], page_s;
+        uint4 code[2][NP];
+        float scale[2];
+        bool in;
+      } buf[2];
+      const int key_s = t & (KT - 1);
+      auto look = [&](Ahead &x, int i) {
+        const int key0 = w.s.first + i * KT;
+        auto page = [&](int key) {
+          return i < w.to && key < w.s.end
+                     ? a.c.table[(size_t)w.b * a.c.max_pages + (key >> shift)]
+                     : INT_MIN;
+        };
+#pragma unroll
+        for (int j = 0; j < NP; ++j) x.page[j] = page(key0 + t / P + j * (128 / P));
+        x.page_s = page(key0 + key_s);
+      };
+      auto load = [&](Ahead &x, int i) {
+        const int key0 = w.s.first + i * KT;
+#pragma unroll
+        for (int j = 0; j < NP; ++j) {
+          x.code[0][j] = x.code[1][j] = make_uint4(0, 0, 0, 0);
+          if ((unsigned)x.page[j] < (unsigned)a.c.pages) {
+            const int key = key0 + t / P + j * (128 / P);
+            const size_t r = cache_row(a.c, x.page[j], 0, w.h, key & (a.c.page - 1));
+            const char *p = static_cast<const char *>(a.c.codes) + r * C::kRow + t % P * 16;
+            x.code[0][j] = *reinterpret_cast<const uint4 *>(p);
+            x.code[1][j] = *reinterpret_cast<const uint4 *>(p + v_off * C::kRow);
+          }
+        }
+        x.scale[0] = x.scale[1] = 0.f;
+        x.in = (unsigned)x.page_s < (unsigned)a.c.pages;
+        if (x.in) {
+          const size_t r = cache_row(a.c, x.page_s, 0, w.h, (key0 + key_s) & (a.c.page - 1));
+          x.scale[0] = a.c.scales[r];
+          x.scale[1] = a.c.scales[r + v_off];
+        } else if (x.page_s != INT_MIN && a.c.status) {
+          atomicCAS(a.c.status, 0, FS_ERR_CACHE);
+        }
+      };
+      auto put = [&](const Ahead &x, int tile) -> bool {
+        const int stage = tile % NS;
+        if (tile >= NS && !wait(&bar.empty[stage], tile / NS - 1)) return false;
+        char *dst = smem + stage * C::kStage;
+#pragma unroll
+        for (int part = 0; part < 2; ++part)
+#pragma unroll
+          for (int j = 0; j < NP; ++j) {
+            const int r = t / P + j * (128 / P);
+            const uint32_t wd[4] = {x.code[part][j].x, x.code[part][j].y, x.code[part][j].z,
+                                    x.code[part][j].w};
+            constexpr int CH = 128 / C::kBits / 8;  // chunks of the piece: 2 or 4
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+              const int chunk = t % P * CH + c;  // of the row's D / 8
+              uint4 y;
+              to_chunk<F>(magic, wd + c * (4 / CH), y);
+              *reinterpret_cast<uint4 *>(dst + (part * C::kCols + chunk / 8) * C::kBlock +
+                                         swz128(r, chunk % 8)) = y;
+            }
+          }
+        float *sd = reinterpret_cast<float *>(side + stage * C::kSide);
+        uint32_t *valid = reinterpret_cast<uint32_t *>(sd + 2 * KT);
+        const uint32_t in = __ballot_sync(~0u, x.in);
+        const float v = x.scale[1];
+        const uint32_t top =
+            __reduce_max_sync(~0u, v <= FLT_MAX ? __float_as_uint(fmaxf(v, 0.f)) : 0u);
+        if (t < KT) {
+          sd[t] = x.scale[0];
+          sd[KT + t] = v;
+          if (lane == 0) {
+            valid[t / 32] = in;
+            valid[KT / 32 + t / 32] = top;
+          }
+        }
+        tc::fence_async_smem();
+        tc::mbar_arrive(&bar.full[stage]);
+        return true;
+      };
+      const int n = w.to - w.from;
+      look(buf[0], w.from);
+      look(buf[1], w.from + 1);
+      load(buf[0], w.from);
+      look(buf[0], w.from + 2);
+      load(buf[1], w.from + 1);
+      look(buf[1], w.from + 3);
+#pragma unroll 1
+      for (int i = 0; ok && i < n; i += 2) {
+        if (!(ok = put(buf[0], it + i))) break;
+        load(buf[0], w.from + i + 2);
+        look(buf[0], w.from + i + 4);
+        if (i + 1 < n) {
+          if (!(ok = put(buf[1], it + i + 1))) break;
+          load(buf[1], w.from + i + 3);
+          look(buf[1], w.from + i + 5);
+        }
+      }
+      it += n;
+    }
+  } else if (warp < 14 && lane == 0) {
+    // ------------------------------------------------------ a stream's products
+    const int st = warp - 12;
+    const uint32_t tm = tmem_base + st * C::kTmem;
+    const uint32_t ring = smem_u32(smem), q = smem_u32(qs);
+    constexpr uint32_t kQK = tc::idesc_f16(128, KT, 0), kPV = tc::idesc_f16(128, 64, 1);
+    uint32_t jt = 0;
+    bool ok = true;
+    for (; ok && w.next(k); ++seg) {
+      const int n = w.to - w.from;
+      if (!(ok = wait_one(&bar.q_full, seg))) break;
+      auto scores = [&](int i, uint32_t j) -> bool {
+        const int tile = it + i, stage = tile % NS;
+        if (!wait_one(&bar.full[stage], tile / NS)) return false;
+        if (j > 0 && !wait_one(&bar.s_free[st], j - 1)) return false;
+        tc::fence_after_sync();
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s) {
+          const uint32_t off = s / 4, in = s % 4 * 32;
+          tc::mma_ss(tm + C::kS, tc::desc_sw128(q + off * (128 * 128) + in),
+                     tc::desc_sw128(ring + stage * C::kStage + off * C::kBlock + in), kQK, s > 0);
+        }
+        tc::mma_commit(&bar.s_full[st]);
+        return true;
+      };
+      if (st < n && !(ok = scores(st, jt))) break;
+      for (int i = st; i < n; i += 2, ++jt) {
+        const int stage = (it + i) % NS;
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          if (!(ok = wait_one(&bar.p_full[st][half], jt))) break;
+          tc::fence_after_sync();
+          const uint32_t v = ring + stage * C::kStage + C::kCols * C::kBlock;
+#pragma unroll
+          for (int c = 0; c < C::kCols; ++c)
+#pragma unroll
+            for (int s = 0; s < HALF / 16; ++s) {
+              const int key = half * HALF + s * 16;
+              tc::mma_ts(tm + C::kO + c * 64, tm + C::kP + key / 2,
+                         tc::desc_sw128(v + c * C::kBlock + key * 128), kPV,
+                         i != st || half || s > 0);
+            }
+          tc::mma_commit(&bar.p_free[st][half]);
+          if (half) tc::mma_commit(&bar.empty[stage]);
+          if (!half && i + 2 < n && !(ok = scores(i + 2, jt + 1))) break;
+        }
+        if (!ok) break;
+      }
+      it += n;
+    }
+  }
+  __syncthreads();
+  if (tid == 0 && fail && a.c.status) tc::report_error(a.c.status, FS_ERR_TIMEOUT);
+  __syncwarp();
+  if (warp == 12) tc::tmem_dealloc(tmem_base, 512);
+}
+
+template <int F, int D>
+cudaError_t launch_fd(TreeK k, cudaStream_t st) {
+  using C = Wide<F, D>;
+  k.M = 128;
+  k.unit = C::KT;
+  k.least = 2;
+  k.blocks = kTreeSMs;
+  auto fn = k13_tree_wide_kernel<F, D>;
+  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (e != cudaSuccess) return e;
+  fn<<<k.blocks, 512, C::kSmem, st>>>(k);
+  e = cudaGetLastError();
+  return e != cudaSuccess ? e : launch_tree_join(k, st);
+}
+
+}  // namespace
+
+cudaError_t launch_tree_wide(const TreeK &k, cudaStream_t st) {
+  const bool small = k.a.c.d == 64;
+  switch (k.a.c.format) {
+    case FS_CACHE_E4M3:
+      return small ? launch_fd<FS_CACHE_E4M3, 64>(k, st) : launch_fd<FS_CACHE_E4M3, 128>(k, st);
+    case FS_CACHE_INT8:
+      return small ? launch_fd<FS_CACHE_INT8, 64>(k, st) : launch_fd<FS_CACHE_INT8, 128>(k, st);
+    case FS_CACHE_INT4:
+      return small ? launch_fd<FS_CACHE_INT4, 64>(k, st) : launch_fd<FS_CACHE_INT4, 128>(k, st);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace fs

@@ -682,24 +682,29 @@ _Strides = ctypes.c_longlong * 3
 
 
 def _on(t, dev, name, dtype, shape=None):
-    """``t`` is a CUDA tensor of ``dtype`` on ``dev``, contiguous in ``shape`` when given."""
+    """Pointer of ``t``, a CUDA tensor of ``dtype`` on ``dev``, contiguous in ``shape`` when given."""
     if not isinstance(t, torch.Tensor) or t.device != dev:
         raise ValueError(f"{name} must be a tensor on {dev}")
     if t.dtype != dtype:
         raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if shape is not None and (tuple(t.shape) != tuple(shape) or not t.is_contiguous()):
+    if shape is not None and (t.shape != shape or not t.is_contiguous()):
         raise ValueError(f"{name} must be contiguous {list(shape)}, not {list(t.shape)}")
     return t.data_ptr()
 
 
-def _rows(t, dev, name, dtype, shape=None):
-    """Pointer and strides of a [batch, H, N, d] tensor whose d values lie together."""
-    _on(t, dev, name, dtype)
-    if t.dim() != 4 or (shape is not None and tuple(t.shape) != tuple(shape)):
-        raise ValueError(f"{name} must be {list(shape) if shape else '[batch, H, N, d]'}, "
-                         f"not {list(t.shape)}")
+def _rows(t, dev, name, dtype, shape):
+    """Pointer and strides (None: contiguous) of a [batch, H, N, d] tensor of ``shape`` whose d
+    values lie together."""
+    if not isinstance(t, torch.Tensor) or t.device != dev:
+        raise ValueError(f"{name} must be a tensor on {dev}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, not {list(t.shape)}")
+    if t.is_contiguous():
+        return t.data_ptr(), None
     a, b, c, e = t.stride()
-    if e != 1 and t.shape[3] > 1:
+    if e != 1 and shape[3] > 1:
         raise ValueError(f"{name}: the values of a head must be contiguous")
     return t.data_ptr(), _Strides(a, b, c)
 
@@ -712,14 +717,17 @@ def _cuda(t, name):
 
 def _launch(dev, stream, fn, where, *args):
     """Calls ``fn`` for device ``dev`` on ``stream`` (default: the device's current one)."""
-    s = stream if stream is not None else torch.cuda.current_stream(dev)
-    if s.device != dev:
-        raise ValueError(f"{where}: the stream is on {s.device}, the tensors on {dev}")
-    if torch.cuda.current_device() == dev.index:
-        rc = fn(*args, s.cuda_stream)
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(dev.index)
+    elif stream.device != dev:
+        raise ValueError(f"{where}: the stream is on {stream.device}, the tensors on {dev}")
+    else:
+        raw = stream.cuda_stream
+    if torch._C._cuda_getDevice() == dev.index:
+        rc = fn(*args, raw)
     else:
         with torch.cuda.device(dev):
-            rc = fn(*args, s.cuda_stream)
+            rc = fn(*args, raw)
     if rc != FS_OK:
         raise FSError(rc, where)
 
@@ -744,32 +752,41 @@ def fs_rope(q, k, pos, plan, inverse=False, q_out=None, k_out=None, stream=None)
     int for positions pos, pos + 1, ...  ``inverse`` applies the transposed rotation, which takes
     the outputs' gradients to the inputs'.  ``q_out`` / ``k_out`` may be the inputs (in place).
     Returns (q_out, k_out)."""
-    L = load()
+    L = _lib or load()
     dev, dt = _cuda(q, "q"), q.dtype
-    if dt not in (torch.bfloat16, torch.float32):
+    if dt is torch.bfloat16:
+        code = FS_BF16
+    elif dt is torch.float32:
+        code = FS_FP32
+    else:
         raise ValueError(f"q has dtype {dt}, expected bfloat16 or float32")
-    qp, qs = _rows(q, dev, "q", dt)
-    B, Hq, N, d = q.shape
-    q_out = torch.empty_like(q) if q_out is None else q_out
-    qop, qos = _rows(q_out, dev, "q_out", dt, q.shape)
+    shape = q.shape
+    if len(shape) != 4:
+        raise ValueError("q must be [batch, Hq, N, d]")
+    B, Hq, N, d = shape
+    qp, qs = _rows(q, dev, "q", dt, shape)
+    if q_out is None:
+        q_out = torch.empty_like(q)
+    qop, qos = _rows(q_out, dev, "q_out", dt, shape)
     kp = ks = kop = kos = None
     Hk = 0
     if k is not None:
-        kp, ks = _rows(k, dev, "k", dt)
-        Hk = k.shape[1]
-        if tuple(k.shape) != (B, Hk, N, d):
-            raise ValueError(f"k must be [{B}, Hk, {N}, {d}], not {list(k.shape)}")
-        k_out = torch.empty_like(k) if k_out is None else k_out
-        kop, kos = _rows(k_out, dev, "k_out", dt, k.shape)
+        Hk = k.shape[1] if isinstance(k, torch.Tensor) and k.dim() == 4 else 0
+        shape = (B, Hk, N, d)
+        kp, ks = _rows(k, dev, "k", dt, shape)
+        if k_out is None:
+            k_out = torch.empty_like(k)
+        kop, kos = _rows(k_out, dev, "k_out", dt, shape)
     pp, stride, pos0 = None, 0, 0
     if isinstance(pos, int):
         pos0 = pos
+    elif isinstance(pos, torch.Tensor) and pos.dim() == 2:
+        stride = N
+        pp = _on(pos, dev, "pos", torch.int32, (B, N))
     else:
-        stride = N if pos.dim() == 2 else 0
-        pp = _on(pos, dev, "pos", torch.int32, (B, N) if stride else (N,))
-    _launch(dev, stream, L.fs_rope, "fs_rope", qp, qop, Hq, qs, qos, kp, kop, Hk, ks, kos,
-            FS_BF16 if dt == torch.bfloat16 else FS_FP32, B, N, d, pp, stride, pos0, plan,
-            int(bool(inverse)))
+        pp = _on(pos, dev, "pos", torch.int32, (N,))
+    _launch(dev, stream, L.fs_rope, "fs_rope", qp, qop, Hq, qs, qos, kp, kop, Hk, ks, kos, code, B,
+            N, d, pp, stride, pos0, plan, 1 if inverse else 0)
     return q_out, k_out
 
 
@@ -824,7 +841,7 @@ def _counts(cache, name, t):
 def fs_cache_append(cache, k, v, start, count=None, stream=None):
     """Writes k, v [batch, Hkv, T, d] bf16 (any 16-byte aligned strides) at positions
     start[b] .. start[b] + count[b] - 1 of every sequence (``count`` None: T)."""
-    L = load()
+    L = _lib or load()
     T = k.shape[2] if isinstance(k, torch.Tensor) and k.dim() == 4 else 0
     shape = (cache.batch, cache.Hkv, T, cache.d)
     kp, ks = _rows(k, cache.device, "k", torch.bfloat16, shape)
@@ -840,7 +857,7 @@ def fs_cache_read(cache, start, count=None, k=None, v=None, T=None, dtype=torch.
     """Reads positions start[b] .. start[b] + count[b] - 1 of every sequence into k, v
     [batch, Hkv, T, d] (given, or new zeros of ``T`` rows in ``dtype``); rows past count[b] are
     left as they were.  Returns (k, v)."""
-    L = load()
+    L = _lib or load()
     if (k is None) != (v is None) or (k is None and T is None):
         raise ValueError("give k and v, or T")
     if k is None:
@@ -863,7 +880,7 @@ def fs_cache_read(cache, start, count=None, k=None, v=None, T=None, dtype=torch.
 def fs_cache_accept(cache, start, path, count=None, stream=None):
     """Moves the row at start[b] + path[b, i] to start[b] + i for i < count[b] (``path``
     [batch, A <= 64] int32), every source read before any row is written."""
-    L = load()
+    L = _lib or load()
     if not isinstance(path, torch.Tensor) or path.dim() != 2 or start is None:
         raise ValueError("path must be [batch, A], start given")
     pp = _on(path, cache.device, "path", torch.int32, (cache.batch, path.shape[1]))
@@ -889,7 +906,7 @@ def fs_tree_attn(q, cache, past, tree=None, count=None, window=0, scale=None, ou
     ``count`` [batch]: drafted tokens of each sequence (None: T); ``window`` 0 or >= 64 last
     positions; ``scale`` default d ** -0.5.  Returns out [batch, H, T, d] bf16; rows past count[b]
     are left as they were (a new ``out`` starts as zeros when ``count`` is given)."""
-    L = load()
+    L = _lib or load()
     dev = cache.device
     if not isinstance(q, torch.Tensor) or q.dim() != 4:
         raise ValueError("q must be [batch, H, T, d]")
