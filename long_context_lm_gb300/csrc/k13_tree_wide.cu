@@ -17,7 +17,7 @@
 //
 // Scores, scales, references and probabilities are as in k12_tree.cu (q by a
 // power of two a row, fp16 probabilities up to 2^15, value scales relative to a
-// power of two).  A half whose scores pass their reference by more than 8 (log2)
+// power of two that is part of the exponent here).  A half whose scores pass their reference by more than 8 (log2)
 // raises it, multiplies the row's O by the difference once no product is under
 // way, and is done again.
 //
@@ -36,17 +36,26 @@ struct Wide {
   static constexpr int kCols = D / 64;           // 64-element column blocks
   static constexpr int kBlock = KT * 128;        // bytes of one of them
   static constexpr int kStage = 2 * kCols * kBlock;
-  static constexpr int kStages = D == 64 ? 5 : 3;
+  static constexpr int kStages = 3;
+  static constexpr int kRaws = D == 64 ? 4 : 3;  // tiles of codes under way
+  // a tile's codes, a scale pair a thread and four valid words
+  static constexpr int kRawScale = KT * kRow * 2, kRaw = kRawScale + 1024 + 16;
   static constexpr int kQ = 128 * 128 * kCols;
-  static constexpr int kMerge = 128 * (D + 2) * 4;
-  static constexpr int kSide = KT * 8 + 64;  // scales, valid words, largest value scales
+  static constexpr int kMerge = 128 * (D + 2) * 4;  // begins in place of q
+  static constexpr int kSide = KT * 8 + 64;  // scales, 4 valid words, 4 largest value scales
   static constexpr int kSmem =
-      1024 + kStage * kStages + kQ + kMerge + kSide * kStages + 256;
+      1024 + kStage * kStages + kMerge + kSide * kStages + 256 + kRaws * kRaw;
   // TMEM columns of a stream: S, P, O
   static constexpr int kS = 0, kP = KT, kO = KT + KT / 2, kTmem = 256;
-  static_assert(kO + D <= kTmem && kSmem <= 227 * 1024, "sizes");
+  static_assert(kO + D <= kTmem && kSmem <= 227 * 1024 && kQ <= kMerge, "sizes");
   static constexpr int NP = KT * P / 128;  // pieces of a thread, keys or values
 };
+
+// The least power of two that the value scales are relative to.  Probabilities
+// are made 1 / vref times as large (the products with the scales then need no
+// second factor), and stay within fp32 with their sum.
+constexpr float kLeast = 0x1p-90f;
+constexpr uint32_t kNone = ~0u;
 
 // Element of a head at position i of the tiles' rows: int4 codes leave a word
 // in the order 0 4 1 5 2 6 3 7.
@@ -80,10 +89,10 @@ struct Walk {
 };
 
 struct Bars {
-  uint64_t full[5], empty[5];        // tiles
+  uint64_t full[3], empty[3];        // tiles
   uint64_t s_full[2], s_free[2];     // a stream's scores
   uint64_t p_full[2][2], p_free[2][2];  // a stream's halves of probabilities
-  uint64_t q_full, merge;
+  uint64_t q_full, done, merge, merged;  // of a segment
 };
 
 // Sixteen bytes of codes -> fp16, eight elements to a 16-byte chunk.
@@ -110,13 +119,15 @@ template <int F, int D>
 __global__ void __launch_bounds__(512, 1) k13_tree_wide_kernel(const __grid_constant__ TreeK k) {
   using C = Wide<F, D>;
   constexpr int KT = C::KT, P = C::P, NS = C::kStages, NP = C::NP, HALF = KT / 2;
+  constexpr int kRaws = C::kRaws;
   extern __shared__ char smem_raw[];
   char *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   char *qs = smem + NS * C::kStage;
-  float *mo = reinterpret_cast<float *>(qs + C::kQ);  // the second stream's O [D][128]
+  float *mo = reinterpret_cast<float *>(qs);  // the second stream's O [D][128], over q
   float *mm = mo + 128 * D, *ml = mm + 128;
   char *side = reinterpret_cast<char *>(ml + 128);
   Bars &bar = *reinterpret_cast<Bars *>(side + NS * C::kSide);
+  char *raw = side + NS * C::kSide + 256;
   __shared__ uint32_t tmem_base;
   __shared__ int fail;
   const TreeArgs &a = k.a;
@@ -151,7 +162,9 @@ __global__ void __launch_bounds__(512, 1) k13_tree_wide_kernel(const __grid_cons
       }
     }
     tc::mbar_init(&bar.q_full, 128);
+    tc::mbar_init(&bar.done, 128);
     tc::mbar_init(&bar.merge, 128);
+    tc::mbar_init(&bar.merged, 128);
     tc::mbar_fence_init();
   }
   if (warp == 12) {
@@ -193,23 +206,25 @@ __global__ void __launch_bounds__(512, 1) k13_tree_wide_kernel(const __grid_cons
       }
       // the row's power of two; the first stream writes q
       const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q) + at);
-      uint4 x[D / 8];
       uint32_t most = 0;
-#pragma unroll
+#pragma unroll 8
       for (int i = 0; i < D / 8; ++i) {
-        x[i] = live ? src[i] : make_uint4(0, 0, 0, 0);
-        most = __vmaxu2(most, x[i].x & 0x7fff7fffu);
-        most = __vmaxu2(most, x[i].y & 0x7fff7fffu);
-        most = __vmaxu2(most, x[i].z & 0x7fff7fffu);
-        most = __vmaxu2(most, x[i].w & 0x7fff7fffu);
+        const uint4 x = live ? src[i] : make_uint4(0, 0, 0, 0);
+        most = __vmaxu2(most, x.x & 0x7fff7fffu);
+        most = __vmaxu2(most, x.y & 0x7fff7fffu);
+        most = __vmaxu2(most, x.z & 0x7fff7fffu);
+        most = __vmaxu2(most, x.w & 0x7fff7fffu);
       }
       most = max(most & 0xffffu, most >> 16);
       const float f = __uint_as_float((uint32_t)min(254, 268 - (int)(most >> 7)) << 23);
       const float rf = fmaxf(a.scale * kLog2e * (1.f / f), FLT_MIN);
       if (st == 0) {
-#pragma unroll
+        // (the second stream's results lay there)
+        if (seg > 0 && !(ok = wait(&bar.merged, seg - 1))) break;
+#pragma unroll 2
         for (int i = 0; i < D / 8; ++i) {
-          const uint32_t y[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+          const uint4 x = live ? src[i] : make_uint4(0, 0, 0, 0);
+          const uint32_t y[4] = {x.x, x.y, x.z, x.w};
           uint32_t z[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
@@ -227,7 +242,7 @@ __global__ void __launch_bounds__(512, 1) k13_tree_wide_kernel(const __grid_cons
         break;
       }
 
-      float m = -FLT_MAX, thr = -INFINITY, l0 = 0.f, l1 = 0.f, vref = 0x1p-126f;
+      float m = -FLT_MAX, thr = -INFINITY, l0 = 0.f, l1 = 0.f, vref = kLeast;
       bool begun = false;  // O holds something
       // O *= by, once no product is under way: those of this tile's first half
       // and of the last tile
@@ -250,127 +265,140 @@ __global__ void __launch_bounds__(512, 1) k13_tree_wide_kernel(const __grid_cons
         return true;
       };
 
+      int stage = (it + st) % NS;
+      uint32_t round = (uint32_t)((it + st) / NS);
       for (int i = st; ok && i < n; i += 2, ++jt) {
-        const int tile = it + i, stage = tile % NS;
-        const char *sd = side + stage * C::kSide;
-        const float *ks = reinterpret_cast<const float *>(sd), *vs = ks + KT;
-        const uint32_t *valid = reinterpret_cast<const uint32_t *>(vs + KT);
-        if (!(ok = wait(&bar.full[stage], tile / NS) && wait(&bar.s_full[st], jt))) break;
+        const float *ks = reinterpret_cast<const float *>(side + stage * C::kSide);
+        const uint32_t *valid = reinterpret_cast<const uint32_t *>(ks + 2 * KT);
+        if (!(ok = wait(&bar.full[stage], round) && wait(&bar.s_full[st], jt))) break;
+        if ((stage += 2) >= NS) {
+          stage -= NS;
+          ++round;
+        }
         tc::fence_after_sync();
         const int key0 = w.s.first + (w.from + i) * KT;
-        uint32_t all = ~0u;
-        float top_v = 0.f;
-#pragma unroll
-        for (int j = 0; j < KT / 32; ++j) {
-          all &= valid[j];
-          top_v = fmaxf(top_v, __uint_as_float(valid[KT / 32 + j]));
-        }
-        const bool whole =
-            all == ~0u && __all_sync(~0u, key0 + KT <= w.s.past && key0 >= first);
+        const uint4 in = *reinterpret_cast<const uint4 *>(valid);
+        const float4 tops = *reinterpret_cast<const float4 *>(valid + 4);
+        const bool whole = (KT == 128 ? in.x & in.y & in.z & in.w : in.x & in.y) == ~0u &&
+                           __all_sync(~0u, key0 + KT <= w.s.past && key0 >= first);
+        const float top_v = KT == 128 ? fmaxf(fmaxf(tops.x, tops.y), fmaxf(tops.z, tops.w))
+                                      : fmaxf(tops.x, tops.y);
         if (top_v > vref) {  // the same for all rows
           const float up =
               __uint_as_float((__float_as_uint(top_v) + 0x7fffffu) & 0x7f800000u);
-          if (begun && !(ok = rescale(vref / up, 0))) break;
+          const float back = vref / up;
+          if (begun && !(ok = rescale(back, 0))) break;
+          l0 *= back;
+          l1 *= back;
           vref = up;
         }
-        const float inv = __uint_as_float(0x7f000000u - __float_as_uint(vref));
+        const float lift = 15.f - kRaise - (float)((int)(__float_as_uint(vref) >> 23) - 127);
 
+        // The columns, 32 at a time; what belongs to a half's beginning or end is
+        // done in its first or last round (one copy of the code: it shares the
+        // instruction cache with the other roles').
+        float s0 = 0.f, s1 = 0.f, top = -INFINITY;
+        bool again = false;
 #pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
-          uint32_t p[HALF / 2];
-          float s0 = 0.f, s1 = 0.f;
-#pragma unroll 1
-          for (int tries = 0; tries < 2; ++tries) {
-            float top = -INFINITY;
-            const float ref = 15.f - kRaise - m;
+        for (int c0 = 0; c0 < KT; c0 += 32) {
+          const int half = c0 >= HALF;
+          if (c0 == half * HALF) {
+            if (jt > 0 && !(ok = wait(&bar.p_free[st][half], jt - 1))) break;
+            tc::fence_after_sync();
             s0 = s1 = 0.f;
-#pragma unroll
-            for (int ch = 0; ch < HALF / 32; ++ch) {
-              const int c0 = half * HALF + ch * 32;
-              uint32_t u[32];
-              tc::tmem_ld32(tm + C::kS + c0, u);
-              tc::tmem_wait_ld();
-              uint32_t seen = ~0u;  // of these 32 keys
-              if (!whole) {
-                const int key = key0 + c0;
-                seen = valid[c0 / 32];
-                const int before = min(max(w.s.past - key, 0), 32);  // keys of the prefix
-                const int skip = min(max(first - key, 0), before);   // outside the window
-                uint32_t see = before - skip == 32 ? ~0u
-                               : before > skip    ? ((1u << (before - skip)) - 1) << skip
-                                                  : 0u;
-                if (before < 32) {  // drafted: bit (key + i - past)
-                  const int j = key - w.s.past;  // of key 0; negative inside the prefix
-                  const uint64_t x = j >= 64 ? 0 : j >= 0 ? bits >> j : bits << -j;
-                  see |= (uint32_t)x & (before ? ~0u << before : ~0u);
-                }
-                seen &= see;
-              }
-              auto weigh = [&](auto masked) {
-#pragma unroll
-                for (int j = 0; j < 32; j += 4) {
-                  const float4 kk = *reinterpret_cast<const float4 *>(ks + c0 + j);
-                  const float4 vv = *reinterpret_cast<const float4 *>(vs + c0 + j);
-                  float y[4] = {__uint_as_float(u[j]), __uint_as_float(u[j + 1]),
-                                __uint_as_float(u[j + 2]), __uint_as_float(u[j + 3])};
-                  mul2(y[0], y[1], kk.x, kk.y);
-                  mul2(y[2], y[3], kk.z, kk.w);
-                  if constexpr (masked.value) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) y[e] = seen >> (j + e) & 1 ? y[e] : -INFINITY;
-                  }
-                  top = max3f(max3f(top, y[0], y[1]), y[2], y[3]);
-                  fma2(y[0], y[1], y[0], y[1], rf, ref);
-                  fma2(y[2], y[3], y[2], y[3], rf, ref);
-#pragma unroll
-                  for (int e = 0; e < 4; ++e) y[e] = tc::ex2(y[e]);
-                  add2(s0, s1, y[0], y[1]);
-                  add2(s0, s1, y[2], y[3]);
-                  float z[4] = {vv.x, vv.y, vv.z, vv.w};
-                  mul2(z[0], z[1], inv, inv);
-                  mul2(z[2], z[3], inv, inv);
-                  mul2(y[0], y[1], z[0], z[1]);
-                  mul2(y[2], y[3], z[2], z[3]);
-                  if constexpr (masked.value) {  // (a masked key's scale may be NaN)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) y[e] = seen >> (j + e) & 1 ? y[e] : 0.f;
-                  }
-                  p[ch * 16 + j / 2] = pack_f16(y[0], y[1]);
-                  p[ch * 16 + j / 2 + 1] = pack_f16(y[2], y[3]);
-                }
-              };
-              if (whole)
-                weigh(std::false_type());
-              else
-                weigh(std::true_type());
+            top = -INFINITY;
+          }
+          uint32_t u[32];
+          tc::tmem_ld32(tm + C::kS + c0, u);
+          uint32_t seen = ~0u;  // of these 32 keys
+          if (!whole) {
+            const int key = key0 + c0;
+            const int before = min(max(w.s.past - key, 0), 32);  // keys of the prefix
+            const int skip = min(max(first - key, 0), before);   // outside the window
+            seen = before - skip == 32 ? ~0u
+                   : before > skip     ? ((1u << (before - skip)) - 1) << skip
+                                       : 0u;
+            if (before < 32) {  // drafted: bit (key + i - past)
+              const int j = key - w.s.past;  // of key 0; negative inside the prefix
+              const uint64_t z = j >= 64 ? 0 : j >= 0 ? bits >> j : bits << -j;
+              seen |= (uint32_t)z & (before ? ~0u << before : ~0u);
             }
-            if (tries || !__any_sync(~0u, top > thr)) break;
+            seen &= valid[c0 / 32];
+          }
+          const float ref = lift - m;
+          tc::tmem_wait_ld();
+          // Step by step over all 32 columns: each step's operations do not wait
+          // for one another.
+          float y[32];
+#pragma unroll
+          for (int j = 0; j < 32; j += 4) {
+            const float4 kk = *reinterpret_cast<const float4 *>(ks + c0 + j);
+            y[j] = __uint_as_float(u[j]), y[j + 1] = __uint_as_float(u[j + 1]);
+            y[j + 2] = __uint_as_float(u[j + 2]), y[j + 3] = __uint_as_float(u[j + 3]);
+            mul2(y[j], y[j + 1], kk.x, kk.y);
+            mul2(y[j + 2], y[j + 3], kk.z, kk.w);
+          }
+          if (!whole) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) y[j] = seen >> j & 1 ? y[j] : -INFINITY;
+          }
+          float t0 = y[0], t1 = y[1];
+#pragma unroll
+          for (int j = 2; j < 32; j += 4) {
+            t0 = max3f(t0, y[j], y[j + 1]);
+            if (j + 2 < 32) t1 = max3f(t1, y[j + 2], y[j + 3]);
+          }
+          top = max3f(top, t0, t1);
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) fma2(y[j], y[j + 1], y[j], y[j + 1], rf, ref);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) y[j] = tc::ex2(y[j]);
+          float s2 = 0.f, s3 = 0.f;
+#pragma unroll
+          for (int j = 0; j < 32; j += 4) {
+            add2(s0, s1, y[j], y[j + 1]);
+            add2(s2, s3, y[j + 2], y[j + 3]);
+          }
+          add2(s0, s1, s2, s3);
+#pragma unroll
+          for (int j = 0; j < 32; j += 4) {
+            const float4 vv = *reinterpret_cast<const float4 *>(ks + KT + c0 + j);
+            mul2(y[j], y[j + 1], vv.x, vv.y);
+            mul2(y[j + 2], y[j + 3], vv.z, vv.w);
+          }
+          if (!whole) {  // (a masked key's scale may be NaN)
+#pragma unroll
+            for (int j = 0; j < 32; ++j) y[j] = seen >> j & 1 ? y[j] : 0.f;
+          }
+          uint32_t p[16];
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) p[j / 2] = pack_f16(y[j], y[j + 1]);
+          tc::tmem_st16(tm + C::kP + c0 / 2, p);
+          if (c0 + 32 != (half + 1) * HALF) continue;
+          // the half's end
+          if (!again && __any_sync(~0u, top > thr)) {
+            // P has not been handed on: raise the reference, write it again
             const float up = fmaxf(m, top * rf);
             const float back = exp2f(m - up);
             m = up;
             if (up > -FLT_MAX) thr = (up + kRaise) / rf;
             l0 *= back;
             l1 *= back;
+            tc::tmem_wait_st();
             if (begun && !(ok = rescale(back, half))) break;
+            again = true;
+            c0 -= HALF;
+            continue;
           }
-          if (!ok) break;
-          l0 += s0;
-          l1 += s1;
-          if (half) {
-            tc::fence_before_sync();
-            tc::mbar_arrive(&bar.s_free[st]);
-          }
-          if (jt > 0 && !(ok = wait(&bar.p_free[st][half], jt - 1))) break;
-          tc::fence_after_sync();
-          if constexpr (HALF == 64)
-            tc::tmem_st32(tm + C::kP + half * 32, p);
-          else
-            tc::tmem_st16(tm + C::kP + half * 16, p);
+          again = false;
+          add2(l0, l1, s0, s1);
           tc::tmem_wait_st();
           tc::fence_before_sync();
           tc::mbar_arrive(&bar.p_full[st][half]);
           begun = true;
         }
+        if (!ok) break;
+        tc::mbar_arrive(&bar.s_free[st]);
       }
       if (!ok) break;
       // the segment's end: all products of the stream
@@ -378,8 +406,10 @@ __global__ void __launch_bounds__(512, 1) k13_tree_wide_kernel(const __grid_cons
         if (!(ok = wait(&bar.p_free[st][0], jt - 1) && wait(&bar.p_free[st][1], jt - 1))) break;
         tc::fence_after_sync();
       }
-      const float l = l0 + l1;
+      const float l = (l0 + l1) * vref;
       if (st == 1) {
+        // (it goes where q lies: the first stream's scores must be done as well)
+        if (!(ok = wait(&bar.done, seg))) break;
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
           uint32_t o[32];
@@ -396,6 +426,7 @@ __global__ void __launch_bounds__(512, 1) k13_tree_wide_kernel(const __grid_cons
         tc::fence_before_sync();
         tc::mbar_arrive(&bar.merge);
       } else {
+        tc::mbar_arrive(&bar.done);
         if (!(ok = wait(&bar.merge, seg))) break;
         const float m1 = mm[row], l1_ = ml[row], top = fmaxf(m, m1);
         const float f0 = exp2f(m - top), f1 = exp2f(m1 - top), sum = f0 * l + f1 * l1_;
@@ -432,6 +463,7 @@ __global__ void __launch_bounds__(512, 1) k13_tree_wide_kernel(const __grid_cons
           part[128 * D + 128 + row] = sum;
         }
         tc::fence_before_sync();
+        tc::mbar_arrive(&bar.merged);
       }
       it += n;
     }
@@ -439,111 +471,122 @@ __global__ void __launch_bounds__(512, 1) k13_tree_wide_kernel(const __grid_cons
     // -------------------------------------------------- codes -> fp16 tiles
     const int t = tid - 256, shift = 31 - __clz(a.c.page);
     const Magic magic = make_magic();
-    const size_t v_off = (size_t)a.c.Hkv * a.c.page;  // rows from a key to its value
+    const int v_off = a.c.Hkv * a.c.page;  // rows from a key to its value
     bool ok = true;
     while (ok && w.next(k)) {
-      // A thread's pieces lie in rows t / P + i (128 / P); its scale belongs to
-      // key t % KT (threads past KT: none, with KT = 64 the upper 64 take the
-      // values' scales).  Pages are looked up two tiles ahead of the codes,
-      // codes loaded two tiles ahead of their use.
-      struct Ahead {
-        int page[NP], page_s;
-        uint4 code[2][NP];
-        float scale[2];
-        bool in;
-      } buf[2];
-      const int key_s = t & (KT - 1);
-      auto look = [&](Ahead &x, int i) {
-        const int key0 = w.s.first + i * KT;
-        auto page = [&](int key) {
-          return i < w.to && key < w.s.end
-                     ? a.c.table[(size_t)w.b * a.c.max_pages + (key >> shift)]
-                     : INT_MIN;
-        };
-#pragma unroll
-        for (int j = 0; j < NP; ++j) x.page[j] = page(key0 + t / P + j * (128 / P));
-        x.page_s = page(key0 + key_s);
+      // A thread's pieces lie in rows t / P + j (128 / P), keys and values; it
+      // copies them into a ring of its own and turns them into fp16 when they
+      // have come.  Its scale belongs to key t % KT.
+      //
+      // Where the tiles lie: lane l holds sixteen rows, group l % GP of tile
+      // l / GP of the 32 / GP tiles looked up at a time, as their place among all
+      // groups of sixteen rows (kNone: nothing to read); the next ones' pages are
+      // asked for that many tiles ahead.
+      constexpr int GP = KT / 16, AT = 32 / GP;
+      const int n = w.to - w.from, key_s = t & (KT - 1), groups = a.c.page >> 4;
+      auto key_of = [&](int i) {
+        return w.s.first + (w.from + i + lane / GP) * KT + 16 * (lane % GP);
       };
-      auto load = [&](Ahead &x, int i) {
-        const int key0 = w.s.first + i * KT;
+      auto page_of = [&](int i) {
+        const int key = key_of(i);
+        return i + lane / GP < n && key < w.s.end
+                   ? a.c.table[(size_t)w.b * a.c.max_pages + (key >> shift)]
+                   : INT_MIN;
+      };
+      auto place_of = [&](int i, int page) -> uint32_t {
+        if ((unsigned)page >= (unsigned)a.c.pages) {
+          if (page != INT_MIN && a.c.status) atomicCAS(a.c.status, 0, FS_ERR_CACHE);
+          return kNone;
+        }
+        return (uint32_t)(page * 2 * a.c.Hkv + w.h) * groups + ((key_of(i) & (a.c.page - 1)) >> 4);
+      };
+      uint32_t place = place_of(0, page_of(0));
+      int later = page_of(AT), at = 0, left = w.s.end - w.s.first - w.from * KT;  // keys from here
+      auto copy = [&](int slot) {
+        const uint32_t dst = smem_u32(raw) + slot * C::kRaw;
 #pragma unroll
         for (int j = 0; j < NP; ++j) {
-          x.code[0][j] = x.code[1][j] = make_uint4(0, 0, 0, 0);
-          if ((unsigned)x.page[j] < (unsigned)a.c.pages) {
-            const int key = key0 + t / P + j * (128 / P);
-            const size_t r = cache_row(a.c, x.page[j], 0, w.h, key & (a.c.page - 1));
-            const char *p = static_cast<const char *>(a.c.codes) + r * C::kRow + t % P * 16;
-            x.code[0][j] = *reinterpret_cast<const uint4 *>(p);
-            x.code[1][j] = *reinterpret_cast<const uint4 *>(p + v_off * C::kRow);
-          }
+          const int r = t / P + j * (128 / P);
+          const uint32_t g = __shfl_sync(~0u, place, at * GP + r / 16);
+          const bool have = g != kNone && r < left;
+          const char *p = static_cast<const char *>(a.c.codes) +
+                          ((size_t)(have ? g : 0) * 16 + r % 16) * C::kRow + t % P * 16;
+          cp_async16z(dst + j * 2048 + t * 16, p, have ? 16 : 0);
+          cp_async16z(dst + (NP + j) * 2048 + t * 16, p + (have ? v_off * C::kRow : 0),
+                      have ? 16 : 0);
         }
-        x.scale[0] = x.scale[1] = 0.f;
-        x.in = (unsigned)x.page_s < (unsigned)a.c.pages;
-        if (x.in) {
-          const size_t r = cache_row(a.c, x.page_s, 0, w.h, (key0 + key_s) & (a.c.page - 1));
-          x.scale[0] = a.c.scales[r];
-          x.scale[1] = a.c.scales[r + v_off];
-        } else if (x.page_s != INT_MIN && a.c.status) {
-          atomicCAS(a.c.status, 0, FS_ERR_CACHE);
-        }
+        const uint32_t g = __shfl_sync(~0u, place, at * GP + key_s / 16);
+        const bool in = g != kNone && key_s < left;
+        const float *p = a.c.scales + (size_t)(in ? g : 0) * 16 + key_s % 16;
+        cp_async4z(dst + C::kRawScale + t * 8, p, in ? 4 : 0);
+        cp_async4z(dst + C::kRawScale + t * 8 + 4, p + (in ? v_off : 0), in ? 4 : 0);
+        const uint32_t word = __ballot_sync(~0u, in);
+        if (lane == 0)
+          *reinterpret_cast<uint32_t *>(raw + slot * C::kRaw + C::kRawScale + 1024 +
+                                        (t >> 5) * 4) = word;
+        cp_async_commit();
+        left -= KT;
+        if (++at == AT) at = 0;
       };
-      auto put = [&](const Ahead &x, int tile) -> bool {
-        const int stage = tile % NS;
-        if (tile >= NS && !wait(&bar.empty[stage], tile / NS - 1)) return false;
+      int ahead = 0;  // tiles copied
+      auto copy_next = [&](int slot) {
+        if (at == 0 && ahead) {
+          place = place_of(ahead, later);
+          later = page_of(ahead + AT);
+        }
+        copy(slot);
+        ++ahead;
+      };
+#pragma unroll 1
+      for (int i = 0; i < kRaws - 1; ++i) copy_next(i);
+      int slot = 0, stage = it % NS;
+      uint32_t round = (uint32_t)(it / NS);
+#pragma unroll 1
+      for (int i = 0; i < n; ++i) {
+        copy_next(slot == 0 ? kRaws - 1 : slot - 1);
+        cp_async_wait<kRaws - 1>();
+        if (round > 0 && !(ok = wait(&bar.empty[stage], round - 1))) break;
+        const char *src = raw + slot * C::kRaw;
         char *dst = smem + stage * C::kStage;
+#pragma unroll 1
+        for (int j = 0; j < 2 * NP; ++j) {
+          const int part = j >= NP, r = t / P + (j - part * NP) * (128 / P);
+          const uint4 x = *reinterpret_cast<const uint4 *>(src + j * 2048 + t * 16);
+          const uint32_t wd[4] = {x.x, x.y, x.z, x.w};
+          constexpr int CH = 128 / C::kBits / 8;  // chunks of the piece: 2 or 4
 #pragma unroll
-        for (int part = 0; part < 2; ++part)
-#pragma unroll
-          for (int j = 0; j < NP; ++j) {
-            const int r = t / P + j * (128 / P);
-            const uint32_t wd[4] = {x.code[part][j].x, x.code[part][j].y, x.code[part][j].z,
-                                    x.code[part][j].w};
-            constexpr int CH = 128 / C::kBits / 8;  // chunks of the piece: 2 or 4
-#pragma unroll
-            for (int c = 0; c < CH; ++c) {
-              const int chunk = t % P * CH + c;  // of the row's D / 8
-              uint4 y;
-              to_chunk<F>(magic, wd + c * (4 / CH), y);
-              *reinterpret_cast<uint4 *>(dst + (part * C::kCols + chunk / 8) * C::kBlock +
-                                         swz128(r, chunk % 8)) = y;
-            }
+          for (int c = 0; c < CH; ++c) {
+            const int chunk = t % P * CH + c;  // of the row's D / 8
+            uint4 y;
+            to_chunk<F>(magic, wd + c * (4 / CH), y);
+            *reinterpret_cast<uint4 *>(dst + (part * C::kCols + chunk / 8) * C::kBlock +
+                                       swz128(r, chunk % 8)) = y;
           }
-        float *sd = reinterpret_cast<float *>(side + stage * C::kSide);
-        uint32_t *valid = reinterpret_cast<uint32_t *>(sd + 2 * KT);
-        const uint32_t in = __ballot_sync(~0u, x.in);
-        const float v = x.scale[1];
+        }
+        const float2 sc = *reinterpret_cast<const float2 *>(src + C::kRawScale + t * 8);
+        const uint32_t word = *reinterpret_cast<const uint32_t *>(src + C::kRawScale + 1024 + (t >> 5) * 4);
         const uint32_t top =
-            __reduce_max_sync(~0u, v <= FLT_MAX ? __float_as_uint(fmaxf(v, 0.f)) : 0u);
+            __reduce_max_sync(~0u, sc.y <= FLT_MAX ? __float_as_uint(fmaxf(sc.y, 0.f)) : 0u);
         if (t < KT) {
-          sd[t] = x.scale[0];
-          sd[KT + t] = v;
+          float *sd = reinterpret_cast<float *>(side + stage * C::kSide);
+          sd[t] = sc.x;
+          sd[KT + t] = sc.y;
           if (lane == 0) {
-            valid[t / 32] = in;
-            valid[KT / 32 + t / 32] = top;
+            uint32_t *valid = reinterpret_cast<uint32_t *>(sd + 2 * KT);
+            valid[t / 32] = word;
+            valid[4 + t / 32] = top;
           }
         }
         tc::fence_async_smem();
         tc::mbar_arrive(&bar.full[stage]);
-        return true;
-      };
-      const int n = w.to - w.from;
-      look(buf[0], w.from);
-      look(buf[1], w.from + 1);
-      load(buf[0], w.from);
-      look(buf[0], w.from + 2);
-      load(buf[1], w.from + 1);
-      look(buf[1], w.from + 3);
-#pragma unroll 1
-      for (int i = 0; ok && i < n; i += 2) {
-        if (!(ok = put(buf[0], it + i))) break;
-        load(buf[0], w.from + i + 2);
-        look(buf[0], w.from + i + 4);
-        if (i + 1 < n) {
-          if (!(ok = put(buf[1], it + i + 1))) break;
-          load(buf[1], w.from + i + 3);
-          look(buf[1], w.from + i + 5);
+        slot = slot + 1 == kRaws ? 0 : slot + 1;
+        if (++stage == NS) {
+          stage = 0;
+          ++round;
         }
+        __syncwarp();
       }
+      cp_async_wait<0>();
       it += n;
     }
   } else if (warp < 14 && lane == 0) {
@@ -557,9 +600,10 @@ __global__ void __launch_bounds__(512, 1) k13_tree_wide_kernel(const __grid_cons
     for (; ok && w.next(k); ++seg) {
       const int n = w.to - w.from;
       if (!(ok = wait_one(&bar.q_full, seg))) break;
-      auto scores = [&](int i, uint32_t j) -> bool {
-        const int tile = it + i, stage = tile % NS;
-        if (!wait_one(&bar.full[stage], tile / NS)) return false;
+      int stage = (it + st) % NS;  // of the next scores
+      uint32_t round = (uint32_t)((it + st) / NS);
+      auto scores = [&](uint32_t j) -> bool {
+        if (!wait_one(&bar.full[stage], round)) return false;
         if (j > 0 && !wait_one(&bar.s_free[st], j - 1)) return false;
         tc::fence_after_sync();
 #pragma unroll
@@ -569,16 +613,20 @@ __global__ void __launch_bounds__(512, 1) k13_tree_wide_kernel(const __grid_cons
                      tc::desc_sw128(ring + stage * C::kStage + off * C::kBlock + in), kQK, s > 0);
         }
         tc::mma_commit(&bar.s_full[st]);
+        if ((stage += 2) >= NS) {
+          stage -= NS;
+          ++round;
+        }
         return true;
       };
-      if (st < n && !(ok = scores(st, jt))) break;
+      int now = stage;  // of the values
+      if (st < n && !(ok = scores(jt))) break;
       for (int i = st; i < n; i += 2, ++jt) {
-        const int stage = (it + i) % NS;
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {
           if (!(ok = wait_one(&bar.p_full[st][half], jt))) break;
           tc::fence_after_sync();
-          const uint32_t v = ring + stage * C::kStage + C::kCols * C::kBlock;
+          const uint32_t v = ring + now * C::kStage + C::kCols * C::kBlock;
 #pragma unroll
           for (int c = 0; c < C::kCols; ++c)
 #pragma unroll
@@ -589,10 +637,11 @@ __global__ void __launch_bounds__(512, 1) k13_tree_wide_kernel(const __grid_cons
                          i != st || half || s > 0);
             }
           tc::mma_commit(&bar.p_free[st][half]);
-          if (half) tc::mma_commit(&bar.empty[stage]);
-          if (!half && i + 2 < n && !(ok = scores(i + 2, jt + 1))) break;
+          if (half) tc::mma_commit(&bar.empty[now]);
+          if (!half && i + 2 < n && !(ok = scores(jt + 1))) break;
         }
         if (!ok) break;
+        now = now + 2 >= NS ? now + 2 - NS : now + 2;
       }
       it += n;
     }

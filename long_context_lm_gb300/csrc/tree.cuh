@@ -210,6 +210,21 @@ __device__ __forceinline__ void mul2(float &x, float &y, float a, float b) {
   y = __uint_as_float((uint32_t)(r >> 32));
 }
 
+// Asynchronous copies of 16 and 4 bytes; with bytes = 0 zeros are written and
+// nothing is read.
+__device__ __forceinline__ void cp_async16z(uint32_t dst, const void *src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(bytes));
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst), "l"(src));
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n" ::"r"(dst), "l"(src));
+}
+__device__ __forceinline__ void cp_async4z(uint32_t dst, const void *src, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(dst), "l"(src), "r"(bytes));
+}
+
 // Elements e .. e + 3 of a row's output; zeros where the row sees nothing.
 template <int D>
 __device__ __forceinline__ void put_row(const TreeK &k, int b, int h, int row, int e, float4 x,
