@@ -742,73 +742,85 @@ k12_tree_kernel(const __grid_constant__ TreeK k) {
   }
 }
 
-// A block per (row of a tile, tile, kv head) and sequence: adds what the blocks
-// of the line left of a segment.
-template <int D>
+// Adds what the blocks of the line left of a segment: a block for ROWS rows of
+// one kv head and sequence (of one row tile: ROWS divides its size), 256 / ROWS
+// threads a row.  One row a block where there are few, so that many blocks' parts
+// are read at once (152 parts of one row: 5 us against 13); eight where there are
+// many.
+template <int D, int ROWS>
 __global__ void __launch_bounds__(256) k12_join_kernel(const __grid_constant__ TreeK k) {
-  constexpr int L = D / 4, GROUPS = 256 / L;
-  __shared__ float wt[152 * 2 + 1], red[2][8];
-  __shared__ float4 acc_s[256];
-  const TreeArgs &a = k.a;
-  const int b = blockIdx.y, tid = threadIdx.x;
-  const int row = blockIdx.x % (a.T * k.G), h = blockIdx.x / (a.T * k.G);
+  constexpr int L = D / 4, LANES = 256 / ROWS;  // lanes of a row's output, of a row
+  __shared__ float wt[ROWS][2 * kTreeSMs];
+  __shared__ float red[2][8];
+  __shared__ float4 acc[LANES > 32 ? 8 * L : 1];
+  const int b = blockIdx.z, h = blockIdx.y, tid = threadIdx.x, lane = tid % LANES;
   const Line line = line_of(k, [&](long long, int i, long long, long long) { return i == b; });
   const Seq s = line.s;
   // What the earlier kernel wrote is read after this; every block waits, so that
   // the end of this kernel is the end of both.
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int rows = s.n * k.G;
-  if (row >= rows) return;  // also a sequence without units
+  const int rows = s.n * k.G, row0 = blockIdx.x * ROWS;
+  if (row0 >= rows || s.units == 0) return;
   const Share share(k, line.total);
-  const int rt = row / k.M, r = row % k.M;
+  const int rt = row0 / k.M, M = k.M;
   const long long s0 = line.begin + ((long long)h * s.tiles + rt) * s.units;
   const int c0 = share.of(s0), c1 = share.of(s0 + s.units - 1);
   if (c0 == c1) return;  // written by its block
-  const int n = c1 - c0 + 1, M = k.M;
+  const int n = c1 - c0 + 1, i0 = tid / LANES, row = row0 + i0, r = row % M;
+  if (row >= rows) return;  // (whole warps, or the block)
   // the first block left it as its last segment (1), the others as their first (0)
-  auto part = [&](int i) {
-    return k.part + ((size_t)(c0 + i) * 2 + (i == 0)) * M * (D + 2);
+  auto part = [&](int i) { return k.part + ((size_t)(c0 + i) * 2 + (i == 0)) * M * (D + 2); };
+  auto over_block = [&](float *sh, float x, auto op) {  // of the warps' results
+    if constexpr (LANES > 32) {
+      if (tid % 32 == 0) sh[tid / 32] = x;
+      __syncthreads();
+      x = sh[0];
+#pragma unroll
+      for (int w = 1; w < 8; ++w) x = op(x, sh[w]);
+    }
+    return x;
   };
   float top = -FLT_MAX;
-  for (int i = tid; i < n; i += 256) top = fmaxf(top, part(i)[M * D + r]);
+  for (int i = lane; i < n; i += LANES) top = fmaxf(top, part(i)[M * D + r]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-  if (tid % 32 == 0) red[0][tid / 32] = top;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < 8; ++w) top = fmaxf(top, red[0][w]);
+  top = over_block(red[0], top, [](float x, float y) { return fmaxf(x, y); });
   float sum = 0.f;
-  for (int i = tid; i < n; i += 256) {
+  for (int i = lane; i < n; i += LANES) {
     const float *p = part(i);
     const float f = exp2f(p[M * D + r] - top);
-    wt[i] = f;
+    wt[i0][i] = f;
     sum += f * p[M * D + M + r];
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
-  if (tid % 32 == 0) red[1][tid / 32] = sum;
-  __syncthreads();
-  sum = 0.f;
-#pragma unroll
-  for (int w = 0; w < 8; ++w) sum += red[1][w];
-  const int e = tid % L, grp = tid / L;
+  __syncwarp();
+  sum = over_block(red[1], sum, [](float x, float y) { return x + y; });  // (and wt is whole)
   float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-  for (int i = grp; i < n; i += GROUPS) {
-    const float4 y = *reinterpret_cast<const float4 *>(part(i) + r * D + e * 4);
-    const float f = wt[i];
+  for (int i = lane / L; i < n; i += LANES / L) {
+    const float4 y = *reinterpret_cast<const float4 *>(part(i) + r * D + lane % L * 4);
+    const float f = wt[i0][i];
     x.x += f * y.x, x.y += f * y.y, x.z += f * y.z, x.w += f * y.w;
   }
-  acc_s[tid] = x;
-  __syncthreads();
-  if (tid < L) {
-#pragma unroll
-    for (int w = 1; w < GROUPS; ++w) {
-      const float4 y = acc_s[w * L + tid];
-      x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
-    }
-    put_row<D>(k, b, h, row, e * 4, x, sum);
+  if constexpr (L == 16) {
+    x.x += __shfl_xor_sync(~0u, x.x, 16);
+    x.y += __shfl_xor_sync(~0u, x.y, 16);
+    x.z += __shfl_xor_sync(~0u, x.z, 16);
+    x.w += __shfl_xor_sync(~0u, x.w, 16);
   }
+  if constexpr (LANES > 32) {
+    if (tid % 32 < L) acc[tid / 32 * L + tid % 32] = x;
+    __syncthreads();
+    if (lane < L) {
+#pragma unroll
+      for (int w = 1; w < 8; ++w) {
+        const float4 y = acc[w * L + lane];
+        x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+      }
+    }
+  }
+  if (lane < L) put_row<D>(k, b, h, row, lane * 4, x, sum);
 }
 
 template <int F, int D, int MT>
@@ -846,11 +858,13 @@ bool wide(const fs_cache &c, int H, int T) {
   return c.format != FS_CACHE_BF16 && H / c.Hkv * T >= kWideRows;
 }
 
-cudaError_t launch_tree_join(const TreeK &k, cudaStream_t st) {
+template <int D, int ROWS>
+cudaError_t launch_join(const TreeK &k, cudaStream_t st) {
   // its blocks may start, and look up their rows, while the last ones of the
   // kernel before run
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(k.a.T * k.a.H), (unsigned)k.a.c.batch);
+  cfg.gridDim = dim3((unsigned)((k.a.T * k.G + ROWS - 1) / ROWS), (unsigned)k.a.c.Hkv,
+                     (unsigned)k.a.c.batch);
   cfg.blockDim = dim3(256);
   cfg.stream = st;
   cudaLaunchAttribute at{};
@@ -858,8 +872,13 @@ cudaError_t launch_tree_join(const TreeK &k, cudaStream_t st) {
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return k.a.c.d == 64 ? cudaLaunchKernelEx(&cfg, k12_join_kernel<64>, k)
-                       : cudaLaunchKernelEx(&cfg, k12_join_kernel<128>, k);
+  return cudaLaunchKernelEx(&cfg, k12_join_kernel<D, ROWS>, k);
+}
+
+cudaError_t launch_tree_join(const TreeK &k, cudaStream_t st) {
+  const bool few = (long long)k.a.T * k.a.H * k.a.c.batch <= kTreeSMs * 8;
+  if (k.a.c.d == 64) return few ? launch_join<64, 1>(k, st) : launch_join<64, 8>(k, st);
+  return few ? launch_join<128, 1>(k, st) : launch_join<128, 8>(k, st);
 }
 
 size_t tree_workspace_bytes(const fs_cache &c, int H, int T) {

@@ -36,18 +36,20 @@ struct Wide {
   static constexpr int kCols = D / 64;           // 64-element column blocks
   static constexpr int kBlock = KT * 128;        // bytes of one of them
   static constexpr int kStage = 2 * kCols * kBlock;
-  static constexpr int kStages = 3;
-  static constexpr int kRaws = D == 64 ? 4 : 3;  // tiles of codes under way
+  static constexpr int kStages = 4;
   // a tile's codes, a scale pair a thread and four valid words
   static constexpr int kRawScale = KT * kRow * 2, kRaw = kRawScale + 1024 + 16;
   static constexpr int kQ = 128 * 128 * kCols;
-  static constexpr int kMerge = 128 * (D + 2) * 4;  // begins in place of q
+  static constexpr int kMerge = 128 * (64 + 2) * 4;  // begins in place of q
+  static constexpr int kRounds = D / 64;  // of handing it over
   static constexpr int kSide = KT * 8 + 64;  // scales, 4 valid words, 4 largest value scales
-  static constexpr int kSmem =
-      1024 + kStage * kStages + kMerge + kSide * kStages + 256 + kRaws * kRaw;
+  static constexpr int kRest = 1024 + kStage * kStages + kMerge + kSide * kStages + 256;
+  static constexpr int kFit = (226 * 1024 - kRest) / kRaw;
+  static constexpr int kRaws = kFit > 5 ? 5 : kFit;  // tiles of codes under way
+  static constexpr int kSmem = kRest + kRaws * kRaw;
   // TMEM columns of a stream: S, P, O
   static constexpr int kS = 0, kP = KT, kO = KT + KT / 2, kTmem = 256;
-  static_assert(kO + D <= kTmem && kSmem <= 227 * 1024 && kQ <= kMerge, "sizes");
+  static_assert(kO + D <= kTmem && kRaws >= 2 && kQ <= kMerge, "sizes");
   static constexpr int NP = KT * P / 128;  // pieces of a thread, keys or values
 };
 
@@ -89,7 +91,7 @@ struct Walk {
 };
 
 struct Bars {
-  uint64_t full[3], empty[3];        // tiles
+  uint64_t full[4], empty[4];           // tiles
   uint64_t s_full[2], s_free[2];     // a stream's scores
   uint64_t p_full[2][2], p_free[2][2];  // a stream's halves of probabilities
   uint64_t q_full, done, merge, merged;  // of a segment
@@ -123,8 +125,8 @@ __global__ void __launch_bounds__(512, 1) k13_tree_wide_kernel(const __grid_cons
   extern __shared__ char smem_raw[];
   char *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   char *qs = smem + NS * C::kStage;
-  float *mo = reinterpret_cast<float *>(qs);  // the second stream's O [D][128], over q
-  float *mm = mo + 128 * D, *ml = mm + 128;
+  float *mo = reinterpret_cast<float *>(qs);  // 64 columns of the second stream's O, over q
+  float *mm = mo + 128 * 64, *ml = mm + 128;
   char *side = reinterpret_cast<char *>(ml + 128);
   Bars &bar = *reinterpret_cast<Bars *>(side + NS * C::kSide);
   char *raw = side + NS * C::kSide + 256;
@@ -220,7 +222,7 @@ __global__ void __launch_bounds__(512, 1) k13_tree_wide_kernel(const __grid_cons
       const float rf = fmaxf(a.scale * kLog2e * (1.f / f), FLT_MIN);
       if (st == 0) {
         // (the second stream's results lay there)
-        if (seg > 0 && !(ok = wait(&bar.merged, seg - 1))) break;
+        if (seg > 0 && !(ok = wait(&bar.merged, seg * C::kRounds - 1))) break;
 #pragma unroll 2
         for (int i = 0; i < D / 8; ++i) {
           const uint4 x = live ? src[i] : make_uint4(0, 0, 0, 0);
@@ -299,19 +301,11 @@ __global__ void __launch_bounds__(512, 1) k13_tree_wide_kernel(const __grid_cons
         // instruction cache with the other roles').
         float s0 = 0.f, s1 = 0.f, top = -INFINITY;
         bool again = false;
-#pragma unroll 1
-        for (int c0 = 0; c0 < KT; c0 += 32) {
-          const int half = c0 >= HALF;
-          if (c0 == half * HALF) {
-            if (jt > 0 && !(ok = wait(&bar.p_free[st][half], jt - 1))) break;
-            tc::fence_after_sync();
-            s0 = s1 = 0.f;
-            top = -INFINITY;
-          }
+        auto weigh = [&](int c0, auto masked) {
           uint32_t u[32];
           tc::tmem_ld32(tm + C::kS + c0, u);
-          uint32_t seen = ~0u;  // of these 32 keys
-          if (!whole) {
+          [[maybe_unused]] uint32_t seen = ~0u;  // of these 32 keys
+          if constexpr (masked.value) {
             const int key = key0 + c0;
             const int before = min(max(w.s.past - key, 0), 32);  // keys of the prefix
             const int skip = min(max(first - key, 0), before);   // outside the window
@@ -338,7 +332,7 @@ __global__ void __launch_bounds__(512, 1) k13_tree_wide_kernel(const __grid_cons
             mul2(y[j], y[j + 1], kk.x, kk.y);
             mul2(y[j + 2], y[j + 3], kk.z, kk.w);
           }
-          if (!whole) {
+          if constexpr (masked.value) {
 #pragma unroll
             for (int j = 0; j < 32; ++j) y[j] = seen >> j & 1 ? y[j] : -INFINITY;
           }
@@ -366,7 +360,7 @@ __global__ void __launch_bounds__(512, 1) k13_tree_wide_kernel(const __grid_cons
             mul2(y[j], y[j + 1], vv.x, vv.y);
             mul2(y[j + 2], y[j + 3], vv.z, vv.w);
           }
-          if (!whole) {  // (a masked key's scale may be NaN)
+          if constexpr (masked.value) {  // (a masked key's scale may be NaN)
 #pragma unroll
             for (int j = 0; j < 32; ++j) y[j] = seen >> j & 1 ? y[j] : 0.f;
           }
@@ -374,6 +368,22 @@ __global__ void __launch_bounds__(512, 1) k13_tree_wide_kernel(const __grid_cons
 #pragma unroll
           for (int j = 0; j < 32; j += 2) p[j / 2] = pack_f16(y[j], y[j + 1]);
           tc::tmem_st16(tm + C::kP + c0 / 2, p);
+        };
+#pragma unroll 1
+        for (int c0 = 0; c0 < KT; c0 += 32) {
+          const int half = c0 >= HALF;
+          if (c0 == half * HALF) {
+            if (jt > 0 && !(ok = wait(&bar.p_free[st][half], jt - 1))) break;
+            tc::fence_after_sync();
+            s0 = s1 = 0.f;
+            top = -INFINITY;
+          }
+          // (two copies: one with masks under a condition would test and select
+          // for every element of every tile)
+          if (whole)
+            weigh(c0, std::false_type());
+          else
+            weigh(c0, std::true_type());
           if (c0 + 32 != (half + 1) * HALF) continue;
           // the half's end
           if (!again && __any_sync(~0u, top > thr)) {
@@ -410,8 +420,11 @@ __global__ void __launch_bounds__(512, 1) k13_tree_wide_kernel(const __grid_cons
       if (st == 1) {
         // (it goes where q lies: the first stream's scores must be done as well)
         if (!(ok = wait(&bar.done, seg))) break;
+        mm[row] = m;
+        ml[row] = l;
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
+          if (c % 64 == 0 && c && !(ok = wait(&bar.merged, seg * C::kRounds + c / 64 - 1))) break;
           uint32_t o[32];
           if (begun) {
             tc::tmem_ld32(tm + C::kO + c, o);
@@ -419,29 +432,41 @@ __global__ void __launch_bounds__(512, 1) k13_tree_wide_kernel(const __grid_cons
           }
 #pragma unroll
           for (int i = 0; i < 32; ++i)
-            mo[(c + i) * 128 + row] = begun ? __uint_as_float(o[i]) * vref : 0.f;
+            mo[(c % 64 + i) * 128 + row] = begun ? __uint_as_float(o[i]) * vref : 0.f;
+          if (c % 64) tc::mbar_arrive(&bar.merge);
         }
-        mm[row] = m;
-        ml[row] = l;
+        if (!ok) break;
         tc::fence_before_sync();
-        tc::mbar_arrive(&bar.merge);
       } else {
         tc::mbar_arrive(&bar.done);
-        if (!(ok = wait(&bar.merge, seg))) break;
-        const float m1 = mm[row], l1_ = ml[row], top = fmaxf(m, m1);
-        const float f0 = exp2f(m - top), f1 = exp2f(m1 - top), sum = f0 * l + f1 * l1_;
         const bool alone = w.from == 0 && w.to == w.s.units;
         float *part = k.part + ((size_t)blockIdx.x * 2 + (w.from == 0)) * 128 * (D + 2);
-        const float unit = f0 * vref, inv = sum == 0.f ? 0.f : 1.f / sum;
+        float unit = 0.f, other = 0.f, inv = 0.f;
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
+          if (c % 64 == 0) {
+            if (!(ok = wait(&bar.merge, seg * C::kRounds + c / 64))) break;
+            if (c == 0) {
+              const float m1 = mm[row], top = fmaxf(m, m1), f0 = exp2f(m - top);
+              other = exp2f(m1 - top);
+              const float sum = f0 * l + other * ml[row];
+              unit = f0 * vref;
+              inv = sum == 0.f ? 0.f : 1.f / sum;
+              if (live && !alone) {
+                part[128 * D + row] = top;
+                part[128 * D + 128 + row] = sum;
+              }
+            }
+          }
           uint32_t o[32];
           tc::tmem_ld32(tm + C::kO + c, o);  // (the first stream has a tile of every segment)
           tc::tmem_wait_ld();
           float y[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i)
-            y[element_of<F>(i)] = __uint_as_float(o[i]) * unit + mo[(c + i) * 128 + row] * f1;
+            y[element_of<F>(i)] =
+                __uint_as_float(o[i]) * unit + mo[(c % 64 + i) * 128 + row] * other;
+          if (c % 64) tc::mbar_arrive(&bar.merged);
           if (live && alone) {
             uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + at + c);
 #pragma unroll
@@ -458,12 +483,8 @@ __global__ void __launch_bounds__(512, 1) k13_tree_wide_kernel(const __grid_cons
           }
           __syncwarp();
         }
-        if (live && !alone) {
-          part[128 * D + row] = top;
-          part[128 * D + 128 + row] = sum;
-        }
+        if (!ok) break;
         tc::fence_before_sync();
-        tc::mbar_arrive(&bar.merged);
       }
       it += n;
     }
