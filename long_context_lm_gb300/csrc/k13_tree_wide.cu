@@ -49,7 +49,7 @@ struct Wide {
   static constexpr int kSmem = kRest + kRaws * kRaw;
   // TMEM columns of a stream: S, P, O
   static constexpr int kS = 0, kP = KT, kO = KT + KT / 2, kTmem = 256;
-  static_assert(kO + D <= kTmem && kRaws >= 2 && kQ <= kMerge, "sizes");
+  static_assert(128 / P % 16 == 0 && kO + D <= kTmem && kRaws >= 2 && kQ <= kMerge, "sizes");
   static constexpr int NP = KT * P / 128;  // pieces of a thread, keys or values
 };
 
@@ -64,6 +64,29 @@ constexpr uint32_t kNone = ~0u;
 template <int F>
 __device__ __forceinline__ constexpr int element_of(int i) {
   return F == FS_CACHE_INT4 ? (i & ~7) | ((i & 7) >> 1) | ((i & 1) << 2) : i;
+}
+
+// tc::mbar_wait with a hint of how long the thread may sleep in a try: nearly
+// all of these waits are long, and their polls would take issue slots from the
+// rows' warps.
+__device__ __forceinline__ bool wait_asleep(uint64_t *bar, uint32_t parity, int *fail) {
+  const long long t0 = clock64();
+  for (uint32_t i = 1;; ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+        " selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(1000000u)
+        : "memory");
+    if (ok) return true;
+    if ((i & 15u) == 0) {
+      if (clock64() - t0 > tc::kWaitCycles) break;
+      if (*reinterpret_cast<volatile int *>(fail) != 0) return false;
+    }
+  }
+  tc::report_error(fail, FS_ERR_TIMEOUT);
+  return false;
 }
 
 // The segments of a block, one after the other.
@@ -180,7 +203,7 @@ __global__ void __launch_bounds__(512, 1) k13_tree_wide_kernel(const __grid_cons
   Walk w{share.begin(blockIdx.x), share.begin(blockIdx.x + 1), line.begin, line.b, line.s, 0, 0, 0, 0};
   // Waits give up after a limit and say so in `fail`; every role then leaves its
   // loops for the barrier at the end.
-  auto wait_one = [&](uint64_t *b, uint32_t phase) { return tc::mbar_wait(b, phase & 1, &fail); };
+  auto wait_one = [&](uint64_t *b, uint32_t phase) { return wait_asleep(b, phase & 1, &fail); };
   auto wait = [&](uint64_t *b, uint32_t phase) {  // the same answer in a warp
     return (bool)__all_sync(~0u, wait_one(b, phase));
   };
@@ -523,28 +546,45 @@ __global__ void __launch_bounds__(512, 1) k13_tree_wide_kernel(const __grid_cons
       };
       uint32_t place = place_of(0, page_of(0));
       int later = page_of(AT), at = 0, left = w.s.end - w.s.first - w.from * KT;  // keys from here
+      const char *codes = static_cast<const char *>(a.c.codes) +
+                          (t / P % 16) * C::kRow + t % P * 16;  // the thread's piece of a group
       auto copy = [&](int slot) {
-        const uint32_t dst = smem_u32(raw) + slot * C::kRaw;
+        const uint32_t dst = smem_u32(raw) + slot * C::kRaw + t * 16;
+        const uint32_t to = smem_u32(raw) + slot * C::kRaw + C::kRawScale + t * 8;
+        uint32_t *word = reinterpret_cast<uint32_t *>(raw + slot * C::kRaw + C::kRawScale + 1024) +
+                         (t >> 5);
+        const uint32_t gs = __shfl_sync(~0u, place, at * GP + key_s / 16);
+        // (kNone in any of the tile's groups, or a tile that ends early)
+        if (left >= KT && !__any_sync(~0u, lane / GP == at && place == kNone)) {
 #pragma unroll
-        for (int j = 0; j < NP; ++j) {
-          const int r = t / P + j * (128 / P);
-          const uint32_t g = __shfl_sync(~0u, place, at * GP + r / 16);
-          const bool have = g != kNone && r < left;
-          const char *p = static_cast<const char *>(a.c.codes) +
-                          ((size_t)(have ? g : 0) * 16 + r % 16) * C::kRow + t % P * 16;
-          cp_async16z(dst + j * 2048 + t * 16, p, have ? 16 : 0);
-          cp_async16z(dst + (NP + j) * 2048 + t * 16, p + (have ? v_off * C::kRow : 0),
-                      have ? 16 : 0);
+          for (int j = 0; j < NP; ++j) {
+            const uint32_t g = __shfl_sync(~0u, place, at * GP + (t / P + j * (128 / P)) / 16);
+            const char *p = codes + (size_t)g * (16 * C::kRow);
+            cp_async16(dst + j * 2048, p);
+            cp_async16(dst + (NP + j) * 2048, p + v_off * C::kRow);
+          }
+          const float *p = a.c.scales + (size_t)gs * 16 + key_s % 16;
+          cp_async4(to, p);
+          cp_async4(to + 4, p + v_off);
+          if (lane == 0) *word = ~0u;
+        } else {
+#pragma unroll
+          for (int j = 0; j < NP; ++j) {
+            const int r = t / P + j * (128 / P);
+            const uint32_t g = __shfl_sync(~0u, place, at * GP + r / 16);
+            const bool have = g != kNone && r < left;
+            const char *p = have ? codes + (size_t)g * (16 * C::kRow)
+                                 : static_cast<const char *>(a.c.codes);
+            cp_async16z(dst + j * 2048, p, have ? 16 : 0);
+            cp_async16z(dst + (NP + j) * 2048, have ? p + v_off * C::kRow : p, have ? 16 : 0);
+          }
+          const bool in = gs != kNone && key_s < left;
+          const float *p = in ? a.c.scales + (size_t)gs * 16 + key_s % 16 : a.c.scales;
+          cp_async4z(to, p, in ? 4 : 0);
+          cp_async4z(to + 4, in ? p + v_off : p, in ? 4 : 0);
+          const uint32_t some = __ballot_sync(~0u, in);
+          if (lane == 0) *word = some;
         }
-        const uint32_t g = __shfl_sync(~0u, place, at * GP + key_s / 16);
-        const bool in = g != kNone && key_s < left;
-        const float *p = a.c.scales + (size_t)(in ? g : 0) * 16 + key_s % 16;
-        cp_async4z(dst + C::kRawScale + t * 8, p, in ? 4 : 0);
-        cp_async4z(dst + C::kRawScale + t * 8 + 4, p + (in ? v_off : 0), in ? 4 : 0);
-        const uint32_t word = __ballot_sync(~0u, in);
-        if (lane == 0)
-          *reinterpret_cast<uint32_t *>(raw + slot * C::kRaw + C::kRawScale + 1024 +
-                                        (t >> 5) * 4) = word;
         cp_async_commit();
         left -= KT;
         if (++at == AT) at = 0;
@@ -562,6 +602,12 @@ __global__ void __launch_bounds__(512, 1) k13_tree_wide_kernel(const __grid_cons
       for (int i = 0; i < kRaws - 1; ++i) copy_next(i);
       int slot = 0, stage = it % NS;
       uint32_t round = (uint32_t)(it / NS);
+      int chunk_at[128 / C::kBits / 8];
+#pragma unroll
+      for (int c = 0; c < 128 / C::kBits / 8; ++c) {
+        const int chunk = t % P * (128 / C::kBits / 8) + c;  // of the row's D / 8
+        chunk_at[c] = chunk / 8 * C::kBlock + swz128(t / P, chunk % 8);
+      }
 #pragma unroll 1
       for (int i = 0; i < n; ++i) {
         copy_next(slot == 0 ? kRaws - 1 : slot - 1);
@@ -569,19 +615,25 @@ __global__ void __launch_bounds__(512, 1) k13_tree_wide_kernel(const __grid_cons
         if (round > 0 && !(ok = wait(&bar.empty[stage], round - 1))) break;
         const char *src = raw + slot * C::kRaw;
         char *dst = smem + stage * C::kStage;
+        // (the row's place in the swizzle is the same for all of the thread's rows:
+        // they lie a multiple of eight apart)
+        constexpr int CH = 128 / C::kBits / 8;  // chunks of the piece: 2 or 4
 #pragma unroll 1
-        for (int j = 0; j < 2 * NP; ++j) {
-          const int part = j >= NP, r = t / P + (j - part * NP) * (128 / P);
-          const uint4 x = *reinterpret_cast<const uint4 *>(src + j * 2048 + t * 16);
-          const uint32_t wd[4] = {x.x, x.y, x.z, x.w};
-          constexpr int CH = 128 / C::kBits / 8;  // chunks of the piece: 2 or 4
+        for (int part = 0; part < 2; ++part) {
+          uint4 x[NP];
 #pragma unroll
-          for (int c = 0; c < CH; ++c) {
-            const int chunk = t % P * CH + c;  // of the row's D / 8
-            uint4 y;
-            to_chunk<F>(magic, wd + c * (4 / CH), y);
-            *reinterpret_cast<uint4 *>(dst + (part * C::kCols + chunk / 8) * C::kBlock +
-                                       swz128(r, chunk % 8)) = y;
+          for (int j = 0; j < NP; ++j)
+            x[j] = *reinterpret_cast<const uint4 *>(src + (part * NP + j) * 2048 + t * 16);
+          char *to = dst + part * (C::kCols * C::kBlock);
+#pragma unroll
+          for (int j = 0; j < NP; ++j) {
+            const uint32_t wd[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+              uint4 y;
+              to_chunk<F>(magic, wd + c * (4 / CH), y);
+              *reinterpret_cast<uint4 *>(to + chunk_at[c] + j * (128 / P) * 128) = y;
+            }
           }
         }
         const float2 sc = *reinterpret_cast<const float2 *>(src + C::kRawScale + t * 8);
