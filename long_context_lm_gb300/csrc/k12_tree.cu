@@ -29,9 +29,10 @@
 // the output at the end.
 //
 // Probabilities go into the second product as fp16 (half a step 2^-11) between
-// 0 and 2^15, so that one of 2^-38 of the largest still counts; with bf16
-// values as a bf16 pair (high and low part, 2^-16).  The maximum follows
-// lazily: a row's reference moves only when a score passes it by 8 (log2).
+// 0 and 2^15, the row's largest at least 2^11: half a step of the smallest is
+// 2^-36 of the largest; with bf16 values as a bf16 pair (high and low part,
+// 2^-16).  The maximum follows lazily: a row's reference moves only when a score
+// passes it by 4 (log2).
 #include <type_traits>
 
 #include "tree.cuh"

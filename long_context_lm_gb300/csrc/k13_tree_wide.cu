@@ -10,16 +10,16 @@
 //     stream with its own scores, probabilities, output (TMEM), running
 //     reference and sum, so that neither waits for the other;
 //   * one thread of warp 12 (13) issues the first (second) stream's products:
-//     S = Q K^T, then O += P V with P from TMEM, in two halves of the tile's
-//     keys, so that the next tile's S and the second half of P are made while
-//     the first half is multiplied.
+//     the next tile's S = Q K^T as soon as the rows have read this one's, then
+//     O += P V with P from TMEM.
 // The streams are joined through shared memory at the end of a segment.
 //
 // Scores, scales, references and probabilities are as in k12_tree.cu (q by a
 // power of two a row, fp16 probabilities up to 2^15, value scales relative to a
-// power of two that is part of the exponent here).  A half whose scores pass their reference by more than 8 (log2)
-// raises it, multiplies the row's O by the difference once no product is under
-// way, and is done again.
+// power of two that is part of the exponent here).  Where a score passes its
+// row's reference by more than 4 (log2), the reference is raised to it before the 32
+// columns are weighed: the row's sum, its O (between two products) and its
+// earlier probabilities of the tile are multiplied by the difference.
 //
 // Bound by: the exponentials and the roughly five operations around each
 // (128 x KT a tile), then the products' issue.
@@ -116,7 +116,7 @@ struct Walk {
 struct Bars {
   uint64_t full[4], empty[4];           // tiles
   uint64_t s_full[2], s_free[2];     // a stream's scores
-  uint64_t p_full[2][2], p_free[2][2];  // a stream's halves of probabilities
+  uint64_t p_full[2], p_free[2];        // a stream's probabilities
   uint64_t q_full, done, merge, merged;  // of a segment
 };
 
@@ -143,7 +143,7 @@ __device__ __forceinline__ void to_chunk(const Magic &m, const uint32_t *w, uint
 template <int F, int D>
 __global__ void __launch_bounds__(512, 1) k13_tree_wide_kernel(const __grid_constant__ TreeK k) {
   using C = Wide<F, D>;
-  constexpr int KT = C::KT, P = C::P, NS = C::kStages, NP = C::NP, HALF = KT / 2;
+  constexpr int KT = C::KT, P = C::P, NS = C::kStages, NP = C::NP;
   constexpr int kRaws = C::kRaws;
   extern __shared__ char smem_raw[];
   char *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -181,10 +181,8 @@ __global__ void __launch_bounds__(512, 1) k13_tree_wide_kernel(const __grid_cons
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&bar.s_full[i], 1);
       tc::mbar_init(&bar.s_free[i], 128);
-      for (int j = 0; j < 2; ++j) {
-        tc::mbar_init(&bar.p_full[i][j], 128);
-        tc::mbar_init(&bar.p_free[i][j], 1);
-      }
+      tc::mbar_init(&bar.p_full[i], 128);
+      tc::mbar_init(&bar.p_free[i], 1);
     }
     tc::mbar_init(&bar.q_full, 128);
     tc::mbar_init(&bar.done, 128);
@@ -269,22 +267,18 @@ __global__ void __launch_bounds__(512, 1) k13_tree_wide_kernel(const __grid_cons
 
       float m = -FLT_MAX, thr = -INFINITY, l0 = 0.f, l1 = 0.f, vref = kLeast;
       bool begun = false;  // O holds something
-      // O *= by, once no product is under way: those of this tile's first half
-      // and of the last tile
-      auto rescale = [&](float by, int half) -> bool {
-        if (jt > 0 || half)
-          if (!wait(&bar.p_free[st][0], half ? jt : jt - 1)) return false;
-        if (jt > 0)
-          if (!wait(&bar.p_free[st][1], jt - 1)) return false;
+      // O *= by, once the last tile's product has ended (this one's has not begun)
+      auto rescale = [&](float by) -> bool {
+        if (jt > 0 && !wait(&bar.p_free[st], jt - 1)) return false;
         tc::fence_after_sync();
 #pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
-          uint32_t o[32];
-          tc::tmem_ld32(tm + C::kO + c, o);
+        for (int c = 0; c < D; c += 8) {  // (few registers: 32 columns wait meanwhile)
+          uint32_t o[8];
+          tc::tmem_ld8(tm + C::kO + c, o);
           tc::tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * by);
-          tc::tmem_st32(tm + C::kO + c, o);
+          for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * by);
+          tc::tmem_st8(tm + C::kO + c, o);
         }
         tc::tmem_wait_st();
         return true;
@@ -312,18 +306,14 @@ __global__ void __launch_bounds__(512, 1) k13_tree_wide_kernel(const __grid_cons
           const float up =
               __uint_as_float((__float_as_uint(top_v) + 0x7fffffu) & 0x7f800000u);
           const float back = vref / up;
-          if (begun && !(ok = rescale(back, 0))) break;
+          if (begun && !(ok = rescale(back))) break;
           l0 *= back;
           l1 *= back;
           vref = up;
         }
         const float lift = 15.f - kRaise - (float)((int)(__float_as_uint(vref) >> 23) - 127);
 
-        // The columns, 32 at a time; what belongs to a half's beginning or end is
-        // done in its first or last round (one copy of the code: it shares the
-        // instruction cache with the other roles').
-        float s0 = 0.f, s1 = 0.f, top = -INFINITY;
-        bool again = false;
+        // The columns, 32 at a time.
         auto weigh = [&](int c0, auto masked) {
           uint32_t u[32];
           tc::tmem_ld32(tm + C::kS + c0, u);
@@ -342,8 +332,11 @@ __global__ void __launch_bounds__(512, 1) k13_tree_wide_kernel(const __grid_cons
             }
             seen &= valid[c0 / 32];
           }
-          const float ref = lift - m;
           tc::tmem_wait_ld();
+          if (c0 + 32 == KT) {  // the next tile's scores may be made
+            tc::fence_before_sync();
+            tc::mbar_arrive(&bar.s_free[st]);
+          }
           // Step by step over all 32 columns: each step's operations do not wait
           // for one another.
           float y[32];
@@ -365,7 +358,33 @@ __global__ void __launch_bounds__(512, 1) k13_tree_wide_kernel(const __grid_cons
             t0 = max3f(t0, y[j], y[j + 1]);
             if (j + 2 < 32) t1 = max3f(t1, y[j + 2], y[j + 3]);
           }
-          top = max3f(top, t0, t1);
+          t0 = fmaxf(t0, t1);
+          if (__any_sync(~0u, t0 > thr)) {  // raise the rows' references
+            // by a whole number, so that the factor is a power of two: exact for the
+            // fp16 probabilities that are made already
+            const float by_log2 = ceilf(fmaxf(t0 * rf - m, 0.f));
+            const bool none = m == -FLT_MAX;  // the row has seen no key
+            const float back = none ? 0.f : exp2f(-by_log2);
+            m = none ? fmaxf(t0 * rf, -FLT_MAX) : m + by_log2;
+            if (m > -FLT_MAX) thr = (m + kRaise) / rf;
+            l0 *= back;
+            l1 *= back;
+            if (begun) ok = rescale(back);
+#pragma unroll 1
+            for (int c = 0; c < c0 / 2; c += 8) {  // this tile's earlier columns
+              uint32_t z[8];
+              tc::tmem_wait_st();
+              tc::tmem_ld8(tm + C::kP + c, z);
+              tc::tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&z[i]));
+                z[i] = pack_f16(f.x * back, f.y * back);
+              }
+              tc::tmem_st8(tm + C::kP + c, z);
+            }
+          }
+          const float ref = lift - m;
 #pragma unroll
           for (int j = 0; j < 32; j += 2) fma2(y[j], y[j + 1], y[j], y[j + 1], rf, ref);
 #pragma unroll
@@ -373,10 +392,10 @@ __global__ void __launch_bounds__(512, 1) k13_tree_wide_kernel(const __grid_cons
           float s2 = 0.f, s3 = 0.f;
 #pragma unroll
           for (int j = 0; j < 32; j += 4) {
-            add2(s0, s1, y[j], y[j + 1]);
+            add2(l0, l1, y[j], y[j + 1]);
             add2(s2, s3, y[j + 2], y[j + 3]);
           }
-          add2(s0, s1, s2, s3);
+          add2(l0, l1, s2, s3);
 #pragma unroll
           for (int j = 0; j < 32; j += 4) {
             const float4 vv = *reinterpret_cast<const float4 *>(ks + KT + c0 + j);
@@ -390,53 +409,31 @@ __global__ void __launch_bounds__(512, 1) k13_tree_wide_kernel(const __grid_cons
           uint32_t p[16];
 #pragma unroll
           for (int j = 0; j < 32; j += 2) p[j / 2] = pack_f16(y[j], y[j + 1]);
+          if (c0 == 0 && jt > 0) {  // the last tile's product has read P
+            ok = wait(&bar.p_free[st], jt - 1) && ok;
+            tc::fence_after_sync();
+          }
           tc::tmem_st16(tm + C::kP + c0 / 2, p);
         };
+        // (two copies: one with masks under a condition would test and select for
+        // every element of every tile)
+        if (whole) {
 #pragma unroll 1
-        for (int c0 = 0; c0 < KT; c0 += 32) {
-          const int half = c0 >= HALF;
-          if (c0 == half * HALF) {
-            if (jt > 0 && !(ok = wait(&bar.p_free[st][half], jt - 1))) break;
-            tc::fence_after_sync();
-            s0 = s1 = 0.f;
-            top = -INFINITY;
-          }
-          // (two copies: one with masks under a condition would test and select
-          // for every element of every tile)
-          if (whole)
-            weigh(c0, std::false_type());
-          else
-            weigh(c0, std::true_type());
-          if (c0 + 32 != (half + 1) * HALF) continue;
-          // the half's end
-          if (!again && __any_sync(~0u, top > thr)) {
-            // P has not been handed on: raise the reference, write it again
-            const float up = fmaxf(m, top * rf);
-            const float back = exp2f(m - up);
-            m = up;
-            if (up > -FLT_MAX) thr = (up + kRaise) / rf;
-            l0 *= back;
-            l1 *= back;
-            tc::tmem_wait_st();
-            if (begun && !(ok = rescale(back, half))) break;
-            again = true;
-            c0 -= HALF;
-            continue;
-          }
-          again = false;
-          add2(l0, l1, s0, s1);
-          tc::tmem_wait_st();
-          tc::fence_before_sync();
-          tc::mbar_arrive(&bar.p_full[st][half]);
-          begun = true;
+          for (int c0 = 0; ok && c0 < KT; c0 += 32) weigh(c0, std::false_type());
+        } else {
+#pragma unroll 1
+          for (int c0 = 0; ok && c0 < KT; c0 += 32) weigh(c0, std::true_type());
         }
         if (!ok) break;
-        tc::mbar_arrive(&bar.s_free[st]);
+        tc::tmem_wait_st();
+        tc::fence_before_sync();
+        tc::mbar_arrive(&bar.p_full[st]);
+        begun = true;
       }
       if (!ok) break;
       // the segment's end: all products of the stream
       if (begun) {
-        if (!(ok = wait(&bar.p_free[st][0], jt - 1) && wait(&bar.p_free[st][1], jt - 1))) break;
+        if (!(ok = wait(&bar.p_free[st], jt - 1))) break;
         tc::fence_after_sync();
       }
       const float l = (l0 + l1) * vref;
@@ -695,25 +692,19 @@ __global__ void __launch_bounds__(512, 1) k13_tree_wide_kernel(const __grid_cons
       int now = stage;  // of the values
       if (st < n && !(ok = scores(jt))) break;
       for (int i = st; i < n; i += 2, ++jt) {
-#pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
-          if (!(ok = wait_one(&bar.p_full[st][half], jt))) break;
-          tc::fence_after_sync();
-          const uint32_t v = ring + now * C::kStage + C::kCols * C::kBlock;
+        // the next tile's scores first: they are there when this one's rows are done
+        if (i + 2 < n && !(ok = scores(jt + 1))) break;
+        if (!(ok = wait_one(&bar.p_full[st], jt))) break;
+        tc::fence_after_sync();
+        const uint32_t v = ring + now * C::kStage + C::kCols * C::kBlock;
 #pragma unroll
-          for (int c = 0; c < C::kCols; ++c)
+        for (int c = 0; c < C::kCols; ++c)
 #pragma unroll
-            for (int s = 0; s < HALF / 16; ++s) {
-              const int key = half * HALF + s * 16;
-              tc::mma_ts(tm + C::kO + c * 64, tm + C::kP + key / 2,
-                         tc::desc_sw128(v + c * C::kBlock + key * 128), kPV,
-                         i != st || half || s > 0);
-            }
-          tc::mma_commit(&bar.p_free[st][half]);
-          if (half) tc::mma_commit(&bar.empty[now]);
-          if (!half && i + 2 < n && !(ok = scores(jt + 1))) break;
-        }
-        if (!ok) break;
+          for (int s = 0; s < KT / 16; ++s)
+            tc::mma_ts(tm + C::kO + c * 64, tm + C::kP + s * 8,
+                       tc::desc_sw128(v + c * C::kBlock + s * 2048), kPV, i != st || s > 0);
+        tc::mma_commit(&bar.p_free[st]);
+        tc::mma_commit(&bar.empty[now]);
         now = now + 2 >= NS ? now + 2 - NS : now + 2;
       }
       it += n;

@@ -13,7 +13,7 @@
 namespace fs {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kRaise = 8.f;    // how far a score may pass its reference (log2)
+constexpr float kRaise = 4.f;  // how far a score may pass its reference (log2)
 
 // ---------------------------------------------------------------------------
 // the line of units
