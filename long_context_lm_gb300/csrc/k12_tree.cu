@@ -29,10 +29,10 @@
 // the output at the end.
 //
 // Probabilities go into the second product as fp16 (half a step 2^-11) between
-// 0 and 2^15, the row's largest at least 2^11: half a step of the smallest is
-// 2^-36 of the largest; with bf16 values as a bf16 pair (high and low part,
+// 0 and 2^15, the row's largest at least 2^7: half a step of the smallest is
+// 2^-32 of the largest; with bf16 values as a bf16 pair (high and low part,
 // 2^-16).  The maximum follows lazily: a row's reference moves only when a score
-// passes it by 4 (log2).
+// passes it by 8 (log2).
 #include <type_traits>
 
 #include "tree.cuh"
@@ -848,15 +848,20 @@ template <int F>
 cudaError_t launch_f(const TreeK &k, cudaStream_t st) {
   const bool one = k.a.T * k.G <= 16;
   if (k.a.c.d == 64) return one ? launch_mt<F, 64, 1>(k, st) : launch_mt<F, 64, 2>(k, st);
-  return one ? launch_mt<F, 128, 1>(k, st) : launch_mt<F, 128, 2>(k, st);
+  if constexpr (F == FS_CACHE_BF16)
+    if (!one) return launch_mt<F, 128, 2>(k, st);
+  return launch_mt<F, 128, 1>(k, st);
 }
 
 }  // namespace
 
-// From how many rows to a kv head on 128 of them are taken at a time.
-constexpr int kWideRows = 33;
+// Whether 128 rows are taken at a time, on tcgen05: from more rows to a kv head
+// than the kernel above does well.  Measured on 4 sequences of 16384 int8 keys, 8
+// kv heads, here against there: d = 64 with 32 rows 45 and 54 us, 48 rows 58 and
+// 55, 128 rows 91 and 59; d = 128, whose 32 rows do not fit the registers, 32 rows
+// 88 and 77, 128 rows 215 and 86.  (bf16 codes are not exact in fp16: here.)
 bool wide(const fs_cache &c, int H, int T) {
-  return c.format != FS_CACHE_BF16 && H / c.Hkv * T >= kWideRows;
+  return c.format != FS_CACHE_BF16 && H / c.Hkv * T > (c.d == 64 ? 32 : 16);
 }
 
 template <int D, int ROWS>

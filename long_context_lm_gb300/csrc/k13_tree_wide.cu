@@ -17,7 +17,7 @@
 // Scores, scales, references and probabilities are as in k12_tree.cu (q by a
 // power of two a row, fp16 probabilities up to 2^15, value scales relative to a
 // power of two that is part of the exponent here).  Where a score passes its
-// row's reference by more than 4 (log2), the reference is raised to it before the 32
+// row's reference by more than 8 (log2), the reference is raised to it before the 32
 // columns are weighed: the row's sum, its O (between two products) and its
 // earlier probabilities of the tile are multiplied by the difference.
 //
@@ -272,13 +272,13 @@ __global__ void __launch_bounds__(512, 1) k13_tree_wide_kernel(const __grid_cons
         if (jt > 0 && !wait(&bar.p_free[st], jt - 1)) return false;
         tc::fence_after_sync();
 #pragma unroll 1
-        for (int c = 0; c < D; c += 8) {  // (few registers: 32 columns wait meanwhile)
-          uint32_t o[8];
-          tc::tmem_ld8(tm + C::kO + c, o);
+        for (int c = 0; c < D; c += 16) {  // (few registers: 32 columns wait meanwhile)
+          uint32_t o[16];
+          tc::tmem_ld16(tm + C::kO + c, o);
           tc::tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * by);
-          tc::tmem_st8(tm + C::kO + c, o);
+          for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * by);
+          tc::tmem_st16(tm + C::kO + c, o);
         }
         tc::tmem_wait_st();
         return true;

@@ -13,7 +13,10 @@
 namespace fs {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kRaise = 4.f;  // how far a score may pass its reference (log2)
+// How far a score may pass its row's reference (log2).  Raising one costs the wide
+// kernel a pass over its O: 8 against 4 is 157 against 168 us for 64 tokens x 32
+// heads over 16384 int8 keys.
+constexpr float kRaise = 8.f;
 
 // ---------------------------------------------------------------------------
 // the line of units

@@ -767,7 +767,9 @@ def fs_rope(q, k, pos, plan, inverse=False, q_out=None, k_out=None, stream=None)
     qp, qs = _rows(q, dev, "q", dt, shape)
     if q_out is None:
         q_out = torch.empty_like(q)
-    qop, qos = _rows(q_out, dev, "q_out", dt, shape)
+        qop, qos = (q_out.data_ptr(), None) if qs is None else _rows(q_out, dev, "q_out", dt, shape)
+    else:
+        qop, qos = _rows(q_out, dev, "q_out", dt, shape)
     kp = ks = kop = kos = None
     Hk = 0
     if k is not None:
@@ -776,7 +778,10 @@ def fs_rope(q, k, pos, plan, inverse=False, q_out=None, k_out=None, stream=None)
         kp, ks = _rows(k, dev, "k", dt, shape)
         if k_out is None:
             k_out = torch.empty_like(k)
-        kop, kos = _rows(k_out, dev, "k_out", dt, shape)
+            kop, kos = (k_out.data_ptr(), None) if ks is None else \
+                _rows(k_out, dev, "k_out", dt, shape)
+        else:
+            kop, kos = _rows(k_out, dev, "k_out", dt, shape)
     pp, stride, pos0 = None, 0, 0
     if isinstance(pos, int):
         pos0 = pos

@@ -7,13 +7,13 @@ scale factors included), so a probability is off by that much (ds) relative,
 and by 2^-21 for the exponential and the running rescaling.  A probability is
 held for the product with the values in no less than fp16: half a step is 2^-11
 relative and, below 2^-14, 2^-25.  The largest probability of a row, and with it
-their sum, is held as 2^11 at least (a reference follows the maximum to within a
-factor of 16 below the 2^15 that the largest may reach), so 2^-25 is 2^-36 of
+their sum, is held as 2^7 at least (a reference follows the maximum to within a
+factor of 2^8 below the 2^15 that the largest may reach), so 2^-25 is 2^-32 of
 the sum, twice that where a probability is scaled down to a new reference and
-rounded again; the value it multiplies is |v| at most: n 2^-35 max|v| together.
+rounded again; the value it multiplies is |v| at most: n 2^-31 max|v| together.
 The values are exact, or scaled in fp32 (2^-24).  The sum of probabilities is off
 by ds + 2^-20.  So the output is within
-    (2 ds + 2^-11 + 2^-18) M + n 2^-35 max|v|,   M = sum p |v| / sum p,
+    (2 ds + 2^-11 + 2^-18) M + n 2^-31 max|v|,   M = sum p |v| / sum p,
 and then rounded to bf16, by at most 2^-8 relative."""
 import pytest
 import torch
@@ -73,7 +73,7 @@ def _check(q, cache, past, out, tree=None, count=None, window=0, scale=None):
         x = x[torch.isfinite(x)]
         vmax = max(vmax, float(x.abs().max()) if x.numel() else 0.0)
     bound = 1.01 * 2.0 ** -8 * want.abs() + (2 * ds + 2.0 ** -11 + 2.0 ** -18) * mean + \
-        (max(past) + T) * 2.0 ** -35 * vmax
+        (max(past) + T) * 2.0 ** -31 * vmax
     for b, n in enumerate(count):
         w, o = want[b, :, :n], out[b, :, :n].double()
         fine = torch.isfinite(w)
