@@ -4,7 +4,7 @@
 //
 // A row of d elements belongs to d / 16 neighbouring lanes, sixteen elements (two
 // 16-byte pieces of bf16) each; the row's largest magnitude is a shuffle
-// reduction over them.  A block takes up to 128 tokens of one (sequence, head,
+// reduction over them.  A block takes up to 256 tokens of one (sequence, head,
 // key or value); their pages are looked up once, into shared memory, and all
 // loads of a thread stand before their first use.  Bound by memory (append: 2 d
 // bytes in, d bits / 8 + 4 out a row; read: the other way) as long as no more
@@ -317,8 +317,10 @@ cudaError_t read(const CacheRowsArgs &a, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-// Two rows a thread keep 64 bytes of loads in flight; with no more tokens than a
-// block of single rows has, that would only idle threads.
+// Four rows a thread keep 128 bytes of loads in flight for the append (65536 x 16
+// x 64 to e4m3 and back 140 us, two rows 146, one 163), two for the read (four:
+// 143); with no more tokens than a block of single rows has, more would only idle
+// threads.
 template <int L>
 bool few(const CacheRowsArgs &a) {
   return a.T <= Rows<L, 1>::kAll;
@@ -333,8 +335,8 @@ cudaError_t read_l(const CacheRowsArgs &a, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_cache_append(const CacheRowsArgs &a, cudaStream_t st) {
-  if (a.c.d == 64) return few<4>(a) ? append<4, 1>(a, st) : append<4, 2>(a, st);
-  return few<8>(a) ? append<8, 1>(a, st) : append<8, 2>(a, st);
+  if (a.c.d == 64) return few<4>(a) ? append<4, 1>(a, st) : append<4, 4>(a, st);
+  return few<8>(a) ? append<8, 1>(a, st) : append<8, 4>(a, st);
 }
 
 cudaError_t launch_cache_read(const CacheRowsArgs &a, cudaStream_t st) {
