@@ -73,7 +73,7 @@ struct Cfg {
   static constexpr int kRow = D * kBits / 8;  // bytes of a row
   static constexpr int P = kRow / 16;         // 16-byte pieces of a row
   static constexpr int kM = 16 * MT;
-  static constexpr int kWarps = kRow >= 256 ? 4 : D == 128 && MT == 1 ? 12 : 8;
+  static constexpr int kWarps = kRow >= 256 ? 4 : 8;
   static constexpr int kCodes = kUnit * kRow;  // bytes of a unit's keys
   // keys, values, 32 + 32 scales, which keys can be read
   static constexpr int kStage = 2 * kCodes + 8 * kUnit + 16;
@@ -220,15 +220,13 @@ k12_tree_kernel(const __grid_constant__ TreeK k) {
   if (blockIdx.x == 0)
     for (int i = tid; i < a.c.batch; i += W * 32)
       if (a.c.status && seq_outside(k, i)) atomicCAS(a.c.status, 0, FS_ERR_CACHE);
-  const Line line = line_of(k, [&](long long total, int, long long x, long long y) {
-    if (total == 0) return false;
-    const Share share(k, total);
+  const Line line = line_of(k, [&](const Share &share, int, long long x, long long y) {
     const long long at = share.begin(blockIdx.x);
     return (int)blockIdx.x < share.blocks && at >= x && at < y;
   });
   const long long total = line.total;
   if (total == 0) return;
-  const Share share(k, total);
+  const Share &share = line.share;
   if ((int)blockIdx.x >= share.blocks) return;
   const long long u0 = share.begin(blockIdx.x), u1 = share.begin(blockIdx.x + 1);
   int b = line.b;
@@ -241,6 +239,13 @@ k12_tree_kernel(const __grid_constant__ TreeK k) {
   const int v_off = a.c.Hkv * a.c.page;  // rows from a key to its value
 
   uint32_t whole_units = 0;  // stages whose 32 keys can all be read
+  // where the lane's words of keys g and values 2 c, 2 c + 1 lie in a stage
+  constexpr int VW = D == 64 ? C::kBits / 4 : (C::kBF ? 4 : C::kBits / 2);  // words at a time
+  const int v_byte = g * VW * 4;  // inside the row (its first set)
+  const int k_at = D * C::kBits / 128 == 2 ? g * C::kRow + c * 8 : k_place<P>(g, c) * 16;
+  [[maybe_unused]] const int k_half = (k_at & 64) ? -64 : 64;
+  const int v_at[2] = {v_place<P>(2 * c, v_byte / 16) * 16 + v_byte % 16,
+                       v_place<P>(2 * c + 1, v_byte / 16) * 16 + v_byte % 16};
 
   long long u = u0;
   while (u < u1) {
@@ -249,13 +254,25 @@ k12_tree_kernel(const __grid_constant__ TreeK k) {
       s = seq_of(k, ++b);
     }
     if (s.units == 0) break;  // (lengths that changed under the call)
-    const int seg = (int)((u - begin) / s.units);
+    const int seg = (int)quot(u - begin, s.units);
     const long long seg0 = begin + (long long)seg * s.units;
     const int rt = seg % s.tiles, h = seg / s.tiles;
     const int from = (int)(u - seg0), to = (int)min((long long)s.units, u1 - seg0);
     const int rows = s.n * k.G;
 
     __syncthreads();  // the ring held the last segment's results
+    // q first: loads behind the units' copies would wait for them
+    uint32_t raw[MT][2][KS][2];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        const int r = rt * M + mt * 16 + hf * 8 + g;
+        const bool live = r < rows;
+        const int t = live ? r / k.G : 0, head = h * k.G + (live ? r % k.G : 0);
+        q_words<F, D>(static_cast<const uint16_t *>(a.q) + (((size_t)b * a.H + head) * a.T + t) * D,
+                      c, live, raw[mt][hf]);
+      }
     // Where sixteen of the warp's units lie, two halves of sixteen rows to a unit:
     // lane 2 i + j holds half j of unit x + W i, as its place among all groups of
     // sixteen rows (kNone: nothing to read).  The table is read sixteen units
@@ -365,18 +382,11 @@ k12_tree_kernel(const __grid_constant__ TreeK k) {
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
-        const int r = rt * M + mt * 16 + hf * 8 + g;
-        const bool live = r < rows;
-        const int t = live ? r / k.G : 0, head = h * k.G + (live ? r % k.G : 0);
-        const uint16_t *src = static_cast<const uint16_t *>(a.q) +
-                              (((size_t)b * a.H + head) * a.T + t) * D;
-        uint32_t raw[KS][2];
-        q_words<F, D>(src, c, live, raw);
         uint32_t most = 0;
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) most = __vmaxu2(most, raw[ks][e] & 0x7fff7fffu);
+          for (int e = 0; e < 2; ++e) most = __vmaxu2(most, raw[mt][hf][ks][e] & 0x7fff7fffu);
         most = max(most & 0xffffu, most >> 16);
         float f = 1.f;
         if constexpr (!C::kBF) {
@@ -391,7 +401,7 @@ k12_tree_kernel(const __grid_constant__ TreeK k) {
         for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            uint32_t x = raw[ks][e];
+            uint32_t x = raw[mt][hf][ks][e];
             if constexpr (!C::kBF) {
               x = pack_f16(bf16_lo(x) * f, bf16_hi(x) * f);
               if constexpr (kBias<F> != 0.f) {
@@ -421,39 +431,14 @@ k12_tree_kernel(const __grid_constant__ TreeK k) {
       m[mt][0] = m[mt][1] = -FLT_MAX;
       thr[mt][0] = thr[mt][1] = -INFINITY;
     }
-    float vref = 0x1p-126f;
+    float vref = kLeast;
 
     int stage = 0;
     for (int x = from + warp; x < to; x += W) {
-      issue_next(stage == 0 ? NS - 1 : stage - 1);
-      cp_async_wait<NS - 1>();
+      cp_async_wait<NS - 2>();
       __syncwarp();
       const char *st = ring + stage * C::kStage;
-      const int key0 = s.first + x * kUnit;
-      const bool whole = (whole_units >> stage & 1) && key0 + kUnit <= s.past && key0 >= lead;
-
-      float sc[MT][4][4];
-#pragma unroll
-      for (int nt = 0; nt < 4; ++nt) {
-        constexpr int KW = D * C::kBits / 128;  // words of a lane: a quarter of the row
-        uint32_t w[KW];
-        const int r = nt * 8 + g;
-        if constexpr (KW <= 4) {
-          lds_words<KW>(st + (KW == 2 ? r * C::kRow + c * 8 : k_place<P>(r, c) * 16), w);
-        } else {
-#pragma unroll
-          for (int j = 0; j < KW / 4; ++j) lds_words<4>(st + k_place<P>(r, c + 4 * j) * 16, w + 4 * j);
-        }
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-          uint32_t b0, b1;
-          k_regs<F>(magic, w, ks, b0, b1);
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) mma16816<C::kBF>(sc[mt][nt], q[mt][ks], b0, b1, ks > 0);
-        }
-      }
-      // scales, masks, the rows' references
-      float vf[4][2];  // value scales over vref
+      // the value scales' power of two, before anything waits for the products
       const float *kscale = reinterpret_cast<const float *>(st + 2 * C::kCodes);
       if constexpr (!C::kBF) {
         const float mine = kscale[kUnit + lane];
@@ -464,20 +449,50 @@ k12_tree_kernel(const __grid_constant__ TreeK k) {
           const float back = vref / up;
           vref = up;
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
+          for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) l[mt][e / 2][e % 2] *= back;
 #pragma unroll
             for (int i = 0; i < NT; ++i)
 #pragma unroll
               for (int e = 0; e < 4; ++e) o[mt][i][e] *= back;
+          }
         }
-        const float inv = __uint_as_float(0x7f000000u - __float_as_uint(vref));  // a power of two
+      }
+      const int key0 = s.first + x * kUnit;
+      const bool whole = (whole_units >> stage & 1) && key0 + kUnit <= s.past && key0 >= lead;
+
+      float sc[MT][4][4];
+#pragma unroll
+      for (int nt = 0; nt < 4; ++nt) {
+        constexpr int KW = D * C::kBits / 128;  // words of a lane: a quarter of the row
+        uint32_t w[KW];
+        const char *row = st + k_at + nt * 8 * C::kRow;
+        if constexpr (KW <= 4) {
+          lds_words<KW>(row, w);
+        } else {
+          // (four pieces on: within a row of eight the place's other half)
+#pragma unroll
+          for (int j = 0; j < KW / 4; ++j)
+            lds_words<4>(P == 8 ? st + (k_at ^ (64 * j)) + nt * 8 * C::kRow
+                                : row + (j & 1 ? k_half : 0) + j / 2 * 128,
+                         w + 4 * j);
+        }
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          uint32_t b0, b1;
+          k_regs<F>(magic, w, ks, b0, b1);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) mma16816<C::kBF>(sc[mt][nt], q[mt][ks], b0, b1, ks > 0);
+        }
+      }
+      // the next unit's copies while the products are under way
+      issue_next(stage == 0 ? NS - 1 : stage - 1);
+      // scales, masks, the rows' references
+      if constexpr (!C::kBF) {
 #pragma unroll
         for (int nt = 0; nt < 4; ++nt) {
           const float2 ks = *reinterpret_cast<const float2 *>(kscale + nt * 8 + 2 * c);
-          const float2 vs = *reinterpret_cast<const float2 *>(kscale + kUnit + nt * 8 + 2 * c);
-          vf[nt][0] = vs.x;
-          vf[nt][1] = vs.y;
-          mul2(vf[nt][0], vf[nt][1], inv, inv);
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -548,12 +563,23 @@ k12_tree_kernel(const __grid_constant__ TreeK k) {
       }
       // probabilities, at most 2^15 (fp16) or 1 (bf16)
       constexpr float kLift = C::kBF ? -kRaise : 15.f - kRaise;
+      const float lift =
+          C::kBF ? kLift : kLift - (float)((int)(__float_as_uint(vref) >> 23) - 127);
       auto weigh = [&](auto masked) {
+        [[maybe_unused]] float vf[4][2];
+        if constexpr (!C::kBF) {
+#pragma unroll
+          for (int nt = 0; nt < 4; ++nt) {
+            const float2 vs = *reinterpret_cast<const float2 *>(kscale + kUnit + nt * 8 + 2 * c);
+            vf[nt][0] = vs.x;
+            vf[nt][1] = vs.y;
+          }
+        }
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
-            const float ref = kLift - m[mt][hf];
+            const float ref = lift - m[mt][hf];
 #pragma unroll
             for (int nt = 0; nt < 4; ++nt) {
               float &x = sc[mt][nt][2 * hf], &y = sc[mt][nt][2 * hf + 1];
@@ -641,17 +667,15 @@ k12_tree_kernel(const __grid_constant__ TreeK k) {
                 p[mt][j] = pack_f16(x0, x1);
               }
             }
-          const int r0 = 16 * kk + 2 * c;
-          constexpr int VW = D == 64 ? C::kBits / 4 : (C::kBF ? 4 : C::kBits / 2);  // words at a time
           constexpr int SETS = C::kBF ? D / 64 : 1;
 #pragma unroll
           for (int set = 0; set < SETS; ++set) {
             uint32_t w[4][VW];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const int r = r0 + (i & 1) + 8 * (i >> 1);
-              const int byte = g * VW * 4;  // inside the row (its first set)
-              lds_words<VW>(vs + v_place<P>(r, byte / 16 + 8 * set) * 16 + byte % 16, w[i]);
+              // row 16 kk + 2 c + (i & 1) + 8 (i / 2): eight rows on, the places repeat
+              lds_words<VW>(vs + v_at[i & 1] + (16 * kk + 8 * (i >> 1)) * C::kRow + 128 * set,
+                            w[i]);
             }
 #pragma unroll
             for (int j = 0; j < NT / SETS / 2; ++j) {
@@ -694,7 +718,7 @@ k12_tree_kernel(const __grid_constant__ TreeK k) {
         if (row >= live) continue;
         if (c == 0) {
           jm[r] = m[mt][hf];
-          jl[r] = sum;
+          jl[r] = C::kBF ? sum : sum * vref;
         }
         const float unit = C::kBF ? 1.f : vref;
 #pragma unroll
@@ -755,14 +779,14 @@ __global__ void __launch_bounds__(256) k12_join_kernel(const __grid_constant__ T
   __shared__ float red[2][8];
   __shared__ float4 acc[LANES > 32 ? 8 * L : 1];
   const int b = blockIdx.z, h = blockIdx.y, tid = threadIdx.x, lane = tid % LANES;
-  const Line line = line_of(k, [&](long long, int i, long long, long long) { return i == b; });
+  const Line line = line_of(k, [&](const Share &, int i, long long, long long) { return i == b; });
   const Seq s = line.s;
   // What the earlier kernel wrote is read after this; every block waits, so that
   // the end of this kernel is the end of both.
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int rows = s.n * k.G, row0 = blockIdx.x * ROWS;
   if (row0 >= rows || s.units == 0) return;
-  const Share share(k, line.total);
+  const Share &share = line.share;
   const int rt = row0 / k.M, M = k.M;
   const long long s0 = line.begin + ((long long)h * s.tiles + rt) * s.units;
   const int c0 = share.of(s0), c1 = share.of(s0 + s.units - 1);

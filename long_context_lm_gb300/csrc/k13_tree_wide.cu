@@ -53,10 +53,6 @@ struct Wide {
   static constexpr int NP = KT * P / 128;  // pieces of a thread, keys or values
 };
 
-// The least power of two that the value scales are relative to.  Probabilities
-// are made 1 / vref times as large (the products with the scales then need no
-// second factor), and stay within fp32 with their sum.
-constexpr float kLeast = 0x1p-90f;
 constexpr uint32_t kNone = ~0u;
 
 // Element of a head at position i of the tiles' rows: int4 codes leave a word
@@ -102,7 +98,7 @@ struct Walk {
       s = seq_of(k, ++b);
     }
     if (s.units == 0) return false;  // (lengths that changed under the call)
-    const int seg = (int)((u - begin) / s.units);
+    const int seg = (int)quot(u - begin, s.units);
     const long long seg0 = begin + (long long)seg * s.units;
     rt = seg % s.tiles;
     h = seg / s.tiles;
@@ -162,14 +158,12 @@ __global__ void __launch_bounds__(512, 1) k13_tree_wide_kernel(const __grid_cons
   if (blockIdx.x == 0)
     for (int i = tid; i < a.c.batch; i += 512)
       if (a.c.status && seq_outside(k, i)) atomicCAS(a.c.status, 0, FS_ERR_CACHE);
-  const Line line = line_of(k, [&](long long total, int, long long x, long long y) {
-    if (total == 0) return false;
-    const Share share(k, total);
+  const Line line = line_of(k, [&](const Share &share, int, long long x, long long y) {
     const long long at = share.begin(blockIdx.x);
     return (int)blockIdx.x < share.blocks && at >= x && at < y;
   });
   if (line.total == 0) return;
-  const Share share(k, line.total);
+  const Share &share = line.share;
   if ((int)blockIdx.x >= share.blocks) return;
 
   if (tid == 0) {

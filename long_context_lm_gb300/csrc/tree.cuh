@@ -18,6 +18,11 @@ constexpr float kLog2e = 1.4426950408889634f;
 // heads over 16384 int8 keys.
 constexpr float kRaise = 8.f;
 
+// The least power of two that the value scales are relative to.  Probabilities
+// are made 1 / vref times as large (the products with the scales then need no
+// second factor), and stay within fp32 with their sum.
+constexpr float kLeast = 0x1p-90f;
+
 // ---------------------------------------------------------------------------
 // the line of units
 // ---------------------------------------------------------------------------
@@ -62,11 +67,36 @@ __device__ __forceinline__ bool seq_outside(const TreeK &k, int b) {
   return n > 0 && (past < 0 || (long long)past + n > (long long)k.a.c.max_pages * k.a.c.page);
 }
 
-// Length of the line, and of the one sequence that `pick(total, b, begin, end)`
-// chooses (the units [begin, end) are its own) the number, beginning and sizes.
-// Called by all threads of a block.
+// a / b; nearly always both fit 32 bits, whose division is several times faster.
+__device__ __forceinline__ long long quot(long long a, int b) {
+  return a >> 32 ? a / b : (long long)((uint32_t)a / (uint32_t)b);
+}
+// How the line is shared: at most one block for every `least` units; the first `more` blocks have a unit more than the others.
+struct Share {
+  int blocks = 1, more = 0;
+  long long each = 0;
+  Share() = default;
+  __device__ __forceinline__ Share(const TreeK &k, long long total) {
+    const long long n = quot(total + k.least - 1, k.least);
+    blocks = (int)(n < k.blocks ? (n < 1 ? 1 : n) : k.blocks);
+    each = quot(total, blocks);
+    more = (int)(total - each * blocks);
+  }
+  __device__ __forceinline__ long long begin(int c) const { return c * each + min(c, more); }
+  // the block that holds unit u
+  __device__ __forceinline__ int of(long long u) const {
+    const long long first = more * (each + 1);
+    if (each >> 31) return (int)(u < first ? u / (each + 1) : more + (u - first) / each);
+    return (int)(u < first ? quot(u, (int)each + 1) : more + quot(u - first, (int)each));
+  }
+};
+
+// Length of the line, how it is shared, and of the one sequence that
+// `pick(share, b, begin, end)` chooses (the units [begin, end) are its own) the
+// number, beginning and sizes.  Called by all threads of a block.
 struct Line {
   long long total, begin;
+  Share share;
   int b;
   Seq s;
 };
@@ -88,8 +118,9 @@ __device__ __forceinline__ Line line_of(const TreeK &k, const Pick &pick) {
     }
     Line out;
     out.total = __shfl_sync(~0u, x, k.a.c.batch - 1);
+    out.share = Share(k, out.total);
     const uint32_t mine =
-        __ballot_sync(~0u, lane < k.a.c.batch && pick(out.total, lane, x - u, x));
+        __ballot_sync(~0u, lane < k.a.c.batch && pick(out.share, lane, x - u, x));
     out.b = mine ? __ffs(mine) - 1 : 0;
     out.begin = __shfl_sync(~0u, x - u, out.b);
     out.s.past = __shfl_sync(~0u, s.past, out.b);
@@ -104,6 +135,7 @@ __device__ __forceinline__ Line line_of(const TreeK &k, const Pick &pick) {
   __shared__ Line found;
   const bool once = k.a.c.batch <= (int)blockDim.x;
   long long total = 0;
+  Share share;
 #pragma unroll 1
   for (int round = once ? 1 : 0; round < 2; ++round) {  // a long batch goes through twice
     long long before_all = 0;
@@ -132,42 +164,21 @@ __device__ __forceinline__ Line line_of(const TreeK &k, const Pick &pick) {
       }
       x += before_all;
       before_all += all;
-      if (once) total = all;
-      if (round == 1 && b < k.a.c.batch && pick(total, b, x - u, x)) {
+      if (once) share = Share(k, total = all);
+      if (round == 1 && b < k.a.c.batch && pick(share, b, x - u, x)) {
         found.b = b;
         found.begin = x - u;
         found.s = s;
       }
     }
-    total = before_all;
+    if (!once) share = Share(k, total = before_all);
     __syncthreads();
   }
   Line out = found;
   out.total = total;
+  out.share = share;
   return out;
 }
-
-// a / b; nearly always both fit 32 bits, whose division is several times faster.
-__device__ __forceinline__ long long quot(long long a, int b) {
-  return a >> 32 ? a / b : (long long)((uint32_t)a / (uint32_t)b);
-}
-// How the line is shared: at most one block for every `least` units; the first `more` blocks have a unit more than the others.
-struct Share {
-  int blocks, more;
-  long long each;
-  __device__ __forceinline__ Share(const TreeK &k, long long total) {
-    const long long n = quot(total + k.least - 1, k.least);
-    blocks = (int)(n < k.blocks ? (n < 1 ? 1 : n) : k.blocks);
-    each = quot(total, blocks);
-    more = (int)(total - each * blocks);
-  }
-  __device__ __forceinline__ long long begin(int c) const { return c * each + min(c, more); }
-  // the block that holds unit u
-  __device__ __forceinline__ int of(long long u) const {
-    const long long first = more * (each + 1);
-    return (int)(u < first ? u / (each + 1) : more + (u - first) / each);
-  }
-};
 
 __device__ __forceinline__ uint32_t h2add(uint32_t a, uint32_t b) {
   __half2 r = __hadd2(*reinterpret_cast<__half2 *>(&a), *reinterpret_cast<__half2 *>(&b));
