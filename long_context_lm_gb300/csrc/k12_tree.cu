@@ -67,17 +67,19 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
           "f"(z3));
 }
 
+// MT sixteens of rows a tile; MT = 0: eight rows.
 template <int F, int D, int MT>
 struct Cfg {
   static constexpr int kBits = Fmt<F>::kBits;
   static constexpr int kRow = D * kBits / 8;  // bytes of a row
   static constexpr int P = kRow / 16;         // 16-byte pieces of a row
-  static constexpr int kM = 16 * MT;
+  static constexpr int kM = MT ? 16 * MT : 8;
   static constexpr int kWarps = kRow >= 256 ? 4 : 8;
   static constexpr int kCodes = kUnit * kRow;  // bytes of a unit's keys
   // keys, values, 32 + 32 scales, which keys can be read
   static constexpr int kStage = 2 * kCodes + 8 * kUnit + 16;
-  static constexpr int kCtas = MT == 1 && D == 64 && kStage * kWarps * 3 <= 112 * 1024 ? 2 : 1;
+  static constexpr int kCtas =
+      (MT == 0 || (MT == 1 && D == 64)) && kStage * kWarps * 3 <= 112 * 1024 ? 2 : 1;
   static constexpr int kRoom = (kCtas == 2 ? 110 : 220) * 1024;
   static constexpr int kFit = kRoom / (kStage * kWarps);
   static constexpr int kStages = kFit > 6 ? 6 : kFit;
@@ -88,15 +90,14 @@ struct Cfg {
   static_assert(kStages >= 2 && kSmem <= kRoom, "ring");
 };
 
-// The lane's registers of one row of q, two for every k step.  Lane column c
+// The lane's registers of one row of q (null: zeros), two for every k step.  Lane column c
 // (lane % 4) holds the elements that its key words hold:
 //   bf16          8-element pieces c, c + 4, ...
 //   8 bits        16-element pieces c, c + 4
 //   4 bits        elements D / 4 c ..., in every eight the pairs (0, 4), (1, 5),
 //                 (2, 6), (3, 7)
 template <int F, int D>
-__device__ __forceinline__ void q_words(const uint16_t *row, int c, bool live,
-                                        uint32_t (&raw)[D / 16][2]) {
+__device__ __forceinline__ void q_words(const uint16_t *row, int c, uint32_t (&raw)[D / 16][2]) {
   constexpr int N = D / 8;  // words of a lane: a quarter of the row
   uint32_t w[N];
 #pragma unroll
@@ -105,7 +106,7 @@ __device__ __forceinline__ void q_words(const uint16_t *row, int c, bool live,
                       : F == FS_CACHE_INT4 ? N / 4 * c + i
                                            : 2 * (c + 4 * (i / 2)) + i % 2;
     uint4 u = make_uint4(0, 0, 0, 0);
-    if (live) u = *reinterpret_cast<const uint4 *>(row + piece * 8);
+    if (row) u = *reinterpret_cast<const uint4 *>(row + piece * 8);
     w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
   }
 #pragma unroll
@@ -200,6 +201,598 @@ __device__ __forceinline__ void lds_words(const char *p, uint32_t *w) {
   }
 }
 
+// An 8 x 8 matrix of 16-bit elements, two of row g in lane (g, c), transposed.
+__device__ __forceinline__ uint32_t turned(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(x));
+  return y;
+}
+// Element el of value r of a unit (bf16).
+template <int F, int D>
+__device__ __forceinline__ float value_at(const char *vs, int r, int el) {
+  constexpr int P = D * Fmt<F>::kBits / 128;
+  const uint16_t bits =
+      *reinterpret_cast<const uint16_t *>(vs + v_place<P>(r, el / 8) * 16 + (el % 8) * 2);
+  return __uint_as_float((uint32_t)bits << 16);
+}
+
+// Where a lane's words of a unit lie, and the loads of them.
+template <int F, int D>
+struct Words {
+  static constexpr int kBits = Fmt<F>::kBits, kRow = D * kBits / 8, P = kRow / 16;
+  static constexpr bool kBF = F == FS_CACHE_BF16;
+  static constexpr int KW = D * kBits / 128;  // of a key: a quarter of the row
+  static constexpr int VW = D == 64 ? kBits / 4 : (kBF ? 4 : kBits / 2);  // of a value, at a time
+  static constexpr int SETS = kBF ? D / 64 : 1;
+  int g, c;
+  int k_at, k_half, v_at[2];
+  __device__ __forceinline__ Words(int lane) : g(lane >> 2), c(lane & 3) {
+    const int v_byte = g * VW * 4;  // inside the row (its first set)
+    k_at = KW == 2 ? g * kRow + c * 8 : k_place<P>(g, c) * 16;
+    k_half = (k_at & 64) ? -64 : 64;
+    v_at[0] = v_place<P>(2 * c, v_byte / 16) * 16 + v_byte % 16;
+    v_at[1] = v_place<P>(2 * c + 1, v_byte / 16) * 16 + v_byte % 16;
+  }
+  // of key 8 nt + g
+  __device__ __forceinline__ void key(const char *st, int nt, uint32_t (&w)[KW]) const {
+    const char *row = st + k_at + nt * 8 * kRow;
+    if constexpr (KW <= 4) {
+      lds_words<KW>(row, w);
+    } else {
+      // (four pieces on: within a row of eight the place's other half)
+#pragma unroll
+      for (int j = 0; j < KW / 4; ++j)
+        lds_words<4>(P == 8 ? st + (k_at ^ (64 * j)) + nt * 8 * kRow
+                            : row + (j & 1 ? k_half : 0) + j / 2 * 128,
+                     w + 4 * j);
+    }
+  }
+  // of values 16 kk + 2 c + (i & 1) + 8 (i / 2): eight rows on, the places repeat
+  __device__ __forceinline__ void values(const char *vs, int kk, int set,
+                                         uint32_t (&w)[4][VW]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      lds_words<VW>(vs + v_at[i & 1] + (16 * kk + 8 * (i >> 1)) * kRow + 128 * set, w[i]);
+  }
+};
+
+// What the rows of a tile see of a unit that not all of them see whole.
+struct Sight {
+  const uint64_t *bits;  // of the tile's rows: drafted tokens,
+  const int *first;      // first key of the prefix
+  int past, key0;
+  uint32_t valid;  // keys that can be read
+  __device__ __forceinline__ bool sees(uint64_t b, int f, int at) const {
+    const int key = key0 + at;
+    return (valid >> at & 1) && (key < past ? key >= f : (bool)(b >> (key - past) & 1));
+  }
+};
+
+// Probabilities are at most 2^15 (fp16) or 1 (bf16).
+template <int F>
+constexpr float kLift = F == FS_CACHE_BF16 ? -kRaise : 15.f - kRaise;
+template <int F>
+__device__ __forceinline__ float lift_of(float vref) {
+  return F == FS_CACHE_BF16 ? kLift<F>
+                            : kLift<F> - (float)((int)(__float_as_uint(vref) >> 23) - 127);
+}
+
+// One row of q as the lane holds it (q_words): to fp16 by a power of two.  f: the
+// row's factor; sum: of its fp16 elements, over the row's four lanes, where the
+// key codes have a bias.
+template <int F, int D>
+__device__ __forceinline__ void q_to_f16(const Magic &magic, uint32_t (&raw)[D / 16][2], float &f,
+                                         float &sum) {
+  f = 1.f;
+  sum = 0.f;
+  if constexpr (F != FS_CACHE_BF16) {
+    uint32_t most = 0;
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) most = __vmaxu2(most, raw[ks][e] & 0x7fff7fffu);
+    most = max(most & 0xffffu, most >> 16);
+    most = max(most, __shfl_xor_sync(~0u, most, 1));
+    most = max(most, __shfl_xor_sync(~0u, most, 2));
+    // the largest magnitude goes to [2^14, 2^15)
+    f = __uint_as_float((uint32_t)min(254, 268 - (int)(most >> 7)) << 23);
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        uint32_t x = pack_f16(bf16_lo(raw[ks][e]) * f, bf16_hi(raw[ks][e]) * f);
+        if constexpr (kBias<F> != 0.f) {
+          const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&x));
+          sum += y.x + y.y;
+        }
+        if constexpr (F == FS_CACHE_INT4)
+          if (e) x = h2fma(x, magic.sixteenth, 0u);
+        raw[ks][e] = x;
+      }
+    if constexpr (kBias<F> != 0.f) {
+      sum += __shfl_xor_sync(~0u, sum, 1);
+      sum += __shfl_xor_sync(~0u, sum, 2);
+    }
+  }
+}
+// Product of the fragments -> log2 units, and what the bias adds to a product.
+template <int F>
+__device__ __forceinline__ float score_factor(float scale, float f) {
+  const float rf = fmaxf(scale * kLog2e * (1.f / f), FLT_MIN);
+  return kBias<F> != 0.f ? rf * 0x1p24f : rf;
+}
+template <int F>
+__device__ __forceinline__ float bias_of(float sum) {
+  return -0x1p-24f * kBias<F> * sum;
+}
+
+// Up to 16 MT rows: S = Q K^T, O = P V, rows g and g + 8 of every sixteen in the
+// lane.
+template <int F, int D, int MT>
+struct RowForm {
+  static constexpr bool kBF = F == FS_CACHE_BF16;
+  static constexpr int KS = D / 16, NT = D / 8;  // k steps, value tiles
+  using W = Words<F, D>;
+  const W &at;
+  uint32_t raw[MT][2][KS][2];
+  uint32_t q[MT][KS][4];
+  float rf[MT][2], bias[MT][2];
+  // reference, the product that passes it too far, sum (of even and odd keys)
+  float m[MT][2], thr[MT][2], l[MT][2][2], o[MT][NT][4], sc[MT][4][4];
+
+  __device__ __forceinline__ RowForm(const W &w) : at(w) {}
+  // src(row): the row's elements, null past the last
+  template <class Src>
+  __device__ __forceinline__ void load(const Src &src) {
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) q_words<F, D>(src(mt * 16 + hf * 8 + at.g), at.c, raw[mt][hf]);
+  }
+  __device__ __forceinline__ void begin(const Magic &magic, float scale) {
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        float f, sum;
+        q_to_f16<F, D>(magic, raw[mt][hf], f, sum);
+        rf[mt][hf] = score_factor<F>(scale, f);
+        bias[mt][hf] = bias_of<F>(sum);
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          q[mt][ks][hf] = raw[mt][hf][ks][0];
+          q[mt][ks][2 + hf] = raw[mt][hf][ks][1];
+        }
+        m[mt][hf] = -FLT_MAX;
+        thr[mt][hf] = -INFINITY;
+        l[mt][hf][0] = l[mt][hf][1] = 0.f;
+#pragma unroll
+        for (int i = 0; i < NT; ++i) o[mt][i][2 * hf] = o[mt][i][2 * hf + 1] = 0.f;
+      }
+  }
+  __device__ __forceinline__ void rescale(float back) {
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) l[mt][e / 2][e % 2] *= back;
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[mt][i][e] *= back;
+    }
+  }
+  __device__ __forceinline__ void scores(const Magic &magic, const char *st) {
+#pragma unroll
+    for (int nt = 0; nt < 4; ++nt) {
+      uint32_t w[W::KW];
+      at.key(st, nt, w);
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        uint32_t b0, b1;
+        k_regs<F>(magic, w, ks, b0, b1);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) mma16816<kBF>(sc[mt][nt], q[mt][ks], b0, b1, ks > 0);
+      }
+    }
+  }
+  __device__ __forceinline__ void scale_keys(const float *kscale) {
+    if constexpr (!kBF) {
+#pragma unroll
+      for (int nt = 0; nt < 4; ++nt) {
+        const float2 ks = *reinterpret_cast<const float2 *>(kscale + nt * 8 + 2 * at.c);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            float &x = sc[mt][nt][2 * hf], &y = sc[mt][nt][2 * hf + 1];
+            if constexpr (kBias<F> != 0.f) add2(x, y, bias[mt][hf], bias[mt][hf]);
+            mul2(x, y, ks.x, ks.y);
+          }
+      }
+    }
+  }
+  __device__ __forceinline__ void mask(const Sight &si) {
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        const uint64_t bits = si.bits[mt * 16 + hf * 8 + at.g];
+        const int first = si.first[mt * 16 + hf * 8 + at.g];
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            if (!si.sees(bits, first, nt * 8 + 2 * at.c + e)) sc[mt][nt][2 * hf + e] = -INFINITY;
+      }
+  }
+  __device__ __forceinline__ float top_of(int mt, int hf) const {
+    float top = fmaxf(sc[mt][0][2 * hf], sc[mt][0][2 * hf + 1]);
+#pragma unroll
+    for (int nt = 1; nt < 4; ++nt) top = max3f(top, sc[mt][nt][2 * hf], sc[mt][nt][2 * hf + 1]);
+    return top;
+  }
+  __device__ __forceinline__ void follow() {  // the rows' references
+    bool raise = false;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) raise = raise || top_of(mt, hf) > thr[mt][hf];
+    if (!__any_sync(~0u, raise)) return;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        float top = top_of(mt, hf);
+        top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+        top = fmaxf(m[mt][hf], top * rf[mt][hf]);
+        const float back = exp2f(m[mt][hf] - top);
+        m[mt][hf] = top;
+        if (top > -FLT_MAX) thr[mt][hf] = (top + kRaise) / rf[mt][hf];
+        l[mt][hf][0] *= back;
+        l[mt][hf][1] *= back;
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+          o[mt][i][2 * hf] *= back;
+          o[mt][i][2 * hf + 1] *= back;
+        }
+      }
+  }
+  template <bool MASKED>
+  __device__ __forceinline__ void weigh(const float *kscale, float lift) {
+    [[maybe_unused]] float2 vs[4];
+    if constexpr (!kBF) {
+#pragma unroll
+      for (int nt = 0; nt < 4; ++nt)
+        vs[nt] = *reinterpret_cast<const float2 *>(kscale + kUnit + nt * 8 + 2 * at.c);
+    }
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        const float ref = lift - m[mt][hf];
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt) {
+          float &x = sc[mt][nt][2 * hf], &y = sc[mt][nt][2 * hf + 1];
+          [[maybe_unused]] const bool sx = x != -INFINITY, sy = y != -INFINITY;
+          fma2(x, y, x, y, rf[mt][hf], ref);
+          x = tc::ex2(x);
+          y = tc::ex2(y);
+          add2(l[mt][hf][0], l[mt][hf][1], x, y);
+          if constexpr (!kBF) {
+            mul2(x, y, vs[nt].x, vs[nt].y);
+            if constexpr (MASKED) {  // (a masked key's scale may be NaN)
+              x = sx ? x : 0.f;
+              y = sy ? y : 0.f;
+            }
+          }
+        }
+      }
+  }
+  // One value at a time, for values that are not finite; pt: room for [key][row].
+  __device__ __forceinline__ void add_values_singly(const char *vs, float *pt) {
+    constexpr int M = 16 * MT;
+    __syncwarp();
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          pt[(nt * 8 + 2 * at.c + (e & 1)) * M + mt * 16 + (e >> 1) * 8 + at.g] = sc[mt][nt][e];
+    __syncwarp();
+#pragma unroll 1
+    for (int r = 0; r < kUnit; ++r) {
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float v = value_at<F, D>(vs, r, v_element<F, D>(2 * at.c + e, i));
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+              const float p = pt[r * M + mt * 16 + hf * 8 + at.g];
+              if (p != 0.f) o[mt][i][2 * hf + e] += p * v;
+            }
+        }
+    }
+  }
+  __device__ __forceinline__ void add_values(const Magic &magic, const char *vs) {
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+      uint32_t p[MT][4], lo[MT][4];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float x0 = sc[mt][2 * kk + j / 2][2 * (j % 2)];
+          const float x1 = sc[mt][2 * kk + j / 2][2 * (j % 2) + 1];
+          if constexpr (kBF) {
+            p[mt][j] = pack_bf16(x0, x1);
+            lo[mt][j] = pack_bf16(x0 - bf16_lo(p[mt][j]), x1 - bf16_hi(p[mt][j]));
+          } else {
+            p[mt][j] = pack_f16(x0, x1);
+          }
+        }
+#pragma unroll
+      for (int set = 0; set < W::SETS; ++set) {
+        uint32_t w[4][W::VW];
+        at.values(vs, kk, set, w);
+#pragma unroll
+        for (int j = 0; j < NT / W::SETS / 2; ++j) {
+          uint32_t b00, b01, b10, b11;
+          v_regs<F>(magic, w[0], w[1], j, b00, b10);
+          v_regs<F>(magic, w[2], w[3], j, b01, b11);
+          const int i = set * (NT / W::SETS) + 2 * j;
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            mma16816<kBF>(o[mt][i], p[mt], b00, b01);
+            mma16816<kBF>(o[mt][i + 1], p[mt], b10, b11);
+            if constexpr (kBF) {
+              mma16816<true>(o[mt][i], lo[mt], b00, b01);
+              mma16816<true>(o[mt][i + 1], lo[mt], b10, b11);
+            }
+          }
+        }
+      }
+    }
+  }
+  // The warp's results: rows of SD floats, references, sums.
+  template <int SD>
+  __device__ __forceinline__ void leave(float *jo, float *jm, float *jl, int live, float vref) {
+    const float unit = kBF ? 1.f : vref;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        float sum = l[mt][hf][0] + l[mt][hf][1];
+        sum += __shfl_xor_sync(~0u, sum, 1);
+        sum += __shfl_xor_sync(~0u, sum, 2);
+        const int row = mt * 16 + hf * 8 + at.g;
+        if (row >= live) continue;
+        if (at.c == 0) {
+          jm[row] = m[mt][hf];
+          jl[row] = sum * unit;
+        }
+#pragma unroll
+        for (int i = 0; i < NT; i += 4)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            *reinterpret_cast<float4 *>(jo + row * SD + v_element<F, D>(2 * at.c + e, i)) =
+                make_float4(o[mt][i][2 * hf + e] * unit, o[mt][i + 1][2 * hf + e] * unit,
+                            o[mt][i + 2][2 * hf + e] * unit, o[mt][i + 3][2 * hf + e] * unit);
+      }
+  }
+};
+
+// Up to eight rows: S^T = K Q^T and O^T = V^T P^T, so that the keys and the
+// elements of a head fill the products' sixteens and the rows their eight columns:
+// half the products and weights of RowForm, from the same registers.  Rows 2 c and
+// 2 c + 1 in the lane.
+template <int F, int D>
+struct ColForm {
+  static constexpr bool kBF = F == FS_CACHE_BF16;
+  static constexpr int KS = D / 16, NT = D / 8;
+  using W = Words<F, D>;
+  const W &at;
+  uint32_t q[KS][2];  // of row g
+  float rf[2], bias[2];
+  float m[2], thr[2], l[2];
+  float o[NT / 2][4];  // element v_element(g, 2 j + i / 2), row 2 c + i % 2
+  float sc[2][4];      // key 16 mt + 8 (i / 2) + g, row 2 c + i % 2
+
+  __device__ __forceinline__ ColForm(const W &w) : at(w) {}
+  template <class Src>
+  __device__ __forceinline__ void load(const Src &src) {
+    q_words<F, D>(src(at.g), at.c, q);
+  }
+  __device__ __forceinline__ void begin(const Magic &magic, float scale) {
+    float f, sum;
+    q_to_f16<F, D>(magic, q, f, sum);
+    const float r = score_factor<F>(scale, f), b = bias_of<F>(sum);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      rf[e] = __shfl_sync(~0u, r, 4 * (2 * at.c + e));
+      bias[e] = __shfl_sync(~0u, b, 4 * (2 * at.c + e));
+      m[e] = -FLT_MAX;
+      thr[e] = -INFINITY;
+      l[e] = 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < NT / 2; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[j][i] = 0.f;
+  }
+  __device__ __forceinline__ void rescale(float back) {
+    l[0] *= back;
+    l[1] *= back;
+#pragma unroll
+    for (int j = 0; j < NT / 2; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[j][i] *= back;
+  }
+  __device__ __forceinline__ void scores(const Magic &magic, const char *st) {
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt) {
+      uint32_t w[2][W::KW];
+      at.key(st, 2 * mt, w[0]);
+      at.key(st, 2 * mt + 1, w[1]);
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        uint32_t a[4];
+        k_regs<F>(magic, w[0], ks, a[0], a[2]);
+        k_regs<F>(magic, w[1], ks, a[1], a[3]);
+        mma16816<kBF>(sc[mt], a, q[ks][0], q[ks][1], ks > 0);
+      }
+    }
+  }
+  __device__ __forceinline__ void scale_keys(const float *kscale) {
+    if constexpr (!kBF) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float ks = kscale[8 * i + at.g];
+        float &x = sc[i / 2][2 * (i % 2)], &y = sc[i / 2][2 * (i % 2) + 1];
+        if constexpr (kBias<F> != 0.f) add2(x, y, bias[0], bias[1]);
+        mul2(x, y, ks, ks);
+      }
+    }
+  }
+  __device__ __forceinline__ void mask(const Sight &si) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const uint64_t bits = si.bits[2 * at.c + e];
+      const int first = si.first[2 * at.c + e];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (!si.sees(bits, first, 8 * i + at.g)) sc[i / 2][2 * (i % 2) + e] = -INFINITY;
+    }
+  }
+  __device__ __forceinline__ float top_of(int e) const {
+    return fmaxf(max3f(sc[0][e], sc[0][2 + e], sc[1][e]), sc[1][2 + e]);
+  }
+  __device__ __forceinline__ void follow() {
+    if (!__any_sync(~0u, top_of(0) > thr[0] || top_of(1) > thr[1])) return;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float top = top_of(e);
+#pragma unroll
+      for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, x));
+      top = fmaxf(m[e], top * rf[e]);
+      const float back = exp2f(m[e] - top);
+      m[e] = top;
+      if (top > -FLT_MAX) thr[e] = (top + kRaise) / rf[e];
+      l[e] *= back;
+#pragma unroll
+      for (int j = 0; j < NT / 2; ++j) {
+        o[j][e] *= back;
+        o[j][2 + e] *= back;
+      }
+    }
+  }
+  template <bool MASKED>
+  __device__ __forceinline__ void weigh(const float *kscale, float lift) {
+    const float ref0 = lift - m[0], ref1 = lift - m[1];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float &x = sc[i / 2][2 * (i % 2)], &y = sc[i / 2][2 * (i % 2) + 1];
+      [[maybe_unused]] const bool sx = x != -INFINITY, sy = y != -INFINITY;
+      x = tc::ex2(fmaf(x, rf[0], ref0));
+      y = tc::ex2(fmaf(y, rf[1], ref1));
+      add2(l[0], l[1], x, y);
+      if constexpr (!kBF) {
+        const float vs = kscale[kUnit + 8 * i + at.g];
+        mul2(x, y, vs, vs);
+        if constexpr (MASKED) {  // (a masked key's scale may be NaN)
+          x = sx ? x : 0.f;
+          y = sy ? y : 0.f;
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void add_values_singly(const char *vs, float *pt) {
+    constexpr int M = 8;
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        pt[(8 * i + at.g) * M + 2 * at.c + e] = sc[i / 2][2 * (i % 2) + e];
+    __syncwarp();
+#pragma unroll 1
+    for (int r = 0; r < kUnit; ++r) {
+      const float p0 = pt[r * M + 2 * at.c], p1 = pt[r * M + 2 * at.c + 1];
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        const float v = value_at<F, D>(vs, r, v_element<F, D>(at.g, i));
+        if (p0 != 0.f) o[i / 2][2 * (i % 2)] += p0 * v;
+        if (p1 != 0.f) o[i / 2][2 * (i % 2) + 1] += p1 * v;
+      }
+    }
+  }
+  __device__ __forceinline__ void add_values(const Magic &magic, const char *vs) {
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+      // a transposed 8 x 8: the lane's two rows of key g -> two keys of row g
+      uint32_t p[2], lo[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float x = sc[kk][2 * i], y = sc[kk][2 * i + 1];
+        if constexpr (kBF) {
+          const uint32_t hi = pack_bf16(x, y);
+          p[i] = turned(hi);
+          lo[i] = turned(pack_bf16(x - bf16_lo(hi), y - bf16_hi(hi)));
+        } else {
+          p[i] = turned(pack_f16(x, y));
+        }
+      }
+#pragma unroll
+      for (int set = 0; set < W::SETS; ++set) {
+        uint32_t w[4][W::VW];
+        at.values(vs, kk, set, w);
+#pragma unroll
+        for (int j = 0; j < NT / W::SETS / 2; ++j) {
+          uint32_t a[4];
+          v_regs<F>(magic, w[0], w[1], j, a[0], a[1]);
+          v_regs<F>(magic, w[2], w[3], j, a[2], a[3]);
+          const int i = set * (NT / W::SETS / 2) + j;
+          mma16816<kBF>(o[i], a, p[0], p[1]);
+          if constexpr (kBF) mma16816<true>(o[i], a, lo[0], lo[1]);
+        }
+      }
+    }
+  }
+  template <int SD>
+  __device__ __forceinline__ void leave(float *jo, float *jm, float *jl, int live, float vref) {
+    const float unit = kBF ? 1.f : vref;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float sum = l[e];
+#pragma unroll
+      for (int x = 4; x < 32; x <<= 1) sum += __shfl_xor_sync(~0u, sum, x);
+      const int row = 2 * at.c + e;
+      if (row >= live) continue;
+      if (at.g == 0) {
+        jm[row] = m[e];
+        jl[row] = sum * unit;
+      }
+#pragma unroll
+      for (int j = 0; j < NT / 2; j += 2)
+        *reinterpret_cast<float4 *>(jo + row * SD + v_element<F, D>(at.g, 2 * j)) =
+            make_float4(o[j][e] * unit, o[j][2 + e] * unit, o[j + 1][e] * unit,
+                        o[j + 1][2 + e] * unit);
+    }
+  }
+};
+template <int F, int D, int MT>
+struct FormOf {
+  using type = RowForm<F, D, MT>;
+};
+template <int F, int D>
+struct FormOf<F, D, 0> {
+  using type = ColForm<F, D>;
+};
+
 // ---------------------------------------------------------------------------
 // the kernel
 // ---------------------------------------------------------------------------
@@ -208,12 +801,11 @@ __global__ void __launch_bounds__(Cfg<F, D, MT>::kWarps * 32, Cfg<F, D, MT>::kCt
 k12_tree_kernel(const __grid_constant__ TreeK k) {
   using C = Cfg<F, D, MT>;
   constexpr int P = C::P, W = C::kWarps, M = C::kM, NS = C::kStages;
-  constexpr int KS = D / 16, NT = D / 8;  // k steps of a score, value tiles
   extern __shared__ __align__(128) char smem[];
   __shared__ uint64_t row_bits[M];
   __shared__ int row_first[M];
   const TreeArgs &a = k.a;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int shift = 31 - __clz(a.c.page);
   asm volatile("griddepcontrol.launch_dependents;");
 
@@ -239,13 +831,8 @@ k12_tree_kernel(const __grid_constant__ TreeK k) {
   const int v_off = a.c.Hkv * a.c.page;  // rows from a key to its value
 
   uint32_t whole_units = 0;  // stages whose 32 keys can all be read
-  // where the lane's words of keys g and values 2 c, 2 c + 1 lie in a stage
-  constexpr int VW = D == 64 ? C::kBits / 4 : (C::kBF ? 4 : C::kBits / 2);  // words at a time
-  const int v_byte = g * VW * 4;  // inside the row (its first set)
-  const int k_at = D * C::kBits / 128 == 2 ? g * C::kRow + c * 8 : k_place<P>(g, c) * 16;
-  [[maybe_unused]] const int k_half = (k_at & 64) ? -64 : 64;
-  const int v_at[2] = {v_place<P>(2 * c, v_byte / 16) * 16 + v_byte % 16,
-                       v_place<P>(2 * c + 1, v_byte / 16) * 16 + v_byte % 16};
+  const Words<F, D> words(lane);
+  typename FormOf<F, D, MT>::type form(words);
 
   long long u = u0;
   while (u < u1) {
@@ -262,17 +849,12 @@ k12_tree_kernel(const __grid_constant__ TreeK k) {
 
     __syncthreads();  // the ring held the last segment's results
     // q first: loads behind the units' copies would wait for them
-    uint32_t raw[MT][2][KS][2];
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        const int r = rt * M + mt * 16 + hf * 8 + g;
-        const bool live = r < rows;
-        const int t = live ? r / k.G : 0, head = h * k.G + (live ? r % k.G : 0);
-        q_words<F, D>(static_cast<const uint16_t *>(a.q) + (((size_t)b * a.H + head) * a.T + t) * D,
-                      c, live, raw[mt][hf]);
-      }
+    form.load([&](int r) -> const uint16_t * {
+      const int row = rt * M + r;
+      if (row >= rows) return nullptr;
+      const int t = row / k.G, head = h * k.G + row - t * k.G;
+      return static_cast<const uint16_t *>(a.q) + (((size_t)b * a.H + head) * a.T + t) * D;
+    });
     // Where sixteen of the warp's units lie, two halves of sixteen rows to a unit:
     // lane 2 i + j holds half j of unit x + W i, as its place among all groups of
     // sixteen rows (kNone: nothing to read).  The table is read sixteen units
@@ -374,63 +956,11 @@ k12_tree_kernel(const __grid_constant__ TreeK k) {
     }
     __syncthreads();
 
-    // q: fragments of the lane's rows
-    uint32_t q[MT][KS][4];
-    float rf[MT][2];  // score of the fragments' product -> log2 units
-    [[maybe_unused]] float bias[MT][2];
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        uint32_t most = 0;
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) most = __vmaxu2(most, raw[mt][hf][ks][e] & 0x7fff7fffu);
-        most = max(most & 0xffffu, most >> 16);
-        float f = 1.f;
-        if constexpr (!C::kBF) {
-          most = max(most, __shfl_xor_sync(~0u, most, 1));
-          most = max(most, __shfl_xor_sync(~0u, most, 2));
-          // the largest magnitude goes to [2^14, 2^15)
-          f = __uint_as_float((uint32_t)min(254, 268 - (int)(most >> 7)) << 23);
-        }
-        rf[mt][hf] = fmaxf(a.scale * kLog2e * (1.f / f), FLT_MIN);
-        float sum = 0.f;
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            uint32_t x = raw[mt][hf][ks][e];
-            if constexpr (!C::kBF) {
-              x = pack_f16(bf16_lo(x) * f, bf16_hi(x) * f);
-              if constexpr (kBias<F> != 0.f) {
-                const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&x));
-                sum += y.x + y.y;
-              }
-              if constexpr (F == FS_CACHE_INT4)
-                if (e) x = h2fma(x, magic.sixteenth, 0u);
-            }
-            q[mt][ks][2 * e + hf] = x;
-          }
-        if constexpr (kBias<F> != 0.f) {
-          sum += __shfl_xor_sync(~0u, sum, 1);
-          sum += __shfl_xor_sync(~0u, sum, 2);
-          bias[mt][hf] = -0x1p-24f * kBias<F> * sum;
-          rf[mt][hf] *= 0x1p24f;
-        }
-      }
+    form.begin(magic, a.scale);
     int lead = 0;  // no row's prefix begins later
     if (a.window)
       for (int r = 0; r < M; ++r) lead = max(lead, row_first[r] == INT_MAX ? 0 : row_first[r]);
 
-    // reference, the product that passes it too far, sum (of even and odd keys)
-    float o[MT][NT][4] = {}, m[MT][2], thr[MT][2], l[MT][2][2] = {};
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      m[mt][0] = m[mt][1] = -FLT_MAX;
-      thr[mt][0] = thr[mt][1] = -INFINITY;
-    }
     float vref = kLeast;
 
     int stage = 0;
@@ -446,162 +976,27 @@ k12_tree_kernel(const __grid_constant__ TreeK k) {
           const uint32_t top =
               __reduce_max_sync(~0u, mine <= FLT_MAX ? __float_as_uint(fmaxf(mine, 0.f)) : 0u);
           const float up = __uint_as_float((top + 0x7fffffu) & 0x7f800000u);
-          const float back = vref / up;
+          form.rescale(vref / up);
           vref = up;
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) l[mt][e / 2][e % 2] *= back;
-#pragma unroll
-            for (int i = 0; i < NT; ++i)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) o[mt][i][e] *= back;
-          }
         }
       }
       const int key0 = s.first + x * kUnit;
       const bool whole = (whole_units >> stage & 1) && key0 + kUnit <= s.past && key0 >= lead;
 
-      float sc[MT][4][4];
-#pragma unroll
-      for (int nt = 0; nt < 4; ++nt) {
-        constexpr int KW = D * C::kBits / 128;  // words of a lane: a quarter of the row
-        uint32_t w[KW];
-        const char *row = st + k_at + nt * 8 * C::kRow;
-        if constexpr (KW <= 4) {
-          lds_words<KW>(row, w);
-        } else {
-          // (four pieces on: within a row of eight the place's other half)
-#pragma unroll
-          for (int j = 0; j < KW / 4; ++j)
-            lds_words<4>(P == 8 ? st + (k_at ^ (64 * j)) + nt * 8 * C::kRow
-                                : row + (j & 1 ? k_half : 0) + j / 2 * 128,
-                         w + 4 * j);
-        }
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-          uint32_t b0, b1;
-          k_regs<F>(magic, w, ks, b0, b1);
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) mma16816<C::kBF>(sc[mt][nt], q[mt][ks], b0, b1, ks > 0);
-        }
-      }
+      form.scores(magic, st);
       // the next unit's copies while the products are under way
       issue_next(stage == 0 ? NS - 1 : stage - 1);
-      // scales, masks, the rows' references
-      if constexpr (!C::kBF) {
-#pragma unroll
-        for (int nt = 0; nt < 4; ++nt) {
-          const float2 ks = *reinterpret_cast<const float2 *>(kscale + nt * 8 + 2 * c);
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-              float &x = sc[mt][nt][2 * hf], &y = sc[mt][nt][2 * hf + 1];
-              if constexpr (kBias<F> != 0.f) add2(x, y, bias[mt][hf], bias[mt][hf]);
-              mul2(x, y, ks.x, ks.y);
-            }
-        }
-      }
-      if (!whole) {
-        const uint32_t valid =
-            whole_units >> stage & 1
-                ? ~0u
-                : *reinterpret_cast<const uint32_t *>(st + 2 * C::kCodes + 8 * kUnit);
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            const uint64_t bits = row_bits[mt * 16 + hf * 8 + g];
-            const int first = row_first[mt * 16 + hf * 8 + g];
-#pragma unroll
-            for (int nt = 0; nt < 4; ++nt)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const int at = nt * 8 + 2 * c + e, key = key0 + at;
-                const bool see = (valid >> at & 1) &&
-                                 (key < s.past ? key >= first : (bool)(bits >> (key - s.past) & 1));
-                if (!see) sc[mt][nt][2 * hf + e] = -INFINITY;
-              }
-          }
-      }
-      bool raise = false;
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          const float *y = &sc[mt][0][2 * hf];
-          float top = fmaxf(y[0], y[1]);
-#pragma unroll
-          for (int nt = 1; nt < 4; ++nt) top = max3f(top, sc[mt][nt][2 * hf], sc[mt][nt][2 * hf + 1]);
-          raise = raise || top > thr[mt][hf];
-        }
-      if (__any_sync(~0u, raise)) {
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            float top = -INFINITY;
-#pragma unroll
-            for (int nt = 0; nt < 4; ++nt)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) top = fmaxf(top, sc[mt][nt][2 * hf + e]);
-            top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
-            top = fmaxf(m[mt][hf], top * rf[mt][hf]);
-            const float back = exp2f(m[mt][hf] - top);
-            m[mt][hf] = top;
-            if (top > -FLT_MAX) thr[mt][hf] = (top + kRaise) / rf[mt][hf];
-            l[mt][hf][0] *= back;
-            l[mt][hf][1] *= back;
-#pragma unroll
-            for (int i = 0; i < NT; ++i) {
-              o[mt][i][2 * hf] *= back;
-              o[mt][i][2 * hf + 1] *= back;
-            }
-          }
-      }
-      // probabilities, at most 2^15 (fp16) or 1 (bf16)
-      constexpr float kLift = C::kBF ? -kRaise : 15.f - kRaise;
-      const float lift =
-          C::kBF ? kLift : kLift - (float)((int)(__float_as_uint(vref) >> 23) - 127);
-      auto weigh = [&](auto masked) {
-        [[maybe_unused]] float vf[4][2];
-        if constexpr (!C::kBF) {
-#pragma unroll
-          for (int nt = 0; nt < 4; ++nt) {
-            const float2 vs = *reinterpret_cast<const float2 *>(kscale + kUnit + nt * 8 + 2 * c);
-            vf[nt][0] = vs.x;
-            vf[nt][1] = vs.y;
-          }
-        }
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            const float ref = lift - m[mt][hf];
-#pragma unroll
-            for (int nt = 0; nt < 4; ++nt) {
-              float &x = sc[mt][nt][2 * hf], &y = sc[mt][nt][2 * hf + 1];
-              [[maybe_unused]] const bool sx = x != -INFINITY, sy = y != -INFINITY;
-              fma2(x, y, x, y, rf[mt][hf], ref);
-              x = tc::ex2(x);
-              y = tc::ex2(y);
-              add2(l[mt][hf][0], l[mt][hf][1], x, y);
-              if constexpr (!C::kBF) {
-                mul2(x, y, vf[nt][0], vf[nt][1]);
-                if constexpr (masked.value) {  // (a masked key's scale may be NaN)
-                  x = sx ? x : 0.f;
-                  y = sy ? y : 0.f;
-                }
-              }
-            }
-          }
-      };
+      form.scale_keys(kscale);
+      if (!whole)
+        form.mask(Sight{row_bits, row_first, s.past, key0,
+                        whole_units >> stage & 1
+                            ? ~0u
+                            : *reinterpret_cast<const uint32_t *>(st + 2 * C::kCodes + 8 * kUnit)});
+      form.follow();
       if (C::kBF || whole)
-        weigh(std::false_type());
+        form.template weigh<false>(kscale, lift_of<F>(vref));
       else
-        weigh(std::true_type());
+        form.template weigh<true>(kscale, lift_of<F>(vref));
 
       const char *vs = st + C::kCodes;
       bool plain = true;
@@ -618,84 +1013,11 @@ k12_tree_kernel(const __grid_constant__ TreeK k) {
               odd = odd || (w[j] & 0x7f80u) == 0x7f80u || (w[j] & 0x7f800000u) == 0x7f800000u;
           }
           plain = !__any_sync(~0u, odd);
-          if (!plain) {
-            __syncwarp();
-            float *pt = reinterpret_cast<float *>(ring + stage * C::kStage);  // [key][row]
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-              for (int nt = 0; nt < 4; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  pt[(nt * 8 + 2 * c + (e & 1)) * M + mt * 16 + (e >> 1) * 8 + g] = sc[mt][nt][e];
-            __syncwarp();
-            for (int r = 0; r < kUnit; ++r) {
-#pragma unroll
-              for (int i = 0; i < NT; ++i)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  const int el = v_element<F, D>(2 * c + e, i);
-                  const uint16_t bits = *reinterpret_cast<const uint16_t *>(
-                      vs + v_place<P>(r, el / 8) * 16 + (el % 8) * 2);
-                  const float v = __uint_as_float((uint32_t)bits << 16);
-#pragma unroll
-                  for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                    for (int hf = 0; hf < 2; ++hf) {
-                      const float p = pt[r * M + mt * 16 + hf * 8 + g];
-                      if (p != 0.f) o[mt][i][2 * hf + e] += p * v;
-                    }
-                }
-            }
-          }
+          if (!plain)  // (the keys of the stage have been used)
+            form.add_values_singly(vs, reinterpret_cast<float *>(ring + stage * C::kStage));
         }
       }
-      if (plain) {
-#pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
-          uint32_t p[MT][4], lo[MT][4];
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float x0 = sc[mt][2 * kk + j / 2][2 * (j % 2)];
-              const float x1 = sc[mt][2 * kk + j / 2][2 * (j % 2) + 1];
-              if constexpr (C::kBF) {
-                p[mt][j] = pack_bf16(x0, x1);
-                lo[mt][j] = pack_bf16(x0 - bf16_lo(p[mt][j]), x1 - bf16_hi(p[mt][j]));
-              } else {
-                p[mt][j] = pack_f16(x0, x1);
-              }
-            }
-          constexpr int SETS = C::kBF ? D / 64 : 1;
-#pragma unroll
-          for (int set = 0; set < SETS; ++set) {
-            uint32_t w[4][VW];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              // row 16 kk + 2 c + (i & 1) + 8 (i / 2): eight rows on, the places repeat
-              lds_words<VW>(vs + v_at[i & 1] + (16 * kk + 8 * (i >> 1)) * C::kRow + 128 * set,
-                            w[i]);
-            }
-#pragma unroll
-            for (int j = 0; j < NT / SETS / 2; ++j) {
-              uint32_t b00, b01, b10, b11;
-              v_regs<F>(magic, w[0], w[1], j, b00, b10);
-              v_regs<F>(magic, w[2], w[3], j, b01, b11);
-              const int i = set * (NT / SETS) + 2 * j;
-#pragma unroll
-              for (int mt = 0; mt < MT; ++mt) {
-                mma16816<C::kBF>(o[mt][i], p[mt], b00, b01);
-                mma16816<C::kBF>(o[mt][i + 1], p[mt], b10, b11);
-                if constexpr (C::kBF) {
-                  mma16816<true>(o[mt][i], lo[mt], b00, b01);
-                  mma16816<true>(o[mt][i + 1], lo[mt], b10, b11);
-                }
-              }
-            }
-          }
-        }
-      }
+      if (plain) form.add_values(magic, vs);
       __syncwarp();  // before the stage is filled again
       stage = stage + 1 == NS ? 0 : stage + 1;
     }
@@ -707,28 +1029,7 @@ k12_tree_kernel(const __grid_constant__ TreeK k) {
     float *jo = reinterpret_cast<float *>(smem);  // [warp][M][SD]
     float *jm = jo + W * M * SD, *jl = jm + W * M;  // [warp][M]
     const int live = min(M, rows - rt * M);
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        float sum = l[mt][hf][0] + l[mt][hf][1];
-        sum += __shfl_xor_sync(~0u, sum, 1);
-        sum += __shfl_xor_sync(~0u, sum, 2);
-        const int row = mt * 16 + hf * 8 + g, r = warp * M + row;
-        if (row >= live) continue;
-        if (c == 0) {
-          jm[r] = m[mt][hf];
-          jl[r] = C::kBF ? sum : sum * vref;
-        }
-        const float unit = C::kBF ? 1.f : vref;
-#pragma unroll
-        for (int i = 0; i < NT; i += 4)
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-            *reinterpret_cast<float4 *>(jo + r * SD + v_element<F, D>(2 * c + e, i)) =
-                make_float4(o[mt][i][2 * hf + e] * unit, o[mt][i + 1][2 * hf + e] * unit,
-                            o[mt][i + 2][2 * hf + e] * unit, o[mt][i + 3][2 * hf + e] * unit);
-      }
+    form.template leave<SD>(jo + warp * M * SD, jm + warp * M, jl + warp * M, live, vref);
     __syncthreads();
     const bool alone = from == 0 && to == s.units;
     float *part = k.part + ((size_t)blockIdx.x * 2 + (from == 0)) * M * (D + 2);
@@ -871,6 +1172,7 @@ cudaError_t launch_mt(TreeK k, cudaStream_t st) {
 template <int F>
 cudaError_t launch_f(const TreeK &k, cudaStream_t st) {
   const bool one = k.a.T * k.G <= 16;
+  if (k.a.T * k.G <= 8) return k.a.c.d == 64 ? launch_mt<F, 64, 0>(k, st) : launch_mt<F, 128, 0>(k, st);
   if (k.a.c.d == 64) return one ? launch_mt<F, 64, 1>(k, st) : launch_mt<F, 64, 2>(k, st);
   if constexpr (F == FS_CACHE_BF16)
     if (!one) return launch_mt<F, 128, 2>(k, st);
