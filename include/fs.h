@@ -499,10 +499,12 @@ int fs_rope_make_plan(const fs_rope_params *p, fs_rope_plan *plan);
  *                   of a head lie together
  *   q_out, k_out    the same shapes and type, with their own strides; each may
  *                   be its input with the input's strides (in place); other
- *                   overlaps give undefined results
+ *                   overlaps give undefined results (a stride of 0 over more than
+ *                   one row: FS_ERR_INVALID_ARG)
  *   pos             int32 positions: token n of batch b is at
  *                   pos[b * pos_stride + n] (pos_stride N, or 0 for positions
- *                   that all batches share); NULL: positions pos0 + n
+ *                   that all batches share); NULL: positions pos0 + n, all below
+ *                   2^31
  *   inverse         0, or 1 for the transposed rotation: the gradient of q
  *                   from the gradient of q_out
  * Computed in fp32, rounded once.  Enqueues one kernel on `stream`. */
@@ -535,9 +537,10 @@ int fs_rope(const void *q, void *q_out, int Hq, const long long *q_strides,
  *           here (fs_check_status reads it).  The caller zeroes it; no call
  *           clears it.  May be NULL.
  * page: 16, 32, 64, 128 or 256; d: 64 or 128; codes 16-byte aligned; batch *
- * Hkv < 2^16, max_pages * page <= 2^30, pages * Hkv * page < 2^34; other sizes
- * give FS_ERR_UNSUPPORTED (non-positive ones FS_ERR_INVALID_ARG).
- * Sequences may share pages to read; two that write one row race. */
+ * Hkv < 2^16, max_pages * page <= 2^30, pages * Hkv * page < 2^34, Hkv *
+ * page * row bytes < 2^31; other sizes give FS_ERR_UNSUPPORTED
+ * (non-positive ones FS_ERR_INVALID_ARG).  e4m3 codes are numbers: what is to
+ * read as NaN has a NaN scale.  Sequences may share pages to read; two that write one row race. */
 typedef enum {
   FS_CACHE_BF16 = 0,
   FS_CACHE_E4M3 = 1,
@@ -591,7 +594,7 @@ int fs_cache_accept(const fs_cache *cache, const int32_t *start,
  * decoding:
  *   out = sum p v / sum p,  p = exp(scale q . k)  over what the row sees,
  * zeros where a row sees nothing.
- *   q, out  [batch, H, T, d] bf16; H a multiple of the cache's Hkv, query head
+ *   q, out  [batch, H, T, d] bf16, not overlapping; H a multiple of the cache's Hkv, query head
  *           h reading kv head h / (H / Hkv)
  *   past    [batch] int32; count [batch] int32 or NULL (all T); rows
  *           i >= count[b] of out are left as they were
@@ -603,7 +606,9 @@ int fs_cache_accept(const fs_cache *cache, const int32_t *start,
  * T <= 64.  ws: device workspace of fs_tree_workspace_bytes() bytes for one
  * call at a time.  Rows of a sequence with a position past the table or a page
  * outside the cache see only what can be read (and the cache's status says
- * so).  Deterministic. */
+ * so).  Deterministic.  Two kernels; with many rows to a kv head the first waits
+ * on mbarriers, within a limit after which it records FS_ERR_TIMEOUT in the
+ * cache's status, and out is then not valid. */
 size_t fs_tree_workspace_bytes(const fs_cache *cache, int H, int T);
 int fs_tree_attn(const void *q, const fs_cache *cache, const int32_t *past,
                  const int32_t *count, const int64_t *tree, int H, int T,

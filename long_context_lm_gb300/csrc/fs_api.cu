@@ -846,8 +846,11 @@ int check_cache(const fs_cache *c) {
   if (c->d != 64 && c->d != 128) return FS_ERR_UNSUPPORTED;
   if ((long long)c->batch * c->Hkv > 65535) return FS_ERR_UNSUPPORTED;
   if ((long long)c->max_pages * c->page > (1ll << 30)) return FS_ERR_UNSUPPORTED;
-  // rows in groups of sixteen are counted in 32 bits
+  // rows in groups of sixteen are counted in 32 bits, and so are the bytes between
+  // a key and its value
   if ((double)c->pages * 2 * c->Hkv * (c->page / 16) >= 2147483648.0) return FS_ERR_UNSUPPORTED;
+  if ((double)c->Hkv * c->page * fs_cache_row_bytes(c->d, c->format) >= 2147483648.0)
+    return FS_ERR_UNSUPPORTED;
   return FS_OK;
 }
 
@@ -880,6 +883,7 @@ extern "C" int fs_rope(const void *q, void *q_out, int Hq, const long long *q_st
     return FS_ERR_INVALID_ARG;
   if (plan->layout != FS_ROPE_HALF && plan->layout != FS_ROPE_PAIRS) return FS_ERR_INVALID_ARG;
   if (pos_stride < 0 || (inverse != 0 && inverse != 1)) return FS_ERR_INVALID_ARG;
+  if (!pos && (long long)pos0 + N - 1 > 0x7fffffffll) return FS_ERR_INVALID_ARG;
   if ((long long)batch * N >= (1ll << 32) / d || Hq > 65535 || Hk > 65535 - Hq)
     return FS_ERR_UNSUPPORTED;
   const size_t align = dtype == FS_FP32 ? 4 : 2;
@@ -896,6 +900,11 @@ extern "C" int fs_rope(const void *q, void *q_out, int Hq, const long long *q_st
   a.H[1] = Hk;
   set_strides(a.xs[1], k_strides, Hk, N, d);
   set_strides(a.ys[1], k_out_strides, Hk, N, d);
+  for (int i = 0; i < 2; ++i) {  // an output whose rows lie on one another
+    const long long size[3] = {batch, a.H[i], N};
+    for (int j = 0; a.H[i] && j < 3; ++j)
+      if (size[j] > 1 && a.ys[i][j] == 0) return FS_ERR_INVALID_ARG;
+  }
   a.f32 = dtype == FS_FP32;
   a.batch = batch;
   a.N = N;
@@ -998,6 +1007,10 @@ extern "C" int fs_tree_attn(const void *q, const fs_cache *cache, const int32_t 
        reinterpret_cast<uintptr_t>(ws)) % 16)
     return FS_ERR_UNSUPPORTED;
   if (ws_bytes < tree_workspace_bytes(*cache, H, T)) return FS_ERR_INVALID_ARG;
+  // rows of q are read while others of out are written
+  const size_t bytes = (size_t)cache->batch * H * T * cache->d * 2;
+  const uintptr_t q0 = reinterpret_cast<uintptr_t>(q), o0 = reinterpret_cast<uintptr_t>(out);
+  if (q0 < o0 + bytes && o0 < q0 + bytes) return FS_ERR_INVALID_ARG;
   TreeArgs a{};
   a.c = *cache;
   a.q = q;

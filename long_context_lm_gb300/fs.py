@@ -732,6 +732,14 @@ def _launch(dev, stream, fn, where, *args):
         raise FSError(rc, where)
 
 
+def _new(stream, make):
+    """What ``make`` allocates, for use on ``stream`` (None: the current one)."""
+    if stream is None:
+        return make()
+    with torch.cuda.stream(stream):
+        return make()
+
+
 def fs_rope_plan(rot, layout="half", scaling="none", base=10000.0, factor=1.0, original=4096,
                  beta_fast=32.0, beta_slow=1.0, amplitude=1.0):
     """A model's rotary frequencies, worked out once on the host (fs_rope_make_plan):
@@ -766,7 +774,7 @@ def fs_rope(q, k, pos, plan, inverse=False, q_out=None, k_out=None, stream=None)
     B, Hq, N, d = shape
     qp, qs = _rows(q, dev, "q", dt, shape)
     if q_out is None:
-        q_out = torch.empty_like(q)
+        q_out = _new(stream, lambda: torch.empty_like(q))
         qop, qos = (q_out.data_ptr(), None) if qs is None else _rows(q_out, dev, "q_out", dt, shape)
     else:
         qop, qos = _rows(q_out, dev, "q_out", dt, shape)
@@ -777,13 +785,15 @@ def fs_rope(q, k, pos, plan, inverse=False, q_out=None, k_out=None, stream=None)
         shape = (B, Hk, N, d)
         kp, ks = _rows(k, dev, "k", dt, shape)
         if k_out is None:
-            k_out = torch.empty_like(k)
+            k_out = _new(stream, lambda: torch.empty_like(k))
             kop, kos = (k_out.data_ptr(), None) if ks is None else \
                 _rows(k_out, dev, "k_out", dt, shape)
         else:
             kop, kos = _rows(k_out, dev, "k_out", dt, shape)
     pp, stride, pos0 = None, 0, 0
     if isinstance(pos, int):
+        if not -2 ** 31 <= pos < 2 ** 31:
+            raise ValueError(f"pos {pos} does not fit 32 bits")
         pos0 = pos
     elif isinstance(pos, torch.Tensor) and pos.dim() == 2:
         stride = N
@@ -866,8 +876,8 @@ def fs_cache_read(cache, start, count=None, k=None, v=None, T=None, dtype=torch.
     if (k is None) != (v is None) or (k is None and T is None):
         raise ValueError("give k and v, or T")
     if k is None:
-        k, v = (torch.zeros((cache.batch, cache.Hkv, T, cache.d), dtype=dtype, device=cache.device)
-                for _ in range(2))
+        k, v = _new(stream, lambda: torch.zeros((2, cache.batch, cache.Hkv, T, cache.d), dtype=dtype,
+                                                device=cache.device)).unbind(0)
     if not isinstance(k, torch.Tensor) or k.dim() != 4 or \
             k.dtype not in (torch.bfloat16, torch.float32):
         raise ValueError("k must be [batch, Hkv, T, d], bfloat16 or float32")
@@ -921,10 +931,10 @@ def fs_tree_attn(q, cache, past, tree=None, count=None, window=0, scale=None, ou
         raise ValueError("past must be given")
     tp = None if tree is None else _on(tree, dev, "tree", torch.int64, (B, T))
     if out is None:
-        out = torch.empty_like(q) if count is None else torch.zeros_like(q)
+        out = _new(stream, lambda: torch.empty_like(q) if count is None else torch.zeros_like(q))
     op = _on(out, dev, "out", torch.bfloat16, q.shape)
     if ws is None:
-        ws = fs_tree_workspace(cache, B, H, T)
+        ws = _new(stream, lambda: fs_tree_workspace(cache, B, H, T))
     wp = _on(ws, dev, "ws", torch.uint8)
     _launch(dev, stream, L.fs_tree_attn, "fs_tree_attn", qp, cache.desc,
             _counts(cache, "past", past), _counts(cache, "count", count), tp, H, T, int(window),

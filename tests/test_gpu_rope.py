@@ -138,6 +138,22 @@ def test_values_that_are_not_finite_stay_in_their_pair():
     assert bad.nonzero().tolist() == [[0, 3], [0, 35], [1, 8], [1, 40]]
 
 
+def test_rope_refusals_on_the_gpu():
+    x = torch.randn((2, 2, 4, 64), device="cuda")
+    plan = fs.fs_rope_plan(64)
+    with pytest.raises(fs.FSError):
+        fs.fs_rope(x, None, 0, plan, q_out=x[:1].clone().expand(2, 2, 4, 64))
+    with pytest.raises(fs.FSError):
+        fs.fs_rope(x, None, 2 ** 31 - 3, plan)
+    with pytest.raises(ValueError):
+        fs.fs_rope(x, None, 2 ** 31, plan)
+    with pytest.raises(ValueError):
+        fs.fs_rope(x, x[:, :, :2], 0, plan)
+    y, _ = fs.fs_rope(x[:1].expand(2, 2, 4, 64), None, 0, plan)      # an input may repeat
+    z, _ = fs.fs_rope(x[:1], None, 0, plan)
+    assert torch.equal(y, z.expand(2, 2, 4, 64))
+
+
 def test_rope_streams_and_graphs():
     x = torch.randn((2, 4, 100, 64), device="cuda").bfloat16()
     pos = _positions(2, 100, 9999, seed=3)

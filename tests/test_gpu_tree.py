@@ -146,7 +146,7 @@ def test_rows_that_see_nothing_and_single_bits(fmt):
 
 
 @pytest.mark.parametrize("fmt", ref.FORMATS)
-@pytest.mark.parametrize("T,H,Hkv", [(8, 2, 1), (64, 4, 1)])
+@pytest.mark.parametrize("T,H,Hkv", [(8, 2, 1), (64, 4, 1), (8, 1, 1), (7, 2, 2), (24, 1, 1)])
 def test_not_finite_rows_reach_only_the_rows_that_see_them(fmt, T, H, Hkv):
     past = [200, 7]
     cache = _filled(past, T, Hkv, 16, 64, fmt, seed=5)
@@ -168,18 +168,62 @@ def test_not_finite_rows_reach_only_the_rows_that_see_them(fmt, T, H, Hkv):
 
 
 @pytest.mark.parametrize("fmt", ref.FORMATS)
-def test_not_finite_rows_outside_the_window(fmt):
+@pytest.mark.parametrize("H", [2, 4])
+def test_not_finite_rows_outside_the_window(fmt, H):
     # row i sees the last 64 positions: the poisoned ones leave the window row by row
     past, T = [500], 32
     cache = _filled(past, T, 2, 32, 64, fmt, seed=6)
     x = torch.full((1, 2, 8, 64), float("inf"), device="cuda").bfloat16()
     fs.fs_cache_append(cache, _rows((1, 2, 8, 64), 1), x, _ints([440]))
     fs.fs_cache_append(cache, x, x, _ints([100]))          # far outside for every row
-    q = _rows((1, 2, T, 64), 3)
+    q = _rows((1, H, T, 64), 3)
     out = fs.fs_tree_attn(q, cache, _ints(past), window=64)
     want, _, _ = ref.tree_attention(q, cache, past, None, [T], window=64)
     assert torch.equal(torch.isfinite(want), torch.isfinite(out))
     assert torch.isfinite(want[0, :, 12:]).all() and not torch.isfinite(want[0, :, :11]).any()
+
+
+@pytest.mark.parametrize("fmt", ref.FORMATS)
+def test_not_finite_rows_outside_the_window_of_few_rows(fmt):
+    past, T = [500], 8
+    cache = _filled(past, T, 2, 32, 64, fmt, seed=6)
+    x = torch.full((1, 2, 4, 64), float("nan"), device="cuda").bfloat16()
+    fs.fs_cache_append(cache, _rows((1, 2, 4, 64), 1), x, _ints([437]))   # 437 .. 440
+    q = _rows((1, 2, T, 64), 3)
+    out = fs.fs_tree_attn(q, cache, _ints(past), window=64)                # row i from 437 + i on
+    want, _, _ = ref.tree_attention(q, cache, past, None, [T], window=64)
+    assert torch.equal(torch.isfinite(want), torch.isfinite(out))
+    assert torch.isfinite(want[0, :, 4:]).all() and not torch.isfinite(want[0, :, :4]).any()
+
+
+@pytest.mark.parametrize("fmt", ref.FORMATS)
+@pytest.mark.parametrize("T,H", [(6, 1), (6, 2), (30, 1), (50, 1)])
+def test_queries_that_are_not_finite_stay_in_their_row(fmt, T, H):
+    cache = _filled([300], T, 1, 16, 64, fmt)
+    q = _rows((1, H, T, 64), 3)
+    fine = fs.fs_tree_attn(q, cache, _ints([300]))
+    q[0, 0, 2, 7], q[0, H - 1, 4, 9] = float("nan"), float("inf")
+    out = fs.fs_tree_attn(q, cache, _ints([300]))
+    bad = torch.zeros((1, H, T), dtype=torch.bool, device="cuda")
+    bad[0, 0, 2] = bad[0, H - 1, 4] = True
+    assert torch.isnan(out[bad]).all()
+    assert torch.equal(out[~bad], fine[~bad])
+
+
+@pytest.mark.parametrize("fmt,d", [("bf16", 64), ("int8", 64), ("bf16", 128), ("int4", 128)])
+@pytest.mark.parametrize("B,T", [(33, 2), (70, 40), (300, 1), (600, 3), (530, 34)])
+def test_large_batches(B, T, fmt, d):
+    # more sequences than a warp, than a block has threads; many of them empty
+    g = torch.Generator().manual_seed(B)
+    past = torch.randint(0, 90, (B,), generator=g).tolist()
+    count = torch.randint(0, T + 1, (B,), generator=g).tolist()
+    past[B // 2], count[-1] = 1500, T
+    cache = _filled(past, T, 1, 16, d, fmt, seed=1)
+    q = _rows((B, 1, T, d), 3)
+    out = torch.full_like(q, 9.0)
+    fs.fs_tree_attn(q, cache, _ints(past), out=out, count=_ints(count))
+    _check(q, cache, past, out, None, count)
+    fs.fs_check_status(cache.status)
 
 
 def test_scales_scores_and_values_of_extreme_sizes():
@@ -293,6 +337,8 @@ def test_binding_refusals():
         fs.fs_tree_attn(q, cache, ws=torch.empty(16, dtype=torch.uint8, device="cuda"), **ok)
     with pytest.raises(fs.FSError):
         fs.fs_tree_attn(_rows((1, 3, 2, 64), 3), cache, **ok)
+    with pytest.raises(fs.FSError):
+        fs.fs_tree_attn(q, cache, out=q, **ok)             # rows of q are read later on
 
 
 def test_a_verification_step_end_to_end():

@@ -94,6 +94,8 @@ BAD_CACHES = [
     (dict(format=-1), fs.FS_ERR_INVALID_ARG), (dict(page=48), fs.FS_ERR_UNSUPPORTED),
     (dict(page=512), fs.FS_ERR_UNSUPPORTED), (dict(d=80), fs.FS_ERR_UNSUPPORTED),
     (dict(codes=264), fs.FS_ERR_UNSUPPORTED), (dict(batch=40000), fs.FS_ERR_UNSUPPORTED),
+    (dict(max_pages=1 << 27), fs.FS_ERR_UNSUPPORTED), (dict(pages=1 << 30), fs.FS_ERR_UNSUPPORTED),
+    (dict(Hkv=40000, batch=1, page=256, format=0, d=128), fs.FS_ERR_UNSUPPORTED),
 ]
 
 
@@ -118,7 +120,7 @@ def _accept(c, **kw):
 
 
 def _tree(c, **kw):
-    a = dict(q=256, past=256, H=4, T=8, window=0, scale=0.125, out=256, ws=256, wsb=1 << 40)
+    a = dict(q=256, past=256, H=4, T=8, window=0, scale=0.125, out=1 << 30, ws=256, wsb=1 << 40)
     a.update(kw)
     return fs.load().fs_tree_attn(vp(a["q"]), c, vp(a["past"]), None, None, a["H"], a["T"],
                                   a["window"], a["scale"], vp(a["out"]), vp(a["ws"]), a["wsb"], None)
@@ -145,6 +147,7 @@ def test_cache_refusals(call, kw, status):
     (_tree, dict(H=3), fs.FS_ERR_INVALID_ARG), (_tree, dict(window=63), fs.FS_ERR_INVALID_ARG),
     (_tree, dict(window=-1), fs.FS_ERR_INVALID_ARG), (_tree, dict(scale=0.0), fs.FS_ERR_INVALID_ARG),
     (_tree, dict(scale=math.nan), fs.FS_ERR_INVALID_ARG), (_tree, dict(out=264), fs.FS_ERR_UNSUPPORTED),
+    (_tree, dict(out=256), fs.FS_ERR_INVALID_ARG), (_tree, dict(out=256 + 1024), fs.FS_ERR_INVALID_ARG),
 ])
 def test_call_refusals(call, kw, status):
     assert call(_desc(), **kw) == status
