@@ -927,19 +927,8 @@ k12_tree_kernel(const __grid_constant__ TreeK k) {
     };
 
     int next = from + warp, at = 0;  // unit to issue, its place among sixteen
-    uint32_t place = place_of(next, page_of(next));
+    const int page = page_of(next);
     int later = page_of(next + 16 * W);
-    auto issue_next = [&](int stage) {
-      issue(next, stage, place, at);
-      next += W;
-      if (++at == 16) {
-        at = 0;
-        place = place_of(next, later);
-        later = page_of(next + 16 * W);
-      }
-    };
-#pragma unroll 1
-    for (int i = 0; i < NS - 1; ++i) issue_next(i);
     // what every row sees: its bits, and its first key of the prefix
     if (tid < M) {
       const int r = rt * M + tid;
@@ -956,6 +945,18 @@ k12_tree_kernel(const __grid_constant__ TreeK k) {
     }
     __syncthreads();
 
+    uint32_t place = place_of(next, page);
+    auto issue_next = [&](int stage) {
+      issue(next, stage, place, at);
+      next += W;
+      if (++at == 16) {
+        at = 0;
+        place = place_of(next, later);
+        later = page_of(next + 16 * W);
+      }
+    };
+#pragma unroll 1
+    for (int i = 0; i < NS - 1; ++i) issue_next(i);
     form.begin(magic, a.scale);
     int lead = 0;  // no row's prefix begins later
     if (a.window)
