@@ -1175,20 +1175,20 @@ cudaError_t launch_f(const TreeK &k, cudaStream_t st) {
   const bool one = k.a.T * k.G <= 16;
   if (k.a.T * k.G <= 8) return k.a.c.d == 64 ? launch_mt<F, 64, 0>(k, st) : launch_mt<F, 128, 0>(k, st);
   if (k.a.c.d == 64) return one ? launch_mt<F, 64, 1>(k, st) : launch_mt<F, 64, 2>(k, st);
-  if constexpr (F == FS_CACHE_BF16)
-    if (!one) return launch_mt<F, 128, 2>(k, st);
   return launch_mt<F, 128, 1>(k, st);
 }
 
 }  // namespace
 
 // Whether 128 rows are taken at a time, on tcgen05: from more rows to a kv head
-// than the kernel above does well.  Measured on 4 sequences of 16384 int8 keys, 8
-// kv heads, here against there: d = 64 with 32 rows 45 and 54 us, 48 rows 58 and
-// 55, 128 rows 91 and 59; d = 128, whose 32 rows do not fit the registers, 32 rows
-// 88 and 77, 128 rows 215 and 86.  (bf16 codes are not exact in fp16: here.)
+// than the kernel above does well.  Measured on 4 sequences of 16384 keys, 8 kv
+// heads, here against there (us).  int8, d = 64: 64 rows 57 and 58, 96 rows 74 and
+// 59; d = 128: 32 rows 62 and 77, 40 rows 78 and 77, 64 rows 97 and 79.  bf16,
+// whose probabilities are two products here and whose rows need no conversion
+// there, d = 64: 32 rows 43 and 55, 40 rows 62 and 58; d = 128: 16 rows 56 and 71,
+// 20 rows 96 and 74.
 bool wide(const fs_cache &c, int H, int T) {
-  return c.format != FS_CACHE_BF16 && H / c.Hkv * T > (c.d == 64 ? 32 : 16);
+  return H / c.Hkv * T > (c.d == 64 ? 64 : 32) / (c.format == FS_CACHE_BF16 ? 2 : 1);
 }
 
 template <int D, int ROWS>

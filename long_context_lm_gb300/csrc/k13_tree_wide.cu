@@ -5,24 +5,38 @@
 // k12_tree.cu's; a unit here is a tile of KT keys.  A block works on one
 // segment at a time:
 //   * warps 8-11 turn codes into fp16 tiles in shared memory (exact: codes have
-//     at most 8 bits), a ring of them, with the scales beside them;
+//     at most 8 bits), rings of keys and of values, with the scales beside them; two
+//     warps to a tile, the other two on the next one.  bf16 rows are tiles as they
+//     lie: TMA brings them, keys and values of even and of odd tiles a warp each, and
+//     warps 14, 15 look through the values that not all rows see;
 //   * two streams of four warps take the tiles in turn, a thread a row, each
 //     stream with its own scores, probabilities, output (TMEM), running
 //     reference and sum, so that neither waits for the other;
 //   * one thread of warp 12 (13) issues the first (second) stream's products:
-//     the next tile's S = Q K^T as soon as the rows have read this one's, then
-//     O += P V with P from TMEM.
+//     S = Q K^T a tile or two ahead of the rows, O += P V with P from TMEM.
 // The streams are joined through shared memory at the end of a segment.
 //
 // Scores, scales, references and probabilities are as in k12_tree.cu (q by a
 // power of two a row, fp16 probabilities up to 2^15, value scales relative to a
-// power of two that is part of the exponent here).  Where a score passes its
-// row's reference by more than 8 (log2), the reference is raised to it before the 32
+// power of two that is part of the exponent here; bf16: the first 8 bits of a
+// probability and the next 8, two products).  Where a score passes its row's
+// reference by more than 8 (log2), the reference is raised to it before the 32
 // columns are weighed: the row's sum, its O (between two products) and its
 // earlier probabilities of the tile are multiplied by the difference.
 //
-// Bound by: the exponentials and the roughly five operations around each
-// (128 x KT a tile), then the products' issue.
+// Tiles of 128 codes with heads of 64 (scores, probabilities and output fill a
+// stream's half of TMEM), else of 64 with the scores held twice and P written over
+// them: 64 tokens x 4 heads a kv head over 8 x 16384 int8 keys take 154 us with the
+// former and 161 with the latter.  Four warps on the same tile, each waiting for the
+// same barriers, were what everything waited for: 205 us (bf16, one warp for all TMA
+// copies: 182, now 150).
+//
+// Bound by: with codes, the rows' warps, which read two scales a column from shared
+// memory (128 us without those reads) around the exponentials (128 x KT a tile);
+// with bf16 and heads of 128 the products and their issue (103 of 107 us remain
+// without the rows' work).
+#include <cuda.h>
+
 #include "tree.cuh"
 
 namespace fs {
@@ -30,27 +44,40 @@ namespace {
 
 template <int F, int D>
 struct Wide {
+  static constexpr bool kBF = F == FS_CACHE_BF16;
   static constexpr int kBits = Fmt<F>::kBits;
   static constexpr int kRow = D * kBits / 8, P = kRow / 16;
-  static constexpr int KT = D == 64 ? 128 : 64;  // keys of a tile
+  static constexpr int KT = D == 64 && !kBF ? 128 : 64;  // keys of a tile
+  static constexpr bool kTwice = KT == 64;               // scores are held twice
   static constexpr int kCols = D / 64;           // 64-element column blocks
   static constexpr int kBlock = KT * 128;        // bytes of one of them
-  static constexpr int kStage = 2 * kCols * kBlock;
-  static constexpr int kStages = 4;
-  // a tile's codes, a scale pair a thread and four valid words
-  static constexpr int kRawScale = KT * kRow * 2, kRaw = kRawScale + 1024 + 16;
+  static constexpr int kTile = kCols * kBlock;   // keys or values of a tile
+  // tiles of keys and of values held
+  static constexpr int NK = !kBF ? 2 : D == 64 ? 6 : 4, NV = !kBF ? 4 : D == 64 ? 8 : 6;
+  // Codes: a tile is two warps' with half of its keys each, the next one the other two's,
+  // so that the waits of one pair hide behind the work of the other.
+  static constexpr int kMates = 2, KW = KT / kMates;
+  // a warp's codes of a tile, a scale pair a key, valid words
+  static constexpr int kRawScale = KW * kRow * 2, kRaw = kBF ? 0 : kRawScale + KW * 8 + 16;
   static constexpr int kQ = 128 * 128 * kCols;
   static constexpr int kMerge = 128 * (64 + 2) * 4;  // begins in place of q
   static constexpr int kRounds = D / 64;  // of handing it over
-  static constexpr int kSide = KT * 8 + 64;  // scales, 4 valid words, 4 largest value scales
-  static constexpr int kRest = 1024 + kStage * kStages + kMerge + kSide * kStages + 256;
-  static constexpr int kFit = (226 * 1024 - kRest) / kRaw;
-  static constexpr int kRaws = kFit > 5 ? 5 : kFit;  // tiles of codes under way
-  static constexpr int kSmem = kRest + kRaws * kRaw;
-  // TMEM columns of a stream: S, P, O
-  static constexpr int kS = 0, kP = KT, kO = KT + KT / 2, kTmem = 256;
-  static_assert(128 / P % 16 == 0 && kO + D <= kTmem && kRaws >= 2 && kQ <= kMerge, "sizes");
-  static constexpr int NP = KT * P / 128;  // pieces of a thread, keys or values
+  // scales, valid words and largest value scales of 32 keys each; bf16: 2 valid words, 2
+  // of odd values
+  static constexpr int kSide = kBF ? 16 : KT * 8 + KT / 4;
+  static constexpr int kBars = 496;
+  static constexpr int kRest = 1024 + kTile * (NK + NV) + kMerge + kSide * NV + kBars;
+  static constexpr int kFit = kBF ? 0 : (226 * 1024 - kRest) / (kBF ? 1 : 4 * kRaw);
+  static constexpr int kRaws = kFit > 3 ? 3 : kFit;  // tiles of codes under way, a warp
+  static constexpr int kSmem = kRest + 4 * kRaws * kRaw;
+  // TMEM columns of a stream: S twice, O, and P in place of S, 32 columns at a time (16
+  // of fp16, or of high parts and 16 of low ones); or S, P, O.
+  static constexpr int kO = kTwice ? 2 * KT : KT + KT / 2, kTmem = 256;
+  static_assert(kO + D <= kTmem && kQ <= kMerge && kSmem <= 226 * 1024, "sizes");
+  // (a place in the rings always is the same stream's: no wait misses a phase)
+  static_assert(NK % 2 == 0 && NV % 2 == 0, "rings");
+  static_assert(kBF || kRaws >= 2, "pieces");
+  static constexpr int NP = KW * P / 32;  // pieces of a lane, keys or values
 };
 
 constexpr uint32_t kNone = ~0u;
@@ -66,6 +93,7 @@ __device__ __forceinline__ constexpr int element_of(int i) {
 // all of these waits are long, and their polls would take issue slots from the
 // rows' warps.
 __device__ __forceinline__ bool wait_asleep(uint64_t *bar, uint32_t parity, int *fail) {
+  if (tc::mbar_try_wait(bar, parity)) return true;  // (reading the clock takes as long)
   const long long t0 = clock64();
   for (uint32_t i = 1;; ++i) {
     uint32_t ok;
@@ -110,9 +138,14 @@ struct Walk {
 };
 
 struct Bars {
-  uint64_t full[4], empty[4];           // tiles
-  uint64_t s_full[2], s_free[2];     // a stream's scores
-  uint64_t p_full[2], p_free[2];        // a stream's probabilities
+  uint64_t kfull[8], kempty[8];         // tiles of keys
+  uint64_t vfull[8], vempty[8];         // of values, with scales and valid words
+  uint64_t landed[8];                   // values that are looked through first (bf16)
+  uint64_t s_full[2][2], s_free[2];     // a stream's scores
+  // A stream's probabilities and the products that read them, of even and of odd
+  // tiles: a warp may be a tile ahead of another, the rows two ahead of the products.
+  uint64_t p_full[2][2], p_free[2][2];
+  uint64_t added[2];                    // values that are not finite were (bf16)
   uint64_t q_full, done, merge, merged;  // of a segment
 };
 
@@ -136,19 +169,47 @@ __device__ __forceinline__ void to_chunk(const Magic &m, const uint32_t *w, uint
   }
 }
 
+// bf16 rows come by TMA: the map of all groups of sixteen rows.
+struct NoMap {};
+template <int F>
+using MapOf = std::conditional_t<F == FS_CACHE_BF16, CUtensorMap, NoMap>;
+
+// The box of 64 elements from x on of the groups from g on; zeros where one is outside.
+__device__ __forceinline__ void load_group(void *dst, const void *map, uint64_t *bar, int x, int g) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, "
+      "{%3, 0, %4}], [%2];\n" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(g)
+      : "memory");
+}
+
+// tc::desc_sw128 for elements in several blocks of 64, `apart` bytes from one to the next.
+__device__ __forceinline__ uint64_t desc_blocks(uint32_t at, uint32_t apart) {
+  return (tc::desc_sw128(at) & ~(0x3fffull << 16)) | (uint64_t)(apart >> 4) << 16;
+}
+
+// Bits of two bf16 elements that are NaN or infinite: their masks, 0 if both are finite.
+__device__ __forceinline__ uint32_t not_finite(uint32_t w) {
+  return ((w & 0x7f80u) == 0x7f80u ? 0xffffu : 0u) |
+         ((w & 0x7f800000u) == 0x7f800000u ? 0xffff0000u : 0u);
+}
+
 template <int F, int D>
-__global__ void __launch_bounds__(512, 1) k13_tree_wide_kernel(const __grid_constant__ TreeK k) {
+__global__ void __launch_bounds__(512, 1)
+k13_tree_wide_kernel(const __grid_constant__ TreeK k, const __grid_constant__ MapOf<F> map) {
   using C = Wide<F, D>;
-  constexpr int KT = C::KT, P = C::P, NS = C::kStages, NP = C::NP;
+  constexpr int KT = C::KT, P = C::P, NK = C::NK, NV = C::NV, NP = C::NP;
   constexpr int kRaws = C::kRaws;
+  constexpr bool kBF = C::kBF;
   extern __shared__ char smem_raw[];
   char *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-  char *qs = smem + NS * C::kStage;
+  char *vals = smem + NK * C::kTile, *qs = vals + NV * C::kTile;
   float *mo = reinterpret_cast<float *>(qs);  // 64 columns of the second stream's O, over q
   float *mm = mo + 128 * 64, *ml = mm + 128;
   char *side = reinterpret_cast<char *>(ml + 128);
-  Bars &bar = *reinterpret_cast<Bars *>(side + NS * C::kSide);
-  char *raw = side + NS * C::kSide + 256;
+  static_assert(sizeof(Bars) <= C::kBars, "sizes");
+  Bars &bar = *reinterpret_cast<Bars *>(side + NV * C::kSide);
+  [[maybe_unused]] char *raw = side + NV * C::kSide + C::kBars;
   __shared__ uint32_t tmem_base;
   __shared__ int fail;
   const TreeArgs &a = k.a;
@@ -168,15 +229,22 @@ __global__ void __launch_bounds__(512, 1) k13_tree_wide_kernel(const __grid_cons
 
   if (tid == 0) {
     fail = 0;
-    for (int i = 0; i < NS; ++i) {
-      tc::mbar_init(&bar.full[i], 128);
-      tc::mbar_init(&bar.empty[i], 1);
+    for (int i = 0; i < 8; ++i) {
+      tc::mbar_init(&bar.kfull[i], kBF ? 1 : C::kMates);
+      tc::mbar_init(&bar.vfull[i], kBF ? 1 : C::kMates);
+      tc::mbar_init(&bar.landed[i], 1);
+      tc::mbar_init(&bar.kempty[i], 1);
+      tc::mbar_init(&bar.vempty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      tc::mbar_init(&bar.s_full[i], 1);
+      tc::mbar_init(&bar.s_full[i][0], 1);
+      tc::mbar_init(&bar.s_full[i][1], 1);
       tc::mbar_init(&bar.s_free[i], 128);
-      tc::mbar_init(&bar.p_full[i], 128);
-      tc::mbar_init(&bar.p_free[i], 1);
+      tc::mbar_init(&bar.p_full[i][0], 128);
+      tc::mbar_init(&bar.p_full[i][1], 128);
+      tc::mbar_init(&bar.added[i], 128);
+      tc::mbar_init(&bar.p_free[i][0], 1);
+      tc::mbar_init(&bar.p_free[i][1], 1);
     }
     tc::mbar_init(&bar.q_full, 128);
     tc::mbar_init(&bar.done, 128);
@@ -199,7 +267,7 @@ __global__ void __launch_bounds__(512, 1) k13_tree_wide_kernel(const __grid_cons
   auto wait = [&](uint64_t *b, uint32_t phase) {  // the same answer in a warp
     return (bool)__all_sync(~0u, wait_one(b, phase));
   };
-  int it = 0;  // tiles of the block before the current segment
+  uint32_t it = 0;  // tiles of the block before the current segment
   uint32_t seg = 0;
 
   if (warp < 8) {
@@ -223,17 +291,20 @@ __global__ void __launch_bounds__(512, 1) k13_tree_wide_kernel(const __grid_cons
       }
       // the row's power of two; the first stream writes q
       const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q) + at);
-      uint32_t most = 0;
+      float f = 1.f;
+      if constexpr (!kBF) {
+        uint32_t most = 0;
 #pragma unroll 8
-      for (int i = 0; i < D / 8; ++i) {
-        const uint4 x = live ? src[i] : make_uint4(0, 0, 0, 0);
-        most = __vmaxu2(most, x.x & 0x7fff7fffu);
-        most = __vmaxu2(most, x.y & 0x7fff7fffu);
-        most = __vmaxu2(most, x.z & 0x7fff7fffu);
-        most = __vmaxu2(most, x.w & 0x7fff7fffu);
+        for (int i = 0; i < D / 8; ++i) {
+          const uint4 x = live ? src[i] : make_uint4(0, 0, 0, 0);
+          most = __vmaxu2(most, x.x & 0x7fff7fffu);
+          most = __vmaxu2(most, x.y & 0x7fff7fffu);
+          most = __vmaxu2(most, x.z & 0x7fff7fffu);
+          most = __vmaxu2(most, x.w & 0x7fff7fffu);
+        }
+        most = max(most & 0xffffu, most >> 16);
+        f = __uint_as_float((uint32_t)min(254, 268 - (int)(most >> 7)) << 23);
       }
-      most = max(most & 0xffffu, most >> 16);
-      const float f = __uint_as_float((uint32_t)min(254, 268 - (int)(most >> 7)) << 23);
       const float rf = fmaxf(a.scale * kLog2e * (1.f / f), FLT_MIN);
       if (st == 0) {
         // (the second stream's results lay there)
@@ -245,6 +316,10 @@ __global__ void __launch_bounds__(512, 1) k13_tree_wide_kernel(const __grid_cons
           uint32_t z[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
+            if constexpr (kBF) {
+              z[j] = y[j];
+              continue;
+            }
             const int e0 = element_of<F>(2 * j), e1 = element_of<F>(2 * j + 1);
             const float v0 = e0 % 2 ? bf16_hi(y[e0 / 2]) : bf16_lo(y[e0 / 2]);
             const float v1 = e1 % 2 ? bf16_hi(y[e1 / 2]) : bf16_lo(y[e1 / 2]);
@@ -259,11 +334,11 @@ __global__ void __launch_bounds__(512, 1) k13_tree_wide_kernel(const __grid_cons
         break;
       }
 
-      float m = -FLT_MAX, thr = -INFINITY, l0 = 0.f, l1 = 0.f, vref = kLeast;
+      float m = -FLT_MAX, thr = -INFINITY, l0 = 0.f, l1 = 0.f, vref = kBF ? 1.f : kLeast;
       bool begun = false;  // O holds something
       // O *= by, once the last tile's product has ended (this one's has not begun)
       auto rescale = [&](float by) -> bool {
-        if (jt > 0 && !wait(&bar.p_free[st], jt - 1)) return false;
+        if (jt > 0 && !wait(&bar.p_free[st][jt - 1 & 1], jt - 1 >> 1)) return false;
         tc::fence_after_sync();
 #pragma unroll 1
         for (int c = 0; c < D; c += 16) {  // (few registers: 32 columns wait meanwhile)
@@ -278,39 +353,42 @@ __global__ void __launch_bounds__(512, 1) k13_tree_wide_kernel(const __grid_cons
         return true;
       };
 
-      int stage = (it + st) % NS;
-      uint32_t round = (uint32_t)((it + st) / NS);
       for (int i = st; ok && i < n; i += 2, ++jt) {
-        const float *ks = reinterpret_cast<const float *>(side + stage * C::kSide);
-        const uint32_t *valid = reinterpret_cast<const uint32_t *>(ks + 2 * KT);
-        if (!(ok = wait(&bar.full[stage], round) && wait(&bar.s_full[st], jt))) break;
-        if ((stage += 2) >= NS) {
-          stage -= NS;
-          ++round;
-        }
-        tc::fence_after_sync();
+        const uint32_t x = it + i, slot = x % NV;
+        const uint32_t x2 = C::kTwice ? jt & 1 : 0, tile2 = C::kTwice ? jt >> 1 : jt;
+        const uint32_t ts = tm + x2 * KT, tp = C::kTwice ? ts : tm + KT;  // S, P
+        const float *ks = reinterpret_cast<const float *>(side + slot * C::kSide);
+        const uint32_t *valid = reinterpret_cast<const uint32_t *>(ks + (kBF ? 0 : 2 * KT));
         const int key0 = w.s.first + (w.from + i) * KT;
+        if (!(ok = wait(&bar.vfull[slot], x / NV))) break;
         const uint4 in = *reinterpret_cast<const uint4 *>(valid);
-        const float4 tops = *reinterpret_cast<const float4 *>(valid + 4);
+        if (!(ok = wait(&bar.s_full[st][x2], tile2))) break;
+        tc::fence_after_sync();
         const bool whole = (KT == 128 ? in.x & in.y & in.z & in.w : in.x & in.y) == ~0u &&
                            __all_sync(~0u, key0 + KT <= w.s.past && key0 >= first);
-        const float top_v = KT == 128 ? fmaxf(fmaxf(tops.x, tops.y), fmaxf(tops.z, tops.w))
-                                      : fmaxf(tops.x, tops.y);
-        if (top_v > vref) {  // the same for all rows
-          const float up =
-              __uint_as_float((__float_as_uint(top_v) + 0x7fffffu) & 0x7f800000u);
-          const float back = vref / up;
-          if (begun && !(ok = rescale(back))) break;
-          l0 *= back;
-          l1 *= back;
-          vref = up;
+        float lift = 0.f;
+        if constexpr (!kBF) {
+          float top_v = fmaxf(__uint_as_float(in.z), __uint_as_float(in.w));
+          if constexpr (KT == 128) {
+            const float4 tops = *reinterpret_cast<const float4 *>(valid + 4);
+            top_v = fmaxf(fmaxf(tops.x, tops.y), fmaxf(tops.z, tops.w));
+          }
+          if (top_v > vref) {  // the same for all rows
+            const float up =
+                __uint_as_float((__float_as_uint(top_v) + 0x7fffffu) & 0x7f800000u);
+            const float back = vref / up;
+            if (begun && !(ok = rescale(back))) break;
+            l0 *= back;
+            l1 *= back;
+            vref = up;
+          }
+          lift = 15.f - kRaise - (float)((int)(__float_as_uint(vref) >> 23) - 127);
         }
-        const float lift = 15.f - kRaise - (float)((int)(__float_as_uint(vref) >> 23) - 127);
 
         // The columns, 32 at a time.
         auto weigh = [&](int c0, auto masked) {
           uint32_t u[32];
-          tc::tmem_ld32(tm + C::kS + c0, u);
+          tc::tmem_ld32(ts + c0, u);
           [[maybe_unused]] uint32_t seen = ~0u;  // of these 32 keys
           if constexpr (masked.value) {
             const int key = key0 + c0;
@@ -327,7 +405,7 @@ __global__ void __launch_bounds__(512, 1) k13_tree_wide_kernel(const __grid_cons
             seen &= valid[c0 / 32];
           }
           tc::tmem_wait_ld();
-          if (c0 + 32 == KT) {  // the next tile's scores may be made
+          if (!C::kTwice && c0 + 32 == KT) {  // the next tile's scores may be made
             tc::fence_before_sync();
             tc::mbar_arrive(&bar.s_free[st]);
           }
@@ -336,11 +414,13 @@ __global__ void __launch_bounds__(512, 1) k13_tree_wide_kernel(const __grid_cons
           float y[32];
 #pragma unroll
           for (int j = 0; j < 32; j += 4) {
-            const float4 kk = *reinterpret_cast<const float4 *>(ks + c0 + j);
             y[j] = __uint_as_float(u[j]), y[j + 1] = __uint_as_float(u[j + 1]);
             y[j + 2] = __uint_as_float(u[j + 2]), y[j + 3] = __uint_as_float(u[j + 3]);
-            mul2(y[j], y[j + 1], kk.x, kk.y);
-            mul2(y[j + 2], y[j + 3], kk.z, kk.w);
+            if constexpr (!kBF) {
+              const float4 kk = *reinterpret_cast<const float4 *>(ks + c0 + j);
+              mul2(y[j], y[j + 1], kk.x, kk.y);
+              mul2(y[j + 2], y[j + 3], kk.z, kk.w);
+            }
           }
           if constexpr (masked.value) {
 #pragma unroll
@@ -365,17 +445,22 @@ __global__ void __launch_bounds__(512, 1) k13_tree_wide_kernel(const __grid_cons
             l1 *= back;
             if (begun) ok = rescale(back);
 #pragma unroll 1
-            for (int c = 0; c < c0 / 2; c += 8) {  // this tile's earlier columns
+            for (int c = 0; c < (C::kTwice ? c0 : c0 / 2);
+                 c += C::kTwice && !kBF && c % 32 ? 24 : 8) {  // this tile's earlier columns
               uint32_t z[8];
               tc::tmem_wait_st();
-              tc::tmem_ld8(tm + C::kP + c, z);
+              tc::tmem_ld8(tp + c, z);
               tc::tmem_wait_ld();
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
-                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&z[i]));
-                z[i] = pack_f16(f.x * back, f.y * back);
+                if constexpr (kBF) {
+                  z[i] = pack_bf16(bf16_lo(z[i]) * back, bf16_hi(z[i]) * back);
+                } else {
+                  const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&z[i]));
+                  z[i] = pack_f16(f.x * back, f.y * back);
+                }
               }
-              tc::tmem_st8(tm + C::kP + c, z);
+              tc::tmem_st8(tp + c, z);
             }
           }
           const float ref = lift - m;
@@ -390,24 +475,35 @@ __global__ void __launch_bounds__(512, 1) k13_tree_wide_kernel(const __grid_cons
             add2(s2, s3, y[j + 2], y[j + 3]);
           }
           add2(l0, l1, s2, s3);
+          if constexpr (!kBF) {
 #pragma unroll
-          for (int j = 0; j < 32; j += 4) {
-            const float4 vv = *reinterpret_cast<const float4 *>(ks + KT + c0 + j);
-            mul2(y[j], y[j + 1], vv.x, vv.y);
-            mul2(y[j + 2], y[j + 3], vv.z, vv.w);
-          }
-          if constexpr (masked.value) {  // (a masked key's scale may be NaN)
+            for (int j = 0; j < 32; j += 4) {
+              const float4 vv = *reinterpret_cast<const float4 *>(ks + KT + c0 + j);
+              mul2(y[j], y[j + 1], vv.x, vv.y);
+              mul2(y[j + 2], y[j + 3], vv.z, vv.w);
+            }
+            if constexpr (masked.value) {  // (a masked key's scale may be NaN)
 #pragma unroll
-            for (int j = 0; j < 32; ++j) y[j] = seen >> j & 1 ? y[j] : 0.f;
+              for (int j = 0; j < 32; ++j) y[j] = seen >> j & 1 ? y[j] : 0.f;
+            }
           }
           uint32_t p[16];
+          [[maybe_unused]] uint32_t rest[16];
 #pragma unroll
-          for (int j = 0; j < 32; j += 2) p[j / 2] = pack_f16(y[j], y[j + 1]);
-          if (c0 == 0 && jt > 0) {  // the last tile's product has read P
-            ok = wait(&bar.p_free[st], jt - 1) && ok;
+          for (int j = 0; j < 32; j += 2) {
+            if constexpr (kBF) {  // cut off after 8 bits, and the next 8
+              p[j / 2] = __byte_perm(__float_as_uint(y[j]), __float_as_uint(y[j + 1]), 0x7632);
+              rest[j / 2] = pack_bf16(y[j] - bf16_lo(p[j / 2]), y[j + 1] - bf16_hi(p[j / 2]));
+            } else {
+              p[j / 2] = pack_f16(y[j], y[j + 1]);
+            }
+          }
+          if (!C::kTwice && c0 == 0 && jt > 0) {  // the last tile's product has read P
+            ok = wait(&bar.p_free[st][jt - 1 & 1], jt - 1 >> 1) && ok;
             tc::fence_after_sync();
           }
-          tc::tmem_st16(tm + C::kP + c0 / 2, p);
+          tc::tmem_st16(tp + (C::kTwice ? c0 : c0 / 2), p);
+          if constexpr (kBF) tc::tmem_st16(tp + c0 + 16, rest);
         };
         // (two copies: one with masks under a condition would test and select for
         // every element of every tile)
@@ -421,13 +517,59 @@ __global__ void __launch_bounds__(512, 1) k13_tree_wide_kernel(const __grid_cons
         if (!ok) break;
         tc::tmem_wait_st();
         tc::fence_before_sync();
-        tc::mbar_arrive(&bar.p_full[st]);
+        tc::mbar_arrive(&bar.p_full[st][jt & 1]);
         begun = true;
+        if constexpr (kBF) {
+          // Values that are not finite were taken out of the tile (0 * inf in the
+          // product would reach the rows that do not see them) and are added here.
+          for (uint64_t odd = (uint64_t)in.w << 32 | in.z; odd; odd &= odd - 1) {
+            if (!(ok = wait(&bar.p_free[st][jt & 1], jt >> 1))) break;
+            tc::fence_after_sync();
+            const int i = __ffsll(odd) - 1, key = key0 + i, page = a.c.page;
+            const int j = key - w.s.past;
+            const bool sees = j < 0 ? key >= first : (bits >> j & 1) != 0;
+            const size_t block =
+                (size_t)a.c.table[(size_t)w.b * a.c.max_pages + key / page] * 2 + 1;
+            const uint4 *v = reinterpret_cast<const uint4 *>(
+                static_cast<const char *>(a.c.codes) +
+                ((block * a.c.Hkv + w.h) * page + key % page) * C::kRow);
+            uint32_t pw[8];
+            tc::tmem_ld8(tp + (i & 32) + (i / 2 & 8), pw);
+            tc::tmem_wait_ld();
+            float p = 0.f;
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+              if (x == (i / 2 & 7)) p = i & 1 ? bf16_hi(pw[x]) : bf16_lo(pw[x]);
+#pragma unroll 1
+            for (int c = 0; c < D; c += 8) {
+              const uint4 x = v[c / 8];
+              const uint32_t y[4] = {x.x & not_finite(x.x), x.y & not_finite(x.y),
+                                     x.z & not_finite(x.z), x.w & not_finite(x.w)};
+              if ((y[0] | y[1] | y[2] | y[3]) == 0) continue;  // the same for all rows
+              uint32_t o[8];
+              tc::tmem_ld8(tm + C::kO + c, o);
+              tc::tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const uint32_t bit = e & 1 ? y[e / 2] & 0xffff0000u : y[e / 2] << 16;
+                if (sees && bit)
+                  o[e] = __float_as_uint(__uint_as_float(o[e]) + p * __uint_as_float(bit));
+              }
+              tc::tmem_st8(tm + C::kO + c, o);
+              tc::tmem_wait_st();
+            }
+          }
+          if (!ok) break;
+          if (in.z | in.w) {
+            tc::fence_before_sync();
+            tc::mbar_arrive(&bar.added[st]);
+          }
+        }
       }
       if (!ok) break;
       // the segment's end: all products of the stream
       if (begun) {
-        if (!(ok = wait(&bar.p_free[st], jt - 1))) break;
+        if (!(ok = wait(&bar.p_free[st][jt - 1 & 1], jt - 1 >> 1))) break;
         tc::fence_after_sync();
       }
       const float l = (l0 + l1) * vref;
@@ -502,204 +644,322 @@ __global__ void __launch_bounds__(512, 1) k13_tree_wide_kernel(const __grid_cons
       }
       it += n;
     }
-  } else if (warp < 12) {
-    // -------------------------------------------------- codes -> fp16 tiles
-    const int t = tid - 256, shift = 31 - __clz(a.c.page);
-    const Magic magic = make_magic();
-    const int v_off = a.c.Hkv * a.c.page;  // rows from a key to its value
-    bool ok = true;
-    while (ok && w.next(k)) {
-      // A thread's pieces lie in rows t / P + j (128 / P), keys and values; it
-      // copies them into a ring of its own and turns them into fp16 when they
-      // have come.  Its scale belongs to key t % KT.
-      //
-      // Where the tiles lie: lane l holds sixteen rows, group l % GP of tile
-      // l / GP of the 32 / GP tiles looked up at a time, as their place among all
-      // groups of sixteen rows (kNone: nothing to read); the next ones' pages are
-      // asked for that many tiles ahead.
-      constexpr int GP = KT / 16, AT = 32 / GP;
-      const int n = w.to - w.from, key_s = t & (KT - 1), groups = a.c.page >> 4;
-      auto key_of = [&](int i) {
-        return w.s.first + (w.from + i + lane / GP) * KT + 16 * (lane % GP);
-      };
-      auto page_of = [&](int i) {
-        const int key = key_of(i);
-        return i + lane / GP < n && key < w.s.end
-                   ? a.c.table[(size_t)w.b * a.c.max_pages + (key >> shift)]
-                   : INT_MIN;
-      };
-      auto place_of = [&](int i, int page) -> uint32_t {
-        if ((unsigned)page >= (unsigned)a.c.pages) {
-          if (page != INT_MIN && a.c.status) atomicCAS(a.c.status, 0, FS_ERR_CACHE);
-          return kNone;
-        }
-        return (uint32_t)(page * 2 * a.c.Hkv + w.h) * groups + ((key_of(i) & (a.c.page - 1)) >> 4);
-      };
-      uint32_t place = place_of(0, page_of(0));
-      int later = page_of(AT), at = 0, left = w.s.end - w.s.first - w.from * KT;  // keys from here
-      const char *codes = static_cast<const char *>(a.c.codes) +
-                          (t / P % 16) * C::kRow + t % P * 16;  // the thread's piece of a group
-      auto copy = [&](int slot) {
-        const uint32_t dst = smem_u32(raw) + slot * C::kRaw + t * 16;
-        const uint32_t to = smem_u32(raw) + slot * C::kRaw + C::kRawScale + t * 8;
-        uint32_t *word = reinterpret_cast<uint32_t *>(raw + slot * C::kRaw + C::kRawScale + 1024) +
-                         (t >> 5);
-        const uint32_t gs = __shfl_sync(~0u, place, at * GP + key_s / 16);
-        // (kNone in any of the tile's groups, or a tile that ends early)
-        if (left >= KT && !__any_sync(~0u, lane / GP == at && place == kNone)) {
-#pragma unroll
-          for (int j = 0; j < NP; ++j) {
-            const uint32_t g = __shfl_sync(~0u, place, at * GP + (t / P + j * (128 / P)) / 16);
-            const char *p = codes + (size_t)g * (16 * C::kRow);
-            cp_async16(dst + j * 2048, p);
-            cp_async16(dst + (NP + j) * 2048, p + v_off * C::kRow);
-          }
-          const float *p = a.c.scales + (size_t)gs * 16 + key_s % 16;
-          cp_async4(to, p);
-          cp_async4(to + 4, p + v_off);
-          if (lane == 0) *word = ~0u;
-        } else {
-#pragma unroll
-          for (int j = 0; j < NP; ++j) {
-            const int r = t / P + j * (128 / P);
-            const uint32_t g = __shfl_sync(~0u, place, at * GP + r / 16);
-            const bool have = g != kNone && r < left;
-            const char *p = have ? codes + (size_t)g * (16 * C::kRow)
-                                 : static_cast<const char *>(a.c.codes);
-            cp_async16z(dst + j * 2048, p, have ? 16 : 0);
-            cp_async16z(dst + (NP + j) * 2048, have ? p + v_off * C::kRow : p, have ? 16 : 0);
-          }
-          const bool in = gs != kNone && key_s < left;
-          const float *p = in ? a.c.scales + (size_t)gs * 16 + key_s % 16 : a.c.scales;
-          cp_async4z(to, p, in ? 4 : 0);
-          cp_async4z(to + 4, in ? p + v_off : p, in ? 4 : 0);
-          const uint32_t some = __ballot_sync(~0u, in);
-          if (lane == 0) *word = some;
-        }
-        cp_async_commit();
-        left -= KT;
-        if (++at == AT) at = 0;
-      };
-      int ahead = 0;  // tiles copied
-      auto copy_next = [&](int slot) {
-        if (at == 0 && ahead) {
-          place = place_of(ahead, later);
-          later = page_of(ahead + AT);
-        }
-        copy(slot);
-        ++ahead;
-      };
-#pragma unroll 1
-      for (int i = 0; i < kRaws - 1; ++i) copy_next(i);
-      int slot = 0, stage = it % NS;
-      uint32_t round = (uint32_t)(it / NS);
-      int chunk_at[128 / C::kBits / 8];
-#pragma unroll
-      for (int c = 0; c < 128 / C::kBits / 8; ++c) {
-        const int chunk = t % P * (128 / C::kBits / 8) + c;  // of the row's D / 8
-        chunk_at[c] = chunk / 8 * C::kBlock + swz128(t / P, chunk % 8);
+  } else if (warp < 12 || warp >= 14) {
+    // Where the tiles lie: lane l holds sixteen rows, group l % GP of the (l / GP)th of
+    // the warp's next 32 / GP tiles, as their place among all groups of sixteen rows
+    // (kNone: nothing to read); the following ones' pages are asked for meanwhile.
+    constexpr int GP = KT / 16, AT = 32 / GP;
+    const int shift = 31 - __clz(a.c.page), groups = a.c.page >> 4;
+    int n = 0;
+    auto key_of = [&](int i, int turn) {
+      return w.s.first + (w.from + i + lane / GP * turn) * KT + 16 * (lane % GP);
+    };
+    auto page_of = [&](int i, int turn) {
+      const int key = key_of(i, turn);
+      return i + lane / GP * turn < n && key < w.s.end
+                 ? a.c.table[(size_t)w.b * a.c.max_pages + (key >> shift)]
+                 : INT_MIN;
+    };
+    auto place_of = [&](int i, int turn, int page) -> uint32_t {
+      if ((unsigned)page >= (unsigned)a.c.pages) {
+        if (page != INT_MIN && a.c.status) atomicCAS(a.c.status, 0, FS_ERR_CACHE);
+        return kNone;
       }
+      return (uint32_t)(page * 2 * a.c.Hkv + w.h) * groups +
+             ((key_of(i, turn) & (a.c.page - 1)) >> 4);
+    };
+    bool ok = true;
+    if constexpr (kBF) {
+      // ------------------------ tiles by TMA: keys (warps 8, 9) and values (10, 11) of
+      // the even and the odd ones, a warp's tiles one stream's.  Values of tiles that
+      // not all rows see whole go through warps 14, 15 first: those of keys that are
+      // not there and those that are not finite become zeros.
+      const uint32_t mine = warp & 1;
+      const bool look_only = warp >= 14, values = warp >= 10;
+      const int box = min(groups, 4);      // groups of sixteen rows that come in one copy
+      uint32_t looked = 0, landed = 0;     // places whose tile goes by `landed`, and its phases
+      while (ok && w.next(k)) {
+        n = w.to - w.from;
+        const int lead = a.window ? w.s.past + w.s.n - a.window : 0;  // no row begins later
+        const int i0 = (it & 1) == mine ? 0 : 1;
+        uint32_t place = kNone;
+        int later = look_only ? 0 : page_of(i0, 2), at = 0;
 #pragma unroll 1
-      for (int i = 0; i < n; ++i) {
-        copy_next(slot == 0 ? kRaws - 1 : slot - 1);
-        cp_async_wait<kRaws - 1>();
-        if (round > 0 && !(ok = wait(&bar.empty[stage], round - 1))) break;
-        const char *src = raw + slot * C::kRaw;
-        char *dst = smem + stage * C::kStage;
-        // (the row's place in the swizzle is the same for all of the thread's rows:
-        // they lie a multiple of eight apart)
-        constexpr int CH = 128 / C::kBits / 8;  // chunks of the piece: 2 or 4
+        for (int i = i0; i < n; i += 2) {
+          const uint32_t t = it + i, slot = values ? t % NV : t % NK;
+          char *dst = (values ? vals : smem) + slot * C::kTile;
+          uint32_t *valid = reinterpret_cast<uint32_t *>(side + slot * C::kSide);
+          const int key0 = w.s.first + (w.from + i) * KT;
+          const bool look = key0 + KT > w.s.past || key0 < lead;
+          if (!look_only) {
+            if (at == 0) {
+              place = place_of(i, 2, later);
+              later = page_of(i + 2 * AT, 2);
+            }
+            const uint32_t turn = values ? t / NV : t / NK;
+            if (turn > 0 &&
+                !(ok = wait(values ? &bar.vempty[slot] : &bar.kempty[slot], turn - 1))) {
+              // no copy may be under way when the block ends
+              const uint32_t held = values ? NV : NK;
+              for (uint32_t x = t - held; x < t; x += 2)
+                if (looked >> x % held & 1)
+                  tc::mbar_wait(&bar.landed[x % held], ~landed >> x % held & 1, nullptr);
+                else
+                  tc::mbar_wait(values ? &bar.vfull[x % held] : &bar.kfull[x % held],
+                                x / held & 1, nullptr);
+              break;
+            }
+            const uint32_t have = __ballot_sync(~0u, place != kNone) >> (at * GP);
+            uint64_t *to = values ? &bar.vfull[slot] : &bar.kfull[slot];
+            if (values) {
+              looked = looked & ~(1u << slot) | (uint32_t)look << slot;
+              landed ^= (uint32_t)look << slot;
+              if (look) to = &bar.landed[slot];
+              if (lane == 0)
+                *reinterpret_cast<uint4 *>(valid) =
+                    make_uint4((have & 1 ? 0xffffu : 0u) | (have & 2 ? 0xffff0000u : 0u),
+                               (have & 4 ? 0xffffu : 0u) | (have & 8 ? 0xffff0000u : 0u), 0, 0);
+            }
+            if (lane == 0) tc::mbar_arrive_expect_tx(to, C::kTile);
+            __syncwarp();
+            if (lane / GP == at && lane % GP % box == 0) {
+              // (a group that is not there: before the first one, zeros)
+              const int g = place == kNone ? -4 : (int)place + (values ? a.c.Hkv * groups : 0);
+#pragma unroll
+              for (int c = 0; c < C::kCols; ++c)
+                load_group(dst + c * C::kBlock + lane % GP * 2048, &map, to, c * 64, g);
+            }
+            if (++at == AT) at = 0;
+          } else if (look) {
+            if (!(ok = wait(&bar.landed[slot], landed >> slot & 1))) break;
+            landed ^= 1u << slot;
+            uint32_t odd[2];
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              const int r = half * 32 + lane;
+              const bool in = key0 + r < w.s.end;
+              uint32_t any = 0;
 #pragma unroll 1
-        for (int part = 0; part < 2; ++part) {
-          uint4 x[NP];
+              for (int c = 0; c < C::kCols; ++c)
 #pragma unroll
-          for (int j = 0; j < NP; ++j)
-            x[j] = *reinterpret_cast<const uint4 *>(src + (part * NP + j) * 2048 + t * 16);
-          char *to = dst + part * (C::kCols * C::kBlock);
+                for (int j = 0; j < 8; ++j) {
+                  uint4 *x = reinterpret_cast<uint4 *>(dst + c * C::kBlock + swz128(r, j));
+                  const uint4 v = *x;
+                  const uint4 z = make_uint4(not_finite(v.x), not_finite(v.y), not_finite(v.z),
+                                             not_finite(v.w));
+                  const uint32_t some = z.x | z.y | z.z | z.w;
+                  any |= some;
+                  if (!in) {
+                    *x = make_uint4(0, 0, 0, 0);
+                  } else if (some) {
+                    *x = make_uint4(v.x & ~z.x, v.y & ~z.y, v.z & ~z.z, v.w & ~z.w);
+                  }
+                }
+              odd[half] = __ballot_sync(~0u, in && any);
+            }
+            if (lane == 0) {
+              valid[2] = odd[0];
+              valid[3] = odd[1];
+            }
+            tc::fence_async_smem();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&bar.vfull[slot]);
+          }
+        }
+        it += n;
+      }
+    } else {
+      // ------------------------------------------------ codes -> fp16 tiles (warps 8-11)
+      // A lane's pieces lie in rows row0 + lane / P + j (32 / P) of the tile, keys and
+      // values; it copies them into a ring of its own and turns them into fp16 when
+      // they have come.
+      constexpr int KW = C::KW, TURN = 4 / C::kMates, CH = 128 / C::kBits / 8;  // chunks of a piece
+      const int mate = (warp - 8) % C::kMates, mine = (warp - 8) / C::kMates, row0 = mate * KW;
+      const Magic magic = make_magic();
+      const int v_off = a.c.Hkv * a.c.page;  // rows from a key to its value
+      char *ring = raw + (warp - 8) * kRaws * C::kRaw;
+      const char *codes = static_cast<const char *>(a.c.codes) + lane / P * C::kRow + lane % P * 16;
+      int chunk_at[CH];
 #pragma unroll
-          for (int j = 0; j < NP; ++j) {
-            const uint32_t wd[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+      for (int c = 0; c < CH; ++c) {
+        const int chunk = lane % P * CH + c;  // of the row's D / 8
+        chunk_at[c] = chunk / 8 * C::kBlock + swz128(row0 + lane / P, chunk % 8);
+      }
+      while (ok && warp < 12 && w.next(k)) {
+        n = w.to - w.from;
+        const int i0 = (int)((mine - it) % TURN);
+        uint32_t place = kNone;
+        int later = page_of(i0, TURN), at = 0, ahead = i0;  // the next tile to copy
+        auto copy = [&](int slot) {
+          if (at == 0) {
+            place = place_of(ahead, TURN, later);
+            later = page_of(ahead + TURN * AT, TURN);
+          }
+          char *to = ring + slot * C::kRaw;
+          const uint32_t dst = smem_u32(to) + lane * 16;
+          const uint32_t sc = smem_u32(to) + C::kRawScale + lane * 8;
+          uint32_t *word = reinterpret_cast<uint32_t *>(to + C::kRawScale + KW * 8);
+          const int left = w.s.end - w.s.first - (w.from + ahead) * KT;  // keys from the tile's first
+          // (kNone in any of the tile's groups, or a tile that ends early)
+          if (left >= KT && !__any_sync(~0u, lane / GP == at && place == kNone)) {
 #pragma unroll
-            for (int c = 0; c < CH; ++c) {
-              uint4 y;
-              to_chunk<F>(magic, wd + c * (4 / CH), y);
-              *reinterpret_cast<uint4 *>(to + chunk_at[c] + j * (128 / P) * 128) = y;
+            for (int j = 0; j < NP; ++j) {
+              const int r = j * (32 / P);
+              const uint32_t g = __shfl_sync(~0u, place, at * GP + (row0 + r) / 16);
+              const char *p = codes + ((size_t)g * 16 + r % 16) * C::kRow;
+              cp_async16(dst + j * 512, p);
+              cp_async16(dst + (NP + j) * 512, p + v_off * C::kRow);
+            }
+#pragma unroll
+            for (int x = 0; x < KW; x += 32) {
+              const uint32_t g = __shfl_sync(~0u, place, at * GP + (row0 + x + lane) / 16);
+              const float *p = a.c.scales + (size_t)g * 16 + lane % 16;
+              cp_async4(sc + x * 8, p);
+              cp_async4(sc + x * 8 + 4, p + v_off);
+              if (lane == 0) word[x / 32] = ~0u;
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < NP; ++j) {
+              const int r = j * (32 / P);
+              const uint32_t g = __shfl_sync(~0u, place, at * GP + (row0 + r) / 16);
+              const bool have = g != kNone && row0 + r + lane / P < left;
+              const char *p = have ? codes + ((size_t)g * 16 + r % 16) * C::kRow
+                                   : static_cast<const char *>(a.c.codes);
+              cp_async16z(dst + j * 512, p, have ? 16 : 0);
+              cp_async16z(dst + (NP + j) * 512, have ? p + v_off * C::kRow : p, have ? 16 : 0);
+            }
+#pragma unroll
+            for (int x = 0; x < KW; x += 32) {
+              const uint32_t g = __shfl_sync(~0u, place, at * GP + (row0 + x + lane) / 16);
+              const bool in = g != kNone && row0 + x + lane < left;
+              const float *p = in ? a.c.scales + (size_t)g * 16 + lane % 16 : a.c.scales;
+              cp_async4z(sc + x * 8, p, in ? 4 : 0);
+              cp_async4z(sc + x * 8 + 4, in ? p + v_off : p, in ? 4 : 0);
+              const uint32_t some = __ballot_sync(~0u, in);
+              if (lane == 0) word[x / 32] = some;
             }
           }
-        }
-        const float2 sc = *reinterpret_cast<const float2 *>(src + C::kRawScale + t * 8);
-        const uint32_t word = *reinterpret_cast<const uint32_t *>(src + C::kRawScale + 1024 + (t >> 5) * 4);
-        const uint32_t top =
-            __reduce_max_sync(~0u, sc.y <= FLT_MAX ? __float_as_uint(fmaxf(sc.y, 0.f)) : 0u);
-        if (t < KT) {
-          float *sd = reinterpret_cast<float *>(side + stage * C::kSide);
-          sd[t] = sc.x;
-          sd[KT + t] = sc.y;
-          if (lane == 0) {
-            uint32_t *valid = reinterpret_cast<uint32_t *>(sd + 2 * KT);
-            valid[t / 32] = word;
-            valid[4 + t / 32] = top;
+          cp_async_commit();
+          ahead += TURN;
+          if (++at == AT) at = 0;
+        };
+#pragma unroll 1
+        for (int i = 0; i < kRaws - 1; ++i) copy(i);
+        int slot = 0;
+#pragma unroll 1
+        for (int i = i0; i < n; i += TURN) {
+          copy(slot == 0 ? kRaws - 1 : slot - 1);
+          cp_async_wait<kRaws - 1>();
+          __syncwarp();
+          const uint32_t t = it + i;
+          const char *src = ring + slot * C::kRaw;
+#pragma unroll 1
+          for (int part = 0; part < 2; ++part) {  // keys, values
+            const uint32_t place = part ? t % NV : t % NK, turn = part ? t / NV : t / NK;
+            if (turn > 0 && !(ok = wait(part ? &bar.vempty[place] : &bar.kempty[place], turn - 1)))
+              break;
+            uint4 x[NP];
+#pragma unroll
+            for (int j = 0; j < NP; ++j)
+              x[j] = *reinterpret_cast<const uint4 *>(src + (part * NP + j) * 512 + lane * 16);
+            char *to = (part ? vals : smem) + place * C::kTile;
+#pragma unroll
+            for (int j = 0; j < NP; ++j) {
+              const uint32_t wd[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+#pragma unroll
+              for (int c = 0; c < CH; ++c) {
+                uint4 y;
+                to_chunk<F>(magic, wd + c * (4 / CH), y);
+                // (the swizzle repeats after eight rows)
+                *reinterpret_cast<uint4 *>(to + (chunk_at[c] ^ j * (32 / P) % 8 * 16) +
+                                           j * (32 / P) * 128) = y;
+              }
+            }
+            if (part) {
+              float *sd = reinterpret_cast<float *>(side + place * C::kSide) + row0;
+              uint32_t *valid = reinterpret_cast<uint32_t *>(sd - row0 + 2 * KT) + row0 / 32;
+#pragma unroll
+              for (int y = 0; y < KW; y += 32) {
+                const float2 sc =
+                    *reinterpret_cast<const float2 *>(src + C::kRawScale + (y + lane) * 8);
+                const uint32_t top = __reduce_max_sync(
+                    ~0u, sc.y <= FLT_MAX ? __float_as_uint(fmaxf(sc.y, 0.f)) : 0u);
+                sd[y + lane] = sc.x;
+                sd[KT + y + lane] = sc.y;
+                if (lane == 0) {
+                  valid[y / 32] =
+                      *reinterpret_cast<const uint32_t *>(src + C::kRawScale + KW * 8 + y / 8);
+                  valid[KT / 32 + y / 32] = top;
+                }
+              }
+            }
+            tc::fence_async_smem();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(part ? &bar.vfull[place] : &bar.kfull[place]);
           }
+          if (!ok) break;
+          slot = slot + 1 == kRaws ? 0 : slot + 1;
         }
-        tc::fence_async_smem();
-        tc::mbar_arrive(&bar.full[stage]);
-        slot = slot + 1 == kRaws ? 0 : slot + 1;
-        if (++stage == NS) {
-          stage = 0;
-          ++round;
-        }
+        cp_async_wait<0>();
         __syncwarp();
+        it += n;
       }
-      cp_async_wait<0>();
-      it += n;
     }
   } else if (warp < 14 && lane == 0) {
     // ------------------------------------------------------ a stream's products
     const int st = warp - 12;
     const uint32_t tm = tmem_base + st * C::kTmem;
-    const uint32_t ring = smem_u32(smem), q = smem_u32(qs);
-    constexpr uint32_t kQK = tc::idesc_f16(128, KT, 0), kPV = tc::idesc_f16(128, 64, 1);
-    uint32_t jt = 0;
+    const uint32_t keys = smem_u32(smem), q = smem_u32(qs);
+    constexpr uint32_t kQK = kBF ? tc::idesc_bf16(128, KT, 0) : tc::idesc_f16(128, KT, 0);
+    constexpr uint32_t kPV = kBF ? tc::idesc_bf16(128, D, 1) : tc::idesc_f16(128, D, 1);
+    constexpr int kPVs = KT / 16 * (kBF ? 2 : 1);  // steps: high parts, low parts
+    uint32_t jt = 0, added = 0;
     bool ok = true;
     for (; ok && w.next(k); ++seg) {
       const int n = w.to - w.from;
       if (!(ok = wait_one(&bar.q_full, seg))) break;
-      int stage = (it + st) % NS;  // of the next scores
-      uint32_t round = (uint32_t)((it + st) / NS);
-      auto scores = [&](uint32_t j) -> bool {
-        if (!wait_one(&bar.full[stage], round)) return false;
-        if (j > 0 && !wait_one(&bar.s_free[st], j - 1)) return false;
+      auto scores = [&](uint32_t j, uint32_t x) -> bool {
+        const uint32_t slot = x % NK;
+        if (!wait_one(&bar.kfull[slot], x / NK)) return false;
+        if (!C::kTwice && j > 0 && !wait_one(&bar.s_free[st], j - 1)) return false;
         tc::fence_after_sync();
 #pragma unroll
         for (int s = 0; s < D / 16; ++s) {
           const uint32_t off = s / 4, in = s % 4 * 32;
-          tc::mma_ss(tm + C::kS, tc::desc_sw128(q + off * (128 * 128) + in),
-                     tc::desc_sw128(ring + stage * C::kStage + off * C::kBlock + in), kQK, s > 0);
+          tc::mma_ss(tm + (C::kTwice ? (j & 1) * KT : 0), tc::desc_sw128(q + off * (128 * 128) + in),
+                     tc::desc_sw128(keys + slot * C::kTile + off * C::kBlock + in), kQK, s > 0);
         }
-        tc::mma_commit(&bar.s_full[st]);
-        if ((stage += 2) >= NS) {
-          stage -= NS;
-          ++round;
-        }
+        tc::mma_commit(&bar.s_full[st][C::kTwice ? j & 1 : 0]);
+        tc::mma_commit(&bar.kempty[slot]);
         return true;
       };
-      int now = stage;  // of the values
-      if (st < n && !(ok = scores(jt))) break;
+      // one or two tiles of scores ahead of the rows
+      if (st < n && !(ok = scores(jt, it + st))) break;
+      if (C::kTwice && st + 2 < n && !(ok = scores(jt + 1, it + st + 2))) break;
       for (int i = st; i < n; i += 2, ++jt) {
-        // the next tile's scores first: they are there when this one's rows are done
-        if (i + 2 < n && !(ok = scores(jt + 1))) break;
-        if (!(ok = wait_one(&bar.p_full[st], jt))) break;
+        const uint32_t slot = (it + i) % NV;
+        if (!C::kTwice && i + 2 < n && !(ok = scores(jt + 1, it + i + 2))) break;
+        if (!(ok = wait_one(&bar.vfull[slot], (it + i) / NV) && wait_one(&bar.p_full[st][jt & 1], jt >> 1)))
+          break;
         tc::fence_after_sync();
-        const uint32_t v = ring + now * C::kStage + C::kCols * C::kBlock;
+        const uint32_t v = smem_u32(vals) + slot * C::kTile;
+        uint2 odd = make_uint2(0, 0);
+        if constexpr (kBF) odd = *reinterpret_cast<const uint2 *>(side + slot * C::kSide + 8);
 #pragma unroll
-        for (int c = 0; c < C::kCols; ++c)
-#pragma unroll
-          for (int s = 0; s < KT / 16; ++s)
-            tc::mma_ts(tm + C::kO + c * 64, tm + C::kP + s * 8,
-                       tc::desc_sw128(v + c * C::kBlock + s * 2048), kPV, i != st || s > 0);
-        tc::mma_commit(&bar.p_free[st]);
-        tc::mma_commit(&bar.empty[now]);
-        now = now + 2 >= NS ? now + 2 - NS : now + 2;
+        for (int s = 0; s < kPVs; ++s)
+          tc::mma_ts(tm + C::kO,
+                     C::kTwice ? tm + (jt & 1) * KT + s % (KT / 16) / 2 * 32 + s % 2 * 8 +
+                                     s / (KT / 16) * 16
+                               : tm + KT + s * 8,
+                     desc_blocks(v + s % (KT / 16) * 2048, C::kBlock), kPV, i != st || s > 0);
+        tc::mma_commit(&bar.p_free[st][jt & 1]);
+        tc::mma_commit(&bar.vempty[slot]);
+        if ((odd.x | odd.y) && !(ok = wait_one(&bar.added[st], added++))) break;
+        // (the scores after the next go where this tile's P lies)
+        if (C::kTwice && i + 4 < n &&
+            !(ok = wait_one(&bar.p_free[st][jt & 1], jt >> 1) && scores(jt + 2, it + i + 4)))
+          break;
       }
       it += n;
     }
@@ -708,6 +968,39 @@ __global__ void __launch_bounds__(512, 1) k13_tree_wide_kernel(const __grid_cons
   if (tid == 0 && fail && a.c.status) tc::report_error(a.c.status, FS_ERR_TIMEOUT);
   __syncwarp();
   if (warp == 12) tc::tmem_dealloc(tmem_base, 512);
+}
+
+using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                                 const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                                 const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_fn() {
+  static EncodeTiled fn = nullptr;
+  if (!fn) {
+    void *ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault,
+                                         &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeTiled>(ptr);
+  }
+  return fn;
+}
+
+// All rows of the cache as [groups of sixteen][16][d], boxes of 64
+// elements of the groups of a page, at most four (a tile).
+bool make_cache_map(CUtensorMap *map, const fs_cache &c) {
+  EncodeTiled fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)c.d, 16,
+                              (cuuint64_t)c.pages * 2 * c.Hkv * (c.page / 16)};
+  const cuuint64_t strides[2] = {(cuuint64_t)c.d * 2, (cuuint64_t)c.d * 32};
+  const cuuint32_t box[3] = {64, 16, (cuuint32_t)(c.page >= 64 ? 4 : c.page / 16)};
+  const cuuint32_t steps[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, c.codes, dims, strides, box, steps,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int F, int D>
@@ -720,7 +1013,11 @@ cudaError_t launch_fd(TreeK k, cudaStream_t st) {
   auto fn = k13_tree_wide_kernel<F, D>;
   cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
-  fn<<<k.blocks, 512, C::kSmem, st>>>(k);
+  MapOf<F> map;
+  if constexpr (C::kBF) {
+    if (!make_cache_map(&map, k.a.c)) return cudaErrorInvalidValue;
+  }
+  fn<<<k.blocks, 512, C::kSmem, st>>>(k, map);
   e = cudaGetLastError();
   return e != cudaSuccess ? e : launch_tree_join(k, st);
 }
@@ -736,7 +1033,8 @@ cudaError_t launch_tree_wide(const TreeK &k, cudaStream_t st) {
       return small ? launch_fd<FS_CACHE_INT8, 64>(k, st) : launch_fd<FS_CACHE_INT8, 128>(k, st);
     case FS_CACHE_INT4:
       return small ? launch_fd<FS_CACHE_INT4, 64>(k, st) : launch_fd<FS_CACHE_INT4, 128>(k, st);
-    default: return cudaErrorInvalidValue;
+    default:
+      return small ? launch_fd<FS_CACHE_BF16, 64>(k, st) : launch_fd<FS_CACHE_BF16, 128>(k, st);
   }
 }
 

@@ -271,6 +271,71 @@ def test_pages_outside_and_tables_that_end():
         fs.fs_check_status(cache.status)
 
 
+@pytest.mark.parametrize("fmt", ref.FORMATS)
+@pytest.mark.parametrize("page,d,H", [(16, 64, 2), (32, 128, 2), (64, 64, 4), (128, 128, 1)])
+def test_pages_outside_with_many_rows(page, d, H, fmt):
+    # 64 to 256 rows to a kv head; a page of the prefix and the last one cannot be read
+    past, T = [1000, 700], 64
+    cache = _filled(past, T, 1, page, d, fmt, seed=2)
+    q = _rows((2, H, T, d), 3, 0.3)
+    good = fs.fs_tree_attn(q, cache, _ints(past))
+    gone = 256 // page
+    cache.table[0, gone] = cache.codes.shape[0]    # one past the last
+    cache.table[0, (past[0] + T - 1) // page] = -1
+    bad = fs.fs_tree_attn(q, cache, _ints(past))
+    assert torch.equal(good[1], bad[1])
+    with pytest.raises(fs.FSError) as e:
+        fs.fs_check_status(cache.status)
+    assert e.value.status == fs.FS_ERR_CACHE
+    keys = torch.arange(past[0] + T, device="cuda")
+    there = (keys // page != gone) & (keys // page != (past[0] + T - 1) // page)
+    cache.table[0, gone] = cache.table[0, 0]
+    cache.table[0, (past[0] + T - 1) // page] = cache.table[0, 0]
+    kv = [ref.values(*ref.gather(cache, 0, past[0] + T, x), cache.format)[there, 0] for x in (0, 1)]
+    rows = torch.arange(T, device="cuda")
+    seen = (keys[None] <= past[0] + rows[:, None])[:, there]
+    s = (q[0].double() @ kv[0].T * d ** -0.5).masked_fill(~seen, float("-inf"))
+    p = torch.softmax(s, -1)
+    want, mean = p @ kv[1], p @ kv[1].abs()
+    ds = (d + 3) * 2.0 ** -24 * d ** -0.5 * float((q[0].double().abs() @ kv[0].abs().T).max())
+    bound = 1.01 * 2.0 ** -8 * want.abs() + (2 * ds + 2.0 ** -11 + 2.0 ** -18) * mean + \
+        len(keys) * 2.0 ** -31 * float(kv[1].abs().max())
+    assert torch.all((bad[0].double() - want).abs() <= bound)
+
+
+@pytest.mark.parametrize("fmt", ref.FORMATS)
+@pytest.mark.parametrize("page,d,H,window", [(16, 64, 2, 64), (128, 128, 1, 100), (64, 64, 3, 0)])
+def test_not_finite_values_and_many_rows(page, d, H, window, fmt):
+    # values that are not finite in the last tile of the prefix, among the drafted tokens and
+    # where the window of some rows begins, with and without earlier tiles
+    for past in (20, 2000):
+        T = 64
+        cache = _filled([past], T, 1, page, d, fmt, seed=6)
+        q, tree = _rows((1, H, T, d), 3, 0.3), _trees(1, T, 5)
+        x = _rows((1, 1, 3, d), 1)
+        x[:, :, 0, 3], x[:, :, 1, 40], x[:, :, 2, d - 1] = float("inf"), float("nan"), float("-inf")
+        for at in (past + 1, past + 40, max(past - window + 5, 0) if window else past + 20):
+            fs.fs_cache_append(cache, _rows((1, 1, 3, d), 2), x, _ints([at]))
+        out = fs.fs_tree_attn(q, cache, _ints([past]), tree=tree, window=window)
+        want, _, _ = ref.tree_attention(q, cache, [past], tree, [T], window=window)
+        assert torch.equal(torch.isfinite(want), torch.isfinite(out))
+        assert not torch.isfinite(want).all()
+
+
+@pytest.mark.parametrize("fmt", ref.FORMATS)
+def test_long_sequences_with_many_rows(fmt):
+    # many tiles to a block, so that every ring goes round often; several segments to a block
+    for B, Hkv, past, d in ((1, 1, 40000, 64), (1, 1, 40000, 128), (70, 3, 700, 64), (5, 1, 30000, 128)):
+        cache = _filled([past] * B, 64, Hkv, 64, d, fmt, seed=4)
+        q, tree = _rows((B, 2 * Hkv, 64, d), 8, 0.3), _trees(B, 64, 3)
+        at = _ints([past] * B)
+        out = fs.fs_tree_attn(q, cache, at, tree=tree)
+        _check(q[:2], cache, [past] * min(B, 2), out[:2], tree[:2])
+        for _ in range(3):
+            assert torch.equal(out, fs.fs_tree_attn(q, cache, at, tree=tree))
+        fs.fs_check_status(cache.status)
+
+
 def test_sequences_that_share_pages_and_repeat():
     cache = _filled([64, 64, 64], 4, 2, 16, 64, "e4m3", seed=8)
     cache.table[1, :4] = cache.table[0, :4]                # a shared prefix
