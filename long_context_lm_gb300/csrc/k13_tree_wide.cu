@@ -307,27 +307,33 @@ k13_tree_wide_kernel(const __grid_constant__ TreeK k, const __grid_constant__ Ma
       }
       const float rf = fmaxf(a.scale * kLog2e * (1.f / f), FLT_MIN);
       if (st == 0) {
-        // (the second stream's results lay there)
-        if (seg > 0 && !(ok = wait(&bar.merged, seg * C::kRounds - 1))) break;
-#pragma unroll 2
-        for (int i = 0; i < D / 8; ++i) {
-          const uint4 x = live ? src[i] : make_uint4(0, 0, 0, 0);
-          const uint32_t y[4] = {x.x, x.y, x.z, x.w};
-          uint32_t z[4];
+#pragma unroll 1
+        for (int c = 0; ok && c < C::kCols; ++c) {
+          uint4 x[8];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if constexpr (kBF) {
-              z[j] = y[j];
-              continue;
+          for (int i = 0; i < 8; ++i) x[i] = live ? src[c * 8 + i] : make_uint4(0, 0, 0, 0);
+          // (the second stream's results lay there)
+          if (c == 0 && seg > 0 && !(ok = wait(&bar.merged, seg * C::kRounds - 1))) break;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t y[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+            uint32_t z[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              if constexpr (kBF) {
+                z[j] = y[j];
+                continue;
+              }
+              const int e0 = element_of<F>(2 * j), e1 = element_of<F>(2 * j + 1);
+              const float v0 = e0 % 2 ? bf16_hi(y[e0 / 2]) : bf16_lo(y[e0 / 2]);
+              const float v1 = e1 % 2 ? bf16_hi(y[e1 / 2]) : bf16_lo(y[e1 / 2]);
+              z[j] = pack_f16(v0 * f, v1 * f);
             }
-            const int e0 = element_of<F>(2 * j), e1 = element_of<F>(2 * j + 1);
-            const float v0 = e0 % 2 ? bf16_hi(y[e0 / 2]) : bf16_lo(y[e0 / 2]);
-            const float v1 = e1 % 2 ? bf16_hi(y[e1 / 2]) : bf16_lo(y[e1 / 2]);
-            z[j] = pack_f16(v0 * f, v1 * f);
+            *reinterpret_cast<uint4 *>(qs + c * (128 * 128) + swz128(row, i)) =
+                make_uint4(z[0], z[1], z[2], z[3]);
           }
-          *reinterpret_cast<uint4 *>(qs + i / 8 * (128 * 128) + swz128(row, i % 8)) =
-              make_uint4(z[0], z[1], z[2], z[3]);
         }
+        if (!ok) break;
         tc::fence_async_smem();
         tc::mbar_arrive(&bar.q_full);
       } else if (!(ok = wait(&bar.q_full, seg))) {  // (the last segment's results have been taken)
