@@ -270,7 +270,7 @@ struct Sight {
 
 // Probabilities are at most 2^15 (fp16) or 1 (bf16).
 template <int F>
-constexpr float kLift = F == FS_CACHE_BF16 ? -kRaise : 15.f - kRaise;
+constexpr float kLift = F == FS_CACHE_BF16 ? -kRaise<F> : 15.f - kRaise<F>;
 template <int F>
 __device__ __forceinline__ float lift_of(float vref) {
   return F == FS_CACHE_BF16 ? kLift<F>
@@ -448,7 +448,7 @@ struct RowForm {
         top = fmaxf(m[mt][hf], top * rf[mt][hf]);
         const float back = exp2f(m[mt][hf] - top);
         m[mt][hf] = top;
-        if (top > -FLT_MAX) thr[mt][hf] = (top + kRaise) / rf[mt][hf];
+        if (top > -FLT_MAX) thr[mt][hf] = (top + kRaise<F>) / rf[mt][hf];
         l[mt][hf][0] *= back;
         l[mt][hf][1] *= back;
 #pragma unroll
@@ -681,7 +681,7 @@ struct ColForm {
       top = fmaxf(m[e], top * rf[e]);
       const float back = exp2f(m[e] - top);
       m[e] = top;
-      if (top > -FLT_MAX) thr[e] = (top + kRaise) / rf[e];
+      if (top > -FLT_MAX) thr[e] = (top + kRaise<F>) / rf[e];
       l[e] *= back;
 #pragma unroll
       for (int j = 0; j < NT / 2; ++j) {

@@ -20,7 +20,7 @@
 // power of two a row, fp16 probabilities up to 2^15, value scales relative to a
 // power of two that is part of the exponent here; bf16: the first 8 bits of a
 // probability and the next 8, two products).  Where a score passes its row's
-// reference by more than 8 (log2), the reference is raised to it before the 32
+// reference by more than 8 (log2; bf16: 16), the reference is raised to it before the 32
 // columns are weighed: the row's sum, its O (between two products) and its
 // earlier probabilities of the tile are multiplied by the difference.
 //
@@ -29,12 +29,12 @@
 // them: 64 tokens x 4 heads a kv head over 8 x 16384 int8 keys take 154 us with the
 // former and 161 with the latter.  Four warps on the same tile, each waiting for the
 // same barriers, were what everything waited for: 205 us (bf16, one warp for all TMA
-// copies: 182, now 150).
+// copies: 182, now 145).
 //
 // Bound by: with codes, the rows' warps, which read two scales a column from shared
 // memory (128 us without those reads) around the exponentials (128 x KT a tile);
-// with bf16 and heads of 128 the products and their issue (103 of 107 us remain
-// without the rows' work).
+// with bf16 and heads of 128 the products' issue and the keys that come twice, once
+// for each 128 rows (4 of 107 us went with the rows' work).
 #include <cuda.h>
 
 #include "tree.cuh"
@@ -388,7 +388,7 @@ k13_tree_wide_kernel(const __grid_constant__ TreeK k, const __grid_constant__ Ma
             l1 *= back;
             vref = up;
           }
-          lift = 15.f - kRaise - (float)((int)(__float_as_uint(vref) >> 23) - 127);
+          lift = 15.f - kRaise<F> - (float)((int)(__float_as_uint(vref) >> 23) - 127);
         }
 
         // The columns, 32 at a time.
@@ -446,7 +446,7 @@ k13_tree_wide_kernel(const __grid_constant__ TreeK k, const __grid_constant__ Ma
             const bool none = m == -FLT_MAX;  // the row has seen no key
             const float back = none ? 0.f : exp2f(-by_log2);
             m = none ? fmaxf(t0 * rf, -FLT_MAX) : m + by_log2;
-            if (m > -FLT_MAX) thr = (m + kRaise) / rf;
+            if (m > -FLT_MAX) thr = (m + kRaise<F>) / rf;
             l0 *= back;
             l1 *= back;
             if (begun) ok = rescale(back);

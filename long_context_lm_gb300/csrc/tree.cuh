@@ -14,9 +14,11 @@ namespace fs {
 
 constexpr float kLog2e = 1.4426950408889634f;
 // How far a score may pass its row's reference (log2).  Raising one costs the wide
-// kernel a pass over its O: 8 against 4 is 157 against 168 us for 64 tokens x 32
-// heads over 16384 int8 keys.
-constexpr float kRaise = 8.f;
+// kernel a pass over its O: 4, 8 and 12 are 166, 154 and 149 us for 64 tokens x 32
+// heads over 16384 int8 keys.  8 leaves a row's largest fp16 probability at 2^7 or
+// more, 2^31 times the step of the smallest ones; bf16 ones are relative, and take 16.
+template <int F>
+constexpr float kRaise = F == FS_CACHE_BF16 ? 16.f : 8.f;
 
 // The least power of two that the value scales are relative to.  Probabilities
 // are made 1 / vref times as large (the products with the scales then need no
