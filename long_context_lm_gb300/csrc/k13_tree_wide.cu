@@ -74,7 +74,10 @@ struct Wide {
   // of fp16, or of high parts and 16 of low ones); or S, P, O.
   static constexpr int kO = kTwice ? 2 * KT : KT + KT / 2, kTmem = 256;
   static_assert(kO + D <= kTmem && kQ <= kMerge && kSmem <= 226 * 1024, "sizes");
-  // (a place in the rings always is the same stream's: no wait misses a phase)
+  // A wait by parity must not fall two phases behind.  A place in the rings holds tiles of
+  // one parity, which are one loader's and, within a segment, one stream's; after a segment
+  // with an odd number of tiles the streams change places, but no tile of the next
+  // one is read before q_full, which follows the last reads of this one.
   static_assert(NK % 2 == 0 && NV % 2 == 0, "rings");
   static_assert(kBF || kRaws >= 2, "pieces");
   static constexpr int NP = KW * P / 32;  // pieces of a lane, keys or values
@@ -246,7 +249,9 @@ k13_tree_wide_kernel(const __grid_constant__ TreeK k, const __grid_constant__ Ma
       tc::mbar_init(&bar.p_free[i][0], 1);
       tc::mbar_init(&bar.p_free[i][1], 1);
     }
-    tc::mbar_init(&bar.q_full, 128);
+    // the rows of the first stream, and the second stream's issuing thread: a segment of
+    // one tile has no other wait that ties it to the others
+    tc::mbar_init(&bar.q_full, 129);
     tc::mbar_init(&bar.done, 128);
     tc::mbar_init(&bar.merge, 128);
     tc::mbar_init(&bar.merged, 128);
@@ -924,6 +929,7 @@ k13_tree_wide_kernel(const __grid_constant__ TreeK k, const __grid_constant__ Ma
     bool ok = true;
     for (; ok && w.next(k); ++seg) {
       const int n = w.to - w.from;
+      if (st == 1) tc::mbar_arrive(&bar.q_full);
       if (!(ok = wait_one(&bar.q_full, seg))) break;
       auto scores = [&](uint32_t j, uint32_t x) -> bool {
         const uint32_t slot = x % NK;
