@@ -24,15 +24,15 @@
 // and turns them into fragments in registers.  Codes of 8 and 4 bits are exact
 // in fp16; q is brought into fp16's range by a power of two a row (exact but
 // for elements below 2^-39 of the row's largest).  The key's scale multiplies
-// the score; the value's scale multiplies the probability, relative to a power
-// of two at least as large as every scale seen (exact to follow), which joins
-// the output at the end.
+// the score, the value's scale the probability: a weight.
 //
-// Probabilities go into the second product as fp16 (half a step 2^-11) between
-// 0 and 2^15, the row's largest at least 2^7: half a step of the smallest is
-// 2^-32 of the largest; with bf16 values as a bf16 pair (high and low part,
-// 2^-16).  The maximum follows lazily: a row's reference moves only when a score
-// passes it by 8 (log2).
+// Weights go into the second product as fp16 (half a step 2^-11), the row's
+// largest at least 2^7: half a step of the smallest is 2^-32 of the largest; with
+// bf16 values as a bf16 pair (high and low part, 2^-16).  A row's reference follows
+// the largest weight of the keys that it sees, lazily (tree.cuh): a common one
+// for all rows, from the largest value scale of the unit, would let values that a row
+// does not see, or sees with next to no probability, take its weights out of fp16's
+// range.
 #include <type_traits>
 
 #include "tree.cuh"
@@ -268,15 +268,6 @@ struct Sight {
   }
 };
 
-// Probabilities are at most 2^15 (fp16) or 1 (bf16).
-template <int F>
-constexpr float kLift = F == FS_CACHE_BF16 ? -kRaise<F> : 15.f - kRaise<F>;
-template <int F>
-__device__ __forceinline__ float lift_of(float vref) {
-  return F == FS_CACHE_BF16 ? kLift<F>
-                            : kLift<F> - (float)((int)(__float_as_uint(vref) >> 23) - 127);
-}
-
 // One row of q as the lane holds it (q_words): to fp16 by a power of two.  f: the
 // row's factor; sum: of its fp16 elements, over the row's four lanes, where the
 // key codes have a bias.
@@ -337,8 +328,8 @@ struct RowForm {
   uint32_t raw[MT][2][KS][2];
   uint32_t q[MT][KS][4];
   float rf[MT][2], bias[MT][2];
-  // reference, the product that passes it too far, sum (of even and odd keys)
-  float m[MT][2], thr[MT][2], l[MT][2][2], o[MT][NT][4], sc[MT][4][4];
+  // reference, sum (of even and odd keys)
+  float ref[MT][2], l[MT][2][2], o[MT][NT][4], sc[MT][4][4];
 
   __device__ __forceinline__ RowForm(const W &w) : at(w) {}
   // src(row): the row's elements, null past the last
@@ -363,23 +354,11 @@ struct RowForm {
           q[mt][ks][hf] = raw[mt][hf][ks][0];
           q[mt][ks][2 + hf] = raw[mt][hf][ks][1];
         }
-        m[mt][hf] = -FLT_MAX;
-        thr[mt][hf] = -INFINITY;
+        ref[mt][hf] = FLT_MAX;
         l[mt][hf][0] = l[mt][hf][1] = 0.f;
 #pragma unroll
         for (int i = 0; i < NT; ++i) o[mt][i][2 * hf] = o[mt][i][2 * hf + 1] = 0.f;
       }
-  }
-  __device__ __forceinline__ void rescale(float back) {
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) l[mt][e / 2][e % 2] *= back;
-#pragma unroll
-      for (int i = 0; i < NT; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[mt][i][e] *= back;
-    }
   }
   __device__ __forceinline__ void scores(const Magic &magic, const char *st) {
 #pragma unroll
@@ -431,35 +410,48 @@ struct RowForm {
     for (int nt = 1; nt < 4; ++nt) top = max3f(top, sc[mt][nt][2 * hf], sc[mt][nt][2 * hf + 1]);
     return top;
   }
-  __device__ __forceinline__ void follow() {  // the rows' references
+  __device__ __forceinline__ void follow(const float *kscale, float high) {  // the rows' references
     bool raise = false;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) raise = raise || top_of(mt, hf) > thr[mt][hf];
+      for (int hf = 0; hf < 2; ++hf)
+        raise = raise || fmaf(top_of(mt, hf), rf[mt][hf], ref[mt][hf]) > high;
     if (!__any_sync(~0u, raise)) return;
+    [[maybe_unused]] float lv[8];
+    if constexpr (!kBF) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) lv[i] = lg2(fabsf(kscale[kUnit + i / 2 * 8 + 2 * at.c + i % 2]));
+    }
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
-        float top = top_of(mt, hf);
-        top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
-        top = fmaxf(m[mt][hf], top * rf[mt][hf]);
-        const float back = exp2f(m[mt][hf] - top);
-        m[mt][hf] = top;
-        if (top > -FLT_MAX) thr[mt][hf] = (top + kRaise<F>) / rf[mt][hf];
-        l[mt][hf][0] *= back;
-        l[mt][hf][1] *= back;
+        float score = top_of(mt, hf) * rf[mt][hf], weight = -INFINITY;
+        if constexpr (!kBF) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            weight = fmaxf(weight, fmaf(sc[mt][i / 2][2 * hf + i % 2], rf[mt][hf], lv[i]));
+        }
+#pragma unroll
+        for (int x = 1; x < 4; x <<= 1) {
+          score = fmaxf(score, __shfl_xor_sync(~0u, score, x));
+          if constexpr (!kBF) weight = fmaxf(weight, __shfl_xor_sync(~0u, weight, x));
+        }
+        const float to = moved<F>(ref[mt][hf], score, weight);
+        const Back back(ref[mt][hf], to);
+        ref[mt][hf] = to;
+        l[mt][hf][0] = back(l[mt][hf][0]);
+        l[mt][hf][1] = back(l[mt][hf][1]);
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
-          o[mt][i][2 * hf] *= back;
-          o[mt][i][2 * hf + 1] *= back;
+          o[mt][i][2 * hf] = back(o[mt][i][2 * hf]);
+          o[mt][i][2 * hf + 1] = back(o[mt][i][2 * hf + 1]);
         }
       }
   }
   template <bool MASKED>
-  __device__ __forceinline__ void weigh(const float *kscale, float lift) {
+  __device__ __forceinline__ void weigh(const float *kscale) {
     [[maybe_unused]] float2 vs[4];
     if constexpr (!kBF) {
 #pragma unroll
@@ -470,12 +462,11 @@ struct RowForm {
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
-        const float ref = lift - m[mt][hf];
 #pragma unroll
         for (int nt = 0; nt < 4; ++nt) {
           float &x = sc[mt][nt][2 * hf], &y = sc[mt][nt][2 * hf + 1];
           [[maybe_unused]] const bool sx = x != -INFINITY, sy = y != -INFINITY;
-          fma2(x, y, x, y, rf[mt][hf], ref);
+          fma2(x, y, x, y, rf[mt][hf], ref[mt][hf]);
           x = tc::ex2(x);
           y = tc::ex2(y);
           add2(l[mt][hf][0], l[mt][hf][1], x, y);
@@ -560,8 +551,7 @@ struct RowForm {
   }
   // The warp's results: rows of SD floats, references, sums.
   template <int SD>
-  __device__ __forceinline__ void leave(float *jo, float *jm, float *jl, int live, float vref) {
-    const float unit = kBF ? 1.f : vref;
+  __device__ __forceinline__ void leave(float *jo, float *jm, float *jl, int live) {
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -572,16 +562,16 @@ struct RowForm {
         const int row = mt * 16 + hf * 8 + at.g;
         if (row >= live) continue;
         if (at.c == 0) {
-          jm[row] = m[mt][hf];
-          jl[row] = sum * unit;
+          jm[row] = -ref[mt][hf];
+          jl[row] = sum;
         }
 #pragma unroll
         for (int i = 0; i < NT; i += 4)
 #pragma unroll
           for (int e = 0; e < 2; ++e)
             *reinterpret_cast<float4 *>(jo + row * SD + v_element<F, D>(2 * at.c + e, i)) =
-                make_float4(o[mt][i][2 * hf + e] * unit, o[mt][i + 1][2 * hf + e] * unit,
-                            o[mt][i + 2][2 * hf + e] * unit, o[mt][i + 3][2 * hf + e] * unit);
+                make_float4(o[mt][i][2 * hf + e], o[mt][i + 1][2 * hf + e],
+                            o[mt][i + 2][2 * hf + e], o[mt][i + 3][2 * hf + e]);
       }
   }
 };
@@ -598,7 +588,7 @@ struct ColForm {
   const W &at;
   uint32_t q[KS][2];  // of row g
   float rf[2], bias[2];
-  float m[2], thr[2], l[2];
+  float ref[2], l[2];
   float o[NT / 2][4];  // element v_element(g, 2 j + i / 2), row 2 c + i % 2
   float sc[2][4];      // key 16 mt + 8 (i / 2) + g, row 2 c + i % 2
 
@@ -615,22 +605,13 @@ struct ColForm {
     for (int e = 0; e < 2; ++e) {
       rf[e] = __shfl_sync(~0u, r, 4 * (2 * at.c + e));
       bias[e] = __shfl_sync(~0u, b, 4 * (2 * at.c + e));
-      m[e] = -FLT_MAX;
-      thr[e] = -INFINITY;
+      ref[e] = FLT_MAX;
       l[e] = 0.f;
     }
 #pragma unroll
     for (int j = 0; j < NT / 2; ++j)
 #pragma unroll
       for (int i = 0; i < 4; ++i) o[j][i] = 0.f;
-  }
-  __device__ __forceinline__ void rescale(float back) {
-    l[0] *= back;
-    l[1] *= back;
-#pragma unroll
-    for (int j = 0; j < NT / 2; ++j)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) o[j][i] *= back;
   }
   __device__ __forceinline__ void scores(const Magic &magic, const char *st) {
 #pragma unroll
@@ -671,34 +652,47 @@ struct ColForm {
   __device__ __forceinline__ float top_of(int e) const {
     return fmaxf(max3f(sc[0][e], sc[0][2 + e], sc[1][e]), sc[1][2 + e]);
   }
-  __device__ __forceinline__ void follow() {
-    if (!__any_sync(~0u, top_of(0) > thr[0] || top_of(1) > thr[1])) return;
+  __device__ __forceinline__ void follow(const float *kscale, float high) {
+    if (!__any_sync(~0u, fmaf(top_of(0), rf[0], ref[0]) > high ||
+                             fmaf(top_of(1), rf[1], ref[1]) > high))
+      return;
+    [[maybe_unused]] float lv[4];
+    if constexpr (!kBF) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) lv[i] = lg2(fabsf(kscale[kUnit + 8 * i + at.g]));
+    }
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      float top = top_of(e);
+      float score = top_of(e) * rf[e], weight = -INFINITY;
+      if constexpr (!kBF) {
 #pragma unroll
-      for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, x));
-      top = fmaxf(m[e], top * rf[e]);
-      const float back = exp2f(m[e] - top);
-      m[e] = top;
-      if (top > -FLT_MAX) thr[e] = (top + kRaise<F>) / rf[e];
-      l[e] *= back;
+        for (int i = 0; i < 4; ++i)
+          weight = fmaxf(weight, fmaf(sc[i / 2][2 * (i % 2) + e], rf[e], lv[i]));
+      }
+#pragma unroll
+      for (int x = 4; x < 32; x <<= 1) {
+        score = fmaxf(score, __shfl_xor_sync(~0u, score, x));
+        if constexpr (!kBF) weight = fmaxf(weight, __shfl_xor_sync(~0u, weight, x));
+      }
+      const float to = moved<F>(ref[e], score, weight);
+      const Back back(ref[e], to);
+      ref[e] = to;
+      l[e] = back(l[e]);
 #pragma unroll
       for (int j = 0; j < NT / 2; ++j) {
-        o[j][e] *= back;
-        o[j][2 + e] *= back;
+        o[j][e] = back(o[j][e]);
+        o[j][2 + e] = back(o[j][2 + e]);
       }
     }
   }
   template <bool MASKED>
-  __device__ __forceinline__ void weigh(const float *kscale, float lift) {
-    const float ref0 = lift - m[0], ref1 = lift - m[1];
+  __device__ __forceinline__ void weigh(const float *kscale) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       float &x = sc[i / 2][2 * (i % 2)], &y = sc[i / 2][2 * (i % 2) + 1];
       [[maybe_unused]] const bool sx = x != -INFINITY, sy = y != -INFINITY;
-      x = tc::ex2(fmaf(x, rf[0], ref0));
-      y = tc::ex2(fmaf(y, rf[1], ref1));
+      x = tc::ex2(fmaf(x, rf[0], ref[0]));
+      y = tc::ex2(fmaf(y, rf[1], ref[1]));
       add2(l[0], l[1], x, y);
       if constexpr (!kBF) {
         const float vs = kscale[kUnit + 8 * i + at.g];
@@ -763,8 +757,7 @@ struct ColForm {
     }
   }
   template <int SD>
-  __device__ __forceinline__ void leave(float *jo, float *jm, float *jl, int live, float vref) {
-    const float unit = kBF ? 1.f : vref;
+  __device__ __forceinline__ void leave(float *jo, float *jm, float *jl, int live) {
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       float sum = l[e];
@@ -773,14 +766,13 @@ struct ColForm {
       const int row = 2 * at.c + e;
       if (row >= live) continue;
       if (at.g == 0) {
-        jm[row] = m[e];
-        jl[row] = sum * unit;
+        jm[row] = -ref[e];
+        jl[row] = sum;
       }
 #pragma unroll
       for (int j = 0; j < NT / 2; j += 2)
         *reinterpret_cast<float4 *>(jo + row * SD + v_element<F, D>(at.g, 2 * j)) =
-            make_float4(o[j][e] * unit, o[j][2 + e] * unit, o[j + 1][e] * unit,
-                        o[j + 1][2 + e] * unit);
+            make_float4(o[j][e], o[j][2 + e], o[j + 1][e], o[j + 1][2 + e]);
     }
   }
 };
@@ -962,25 +954,14 @@ k12_tree_kernel(const __grid_constant__ TreeK k) {
     if (a.window)
       for (int r = 0; r < M; ++r) lead = max(lead, row_first[r] == INT_MAX ? 0 : row_first[r]);
 
-    float vref = kLeast;
-
     int stage = 0;
     for (int x = from + warp; x < to; x += W) {
       cp_async_wait<NS - 2>();
       __syncwarp();
       const char *st = ring + stage * C::kStage;
-      // the value scales' power of two, before anything waits for the products
       const float *kscale = reinterpret_cast<const float *>(st + 2 * C::kCodes);
-      if constexpr (!C::kBF) {
-        const float mine = kscale[kUnit + lane];
-        if (__any_sync(~0u, mine > vref && mine <= FLT_MAX)) {
-          const uint32_t top =
-              __reduce_max_sync(~0u, mine <= FLT_MAX ? __float_as_uint(fmaxf(mine, 0.f)) : 0u);
-          const float up = __uint_as_float((top + 0x7fffffu) & 0x7f800000u);
-          form.rescale(vref / up);
-          vref = up;
-        }
-      }
+      uint32_t top = 0;  // of the value scales, before anything waits for the products
+      if constexpr (!C::kBF) top = __reduce_max_sync(~0u, scale_bits(kscale[kUnit + lane]));
       const int key0 = s.first + x * kUnit;
       const bool whole = (whole_units >> stage & 1) && key0 + kUnit <= s.past && key0 >= lead;
 
@@ -993,11 +974,11 @@ k12_tree_kernel(const __grid_constant__ TreeK k) {
                         whole_units >> stage & 1
                             ? ~0u
                             : *reinterpret_cast<const uint32_t *>(st + 2 * C::kCodes + 8 * kUnit)});
-      form.follow();
+      form.follow(kscale, border<F>(top));
       if (C::kBF || whole)
-        form.template weigh<false>(kscale, lift_of<F>(vref));
+        form.template weigh<false>(kscale);
       else
-        form.template weigh<true>(kscale, lift_of<F>(vref));
+        form.template weigh<true>(kscale);
 
       const char *vs = st + C::kCodes;
       bool plain = true;
@@ -1030,19 +1011,19 @@ k12_tree_kernel(const __grid_constant__ TreeK k) {
     float *jo = reinterpret_cast<float *>(smem);  // [warp][M][SD]
     float *jm = jo + W * M * SD, *jl = jm + W * M;  // [warp][M]
     const int live = min(M, rows - rt * M);
-    form.template leave<SD>(jo + warp * M * SD, jm + warp * M, jl + warp * M, live, vref);
+    form.template leave<SD>(jo + warp * M * SD, jm + warp * M, jl + warp * M, live);
     __syncthreads();
     const bool alone = from == 0 && to == s.units;
     float *part = k.part + ((size_t)blockIdx.x * 2 + (from == 0)) * M * (D + 2);
-    if (tid < live) {  // a row: the warps' weights in place of their references
+    if (tid < live) {  // a row: the warps' factors in place of their references
       float top = jm[tid], sum = 0.f;
 #pragma unroll
       for (int w = 1; w < W; ++w) top = fmaxf(top, jm[w * M + tid]);
 #pragma unroll
       for (int w = 0; w < W; ++w) {
-        const float f = exp2f(jm[w * M + tid] - top);
+        const float f = root_of(jm[w * M + tid], top);
         jm[w * M + tid] = f;
-        sum += f * jl[w * M + tid];
+        sum += joined(f, jl[w * M + tid]);
       }
       if (!alone) {
         part[M * D + tid] = top;
@@ -1058,7 +1039,7 @@ k12_tree_kernel(const __grid_constant__ TreeK k) {
       for (int w = 0; w < W; ++w) {
         const float f = jm[w * M + r];
         const float4 y = *reinterpret_cast<const float4 *>(jo + (w * M + r) * SD + e);
-        x.x += f * y.x, x.y += f * y.y, x.z += f * y.z, x.w += f * y.w;
+        x.x += joined(f, y.x), x.y += joined(f, y.y), x.z += joined(f, y.z), x.w += joined(f, y.w);
       }
       if (alone)
         put_row<D>(k, b, h, row, e, x, jl[r]);
@@ -1115,9 +1096,9 @@ __global__ void __launch_bounds__(256) k12_join_kernel(const __grid_constant__ T
   float sum = 0.f;
   for (int i = lane; i < n; i += LANES) {
     const float *p = part(i);
-    const float f = exp2f(p[M * D + r] - top);
+    const float f = root_of(p[M * D + r], top);
     wt[i0][i] = f;
-    sum += f * p[M * D + M + r];
+    sum += joined(f, p[M * D + M + r]);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
@@ -1128,7 +1109,7 @@ __global__ void __launch_bounds__(256) k12_join_kernel(const __grid_constant__ T
   for (int i = lane / L; i < n; i += LANES / L) {
     const float4 y = *reinterpret_cast<const float4 *>(part(i) + r * D + lane % L * 4);
     const float f = wt[i0][i];
-    x.x += f * y.x, x.y += f * y.y, x.z += f * y.z, x.w += f * y.w;
+    x.x += joined(f, y.x), x.y += joined(f, y.y), x.z += joined(f, y.z), x.w += joined(f, y.w);
   }
   if constexpr (L == 16) {
     x.x += __shfl_xor_sync(~0u, x.x, 16);

@@ -16,13 +16,13 @@
 //     S = Q K^T a tile or two ahead of the rows, O += P V with P from TMEM.
 // The streams are joined through shared memory at the end of a segment.
 //
-// Scores, scales, references and probabilities are as in k12_tree.cu (q by a
-// power of two a row, fp16 probabilities up to 2^15, value scales relative to a
-// power of two that is part of the exponent here; bf16: the first 8 bits of a
-// probability and the next 8, two products).  Where a score passes its row's
-// reference by more than 8 (log2; bf16: 16), the reference is raised to it before the 32
-// columns are weighed: the row's sum, its O (between two products) and its
-// earlier probabilities of the tile are multiplied by the difference.
+// Scores, scales, references and weights are as in k12_tree.cu (q by a power of
+// two a row, weights in fp16; bf16: the first 8 bits of a probability and the
+// next 8, two products).  Where the largest score of 32 columns, with the largest of
+// their value scales, could take a weight past fp16's range, the row's reference is
+// moved by what the row sees before they are weighed: its sum, its O (between
+// two products) and its earlier weights of the tile are multiplied by the
+// difference.
 //
 // Tiles of 128 codes with heads of 64 (scores, probabilities and output fill a
 // stream's half of TMEM), else of 64 with the scores held twice and P written over
@@ -62,9 +62,9 @@ struct Wide {
   static constexpr int kQ = 128 * 128 * kCols;
   static constexpr int kMerge = 128 * (64 + 2) * 4;  // begins in place of q
   static constexpr int kRounds = D / 64;  // of handing it over
-  // scales, valid words and largest value scales of 32 keys each; bf16: 2 valid words, 2
-  // of odd values
-  static constexpr int kSide = kBF ? 16 : KT * 8 + KT / 4;
+  // key scales, value scales, their log2, valid words and borders of 32 keys each; bf16: 2
+  // valid words, 2 of odd values
+  static constexpr int kSide = kBF ? 16 : KT * 12 + KT / 4;
   static constexpr int kBars = 496;
   static constexpr int kRest = 1024 + kTile * (NK + NV) + kMerge + kSide * NV + kBars;
   static constexpr int kFit = kBF ? 0 : (226 * 1024 - kRest) / (kBF ? 1 : 4 * kRaw);
@@ -345,10 +345,10 @@ k13_tree_wide_kernel(const __grid_constant__ TreeK k, const __grid_constant__ Ma
         break;
       }
 
-      float m = -FLT_MAX, thr = -INFINITY, l0 = 0.f, l1 = 0.f, vref = kBF ? 1.f : kLeast;
+      float ref = FLT_MAX, l0 = 0.f, l1 = 0.f;
       bool begun = false;  // O holds something
-      // O *= by, once the last tile's product has ended (this one's has not begun)
-      auto rescale = [&](float by) -> bool {
+      // O to a new reference, once the last tile's product has ended (this one's has not begun)
+      auto rescale = [&](const Back &back) -> bool {
         if (jt > 0 && !wait(&bar.p_free[st][jt - 1 & 1], jt - 1 >> 1)) return false;
         tc::fence_after_sync();
 #pragma unroll 1
@@ -357,7 +357,7 @@ k13_tree_wide_kernel(const __grid_constant__ TreeK k, const __grid_constant__ Ma
           tc::tmem_ld16(tm + C::kO + c, o);
           tc::tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * by);
+          for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(back(__uint_as_float(o[i])));
           tc::tmem_st16(tm + C::kO + c, o);
         }
         tc::tmem_wait_st();
@@ -369,7 +369,7 @@ k13_tree_wide_kernel(const __grid_constant__ TreeK k, const __grid_constant__ Ma
         const uint32_t x2 = C::kTwice ? jt & 1 : 0, tile2 = C::kTwice ? jt >> 1 : jt;
         const uint32_t ts = tm + x2 * KT, tp = C::kTwice ? ts : tm + KT;  // S, P
         const float *ks = reinterpret_cast<const float *>(side + slot * C::kSide);
-        const uint32_t *valid = reinterpret_cast<const uint32_t *>(ks + (kBF ? 0 : 2 * KT));
+        const uint32_t *valid = reinterpret_cast<const uint32_t *>(ks + (kBF ? 0 : 3 * KT));
         const int key0 = w.s.first + (w.from + i) * KT;
         if (!(ok = wait(&bar.vfull[slot], x / NV))) break;
         const uint4 in = *reinterpret_cast<const uint4 *>(valid);
@@ -377,25 +377,6 @@ k13_tree_wide_kernel(const __grid_constant__ TreeK k, const __grid_constant__ Ma
         tc::fence_after_sync();
         const bool whole = (KT == 128 ? in.x & in.y & in.z & in.w : in.x & in.y) == ~0u &&
                            __all_sync(~0u, key0 + KT <= w.s.past && key0 >= first);
-        float lift = 0.f;
-        if constexpr (!kBF) {
-          float top_v = fmaxf(__uint_as_float(in.z), __uint_as_float(in.w));
-          if constexpr (KT == 128) {
-            const float4 tops = *reinterpret_cast<const float4 *>(valid + 4);
-            top_v = fmaxf(fmaxf(tops.x, tops.y), fmaxf(tops.z, tops.w));
-          }
-          if (top_v > vref) {  // the same for all rows
-            const float up =
-                __uint_as_float((__float_as_uint(top_v) + 0x7fffffu) & 0x7f800000u);
-            const float back = vref / up;
-            if (begun && !(ok = rescale(back))) break;
-            l0 *= back;
-            l1 *= back;
-            vref = up;
-          }
-          lift = 15.f - kRaise<F> - (float)((int)(__float_as_uint(vref) >> 23) - 127);
-        }
-
         // The columns, 32 at a time.
         auto weigh = [&](int c0, auto masked) {
           uint32_t u[32];
@@ -444,19 +425,28 @@ k13_tree_wide_kernel(const __grid_constant__ TreeK k, const __grid_constant__ Ma
             if (j + 2 < 32) t1 = max3f(t1, y[j + 2], y[j + 3]);
           }
           t0 = fmaxf(t0, t1);
-          if (__any_sync(~0u, t0 > thr)) {  // raise the rows' references
-            // by a whole number, so that the factor is a power of two: exact for the
-            // fp16 probabilities that are made already
-            const float by_log2 = ceilf(fmaxf(t0 * rf - m, 0.f));
-            const bool none = m == -FLT_MAX;  // the row has seen no key
-            const float back = none ? 0.f : exp2f(-by_log2);
-            m = none ? fmaxf(t0 * rf, -FLT_MAX) : m + by_log2;
-            if (m > -FLT_MAX) thr = (m + kRaise<F>) / rf;
-            l0 *= back;
-            l1 *= back;
-            if (begun) ok = rescale(back);
+          const float high =
+              kBF ? Range<F>::kHigh : __uint_as_float(valid[KT / 32 + c0 / 32]);
+          if (__any_sync(~0u, fmaf(t0, rf, ref) > high)) {  // move the rows' references
+            float weight = -INFINITY;
+            if constexpr (!kBF) {
+#pragma unroll
+              for (int j = 0; j < 32; j += 4) {
+                const float4 lv = *reinterpret_cast<const float4 *>(ks + 2 * KT + c0 + j);
+                weight = max3f(weight, fmaf(y[j], rf, lv.x), fmaf(y[j + 1], rf, lv.y));
+                weight = max3f(weight, fmaf(y[j + 2], rf, lv.z), fmaf(y[j + 3], rf, lv.w));
+              }
+            }
+            const float to = moved<F>(ref, t0 * rf, weight);
+            const Back back(ref, to);
+            // (none moves where the large values of a tile are hidden from all rows)
+            const bool some = __any_sync(~0u, to != ref);
+            ref = to;
+            l0 = back(l0);
+            l1 = back(l1);
+            if (some && begun) ok = rescale(back);
 #pragma unroll 1
-            for (int c = 0; c < (C::kTwice ? c0 : c0 / 2);
+            for (int c = 0; some && c < (C::kTwice ? c0 : c0 / 2);
                  c += C::kTwice && !kBF && c % 32 ? 24 : 8) {  // this tile's earlier columns
               uint32_t z[8];
               tc::tmem_wait_st();
@@ -465,16 +455,15 @@ k13_tree_wide_kernel(const __grid_constant__ TreeK k, const __grid_constant__ Ma
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
                 if constexpr (kBF) {
-                  z[i] = pack_bf16(bf16_lo(z[i]) * back, bf16_hi(z[i]) * back);
+                  z[i] = pack_bf16(back(bf16_lo(z[i])), back(bf16_hi(z[i])));
                 } else {
                   const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&z[i]));
-                  z[i] = pack_f16(f.x * back, f.y * back);
+                  z[i] = pack_f16(back(f.x), back(f.y));
                 }
               }
               tc::tmem_st8(tp + c, z);
             }
           }
-          const float ref = lift - m;
 #pragma unroll
           for (int j = 0; j < 32; j += 2) fma2(y[j], y[j + 1], y[j], y[j + 1], rf, ref);
 #pragma unroll
@@ -583,11 +572,11 @@ k13_tree_wide_kernel(const __grid_constant__ TreeK k, const __grid_constant__ Ma
         if (!(ok = wait(&bar.p_free[st][jt - 1 & 1], jt - 1 >> 1))) break;
         tc::fence_after_sync();
       }
-      const float l = (l0 + l1) * vref;
+      const float l = l0 + l1;
       if (st == 1) {
         // (it goes where q lies: the first stream's scores must be done as well)
         if (!(ok = wait(&bar.done, seg))) break;
-        mm[row] = m;
+        mm[row] = -ref;
         ml[row] = l;
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
@@ -599,7 +588,7 @@ k13_tree_wide_kernel(const __grid_constant__ TreeK k, const __grid_constant__ Ma
           }
 #pragma unroll
           for (int i = 0; i < 32; ++i)
-            mo[(c % 64 + i) * 128 + row] = begun ? __uint_as_float(o[i]) * vref : 0.f;
+            mo[(c % 64 + i) * 128 + row] = begun ? __uint_as_float(o[i]) : 0.f;
           if (c % 64) tc::mbar_arrive(&bar.merge);
         }
         if (!ok) break;
@@ -614,10 +603,10 @@ k13_tree_wide_kernel(const __grid_constant__ TreeK k, const __grid_constant__ Ma
           if (c % 64 == 0) {
             if (!(ok = wait(&bar.merge, seg * C::kRounds + c / 64))) break;
             if (c == 0) {
-              const float m1 = mm[row], top = fmaxf(m, m1), f0 = exp2f(m - top);
-              other = exp2f(m1 - top);
-              const float sum = f0 * l + other * ml[row];
-              unit = f0 * vref;
+              const float m1 = mm[row], top = fmaxf(-ref, m1);
+              unit = root_of(-ref, top);
+              other = root_of(m1, top);
+              const float sum = joined(unit, l) + joined(other, ml[row]);
               inv = sum == 0.f ? 0.f : 1.f / sum;
               if (live && !alone) {
                 part[128 * D + row] = top;
@@ -631,8 +620,8 @@ k13_tree_wide_kernel(const __grid_constant__ TreeK k, const __grid_constant__ Ma
           float y[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i)
-            y[element_of<F>(i)] =
-                __uint_as_float(o[i]) * unit + mo[(c % 64 + i) * 128 + row] * other;
+            y[element_of<F>(i)] = joined(unit, __uint_as_float(o[i])) +
+                                  joined(other, mo[(c % 64 + i) * 128 + row]);
           if (c % 64) tc::mbar_arrive(&bar.merged);
           if (live && alone) {
             uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + at + c);
@@ -889,19 +878,19 @@ k13_tree_wide_kernel(const __grid_constant__ TreeK k, const __grid_constant__ Ma
             }
             if (part) {
               float *sd = reinterpret_cast<float *>(side + place * C::kSide) + row0;
-              uint32_t *valid = reinterpret_cast<uint32_t *>(sd - row0 + 2 * KT) + row0 / 32;
+              uint32_t *valid = reinterpret_cast<uint32_t *>(sd - row0 + 3 * KT) + row0 / 32;
 #pragma unroll
               for (int y = 0; y < KW; y += 32) {
                 const float2 sc =
                     *reinterpret_cast<const float2 *>(src + C::kRawScale + (y + lane) * 8);
-                const uint32_t top = __reduce_max_sync(
-                    ~0u, sc.y <= FLT_MAX ? __float_as_uint(fmaxf(sc.y, 0.f)) : 0u);
+                const uint32_t top = __reduce_max_sync(~0u, scale_bits(sc.y));
                 sd[y + lane] = sc.x;
                 sd[KT + y + lane] = sc.y;
+                sd[2 * KT + y + lane] = lg2(fabsf(sc.y));
                 if (lane == 0) {
                   valid[y / 32] =
                       *reinterpret_cast<const uint32_t *>(src + C::kRawScale + KW * 8 + y / 8);
-                  valid[KT / 32 + y / 32] = top;
+                  valid[KT / 32 + y / 32] = __float_as_uint(border<F>(top));
                 }
               }
             }

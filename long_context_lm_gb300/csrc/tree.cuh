@@ -13,18 +13,77 @@
 namespace fs {
 
 constexpr float kLog2e = 1.4426950408889634f;
-// How far a score may pass its row's reference (log2).  Raising one costs the wide
-// kernel a pass over its O: 4, 8 and 12 are 166, 154 and 149 us for 64 tokens x 32
-// heads over 16384 int8 keys.  8 leaves a row's largest fp16 probability at 2^7 or
-// more, 2^31 times the step of the smallest ones; bf16 ones are relative, and take 16.
+
+// ---------------------------------------------------------------------------
+// references
+// ---------------------------------------------------------------------------
+// A row's probabilities are p = 2^(score + ref), scores in log2 units; its weights,
+// which go into the product with the values, are p, or p times the value's scale where
+// values are codes.  Sum and output are relative to the row's own reference, which what
+// other rows see cannot move.  FLT_MAX: the row has seen no key.  A reference moves when a
+// key that the row sees passes kHigh, and by so much that the largest is at kLow:
+//   bf16   p alone; its parts are bf16 numbers, so any range would do: 2^-46 to 2^-30
+//          leaves room for 2^30 keys of the largest values.
+//   codes  weights go to fp16, whose largest number is below 2^16; the row's largest stays
+//          at 2^7 or more, 2^31 times the step of the smallest ones.  A second border, on p,
+//          keeps the sums of 2^30 keys within fp32 where values are tiny or zero (it
+//          costs weights bits where the largest value scale is below 2^-78, and p loses keys
+//          2^-20 of the largest, below 2^-126, where that scale is above 2^113).
+// Moving one costs the tcgen05 kernel a pass over its O.
 template <int F>
-constexpr float kRaise = F == FS_CACHE_BF16 ? 16.f : 8.f;
+struct Range {
+  static constexpr bool kBF = F == FS_CACHE_BF16;
+  static constexpr float kLow = kBF ? -46.f : 8.f, kHigh = kBF ? -30.f : 15.99f;
+  static constexpr float kSumLow = 85.f, kSumHigh = 93.f;
+};
 
-// The least power of two that the value scales are relative to.  Probabilities
-// are made 1 / vref times as large (the products with the scales then need no
-// second factor), and stay within fp32 with their sum.
-constexpr float kLeast = 0x1p-90f;
-
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+// Bits of a value scale's magnitude, 0 for one that is not a number (its row's values are
+// not either).
+__device__ __forceinline__ uint32_t scale_bits(float x) {
+  return fabsf(x) <= FLT_MAX ? __float_as_uint(fabsf(x)) : 0u;
+}
+// What a row's largest score plus reference may be, over keys whose value scales are at
+// most the number with the bits `top`: below it no weight and no p passes its border.
+template <int F>
+__device__ __forceinline__ float border(uint32_t top) {
+  using R = Range<F>;
+  if constexpr (R::kBF) return R::kHigh;
+  return R::kHigh - fmaxf(lg2(__uint_as_float(top)), R::kHigh - R::kSumHigh);
+}
+// A row's reference for keys whose largest score is `score`, and whose largest score plus
+// log2 of the value scale is `weight` (codes), where some row of the warp has passed its border.
+// It moves by whole numbers, so that what is there is multiplied by a power of two, and
+// wherever the largest is above kLow: the warp pays for all its rows or none.
+template <int F>
+__device__ __forceinline__ float moved(float ref, float score, [[maybe_unused]] float weight) {
+  using R = Range<F>;
+  if (score == -INFINITY) return ref;  // none that the row sees
+  if (ref == FLT_MAX)
+    return R::kBF ? R::kLow - score : fminf(R::kLow - weight, R::kSumLow - score);
+  if constexpr (R::kBF) return ref - ceilf(fmaxf(score + ref - R::kLow, 0.f));
+  return ref - ceilf(fmaxf(fmaxf(weight + ref - R::kLow, score + ref - R::kSumLow), 0.f));
+}
+// 2^(to - from) as two factors: from the smallest values to the largest it is below 2^-149,
+// while sums that it multiplies stay far above.  (The difference of two references is a
+// whole number but for the last one's rounding.)
+struct Back {
+  float a, b;
+  __device__ __forceinline__ Back(float from, float to) {
+    const int n = __float2int_rn(fmaxf(to - from, -252.f)), h = n >> 1;
+    a = __uint_as_float((uint32_t)(127 + h) << 23);
+    b = __uint_as_float((uint32_t)(127 + n - h) << 23);
+  }
+  __device__ __forceinline__ float operator()(float x) const { return x * a * b; }
+};
+// Results with references -m are joined at the largest m of them: a factor of 2^(m - most),
+// applied as its square root twice, for the same reason.
+__device__ __forceinline__ float root_of(float m, float most) { return exp2f(0.5f * (m - most)); }
+__device__ __forceinline__ float joined(float root, float x) { return root * x * root; }
 // ---------------------------------------------------------------------------
 // the line of units
 // ---------------------------------------------------------------------------
