@@ -614,6 +614,14 @@ int fs_tree_attn(const void *q, const fs_cache *cache, const int32_t *past,
                  const int32_t *count, const int64_t *tree, int H, int T,
                  int window, float scale, void *out, void *ws,
                  size_t ws_bytes, void *stream);
+/* The same call with another limit for its waits, 1 .. 4e9 SM cycles (the last
+ * is fs_tree_attn's): a test makes them give up.  The call then ends as it does
+ * after a stalled pipeline stage, with FS_ERR_TIMEOUT in the cache's status. */
+int fs_selftest_tree_wait(const void *q, const fs_cache *cache,
+                          const int32_t *past, const int32_t *count,
+                          const int64_t *tree, int H, int T, int window,
+                          float scale, void *out, void *ws, size_t ws_bytes,
+                          long long cycles, void *stream);
 
 #ifdef __cplusplus
 }

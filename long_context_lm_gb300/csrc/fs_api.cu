@@ -996,9 +996,10 @@ extern "C" size_t fs_tree_workspace_bytes(const fs_cache *cache, int H, int T) {
   return check_tree(cache, H, T) == FS_OK ? tree_workspace_bytes(*cache, H, T) : 0;
 }
 
-extern "C" int fs_tree_attn(const void *q, const fs_cache *cache, const int32_t *past,
-                            const int32_t *count, const int64_t *tree, int H, int T, int window,
-                            float scale, void *out, void *ws, size_t ws_bytes, void *stream) {
+namespace {
+int tree_attn(const void *q, const fs_cache *cache, const int32_t *past, const int32_t *count,
+              const int64_t *tree, int H, int T, int window, float scale, void *out, void *ws,
+              size_t ws_bytes, long long wait_cycles, void *stream) {
   FS_TRY(check_cache_memory(cache));
   FS_TRY(check_tree(cache, H, T));
   if (!q || !past || !out || !ws || !(scale > 0.f) || !(scale <= 1e30f)) return FS_ERR_INVALID_ARG;
@@ -1023,7 +1024,25 @@ extern "C" int fs_tree_attn(const void *q, const fs_cache *cache, const int32_t 
   a.scale = scale;
   a.out = out;
   a.ws = ws;
+  a.wait_cycles = wait_cycles;
   return status_of(launch_tree(a, static_cast<cudaStream_t>(stream)));
+}
+}  // namespace
+
+extern "C" int fs_tree_attn(const void *q, const fs_cache *cache, const int32_t *past,
+                            const int32_t *count, const int64_t *tree, int H, int T, int window,
+                            float scale, void *out, void *ws, size_t ws_bytes, void *stream) {
+  return tree_attn(q, cache, past, count, tree, H, T, window, scale, out, ws, ws_bytes,
+                   tc::kWaitCycles, stream);
+}
+
+extern "C" int fs_selftest_tree_wait(const void *q, const fs_cache *cache, const int32_t *past,
+                                     const int32_t *count, const int64_t *tree, int H, int T,
+                                     int window, float scale, void *out, void *ws, size_t ws_bytes,
+                                     long long cycles, void *stream) {
+  if (cycles < 1 || cycles > tc::kWaitCycles) return FS_ERR_INVALID_ARG;
+  return tree_attn(q, cache, past, count, tree, H, T, window, scale, out, ws, ws_bytes, cycles,
+                   stream);
 }
 
 namespace fs {

@@ -178,6 +178,7 @@ struct TreeArgs {
   int H, T, window;
   float scale;
   void *out, *ws;
+  long long wait_cycles;  // after which a wait gives up
 };
 size_t tree_workspace_bytes(const fs_cache &c, int H, int T);
 cudaError_t launch_tree(const TreeArgs &a, cudaStream_t st);

@@ -95,22 +95,22 @@ __device__ __forceinline__ constexpr int element_of(int i) {
 // tc::mbar_wait with a hint of how long the thread may sleep in a try: nearly
 // all of these waits are long, and their polls would take issue slots from the
 // rows' warps.
-__device__ __forceinline__ bool wait_asleep(uint64_t *bar, uint32_t parity, int *fail) {
+__device__ __forceinline__ bool wait_asleep(uint64_t *bar, uint32_t parity, int *fail,
+                                            long long cycles) {
   if (tc::mbar_try_wait(bar, parity)) return true;  // (reading the clock takes as long)
   const long long t0 = clock64();
-  for (uint32_t i = 1;; ++i) {
+  const uint32_t ns = (uint32_t)min(cycles, 1000000ll);
+  while (true) {
     uint32_t ok;
     asm volatile(
         "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
         " selp.u32 %0, 1, 0, p;\n}\n"
         : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity), "r"(1000000u)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(ns)
         : "memory");
     if (ok) return true;
-    if ((i & 15u) == 0) {
-      if (clock64() - t0 > tc::kWaitCycles) break;
-      if (*reinterpret_cast<volatile int *>(fail) != 0) return false;
-    }
+    if (clock64() - t0 > cycles) break;
+    if (*reinterpret_cast<volatile int *>(fail) != 0) return false;
   }
   tc::report_error(fail, FS_ERR_TIMEOUT);
   return false;
@@ -150,6 +150,7 @@ struct Bars {
   uint64_t p_full[2][2], p_free[2][2];
   uint64_t added[2];                    // values that are not finite were (bf16)
   uint64_t q_full, done, merge, merged;  // of a segment
+  uint64_t drained[2];                  // a stream's products, when a wait has given up
 };
 
 // Sixteen bytes of codes -> fp16, eight elements to a 16-byte chunk.
@@ -215,6 +216,12 @@ k13_tree_wide_kernel(const __grid_constant__ TreeK k, const __grid_constant__ Ma
   [[maybe_unused]] char *raw = side + NV * C::kSide + C::kBars;
   __shared__ uint32_t tmem_base;
   __shared__ int fail;
+  // What a TMA warp has issued: the tile after its last one, the places whose last tile goes
+  // by `landed`, and the phases of those.
+  struct Issued {
+    uint32_t next, looked, landed;
+  };
+  __shared__ Issued issued[4];
   const TreeArgs &a = k.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   asm volatile("griddepcontrol.launch_dependents;");
@@ -246,6 +253,7 @@ k13_tree_wide_kernel(const __grid_constant__ TreeK k, const __grid_constant__ Ma
       tc::mbar_init(&bar.p_full[i][0], 128);
       tc::mbar_init(&bar.p_full[i][1], 128);
       tc::mbar_init(&bar.added[i], 128);
+      tc::mbar_init(&bar.drained[i], 1);
       tc::mbar_init(&bar.p_free[i][0], 1);
       tc::mbar_init(&bar.p_free[i][1], 1);
     }
@@ -267,8 +275,11 @@ k13_tree_wide_kernel(const __grid_constant__ TreeK k, const __grid_constant__ Ma
 
   Walk w{share.begin(blockIdx.x), share.begin(blockIdx.x + 1), line.begin, line.b, line.s, 0, 0, 0, 0};
   // Waits give up after a limit and say so in `fail`; every role then leaves its
-  // loops for the barrier at the end.
-  auto wait_one = [&](uint64_t *b, uint32_t phase) { return wait_asleep(b, phase & 1, &fail); };
+  // loops for the barrier at the end, behind which the copies and products that are
+  // still under way are waited for.
+  auto wait_one = [&](uint64_t *b, uint32_t phase) {
+    return wait_asleep(b, phase & 1, &fail, a.wait_cycles);
+  };
   auto wait = [&](uint64_t *b, uint32_t phase) {  // the same answer in a warp
     return (bool)__all_sync(~0u, wait_one(b, phase));
   };
@@ -644,6 +655,8 @@ k13_tree_wide_kernel(const __grid_constant__ TreeK k, const __grid_constant__ Ma
       }
       it += n;
     }
+    tc::tmem_wait_st();  // (where a wait has given up between a store and its own)
+    tc::fence_before_sync();
   } else if (warp < 12 || warp >= 14) {
     // Where the tiles lie: lane l holds sixteen rows, group l % GP of the (l / GP)th of
     // the warp's next 32 / GP tiles, as their place among all groups of sixteen rows
@@ -678,6 +691,7 @@ k13_tree_wide_kernel(const __grid_constant__ TreeK k, const __grid_constant__ Ma
       const bool look_only = warp >= 14, values = warp >= 10;
       const int box = min(groups, 4);      // groups of sixteen rows that come in one copy
       uint32_t looked = 0, landed = 0;     // places whose tile goes by `landed`, and its phases
+      uint32_t next = mine;                // the tile after the last that was issued
       while (ok && w.next(k)) {
         n = w.to - w.from;
         const int lead = a.window ? w.s.past + w.s.n - a.window : 0;  // no row begins later
@@ -698,17 +712,9 @@ k13_tree_wide_kernel(const __grid_constant__ TreeK k, const __grid_constant__ Ma
             }
             const uint32_t turn = values ? t / NV : t / NK;
             if (turn > 0 &&
-                !(ok = wait(values ? &bar.vempty[slot] : &bar.kempty[slot], turn - 1))) {
-              // no copy may be under way when the block ends
-              const uint32_t held = values ? NV : NK;
-              for (uint32_t x = t - held; x < t; x += 2)
-                if (looked >> x % held & 1)
-                  tc::mbar_wait(&bar.landed[x % held], ~landed >> x % held & 1, nullptr);
-                else
-                  tc::mbar_wait(values ? &bar.vfull[x % held] : &bar.kfull[x % held],
-                                x / held & 1, nullptr);
+                !(ok = wait(values ? &bar.vempty[slot] : &bar.kempty[slot], turn - 1)))
               break;
-            }
+            next = t + 2;
             const uint32_t have = __ballot_sync(~0u, place != kNone) >> (at * GP);
             uint64_t *to = values ? &bar.vfull[slot] : &bar.kfull[slot];
             if (values) {
@@ -768,6 +774,7 @@ k13_tree_wide_kernel(const __grid_constant__ TreeK k, const __grid_constant__ Ma
         }
         it += n;
       }
+      if (!look_only && lane == 0) issued[warp - 8] = {next, looked, landed};
     } else {
       // ------------------------------------------------ codes -> fp16 tiles (warps 8-11)
       // A lane's pieces lie in rows row0 + lane / P + j (32 / P) of the tile, keys and
@@ -966,7 +973,27 @@ k13_tree_wide_kernel(const __grid_constant__ TreeK k, const __grid_constant__ Ma
     }
   }
   __syncthreads();
-  if (tid == 0 && fail && a.c.status) tc::report_error(a.c.status, FS_ERR_TIMEOUT);
+  if (fail) {  // nothing may write to shared memory or read TMEM when they are given back
+    if constexpr (kBF) {
+      if (warp >= 8 && warp < 12 && lane == 0) {
+        const Issued s = issued[warp - 8];
+        const bool values = warp >= 10;
+        const uint32_t held = values ? NV : NK;
+        for (uint32_t x = s.next > held ? s.next - held : warp & 1; x < s.next; x += 2)
+          if (s.looked >> x % held & 1)
+            tc::mbar_wait(&bar.landed[x % held], ~s.landed >> x % held & 1, nullptr);
+          else
+            tc::mbar_wait(values ? &bar.vfull[x % held] : &bar.kfull[x % held], x / held & 1,
+                          nullptr);
+      }
+    }
+    if ((warp == 12 || warp == 13) && lane == 0) {
+      tc::mma_commit(&bar.drained[warp - 12]);
+      tc::mbar_wait(&bar.drained[warp - 12], 0, nullptr);
+    }
+    __syncthreads();
+    if (tid == 0 && a.c.status) tc::report_error(a.c.status, FS_ERR_TIMEOUT);
+  }
   __syncwarp();
   if (warp == 12) tc::tmem_dealloc(tmem_base, 512);
 }

@@ -37,7 +37,8 @@ SYMBOLS = ["fs_default_params", "fs_status_string", "fs_last_cuda_error", "fs_wo
            "fs_backward_workspace_bytes", "fs_attention_bwd",
            "fs_fsb_workspace_bytes", "fs_fsb_select",
            "fs_rope_make_plan", "fs_rope", "fs_cache_row_bytes", "fs_cache_append",
-           "fs_cache_read", "fs_cache_accept", "fs_tree_workspace_bytes", "fs_tree_attn"]
+           "fs_cache_read", "fs_cache_accept", "fs_tree_workspace_bytes", "fs_tree_attn",
+           "fs_selftest_tree_wait"]
 FS_ROPE_LAYOUTS = {"half": 0, "pairs": 1}
 FS_ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "ramp": 3}
 FS_CACHE_FORMATS = {"bf16": 0, "e4m3": 1, "int8": 2, "int4": 3}
@@ -162,6 +163,8 @@ def load(build_if_stale: bool = True):
         L.fs_tree_workspace_bytes.argtypes = [PC, I, I]
         L.fs_tree_workspace_bytes.restype = Z
         L.fs_tree_attn.argtypes = [P, PC, P, P, P, I, I, I, F, P, P, Z, P]
+        L.fs_selftest_tree_wait.argtypes = [P, PC, P, P, P, I, I, I, F, P, P, Z,
+                                            ctypes.c_longlong, P]
         for name in SYMBOLS:
             if name not in ("fs_cache_row_bytes", "fs_tree_workspace_bytes",
                             "fs_default_params", "fs_status_string", "fs_last_cuda_error",
@@ -921,7 +924,19 @@ def fs_tree_attn(q, cache, past, tree=None, count=None, window=0, scale=None, ou
     ``count`` [batch]: drafted tokens of each sequence (None: T); ``window`` 0 or >= 64 last
     positions; ``scale`` default d ** -0.5.  Returns out [batch, H, T, d] bf16; rows past count[b]
     are left as they were (a new ``out`` starts as zeros when ``count`` is given)."""
-    L = _lib or load()
+    return _tree_attn((_lib or load()).fs_tree_attn, "fs_tree_attn", (), q, cache, past, tree, count,
+                      window, scale, out, ws, stream)
+
+
+def fs_selftest_tree_wait(q, cache, past, cycles, tree=None, count=None, window=0, scale=None,
+                          out=None, ws=None, stream=None):
+    """fs_tree_attn whose waits give up after ``cycles`` SM cycles (FS_ERR_TIMEOUT in
+    ``cache.status``)."""
+    return _tree_attn((_lib or load()).fs_selftest_tree_wait, "fs_selftest_tree_wait", (int(cycles),),
+                      q, cache, past, tree, count, window, scale, out, ws, stream)
+
+
+def _tree_attn(fn, where, more, q, cache, past, tree, count, window, scale, out, ws, stream):
     dev = cache.device
     if not isinstance(q, torch.Tensor) or q.dim() != 4:
         raise ValueError("q must be [batch, H, T, d]")
@@ -936,7 +951,7 @@ def fs_tree_attn(q, cache, past, tree=None, count=None, window=0, scale=None, ou
     if ws is None:
         ws = _new(stream, lambda: fs_tree_workspace(cache, B, H, T))
     wp = _on(ws, dev, "ws", torch.uint8)
-    _launch(dev, stream, L.fs_tree_attn, "fs_tree_attn", qp, cache.desc,
-            _counts(cache, "past", past), _counts(cache, "count", count), tp, H, T, int(window),
-            d ** -0.5 if scale is None else float(scale), op, wp, ws.numel())
+    _launch(dev, stream, fn, where, qp, cache.desc, _counts(cache, "past", past),
+            _counts(cache, "count", count), tp, H, T, int(window),
+            d ** -0.5 if scale is None else float(scale), op, wp, ws.numel(), *more)
     return out

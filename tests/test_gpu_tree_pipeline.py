@@ -57,3 +57,31 @@ def test_many_short_segments(past, fmt, d):
         fs.fs_tree_attn(q, cache, at, out=again, ws=ws)
         assert torch.equal(out, again)
     fs.fs_check_status(cache.status)
+
+
+@pytest.mark.parametrize("fmt,d", [("bf16", 64), ("bf16", 128), ("int8", 64), ("e4m3", 128), ("int4", 64)])
+def test_waits_that_give_up(fmt, d):
+    # The limit runs out in other places each time, with copies and products under way; the call ends
+    # with a status, and the next one is right.  64 x 4 rows: the many-row kernel.
+    past = [5000, 300, 0, 1900]
+    cache, q, at = _short(fmt, d, past, Hkv=4, G=4, T=64, seed=d)
+    # values that are not finite, so that the rows, too, wait for products
+    bad = torch.full((4, 4, 1, d), float("inf"), device="cuda").bfloat16()
+    fs.fs_cache_append(cache, bad, bad, _ints([4990, 290, 0, 1950]))
+    want = fs.fs_tree_attn(q, cache, at)
+    fs.fs_check_status(cache.status)
+    ws, gave_up = fs.fs_tree_workspace(cache, 4, 16, 64), 0
+    for cycles in (1, 100, 300, 1000, 2000, 4000, 8000, 16000, 32000, 64000, 10 ** 9):
+        out = torch.empty_like(q)
+        fs.fs_selftest_tree_wait(q, cache, at, cycles, out=out, ws=ws)
+        torch.cuda.synchronize()
+        status = int(cache.status[0])
+        assert status in (0, fs.FS_ERR_TIMEOUT)
+        gave_up += status != 0
+        if status == 0:
+            assert torch.equal(out.view(torch.int16), want.view(torch.int16))
+        cache.status.zero_()
+        again = fs.fs_tree_attn(q, cache, at, ws=ws)
+        fs.fs_check_status(cache.status)
+        assert torch.equal(again.view(torch.int16), want.view(torch.int16))
+    assert gave_up > 0 and status == 0
