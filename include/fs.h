@@ -461,8 +461,9 @@ int fs_workspace_view(int batch, int H, int N, int d, const fs_params *p,
  *                   beta_slow turns in `original` tokens,
  *                   lo = floor, hi = ceil of r ln(original / (2 pi beta)) /
  *                   (2 ln base), kept within 0 .. r/2 - 1
- * m is `amplitude`.  Angles are exact for every 32-bit position: pos * f_i is
- * taken modulo one turn in 64-bit fixed point. */
+ * m is `amplitude`.  pos * f_i is taken modulo one turn in 64-bit fixed point,
+ * so that a far position costs nothing; sines and cosines are fp32 numbers,
+ * within 2^-23 of those of the exact angle. */
 typedef enum { FS_ROPE_HALF = 0, FS_ROPE_PAIRS = 1 } fs_rope_layout;
 typedef enum {
   FS_ROPE_PLAIN = 0,

@@ -4,9 +4,11 @@
 // Pair i of a token at position p turns by the angle p f_i.  The plan holds
 // f_i / 2 pi as a fraction F_i of 2^64, so p F_i modulo 2^64 is the fraction of
 // a turn, exact for every 32-bit p apart from F_i's own last bit (2^-53
-// relative, as a double holds f_i): no fp64 arithmetic and no argument
-// reduction.  Its upper 32 bits, as a signed number of half turns, go to
-// sincospif (error below 2^-31 of a half turn).
+// relative, as a double holds f_i): no fp64 arithmetic.  The nearest quarter turn is
+// taken off in whole numbers; 32 bits of what is left, an eighth of a turn at most
+// either way and cut to 2^-34 of one, become a float (half a step: 2^-27 of a half
+// turn) and go to sincospif.  Converted without that, angles near a half turn are off by
+// four times as much.
 //
 // Bound by memory: 4 bytes per bf16 element against a handful of operations.  A
 // thread takes V pairs of one token (two 16-byte pieces of a row), works out
@@ -80,9 +82,14 @@ __global__ void __launch_bounds__(256) k10_rope_kernel(const __grid_constant__ R
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const uint64_t t = (uint64_t)(int64_t)p * a.plan.turns[item * V + i];
-      sincospif((float)(int32_t)(t >> 32) * 0x1p-31f, &s[i], &c[i]);
-      c[i] *= a.plan.amplitude;
-      s[i] *= a.inverse ? -a.plan.amplitude : a.plan.amplitude;
+      const uint32_t hi = (uint32_t)(t >> 32), quarter = (hi + (1u << 29)) >> 30;
+      const int32_t left = (int32_t)__funnelshift_l((uint32_t)t, hi - (quarter << 30), 2);
+      float sn, cs;
+      sincospif((float)left * 0x1p-33f, &sn, &cs);
+      c[i] = quarter & 1 ? sn : cs;
+      s[i] = quarter & 1 ? cs : sn;
+      c[i] *= (quarter + 1) & 2 ? -a.plan.amplitude : a.plan.amplitude;
+      s[i] *= (quarter >> 1) ^ (uint32_t)a.inverse ? -a.plan.amplitude : a.plan.amplitude;
     }
   }
   const int h0 = blockIdx.y * a.per, h1 = min(h0 + a.per, a.H[0] + a.H[1]);
