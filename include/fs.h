@@ -460,7 +460,9 @@ int fs_workspace_view(int batch, int H, int N, int d, const fs_params *p,
  *                   to 1 over i = lo .. hi: the pairs that make beta_fast and
  *                   beta_slow turns in `original` tokens,
  *                   lo = floor, hi = ceil of r ln(original / (2 pi beta)) /
- *                   (2 ln base), kept within 0 .. r/2 - 1
+ *                   (2 ln base), lo at least 0 and hi at most r - 1, as in the
+ *                   published method (YaRN): where hi lies beyond the last pair,
+ *                   r/2 - 1, no pair is slowed by the whole factor
  * m is `amplitude`.  pos * f_i is taken modulo one turn in 64-bit fixed point,
  * so that a far position costs nothing; sines and cosines are fp32 numbers,
  * within 2^-23 of those of the exact angle. */

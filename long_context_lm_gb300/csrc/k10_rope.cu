@@ -204,7 +204,7 @@ int rope_make_plan(const fs_rope_params &p, fs_rope_plan *plan) {
     lo = floor(r * log(p.original / (2.0 * pi * p.beta_fast)) / (2.0 * log(base)));
     hi = ceil(r * log(p.original / (2.0 * pi * p.beta_slow)) / (2.0 * log(base)));
     lo = lo < 0.0 ? 0.0 : lo;
-    hi = hi > r / 2 - 1 ? r / 2 - 1 : hi;
+    hi = hi > r - 1 ? r - 1 : hi;  // (of the elements: beyond the last pair)
   }
   fs_rope_plan out{};
   out.rot = p.rot;
