@@ -562,7 +562,8 @@ typedef struct {
 /* Bytes of one row's codes; 0 for a d or format that the cache does not have. */
 size_t fs_cache_row_bytes(int d, int format);
 
-/* Writes T new tokens of every sequence: token t goes to position start[b] + t.
+/* Writes T < 2^30 new tokens of every sequence: token t goes to position
+ * start[b] + t.
  *   k, v          [batch, Hkv, T, d] bf16; strides as fs_rope's (multiples of
  *                 8 elements and 16-byte aligned pointers, else
  *                 FS_ERR_UNSUPPORTED)
@@ -573,7 +574,7 @@ int fs_cache_append(const fs_cache *cache, const void *k, const void *v,
                     int T, const int32_t *start, const int32_t *count,
                     void *stream);
 
-/* Reads T tokens of every sequence from position start[b] on, as code * scale
+/* Reads T < 2^30 tokens of every sequence from position start[b] on, as code * scale
  * rounded to `dtype` (FS_BF16 or FS_FP32), into contiguous k, v
  * [batch, Hkv, T, d], 16-byte aligned: what fs_attention_fwd, fs_cell_summarize
  * and fs_decode_state_init take.  Rows t >= count[b] are left as they were. */

@@ -861,11 +861,11 @@ int check_cache_memory(const fs_cache *c) {
   return reinterpret_cast<uintptr_t>(c->codes) % 16 ? FS_ERR_UNSUPPORTED : FS_OK;
 }
 
-// T new rows a sequence and head; one thread handles eight elements.
-int check_rows(const fs_cache *c, int T) {
+// T new rows a sequence: no more than positions are (the kernels count a block's tokens
+// past the last one in 32 bits; (sequence, head) and part are the grid's other axes).
+int check_rows(int T) {
   if (T < 1) return FS_ERR_INVALID_ARG;
-  return (long long)c->batch * c->Hkv * 2 * T * (c->d / 8) >= (1ll << 32) - 256 ? FS_ERR_UNSUPPORTED
-                                                                               : FS_OK;
+  return T >= 1 << 30 ? FS_ERR_UNSUPPORTED : FS_OK;
 }
 
 }  // namespace
@@ -933,7 +933,7 @@ extern "C" int fs_cache_append(const fs_cache *cache, const void *k, const void 
                                const int32_t *start, const int32_t *count, void *stream) {
   FS_TRY(check_cache_memory(cache));
   if (!k || !v || !start) return FS_ERR_INVALID_ARG;
-  FS_TRY(check_rows(cache, T));
+  FS_TRY(check_rows(T));
   CacheRowsArgs a{};
   a.c = *cache;
   a.k = k;
@@ -955,7 +955,7 @@ extern "C" int fs_cache_read(const fs_cache *cache, const int32_t *start, const 
   FS_TRY(check_cache_memory(cache));
   FS_TRY(check_dtype(dtype));
   if (!k || !v || !start) return FS_ERR_INVALID_ARG;
-  FS_TRY(check_rows(cache, T));
+  FS_TRY(check_rows(T));
   if ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) % 16)
     return FS_ERR_UNSUPPORTED;
   CacheRowsArgs a{};
