@@ -826,15 +826,11 @@ extern "C" int fs_rope_make_plan(const fs_rope_params *p, fs_rope_plan *plan) {
 
 namespace {
 
-// Strides of [batch, H, N, d], given or contiguous.
-void set_strides(long long (&to)[3], const long long *given, int H, long long N, int d) {
-  if (given) {
-    for (int i = 0; i < 3; ++i) to[i] = given[i];
-    return;
-  }
-  to[0] = H * N * d;
-  to[1] = N * d;
-  to[2] = d;
+// Strides of [batch, H, N, d], given or contiguous.  That of an axis of one is never used
+// and may be anything.
+void set_strides(long long (&to)[3], const long long *given, int batch, int H, long long N, int d) {
+  const long long size[3] = {batch, H, N}, own[3] = {H * N * d, N * d, d};
+  for (int i = 0; i < 3; ++i) to[i] = size[i] == 1 ? 0 : given ? given[i] : own[i];
 }
 
 int check_cache(const fs_cache *c) {
@@ -893,13 +889,13 @@ extern "C" int fs_rope(const void *q, void *q_out, int Hq, const long long *q_st
   a.x[0] = q;
   a.y[0] = q_out;
   a.H[0] = Hq;
-  set_strides(a.xs[0], q_strides, Hq, N, d);
-  set_strides(a.ys[0], q_out_strides, Hq, N, d);
+  set_strides(a.xs[0], q_strides, batch, Hq, N, d);
+  set_strides(a.ys[0], q_out_strides, batch, Hq, N, d);
   a.x[1] = k;
   a.y[1] = k_out;
   a.H[1] = Hk;
-  set_strides(a.xs[1], k_strides, Hk, N, d);
-  set_strides(a.ys[1], k_out_strides, Hk, N, d);
+  set_strides(a.xs[1], k_strides, batch, Hk, N, d);
+  set_strides(a.ys[1], k_out_strides, batch, Hk, N, d);
   for (int i = 0; i < 2; ++i) {  // an output whose rows lie on one another
     const long long size[3] = {batch, a.H[i], N};
     for (int j = 0; a.H[i] && j < 3; ++j)
@@ -938,8 +934,8 @@ extern "C" int fs_cache_append(const fs_cache *cache, const void *k, const void 
   a.c = *cache;
   a.k = k;
   a.v = v;
-  set_strides(a.ks, k_strides, cache->Hkv, T, cache->d);
-  set_strides(a.vs, v_strides, cache->Hkv, T, cache->d);
+  set_strides(a.ks, k_strides, cache->batch, cache->Hkv, T, cache->d);
+  set_strides(a.vs, v_strides, cache->batch, cache->Hkv, T, cache->d);
   for (int i = 0; i < 3; ++i)
     if (a.ks[i] % 8 || a.vs[i] % 8) return FS_ERR_UNSUPPORTED;
   if ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) % 16)

@@ -30,3 +30,28 @@ def test_append_of_a_batch_padded_to_many_tokens(fmt):
     assert torch.equal(a.codes, b.codes)
     assert a.scales is None or torch.equal(a.scales, b.scales)
     fs.fs_check_status(a.status)
+
+
+def test_strides_of_axes_of_one_do_not_matter():
+    # one sequence, or one token, out of a buffer whose rows in between are of odd length
+    H, T, d = 4, 21, 64
+    flat = torch.randn(2 * H * T * d + 8, device="cuda").bfloat16()
+    for size, strides in (((1, H, T, d), (3, T * d, d, 1)), ((1, H, 1, d), (12345, d, 7, 1)),
+                          ((1, 1, T, d), (1, 5, d, 1))):
+        x = torch.as_strided(flat, size, strides)
+        y = x.clone(memory_format=torch.contiguous_format)
+        a, b = (_cache([2], size[1], 16, d, "int8", seed=4) for _ in range(2))
+        # (the binding passes no strides for what torch calls contiguous: the C call with them)
+        start = _ints([3])
+        args = (fs._Strides(*strides[:3]),) * 2 + (size[2], start.data_ptr(), None)
+        fs._launch(a.device, None, fs.load().fs_cache_append, "fs_cache_append", a.desc, x.data_ptr(),
+                   x.data_ptr(), *args)
+        fs.fs_cache_append(b, y, y, start)
+        assert torch.equal(a.codes, b.codes) and torch.equal(a.scales, b.scales)
+    x = torch.as_strided(flat, (1, H, T, d), (H * T * d + 3, d, H * d, 1))    # token-major
+    a, b = (_cache([2], H, 16, d, "int8", seed=4) for _ in range(2))
+    fs.fs_cache_append(a, x, x, _ints([3]))
+    fs.fs_cache_append(b, x.contiguous(), x.contiguous(), _ints([3]))
+    assert torch.equal(a.codes, b.codes)
+    plan = fs.fs_rope_plan(d)
+    assert torch.equal(fs.fs_rope(x, None, 5, plan)[0], fs.fs_rope(x.contiguous(), None, 5, plan)[0])
