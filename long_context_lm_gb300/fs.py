@@ -951,6 +951,8 @@ def _tree_attn(fn, where, more, q, cache, past, tree, count, window, scale, out,
     if ws is None:
         ws = _new(stream, lambda: fs_tree_workspace(cache, B, H, T))
     wp = _on(ws, dev, "ws", torch.uint8)
+    if not ws.is_contiguous():  # its bytes would not be ws.numel() bytes of memory
+        raise ValueError("ws must be contiguous")
     _launch(dev, stream, fn, where, qp, cache.desc, _counts(cache, "past", past),
             _counts(cache, "count", count), tp, H, T, int(window),
             d ** -0.5 if scale is None else float(scale), op, wp, ws.numel(), *more)

@@ -55,3 +55,13 @@ def test_strides_of_axes_of_one_do_not_matter():
     assert torch.equal(a.codes, b.codes)
     plan = fs.fs_rope_plan(d)
     assert torch.equal(fs.fs_rope(x, None, 5, plan)[0], fs.fs_rope(x.contiguous(), None, 5, plan)[0])
+
+
+def test_workspaces_that_are_not_their_own_memory_are_refused():
+    cache = _cache([4], 2, 16, 64, "int8")
+    q = torch.zeros((1, 4, 2, 64), dtype=torch.bfloat16, device="cuda")
+    need = fs.fs_tree_workspace(cache, 1, 4, 2).numel()
+    for ws in (torch.empty(1, dtype=torch.uint8, device="cuda").expand(need),
+               torch.empty(2 * need, dtype=torch.uint8, device="cuda")[::2]):
+        with pytest.raises(ValueError):
+            fs.fs_tree_attn(q, cache, _ints([3]), ws=ws)
