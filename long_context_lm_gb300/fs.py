@@ -682,6 +682,7 @@ def fs_check_status(ws, stream=None):
 # ---------------------------------------------------------------------------
 
 _Strides = ctypes.c_longlong * 3
+_INT_MAX = 2 ** 31 - 1  # (ctypes would take the low 32 bits of more)
 
 
 def _on(t, dev, name, dtype, shape=None):
@@ -750,6 +751,8 @@ def fs_rope_plan(rot, layout="half", scaling="none", base=10000.0, factor=1.0, o
     "linear", "base" or "ramp" by ``factor``."""
     if layout not in FS_ROPE_LAYOUTS or scaling not in FS_ROPE_SCALINGS:
         raise ValueError(f"unknown layout {layout!r} or scaling {scaling!r}")
+    if max(int(rot), int(original)) > _INT_MAX or min(int(rot), int(original)) < -_INT_MAX:
+        raise ValueError(f"rot {rot} or original {original} does not fit 32 bits")
     p = fs_rope_params(int(rot), FS_ROPE_LAYOUTS[layout], FS_ROPE_SCALINGS[scaling], int(original),
                        base, factor, beta_fast, beta_slow, amplitude)
     plan = fs_rope_plan_t()
@@ -954,6 +957,6 @@ def _tree_attn(fn, where, more, q, cache, past, tree, count, window, scale, out,
     if not ws.is_contiguous():  # its bytes would not be ws.numel() bytes of memory
         raise ValueError("ws must be contiguous")
     _launch(dev, stream, fn, where, qp, cache.desc, _counts(cache, "past", past),
-            _counts(cache, "count", count), tp, H, T, int(window),
+            _counts(cache, "count", count), tp, H, T, max(-1, min(int(window), _INT_MAX)),
             d ** -0.5 if scale is None else float(scale), op, wp, ws.numel(), *more)
     return out

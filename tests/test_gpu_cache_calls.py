@@ -65,3 +65,14 @@ def test_workspaces_that_are_not_their_own_memory_are_refused():
                torch.empty(2 * need, dtype=torch.uint8, device="cuda")[::2]):
         with pytest.raises(ValueError):
             fs.fs_tree_attn(q, cache, _ints([3]), ws=ws)
+
+
+def test_windows_past_32_bits():
+    cache = _cache([40], 2, 16, 64, "int8")
+    k, q = (torch.randn((1, 2, n, 64), device="cuda").bfloat16() for n in (600, 2))
+    fs.fs_cache_append(cache, k, k, _ints([0]))
+    want = fs.fs_tree_attn(q, cache, _ints([590]))
+    for window in (2 ** 31 - 1, 2 ** 31, 2 ** 32 + 64, 2 ** 40):       # all of it
+        assert torch.equal(fs.fs_tree_attn(q, cache, _ints([590]), window=window), want)
+    with pytest.raises(fs.FSError):
+        fs.fs_tree_attn(q, cache, _ints([590]), window=64 - 2 ** 32)

@@ -23,3 +23,10 @@ def test_wait_limits_outside_are_refused(cycles):
     rc = fs.load().fs_selftest_tree_wait(_vp(256), _desc(), _vp(256), None, None, 4, 8, 0, 0.125,
                                          _vp(1 << 30), _vp(256), 1 << 40, cycles, None)
     assert rc == fs.FS_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("kw", [dict(rot=2 ** 32 + 64), dict(rot=64, scaling="ramp", original=2 ** 32 + 4096),
+                                dict(rot=64 - 2 ** 32)])
+def test_plan_sizes_past_32_bits_are_refused(kw):
+    with pytest.raises(ValueError):
+        fs.fs_rope_plan(**kw)
