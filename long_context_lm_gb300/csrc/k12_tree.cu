@@ -309,7 +309,7 @@ __device__ __forceinline__ void q_to_f16(const Magic &magic, uint32_t (&raw)[D /
 // Product of the fragments -> log2 units, and what the bias adds to a product.
 template <int F>
 __device__ __forceinline__ float score_factor(float scale, float f) {
-  const float rf = fmaxf(scale * kLog2e * (1.f / f), FLT_MIN);
+  const float rf = log2_factor(scale, f);
   return kBias<F> != 0.f ? rf * 0x1p24f : rf;
 }
 template <int F>

@@ -321,7 +321,7 @@ k13_tree_wide_kernel(const __grid_constant__ TreeK k, const __grid_constant__ Ma
         most = max(most & 0xffffu, most >> 16);
         f = __uint_as_float((uint32_t)min(254, 268 - (int)(most >> 7)) << 23);
       }
-      const float rf = fmaxf(a.scale * kLog2e * (1.f / f), FLT_MIN);
+      const float rf = log2_factor(a.scale, f);
       if (st == 0) {
 #pragma unroll 1
         for (int c = 0; ok && c < C::kCols; ++c) {

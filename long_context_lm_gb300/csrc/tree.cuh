@@ -14,6 +14,13 @@ namespace fs {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
+// Products with a row of q that was multiplied by f -> scores in log2 units.  Not 0, which a
+// masked score's -inf may not meet; below fp32's normal range (q below 2^-110) it is
+// off by 2^-150, a score by 2^-22.
+__device__ __forceinline__ float log2_factor(float scale, float f) {
+  return fmaxf(scale * kLog2e * (1.f / f), 0x1p-149f);
+}
+
 // ---------------------------------------------------------------------------
 // references
 // ---------------------------------------------------------------------------

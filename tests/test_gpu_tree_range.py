@@ -175,3 +175,17 @@ def test_scores_that_rise(T, H, step, d, fmt):
         tree = torch.full((1, T), (1 << min(T, 63)) - 1, dtype=torch.int64).cuda()   # all drafted
         _check(q, cache, past, fs.fs_tree_attn(q, cache, _ints([past]), tree=tree, scale=scale), tree,
                scale=scale)
+
+
+@pytest.mark.parametrize("fmt", ref.FORMATS)
+@pytest.mark.parametrize("T,H", FORMS)
+def test_tiny_queries_and_large_keys(T, H, fmt):
+    # scores of 2^-12 64 scale, from numbers near both ends of bf16; values with the keys' signs, so that
+    # an error of the scores shows in full
+    past, d, scale = 900, 64, 0.01
+    k = torch.ones((1, 1, past + T, d), device="cuda") * 2.0 ** 100
+    k[:, :, ::2] *= -1.0
+    v = k.sign() + 0.01 * _randn(k.shape, 2)
+    cache = _cache(k, v, fmt)
+    q = torch.full((1, H, T, d), 2.0 ** -112, device="cuda").bfloat16()
+    _check(q, cache, past, fs.fs_tree_attn(q, cache, _ints([past]), scale=scale), scale=scale)
