@@ -576,8 +576,10 @@ int fs_cache_append(const fs_cache *cache, const void *k, const void *v,
 
 /* Reads T < 2^30 tokens of every sequence from position start[b] on, as code * scale
  * rounded to `dtype` (FS_BF16 or FS_FP32), into contiguous k, v
- * [batch, Hkv, T, d], 16-byte aligned: what fs_attention_fwd, fs_cell_summarize
- * and fs_decode_state_init take.  Rows t >= count[b] are left as they were. */
+ * [batch, Hkv, T, d], 16-byte aligned.  Rows t >= count[b] are left as they were.
+ * fs_attention_fwd, fs_cell_summarize and fs_decode_state_init rotate inside and
+ * take unrotated keys: from a cache of unrotated ones as they are, from one of
+ * rotated ones (fs_tree_attn's) through fs_rope with inverse = 1 and amplitude 1. */
 int fs_cache_read(const fs_cache *cache, const int32_t *start,
                   const int32_t *count, int T, int dtype, void *k, void *v,
                   void *stream);
@@ -590,7 +592,9 @@ int fs_cache_accept(const fs_cache *cache, const int32_t *start,
                     const int32_t *path, const int32_t *count, int A,
                     void *stream);
 
-/* Attention of T drafted tokens of every sequence over its cache.  The drafted
+/* Attention of T drafted tokens of every sequence over its cache, softmax of
+ * q . k as they are: a model with rotary positions rotates q and the cached keys
+ * beforehand (fs_rope).  The drafted
  * tokens' keys and values lie in the cache at positions past[b] .. past[b] +
  * count[b] - 1, behind the past[b] tokens of the prefix.  Row i of sequence b
  * sees the prefix and the drafted tokens j < count[b] whose bit j of tree[b, i]
@@ -610,7 +614,11 @@ int fs_cache_accept(const fs_cache *cache, const int32_t *start,
  * T <= 64.  ws: device workspace of fs_tree_workspace_bytes() bytes for one
  * call at a time.  Rows of a sequence with a position past the table or a page
  * outside the cache see only what can be read (and the cache's status says
- * so).  Deterministic.  Two kernels; with many rows to a kv head the first waits
+ * so).  What a row does not see has no part in its output, whatever it is;
+ * elements that it sees and that are not finite give NaN or an infinity.  Keys of
+ * quantised caches may have magnitudes up to 2^100; where values pass 2^113, keys
+ * of less than 2^-20 of a row's largest probability are lost from its sum.
+ * Deterministic.  Two kernels; with many rows to a kv head the first waits
  * on mbarriers, within a limit after which it records FS_ERR_TIMEOUT in the
  * cache's status, and out is then not valid. */
 size_t fs_tree_workspace_bytes(const fs_cache *cache, int H, int T);
