@@ -23,7 +23,8 @@
 // order of columns: so every lane reads whole 16-byte (8, 4) pieces of codes
 // and turns them into fragments in registers.  Codes of 8 and 4 bits are exact
 // in fp16; q is brought into fp16's range by a power of two a row (exact but
-// for elements below 2^-39 of the row's largest).  The key's scale multiplies
+// for elements below 2^-31 of the row's largest, which are rounded at 2^-39 of it, 2^-35
+// where int4's odd ones are divided by 16).  The key's scale multiplies
 // the score, the value's scale the probability: a weight.
 //
 // Weights go into the second product as fp16 (half a step 2^-11), the row's
@@ -143,8 +144,10 @@ __device__ __forceinline__ int v_place(int r, int piece) {
 // in as code + bias (128 or 8), the bits of an fp16 subnormal: (code + bias)
 // 2^-24, of an odd nibble 16 times that, which its elements of q make up for.
 // The bias is the same for all keys of a row of q and leaves with one addition.
-// (It costs the fp32 sum at most two bits; the values' codes below, whose sum
-// runs over all keys, go in without one.)
+// It takes bits from the fp32 sum: two where codes fill their range, five to seven
+// where a key row has one outlier and its other codes are a few units.  A score is then off
+// by some (d + 3) 2^-24 of |q|_1 times twice the key row's largest magnitude.  (The values'
+// codes below, whose sum runs over all keys, go in without one.)
 template <int F>
 constexpr float kBias = F == FS_CACHE_INT8 ? 128.f : F == FS_CACHE_INT4 ? 8.f : 0.f;
 template <int F>
@@ -1163,11 +1166,14 @@ cudaError_t launch_f(const TreeK &k, cudaStream_t st) {
 
 // Whether 128 rows are taken at a time, on tcgen05: from more rows to a kv head
 // than the kernel above does well.  Measured on 4 sequences of 16384 keys, 8 kv
-// heads, here against there (us).  int8, d = 64: 64 rows 57 and 58, 96 rows 74 and
-// 59; d = 128: 32 rows 62 and 77, 40 rows 78 and 77, 64 rows 97 and 79.  bf16,
-// whose probabilities are two products here and whose rows need no conversion
-// there, d = 64: 32 rows 43 and 55, 40 rows 62 and 58; d = 128: 16 rows 56 and 71,
-// 20 rows 96 and 74.
+// heads, cold caches, here against there (us):
+//   d = 64    int8 64 rows 65, 65, 96 rows 82, 67   e4m3 61, 65 and 76, 66   int4 60, 63 and 76, 64
+//   d = 128   int8 32 rows 78, 81, 40 rows 93, 80   e4m3 77, 79 and 90, 77   int4 69, 76 and 86, 75
+//   bf16, whose probabilities are two products here and whose rows need no conversion there:
+//   d = 64 32 rows 61, 70, 40 rows 77, 67           d = 128 16 rows 80, 88, 20 rows 123, 90
+// The prefixes' lengths, which the host does not know, play no part: over a few hundred keys
+// both take 18 to 35 us, and the rule costs up to 10 of them (4 x 400 bf16 keys, d = 128,
+// 20 to 48 rows: 24 to 27 here, 34 to 37 there; 8-bit and int4 codes at most 8).
 bool wide(const fs_cache &c, int H, int T) {
   return H / c.Hkv * T > (c.d == 64 ? 64 : 32) / (c.format == FS_CACHE_BF16 ? 2 : 1);
 }

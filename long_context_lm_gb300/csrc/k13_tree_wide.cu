@@ -26,15 +26,15 @@
 //
 // Tiles of 128 codes with heads of 64 (scores, probabilities and output fill a
 // stream's half of TMEM), else of 64 with the scores held twice and P written over
-// them: 64 tokens x 4 heads a kv head over 8 x 16384 int8 keys take 154 us with the
-// former and 161 with the latter.  Four warps on the same tile, each waiting for the
-// same barriers, were what everything waited for: 205 us (bf16, one warp for all TMA
-// copies: 182, now 145).
+// them: 64 tokens x 4 heads a kv head over 8 x 16384 keys take 167 us (int8) and 162
+// (e4m3) with the former, 168 and 165 with the latter.  Four warps on the same tile, each
+// waiting for the same barriers, were what everything waited for: 205 us when pairs in
+// turn took 157 (bf16: one warp for all TMA copies 182, four 150).
 //
 // Bound by: with codes, the rows' warps, which read two scales a column from shared
-// memory (128 us without those reads) around the exponentials (128 x KT a tile);
-// with bf16 and heads of 128 the products' issue and the keys that come twice, once
-// for each 128 rows (4 of 107 us went with the rows' work).
+// memory (26 us of an earlier 154 went with those reads) around the exponentials (128 x KT
+// a tile); with bf16 and heads of 128 the products' issue and the keys that come twice,
+// once for each 128 rows (4 of 107 us went with the rows' work).
 #include <cuda.h>
 
 #include "tree.cuh"
