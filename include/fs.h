@@ -616,8 +616,10 @@ int fs_cache_accept(const fs_cache *cache, const int32_t *start,
  * outside the cache see only what can be read (and the cache's status says
  * so).  What a row does not see has no part in its output, whatever it is;
  * elements that it sees and that are not finite give NaN or an infinity.  Keys of
- * quantised caches may have magnitudes up to 2^100; where values pass 2^113, keys
- * of less than 2^-20 of a row's largest probability are lost from its sum.
+ * quantised caches may have magnitudes up to 2^100.  Keys of next to no probability
+ * count in fewer bits, then not at all: below 2^-87 of the row's largest over bf16
+ * caches, 2^-120 over quantised ones with values of usual sizes (2^-20 where values
+ * pass 2^113).
  * Deterministic.  Two kernels; with many rows to a kv head the first waits
  * on mbarriers, within a limit after which it records FS_ERR_TIMEOUT in the
  * cache's status, and out is then not valid. */

@@ -29,8 +29,10 @@ __device__ __forceinline__ float log2_factor(float scale, float f) {
 // values are codes.  Sum and output are relative to the row's own reference, which what
 // other rows see cannot move.  FLT_MAX: the row has seen no key.  A reference moves when a
 // key that the row sees passes kHigh, and by so much that the largest is at kLow:
-//   bf16   p alone; its parts are bf16 numbers, so any range would do: 2^-46 to 2^-30
-//          leaves room for 2^30 keys of the largest values.
+//   bf16   p alone; its parts are bf16 numbers, so that any range has the same bits.  2^-30
+//          to 2^-14 leaves room for sums of 2^14 of bf16's largest values, and 96 binary
+//          places below the largest p (the lower part's 8 bits: 87), which count where
+//          a key of next to no probability has values that much larger.
 //   codes  weights go to fp16, whose largest number is below 2^16; the row's largest stays
 //          at 2^7 or more, 2^31 times the step of the smallest ones.  A second border, on p,
 //          keeps the sums of 2^30 keys within fp32 where values are tiny or zero (it
@@ -41,7 +43,7 @@ __device__ __forceinline__ float log2_factor(float scale, float f) {
 template <int F>
 struct Range {
   static constexpr bool kBF = F == FS_CACHE_BF16;
-  static constexpr float kLow = kBF ? -46.f : 8.f, kHigh = kBF ? -30.f : 15.99f;
+  static constexpr float kLow = kBF ? -30.f : 8.f, kHigh = kBF ? -14.f : 15.99f;
   static constexpr float kSumLow = 85.f, kSumHigh = 93.f;
 };
 

@@ -189,3 +189,18 @@ def test_tiny_queries_and_large_keys(T, H, fmt):
     cache = _cache(k, v, fmt)
     q = torch.full((1, H, T, d), 2.0 ** -112, device="cuda").bfloat16()
     _check(q, cache, past, fs.fs_tree_attn(q, cache, _ints([past]), scale=scale), scale=scale)
+
+
+@pytest.mark.parametrize("fmt", ref.FORMATS)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("T,H", FORMS)
+def test_a_key_of_no_probability_whose_values_decide(T, H, d, fmt):
+    # its probability is 2^-80 of the others', its values are 2^84 times theirs
+    past = 300
+    k, v = 0.01 * _randn((1, 1, past + T, d), 1), 2.0 ** -40 * _randn((1, 1, past + T, d), 2)
+    k[:, :, 200] = -1.25 * 64 / d
+    v[:, :, 200] *= 2.0 ** 84
+    cache = _cache(k, v, fmt)
+    q = torch.ones((1, H, T, d), device="cuda").bfloat16()
+    scale = math.log(2.0)
+    _check(q, cache, past, fs.fs_tree_attn(q, cache, _ints([past]), scale=scale), scale=scale)
