@@ -637,6 +637,116 @@ int fs_selftest_tree_wait(const void *q, const fs_cache *cache,
                           float scale, void *out, void *ws, size_t ws_bytes,
                           long long cycles, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * Linear attention with a decay for each head, and the norms around a block (no
+ * counterpart on the pages: a layer that keeps no keys at all, for models that
+ * mix such layers with the attention above).
+ *
+ * With lam = exp(decay[h]) and states S [d (key), d (value)] in fp32:
+ *   S_t = lam S_{t-1} + k_t v_t^T,   out_t = scale q_t S_t.
+ * Prompts run in chunks of tokens on the tensor cores, T <= FS_LINEAR_STEPS
+ * tokens one after the other: a decoding step is T = 1.
+ *   q, out        [batch, H, T, d] bf16; k, v [batch, Hkv, T, d] bf16; H a multiple
+ *                 of Hkv, query head h reading kv head h / (H / Hkv).  Strides as
+ *                 fs_rope's, multiples of 8 elements, pointers 16-byte aligned
+ *                 (else FS_ERR_UNSUPPORTED); no negative ones, and 0 between tokens
+ *                 only for T = 1 (FS_ERR_UNSUPPORTED).  out overlaps no input
+ *   decay         [H] f32, the logarithm of the factor a token: 0 or below (-inf:
+ *                 a token sees itself alone).  A constant of the model: there is no
+ *                 gradient for it
+ *   count         [batch] int32 or NULL (all T): sequence b's tokens; rows
+ *                 t >= count[b] of out are left as they were, those of q, k and v
+ *                 may hold anything
+ *   scale         finite, not 0
+ *   state         [batch, H, d, d] f32, 16-byte aligned, the state before the first
+ *                 token, or NULL (zeros); state_out the one after the last, or NULL
+ *                 (not written).  Both may be the same memory (in place); they do
+ *                 not overlap otherwise (FS_ERR_INVALID_ARG)
+ * Products of bf16 numbers are summed in fp32; the factors of the tensor cores'
+ * products that are not bf16 numbers themselves (scores, weighted values, states)
+ * go in as sums of two or three bf16 parts, 16 bits or more for outputs and 24
+ * for states.  An element of v that is not finite makes its
+ * column of that token's and all later outputs, and of the state, NaN or
+ * infinite; one of k or q reaches what the definition says.
+ *   ws            device workspace of fs_linear_workspace_bytes() bytes, for one
+ *                 call at a time; its first int is an error word (fs_check_status(ws))
+ *                 that the caller zeroes once: calls record FS_ERR_TIMEOUT there when
+ *                 a bounded wait gives up, and none clears it.  May be NULL for
+ *                 forward calls with T <= FS_LINEAR_STEPS
+ * d: 64 or 128; batch * H < 2^16, T < 2^30 (else FS_ERR_UNSUPPORTED).
+ * Deterministic. */
+#define FS_LINEAR_STEPS 16
+size_t fs_linear_workspace_bytes(int batch, int H, int Hkv, int T, int d, int backward);
+int fs_linear_attn(const void *q, const void *k, const void *v, const long long *q_strides,
+                   const long long *k_strides, const long long *v_strides, const float *decay,
+                   int batch, int H, int Hkv, int T, int d, const int32_t *count, float scale,
+                   const float *state, float *state_out, void *out, const long long *out_strides,
+                   void *ws, size_t ws_bytes, void *stream);
+
+/* Gradients of L = sum(dout * out) + sum(dstate_out * state_out):
+ *   R_t = scale q_t dout_t^T + lam R_{t+1},  lam R_T = dstate_out,
+ *   dq_t = scale S_t dout_t,  dk_t = R_t v_t,  dv_t = R_t^T k_t,  dstate = lam R_0,
+ * dk and dv summed over the query heads that share a kv head.
+ *   state         the forward's state, or NULL (zeros)
+ *   dout          [batch, H, T, d] bf16; dstate_out [batch, H, d, d] f32 or NULL (zeros)
+ *   dq, dk, dv    bf16, as q, k and v (written; rows t >= count[b] are left as they
+ *                 were); dstate [batch, H, d, d] f32 or NULL.  They overlap neither an
+ *                 input nor one another
+ *   ws            of fs_linear_workspace_bytes(..., 1) bytes, never NULL
+ * The other arguments as the forward's.  Deterministic. */
+int fs_linear_attn_bwd(const void *q, const void *k, const void *v, const long long *q_strides,
+                       const long long *k_strides, const long long *v_strides, const float *decay,
+                       int batch, int H, int Hkv, int T, int d, const int32_t *count, float scale,
+                       const float *state, const void *dout, const long long *dout_strides,
+                       const float *dstate_out, void *dq, void *dk, void *dv,
+                       const long long *dq_strides, const long long *dk_strides,
+                       const long long *dv_strides, float *dstate, void *ws, size_t ws_bytes,
+                       void *stream);
+
+/* The norms after and before a block, its gate and its residual scale, for M rows
+ * of D elements (a block's outputs, or the heads' outputs of M tokens side by side):
+ *   a = x / sqrt(mean of x^2 over its group + eps)   (groups >= 1 groups of D / groups
+ *       elements; groups 0: a = x),  then  a *= gain,  a *= gate / (1 + exp(-gate))
+ *   z = residual + scale a
+ *   y = z / sqrt(mean of z^2 over the row + eps) * next_gain
+ *   x, gate, y    bf16 or f32 (`dtype`); residual, z bf16 or f32 (`res_dtype`: FS_FP32
+ *                 if dtype is, else FS_ERR_UNSUPPORTED).  Rows lie `_stride` elements
+ *                 apart (not below 0; 0 repeats an input's row)
+ *   gate, residual   or NULL: none
+ *   gain, next_gain  [D] f32, or NULL: ones
+ *   z, y          either may be NULL (not wanted; y NULL: no norm of z)
+ * z may be x or residual and y may be x or gate, of the same type, with their
+ * strides (in place); other overlaps give undefined results.  Computed in fp32,
+ * y from z before its rounding; rounded once.  Squares and their sums are to fit fp32.
+ * D <= 16384 (else FS_ERR_UNSUPPORTED), D a multiple of groups, eps >= 0.  One kernel. */
+int fs_block_norm(const void *x, long long x_stride, int dtype, const void *gate,
+                  long long gate_stride, const void *residual, long long residual_stride,
+                  int res_dtype, const float *gain, const float *next_gain, int M, int D, int groups,
+                  float scale, float eps, void *z, long long z_stride, void *y, long long y_stride,
+                  void *stream);
+
+/* Gradients of L = sum(dz * z) + sum(dy * y).
+ *   dz [M, D] of res_dtype, dy of dtype; either may be NULL (zeros), not both.  With
+ *                 dy NULL the norm of z has no part, and residual's values none either
+ *                 (residual is then not read and may be NULL beside a dresidual)
+ *   dx            of dtype (written); dgate of dtype, or NULL; dresidual of res_dtype,
+ *                 or NULL: the gradient of z and of residual alike
+ *   dgain, dnext_gain  [D] f32 (written), or NULL; dnext_gain wants a dy
+ *   ws            of fs_block_norm_workspace_bytes() bytes, for one call at a time; NULL
+ *                 where neither dgain nor dnext_gain is wanted
+ * dx may be x or dy, dgate may be gate, dresidual may be dz or residual, with their
+ * strides; other overlaps give undefined results.  Sums over rows are fp32 within
+ * a block's rows, then fp64 in block order: deterministic.  One or two kernels. */
+size_t fs_block_norm_workspace_bytes(int M, int D);
+int fs_block_norm_bwd(const void *x, long long x_stride, int dtype, const void *gate,
+                      long long gate_stride, const void *residual, long long residual_stride,
+                      int res_dtype, const float *gain, const float *next_gain, int M, int D,
+                      int groups, float scale, float eps, const void *dz, long long dz_stride,
+                      const void *dy, long long dy_stride, void *dx, long long dx_stride,
+                      void *dgate, long long dgate_stride, void *dresidual,
+                      long long dresidual_stride, float *dgain, float *dnext_gain, void *ws,
+                      size_t ws_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1041,6 +1041,308 @@ extern "C" int fs_selftest_tree_wait(const void *q, const fs_cache *cache, const
                    stream);
 }
 
+// ---------------------------------------------------------------------------
+// Linear attention with a decay for each head; the norms around a block.
+// ---------------------------------------------------------------------------
+namespace {
+
+int check_linear(int batch, int H, int Hkv, int T, int d) {
+  if (batch < 1 || H < 1 || Hkv < 1 || H % Hkv || T < 1 || d < 1) return FS_ERR_INVALID_ARG;
+  if ((d != 64 && d != 128) || (long long)batch * H > 65535 || T >= 1 << 30) return FS_ERR_UNSUPPORTED;
+  return FS_OK;
+}
+
+// One of the row tensors: 16-byte rows, no negative strides, tokens apart.
+int check_linear_rows(const void *p, const long long (&s)[3], int T) {
+  if (!p) return FS_ERR_INVALID_ARG;
+  for (long long x : s)
+    if (x < 0) return FS_ERR_INVALID_ARG;
+  for (long long x : s)
+    if (x % 8) return FS_ERR_UNSUPPORTED;
+  if (T > 1 && s[2] == 0) return FS_ERR_UNSUPPORTED;
+  return reinterpret_cast<uintptr_t>(p) % 16 ? FS_ERR_UNSUPPORTED : FS_OK;
+}
+
+int check_linear_out(const void *p, const long long (&s)[3], int batch, int H, int T) {
+  FS_TRY(check_linear_rows(p, s, T));
+  // (rows that lie on one another)
+  if ((batch > 1 && s[0] == 0) || (H > 1 && s[1] == 0)) return FS_ERR_INVALID_ARG;
+  return FS_OK;
+}
+
+int check_states(const float *a, const float *b, bool same, size_t floats) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  if ((x | y) % 16) return FS_ERR_UNSUPPORTED;
+  if (!a || !b || (same && a == b)) return FS_OK;
+  return x < y + floats * 4 && y < x + floats * 4 ? FS_ERR_INVALID_ARG : FS_OK;
+}
+
+LinearRows linear_rows(const void *x, const long long (&s)[3], int share) {
+  LinearRows r{x, {s[0], s[1], s[2]}, share};
+  return r;
+}
+
+// The workspace: the header with the error word, the parts of shared heads' gradients.
+struct LinearLayout {
+  size_t dk, dv, total;
+};
+LinearLayout linear_layout(int batch, int H, int Hkv, int T, int d, bool backward) {
+  LinearLayout L{};
+  size_t off = kHeader;
+  const size_t part = backward && H > Hkv ? (size_t)batch * H * T * d * 4 : 0;
+  L.dk = off;
+  off = align_up(off + part);
+  L.dv = off;
+  off = align_up(off + part);
+  L.total = off;
+  return L;
+}
+
+}  // namespace
+
+extern "C" size_t fs_linear_workspace_bytes(int batch, int H, int Hkv, int T, int d, int backward) {
+  if (check_linear(batch, H, Hkv, T, d) != FS_OK) return 0;
+  return linear_layout(batch, H, Hkv, T, d, backward != 0).total;
+}
+
+extern "C" int fs_linear_attn(const void *q, const void *k, const void *v, const long long *q_strides,
+                              const long long *k_strides, const long long *v_strides,
+                              const float *decay, int batch, int H, int Hkv, int T, int d,
+                              const int32_t *count, float scale, const float *state,
+                              float *state_out, void *out, const long long *out_strides, void *ws,
+                              size_t ws_bytes, void *stream) {
+  FS_TRY(check_linear(batch, H, Hkv, T, d));
+  if (!decay || !(scale - scale == 0.f) || scale == 0.f) return FS_ERR_INVALID_ARG;
+  long long qs[3], ks[3], vs[3], os[3];
+  set_strides(qs, q_strides, batch, H, T, d);
+  set_strides(ks, k_strides, batch, Hkv, T, d);
+  set_strides(vs, v_strides, batch, Hkv, T, d);
+  set_strides(os, out_strides, batch, H, T, d);
+  FS_TRY(check_linear_rows(q, qs, T));
+  FS_TRY(check_linear_rows(k, ks, T));
+  FS_TRY(check_linear_rows(v, vs, T));
+  FS_TRY(check_linear_out(out, os, batch, H, T));
+  if (out == q || out == k || out == v) return FS_ERR_INVALID_ARG;
+  FS_TRY(check_states(state, state_out, true, (size_t)batch * H * d * d));
+  if (ws ? ws_bytes < linear_layout(batch, H, Hkv, T, d, false).total : T > FS_LINEAR_STEPS)
+    return FS_ERR_INVALID_ARG;
+  LinearArgs a{};
+  a.sweeps = 1;
+  LinearSweep &w = a.sweep[0];
+  w.q = linear_rows(q, qs, 1);
+  w.k = linear_rows(k, ks, H / Hkv);
+  w.v = linear_rows(v, vs, H / Hkv);
+  w.out = out;
+  for (int i = 0; i < 3; ++i) w.os[i] = os[i];
+  w.state = state;
+  w.state_out = state_out;
+  w.state_mul = 1.f;
+  a.batch = batch;
+  a.H = H;
+  a.T = T;
+  a.d = d;
+  a.decay = decay;
+  a.count = count;
+  a.scale = scale;
+  return status_of(launch_linear_recurrent(a, static_cast<cudaStream_t>(stream)));
+}
+
+extern "C" int fs_linear_attn_bwd(
+    const void *q, const void *k, const void *v, const long long *q_strides,
+    const long long *k_strides, const long long *v_strides, const float *decay, int batch, int H,
+    int Hkv, int T, int d, const int32_t *count, float scale, const float *state, const void *dout,
+    const long long *dout_strides, const float *dstate_out, void *dq, void *dk, void *dv,
+    const long long *dq_strides, const long long *dk_strides, const long long *dv_strides,
+    float *dstate, void *ws, size_t ws_bytes, void *stream) {
+  FS_TRY(check_linear(batch, H, Hkv, T, d));
+  if (!decay || !(scale - scale == 0.f) || scale == 0.f) return FS_ERR_INVALID_ARG;
+  long long qs[3], ks[3], vs[3], ds[3], gq[3], gk[3], gv[3];
+  set_strides(qs, q_strides, batch, H, T, d);
+  set_strides(ks, k_strides, batch, Hkv, T, d);
+  set_strides(vs, v_strides, batch, Hkv, T, d);
+  set_strides(ds, dout_strides, batch, H, T, d);
+  set_strides(gq, dq_strides, batch, H, T, d);
+  set_strides(gk, dk_strides, batch, Hkv, T, d);
+  set_strides(gv, dv_strides, batch, Hkv, T, d);
+  FS_TRY(check_linear_rows(q, qs, T));
+  FS_TRY(check_linear_rows(k, ks, T));
+  FS_TRY(check_linear_rows(v, vs, T));
+  FS_TRY(check_linear_rows(dout, ds, T));
+  FS_TRY(check_linear_out(dq, gq, batch, H, T));
+  FS_TRY(check_linear_out(dk, gk, batch, Hkv, T));
+  FS_TRY(check_linear_out(dv, gv, batch, Hkv, T));
+  for (const void *o : {dq, dk, dv})
+    if (o == q || o == k || o == v || o == dout) return FS_ERR_INVALID_ARG;
+  if (dq == dk || dq == dv || dk == dv) return FS_ERR_INVALID_ARG;
+  const size_t floats = (size_t)batch * H * d * d;
+  FS_TRY(check_states(state, dstate, false, floats));
+  FS_TRY(check_states(dstate_out, dstate, false, floats));
+  const LinearLayout L = linear_layout(batch, H, Hkv, T, d, true);
+  if (!ws || ws_bytes < L.total) return FS_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(ws) % 16) return FS_ERR_UNSUPPORTED;
+  const int share = H / Hkv;
+  LinearArgs a{};
+  a.sweeps = 3;
+  const LinearRows rq = linear_rows(q, qs, 1), rk = linear_rows(k, ks, share),
+                   rv = linear_rows(v, vs, share), rd = linear_rows(dout, ds, 1);
+  // dq: the forward's sweep with dout for q, v for k and k for v, over the transposed state
+  LinearSweep &wq = a.sweep[0];
+  wq.q = rd, wq.k = rv, wq.v = rk;
+  wq.out = dq;
+  for (int i = 0; i < 3; ++i) wq.os[i] = gq[i];
+  wq.state = state;
+  wq.transposed = true;
+  wq.state_mul = 1.f;
+  // dk and dv: sweeps in reverse over R / scale, transposed for dk
+  LinearSweep &wk = a.sweep[1], &wv = a.sweep[2];
+  wk.q = rv, wk.k = rd, wk.v = rq;
+  wv.q = rk, wv.k = rq, wv.v = rd;
+  char *base = static_cast<char *>(ws);
+  float *part[2] = {reinterpret_cast<float *>(base + L.dk), reinterpret_cast<float *>(base + L.dv)};
+  for (int i = 0; i < 2; ++i) {
+    LinearSweep &w = a.sweep[1 + i];
+    w.out = share > 1 ? static_cast<void *>(part[i]) : i ? dv : dk;
+    w.out_f32 = share > 1;
+    const long long own[3] = {(long long)H * T * d, (long long)T * d, d};
+    for (int j = 0; j < 3; ++j) w.os[j] = share > 1 ? own[j] : i ? gv[j] : gk[j];
+    w.state = dstate_out;
+    w.state_mul = 1.f / scale;
+    w.reverse = true;
+    w.transposed = i == 0;
+  }
+  wv.state_out = dstate;
+  a.batch = batch;
+  a.H = H;
+  a.T = T;
+  a.d = d;
+  a.decay = decay;
+  a.count = count;
+  a.scale = scale;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  FS_TRY(status_of(launch_linear_recurrent(a, st)));
+  for (int i = 0; share > 1 && i < 2; ++i) {
+    LinearSumArgs s{};
+    s.part = part[i];
+    s.out = i ? dv : dk;
+    for (int j = 0; j < 3; ++j) s.os[j] = i ? gv[j] : gk[j];
+    s.batch = batch;
+    s.H = H;
+    s.share = share;
+    s.T = T;
+    s.d = d;
+    s.count = count;
+    FS_TRY(status_of(launch_linear_sum(s, st)));
+  }
+  return FS_OK;
+}
+
+namespace {
+
+int check_norm(const NormArgs &a, int dtype, int res_dtype) {
+  FS_TRY(check_dtype(dtype));
+  FS_TRY(check_dtype(res_dtype));
+  if (!a.x || a.M < 1 || a.D < 1 || a.groups < 0 || (a.groups && a.D % a.groups))
+    return FS_ERR_INVALID_ARG;
+  if (!(a.eps >= 0.f) || !(a.eps <= 1e30f) || !(a.scale - a.scale == 0.f)) return FS_ERR_INVALID_ARG;
+  if (dtype == FS_FP32 && res_dtype != FS_FP32) return FS_ERR_UNSUPPORTED;
+  if (a.D > 16384) return FS_ERR_UNSUPPORTED;
+  for (long long s : {a.xs, a.gs, a.rs, a.zs, a.ys, a.dzs, a.dys, a.dxs, a.dgs, a.drs})
+    if (s < 0) return FS_ERR_INVALID_ARG;
+  // outputs whose rows lie on one another
+  const struct { const void *p; long long s; } outs[] = {
+      {a.z, a.zs}, {a.y, a.ys}, {a.dx, a.dxs}, {a.dgate, a.dgs}, {a.dres, a.drs}};
+  for (const auto &o : outs)
+    if (o.p && a.M > 1 && o.s < a.D) return FS_ERR_INVALID_ARG;
+  const uintptr_t x = dtype == FS_FP32 ? 4 : 2, r = res_dtype == FS_FP32 ? 4 : 2;
+  for (const void *p : {a.x, a.gate, (const void *)a.y, a.dy, (const void *)a.dx, (const void *)a.dgate})
+    if (reinterpret_cast<uintptr_t>(p) % x) return FS_ERR_INVALID_ARG;
+  for (const void *p : {a.residual, (const void *)a.z, a.dz, (const void *)a.dres})
+    if (reinterpret_cast<uintptr_t>(p) % r) return FS_ERR_INVALID_ARG;
+  for (const void *p : {(const void *)a.gain, (const void *)a.next_gain, (const void *)a.dgain,
+                        (const void *)a.dnext, (const void *)a.ws})
+    if (reinterpret_cast<uintptr_t>(p) % 4) return FS_ERR_INVALID_ARG;
+  return FS_OK;
+}
+
+NormArgs norm_args(const void *x, long long x_stride, int dtype, const void *gate,
+                   long long gate_stride, const void *residual, long long residual_stride,
+                   int res_dtype, const float *gain, const float *next_gain, int M, int D, int groups,
+                   float scale, float eps) {
+  NormArgs a{};
+  a.x = x;
+  a.gate = gate;
+  a.residual = residual;
+  // (a stride that no second row uses may be anything)
+  a.xs = M > 1 ? x_stride : 0;
+  a.gs = M > 1 && gate ? gate_stride : 0;
+  a.rs = M > 1 && residual ? residual_stride : 0;
+  a.x_f32 = dtype == FS_FP32;
+  a.r_f32 = res_dtype == FS_FP32;
+  a.gain = gain;
+  a.next_gain = next_gain;
+  a.M = M;
+  a.D = D;
+  a.groups = groups;
+  a.scale = scale;
+  a.eps = eps;
+  return a;
+}
+
+}  // namespace
+
+extern "C" int fs_block_norm(const void *x, long long x_stride, int dtype, const void *gate,
+                             long long gate_stride, const void *residual,
+                             long long residual_stride, int res_dtype, const float *gain,
+                             const float *next_gain, int M, int D, int groups, float scale,
+                             float eps, void *z, long long z_stride, void *y, long long y_stride,
+                             void *stream) {
+  NormArgs a = norm_args(x, x_stride, dtype, gate, gate_stride, residual, residual_stride, res_dtype,
+                         gain, next_gain, M, D, groups, scale, eps);
+  a.z = z;
+  a.y = y;
+  a.zs = M > 1 && z ? z_stride : 0;
+  a.ys = M > 1 && y ? y_stride : 0;
+  a.next = y != nullptr;
+  if (!z && !y) return FS_ERR_INVALID_ARG;
+  FS_TRY(check_norm(a, dtype, res_dtype));
+  return status_of(launch_norm(a, static_cast<cudaStream_t>(stream)));
+}
+
+extern "C" size_t fs_block_norm_workspace_bytes(int M, int D) {
+  return M < 1 || D < 1 || D > 16384 ? 0 : norm_workspace_bytes(M, D);
+}
+
+extern "C" int fs_block_norm_bwd(const void *x, long long x_stride, int dtype, const void *gate,
+                                 long long gate_stride, const void *residual,
+                                 long long residual_stride, int res_dtype, const float *gain,
+                                 const float *next_gain, int M, int D, int groups, float scale,
+                                 float eps, const void *dz, long long dz_stride, const void *dy,
+                                 long long dy_stride, void *dx, long long dx_stride, void *dgate,
+                                 long long dgate_stride, void *dresidual,
+                                 long long dresidual_stride, float *dgain, float *dnext_gain,
+                                 void *ws, size_t ws_bytes, void *stream) {
+  NormArgs a = norm_args(x, x_stride, dtype, gate, gate_stride, residual, residual_stride, res_dtype,
+                         gain, next_gain, M, D, groups, scale, eps);
+  a.dz = dz;
+  a.dy = dy;
+  a.dx = dx;
+  a.dgate = dgate;
+  a.dres = dresidual;
+  a.dzs = M > 1 && dz ? dz_stride : 0;
+  a.dys = M > 1 && dy ? dy_stride : 0;
+  a.dxs = M > 1 ? dx_stride : 0;
+  a.dgs = M > 1 && dgate ? dgate_stride : 0;
+  a.drs = M > 1 && dresidual ? dresidual_stride : 0;
+  a.next = dy != nullptr;
+  a.dgain = dgain;
+  a.dnext = dnext_gain;
+  a.ws = static_cast<float *>(ws);
+  if ((!dz && !dy) || !dx || (dgate && !gate) || (dnext_gain && !dy)) return FS_ERR_INVALID_ARG;
+  FS_TRY(check_norm(a, dtype, res_dtype));
+  if ((dgain || dnext_gain) && (!ws || ws_bytes < norm_workspace_bytes(M, D))) return FS_ERR_INVALID_ARG;
+  return status_of(launch_norm_bwd(a, static_cast<cudaStream_t>(stream)));
+}
+
 namespace fs {
 namespace {
 // One CTA waits on an mbarrier that nothing ever completes: the bounded wait

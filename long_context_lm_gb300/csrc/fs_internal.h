@@ -183,4 +183,67 @@ struct TreeArgs {
 size_t tree_workspace_bytes(const fs_cache &c, int H, int T);
 cudaError_t launch_tree(const TreeArgs &a, cudaStream_t st);
 
+// Linear attention with a decay for each head (k14_linear.cu): one sweep
+//   out_t = scale (state before t, decayed, + sum over the sweep's tokens up to t)
+// over the tokens of every (sequence, head), in order or in reverse.  The
+// forward is one sweep; the gradients are three, with q, k, v and dout in
+// other places.  A head h of the sweep reads head h / share of a tensor.
+// In reverse the state enters the first token without a decay and is decayed
+// once more after the last (it is lam R of the token behind).
+struct LinearRows {
+  const void *x;       // bf16
+  long long s[3];      // elements between sequences, heads, tokens
+  int share;
+};
+struct LinearSweep {
+  LinearRows q, k, v;
+  void *out;
+  long long os[3];
+  bool out_f32;            // parts of a sum over heads: contiguous fp32
+  const float *state;      // [batch, H, d, d] or null (zeros)
+  float *state_out;        // or null; may be `state`
+  bool transposed;         // both are held [value][key]
+  float state_mul;         // what the given state is multiplied by; its inverse for state_out
+  bool reverse;
+};
+struct LinearArgs {
+  LinearSweep sweep[3];
+  int sweeps;
+  int batch, H, T, d;
+  const float *decay;
+  const int32_t *count;
+  float scale;
+};
+cudaError_t launch_linear_recurrent(const LinearArgs &a, cudaStream_t st);
+struct LinearSumArgs {
+  const float *part;   // [batch, H, T, d]
+  void *out;           // bf16 [batch, H / share, T, d]
+  long long os[3];
+  int batch, H, share, T, d;
+  const int32_t *count;
+};
+cudaError_t launch_linear_sum(const LinearSumArgs &a, cudaStream_t st);
+
+// Norms around a block (k15_norm.cu).  Row strides in elements.
+struct NormArgs {
+  const void *x, *gate, *residual;   // gate, residual: or null
+  long long xs, gs, rs;
+  bool x_f32, r_f32;
+  const float *gain, *next_gain;     // or null (ones)
+  int M, D, groups;                  // groups 0: no norm after the block
+  bool next;
+  float scale, eps;
+  void *z, *y;                       // forward
+  long long zs, ys;
+  const void *dz, *dy;               // backward: either may be null
+  long long dzs, dys;
+  void *dx, *dgate, *dres;           // dgate, dres: or null
+  long long dxs, dgs, drs;
+  float *dgain, *dnext;              // or null
+  float *ws;
+};
+size_t norm_workspace_bytes(int M, int D);
+cudaError_t launch_norm(const NormArgs &a, cudaStream_t st);
+cudaError_t launch_norm_bwd(const NormArgs &a, cudaStream_t st);
+
 }  // namespace fs

@@ -38,7 +38,10 @@ SYMBOLS = ["fs_default_params", "fs_status_string", "fs_last_cuda_error", "fs_wo
            "fs_fsb_workspace_bytes", "fs_fsb_select",
            "fs_rope_make_plan", "fs_rope", "fs_cache_row_bytes", "fs_cache_append",
            "fs_cache_read", "fs_cache_accept", "fs_tree_workspace_bytes", "fs_tree_attn",
-           "fs_selftest_tree_wait"]
+           "fs_selftest_tree_wait", "fs_linear_workspace_bytes", "fs_linear_attn",
+           "fs_linear_attn_bwd", "fs_block_norm", "fs_block_norm_workspace_bytes",
+           "fs_block_norm_bwd"]
+FS_LINEAR_STEPS = 16
 FS_ROPE_LAYOUTS = {"half": 0, "pairs": 1}
 FS_ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "ramp": 3}
 FS_CACHE_FORMATS = {"bf16": 0, "e4m3": 1, "int8": 2, "int4": 3}
@@ -165,8 +168,20 @@ def load(build_if_stale: bool = True):
         L.fs_tree_attn.argtypes = [P, PC, P, P, P, I, I, I, F, P, P, Z, P]
         L.fs_selftest_tree_wait.argtypes = [P, PC, P, P, P, I, I, I, F, P, P, Z,
                                             ctypes.c_longlong, P]
+        LL = ctypes.c_longlong
+        L.fs_linear_workspace_bytes.argtypes = [I, I, I, I, I, I]
+        L.fs_linear_workspace_bytes.restype = Z
+        L.fs_linear_attn.argtypes = [P, P, P, S3, S3, S3, P, I, I, I, I, I, P, F, P, P, P, S3, P, Z, P]
+        L.fs_linear_attn_bwd.argtypes = [P, P, P, S3, S3, S3, P, I, I, I, I, I, P, F, P, P, S3, P, P,
+                                         P, P, S3, S3, S3, P, P, Z, P]
+        L.fs_block_norm.argtypes = [P, LL, I, P, LL, P, LL, I, P, P, I, I, I, F, F, P, LL, P, LL, P]
+        L.fs_block_norm_workspace_bytes.argtypes = [I, I]
+        L.fs_block_norm_workspace_bytes.restype = Z
+        L.fs_block_norm_bwd.argtypes = [P, LL, I, P, LL, P, LL, I, P, P, I, I, I, F, F, P, LL, P, LL, P,
+                                        LL, P, LL, P, LL, P, P, P, Z, P]
         for name in SYMBOLS:
-            if name not in ("fs_cache_row_bytes", "fs_tree_workspace_bytes",
+            if name not in ("fs_linear_workspace_bytes", "fs_block_norm_workspace_bytes",
+                            "fs_cache_row_bytes", "fs_tree_workspace_bytes",
                             "fs_default_params", "fs_status_string", "fs_last_cuda_error",
                             "fs_workspace_bytes", "fs_prune_static_scratch_bytes",
                             "fs_prune_workspace_bytes", "fs_window_workspace_bytes",
@@ -960,3 +975,222 @@ def _tree_attn(fn, where, more, q, cache, past, tree, count, window, scale, out,
             _counts(cache, "count", count), tp, H, T, max(-1, min(int(window), _INT_MAX)),
             d ** -0.5 if scale is None else float(scale), op, wp, ws.numel(), *more)
     return out
+
+
+# ---------------------------------------------------------------------------
+# linear attention with a decay for each head, the norms around a block
+# ---------------------------------------------------------------------------
+
+def _scratch(ws, dev):
+    """Pointer and bytes of a workspace."""
+    p = _on(ws, dev, "ws", torch.uint8)
+    if not ws.is_contiguous():  # its bytes would not be ws.numel() bytes of memory
+        raise ValueError("ws must be contiguous")
+    return p, ws.numel()
+
+
+def fs_linear_workspace(batch, H, Hkv, T, d, device, backward=False):
+    """A workspace for fs_linear_attn (or, ``backward``, fs_linear_attn_bwd) of this shape, one call
+    at a time; ``fs_check_status(ws)`` raises if a bounded wait of a call gave up."""
+    if max(batch, H, Hkv, T, d) > _INT_MAX:
+        raise ValueError("a size does not fit 32 bits")
+    n = load().fs_linear_workspace_bytes(batch, H, Hkv, T, d, 1 if backward else 0)
+    if n == 0:
+        raise FSError(FS_ERR_INVALID_ARG, "fs_linear_workspace_bytes")
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    ws[:256].zero_()  # the error word, which no call clears
+    return ws
+
+
+def _linear_inputs(q, k, v, decay, count):
+    dev = _cuda(q, "q")
+    if q.dim() != 4:
+        raise ValueError("q must be [batch, H, T, d]")
+    B, H, T, d = q.shape
+    qp, qs = _rows(q, dev, "q", torch.bfloat16, q.shape)
+    Hkv = k.shape[1] if isinstance(k, torch.Tensor) and k.dim() == 4 else 0
+    shape = (B, Hkv, T, d)
+    kp, ks = _rows(k, dev, "k", torch.bfloat16, shape)
+    vp, vs = _rows(v, dev, "v", torch.bfloat16, shape)
+    gp = _on(decay, dev, "decay", torch.float32, (H,))
+    cp = None if count is None else _on(count, dev, "count", torch.int32, (B,))
+    return dev, Hkv, (qp, kp, vp, qs, ks, vs, gp, B, H, Hkv, T, d, cp)
+
+
+def fs_linear_attn(q, k, v, decay, state=None, state_out=None, count=None, scale=None, out=None,
+                   ws=None, stream=None):
+    """Linear attention with a decay for each head: S = exp(decay) S + k v^T, out = scale q S, token
+    after token.  q [batch, H, T, d], k, v [batch, Hkv, T, d] bf16, any 16-byte aligned strides with
+    the d values together; ``decay`` [H] fp32, 0 or below; ``state`` [batch, H, d, d] fp32 before the
+    first token (None: zeros); ``state_out`` receives the one after the last (may be ``state``);
+    ``count`` [batch]: tokens of each sequence (None: T); ``scale`` default d ** -0.5.  T = 1 is a
+    decoding step.  Returns out [batch, H, T, d] bf16; rows past count[b] are left as they were (a
+    new ``out`` starts as zeros when ``count`` is given)."""
+    L = _lib or load()
+    dev, Hkv, args = _linear_inputs(q, k, v, decay, count)
+    B, H, T, d = q.shape
+    if out is None:
+        out = _new(stream, lambda: torch.empty_like(q, memory_format=torch.contiguous_format)
+                   if count is None else torch.zeros_like(q, memory_format=torch.contiguous_format))
+    op, os_ = _rows(out, dev, "out", torch.bfloat16, q.shape)
+    shape = (B, H, d, d)
+    sp = None if state is None else _on(state, dev, "state", torch.float32, shape)
+    tp = None if state_out is None else _on(state_out, dev, "state_out", torch.float32, shape)
+    wp, wn = None, 0
+    if ws is None and T > FS_LINEAR_STEPS:
+        ws = _new(stream, lambda: fs_linear_workspace(B, H, Hkv, T, d, dev))
+    if ws is not None:
+        wp, wn = _scratch(ws, dev)
+    _launch(dev, stream, L.fs_linear_attn, "fs_linear_attn", *args,
+            d ** -0.5 if scale is None else float(scale), sp, tp, op, os_, wp, wn)
+    return out
+
+
+def fs_linear_attn_bwd(q, k, v, decay, dout, state=None, dstate_out=None, count=None, scale=None,
+                       dq=None, dk=None, dv=None, dstate=None, ws=None, stream=None):
+    """Gradients of sum(dout * out) + sum(dstate_out * state_out) of fs_linear_attn: dq, dk and dv
+    (bf16, as q, k and v), and the gradient of ``state`` into ``dstate`` [batch, H, d, d] fp32 where
+    that is given.  Rows past count[b] are left as they were (new tensors start as zeros when
+    ``count`` is given).  Returns (dq, dk, dv)."""
+    L = _lib or load()
+    dev, Hkv, args = _linear_inputs(q, k, v, decay, count)
+    B, H, T, d = q.shape
+    dp, ds = _rows(dout, dev, "dout", torch.bfloat16, q.shape)
+    grads, ptrs, strides = [], [], []
+    for name, t, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
+        if t is None:
+            t = _new(stream, lambda: torch.empty_like(like, memory_format=torch.contiguous_format)
+                     if count is None else
+                     torch.zeros_like(like, memory_format=torch.contiguous_format))
+        p, s = _rows(t, dev, name, torch.bfloat16, like.shape)
+        grads.append(t), ptrs.append(p), strides.append(s)
+    shape = (B, H, d, d)
+    sp, gp, tp = (None if t is None else _on(t, dev, name, torch.float32, shape) for name, t in
+                  (("state", state), ("dstate_out", dstate_out), ("dstate", dstate)))
+    if ws is None:
+        ws = _new(stream, lambda: fs_linear_workspace(B, H, Hkv, T, d, dev, backward=True))
+    wp, wn = _scratch(ws, dev)
+    _launch(dev, stream, L.fs_linear_attn_bwd, "fs_linear_attn_bwd", *args,
+            d ** -0.5 if scale is None else float(scale), sp, dp, ds, gp, *ptrs, *strides, tp, wp, wn)
+    return tuple(grads)
+
+
+def _matrix(t, dev, name, dtype, shape):
+    """Pointer and row stride of a [..., D] tensor of ``shape`` whose rows lie evenly apart."""
+    if not isinstance(t, torch.Tensor) or t.device != dev:
+        raise ValueError(f"{name} must be a tensor on {dev}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, not {list(t.shape)}")
+    if t.is_contiguous():
+        return t.data_ptr(), shape[-1]
+    if t.stride(-1) != 1 and shape[-1] > 1:
+        raise ValueError(f"{name}: the elements of a row must be contiguous")
+    axes = [(n, s) for n, s in zip(t.shape[:-1], t.stride()[:-1]) if n > 1]
+    for (_, outer), (n, inner) in zip(axes, axes[1:]):
+        if outer != n * inner:
+            raise ValueError(f"{name}: its rows must lie evenly apart, as a matrix's do")
+    return t.data_ptr(), axes[-1][1] if axes else shape[-1]
+
+
+_NORM_DTYPES = (torch.bfloat16, torch.float32)
+
+
+def _norm_inputs(x, gate, residual, gain, next_gain, groups, res_dtype):
+    dev, dt = _cuda(x, "x"), x.dtype
+    if dt not in _NORM_DTYPES or res_dtype not in _NORM_DTYPES:
+        raise ValueError(f"x has dtype {dt}, the residual {res_dtype}: expected bfloat16 or float32")
+    shape = x.shape
+    if not shape or shape[-1] < 1:
+        raise ValueError("x must be [..., D]")
+    D = shape[-1]
+    M = x.numel() // D
+    if M > _INT_MAX or not -_INT_MAX <= groups <= _INT_MAX:
+        raise ValueError("a size does not fit 32 bits")
+    xp, xs = _matrix(x, dev, "x", dt, shape)
+    gp, gs = (None, 0) if gate is None else _matrix(gate, dev, "gate", dt, shape)
+    rp, rs = (None, 0) if residual is None else _matrix(residual, dev, "residual", res_dtype, shape)
+    a = None if gain is None else _on(gain, dev, "gain", torch.float32, (D,))
+    b = None if next_gain is None else _on(next_gain, dev, "next_gain", torch.float32, (D,))
+    return dev, (xp, xs, FS_BF16 if dt == torch.bfloat16 else FS_FP32, gp, gs, rp, rs,
+                 FS_BF16 if res_dtype == torch.bfloat16 else FS_FP32, a, b, M, D, int(groups))
+
+
+def fs_block_norm(x, gate=None, residual=None, groups=0, gain=None, next_norm=False, next_gain=None,
+                  scale=1.0, eps=1e-6, z=None, y=None, stream=None):
+    """The norms after and before a block, its gate and its residual scale, for x [..., D]:
+    a = x, RMS-normalised in ``groups`` groups of its row (0: not), times ``gain`` [D] fp32, times
+    silu(``gate``); z = ``residual`` + ``scale`` a; y = z RMS-normalised, times ``next_gain``
+    (``next_norm``, or a given ``y``).  x, gate and y are bf16 or fp32, residual and z bf16 or fp32 of
+    their own (z without a residual: x's type, or a given ``z``'s).  z may be x or the residual, y
+    may be x or gate (in place).  Returns (z, y), y None without the second norm."""
+    L = _lib or load()
+    res_dtype = residual.dtype if residual is not None else z.dtype if z is not None else x.dtype
+    dev, args = _norm_inputs(x, gate, residual, gain, next_gain, groups, res_dtype)
+    if z is None:
+        z = _new(stream, lambda: torch.empty(x.shape, dtype=res_dtype, device=dev))
+    zp, zs = _matrix(z, dev, "z", res_dtype, x.shape)
+    yp, ys = None, 0
+    if next_norm and y is None:
+        y = _new(stream, lambda: torch.empty(x.shape, dtype=x.dtype, device=dev))
+    if y is not None:
+        yp, ys = _matrix(y, dev, "y", x.dtype, x.shape)
+    elif next_gain is not None:
+        raise ValueError("next_gain without next_norm")
+    _launch(dev, stream, L.fs_block_norm, "fs_block_norm", *args, float(scale), float(eps), zp, zs, yp,
+            ys)
+    return z, y
+
+
+def fs_block_norm_workspace(M, D, device):
+    """A workspace for fs_block_norm_bwd of M rows of D elements (one call at a time)."""
+    if max(M, D) > _INT_MAX:
+        raise ValueError("a size does not fit 32 bits")
+    n = load().fs_block_norm_workspace_bytes(M, D)
+    if n == 0:
+        raise FSError(FS_ERR_INVALID_ARG, "fs_block_norm_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def fs_block_norm_bwd(x, dz=None, dy=None, gate=None, residual=None, groups=0, gain=None,
+                      next_gain=None, scale=1.0, eps=1e-6, dx=None, dgate=None, dresidual=None,
+                      ws=None, stream=None):
+    """Gradients of sum(dz * z) + sum(dy * y) of fs_block_norm with the same x, gate, residual,
+    groups, gains, scale and eps (``dy`` None: without the second norm).  Returns a dict of the
+    gradients of "x", "gate", "residual", "gain" and "next_gain", None where there is no such input.
+    dx may be x or dy, dgate may be gate, dresidual may be dz or residual (in place)."""
+    L = _lib or load()
+    if dz is None and dy is None:
+        raise ValueError("give dz or dy")
+    res_dtype = residual.dtype if residual is not None else dz.dtype if dz is not None else x.dtype
+    dev, args = _norm_inputs(x, gate, residual, gain, next_gain, groups, res_dtype)
+    shape, M, D = x.shape, args[10], args[11]
+    if dy is None and next_gain is not None:
+        raise ValueError("next_gain without dy")
+    dzp, dzs = (None, 0) if dz is None else _matrix(dz, dev, "dz", res_dtype, shape)
+    dyp, dys = (None, 0) if dy is None else _matrix(dy, dev, "dy", x.dtype, shape)
+    grads = []
+    for name, t, of, dt in (("dx", dx, x, x.dtype), ("dgate", dgate, gate, x.dtype),
+                            ("dresidual", dresidual, residual, res_dtype)):
+        if of is None:
+            if t is not None:
+                raise ValueError(f"{name} without its input")
+            grads.append((None, None, 0))
+            continue
+        if t is None:
+            t = _new(stream, lambda: torch.empty(shape, dtype=dt, device=dev))
+        grads.append((t, *_matrix(t, dev, name, dt, shape)))
+    sums = [None if t is None else
+            _new(stream, lambda: torch.empty(D, dtype=torch.float32, device=dev))
+            for t in (gain, next_gain)]
+    wp, wn = None, 0
+    if gain is not None or next_gain is not None:
+        if ws is None:
+            ws = _new(stream, lambda: fs_block_norm_workspace(M, D, dev))
+        wp, wn = _scratch(ws, dev)
+    _launch(dev, stream, L.fs_block_norm_bwd, "fs_block_norm_bwd", *args, float(scale), float(eps),
+            dzp, dzs, dyp, dys, *(x for _, p, s in grads for x in (p, s)),
+            *(None if t is None else t.data_ptr() for t in sums), wp, wn)
+    return {"x": grads[0][0], "gate": grads[1][0], "residual": grads[2][0], "gain": sums[0],
+            "next_gain": sums[1]}
