@@ -1082,20 +1082,31 @@ LinearRows linear_rows(const void *x, const long long (&s)[3], int share) {
   return r;
 }
 
-// The workspace: the header with the error word, the parts of shared heads' gradients.
+// The workspace: the header with the error word, the states between stretches, the parts
+// of shared heads' gradients.
 struct LinearLayout {
-  size_t dk, dv, total;
+  size_t states, dk, dv, total;
 };
 LinearLayout linear_layout(int batch, int H, int Hkv, int T, int d, bool backward) {
   LinearLayout L{};
   size_t off = kHeader;
   const size_t part = backward && H > Hkv ? (size_t)batch * H * T * d * 4 : 0;
+  L.states = off;
+  if (T > FS_LINEAR_STEPS)
+    off = align_up(off + linear_chunk_bytes(backward ? 3 : 1, batch, H, T, d));
   L.dk = off;
   off = align_up(off + part);
   L.dv = off;
   off = align_up(off + part);
   L.total = off;
   return L;
+}
+
+int linear_sweeps(const LinearArgs &a, const LinearLayout &L, void *ws, cudaStream_t st) {
+  if (a.T <= FS_LINEAR_STEPS) return status_of(launch_linear_recurrent(a, st));
+  char *base = static_cast<char *>(ws);
+  return status_of(launch_linear_chunks(a, reinterpret_cast<float *>(base + L.states),
+                                        reinterpret_cast<int *>(base), st));
 }
 
 }  // namespace
@@ -1124,8 +1135,9 @@ extern "C" int fs_linear_attn(const void *q, const void *k, const void *v, const
   FS_TRY(check_linear_out(out, os, batch, H, T));
   if (out == q || out == k || out == v) return FS_ERR_INVALID_ARG;
   FS_TRY(check_states(state, state_out, true, (size_t)batch * H * d * d));
-  if (ws ? ws_bytes < linear_layout(batch, H, Hkv, T, d, false).total : T > FS_LINEAR_STEPS)
-    return FS_ERR_INVALID_ARG;
+  const LinearLayout L = linear_layout(batch, H, Hkv, T, d, false);
+  if (ws ? ws_bytes < L.total : T > FS_LINEAR_STEPS) return FS_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(ws) % 16) return FS_ERR_UNSUPPORTED;
   LinearArgs a{};
   a.sweeps = 1;
   LinearSweep &w = a.sweep[0];
@@ -1144,7 +1156,7 @@ extern "C" int fs_linear_attn(const void *q, const void *k, const void *v, const
   a.decay = decay;
   a.count = count;
   a.scale = scale;
-  return status_of(launch_linear_recurrent(a, static_cast<cudaStream_t>(stream)));
+  return linear_sweeps(a, L, ws, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" int fs_linear_attn_bwd(
@@ -1219,7 +1231,7 @@ extern "C" int fs_linear_attn_bwd(
   a.count = count;
   a.scale = scale;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  FS_TRY(status_of(launch_linear_recurrent(a, st)));
+  FS_TRY(linear_sweeps(a, L, ws, st));
   for (int i = 0; share > 1 && i < 2; ++i) {
     LinearSumArgs s{};
     s.part = part[i];
