@@ -245,6 +245,8 @@ struct NormArgs {
   long long dxs, dgs, drs;
   float *dgain, *dnext;              // or null
   float *ws;
+  int mode, per, list;               // set by the launch: how groups are added, vectors
+  float inv_n, inv_D;                // (elements) of a group, floats of a team's list
 };
 size_t norm_workspace_bytes(int M, int D);
 cudaError_t launch_norm(const NormArgs &a, cudaStream_t st);

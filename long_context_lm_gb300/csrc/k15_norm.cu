@@ -19,60 +19,117 @@
 // into the workspace and a second kernel adds them in block order.
 #include "fs_common.cuh"
 #include "fs_internal.h"
+#include "pairs.cuh"
 
 namespace fs {
 namespace {
 
-// Up to 16 bytes of a row's elements as fp32.
+// How a row's groups are added up.
+enum Groups { kNone, kRow, kShuffle, kList };
+
+// Sixteen bytes of a row of TX, or as many elements of TR: as they are in memory.
 template <typename T, int V>
-__device__ __forceinline__ void load(const void *p, long long at, float (&x)[V]) {
-  const T *s = static_cast<const T *>(p) + at;
-  if constexpr (V == 1) {
-    x[0] = static_cast<float>(*s);
-  } else if constexpr (sizeof(T) == 4) {
+struct Raw {
+  f2 x[V / 2];
+  __device__ __forceinline__ f2 get(int c) const { return x[c]; }
+};
+template <int V>
+struct Raw<__nv_bfloat16, V> {
+  uint32_t x[V / 2];
+  __device__ __forceinline__ f2 get(int c) const { return wide2(x[c]); }
+};
+
+// kWhole: rows are whole vectors on sixteen bytes.  Otherwise element by element.
+template <bool kWhole, typename T, int V>
+__device__ __forceinline__ void load(const void *row, int e, int D, Raw<T, V> &r) {
+  const T *p = static_cast<const T *>(row) + e;
+  if constexpr (kWhole) {
 #pragma unroll
-    for (int i = 0; i < V; i += 4) {
-      const float4 u = *reinterpret_cast<const float4 *>(s + i);
-      x[i] = u.x, x[i + 1] = u.y, x[i + 2] = u.z, x[i + 3] = u.w;
+    for (int c = 0; c < V / 2; ++c) r.x[c] = 0;
+    if (e >= D) return;
+    if constexpr (sizeof(T) == 2) {
+      const uint4 u = *reinterpret_cast<const uint4 *>(p);
+      r.x[0] = u.x, r.x[1] = u.y, r.x[2] = u.z, r.x[3] = u.w;
+    } else {
+#pragma unroll
+      for (int c = 0; c < V / 2; c += 2) {
+        const ulonglong2 u = *reinterpret_cast<const ulonglong2 *>(p + 2 * c);
+        r.x[c] = u.x, r.x[c + 1] = u.y;
+      }
     }
   } else {
-    static_assert(V == 8, "sixteen bytes");
-    const uint4 u = *reinterpret_cast<const uint4 *>(s);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[2 * i] = bf16_lo(w[i]), x[2 * i + 1] = bf16_hi(w[i]);
+    for (int c = 0; c < V / 2; ++c) {
+      const float x = e + 2 * c < D ? static_cast<float>(p[2 * c]) : 0.f;
+      const float y = e + 2 * c + 1 < D ? static_cast<float>(p[2 * c + 1]) : 0.f;
+      if constexpr (sizeof(T) == 2)
+        r.x[c] = pack_bf16(x, y);  // (bf16 numbers: nothing is rounded)
+      else
+        r.x[c] = f2_bits(x, y);
+    }
   }
 }
-template <typename T, int V>
-__device__ __forceinline__ void store(void *p, long long at, const float (&x)[V]) {
-  T *s = static_cast<T *>(p) + at;
-  if constexpr (V == 1) {
-    *s = static_cast<T>(x[0]);
-  } else if constexpr (sizeof(T) == 4) {
+template <bool kWhole, typename T, int V>
+__device__ __forceinline__ void store(void *row, int e, int D, const f2 (&x)[V / 2]) {
+  T *p = static_cast<T *>(row) + e;
+  if constexpr (kWhole) {
+    if (e >= D) return;
+    if constexpr (sizeof(T) == 2) {
+      *reinterpret_cast<uint4 *>(p) = make_uint4(pack2(x[0]), pack2(x[1]), pack2(x[2]), pack2(x[3]));
+    } else {
 #pragma unroll
-    for (int i = 0; i < V; i += 4)
-      *reinterpret_cast<float4 *>(s + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+      for (int c = 0; c < V / 2; c += 2)
+        *reinterpret_cast<ulonglong2 *>(p + 2 * c) = make_ulonglong2(x[c], x[c + 1]);
+    }
   } else {
-    *reinterpret_cast<uint4 *>(s) = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]),
-                                               pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+#pragma unroll
+    for (int c = 0; c < V / 2; ++c) {
+      if (e + 2 * c < D) p[2 * c] = static_cast<T>(lo2(x[c]));
+      if (e + 2 * c + 1 < D) p[2 * c + 1] = static_cast<T>(hi2(x[c]));
+    }
   }
 }
 
-// 1 / (1 + e^-x).  bf16 results need no more than the special-function unit's
-// exponential and reciprocal (2^-20 or better); fp32 ones take the exact pair.
+// 1 / (1 + e^-x) by the special-function unit: 2^-20 of itself, enough for bf16 results.
+// kExact: with the exponent's rounding put back and a Newton step on the reciprocal, 2^-22.
 template <bool kExact>
 __device__ __forceinline__ float sigmoid(float x) {
-  if constexpr (kExact) return 1.f / (1.f + expf(-x));
-  return __fdividef(1.f, 1.f + __expf(-x));
+  constexpr float kL = -1.44269504f, kRest = -1.92596303e-8f;  // -log2 e, what it lacks
+  float t = x * kL, e, r;
+  if constexpr (kExact) t = fminf(t, 126.f);  // (past it the Newton step would meet an infinity)
+  asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(t));
+  if constexpr (kExact) {
+    const float rest = fmaf(x, kL, -t) + x * kRest;
+    if (t < 126.f) e = fmaf(e, rest * 0.693147181f, e);
+  }
+  const float d = 1.f + e;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(d));
+  if constexpr (kExact) r = fmaf(r, fmaf(-d, r, 1.f), r);
+  return r;
+}
+template <bool kExact>
+__device__ __forceinline__ f2 sigmoid2(f2 x) {
+  return f2_bits(sigmoid<kExact>(lo2(x)), sigmoid<kExact>(hi2(x)));
 }
 
-// A team's rows and its way to add.  TPR threads take a row, N vectors of V
-// elements each: vector i of thread t is number t + i TPR of the row.
-template <int TPR, int V, int N>
+// A number for each group, beside the elements of a vector: one for all where vectors are whole.
+template <bool kWhole, int V>
+struct PerGroup {
+  f2 x[kWhole ? 1 : V / 2];
+  __device__ __forceinline__ f2 get(int c) const { return x[kWhole ? 0 : c]; }
+};
+
+__device__ __forceinline__ f2 both(float x) { return f2_bits(x, x); }
+
+// A team's way to add.  TPR threads take a row, N vectors of V elements each: vector i of
+// thread t is number t + i TPR of the row.
+template <int TPR, int V, int N, bool kWhole>
 struct Team {
   static constexpr int kThreads = TPR < 256 ? 256 : TPR, kTeams = kThreads / TPR;
+  static constexpr int kLanes = TPR < 32 ? TPR : 32;
   int t, team;    // thread within the team, team within the block
   float *scratch; // TPR > 32: two halves of the team's warps, in turn
+  float *list;    // sums of vectors (elements), then of groups
   int turn;
 
   __device__ __forceinline__ void sync() const {
@@ -87,7 +144,7 @@ struct Team {
   template <int K>
   __device__ __forceinline__ void add(float (&x)[K]) {
 #pragma unroll
-    for (int m = 1; m < (TPR < 32 ? TPR : 32); m *= 2)
+    for (int m = 1; m < kLanes; m *= 2)
 #pragma unroll
       for (int k = 0; k < K; ++k) x[k] += __shfl_xor_sync(0xffffffffu, x[k], m);
     if constexpr (TPR > 32) {
@@ -97,262 +154,369 @@ struct Team {
 #pragma unroll
         for (int k = 0; k < K; ++k) to[k * kWarps + t / 32] = x[k];
       sync();
+      if constexpr (kWarps <= 4) {
 #pragma unroll
-      for (int k = 0; k < K; ++k) {
-        x[k] = 0.f;
-        for (int j = 0; j < kWarps; ++j) x[k] += to[k * kWarps + j];
+        for (int k = 0; k < K; ++k) {
+          x[k] = to[k * kWarps];
+#pragma unroll
+          for (int j = 1; j < kWarps; ++j) x[k] += to[k * kWarps + j];
+        }
+      } else {  // a warp adds them as it added its own
+#pragma unroll
+        for (int k = 0; k < K; ++k) x[k] = t % 32 < kWarps ? to[k * kWarps + t % 32] : 0.f;
+#pragma unroll
+        for (int m = 1; m < kWarps; m *= 2)
+#pragma unroll
+          for (int k = 0; k < K; ++k) x[k] += __shfl_xor_sync(0xffffffffu, x[k], m);
+#pragma unroll
+        for (int k = 0; k < K; ++k) x[k] = __shfl_sync(0xffffffffu, x[k], 0);
       }
     }
   }
-  // x[i] (vector i's sum) becomes the sum over the group that the vector lies in.
-  // Groups of whole vectors, a power of two of them up to a warp's: by shuffles.
-  // Others: the vectors' sums in `list`, a group to a warp (or small team) at a time.
-  __device__ __forceinline__ void add_groups(float (&x)[N], int D, int groups, float *list) {
-    if (groups == 1) {
-      float s[1] = {0.f};
+  // Sums over groups of the products f(i, c) (pair c of vector i).  Groups of a power of two
+  // of whole vectors, up to a warp's: by shuffles.  Others through `list`: a group to a
+  // warp (or small team) at a time.
+  template <typename F>
+  __device__ __forceinline__ void add_groups(PerGroup<kWhole, V> (&p)[N], const NormArgs &a, F f) {
+    const int mode = kWhole || a.mode <= kRow ? a.mode : kList;
+    const int n = kWhole ? a.D / V : a.D;
+    if (mode == kList) sync();  // (the list is free: its readers are past this)
+    float v[N];
 #pragma unroll
-      for (int i = 0; i < N; ++i) s[0] += x[i];
+    for (int i = 0; i < N; ++i) {
+      f2 s = 0;
+#pragma unroll
+      for (int c = 0; c < V / 2; ++c) {
+        const f2 x = f(i, c);
+        s = c ? add2_bits(s, x) : x;
+        if constexpr (!kWhole) {
+          const int e = (t + i * TPR) * V + 2 * c;
+          if (mode == kList && e < n) list[e] = lo2(x);
+          if (mode == kList && e + 1 < n) list[e + 1] = hi2(x);
+        }
+      }
+      v[i] = lo2(s) + hi2(s);
+    }
+    if (mode == kRow) {
+      float s[1] = {v[0]};
+#pragma unroll
+      for (int i = 1; i < N; ++i) s[0] += v[i];
       add(s);
 #pragma unroll
-      for (int i = 0; i < N; ++i) x[i] = s[0];
-      return;
-    }
-    const int per = D / groups / V;  // vectors in a group
-    constexpr int kLanes = TPR < 32 ? TPR : 32;
-    if (per <= kLanes && (per & (per - 1)) == 0) {
-      for (int m = 1; m < per; m *= 2)
+      for (int i = 0; i < N; ++i) v[i] = s[0];
+    } else if (mode == kShuffle) {
+      for (int m = 1; m < a.per; m *= 2)
 #pragma unroll
-        for (int i = 0; i < N; ++i) x[i] += __shfl_xor_sync(0xffffffffu, x[i], m);
-      return;
+        for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], m);
+    } else {
+      if constexpr (kWhole) {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+          if (t + i * TPR < n) list[t + i * TPR] = v[i];
+      }
+      sync();
+      for (int g = t / kLanes; g < a.groups; g += TPR / kLanes) {
+        float s = 0.f;
+        for (int j = t % kLanes; j < a.per; j += kLanes) s += list[g * a.per + j];
+#pragma unroll
+        for (int m = 1; m < kLanes; m *= 2) s += __shfl_xor_sync(0xffffffffu, s, m);
+        if (t % kLanes == 0) list[n + g] = s;
+      }
+      sync();
+      if constexpr (kWhole) {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+          if (t + i * TPR < n) v[i] = list[n + (t + i * TPR) / a.per];
+      } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+          for (int c = 0; c < V / 2; ++c) {
+            const int e = (t + i * TPR) * V + 2 * c;
+            p[i].x[c] = f2_bits(e < n ? list[n + e / a.per] : 0.f, e + 1 < n ? list[n + (e + 1) / a.per] : 0.f);
+          }
+        return;
+      }
     }
-    const int vectors = D / V;
-    sync();
 #pragma unroll
     for (int i = 0; i < N; ++i)
-      if (t + i * TPR < vectors) list[t + i * TPR] = x[i];
-    sync();
-    for (int g = t / kLanes; g < groups; g += TPR / kLanes) {
-      float s = 0.f;
-      for (int j = t % kLanes; j < per; j += kLanes) s += list[g * per + j];
 #pragma unroll
-      for (int m = 1; m < kLanes; m *= 2)
-        s += __shfl_xor_sync(0xffffffffu, s, m);
-      if (t % kLanes == 0) list[vectors + g] = s;
+      for (int c = 0; c < (kWhole ? 1 : V / 2); ++c) p[i].x[c] = both(v[i]);
+  }
+  // The factors that normalise x's groups (ones where they are not to be).
+  template <typename T>
+  __device__ __forceinline__ void factors(const Raw<T, V> (&x)[N], PerGroup<kWhole, V> (&inv)[N], const NormArgs &a) {
+    if (a.mode == kNone) {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int c = 0; c < (kWhole ? 1 : V / 2); ++c) inv[i].x[c] = both(1.f);
+      return;
     }
-    sync();
+    add_groups(inv, a, [&](int i, int c) { return mul2(x[i].get(c), x[i].get(c)); });
 #pragma unroll
     for (int i = 0; i < N; ++i)
-      if (t + i * TPR < vectors) x[i] = list[vectors + (t + i * TPR) / per];
+#pragma unroll
+      for (int c = 0; c < (kWhole ? 1 : V / 2); ++c) {
+        // (past the row 0: with eps 0 the factor there would be infinite)
+        const int e = (t + i * TPR) * V + 2 * c;
+        const float f = e < a.D ? rsqrtf(fmaf(lo2(inv[i].x[c]), a.inv_n, a.eps)) : 0.f;
+        const float g = kWhole ? f : e + 1 < a.D ? rsqrtf(fmaf(hi2(inv[i].x[c]), a.inv_n, a.eps)) : 0.f;
+        inv[i].x[c] = f2_bits(f, g);
+      }
   }
 };
 
-// What a team knows of its row: x (then h), the group factors, the gate's sigmoid, z.
-template <typename TX, typename TR, int TPR, int V, int N>
-struct Row {
-  float h[N][V], gate[N][V], sig[N][V], z[N][V], inv[N];
-
-  __device__ __forceinline__ void read(const NormArgs &a, long long row, int t, bool residual) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int e = (t + i * TPR) * V;
-      const bool in = e < a.D;
-#pragma unroll
-      for (int j = 0; j < V; ++j) h[i][j] = gate[i][j] = z[i][j] = 0.f;
-      if (in) load<TX, V>(a.x, row * a.xs + e, h[i]);
-      if (in && a.gate) load<TX, V>(a.gate, row * a.gs + e, gate[i]);
-      if (in && residual) load<TR, V>(a.residual, row * a.rs + e, z[i]);
-    }
-  }
-  template <typename TeamT>
-  __device__ __forceinline__ void normalise(const NormArgs &a, TeamT &team, float *list) {
-    // (vectors past the row keep a factor of 0: with eps 0 theirs would be infinite)
-    if (!a.groups) {
-#pragma unroll
-      for (int i = 0; i < N; ++i) inv[i] = 1.f;
-      return;
-    }
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      inv[i] = 0.f;
-#pragma unroll
-      for (int j = 0; j < V; ++j) inv[i] = fmaf(h[i][j], h[i][j], inv[i]);
-    }
-    team.add_groups(inv, a.D, a.groups, list);
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      inv[i] = (team.t + i * TPR) * V < a.D
-                   ? rsqrtf(inv[i] / (float)(a.D / a.groups) + a.eps)
-                   : 0.f;
-#pragma unroll
-      for (int j = 0; j < V; ++j) h[i][j] *= inv[i];
-    }
-  }
-};
-
-template <int V>
-__device__ __forceinline__ void load_gain(const float *p, int e, int D, float (&x)[V]) {
-#pragma unroll
-  for (int j = 0; j < V; ++j) x[j] = 1.f;
-  if (p && e < D) load<float, V>(p, e, x);
-}
-
-template <typename TX, typename TR, int TPR, int V, int N>
-__global__ void __launch_bounds__(Team<TPR, V, N>::kThreads) k15_norm_kernel(
-    const __grid_constant__ NormArgs a) {
-  using T = Team<TPR, V, N>;
+template <typename TX, typename TR, int TPR, int N, bool kWhole>
+__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k15_norm_kernel(const __grid_constant__ NormArgs a) {
+  constexpr int V = 16 / sizeof(TX);
+  using T = Team<TPR, V, N, kWhole>;
   extern __shared__ float lists[];
   __shared__ float scratch[T::kTeams][TPR > 32 ? 4 * TPR / 32 : 1];
-  T team{(int)threadIdx.x % TPR, (int)threadIdx.x / TPR, nullptr, 0};
+  T team{(int)threadIdx.x % TPR, (int)threadIdx.x / TPR, nullptr, nullptr, 0};
   team.scratch = scratch[team.team];
+  team.list = lists + team.team * a.list;
   // (a small team without a row keeps its warp's shuffles and barriers company)
   const long long want = (long long)blockIdx.x * T::kTeams + team.team;
   if (TPR >= 32 && want >= a.M) return;
   const bool have = want < a.M;
   const long long row = have ? want : a.M - 1;
-  float *list = lists + team.team * (a.D / V + a.groups);
+  const int e0 = team.t * V;
 
-  Row<TX, TR, TPR, V, N> r;
-  r.read(a, row, team.t, a.residual != nullptr);
-  r.normalise(a, team, list);
-  float ss[1] = {0.f};
+  Raw<TX, V> x[N], gate[N];
+  f2 z[N][V / 2];
+  {
+    const TX *xr = static_cast<const TX *>(a.x) + row * a.xs;
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    float gain[V];
-    load_gain<V>(a.gain, (team.t + i * TPR) * V, a.D, gain);
+    for (int i = 0; i < N; ++i) load<kWhole>(xr, e0 + i * TPR * V, a.D, x[i]);
+  }
+  if (a.gate) {
+    const TX *gr = static_cast<const TX *>(a.gate) + row * a.gs;
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      float x = r.h[i][j] * gain[j];
-      if (a.gate) x *= r.gate[i][j] * sigmoid<sizeof(TX) == 4>(r.gate[i][j]);
-      r.z[i][j] = fmaf(a.scale, x, r.z[i][j]);
-      ss[0] = fmaf(r.z[i][j], r.z[i][j], ss[0]);
+    for (int i = 0; i < N; ++i) load<kWhole>(gr, e0 + i * TPR * V, a.D, gate[i]);
+  }
+  Raw<TR, V> res[N];
+  if (a.residual) {
+    const TR *rr = static_cast<const TR *>(a.residual) + row * a.rs;
+#pragma unroll
+    for (int i = 0; i < N; ++i) load<kWhole>(rr, e0 + i * TPR * V, a.D, res[i]);
+  }
+  {
+    PerGroup<kWhole, V> inv[N];
+    team.factors(x, inv, a);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int c = 0; c < V / 2; ++c) z[i][c] = mul2(x[i].get(c), inv[i].get(c));
+  }
+  if (a.gain) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      Raw<float, V> g;
+      load<kWhole>(a.gain, e0 + i * TPR * V, a.D, g);
+#pragma unroll
+      for (int c = 0; c < V / 2; ++c) z[i][c] = mul2(z[i][c], g.x[c]);
     }
+  }
+  if (a.gate) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int c = 0; c < V / 2; ++c) {
+        const f2 g = gate[i].get(c);
+        z[i][c] = mul2(z[i][c], mul2(g, sigmoid2<sizeof(TX) == 4>(g)));
+      }
+  }
+  const f2 scale = both(a.scale);
+  if (a.residual) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int c = 0; c < V / 2; ++c) z[i][c] = madd2(scale, z[i][c], res[i].get(c));
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int c = 0; c < V / 2; ++c) z[i][c] = mul2(scale, z[i][c]);
   }
   float f = 0.f;
   if (a.next) {
+    f2 s = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int c = 0; c < V / 2; ++c) s = madd2(z[i][c], z[i][c], s);
+    float ss[1] = {lo2(s) + hi2(s)};
     team.add(ss);
-    f = rsqrtf(ss[0] / (float)a.D + a.eps);
+    f = rsqrtf(fmaf(ss[0], a.inv_D, a.eps));
   }
+  if (!have) return;
+  if (a.z) {
+    TR *zr = static_cast<TR *>(a.z) + row * a.zs;
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const int e = (team.t + i * TPR) * V;
-    if (e >= a.D || !have) continue;
-    if (a.z) store<TR, V>(a.z, row * a.zs + e, r.z[i]);
-    if (a.next) {
-      float gain[V];
-      load_gain<V>(a.next_gain, e, a.D, gain);
+    for (int i = 0; i < N; ++i) store<kWhole, TR, V>(zr, e0 + i * TPR * V, a.D, z[i]);
+  }
+  if (a.next) {
+    TX *yr = static_cast<TX *>(a.y) + row * a.ys;
 #pragma unroll
-      for (int j = 0; j < V; ++j) gain[j] *= r.z[i][j] * f;
-      store<TX, V>(a.y, row * a.ys + e, gain);
+    for (int i = 0; i < N; ++i) {
+#pragma unroll
+      for (int c = 0; c < V / 2; ++c) z[i][c] = mul2(z[i][c], both(f));
+      if (a.next_gain) {
+        Raw<float, V> g;
+        load<kWhole>(a.next_gain, e0 + i * TPR * V, a.D, g);
+#pragma unroll
+        for (int c = 0; c < V / 2; ++c) z[i][c] = mul2(z[i][c], g.x[c]);
+      }
+      store<kWhole, TX, V>(yr, e0 + i * TPR * V, a.D, z[i]);
     }
   }
 }
 
-template <typename TX, typename TR, int TPR, int V, int N>
-__global__ void __launch_bounds__(Team<TPR, V, N>::kThreads) k15_norm_bwd_kernel(
-    const __grid_constant__ NormArgs a) {
-  using T = Team<TPR, V, N>;
+template <typename TX, typename TR, int TPR, int N, bool kWhole>
+__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, 1) k15_norm_bwd_kernel(const __grid_constant__ NormArgs a) {
+  constexpr int V = 16 / sizeof(TX);
+  constexpr bool kExact = sizeof(TX) == 4;
+  using T = Team<TPR, V, N, kWhole>;
   extern __shared__ float lists[];
   __shared__ float scratch[T::kTeams][TPR > 32 ? 4 * TPR / 32 : 1];
-  T team{(int)threadIdx.x % TPR, (int)threadIdx.x / TPR, nullptr, 0};
+  T team{(int)threadIdx.x % TPR, (int)threadIdx.x / TPR, nullptr, nullptr, 0};
   team.scratch = scratch[team.team];
-  const int step = gridDim.x * T::kTeams;
-  float *list = lists + team.team * (a.D / V + a.groups);
-  float dgain[N][V] = {}, dnext[N][V] = {};
-  const float per_row = 1.f / (float)a.D, per_group = a.groups ? (float)a.groups / (float)a.D : 0.f;
+  team.list = lists + team.team * a.list;
+  const int step = gridDim.x * T::kTeams, e0 = team.t * V;
+  f2 dgain[N][V / 2] = {}, dnext[N][V / 2] = {};
+  const f2 scale = both(a.scale);
 
   for (long long want = (long long)blockIdx.x * T::kTeams + team.team;
        TPR >= 32 ? want < a.M : want - team.team < a.M; want += step) {
     const bool have = want < a.M;
     const long long row = have ? want : a.M - 1;
-    Row<TX, TR, TPR, V, N> r;
-    float g[N][V];
-    r.read(a, row, team.t, a.next && a.residual);
+    Raw<TX, V> x[N], gate[N], dy[N];
+    Raw<TR, V> dz[N], res[N];
+    {
+      const TX *xr = static_cast<const TX *>(a.x) + row * a.xs;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int e = (team.t + i * TPR) * V;
-#pragma unroll
-      for (int j = 0; j < V; ++j) g[i][j] = 0.f;
-      if (e < a.D && a.dz) load<TR, V>(a.dz, row * a.dzs + e, g[i]);
+      for (int i = 0; i < N; ++i) load<kWhole>(xr, e0 + i * TPR * V, a.D, x[i]);
     }
-    float dy[N][V];
+    if (a.gate) {
+      const TX *gr = static_cast<const TX *>(a.gate) + row * a.gs;
+#pragma unroll
+      for (int i = 0; i < N; ++i) load<kWhole>(gr, e0 + i * TPR * V, a.D, gate[i]);
+    }
+    if (a.dz) {
+      const TR *dr = static_cast<const TR *>(a.dz) + row * a.dzs;
+#pragma unroll
+      for (int i = 0; i < N; ++i) load<kWhole>(dr, e0 + i * TPR * V, a.D, dz[i]);
+    }
     if (a.next) {
+      const TX *dr = static_cast<const TX *>(a.dy) + row * a.dys;
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const int e = (team.t + i * TPR) * V;
+      for (int i = 0; i < N; ++i) load<kWhole>(dr, e0 + i * TPR * V, a.D, dy[i]);
+      if (a.residual) {
+        const TR *rr = static_cast<const TR *>(a.residual) + row * a.rs;
 #pragma unroll
-        for (int j = 0; j < V; ++j) dy[i][j] = 0.f;
-        if (e < a.D) load<TX, V>(a.dy, row * a.dys + e, dy[i]);
+        for (int i = 0; i < N; ++i) load<kWhole>(rr, e0 + i * TPR * V, a.D, res[i]);
       }
     }
-    r.normalise(a, team, list);
+    // h (x normalised) is worked out again where it is used: x in 16 bits and a group's
+    // factor take fewer registers
+    PerGroup<kWhole, V> inv[N];
+    team.factors(x, inv, a);
+    f2 sig[N][V / 2];
+    if (a.gate) {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int c = 0; c < V / 2; ++c) sig[i][c] = sigmoid2<kExact>(gate[i].get(c));
+    }
+    f2 g[N][V / 2];  // the gradient that reaches z
 #pragma unroll
     for (int i = 0; i < N; ++i)
 #pragma unroll
-      for (int j = 0; j < V; ++j)
-        r.sig[i][j] = a.gate ? sigmoid<sizeof(TX) == 4>(r.gate[i][j]) : 0.f;
+      for (int c = 0; c < V / 2; ++c) g[i][c] = a.dz ? dz[i].get(c) : 0;
     if (a.next) {
-      float s[2] = {0.f, 0.f};
+      f2 z[N][V / 2], s0 = 0, s1 = 0;
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        const int e = (team.t + i * TPR) * V;
-        float gain[V], next[V];
-        load_gain<V>(a.gain, e, a.D, gain);
-        load_gain<V>(a.next_gain, e, a.D, next);
+        Raw<float, V> gain, next;
+        if (a.gain) load<kWhole>(a.gain, e0 + i * TPR * V, a.D, gain);
+        if (a.next_gain) load<kWhole>(a.next_gain, e0 + i * TPR * V, a.D, next);
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-          float x = r.h[i][j] * gain[j];
-          if (a.gate) x *= r.gate[i][j] * r.sig[i][j];
-          r.z[i][j] = fmaf(a.scale, x, r.z[i][j]);
-          s[0] = fmaf(r.z[i][j], r.z[i][j], s[0]);
-          s[1] = fmaf(r.z[i][j], dy[i][j] * next[j], s[1]);
+        for (int c = 0; c < V / 2; ++c) {
+          f2 u = mul2(x[i].get(c), inv[i].get(c));
+          if (a.gain) u = mul2(u, gain.x[c]);
+          if (a.gate) u = mul2(u, mul2(gate[i].get(c), sig[i][c]));
+          u = a.residual ? madd2(scale, u, res[i].get(c)) : mul2(scale, u);
+          z[i][c] = u;
+          s0 = madd2(u, u, s0);
+          f2 w = dy[i].get(c);
+          if (a.next_gain) w = mul2(w, next.x[c]);
+          s1 = madd2(u, w, s1);
         }
       }
+      float s[2] = {lo2(s0) + hi2(s0), lo2(s1) + hi2(s1)};
       team.add(s);
-      const float f = rsqrtf(s[0] * per_row + a.eps), c = f * f * s[1] * per_row;
+      const float r = rsqrtf(fmaf(s[0], a.inv_D, a.eps));
+      const f2 rr = both(r), mc = both(-r * r * s[1] * a.inv_D);
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        float next[V];
-        load_gain<V>(a.next_gain, (team.t + i * TPR) * V, a.D, next);
+        Raw<float, V> next;
+        if (a.next_gain) load<kWhole>(a.next_gain, e0 + i * TPR * V, a.D, next);
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-          g[i][j] = fmaf(f, fmaf(-c, r.z[i][j], dy[i][j] * next[j]), g[i][j]);
-          if (have) dnext[i][j] = fmaf(dy[i][j] * f, r.z[i][j], dnext[i][j]);
+        for (int c = 0; c < V / 2; ++c) {
+          f2 w = dy[i].get(c);
+          if (have) dnext[i][c] = madd2(mul2(w, rr), z[i][c], dnext[i][c]);
+          if (a.next_gain) w = mul2(w, next.x[c]);
+          g[i][c] = madd2(rr, madd2(mc, z[i][c], w), g[i][c]);
         }
       }
     }
-    float sums[N];
+    if (a.dres && have) {
+      TR *dr = static_cast<TR *>(a.dres) + row * a.drs;
+#pragma unroll
+      for (int i = 0; i < N; ++i) store<kWhole, TR, V>(dr, e0 + i * TPR * V, a.D, g[i]);
+    }
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int e = (team.t + i * TPR) * V;
-      const bool in = e < a.D && have;
-      float gain[V], out[V];
-      load_gain<V>(a.gain, e, a.D, gain);
-      if (in && a.dres) store<TR, V>(a.dres, row * a.drs + e, g[i]);
-      sums[i] = 0.f;
+      Raw<float, V> gain;
+      if (a.gain) load<kWhole>(a.gain, e0 + i * TPR * V, a.D, gain);
+      f2 out[V / 2];
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        float u = a.scale * g[i][j];
+      for (int c = 0; c < V / 2; ++c) {
+        const f2 h = mul2(x[i].get(c), inv[i].get(c));
+        f2 u = mul2(scale, g[i][c]);
         if (a.gate) {
-          const float gate = r.gate[i][j], sig = r.sig[i][j];
-          out[j] = u * (r.h[i][j] * gain[j]) * (sig * fmaf(gate, 1.f - sig, 1.f));
-          u *= gate * sig;
+          const f2 gt = gate[i].get(c), sg = sig[i][c];
+          f2 d = mul2(u, h);
+          if (a.gain) d = mul2(d, gain.x[c]);
+          const f2 silu = mul2(gt, sg);
+          // silu' = sig (1 + gate (1 - sig)) = sig + silu - silu sig
+          out[c] = mul2(d, sub2_bits(add2_bits(sg, silu), mul2(silu, sg)));
+          u = mul2(u, silu);
         }
-        if (have) dgain[i][j] = fmaf(u, r.h[i][j], dgain[i][j]);
-        g[i][j] = u * gain[j];
-        sums[i] = fmaf(g[i][j], r.h[i][j], sums[i]);
+        if (have) dgain[i][c] = madd2(u, h, dgain[i][c]);
+        if (a.gain) u = mul2(u, gain.x[c]);
+        g[i][c] = u;
       }
-      if (in && a.dgate) store<TX, V>(a.dgate, row * a.dgs + e, out);
+      if (a.dgate && have)
+        store<kWhole, TX, V>(static_cast<TX *>(a.dgate) + row * a.dgs, e0 + i * TPR * V, a.D, out);
     }
-    if (a.groups) team.add_groups(sums, a.D, a.groups, list);
+    if (a.mode != kNone) {
+      PerGroup<kWhole, V> p[N];
+      team.add_groups(p, a, [&](int i, int c) { return mul2(g[i][c], mul2(x[i].get(c), inv[i].get(c))); });
+      const f2 mn = both(-a.inv_n);
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int e = (team.t + i * TPR) * V;
-      if (a.groups) {
-        const float c = sums[i] * per_group;
+      for (int i = 0; i < N; ++i)
 #pragma unroll
-        for (int j = 0; j < V; ++j) g[i][j] = r.inv[i] * fmaf(-c, r.h[i][j], g[i][j]);
-      }
-      if (e < a.D && have) store<TX, V>(a.dx, row * a.dxs + e, g[i]);
+        for (int c = 0; c < V / 2; ++c) {
+          const f2 h = mul2(x[i].get(c), inv[i].get(c));
+          g[i][c] = mul2(inv[i].get(c), madd2(mul2(mn, p[i].get(c)), h, g[i][c]));
+        }
+    }
+    if (have) {
+      TX *dr = static_cast<TX *>(a.dx) + row * a.dxs;
+#pragma unroll
+      for (int i = 0; i < N; ++i) store<kWhole, TX, V>(dr, e0 + i * TPR * V, a.D, g[i]);
     }
   }
 
@@ -363,15 +527,16 @@ __global__ void __launch_bounds__(Team<TPR, V, N>::kThreads) k15_norm_bwd_kernel
     if (!(which ? a.dnext : a.dgain)) continue;
     float *to = a.ws + ((size_t)(which && a.dgain ? gridDim.x : 0) + blockIdx.x) * a.D;
     for (int k = 0; k < T::kTeams; ++k) {
-      __syncthreads();
+      if (T::kTeams > 1) __syncthreads();
       if (team.team != k) continue;
 #pragma unroll
       for (int i = 0; i < N; ++i) {
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-          const int e = (team.t + i * TPR) * V + j;
+          const int e = e0 + i * TPR * V + j;
           if (e >= a.D) continue;
-          const float x = (k ? total[e] : 0.f) + (which ? dnext[i][j] : dgain[i][j]);
+          const f2 pair = which ? dnext[i][j / 2] : dgain[i][j / 2];
+          const float x = (k ? total[e] : 0.f) + (j % 2 ? hi2(pair) : lo2(pair));
           if (k + 1 < T::kTeams)
             total[e] = x;
           else
@@ -382,25 +547,31 @@ __global__ void __launch_bounds__(Team<TPR, V, N>::kThreads) k15_norm_bwd_kernel
   }
 }
 
-// Column sums of the blocks' parts, in order: 32 columns a block, eight runs of parts.
-__global__ void __launch_bounds__(256) k15_gain_kernel(const float *part, int blocks, int D,
-                                                       float *first, float *second) {
-  __shared__ double run[8][32];
-  const int c = blockIdx.x * 32 + threadIdx.x % 32, k = threadIdx.x / 32;
-  const float *p = part + (size_t)blockIdx.y * blocks * D;
+// Column sums of the blocks' parts in fp64, in order: 32 columns a block, 32 runs of parts.
+__global__ void __launch_bounds__(1024) k15_gain_kernel(const float *part, int blocks, int D,
+                                                        float *first, float *second) {
+  __shared__ double run[32][33];
+  const int lane = threadIdx.x % 32, k = threadIdx.x / 32, c = blockIdx.x * 32 + lane;
+  const float *p = part + (size_t)blockIdx.y * blocks * D + c;
   double x = 0.0;
-  for (int i = k; i < blocks && c < D; i += 8) x += p[(size_t)i * D + c];
-  run[k][threadIdx.x % 32] = x;
+  if (c < D) {
+#pragma unroll 4
+    for (int i = k; i < blocks; i += 32) x += __ldg(p + (size_t)i * D);
+  }
+  run[k][lane] = x;
   __syncthreads();
-  if (k || c >= D) return;
-  for (int i = 1; i < 8; ++i) x += run[i][threadIdx.x];
-  (blockIdx.y ? second : first)[c] = (float)x;
+  // a warp to each column
+  x = run[lane][k];
+#pragma unroll
+  for (int m = 16; m > 0; m /= 2) x += __shfl_xor_sync(0xffffffffu, x, m);
+  const int to = blockIdx.x * 32 + k;
+  if (lane == 0 && to < D) (blockIdx.y ? second : first)[to] = (float)x;
 }
 
-constexpr int kMaxBlocks = 152 * 4;
+constexpr int kMaxBlocks = 152 * 2;
 
 // Sixteen-byte vectors want every row of every tensor on sixteen bytes, and groups of whole vectors.
-bool vectors(const NormArgs &a) {
+bool whole(const NormArgs &a) {
   const int V = a.x_f32 ? 4 : 8;
   if (a.D % V || (a.groups && a.D / a.groups % V)) return false;
   const struct { const void *p; long long s; bool f32; } all[] = {
@@ -413,67 +584,78 @@ bool vectors(const NormArgs &a) {
   return true;
 }
 
-template <typename TX, typename TR, int TPR, int V, int N>
-cudaError_t go(const NormArgs &a, bool back, cudaStream_t st) {
-  using T = Team<TPR, V, N>;
+template <bool kBack, typename TX, typename TR, int TPR, int N, bool kWhole>
+cudaError_t go(NormArgs a, cudaStream_t st) {
+  constexpr int V = 16 / sizeof(TX);
+  using T = Team<TPR, V, N, kWhole>;
+  const int n = a.groups ? a.D / a.groups : 1;
+  a.per = kWhole ? n / V : n;
+  a.inv_n = 1.f / (float)n;
+  a.inv_D = 1.f / (float)a.D;
+  a.mode = !a.groups ? kNone
+           : a.groups == 1 ? kRow
+           : kWhole && a.per <= T::kLanes && (a.per & (a.per - 1)) == 0 ? kShuffle : kList;
+  a.list = a.mode == kList || (!kWhole && a.groups > 1) ? (kWhole ? a.D / V : a.D) + a.groups : 0;
   const long long blocks = ((long long)a.M + T::kTeams - 1) / T::kTeams;
-  size_t smem = a.groups > 1 ? (size_t)T::kTeams * (a.D / V + a.groups) * 4 : 0;
-  if (!back) {
-    auto f = k15_norm_kernel<TX, TR, TPR, V, N>;
-    if (smem > 48 * 1024) {
-      const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-      if (e != cudaSuccess) return e;
-    }
+  size_t smem = (size_t)T::kTeams * a.list * 4;
+  if (kBack && T::kTeams > 1 && smem < (size_t)a.D * 4) smem = (size_t)a.D * 4;
+  void (*f)(NormArgs);
+  if constexpr (kBack)
+    f = k15_norm_bwd_kernel<TX, TR, TPR, N, kWhole>;
+  else
+    f = k15_norm_kernel<TX, TR, TPR, N, kWhole>;
+  cudaError_t e;
+  if (smem > 48 * 1024 &&
+      (e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess)
+    return e;
+  if (!kBack) {
     f<<<(unsigned)blocks, T::kThreads, smem, st>>>(a);
     return cudaGetLastError();
   }
-  auto f = k15_norm_bwd_kernel<TX, TR, TPR, V, N>;
-  if (T::kTeams > 1 && smem < (size_t)a.D * 4) smem = (size_t)a.D * 4;
-  if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-  }
   const int grid = (int)(blocks < kMaxBlocks ? blocks : kMaxBlocks);
   f<<<grid, T::kThreads, smem, st>>>(a);
-  cudaError_t e = cudaGetLastError();
-  const int n = (a.dgain ? 1 : 0) + (a.dnext ? 1 : 0);
-  if (e != cudaSuccess || !n) return e;
-  k15_gain_kernel<<<dim3((a.D + 31) / 32, n), 256, 0, st>>>(
-      a.ws, grid, a.D, a.dgain ? a.dgain : a.dnext, a.dnext);
+  e = cudaGetLastError();
+  const int sums = (a.dgain ? 1 : 0) + (a.dnext ? 1 : 0);
+  if (e != cudaSuccess || !sums) return e;
+  k15_gain_kernel<<<dim3((a.D + 31) / 32, sums), 1024, 0, st>>>(a.ws, grid, a.D,
+                                                                a.dgain ? a.dgain : a.dnext, a.dnext);
   return cudaGetLastError();
 }
 
-// The smallest team whose threads hold the row, 16 elements each (32 for the
-// widest).  Rows by single elements are no path to be quick on: fewer teams.
-template <typename TX, typename TR, int V>
-cudaError_t pick(const NormArgs &a, bool back, cudaStream_t st) {
-  constexpr int kN = 16 / V;  // vectors of sixteen elements
+// The smallest team whose threads hold the row, 16 elements each, 8 in the backward pass,
+// which has twice the values to hold (more for the widest rows).  Rows element by
+// element are no path to be quick on: fewer teams.
+template <bool kBack, typename TX, typename TR>
+cudaError_t pick(const NormArgs &a, cudaStream_t st) {
+  constexpr int V = 16 / sizeof(TX), k8 = 8 / V, k16 = 16 / V, k32 = 32 / V;
   const int D = a.D;
-  if constexpr (V > 1) {
-    if (D <= 64) return go<TX, TR, 8, V, 8 / V>(a, back, st);
-    if (D <= 256) return go<TX, TR, 32, V, 8 / V>(a, back, st);
-    if (D <= 512) return go<TX, TR, 32, V, kN>(a, back, st);
-    if (D <= 1024) return go<TX, TR, 64, V, kN>(a, back, st);
-    if (D <= 2048) return go<TX, TR, 128, V, kN>(a, back, st);
-    if (D <= 4096) return go<TX, TR, 256, V, kN>(a, back, st);
-  } else {
-    if (D <= 128) return go<TX, TR, 8, V, kN>(a, back, st);
-    if (D <= 2048) return go<TX, TR, 128, V, kN>(a, back, st);
+  if (!whole(a)) {
+    if (D <= 128) return go<kBack, TX, TR, 8, k16, false>(a, st);
+    if (D <= 2048) return go<kBack, TX, TR, 128, k16, false>(a, st);
+    return go<kBack, TX, TR, 512, k32, false>(a, st);
   }
-  if (D <= 8192) return go<TX, TR, 512, V, kN>(a, back, st);
-  return go<TX, TR, 512, V, 2 * kN>(a, back, st);
+  if (D <= 64) return go<kBack, TX, TR, 8, k8, true>(a, st);
+  if (D <= 256) return go<kBack, TX, TR, 32, k8, true>(a, st);
+  if constexpr (kBack) {
+    if (D <= 512) return go<kBack, TX, TR, 64, k8, true>(a, st);
+    if (D <= 1024) return go<kBack, TX, TR, 128, k8, true>(a, st);
+    if (D <= 2048) return go<kBack, TX, TR, 256, k8, true>(a, st);
+    if (D <= 4096) return go<kBack, TX, TR, 512, k8, true>(a, st);
+  } else {
+    if (D <= 512) return go<kBack, TX, TR, 32, k16, true>(a, st);
+    if (D <= 1024) return go<kBack, TX, TR, 64, k16, true>(a, st);
+    if (D <= 2048) return go<kBack, TX, TR, 128, k16, true>(a, st);
+    if (D <= 4096) return go<kBack, TX, TR, 256, k16, true>(a, st);
+  }
+  if (D <= 8192) return go<kBack, TX, TR, 512, k16, true>(a, st);
+  return go<kBack, TX, TR, 512, k32, true>(a, st);
 }
 
-template <typename TX, typename TR>
-cudaError_t dispatch(const NormArgs &a, bool back, cudaStream_t st) {
-  constexpr int kV = 16 / sizeof(TX);
-  return vectors(a) ? pick<TX, TR, kV>(a, back, st) : pick<TX, TR, 1>(a, back, st);
-}
-
-cudaError_t launch(const NormArgs &a, bool back, cudaStream_t st) {
-  if (a.x_f32) return dispatch<float, float>(a, back, st);
-  if (a.r_f32) return dispatch<__nv_bfloat16, float>(a, back, st);
-  return dispatch<__nv_bfloat16, __nv_bfloat16>(a, back, st);
+template <bool kBack>
+cudaError_t launch(const NormArgs &a, cudaStream_t st) {
+  if (a.x_f32) return pick<kBack, float, float>(a, st);
+  if (a.r_f32) return pick<kBack, __nv_bfloat16, float>(a, st);
+  return pick<kBack, __nv_bfloat16, __nv_bfloat16>(a, st);
 }
 
 }  // namespace
@@ -482,7 +664,7 @@ size_t norm_workspace_bytes(int M, int D) {
   // one part a block and gain; no more blocks than rows
   return (size_t)(M < kMaxBlocks ? M : kMaxBlocks) * D * 2 * sizeof(float);
 }
-cudaError_t launch_norm(const NormArgs &a, cudaStream_t st) { return launch(a, false, st); }
-cudaError_t launch_norm_bwd(const NormArgs &a, cudaStream_t st) { return launch(a, true, st); }
+cudaError_t launch_norm(const NormArgs &a, cudaStream_t st) { return launch<false>(a, st); }
+cudaError_t launch_norm_bwd(const NormArgs &a, cudaStream_t st) { return launch<true>(a, st); }
 
 }  // namespace fs

@@ -16,13 +16,16 @@
 //
 // A block takes one (sequence, head), or one of `splits` stretches of it, chunk
 // after chunk; S never leaves it.  Warps:
-//   0-3       rows: Q S times the row's power in TMEM; scores to bf16 parts in their own
-//             TMEM columns; the finished rows to memory
-//   4..       states (D / 16 warps): weighted values into a ring of 32-token slabs, S in
+//   0-3       rows: scores to bf16 parts in their own TMEM columns, Q S times the row's
+//             power in place, the finished rows by way of the values' place in shared
+//             memory (a TMA store a warp: 32 rows written by their own threads would be
+//             32 places an instruction)
+//   4..       states (D / 16 warps): weighted values into a ring of two slabs; S in
 //             registers, its bf16 parts into shared memory for the next chunk
-//   then one  TMA loads, and one that issues the products.
-// A chunk's q, k and v lie in shared memory once; each is loaded anew as soon as its
-// last product has read it.  Heads of 64 leave room for two blocks an SM, which
+//   last four one for TMA loads, one that issues the products of the rows, one that issues
+//             those of the slabs (issued by one thread, slabs waited behind the rows'
+//             products, a slab at a time, and took 7000 cycles a chunk in place of 3000)
+// Values are loaded a chunk ahead.  Heads of 64 leave room for two blocks an SM, which
 // fill each other's waits; heads of 128 for one.
 //
 // With fewer (sequence, head) pairs than blocks fit, each is cut into stretches: a
@@ -35,16 +38,14 @@
 #include "fs_common.cuh"
 #include "fs_internal.h"
 #include "linear.cuh"
+#include "pairs.cuh"
 #include "tc05.cuh"
 
 namespace fs {
 namespace {
 
 constexpr int kC = 128;       // tokens of a chunk
-constexpr int kSlab = 32;     // tokens of a slab of weighted values
-constexpr int kSlabs = kC / kSlab;
-constexpr int kRing = 2;      // slabs in the ring
-constexpr uint32_t kAtom = kC * 128;  // 64 elements of a chunk's rows
+constexpr uint32_t kAtom = kC * 128;       // 64 elements of a chunk's rows
 
 struct Params {
   LinearArgs a;
@@ -52,32 +53,44 @@ struct Params {
   float *states;     // [sweep, batch H, splits, D D]: the state before each stretch
   int map[3][3];     // which map holds q, k, v of a sweep
   int axes[4][2];    // 0 where a map's sequences or heads are one
+  int out_axes[3][2];
   int *err;
+};
+
+struct Maps {
+  CUtensorMap in[4], out[3];
 };
 
 template <int D>
 struct Cfg {
   static constexpr int kAtoms = D / 64;
   static constexpr int kStateWarps = D / 16;
-  static constexpr int kTma = 4 + kStateWarps, kMma = kTma + 1;
-  static constexpr int kThreads = 32 * (kMma + 1);
+  static constexpr int kTma = 4 + kStateWarps, kMma = kTma + 1, kMmaU = kTma + 2;
+  static constexpr int kThreads = 32 * (kTma + 4);
+  static constexpr int kSlab = D == 64 ? 32 : 16, kSlabs = kC / kSlab;  // tokens of a slab, slabs
+  static constexpr int kUnits = kSlab / 16;  // 16-byte pieces of a slab for a state thread
+  static constexpr uint32_t kSlabAtom = kSlab * 128;
   static constexpr int kHalves = D / 64;  // groups of 16 rows that a state warp holds
+  static constexpr int kValues = 2;                              // chunks of v held
   static constexpr uint32_t kTile = kAtoms * kAtom;              // q, k or v
-  static constexpr uint32_t kPart = kAtoms * kSlab * 128;        // one part of a slab
+  static constexpr uint32_t kPart = kAtoms * kSlabAtom;          // one part of a slab
   static constexpr uint32_t kSPart = kAtoms * D * 128;           // one part of S
-  static constexpr uint32_t kQ = 0, kK = kTile, kV = 2 * kTile, kS = 3 * kTile,
-                            kSlab0 = kS + 2 * kSPart, kBytes = kSlab0 + kRing * 3 * kPart;
+  static constexpr uint32_t kQ = 0, kK = kTile, kV = kK + kTile, kS = kV + kValues * kTile,
+                            kSlab0 = kS + 2 * kSPart, kBytes = kSlab0 + 2 * 3 * kPart;
   // TMEM columns: scores (then their parts), outputs, the chunk's addition to S
   static constexpr uint32_t kScores = 0, kOut = kC, kU = kC + D, kCols = D == 64 ? 256 : 512;
 };
 
 struct Shared {
-  uint64_t qfull, kfull, vfull, qempty, kempty, vempty;
-  uint64_t slab_full[kRing], slab_empty[kRing];
-  uint64_t s_ready, s_free, scores, inter, parts, done, o_free, u_full, u_free, checked, fin;
+  uint64_t qfull, qempty, kfull, kempty, vfull[2], vempty[2];
+  uint64_t slab_full[2], slab_empty[2];
+  uint64_t s_ready, s_free, scores, inter, parts, done, o_free, u_full, u_free, fin, fin_u;
+  // values looked through: the states' warps may be a chunk ahead of the rows', not two
+  uint64_t checked[2];
   uint32_t tmem;
   int odd[2];                 // a chunk's values are not all finite
-  float power[kC + 1];        // lam^n
+  float power[kC + 4];        // lam^n
+  alignas(16) float cols[3][32];  // see the rows' warps (read four at a time)
   int bad[2][128];            // per column: the first such token in the sweep's order
 };
 
@@ -135,22 +148,26 @@ __device__ __forceinline__ void load_rows(void *dst, const void *map, uint64_t *
       : "memory");
 }
 
-// Two fp32 numbers as pairs of bf16: the nearest, and what is left.
-__device__ __forceinline__ uint32_t split(float &x, float &y) {
-  const uint32_t h = pack_bf16(x, y);
-  x -= bf16_lo(h);
-  y -= bf16_hi(h);
-  return h;
+// The other way, of `map`'s box size; for bulk_commit and bulk_wait_read of the same thread.
+__device__ __forceinline__ void store_rows(const void *src, const void *map, int x, int t, int h, int b) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%2, %3, %4, %5}], [%1];\n" ::"l"(
+          reinterpret_cast<uint64_t>(map)),
+      "r"(smem_u32(src)), "r"(x), "r"(t), "r"(h), "r"(b)
+      : "memory");
+}
+__device__ __forceinline__ void bulk_commit() {
+  asm volatile("cp.async.bulk.commit_group;\n" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;\n" ::"n"(N) : "memory");
 }
 
-__device__ __forceinline__ bool not_finite(const uint4 &u) {
-  auto biggest = [](uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a & 0x7fff7fffu), "r"(b & 0x7fff7fffu));
-    return r;
-  };
-  const uint32_t m = biggest(biggest(u.x, u.y), biggest(u.z, u.w)) & 0x7fff7fffu;
-  return (m & 0xffffu) >= 0x7f80u || (m >> 16) >= 0x7f80u;
+__device__ __forceinline__ void stmatrix4(uint32_t at, const uint32_t (&r)[4]) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1,%2,%3,%4};\n" ::"r"(at), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3])
+               : "memory");
 }
 
 #define WAIT(bar, k) __all_sync(0xffffffffu, tc::mbar_wait(&(bar), (k) & 1, p.err))
@@ -158,9 +175,7 @@ __device__ __forceinline__ bool not_finite(const uint4 &u) {
 // kRows: the whole sweep; without, only the states of the stretches (into p.states).
 template <int D, bool kRows>
 __global__ void __launch_bounds__(Cfg<D>::kThreads, D == 64 ? 2 : 1)
-    k16_linear_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constant__ CUtensorMap map1,
-                      const __grid_constant__ CUtensorMap map2, const __grid_constant__ CUtensorMap map3,
-                      const __grid_constant__ Params p) {
+    k16_linear_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
   using C = Cfg<D>;
   extern __shared__ unsigned char smem_raw[];
   unsigned char *smem = reinterpret_cast<unsigned char *>(
@@ -177,21 +192,28 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, D == 64 ? 2 : 1)
   const float decay = p.a.decay[h];
 
   if (threadIdx.x == 0) {
-    for (uint64_t *x : {&s.qfull, &s.kfull, &s.vfull, &s.qempty, &s.kempty, &s.vempty, &s.s_free,
-                        &s.scores, &s.inter, &s.done, &s.u_full, &s.fin})
+    for (uint64_t *x : {&s.qfull, &s.qempty, &s.kfull, &s.s_free, &s.scores, &s.inter, &s.done, &s.u_full, &s.fin})
       tc::mbar_init(x, 1);
-    for (int i = 0; i < kRing; ++i) {
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&s.vfull[i], 1);
+      tc::mbar_init(&s.vempty[i], kRows ? 4 : C::kStateWarps);
       tc::mbar_init(&s.slab_full[i], C::kStateWarps);
       tc::mbar_init(&s.slab_empty[i], 1);
     }
-    for (uint64_t *x : {&s.s_ready, &s.u_free, &s.checked}) tc::mbar_init(x, C::kStateWarps);
+    for (uint64_t *x : {&s.s_ready, &s.u_free, &s.checked[0], &s.checked[1]}) tc::mbar_init(x, C::kStateWarps);
     for (uint64_t *x : {&s.parts, &s.o_free}) tc::mbar_init(x, 4);
+    tc::mbar_init(&s.kempty, kRows ? 2 : 1);  // read by the scores' product and by the slabs'
+    tc::mbar_init(&s.fin_u, 1);
     tc::mbar_fence_init();
     s.odd[0] = s.odd[1] = 0;
   }
   for (int i = threadIdx.x; i <= kC; i += C::kThreads) {
     const Factor f = decay_power(decay, i);
     s.power[i] = f.hi + f.lo;
+  }
+  for (int i = threadIdx.x; i < 96; i += C::kThreads) {
+    const Factor f = decay_power(decay, 32 * (i / 32 + 1) + (reverse ? i % 32 - 31 : -(i % 32)));
+    s.cols[i / 32][i % 32] = f.hi + f.lo;
   }
   for (int i = threadIdx.x; i < 256; i += C::kThreads) s.bad[i / 128][i % 128] = kC;
   if (warp == C::kMma) {
@@ -204,77 +226,112 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, D == 64 ? 2 : 1)
   const uint32_t tmem = s.tmem, base = smem_u32(smem);
   const uint32_t tu = tmem + (kRows ? C::kU : 0);
   const int chunks = st.to - st.from;
-
+  // Heads of 64: 80 registers a thread at launch, of which the last four warps need half:
+  // 96 + 104 + 40 = 3 x 80.
+  if (warp >= C::kTma) {
+    if constexpr (D == 64) tc::regs_dec<40>();
   if (warp == C::kTma && lane == 0) {
     // ------------------------------------------------------------------ loads
-    const CUtensorMap *maps[4] = {&map0, &map1, &map2, &map3};
     const int mq = p.map[blockIdx.z][0], mk = p.map[blockIdx.z][1], mv = p.map[blockIdx.z][2];
-    auto load = [&](uint32_t at, int m, const LinearRows &x, uint64_t *bar, int t) {
+    auto load = [&](uint32_t at, int m, const LinearRows &x, uint64_t *bar, int i) {
+      const int t = st.chunk(st.from + i, reverse) * kC;
       tc::mbar_arrive_expect_tx(bar, C::kTile);
-      for (int i = 0; i < C::kAtoms; ++i)
-        load_rows(smem + at + i * kAtom, maps[m], bar, 64 * i, t, h / x.share * p.axes[m][1],
+      for (int k = 0; k < C::kAtoms; ++k)
+        load_rows(smem + at + k * kAtom, &maps.in[m], bar, 64 * k, t, h / x.share * p.axes[m][1],
                   b * p.axes[m][0]);
     };
-    int i = 0;
-    int loaded[3] = {0, 0, 0};
-    for (; i < chunks; ++i) {
-      const int t = st.chunk(st.from + i, reverse) * kC;
-      if (kRows) {
-        if (i && !tc::mbar_wait(&s.qempty, (i - 1) & 1, p.err)) break;
-        load(C::kQ, mq, w.q, &s.qfull, t);
-        ++loaded[0];
-      }
-      if (i && !tc::mbar_wait(&s.kempty, (i - 1) & 1, p.err)) break;
-      load(C::kK, mk, w.k, &s.kfull, t);
-      ++loaded[1];
-      if (i && !tc::mbar_wait(&s.vempty, (i - 1) & 1, p.err)) break;
-      load(C::kV, mv, w.v, &s.vfull, t);
-      ++loaded[2];
+    int nq = 0, nk = 0, nv = 0;  // loaded so far
+    bool ok = true;
+    auto load_q = [&]() {
+      if (!kRows || !ok || nq >= chunks) return;
+      if (nq && !(ok = tc::mbar_wait(&s.qempty, (nq - 1) & 1, p.err))) return;
+      load(C::kQ, mq, w.q, &s.qfull, nq);
+      ++nq;
+    };
+    auto load_k = [&]() {
+      if (!ok || nk >= chunks) return;
+      if (nk && !(ok = tc::mbar_wait(&s.kempty, (nk - 1) & 1, p.err))) return;
+      load(C::kK, mk, w.k, &s.kfull, nk);
+      ++nk;
+    };
+    auto load_v = [&]() {
+      const int at = nv % C::kValues;
+      if (!ok || nv >= chunks) return;
+      if (nv >= C::kValues && !(ok = tc::mbar_wait(&s.vempty[at], (nv / C::kValues - 1) & 1, p.err))) return;
+      load(C::kV + at * C::kTile, mv, w.v, &s.vfull[at], nv);
+      ++nv;
+    };
+    // in the order in which places become free
+    load_k();
+    load_q();
+    load_v();
+    load_v();
+    for (int i = 1; i < chunks && ok; ++i) {
+      load_q();
+      load_k();
+      load_v();
     }
     // what is under way lands before the block ends
-    uint64_t *full[3] = {&s.qfull, &s.kfull, &s.vfull};
-    for (int j = 0; j < 3; ++j)
-      if (loaded[j]) tc::mbar_wait(full[j], (loaded[j] - 1) & 1, nullptr);
-  } else if (warp == C::kMma && lane == 0) {
-    // --------------------------------------------------------------- products
+    if (nq) tc::mbar_wait(&s.qfull, (nq - 1) & 1, nullptr);
+    if (nk) tc::mbar_wait(&s.kfull, (nk - 1) & 1, nullptr);
+    for (int i = nv > C::kValues ? nv - C::kValues : 0; i < nv; ++i)
+      tc::mbar_wait(&s.vfull[i % C::kValues], i / C::kValues & 1, nullptr);
+  } else if (kRows && warp == C::kMma && lane == 0) {
+    // ----------------------------------------------------- products of the rows
     constexpr uint32_t kQK = tc::idesc_bf16(128, 128, 0), kB = tc::idesc_bf16(128, D, 1);
-    constexpr uint32_t kUD = tc::idesc_bf16(D, D, 1) | 1u << 15;  // K^T: its rows run along M
+    const uint32_t keys = base + C::kK;
     for (int i = 0; i < chunks; ++i) {
-      if (kRows) {
-        if (!tc::mbar_wait(&s.qfull, i & 1, p.err) || !tc::mbar_wait(&s.kfull, i & 1, p.err)) break;
-        tc::fence_after_sync();
+      const uint32_t values = base + C::kV + i % C::kValues * C::kTile;
+      if (!tc::mbar_wait(&s.kfull, i & 1, p.err) || !tc::mbar_wait(&s.qfull, i & 1, p.err)) break;
+      tc::fence_after_sync();
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          tc::mma_ss(tmem + C::kScores, tc::desc_sw128(base + C::kQ + k / 4 * kAtom + k % 4 * 32),
-                     tc::desc_sw128(base + C::kK + k / 4 * kAtom + k % 4 * 32), kQK, k > 0);
-        tc::mma_commit(&s.scores);
-        if (!tc::mbar_wait(&s.s_ready, i & 1, p.err) ||
-            (i && !tc::mbar_wait(&s.o_free, (i - 1) & 1, p.err)))
-          break;
-        tc::fence_after_sync();
-#pragma unroll
-        for (int k = 0; k < 2 * D / 16; ++k) {
-          const int kk = k % (D / 16), part = k / (D / 16);
-          tc::mma_ss(tmem + C::kOut, tc::desc_sw128(base + C::kQ + kk / 4 * kAtom + kk % 4 * 32),
-                     desc_blocks(base + C::kS + part * C::kSPart + kk * 2048, D * 128), kB, k > 0);
-        }
-        tc::mma_commit(&s.inter);
-        tc::mma_commit(&s.s_free);
-        tc::mma_commit(&s.qempty);
-      } else if (!tc::mbar_wait(&s.kfull, i & 1, p.err)) {
+      for (int k = 0; k < D / 16; ++k)
+        tc::mma_ss(tmem + C::kScores, tc::desc_sw128(base + C::kQ + k / 4 * kAtom + k % 4 * 32),
+                   tc::desc_sw128(keys + k / 4 * kAtom + k % 4 * 32), kQK, k > 0);
+      tc::mma_commit(&s.scores);
+      tc::mma_commit(&s.kempty);
+      if (!tc::mbar_wait(&s.s_ready, i & 1, p.err) ||
+          (i && !tc::mbar_wait(&s.o_free, (i - 1) & 1, p.err)))
         break;
+      tc::fence_after_sync();
+#pragma unroll
+      for (int k = 0; k < 2 * D / 16; ++k) {
+        const int kk = k % (D / 16), part = k / (D / 16);
+        tc::mma_ss(tmem + C::kOut, tc::desc_sw128(base + C::kQ + kk / 4 * kAtom + kk % 4 * 32),
+                   desc_blocks(base + C::kS + part * C::kSPart + kk * 2048, D * 128), kB, k > 0);
       }
+      tc::mma_commit(&s.inter);
+      tc::mma_commit(&s.s_free);
+      tc::mma_commit(&s.qempty);
+      if (!tc::mbar_wait(&s.parts, i & 1, p.err) || !tc::mbar_wait(&s.checked[i & 1], i >> 1 & 1, p.err)) break;
+      tc::fence_after_sync();
+#pragma unroll
+      for (int k = 0; k < 2 * kC / 16; ++k) {
+        const int kk = k % (kC / 16), part = k / (kC / 16);
+        tc::mma_ts(tmem + C::kOut, tmem + C::kScores + kk / 2 * 32 + part * 16 + kk % 2 * 8,
+                   desc_blocks(values + kk * 2048, kAtom), kB, 1);
+      }
+      tc::mma_commit(&s.done);
+    }
+    tc::mma_commit(&s.fin);
+    tc::mbar_wait(&s.fin, 0, nullptr);
+  } else if (warp == C::kMmaU && lane == 0) {
+    // ---------------------------------------------------- products of the slabs
+    constexpr uint32_t kUD = tc::idesc_bf16(D, D, 1) | 1u << 15;  // K^T: its rows run along M
+    const uint32_t keys = base + C::kK;
+    bool ok = true;
+    for (int i = 0; i < chunks && ok; ++i) {
+      if (!tc::mbar_wait(&s.kfull, i & 1, p.err)) break;
       if (i && !tc::mbar_wait(&s.u_free, (i - 1) & 1, p.err)) break;
-      bool ok = true;
-      for (int j = 0; j < kSlabs && ok; ++j) {
-        const int at = i * kSlabs + j, slot = at % kRing;
-        if (!(ok = tc::mbar_wait(&s.slab_full[slot], at / kRing & 1, p.err))) break;
+      for (int j = 0; j < C::kSlabs; ++j) {
+        const int at = i * C::kSlabs + j, slot = at & 1;
+        if (!(ok = tc::mbar_wait(&s.slab_full[slot], at >> 1 & 1, p.err))) break;
         tc::fence_after_sync();
 #pragma unroll
-        for (int k = 0; k < 3 * kSlab / 16; ++k) {
-          const int kk = k % (kSlab / 16), part = k / (kSlab / 16);
-          tc::mma_ss(tu, desc_blocks(base + C::kK + (j * kSlab + kk * 16) * 128, kAtom),
-                     desc_blocks(base + C::kSlab0 + (slot * 3 + part) * C::kPart + kk * 2048, kSlab * 128),
+        for (int k = 0; k < 3 * C::kUnits; ++k) {
+          const int kk = k % C::kUnits, part = k / C::kUnits;
+          tc::mma_ss(tu, desc_blocks(keys + j * C::kSlabAtom + kk * 2048, kAtom),
+                     desc_blocks(base + C::kSlab0 + (slot * 3 + part) * C::kPart + kk * 2048, C::kSlabAtom),
                      kUD, j > 0 || k > 0);
         }
         tc::mma_commit(&s.slab_empty[slot]);
@@ -282,24 +339,15 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, D == 64 ? 2 : 1)
       if (!ok) break;
       tc::mma_commit(&s.u_full);
       tc::mma_commit(&s.kempty);
-      if (kRows) {
-        if (!tc::mbar_wait(&s.parts, i & 1, p.err)) break;
-        tc::fence_after_sync();
-#pragma unroll
-        for (int k = 0; k < 2 * kC / 16; ++k) {
-          const int kk = k % (kC / 16), part = k / (kC / 16);
-          tc::mma_ts(tmem + C::kOut, tmem + C::kScores + kk / 2 * 32 + part * 16 + kk % 2 * 8,
-                     desc_blocks(base + C::kV + kk * 2048, kAtom), kB, 1);
-        }
-        tc::mma_commit(&s.done);
-      }
-      tc::mma_commit(&s.vempty);
     }
-    tc::mma_commit(&s.fin);
-    tc::mbar_wait(&s.fin, 0, nullptr);
-  } else if (warp >= 4 && warp < C::kTma) {
+    tc::mma_commit(&s.fin_u);
+    tc::mbar_wait(&s.fin_u, 0, nullptr);
+  }
+  } else if (warp >= 4) {
+    if constexpr (D == 64) tc::regs_inc<104>();
     // ------------------------------------------------------------------ states
-    const int sw = warp - 4, t = threadIdx.x - 128, kT = 32 * C::kStateWarps;
+    constexpr int kT = 32 * C::kStateWarps;
+    const int sw = warp - 4, t = threadIdx.x - 128;
     // this lane's places in S: rows row0 + 16 g (+ 8), columns col0 + 8 e (+ 1)
     const int row0 = (D == 64 ? sw * 16 : sw % 4 * 32) + lane / 4;
     const int col0 = (D == 64 ? 0 : sw / 4 * 64) + lane % 4 * 2;
@@ -339,17 +387,25 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, D == 64 ? 2 : 1)
           *reinterpret_cast<float4 *>(to + (g * 8 + e / 4) * kT * 4) =
               make_float4(S[g][e], S[g][e + 1], S[g][e + 2], S[g][e + 3]);
     };
-    // S as the factor of the next product: two parts, [row][column] with the columns swizzled
+    // S as the factor of the next product: two parts, [row][column] with the columns
+    // swizzled.  A lane names the row that it is to fill of one of four 8 x 8 blocks:
+    // rows + 0 and + 8 of two neighbours among the blocks of columns.
+    const uint32_t sat = base + C::kS + col0 / 64 * (D * 128) + (row0 - lane / 4 + lane / 8 % 2 * 8 + lane % 8) * 128;
     auto publish = [&]() {
 #pragma unroll
       for (int g = 0; g < C::kHalves; ++g)
 #pragma unroll
-        for (int e = 0; e < 32; e += 2) {
-          const int row = row0 + 16 * g + (e & 2) * 4, col = col0 + e / 4 * 8;
-          const uint32_t at = C::kS + col / 64 * (D * 128) + swz128(row, col % 64 / 8) + col % 8 * 2;
-          float x = S[g][e], y = S[g][e + 1];
-          *reinterpret_cast<uint32_t *>(smem + at) = split(x, y);
-          *reinterpret_cast<uint32_t *>(smem + at + C::kSPart) = pack_bf16(x, y);
+        for (int e = 0; e < 32; e += 8) {
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            f2 x = f2_bits(S[g][e + 2 * k], S[g][e + 2 * k + 1]);
+            hi[k] = split2(x);
+            lo[k] = pack2(x);
+          }
+          const uint32_t at = sat + g * 16 * 128 + (((e / 4 + lane / 16) ^ (lane % 8)) << 4);
+          stmatrix4(at, hi);
+          stmatrix4(at + C::kSPart, lo);
         }
       tc::fence_async_smem();
       __syncwarp();
@@ -357,141 +413,150 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, D == 64 ? 2 : 1)
     };
     if (!kRows && r == 0) save(slot(0));
     if (kRows && chunks) publish();
-    {
-      const Factor whole = decay_power(decay, kC);
-      int i = 0;
-      bool ok = true;
-      for (; i < chunks && ok; ++i) {
-        const int n = st.size(st.chunk(st.from + i, reverse));
-        if (!(ok = WAIT(s.vfull, i))) break;
-        if (n < kC && !(ok = WAIT(s.kfull, i))) break;
-        if (n < kC) {
-          // what lies behind the sequence takes no part, whatever it is
-          for (int u = t; u < (kC - n) * (D / 8); u += kT) {
-            const int row = n + u / (D / 8), ch = u % (D / 8);
-            const uint32_t at = ch / 8 * kAtom + swz128(row, ch % 8);
-            *reinterpret_cast<uint4 *>(smem + C::kK + at) = make_uint4(0, 0, 0, 0);
-            *reinterpret_cast<uint4 *>(smem + C::kV + at) = make_uint4(0, 0, 0, 0);
-          }
-          asm volatile("bar.sync 1, %0;" ::"n"(32 * C::kStateWarps) : "memory");
+    const Factor whole = decay_power(decay, kC);
+    // this thread's sixteen bytes of a slab's row r16 (and r16 + 16)
+    const int r16 = t % 128 / 8, ch = t % 8, atom = t / 128;
+    const uint32_t in = swz128(r16, ch);
+    unsigned char *to = smem + C::kSlab0 + atom * C::kSlabAtom + in;
+    for (int i = 0; i < chunks; ++i) {
+      const int n = st.size(st.chunk(st.from + i, reverse));
+      unsigned char *values = smem + C::kV + i % C::kValues * C::kTile;
+      if (!WAIT(s.vfull[i % C::kValues], i / C::kValues)) break;
+      if (n < kC) {
+        // what lies behind the sequence takes no part, whatever it is
+        if (!WAIT(s.kfull, i)) break;
+        unsigned char *keys = smem + C::kK;
+        for (int u = t; u < (kC - n) * (D / 8); u += kT) {
+          const uint32_t at = u % (D / 8) / 8 * kAtom + swz128(n + u / (D / 8), u % 8);
+          *reinterpret_cast<uint4 *>(keys + at) = make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4 *>(values + at) = make_uint4(0, 0, 0, 0);
         }
-        for (int j = 0; j < kSlabs; ++j) {
-          const int at = i * kSlabs + j, place = at % kRing;
-          if (at >= kRing && !(ok = WAIT(s.slab_empty[place], at / kRing - 1))) break;
-          unsigned char *to = smem + C::kSlab0 + place * 3 * C::kPart;
+        tc::fence_async_smem();
+        asm volatile("bar.sync 1, %0;" ::"n"(32 * C::kStateWarps) : "memory");
+      }
+      unsigned char *from = values + atom * kAtom + in;
+      uint32_t some = 0;  // the bits of all third parts
+      bool ok = true;
+#pragma unroll 1
+      for (int j = 0; j < C::kSlabs; ++j) {
+        uint32_t part[C::kUnits][3][4];
 #pragma unroll
-          for (int u = t; u < kSlab * (D / 8); u += 32 * C::kStateWarps) {
-            const int row = j * kSlab + u / (D / 8), ch = u % (D / 8);
-            uint4 *from = reinterpret_cast<uint4 *>(smem + C::kV + ch / 8 * kAtom + swz128(row, ch % 8));
-            const uint4 x = *from;
-            const float f = row < n ? s.power[reverse ? row + 1 : n - 1 - row] : 0.f;
-            const uint32_t in[4] = {x.x, x.y, x.z, x.w};
-            uint32_t part[3][4];
+        for (int k = 0; k < C::kUnits; ++k) {
+          const int row = j * C::kSlab + r16 + 16 * k;
+          const uint4 x = *reinterpret_cast<const uint4 *>(from + j * C::kSlabAtom + k * 2048);
+          const float f = row < n ? s.power[reverse ? row + 1 : n - 1 - row] : 0.f;
+          const uint32_t v[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              float y = bf16_lo(in[c]) * f, z = bf16_hi(in[c]) * f;
-              part[0][c] = split(y, z);
-              part[1][c] = split(y, z);
-              part[2][c] = pack_bf16(y, z);
-            }
-            const uint32_t off = ch / 8 * (kSlab * 128) + swz128(row % kSlab, ch % 8);
+          for (int c = 0; c < 4; ++c) {
+            f2 y = mul2(wide2(v[c]), f2_bits(f, f));
+            part[k][0][c] = split2(y);
+            part[k][1][c] = split2(y);
+            part[k][2][c] = pack2(y);
+            some |= part[k][2][c];
+          }
+        }
+        const int at = i * C::kSlabs + j, slot = at & 1;
+        if (at > 1 && !(ok = WAIT(s.slab_empty[slot], (at >> 1) - 1))) break;
 #pragma unroll
-            for (int k = 0; k < 3; ++k)
-              *reinterpret_cast<uint4 *>(to + k * C::kPart + off) =
-                  make_uint4(part[k][0], part[k][1], part[k][2], part[k][3]);
-            if (kRows && not_finite(x)) {
-              // out of the tile, whose rows before it (scores 0) would become NaN too
-              uint32_t keep[4];
+        for (int k = 0; k < C::kUnits; ++k)
 #pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                keep[c] = in[c];
-#pragma unroll
-                for (int k = 0; k < 2; ++k)
-                  if ((in[c] >> 16 * k & 0x7f80u) == 0x7f80u) {
-                    keep[c] &= k ? 0xffffu : 0xffff0000u;
-                    atomicMin(&s.bad[i & 1][ch * 8 + 2 * c + k], reverse ? kC - 1 - row : row);
-                  }
-              }
-              *from = make_uint4(keep[0], keep[1], keep[2], keep[3]);
+          for (int q = 0; q < 3; ++q)
+            *reinterpret_cast<uint4 *>(to + (slot * 3 + q) * C::kPart + k * 2048) =
+                make_uint4(part[k][q][0], part[k][q][1], part[k][q][2], part[k][q][3]);
+        // A value that is not finite leaves NaN in the third part (and NaN in the state's column).
+        // It leaves V before the scores' product, where scores of 0 would make NaN of the rows
+        // before it as well; those after it get theirs at the end.
+        if (kRows && j + 1 == C::kSlabs &&
+            ((some & 0x7f80u) == 0x7f80u || (some & 0x7f800000u) == 0x7f800000u)) {
+          for (int u = 0; u < kC / 16; ++u) {
+            const int row = 16 * u + r16;
+            uint32_t *word = reinterpret_cast<uint32_t *>(from + u * 2048);
+            for (int c = 0; c < 8; ++c) {
+              if ((word[c / 2] >> c % 2 * 16 & 0x7f80u) != 0x7f80u) continue;
+              word[c / 2] &= c % 2 ? 0xffffu : 0xffff0000u;
+              atomicMin(&s.bad[i & 1][atom * 64 + ch * 8 + c], reverse ? kC - 1 - row : row);
               s.odd[i & 1] = 1;
             }
           }
-          tc::fence_async_smem();
+        }
+        tc::fence_async_smem();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&s.slab_full[slot]);
+      }
+      if (!ok) break;
+      if (lane == 0) tc::mbar_arrive(kRows ? &s.checked[i & 1] : &s.vempty[i % C::kValues]);
+      if (!WAIT(s.u_full, i)) break;
+      tc::fence_after_sync();
+      const Factor f = n == kC ? whole : decay_power(decay, n);
+      const f2 hi = f2_bits(f.hi, f.hi), lo = f2_bits(f.lo, f.lo);
+#pragma unroll
+      for (int g = 0; g < C::kHalves; ++g) {
+        float u[32];
+        tmem_ld_16x64(lanes + ((uint32_t)(16 * g) << 16), u);
+        if (g == C::kHalves - 1) {
+          tc::fence_before_sync();
           __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&s.slab_full[place]);
+          if (lane == 0) tc::mbar_arrive(&s.u_free);
         }
-        if (!ok) break;
-        if (kRows && lane == 0) tc::mbar_arrive(&s.checked);
-        if (!(ok = WAIT(s.u_full, i))) break;
-        tc::fence_after_sync();
-        const Factor f = n == kC ? whole : decay_power(decay, n);
 #pragma unroll
-        for (int g = 0; g < C::kHalves; ++g) {
-          float u[32];
-          tmem_ld_16x64(lanes + ((uint32_t)(16 * g) << 16), u);
-          if (g == C::kHalves - 1) {
-            tc::fence_before_sync();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&s.u_free);
-          }
-#pragma unroll
-          for (int e = 0; e < 32; ++e) S[g][e] = f.times(S[g][e], u[e]);
+        for (int e = 0; e < 32; e += 2) {
+          const f2 x = f2_bits(S[g][e], S[g][e + 1]);
+          const f2 y = madd2(x, hi, madd2(x, lo, f2_bits(u[e], u[e + 1])));
+          S[g][e] = __uint_as_float((uint32_t)y);
+          S[g][e + 1] = __uint_as_float((uint32_t)(y >> 32));
         }
-        if (kRows && i + 1 < chunks) {
-          if (!(ok = WAIT(s.s_free, i))) break;
-          publish();
-        }
+      }
+      if (kRows && i + 1 < chunks) {
+        if (!WAIT(s.s_free, i)) break;
+        publish();
       }
     }
     if (!kRows) {
       save(slot(r + 1));
     } else if (r == st.last && w.state_out) {
-      float *to = w.state_out + (size_t)blockIdx.y * D * D;
+      float *out = w.state_out + (size_t)blockIdx.y * D * D;
       const int sr = w.transposed ? 1 : D, sc = w.transposed ? D : 1;
       const float mul = 1.f / w.state_mul;
-      each([&](float &x, int row, int col) { to[row * sr + col * sc] = x * mul; });
+      each([&](float &x, int row, int col) { out[row * sr + col * sc] = x * mul; });
     }
-  } else if (kRows && warp < 4) {
+  } else if (kRows) {
+    if constexpr (D == 64) tc::regs_inc<96>();
     // -------------------------------------------------------------------- rows
+    // lam^|i - j| for 32 columns that all rows of the warp see is a factor of the row and
+    // one of the column, counted from the warp's near edge, so that neither passes 1
     const int row = warp * 32 + lane;
     const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
-    const long long out0 = b * w.os[0] + h * w.os[1];
+    const float rowf = s.power[reverse ? 31 - lane : lane];
+    const f2 rowff = f2_bits(rowf, rowf);
+    const CUtensorMap *map = &maps.out[blockIdx.z];
+    const int mh = h * p.out_axes[blockIdx.z][1], mb = b * p.out_axes[blockIdx.z][0];
+    bool storing = false;  // (lane 0) a store may still read the values' place
     for (int i = 0; i < chunks; ++i) {
       const int chunk = st.chunk(st.from + i, reverse), n = st.size(chunk);
-      if (!WAIT(s.inter, i)) break;
-      tc::fence_after_sync();
-      {
-        const float f = s.power[reverse ? max(n - 1 - row, 0) : row + 1];
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t x[32];
-          tc::tmem_ld32(lanes + C::kOut + 32 * c, x);
-          tc::tmem_wait_ld();
-#pragma unroll
-          for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * f);
-          tc::tmem_st32(lanes + C::kOut + 32 * c, x);
-        }
-      }
       if (!WAIT(s.scores, i)) break;
       tc::fence_after_sync();
 #pragma unroll 1
       for (int c = 0; c < 4; ++c) {
         uint32_t hi[16], lo[16];
-        if (reverse ? c < warp : c > warp) {
+        const int off = reverse ? c - warp : warp - c;
+        if (off < 0) {
 #pragma unroll
           for (int e = 0; e < 16; ++e) hi[e] = lo[e] = 0;
         } else {
           uint32_t x[32];
           tc::tmem_ld32(lanes + C::kScores + 32 * c, x);
           tc::tmem_wait_ld();
-          if (c != warp && (!reverse || 32 * c + 32 <= n)) {
-            const float *pw = s.power + (reverse ? 32 * c - row : row - 32 * c);
+          if (off > 0 && (!reverse || 32 * c + 32 <= n)) {
+            const ulonglong2 *cw = reinterpret_cast<const ulonglong2 *>(s.cols[off - 1]);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              float y = __uint_as_float(x[2 * e]) * (reverse ? pw[2 * e] : pw[-2 * e]);
-              float z = __uint_as_float(x[2 * e + 1]) * (reverse ? pw[2 * e + 1] : pw[-2 * e - 1]);
-              hi[e] = split(y, z);
-              lo[e] = pack_bf16(y, z);
+            for (int e = 0; e < 8; ++e) {
+              const ulonglong2 f = cw[e];
+              f2 y = mul2(mul2((f2)x[4 * e] | (f2)x[4 * e + 1] << 32, f.x), rowff);
+              f2 z = mul2(mul2((f2)x[4 * e + 2] | (f2)x[4 * e + 3] << 32, f.y), rowff);
+              hi[2 * e] = split2(y);
+              lo[2 * e] = pack2(y);
+              hi[2 * e + 1] = split2(z);
+              lo[2 * e + 1] = pack2(z);
             }
           } else {
 #pragma unroll
@@ -503,22 +568,52 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, D == 64 ? 2 : 1)
                 const bool seen = lag >= 0 && (!reverse || j < n);
                 v[k] = seen ? __uint_as_float(x[2 * e + k]) * s.power[abs(lag)] : 0.f;
               }
-              hi[e] = split(v[0], v[1]);
-              lo[e] = pack_bf16(v[0], v[1]);
+              f2 y = f2_bits(v[0], v[1]);
+              hi[e] = split2(y);
+              lo[e] = pack2(y);
             }
           }
         }
         tc::tmem_st16(lanes + C::kScores + 32 * c, hi);
         tc::tmem_st16(lanes + C::kScores + 32 * c + 16, lo);
       }
+      if (i && lane == 0) {  // the last chunk's rows are on their way
+        if (storing) bulk_wait_read<0>();
+        tc::mbar_arrive(&s.vempty[(i - 1) % C::kValues]);
+      }
+      __syncwarp();
+      if (!WAIT(s.inter, i)) break;
+      tc::fence_after_sync();
+      {
+        const float f = s.power[reverse ? max(n - 1 - row, 0) : row + 1];
+        const f2 ff = f2_bits(f, f);
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t x[32];
+          tc::tmem_ld32(lanes + C::kOut + 32 * c, x);
+          tc::tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const f2 y = mul2((f2)x[e] | (f2)x[e + 1] << 32, ff);
+            x[e] = (uint32_t)y;
+            x[e + 1] = (uint32_t)(y >> 32);
+          }
+          tc::tmem_st32(lanes + C::kOut + 32 * c, x);
+        }
+      }
       tc::tmem_wait_st();
       tc::fence_before_sync();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&s.parts);
-      if (!WAIT(s.checked, i) || !WAIT(s.done, i)) break;
+      if (!WAIT(s.checked[i & 1], i >> 1) || !WAIT(s.done, i)) break;
       tc::fence_after_sync();
       const bool odd = s.odd[i & 1] != 0;
-      const long long at = out0 + (chunk * (long long)kC + row) * w.os[2];
+      // whole warps of rows leave by TMA, 128 bytes of each at a time; the last ones of a
+      // sequence from their threads
+      const bool whole = 32 * warp + 32 <= n;
+      unsigned char *box = smem + C::kV + i % C::kValues * C::kTile + warp * 4096;
+      const long long at = b * w.os[0] + h * w.os[1] + (chunk * (long long)kC + row) * w.os[2];
+      storing = whole;
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
         uint32_t x[32];
@@ -537,18 +632,46 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, D == 64 ? 2 : 1)
           for (int e = 0; e < 32; ++e)
             if (s.bad[i & 1][32 * c + e] <= (reverse ? kC - 1 - row : row)) y[e] = __uint_as_float(0x7fc00000u);
         }
-        if (row < n) {
-          if (w.out_f32) {
-            float4 *to = reinterpret_cast<float4 *>(static_cast<float *>(w.out) + at + 32 * c);
+        if (w.out_f32) {
+          unsigned char *to = box + c % C::kAtoms * kAtom;
+          if (whole && c >= C::kAtoms) {  // the place is read before it is filled again
+            if (lane == 0) bulk_wait_read<C::kAtoms - 1>();
+            __syncwarp();
+          }
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              to[e] = make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
-          } else {
-            uint4 *to = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(w.out) + at + 32 * c);
+          for (int e = 0; e < 8; ++e) {
+            const float4 z = make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+            if (whole)
+              *reinterpret_cast<float4 *>(to + swz128(lane, e)) = z;
+            else if (row < n)
+              *reinterpret_cast<float4 *>(static_cast<float *>(w.out) + at + 32 * c + 4 * e) = z;
+          }
+          if (whole) {
+            tc::fence_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              store_rows(to, map, 32 * c, chunk * kC + 32 * warp, mh, mb);
+              bulk_commit();
+            }
+          }
+        } else {
+          unsigned char *to = box + c / 2 * kAtom;
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              to[e] = make_uint4(pack_bf16(y[8 * e], y[8 * e + 1]), pack_bf16(y[8 * e + 2], y[8 * e + 3]),
-                                 pack_bf16(y[8 * e + 4], y[8 * e + 5]), pack_bf16(y[8 * e + 6], y[8 * e + 7]));
+          for (int e = 0; e < 4; ++e) {
+            const uint4 z = make_uint4(pack_bf16(y[8 * e], y[8 * e + 1]), pack_bf16(y[8 * e + 2], y[8 * e + 3]),
+                                       pack_bf16(y[8 * e + 4], y[8 * e + 5]), pack_bf16(y[8 * e + 6], y[8 * e + 7]));
+            if (whole)
+              *reinterpret_cast<uint4 *>(to + swz128(lane, c % 2 * 4 + e)) = z;
+            else if (row < n)
+              *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(w.out) + at + 32 * c + 8 * e) = z;
+          }
+          if (whole && c % 2) {
+            tc::fence_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              store_rows(to, map, 64 * (c / 2), chunk * kC + 32 * warp, mh, mb);
+              bulk_commit();
+            }
           }
         }
       }
@@ -558,6 +681,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, D == 64 ? 2 : 1)
         if (row == 0) s.odd[i & 1] = 0;
       }
     }
+    if (lane == 0) bulk_wait_read<0>();
   }
   tc::fence_before_sync();
   __syncthreads();
@@ -614,22 +738,24 @@ EncodeTiled encode_fn() {
   return fn;
 }
 
-// [batch, heads, T, D] bf16 rows in boxes of 128 tokens x 64 elements; an axis that all share
-// (stride 0) is one long.
-bool make_map(CUtensorMap *map, const LinearRows &x, const LinearArgs &a, int *axes) {
+// [batch, heads, T, D] rows in boxes of 128 bytes x `tokens`; an axis of stride 0 (one long, or the
+// same for all) is one long.
+bool make_map(CUtensorMap *map, const void *x, const long long (&s)[3], bool f32, int batch, int heads,
+              int T, int d, int tokens, int *axes) {
   EncodeTiled fn = encode_fn();
   if (!fn) return false;
-  axes[0] = x.s[0] != 0;
-  axes[1] = x.s[1] != 0;
-  const cuuint64_t dims[4] = {(cuuint64_t)a.d, (cuuint64_t)a.T, (cuuint64_t)(axes[1] ? a.H / x.share : 1),
-                              (cuuint64_t)(axes[0] ? a.batch : 1)};
-  const cuuint64_t row = (cuuint64_t)a.d * 2;
-  const cuuint64_t strides[3] = {(cuuint64_t)x.s[2] * 2, axes[1] ? (cuuint64_t)x.s[1] * 2 : row,
-                                 axes[0] ? (cuuint64_t)x.s[0] * 2 : row};
-  const cuuint32_t box[4] = {64, kC, 1, 1}, estr[4] = {1, 1, 1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(x.x), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  const cuuint64_t size = f32 ? 4 : 2;
+  axes[0] = s[0] != 0;
+  axes[1] = s[1] != 0;
+  const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)T, (cuuint64_t)(axes[1] ? heads : 1),
+                              (cuuint64_t)(axes[0] ? batch : 1)};
+  const cuuint64_t strides[3] = {(cuuint64_t)s[2] * size, (axes[1] ? (cuuint64_t)s[1] : d) * size,
+                                 (axes[0] ? (cuuint64_t)s[0] : d) * size};
+  const cuuint32_t box[4] = {(cuuint32_t)(128 / size), (cuuint32_t)tokens, 1, 1}, estr[4] = {1, 1, 1, 1};
+  return fn(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+            const_cast<void *>(x), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // Stretches of a sweep: as many as blocks fit at once, two chunks each at least.
@@ -640,14 +766,14 @@ int splits_of(int sweeps, int pairs, int T, int d) {
 }
 
 template <int D>
-cudaError_t run(const Params &p, const CUtensorMap (&m)[4], cudaStream_t st) {
+cudaError_t run(const Params &p, const Maps &m, cudaStream_t st) {
   constexpr int kSmem = Cfg<D>::kBytes + 1024;
   const int pairs = p.a.batch * p.a.H;
   if (p.splits > 1) {
     auto f = k16_linear_kernel<D, false>;
     cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
-    f<<<dim3(p.splits - 1, pairs, p.a.sweeps), Cfg<D>::kThreads, kSmem, st>>>(m[0], m[1], m[2], m[3], p);
+    f<<<dim3(p.splits - 1, pairs, p.a.sweeps), Cfg<D>::kThreads, kSmem, st>>>(m, p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     k16_join_kernel<D><<<dim3(D * D / 1024, pairs, p.a.sweeps), 256, 0, st>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
@@ -655,7 +781,7 @@ cudaError_t run(const Params &p, const CUtensorMap (&m)[4], cudaStream_t st) {
   auto f = k16_linear_kernel<D, true>;
   const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
-  f<<<dim3(p.splits, pairs, p.a.sweeps), Cfg<D>::kThreads, kSmem, st>>>(m[0], m[1], m[2], m[3], p);
+  f<<<dim3(p.splits, pairs, p.a.sweeps), Cfg<D>::kThreads, kSmem, st>>>(m, p);
   return cudaGetLastError();
 }
 
@@ -674,8 +800,8 @@ cudaError_t launch_linear_chunks(const LinearArgs &a, float *states, int *err, c
   p.states = states;
   p.err = err;
   // one map a tensor: the sweeps share theirs
-  CUtensorMap maps[4];
-  memset(maps, 0, sizeof(maps));
+  Maps maps;
+  memset(&maps, 0, sizeof(maps));
   const LinearRows *seen[4];
   auto same = [](const LinearRows &x, const LinearRows &y) {
     return x.x == y.x && x.share == y.share && x.s[0] == y.s[0] && x.s[1] == y.s[1] && x.s[2] == y.s[2];
@@ -689,10 +815,15 @@ cudaError_t launch_linear_chunks(const LinearArgs &a, float *states, int *err, c
       if (m == n) {
         if (n == 4) return cudaErrorInvalidValue;
         seen[n++] = rows[j];
-        if (!make_map(&maps[m], *rows[j], a, p.axes[m])) return cudaErrorInvalidValue;
+        if (!make_map(&maps.in[m], rows[j]->x, rows[j]->s, false, a.batch, a.H / rows[j]->share, a.T, a.d, kC,
+                      p.axes[m]))
+          return cudaErrorInvalidValue;
       }
       p.map[i][j] = m;
     }
+    if (!make_map(&maps.out[i], a.sweep[i].out, a.sweep[i].os, a.sweep[i].out_f32, a.batch, a.H, a.T, a.d, 32,
+                  p.out_axes[i]))
+      return cudaErrorInvalidValue;
   }
   return a.d == 64 ? run<64>(p, maps, st) : run<128>(p, maps, st);
 }
