@@ -736,7 +736,7 @@ int fs_block_norm(const void *x, long long x_stride, int dtype, const void *gate
  *                 where neither dgain nor dnext_gain is wanted
  * dx may be x or dy, dgate may be gate, dresidual may be dz or residual, with their
  * strides; other overlaps give undefined results.  Sums over rows are fp32 within
- * a block's rows, then fp64 in block order: deterministic.  One or two kernels. */
+ * a block's rows, then compensated in block order: deterministic.  One or two kernels. */
 size_t fs_block_norm_workspace_bytes(int M, int D);
 int fs_block_norm_bwd(const void *x, long long x_stride, int dtype, const void *gate,
                       long long gate_stride, const void *residual, long long residual_stride,

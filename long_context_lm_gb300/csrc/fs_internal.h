@@ -247,6 +247,7 @@ struct NormArgs {
   float *ws;
   int mode, per, list;               // set by the launch: how groups are added, vectors
   float inv_n, inv_D;                // (elements) of a group, floats of a team's list
+  bool wide;                         // fp32 rows go 32 bytes at a time
 };
 size_t norm_workspace_bytes(int M, int D);
 cudaError_t launch_norm(const NormArgs &a, cudaStream_t st);

@@ -2,106 +2,129 @@
 //
 //   S_t = lam S_{t-1} + k_t v_t^T,   out_t = scale q_t S_t,   lam = exp(decay)
 //
-// The columns of S (the elements of v and out) do not meet, so a block takes
-// kCols of them: d x kCols of the state in registers, four columns and
-// d / kTeams rows a thread.  For a decoding step the state's bytes are
-// everything (read once, written once: 2 x 4 d^2 bytes against 8 d bytes of
-// rows), so all of a thread's state is under way before anything is computed.
+// The columns of S (the elements of v and out) do not meet, so a block takes 32 of
+// them: 128 bytes of every row, each thread four columns of d / 16 neighbouring rows.
+// For a decoding step the state's bytes are everything (read once, written once:
+// 2 x 4 d^2 bytes against 8 d bytes of rows), so all of a thread's state is under way
+// before anything is computed, and a thread has enough of it (32 elements at d = 128)
+// to carry the decay's exponential and the sums over rows.
 // lam goes in as two fp32 numbers (linear.cuh): as one it would be off by up to
 // 2^-25 in the same direction at every token, and a head with a long memory adds
 // that up over thousands of them.
 #include "fs_common.cuh"
 #include "fs_internal.h"
 #include "linear.cuh"
+#include "pairs.cuh"
 
 namespace fs {
 namespace {
 
-constexpr int kCols = 16, kThreads = 256, kTeams = kThreads / (kCols / 4);
+constexpr int kCols = 32, kThreads = 128;
 
 template <int D>
 __global__ void __launch_bounds__(kThreads) k14_recurrent_kernel(const __grid_constant__ LinearArgs a) {
-  constexpr int kRows = D / kTeams;
+  constexpr int kRows = D / 16;
   const LinearSweep &w = a.sweep[blockIdx.z];
   const int b = blockIdx.y / a.H, h = blockIdx.y % a.H;
-  const int n = a.count ? min(max(a.count[b], 0), a.T) : a.T;
-  const int tid = threadIdx.x, row = tid / (kCols / 4) * kRows;
-  const int col = blockIdx.x * kCols + tid % (kCols / 4) * 4;
-  __shared__ float part[2][kThreads / 32][kCols];
+  const int tid = threadIdx.x, row = tid / 8 * kRows, col = blockIdx.x * kCols + tid % 8 * 4;
+  __shared__ __align__(16) float part[2][kThreads / 32][kCols];
 
-  float s[kRows][4];
+  f2 s[kRows][2];
   const size_t base = (size_t)blockIdx.y * D * D;
 #pragma unroll
   for (int r = 0; r < kRows; ++r) {
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    s[r][0] = s[r][1] = 0;
     if (w.state && !w.transposed) {
-      x = *reinterpret_cast<const float4 *>(w.state + base + (size_t)(row + r) * D + col);
+      const ulonglong2 x = *reinterpret_cast<const ulonglong2 *>(w.state + base + (size_t)(row + r) * D + col);
+      s[r][0] = x.x, s[r][1] = x.y;
     } else if (w.state) {
       const float *p = w.state + base + (size_t)col * D + row + r;
-      x = make_float4(p[0], p[D], p[2 * D], p[3 * D]);
+      s[r][0] = f2_bits(p[0], p[D]), s[r][1] = f2_bits(p[2 * D], p[3 * D]);
     }
-    s[r][0] = x.x * w.state_mul;
-    s[r][1] = x.y * w.state_mul;
-    s[r][2] = x.z * w.state_mul;
-    s[r][3] = x.w * w.state_mul;
   }
+  const int n = a.count ? min(max(a.count[b], 0), a.T) : a.T;
   auto rows = [&](const LinearRows &x) {
     return static_cast<const __nv_bfloat16 *>(x.x) + b * x.s[0] + h / x.share * x.s[1];
   };
-  const __nv_bfloat16 *q = rows(w.q), *k = rows(w.k), *v = rows(w.v);
+  const __nv_bfloat16 *q = rows(w.q) + row, *k = rows(w.k) + row, *v = rows(w.v) + col;
   const Factor lam = decay_power(a.decay[h], 1);
+  const f2 hi = f2_bits(lam.hi, lam.hi), lo = f2_bits(lam.lo, lam.lo);
+  if (w.state_mul != 1.f) {
+    const f2 m = f2_bits(w.state_mul, w.state_mul);
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) s[r][0] = mul2(s[r][0], m), s[r][1] = mul2(s[r][1], m);
+  }
 
   for (int i = 0; i < n; ++i) {
     const long long t = w.reverse ? n - 1 - i : i;
-    const uint2 vv = *reinterpret_cast<const uint2 *>(v + t * w.v.s[2] + col);
-    const float vf[4] = {bf16_lo(vv.x), bf16_hi(vv.x), bf16_lo(vv.y), bf16_hi(vv.y)};
-    float o[4] = {0.f, 0.f, 0.f, 0.f};
+    const uint2 vv = *reinterpret_cast<const uint2 *>(v + t * w.v.s[2]);
+    uint32_t kk[kRows / 2], qq[kRows / 2];
+    if constexpr (D == 128) {
+      const uint4 x = *reinterpret_cast<const uint4 *>(k + t * w.k.s[2]);
+      const uint4 y = *reinterpret_cast<const uint4 *>(q + t * w.q.s[2]);
+      kk[0] = x.x, kk[1] = x.y, kk[2] = x.z, kk[3] = x.w;
+      qq[0] = y.x, qq[1] = y.y, qq[2] = y.z, qq[3] = y.w;
+    } else {
+      const uint2 x = *reinterpret_cast<const uint2 *>(k + t * w.k.s[2]);
+      const uint2 y = *reinterpret_cast<const uint2 *>(q + t * w.q.s[2]);
+      kk[0] = x.x, kk[1] = x.y;
+      qq[0] = y.x, qq[1] = y.y;
+    }
+    const f2 v2[2] = {wide2(vv.x), wide2(vv.y)};
+    f2 o[2] = {0, 0};
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
-      const float kf = __bfloat162float(k[t * w.k.s[2] + row + r]);
-      const float qf = __bfloat162float(q[t * w.q.s[2] + row + r]);
+      const float kf = r % 2 ? bf16_hi(kk[r / 2]) : bf16_lo(kk[r / 2]);
+      const float qf = r % 2 ? bf16_hi(qq[r / 2]) : bf16_lo(qq[r / 2]);
+      const f2 k2 = f2_bits(kf, kf), q2 = f2_bits(qf, qf);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const float kv = kf * vf[c];
-        const float x = w.reverse ? s[r][c] + kv : lam.times(s[r][c], kv);
-        o[c] = fmaf(qf, x, o[c]);
-        s[r][c] = w.reverse ? lam.times(x, 0.f) : x;
+      for (int c = 0; c < 2; ++c) {
+        f2 x = s[r][c];
+        if (w.reverse) {
+          x = madd2(k2, v2[c], x);
+          s[r][c] = madd2(x, hi, mul2(x, lo));
+        } else {
+          x = s[r][c] = madd2(x, hi, madd2(x, lo, mul2(k2, v2[c])));
+        }
+        o[c] = madd2(q2, x, o[c]);
       }
     }
+    float y[4] = {lo2(o[0]), hi2(o[0]), lo2(o[1]), hi2(o[1])};
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
-#pragma unroll
-      for (int m = kCols / 4; m < 32; m *= 2) o[c] += __shfl_xor_sync(0xffffffffu, o[c], m);
-    if (tid % 32 < kCols / 4)
-      *reinterpret_cast<float4 *>(&part[i & 1][tid / 32][tid % 32 * 4]) =
-          make_float4(o[0], o[1], o[2], o[3]);
+    for (int c = 0; c < 4; ++c) {
+      y[c] += __shfl_xor_sync(0xffffffffu, y[c], 8);
+      y[c] += __shfl_xor_sync(0xffffffffu, y[c], 16);
+    }
+    if (tid % 32 < 8)
+      *reinterpret_cast<float4 *>(&part[i & 1][tid / 32][tid % 32 * 4]) = make_float4(y[0], y[1], y[2], y[3]);
     __syncthreads();  // (the other half of `part` is free: its readers are past this token's barrier)
     if (tid < kCols / 2) {
-      float x = 0.f, y = 0.f;
+      float x = 0.f, z = 0.f;
 #pragma unroll
       for (int j = 0; j < kThreads / 32; ++j) {
         x += part[i & 1][j][2 * tid];
-        y += part[i & 1][j][2 * tid + 1];
+        z += part[i & 1][j][2 * tid + 1];
       }
       const long long at = b * w.os[0] + h * w.os[1] + t * w.os[2] + blockIdx.x * kCols + 2 * tid;
       x *= a.scale;
-      y *= a.scale;
+      z *= a.scale;
       if (w.out_f32)
-        *reinterpret_cast<float2 *>(static_cast<float *>(w.out) + at) = make_float2(x, y);
+        *reinterpret_cast<float2 *>(static_cast<float *>(w.out) + at) = make_float2(x, z);
       else
-        *reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(w.out) + at) = pack_bf16(x, y);
+        *reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(w.out) + at) = pack_bf16(x, z);
     }
   }
   if (!w.state_out) return;
   const float mul = 1.f / w.state_mul;
+  const f2 m = f2_bits(mul, mul);
 #pragma unroll
   for (int r = 0; r < kRows; ++r) {
-    const float4 x = make_float4(s[r][0] * mul, s[r][1] * mul, s[r][2] * mul, s[r][3] * mul);
+    const f2 x = mul2(s[r][0], m), y = mul2(s[r][1], m);
     if (!w.transposed) {
-      *reinterpret_cast<float4 *>(w.state_out + base + (size_t)(row + r) * D + col) = x;
+      *reinterpret_cast<ulonglong2 *>(w.state_out + base + (size_t)(row + r) * D + col) = make_ulonglong2(x, y);
     } else {
       float *p = w.state_out + base + (size_t)col * D + row + r;
-      p[0] = x.x, p[D] = x.y, p[2 * D] = x.z, p[3 * D] = x.w;
+      p[0] = lo2(x), p[D] = hi2(x), p[2 * D] = lo2(y), p[3 * D] = hi2(y);
     }
   }
 }

@@ -11,12 +11,18 @@
 //   dgate = scale g h gain silu'(gate),   dgain = sum over rows of scale g silu(gate) h
 //   dx = r_g (u - h mean_group(u h)),     u = scale g silu(gate) gain
 //
-// Memory bounds both: every tensor is read or written once.  A team of
-// threads holds a row in registers from its loads, all issued together, to
-// its stores, so that z or y may take the place of an input.  Sums are fp32
-// in a fixed order.  The gradients of the gains are sums over rows: a team
-// keeps those of its columns over all rows that it takes, blocks put theirs
-// into the workspace and a second kernel adds them in block order.
+// Memory bounds both: every tensor is read or written once.  A team of threads takes a
+// row.  In the backward pass it takes one after another, each thread its own vectors, and the
+// next row is under way into shared memory (asynchronous copies that nobody else waits
+// for) while it works on this one: 16384 x 1024 gated heads in bf16 42 us instead of 65;
+// rows too wide for that, and rows off sixteen bytes, are read where they lie.  (The
+// forward pass gained nothing from it: 77 us against 71, and 464 against 272 where rows are
+// wide and one block had an SM to itself.)
+// A thread has read an element of an input for the last time before it writes the
+// output that may take its place.  Sums are fp32 in a fixed order.  The
+// gradients of the gains are sums over rows: a thread keeps those of its columns over all
+// rows that it takes, blocks put theirs into the workspace and a second kernel adds them
+// in block order.
 #include "fs_common.cuh"
 #include "fs_internal.h"
 #include "pairs.cuh"
@@ -27,53 +33,76 @@ namespace {
 // How a row's groups are added up.
 enum Groups { kNone, kRow, kShuffle, kList };
 
-// Sixteen bytes of a row of TX, or as many elements of TR: as they are in memory.
+__device__ __forceinline__ f2 both(float x) { return f2_bits(x, x); }
+
+// V elements of a row as they are in memory: sixteen bytes of TX, as many elements of TR.
 template <typename T, int V>
 struct Raw {
-  f2 x[V / 2];
-  __device__ __forceinline__ f2 get(int c) const { return x[c]; }
-};
-template <int V>
-struct Raw<__nv_bfloat16, V> {
-  uint32_t x[V / 2];
-  __device__ __forceinline__ f2 get(int c) const { return wide2(x[c]); }
-};
-
-// kWhole: rows are whole vectors on sixteen bytes.  Otherwise element by element.
-template <bool kWhole, typename T, int V>
-__device__ __forceinline__ void load(const void *row, int e, int D, Raw<T, V> &r) {
-  const T *p = static_cast<const T *>(row) + e;
-  if constexpr (kWhole) {
-#pragma unroll
-    for (int c = 0; c < V / 2; ++c) r.x[c] = 0;
-    if (e >= D) return;
+  static constexpr int kPieces = V * sizeof(T) / 16;
+  uint4 u[kPieces];
+  __device__ __forceinline__ f2 get(int c) const {
     if constexpr (sizeof(T) == 2) {
-      const uint4 u = *reinterpret_cast<const uint4 *>(p);
-      r.x[0] = u.x, r.x[1] = u.y, r.x[2] = u.z, r.x[3] = u.w;
+      return wide2(c == 0 ? u[0].x : c == 1 ? u[0].y : c == 2 ? u[0].z : u[0].w);
     } else {
-#pragma unroll
-      for (int c = 0; c < V / 2; c += 2) {
-        const ulonglong2 u = *reinterpret_cast<const ulonglong2 *>(p + 2 * c);
-        r.x[c] = u.x, r.x[c + 1] = u.y;
-      }
-    }
-  } else {
-#pragma unroll
-    for (int c = 0; c < V / 2; ++c) {
-      const float x = e + 2 * c < D ? static_cast<float>(p[2 * c]) : 0.f;
-      const float y = e + 2 * c + 1 < D ? static_cast<float>(p[2 * c + 1]) : 0.f;
-      if constexpr (sizeof(T) == 2)
-        r.x[c] = pack_bf16(x, y);  // (bf16 numbers: nothing is rounded)
-      else
-        r.x[c] = f2_bits(x, y);
+      const uint4 &w = u[c / 2];
+      return c % 2 ? (f2)w.z | (f2)w.w << 32 : (f2)w.x | (f2)w.y << 32;
     }
   }
+};
+
+// V elements at p, of which the row has `left` more (kWhole: all or none).  `wide`: eight fp32
+// elements lie on 32 bytes and go as one (as two of sixteen bytes each, a warp would touch every
+// sector twice).
+template <bool kWhole, typename T, int V>
+__device__ __forceinline__ Raw<T, V> load(const T *p, int left, bool wide) {
+  Raw<T, V> r;
+  if constexpr (kWhole) {
+#pragma unroll
+    for (int i = 0; i < Raw<T, V>::kPieces; ++i) r.u[i] = make_uint4(0, 0, 0, 0);
+    if (left > 0) {
+      if constexpr (Raw<T, V>::kPieces == 2) {
+        if (wide) {
+          asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                       : "=r"(r.u[0].x), "=r"(r.u[0].y), "=r"(r.u[0].z), "=r"(r.u[0].w), "=r"(r.u[1].x),
+                         "=r"(r.u[1].y), "=r"(r.u[1].z), "=r"(r.u[1].w)
+                       : "l"(p)
+                       : "memory");
+          return r;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < Raw<T, V>::kPieces; ++i) r.u[i] = *(reinterpret_cast<const uint4 *>(p) + i);
+    }
+  } else {
+    uint32_t w[4 * Raw<T, V>::kPieces];
+#pragma unroll
+    for (int c = 0; c < V / 2; ++c) {
+      const float x = 2 * c < left ? static_cast<float>(p[2 * c]) : 0.f;
+      const float y = 2 * c + 1 < left ? static_cast<float>(p[2 * c + 1]) : 0.f;
+      if constexpr (sizeof(T) == 2) {
+        w[c] = pack_bf16(x, y);  // (bf16 numbers: nothing is rounded)
+      } else {
+        w[2 * c] = __float_as_uint(x);
+        w[2 * c + 1] = __float_as_uint(y);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < Raw<T, V>::kPieces; ++i)
+      r.u[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+  }
+  return r;
 }
 template <bool kWhole, typename T, int V>
-__device__ __forceinline__ void store(void *row, int e, int D, const f2 (&x)[V / 2]) {
-  T *p = static_cast<T *>(row) + e;
+__device__ __forceinline__ void store(T *p, int left, const f2 (&x)[V / 2], bool wide) {
   if constexpr (kWhole) {
-    if (e >= D) return;
+    if (left <= 0) return;
+    if constexpr (sizeof(T) == 4 && V == 8) {
+      if (wide) {
+        asm volatile("st.global.v4.b64 [%0], {%1, %2, %3, %4};" ::"l"(p), "l"(x[0]), "l"(x[1]), "l"(x[2]), "l"(x[3])
+                     : "memory");
+        return;
+      }
+    }
     if constexpr (sizeof(T) == 2) {
       *reinterpret_cast<uint4 *>(p) = make_uint4(pack2(x[0]), pack2(x[1]), pack2(x[2]), pack2(x[3]));
     } else {
@@ -84,11 +113,84 @@ __device__ __forceinline__ void store(void *row, int e, int D, const f2 (&x)[V /
   } else {
 #pragma unroll
     for (int c = 0; c < V / 2; ++c) {
-      if (e + 2 * c < D) p[2 * c] = static_cast<T>(lo2(x[c]));
-      if (e + 2 * c + 1 < D) p[2 * c + 1] = static_cast<T>(hi2(x[c]));
+      if (2 * c < left) p[2 * c] = static_cast<T>(lo2(x[c]));
+      if (2 * c + 1 < left) p[2 * c + 1] = static_cast<T>(hi2(x[c]));
     }
   }
 }
+
+// A thread's vectors of one tensor's rows.  kStaged: this row and the next in shared memory, piece
+// after piece, threads side by side.
+template <bool kStaged, bool kWhole, typename T, int V, int N>
+struct Slot {
+  enum { kPieces = Raw<T, V>::kPieces };
+  uint32_t at;    // (shared memory) this thread's first piece of stage 0, 0 without the tensor
+  uint32_t stage; // bytes from a stage to the next
+  const T *row;   // the next row to fetch (not kStaged: to read), at this thread's first element
+  long long step; // elements to the team's row after it
+  __device__ __forceinline__ void init(uint32_t &free, const void *p, long long stride, long long first, int rows,
+                                       int e0) {
+    at = stage = 0;
+    if constexpr (kStaged) {
+      stage = N * kPieces * blockDim.x * 16;
+      if (p) at = free + threadIdx.x * 16, free += 2 * stage;
+    }
+    row = static_cast<const T *>(p) + first * stride + e0;
+    step = rows * stride;
+  }
+  // `left` elements from the thread's first on, 0 without a row; `apart` elements from vector to vector.
+  __device__ __forceinline__ void fetch(int which, int left, int apart) {
+    if constexpr (kStaged) {
+      if (!at) return;
+      const uint32_t to = at + which * stage;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const bool have = left - i * apart > 0;
+#pragma unroll
+        for (int k = 0; k < kPieces; ++k) {
+          const uint32_t piece = to + (i * kPieces + k) * blockDim.x * 16;
+          if (have)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(piece),
+                         "l"(reinterpret_cast<const uint4 *>(row + i * apart) + k));
+          else
+            put(piece, make_uint4(0, 0, 0, 0));
+        }
+      }
+      row += step;
+    }
+  }
+  // A row that stays: the gains'.
+  __device__ __forceinline__ void fill(int left, int apart) {
+    if (!at) return;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const Raw<T, V> r = load<kWhole, T, V>(row + i * apart, left - i * apart, false);
+#pragma unroll
+      for (int k = 0; k < kPieces; ++k) put(at + (i * kPieces + k) * blockDim.x * 16, r.u[k]);
+    }
+  }
+  static __device__ __forceinline__ void put(uint32_t at, const uint4 &x) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(at), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w)
+                 : "memory");
+  }
+  __device__ __forceinline__ void next() {
+    if constexpr (!kStaged) row += step;
+  }
+  __device__ __forceinline__ Raw<T, V> get(int which, int i, int left, int apart) const {
+    if constexpr (kStaged) {
+      Raw<T, V> r;
+#pragma unroll
+      for (int k = 0; k < kPieces; ++k)
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];\n"
+                     : "=r"(r.u[k].x), "=r"(r.u[k].y), "=r"(r.u[k].z), "=r"(r.u[k].w)
+                     : "r"(at + which * stage + (i * kPieces + k) * blockDim.x * 16)
+                     : "memory");
+      return r;
+    } else {
+      return load<kWhole, T, V>(row + i * apart, left - i * apart, false);
+    }
+  }
+};
 
 // 1 / (1 + e^-x) by the special-function unit: 2^-20 of itself, enough for bf16 results.
 // kExact: with the exponent's rounding put back and a Newton step on the reciprocal, 2^-22.
@@ -97,13 +199,13 @@ __device__ __forceinline__ float sigmoid(float x) {
   constexpr float kL = -1.44269504f, kRest = -1.92596303e-8f;  // -log2 e, what it lacks
   float t = x * kL, e, r;
   if constexpr (kExact) t = fminf(t, 126.f);  // (past it the Newton step would meet an infinity)
-  asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(t));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
   if constexpr (kExact) {
     const float rest = fmaf(x, kL, -t) + x * kRest;
     if (t < 126.f) e = fmaf(e, rest * 0.693147181f, e);
   }
   const float d = 1.f + e;
-  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(d));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
   if constexpr (kExact) r = fmaf(r, fmaf(-d, r, 1.f), r);
   return r;
 }
@@ -119,66 +221,51 @@ struct PerGroup {
   __device__ __forceinline__ f2 get(int c) const { return x[kWhole ? 0 : c]; }
 };
 
-__device__ __forceinline__ f2 both(float x) { return f2_bits(x, x); }
-
-// A team's way to add.  TPR threads take a row, N vectors of V elements each: vector i of
-// thread t is number t + i TPR of the row.
-template <int TPR, int V, int N, bool kWhole>
+// A team's way to add: the block's threads (kTeam 0), or kTeam = 8 or 32 of a block of
+// 256.  N vectors of V elements each: vector i of thread t is number t + i size of the row.
+template <int kTeam, int V, int N, bool kWhole>
 struct Team {
-  static constexpr int kThreads = TPR < 256 ? 256 : TPR, kTeams = kThreads / TPR;
-  static constexpr int kLanes = TPR < 32 ? TPR : 32;
-  int t, team;    // thread within the team, team within the block
-  float *scratch; // TPR > 32: two halves of the team's warps, in turn
-  float *list;    // sums of vectors (elements), then of groups
+  static constexpr int kLanes = kTeam ? kTeam : 32;
+  int t, team, size;  // thread within the team, team within the block, threads of a team
+  float *scratch;     // two halves of the block's warps, in turn
+  float *list;        // sums of vectors (elements), then of groups
   int turn;
 
   __device__ __forceinline__ void sync() const {
-    if constexpr (TPR <= 32)
+    if constexpr (kTeam)
       __syncwarp();
-    else if constexpr (kTeams == 1)
-      __syncthreads();
     else
-      asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "n"(TPR) : "memory");
+      __syncthreads();
   }
-  // K sums over the team, the same in every thread.
+  // K <= 2 sums over the team, the same in every thread.
   template <int K>
   __device__ __forceinline__ void add(float (&x)[K]) {
 #pragma unroll
     for (int m = 1; m < kLanes; m *= 2)
 #pragma unroll
       for (int k = 0; k < K; ++k) x[k] += __shfl_xor_sync(0xffffffffu, x[k], m);
-    if constexpr (TPR > 32) {
-      constexpr int kWarps = TPR / 32;
-      float *to = scratch + (turn ^= 1) * 2 * kWarps;
-      if (t % 32 == 0)
+    if (kTeam || size == 32) return;
+    const int warps = size / 32, lane = t % 32;
+    float *to = scratch + (turn ^= 1) * 2 * 16;
+    if (lane == 0)
 #pragma unroll
-        for (int k = 0; k < K; ++k) to[k * kWarps + t / 32] = x[k];
-      sync();
-      if constexpr (kWarps <= 4) {
+      for (int k = 0; k < K; ++k) to[k * 16 + t / 32] = x[k];
+    sync();
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-          x[k] = to[k * kWarps];
+    for (int k = 0; k < K; ++k) x[k] = lane < warps ? to[k * 16 + lane] : 0.f;  // at most sixteen
 #pragma unroll
-          for (int j = 1; j < kWarps; ++j) x[k] += to[k * kWarps + j];
-        }
-      } else {  // a warp adds them as it added its own
+    for (int m = 8; m > 0; m /= 2)
 #pragma unroll
-        for (int k = 0; k < K; ++k) x[k] = t % 32 < kWarps ? to[k * kWarps + t % 32] : 0.f;
+      for (int k = 0; k < K; ++k) x[k] += __shfl_xor_sync(0xffffffffu, x[k], m);
 #pragma unroll
-        for (int m = 1; m < kWarps; m *= 2)
-#pragma unroll
-          for (int k = 0; k < K; ++k) x[k] += __shfl_xor_sync(0xffffffffu, x[k], m);
-#pragma unroll
-        for (int k = 0; k < K; ++k) x[k] = __shfl_sync(0xffffffffu, x[k], 0);
-      }
-    }
+    for (int k = 0; k < K; ++k) x[k] = __shfl_sync(0xffffffffu, x[k], 0);
   }
   // Sums over groups of the products f(i, c) (pair c of vector i).  Groups of a power of two
   // of whole vectors, up to a warp's: by shuffles.  Others through `list`: a group to a
   // warp (or small team) at a time.
   template <typename F>
   __device__ __forceinline__ void add_groups(PerGroup<kWhole, V> (&p)[N], const NormArgs &a, F f) {
-    const int mode = kWhole || a.mode <= kRow ? a.mode : kList;
+    const int mode = a.mode;
     const int n = kWhole ? a.D / V : a.D;
     if (mode == kList) sync();  // (the list is free: its readers are past this)
     float v[N];
@@ -190,7 +277,7 @@ struct Team {
         const f2 x = f(i, c);
         s = c ? add2_bits(s, x) : x;
         if constexpr (!kWhole) {
-          const int e = (t + i * TPR) * V + 2 * c;
+          const int e = (t + i * size) * V + 2 * c;
           if (mode == kList && e < n) list[e] = lo2(x);
           if (mode == kList && e + 1 < n) list[e + 1] = hi2(x);
         }
@@ -212,10 +299,10 @@ struct Team {
       if constexpr (kWhole) {
 #pragma unroll
         for (int i = 0; i < N; ++i)
-          if (t + i * TPR < n) list[t + i * TPR] = v[i];
+          if (t + i * size < n) list[t + i * size] = v[i];
       }
       sync();
-      for (int g = t / kLanes; g < a.groups; g += TPR / kLanes) {
+      for (int g = t / kLanes; g < a.groups; g += size / kLanes) {
         float s = 0.f;
         for (int j = t % kLanes; j < a.per; j += kLanes) s += list[g * a.per + j];
 #pragma unroll
@@ -226,13 +313,13 @@ struct Team {
       if constexpr (kWhole) {
 #pragma unroll
         for (int i = 0; i < N; ++i)
-          if (t + i * TPR < n) v[i] = list[n + (t + i * TPR) / a.per];
+          if (t + i * size < n) v[i] = list[n + (t + i * size) / a.per];
       } else {
 #pragma unroll
         for (int i = 0; i < N; ++i)
 #pragma unroll
           for (int c = 0; c < V / 2; ++c) {
-            const int e = (t + i * TPR) * V + 2 * c;
+            const int e = (t + i * size) * V + 2 * c;
             p[i].x[c] = f2_bits(e < n ? list[n + e / a.per] : 0.f, e + 1 < n ? list[n + (e + 1) / a.per] : 0.f);
           }
         return;
@@ -243,9 +330,9 @@ struct Team {
 #pragma unroll
       for (int c = 0; c < (kWhole ? 1 : V / 2); ++c) p[i].x[c] = both(v[i]);
   }
-  // The factors that normalise x's groups (ones where they are not to be).
-  template <typename T>
-  __device__ __forceinline__ void factors(const Raw<T, V> (&x)[N], PerGroup<kWhole, V> (&inv)[N], const NormArgs &a) {
+  // The factors that normalise x's groups (ones where they are not to be); x(i): vector i.
+  template <typename F>
+  __device__ __forceinline__ void factors(PerGroup<kWhole, V> (&inv)[N], const NormArgs &a, F x) {
     if (a.mode == kNone) {
 #pragma unroll
       for (int i = 0; i < N; ++i)
@@ -253,13 +340,16 @@ struct Team {
         for (int c = 0; c < (kWhole ? 1 : V / 2); ++c) inv[i].x[c] = both(1.f);
       return;
     }
-    add_groups(inv, a, [&](int i, int c) { return mul2(x[i].get(c), x[i].get(c)); });
+    add_groups(inv, a, [&](int i, int c) {
+      const f2 y = x(i).get(c);
+      return mul2(y, y);
+    });
 #pragma unroll
     for (int i = 0; i < N; ++i)
 #pragma unroll
       for (int c = 0; c < (kWhole ? 1 : V / 2); ++c) {
         // (past the row 0: with eps 0 the factor there would be infinite)
-        const int e = (t + i * TPR) * V + 2 * c;
+        const int e = (t + i * size) * V + 2 * c;
         const float f = e < a.D ? rsqrtf(fmaf(lo2(inv[i].x[c]), a.inv_n, a.eps)) : 0.f;
         const float g = kWhole ? f : e + 1 < a.D ? rsqrtf(fmaf(hi2(inv[i].x[c]), a.inv_n, a.eps)) : 0.f;
         inv[i].x[c] = f2_bits(f, g);
@@ -267,308 +357,352 @@ struct Team {
   }
 };
 
-template <typename TX, typename TR, int TPR, int N, bool kWhole>
-__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k15_norm_kernel(const __grid_constant__ NormArgs a) {
+// Blocks of up to 512 threads, two or more to an SM; small teams share blocks of 256.  A team takes
+// one row, all of whose loads are issued before anything else; other blocks' rows fill its waits.
+template <typename TX, typename TR, int kTeam, int N, bool kWhole>
+__global__ void __launch_bounds__(kTeam ? 256 : 512, sizeof(TX) == 4 || N * 8 > 16 ? 1 : 2)
+    k15_norm_kernel(const __grid_constant__ NormArgs a) {
   constexpr int V = 16 / sizeof(TX);
-  using T = Team<TPR, V, N, kWhole>;
-  extern __shared__ float lists[];
-  __shared__ float scratch[T::kTeams][TPR > 32 ? 4 * TPR / 32 : 1];
-  T team{(int)threadIdx.x % TPR, (int)threadIdx.x / TPR, nullptr, nullptr, 0};
-  team.scratch = scratch[team.team];
-  team.list = lists + team.team * a.list;
-  // (a small team without a row keeps its warp's shuffles and barriers company)
-  const long long want = (long long)blockIdx.x * T::kTeams + team.team;
-  if (TPR >= 32 && want >= a.M) return;
-  const bool have = want < a.M;
-  const long long row = have ? want : a.M - 1;
-  const int e0 = team.t * V;
+  extern __shared__ uint4 slots[];
+  __shared__ float scratch[64];
+  Team<kTeam, V, N, kWhole> team;
+  team.size = kTeam ? kTeam : blockDim.x;
+  team.t = kTeam ? threadIdx.x % kTeam : threadIdx.x;
+  team.team = kTeam ? threadIdx.x / kTeam : 0;
+  team.scratch = scratch;
+  team.list = reinterpret_cast<float *>(slots) + team.team * a.list;
+  team.turn = 0;
+  const int e0 = team.t * V, apart = team.size * V;
+  // (a team without a row, in a block with one, keeps its warp company on zeros)
+  const long long row = (long long)blockIdx.x * (kTeam ? 256 / kTeam : 1) + team.team;
+  const int left = row < a.M ? a.D - e0 : 0;
 
   Raw<TX, V> x[N], gate[N];
-  f2 z[N][V / 2];
-  {
-    const TX *xr = static_cast<const TX *>(a.x) + row * a.xs;
-#pragma unroll
-    for (int i = 0; i < N; ++i) load<kWhole>(xr, e0 + i * TPR * V, a.D, x[i]);
-  }
-  if (a.gate) {
-    const TX *gr = static_cast<const TX *>(a.gate) + row * a.gs;
-#pragma unroll
-    for (int i = 0; i < N; ++i) load<kWhole>(gr, e0 + i * TPR * V, a.D, gate[i]);
-  }
   Raw<TR, V> res[N];
-  if (a.residual) {
-    const TR *rr = static_cast<const TR *>(a.residual) + row * a.rs;
+  const TX *xr = static_cast<const TX *>(a.x) + row * a.xs + e0;
 #pragma unroll
-    for (int i = 0; i < N; ++i) load<kWhole>(rr, e0 + i * TPR * V, a.D, res[i]);
-  }
-  {
-    PerGroup<kWhole, V> inv[N];
-    team.factors(x, inv, a);
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-#pragma unroll
-      for (int c = 0; c < V / 2; ++c) z[i][c] = mul2(x[i].get(c), inv[i].get(c));
-  }
-  if (a.gain) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      Raw<float, V> g;
-      load<kWhole>(a.gain, e0 + i * TPR * V, a.D, g);
-#pragma unroll
-      for (int c = 0; c < V / 2; ++c) z[i][c] = mul2(z[i][c], g.x[c]);
-    }
-  }
+  for (int i = 0; i < N; ++i) x[i] = load<kWhole, TX, V>(xr + i * apart, left - i * apart, a.wide);
   if (a.gate) {
+    const TX *gr = static_cast<const TX *>(a.gate) + row * a.gs + e0;
 #pragma unroll
-    for (int i = 0; i < N; ++i)
+    for (int i = 0; i < N; ++i) gate[i] = load<kWhole, TX, V>(gr + i * apart, left - i * apart, a.wide);
+  }
+  if (a.residual) {
+    const TR *rr = static_cast<const TR *>(a.residual) + row * a.rs + e0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) res[i] = load<kWhole, TR, V>(rr + i * apart, left - i * apart, a.wide);
+  }
+  const f2 scale = both(a.scale);
+  PerGroup<kWhole, V> inv[N];
+  team.factors(inv, a, [&](int i) { return x[i]; });
+  f2 z[N][V / 2], ss = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+#pragma unroll
+    for (int c = 0; c < V / 2; ++c) z[i][c] = mul2(x[i].get(c), inv[i].get(c));
+    if (a.gain) {
+      const Raw<float, V> g = load<kWhole, float, V>(a.gain + e0 + i * apart, a.D - e0 - i * apart, a.wide);
+#pragma unroll
+      for (int c = 0; c < V / 2; ++c) z[i][c] = mul2(z[i][c], g.get(c));
+    }
+    if (a.gate) {
 #pragma unroll
       for (int c = 0; c < V / 2; ++c) {
         const f2 g = gate[i].get(c);
         z[i][c] = mul2(z[i][c], mul2(g, sigmoid2<sizeof(TX) == 4>(g)));
       }
-  }
-  const f2 scale = both(a.scale);
-  if (a.residual) {
-#pragma unroll
-    for (int i = 0; i < N; ++i)
+    }
+    if (a.residual) {
 #pragma unroll
       for (int c = 0; c < V / 2; ++c) z[i][c] = madd2(scale, z[i][c], res[i].get(c));
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i)
+    } else {
 #pragma unroll
       for (int c = 0; c < V / 2; ++c) z[i][c] = mul2(scale, z[i][c]);
+    }
   }
-  float f = 0.f;
+  if (a.z) {
+    TR *zr = static_cast<TR *>(a.z) + row * a.zs + e0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) store<kWhole, TR, V>(zr + i * apart, left - i * apart, z[i], a.wide);
+  }
+  f2 f = 0;
   if (a.next) {
-    f2 s = 0;
 #pragma unroll
     for (int i = 0; i < N; ++i)
 #pragma unroll
-      for (int c = 0; c < V / 2; ++c) s = madd2(z[i][c], z[i][c], s);
-    float ss[1] = {lo2(s) + hi2(s)};
-    team.add(ss);
-    f = rsqrtf(fmaf(ss[0], a.inv_D, a.eps));
+      for (int c = 0; c < V / 2; ++c) ss = madd2(z[i][c], z[i][c], ss);
+    float s[1] = {lo2(ss) + hi2(ss)};
+    team.add(s);
+    f = both(rsqrtf(fmaf(s[0], a.inv_D, a.eps)));
   }
-  if (!have) return;
-  if (a.z) {
-    TR *zr = static_cast<TR *>(a.z) + row * a.zs;
+  if (!a.next) return;
+  TX *yr = static_cast<TX *>(a.y) + row * a.ys + e0;
 #pragma unroll
-    for (int i = 0; i < N; ++i) store<kWhole, TR, V>(zr, e0 + i * TPR * V, a.D, z[i]);
-  }
-  if (a.next) {
-    TX *yr = static_cast<TX *>(a.y) + row * a.ys;
+  for (int i = 0; i < N; ++i) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
+    for (int c = 0; c < V / 2; ++c) z[i][c] = mul2(z[i][c], f);
+    if (a.next_gain) {
+      const Raw<float, V> g = load<kWhole, float, V>(a.next_gain + e0 + i * apart, a.D - e0 - i * apart, a.wide);
 #pragma unroll
-      for (int c = 0; c < V / 2; ++c) z[i][c] = mul2(z[i][c], both(f));
-      if (a.next_gain) {
-        Raw<float, V> g;
-        load<kWhole>(a.next_gain, e0 + i * TPR * V, a.D, g);
-#pragma unroll
-        for (int c = 0; c < V / 2; ++c) z[i][c] = mul2(z[i][c], g.x[c]);
-      }
-      store<kWhole, TX, V>(yr, e0 + i * TPR * V, a.D, z[i]);
+      for (int c = 0; c < V / 2; ++c) z[i][c] = mul2(z[i][c], g.get(c));
     }
+    store<kWhole, TX, V>(yr + i * apart, left - i * apart, z[i], a.wide);
   }
 }
 
-template <typename TX, typename TR, int TPR, int N, bool kWhole>
-__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, 1) k15_norm_bwd_kernel(const __grid_constant__ NormArgs a) {
+template <typename TX, typename TR, int kTeam, int N, bool kWhole, bool kStaged>
+__global__ void __launch_bounds__(kTeam ? 256 : 512, 1) k15_norm_bwd_kernel(const __grid_constant__ NormArgs a) {
   constexpr int V = 16 / sizeof(TX);
   constexpr bool kExact = sizeof(TX) == 4;
-  using T = Team<TPR, V, N, kWhole>;
-  extern __shared__ float lists[];
-  __shared__ float scratch[T::kTeams][TPR > 32 ? 4 * TPR / 32 : 1];
-  T team{(int)threadIdx.x % TPR, (int)threadIdx.x / TPR, nullptr, nullptr, 0};
-  team.scratch = scratch[team.team];
-  team.list = lists + team.team * a.list;
-  const int step = gridDim.x * T::kTeams, e0 = team.t * V;
-  f2 dgain[N][V / 2] = {}, dnext[N][V / 2] = {};
+  extern __shared__ uint4 slots[];
+  __shared__ float scratch[64];
+  Team<kTeam, V, N, kWhole> team;
+  team.size = kTeam ? kTeam : blockDim.x;
+  team.t = kTeam ? threadIdx.x % kTeam : threadIdx.x;
+  team.team = kTeam ? threadIdx.x / kTeam : 0;
+  team.scratch = scratch;
+  team.turn = 0;
+  const int teams = kTeam ? 256 / kTeam : 1, rows = gridDim.x * teams;
+  const int e0 = team.t * V, apart = team.size * V;
+  long long row = (long long)blockIdx.x * teams + team.team;
+  uint32_t free = smem_u32(slots);
+  Slot<kStaged, kWhole, TX, V, N> x, gate, dy;
+  Slot<kStaged, kWhole, TR, V, N> dz, res;
+  Slot<kStaged, kWhole, float, V, N> gain, next;  // (one row: stage 0)
+  x.init(free, a.x, a.xs, row, rows, e0);
+  gate.init(free, a.gate, a.gs, row, rows, e0);
+  dz.init(free, a.dz, a.dzs, row, rows, e0);
+  dy.init(free, a.dy, a.dys, row, rows, e0);
+  res.init(free, a.next ? a.residual : nullptr, a.rs, row, rows, e0);
+  gain.init(free, a.gain, 0, 0, 0, e0);
+  if (a.gain) free -= gain.stage;
+  next.init(free, a.next_gain, 0, 0, 0, e0);
+  if (a.next_gain) free -= next.stage;
+  if constexpr (kStaged) gain.fill(a.D - e0, apart), next.fill(a.D - e0, apart);
+  team.list = reinterpret_cast<float *>(slots) + (free - smem_u32(slots)) / 4 + team.team * a.list;
+  TX *dxr = static_cast<TX *>(a.dx) + row * a.dxs + e0, *dgr = static_cast<TX *>(a.dgate) + row * a.dgs + e0;
+  TR *drr = static_cast<TR *>(a.dres) + row * a.drs + e0;
+  auto fetch = [&](int which, bool have) {
+    const int left = have ? a.D - e0 : 0;
+    x.fetch(which, left, apart);
+    gate.fetch(which, left, apart);
+    dz.fetch(which, left, apart);
+    dy.fetch(which, left, apart);
+    res.fetch(which, left, apart);
+    cp_async_commit();
+  };
+  if constexpr (kStaged) fetch(0, row < a.M);
+  f2 dgain[N][V / 2] = {}, dnext[N][V / 2] = {};  // (zeros of a team without a row add nothing)
   const f2 scale = both(a.scale);
-
-  for (long long want = (long long)blockIdx.x * T::kTeams + team.team;
-       TPR >= 32 ? want < a.M : want - team.team < a.M; want += step) {
-    const bool have = want < a.M;
-    const long long row = have ? want : a.M - 1;
-    Raw<TX, V> x[N], gate[N], dy[N];
-    Raw<TR, V> dz[N], res[N];
-    {
-      const TX *xr = static_cast<const TX *>(a.x) + row * a.xs;
-#pragma unroll
-      for (int i = 0; i < N; ++i) load<kWhole>(xr, e0 + i * TPR * V, a.D, x[i]);
+  int which = 0;
+  for (; row - team.team < a.M; row += rows, which ^= 1) {
+    if constexpr (kStaged) {
+      fetch(which ^ 1, row + rows < a.M);
+      cp_async_wait<1>();
     }
-    if (a.gate) {
-      const TX *gr = static_cast<const TX *>(a.gate) + row * a.gs;
+    const int left = row < a.M ? a.D - e0 : 0;
+    PerGroup<kWhole, V> inv[N];
+    team.factors(inv, a, [&](int i) { return x.get(which, i, left, apart); });
+    f2 sig[N][V / 2], g[N][V / 2];  // g: the gradient that reaches z
 #pragma unroll
-      for (int i = 0; i < N; ++i) load<kWhole>(gr, e0 + i * TPR * V, a.D, gate[i]);
-    }
-    if (a.dz) {
-      const TR *dr = static_cast<const TR *>(a.dz) + row * a.dzs;
+    for (int i = 0; i < N; ++i) {
+      if (a.gate) {
+        const Raw<TX, V> gv = gate.get(which, i, left, apart);
 #pragma unroll
-      for (int i = 0; i < N; ++i) load<kWhole>(dr, e0 + i * TPR * V, a.D, dz[i]);
-    }
-    if (a.next) {
-      const TX *dr = static_cast<const TX *>(a.dy) + row * a.dys;
+        for (int c = 0; c < V / 2; ++c) sig[i][c] = sigmoid2<kExact>(gv.get(c));
+      }
+      if (a.dz) {
+        const Raw<TR, V> dv = dz.get(which, i, left, apart);
 #pragma unroll
-      for (int i = 0; i < N; ++i) load<kWhole>(dr, e0 + i * TPR * V, a.D, dy[i]);
-      if (a.residual) {
-        const TR *rr = static_cast<const TR *>(a.residual) + row * a.rs;
+        for (int c = 0; c < V / 2; ++c) g[i][c] = dv.get(c);
+      } else {
 #pragma unroll
-        for (int i = 0; i < N; ++i) load<kWhole>(rr, e0 + i * TPR * V, a.D, res[i]);
+        for (int c = 0; c < V / 2; ++c) g[i][c] = 0;
       }
     }
-    // h (x normalised) is worked out again where it is used: x in 16 bits and a group's
-    // factor take fewer registers
-    PerGroup<kWhole, V> inv[N];
-    team.factors(x, inv, a);
-    f2 sig[N][V / 2];
-    if (a.gate) {
-#pragma unroll
-      for (int i = 0; i < N; ++i)
-#pragma unroll
-        for (int c = 0; c < V / 2; ++c) sig[i][c] = sigmoid2<kExact>(gate[i].get(c));
-    }
-    f2 g[N][V / 2];  // the gradient that reaches z
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-#pragma unroll
-      for (int c = 0; c < V / 2; ++c) g[i][c] = a.dz ? dz[i].get(c) : 0;
     if (a.next) {
       f2 z[N][V / 2], s0 = 0, s1 = 0;
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        Raw<float, V> gain, next;
-        if (a.gain) load<kWhole>(a.gain, e0 + i * TPR * V, a.D, gain);
-        if (a.next_gain) load<kWhole>(a.next_gain, e0 + i * TPR * V, a.D, next);
+        const Raw<TX, V> xv = x.get(which, i, left, apart);
 #pragma unroll
-        for (int c = 0; c < V / 2; ++c) {
-          f2 u = mul2(x[i].get(c), inv[i].get(c));
-          if (a.gain) u = mul2(u, gain.x[c]);
-          if (a.gate) u = mul2(u, mul2(gate[i].get(c), sig[i][c]));
-          u = a.residual ? madd2(scale, u, res[i].get(c)) : mul2(scale, u);
-          z[i][c] = u;
-          s0 = madd2(u, u, s0);
-          f2 w = dy[i].get(c);
-          if (a.next_gain) w = mul2(w, next.x[c]);
-          s1 = madd2(u, w, s1);
+        for (int c = 0; c < V / 2; ++c) z[i][c] = mul2(xv.get(c), inv[i].get(c));
+        if (a.gain) {
+          const Raw<float, V> gv = gain.get(0, i, a.D - e0, apart);
+#pragma unroll
+          for (int c = 0; c < V / 2; ++c) z[i][c] = mul2(z[i][c], gv.get(c));
         }
+        if (a.gate) {
+          const Raw<TX, V> gv = gate.get(which, i, left, apart);
+#pragma unroll
+          for (int c = 0; c < V / 2; ++c) z[i][c] = mul2(z[i][c], mul2(gv.get(c), sig[i][c]));
+        }
+        if (a.residual) {
+          const Raw<TR, V> rv = res.get(which, i, left, apart);
+#pragma unroll
+          for (int c = 0; c < V / 2; ++c) z[i][c] = madd2(scale, z[i][c], rv.get(c));
+        } else {
+#pragma unroll
+          for (int c = 0; c < V / 2; ++c) z[i][c] = mul2(scale, z[i][c]);
+        }
+        const Raw<TX, V> dv = dy.get(which, i, left, apart);
+        if (a.next_gain) {
+          const Raw<float, V> nv = next.get(0, i, a.D - e0, apart);
+#pragma unroll
+          for (int c = 0; c < V / 2; ++c) s1 = madd2(z[i][c], mul2(dv.get(c), nv.get(c)), s1);
+        } else {
+#pragma unroll
+          for (int c = 0; c < V / 2; ++c) s1 = madd2(z[i][c], dv.get(c), s1);
+        }
+#pragma unroll
+        for (int c = 0; c < V / 2; ++c) s0 = madd2(z[i][c], z[i][c], s0);
       }
       float s[2] = {lo2(s0) + hi2(s0), lo2(s1) + hi2(s1)};
       team.add(s);
       const float r = rsqrtf(fmaf(s[0], a.inv_D, a.eps));
-      const f2 rr = both(r), mc = both(-r * r * s[1] * a.inv_D);
+      const f2 rf = both(r), mc = both(-r * r * s[1] * a.inv_D);
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        Raw<float, V> next;
-        if (a.next_gain) load<kWhole>(a.next_gain, e0 + i * TPR * V, a.D, next);
+        const Raw<TX, V> dv = dy.get(which, i, left, apart);
+        f2 w[V / 2];
 #pragma unroll
         for (int c = 0; c < V / 2; ++c) {
-          f2 w = dy[i].get(c);
-          if (have) dnext[i][c] = madd2(mul2(w, rr), z[i][c], dnext[i][c]);
-          if (a.next_gain) w = mul2(w, next.x[c]);
-          g[i][c] = madd2(rr, madd2(mc, z[i][c], w), g[i][c]);
+          w[c] = dv.get(c);
+          dnext[i][c] = madd2(mul2(w[c], rf), z[i][c], dnext[i][c]);
         }
+        if (a.next_gain) {
+          const Raw<float, V> nv = next.get(0, i, a.D - e0, apart);
+#pragma unroll
+          for (int c = 0; c < V / 2; ++c) w[c] = mul2(w[c], nv.get(c));
+        }
+#pragma unroll
+        for (int c = 0; c < V / 2; ++c) g[i][c] = madd2(rf, madd2(mc, z[i][c], w[c]), g[i][c]);
       }
     }
-    if (a.dres && have) {
-      TR *dr = static_cast<TR *>(a.dres) + row * a.drs;
+    if (a.dres) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) store<kWhole, TR, V>(dr, e0 + i * TPR * V, a.D, g[i]);
+      for (int i = 0; i < N; ++i) store<kWhole, TR, V>(drr + i * apart, left - i * apart, g[i], a.wide);
+      drr += rows * a.drs;
     }
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      Raw<float, V> gain;
-      if (a.gain) load<kWhole>(a.gain, e0 + i * TPR * V, a.D, gain);
-      f2 out[V / 2];
+      const Raw<TX, V> xv = x.get(which, i, left, apart);
+      Raw<float, V> gn;
+      if (a.gain) gn = gain.get(0, i, a.D - e0, apart);
 #pragma unroll
-      for (int c = 0; c < V / 2; ++c) {
-        const f2 h = mul2(x[i].get(c), inv[i].get(c));
-        f2 u = mul2(scale, g[i][c]);
-        if (a.gate) {
-          const f2 gt = gate[i].get(c), sg = sig[i][c];
-          f2 d = mul2(u, h);
-          if (a.gain) d = mul2(d, gain.x[c]);
-          const f2 silu = mul2(gt, sg);
-          // silu' = sig (1 + gate (1 - sig)) = sig + silu - silu sig
-          out[c] = mul2(d, sub2_bits(add2_bits(sg, silu), mul2(silu, sg)));
-          u = mul2(u, silu);
-        }
-        if (have) dgain[i][c] = madd2(u, h, dgain[i][c]);
-        if (a.gain) u = mul2(u, gain.x[c]);
-        g[i][c] = u;
-      }
-      if (a.dgate && have)
-        store<kWhole, TX, V>(static_cast<TX *>(a.dgate) + row * a.dgs, e0 + i * TPR * V, a.D, out);
-    }
-    if (a.mode != kNone) {
-      PerGroup<kWhole, V> p[N];
-      team.add_groups(p, a, [&](int i, int c) { return mul2(g[i][c], mul2(x[i].get(c), inv[i].get(c))); });
-      const f2 mn = both(-a.inv_n);
-#pragma unroll
-      for (int i = 0; i < N; ++i)
+      for (int c = 0; c < V / 2; ++c) g[i][c] = mul2(scale, g[i][c]);
+      if (a.gate) {
+        const Raw<TX, V> gv = gate.get(which, i, left, apart);
+        f2 out[V / 2];
 #pragma unroll
         for (int c = 0; c < V / 2; ++c) {
-          const f2 h = mul2(x[i].get(c), inv[i].get(c));
+          f2 d = mul2(g[i][c], mul2(xv.get(c), inv[i].get(c)));
+          if (a.gain) d = mul2(d, gn.get(c));
+          const f2 sg = sig[i][c], silu = mul2(gv.get(c), sg);
+          // silu' = sig (1 + gate (1 - sig)) = sig + silu - silu sig
+          out[c] = mul2(d, sub2_bits(add2_bits(sg, silu), mul2(silu, sg)));
+          g[i][c] = mul2(g[i][c], silu);
+        }
+        if (a.dgate) store<kWhole, TX, V>(dgr + i * apart, left - i * apart, out, a.wide);
+      }
+#pragma unroll
+      for (int c = 0; c < V / 2; ++c) {
+        dgain[i][c] = madd2(g[i][c], mul2(xv.get(c), inv[i].get(c)), dgain[i][c]);
+        if (a.gain) g[i][c] = mul2(g[i][c], gn.get(c));
+      }
+    }
+    dgr += rows * a.dgs;
+    if (a.mode != kNone) {
+      PerGroup<kWhole, V> p[N];
+      team.add_groups(p, a, [&](int i, int c) { return mul2(g[i][c], mul2(x.get(which, i, left, apart).get(c), inv[i].get(c))); });
+      const f2 mn = both(-a.inv_n);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const Raw<TX, V> xv = x.get(which, i, left, apart);
+#pragma unroll
+        for (int c = 0; c < V / 2; ++c) {
+          const f2 h = mul2(xv.get(c), inv[i].get(c));
           g[i][c] = mul2(inv[i].get(c), madd2(mul2(mn, p[i].get(c)), h, g[i][c]));
         }
+      }
     }
-    if (have) {
-      TX *dr = static_cast<TX *>(a.dx) + row * a.dxs;
 #pragma unroll
-      for (int i = 0; i < N; ++i) store<kWhole, TX, V>(dr, e0 + i * TPR * V, a.D, g[i]);
-    }
+    for (int i = 0; i < N; ++i) store<kWhole, TX, V>(dxr + i * apart, left - i * apart, g[i], a.wide);
+    dxr += rows * a.dxs;
+    x.next(), gate.next(), dz.next(), dy.next(), res.next();
   }
+  cp_async_wait<0>();
 
   // the block's gains: its teams' added in their order
-  float *total = lists;  // (no team is in a row any more once all are here)
+  float *total = reinterpret_cast<float *>(slots);  // (no team is in a row any more once all are here)
 #pragma unroll 1
-  for (int which = 0; which < 2; ++which) {
-    if (!(which ? a.dnext : a.dgain)) continue;
-    float *to = a.ws + ((size_t)(which && a.dgain ? gridDim.x : 0) + blockIdx.x) * a.D;
-    for (int k = 0; k < T::kTeams; ++k) {
-      if (T::kTeams > 1) __syncthreads();
+  for (int k2 = 0; k2 < 2; ++k2) {
+    if (!(k2 ? a.dnext : a.dgain)) continue;
+    float *to = a.ws + ((size_t)(k2 && a.dgain ? gridDim.x : 0) + blockIdx.x) * a.D;
+    for (int k = 0; k < teams; ++k) {
+      if (teams > 1) __syncthreads();
       if (team.team != k) continue;
 #pragma unroll
       for (int i = 0; i < N; ++i) {
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-          const int e = e0 + i * TPR * V + j;
+          const int e = e0 + i * apart + j;
           if (e >= a.D) continue;
-          const f2 pair = which ? dnext[i][j / 2] : dgain[i][j / 2];
-          const float x = (k ? total[e] : 0.f) + (j % 2 ? hi2(pair) : lo2(pair));
-          if (k + 1 < T::kTeams)
-            total[e] = x;
+          const f2 pair = k2 ? dnext[i][j / 2] : dgain[i][j / 2];
+          const float v = (k ? total[e] : 0.f) + (j % 2 ? hi2(pair) : lo2(pair));
+          if (k + 1 < teams)
+            total[e] = v;
           else
-            to[e] = x;
+            to[e] = v;
         }
       }
     }
   }
 }
 
-// Column sums of the blocks' parts in fp64, in order: 32 columns a block, 32 runs of parts.
+// Column sums of the blocks' parts, in order: 32 columns a block, 32 runs of parts, each with
+// what its additions lose carried beside it (in fp64, whose unit here adds two numbers a cycle,
+// the sums took 16 us).
 __global__ void __launch_bounds__(1024) k15_gain_kernel(const float *part, int blocks, int D,
                                                         float *first, float *second) {
-  __shared__ double run[32][33];
+  __shared__ float run[2][32][33];
   const int lane = threadIdx.x % 32, k = threadIdx.x / 32, c = blockIdx.x * 32 + lane;
   const float *p = part + (size_t)blockIdx.y * blocks * D + c;
-  double x = 0.0;
+  float x = 0.f, lost = 0.f;
+  auto add = [&](float y) {
+    const float s = x + y, z = s - x;
+    lost += (x - (s - z)) + (y - z);
+    x = s;
+  };
   if (c < D) {
-#pragma unroll 4
-    for (int i = k; i < blocks; i += 32) x += __ldg(p + (size_t)i * D);
+    constexpr int kAhead = 10;
+    for (int i = k; i < blocks; i += 32 * kAhead) {
+      float y[kAhead];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) y[j] = i + 32 * j < blocks ? __ldg(p + (size_t)(i + 32 * j) * D) : 0.f;
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) add(y[j]);
+    }
   }
-  run[k][lane] = x;
+  run[0][k][lane] = x;
+  run[1][k][lane] = lost;
   __syncthreads();
   // a warp to each column
-  x = run[lane][k];
+  x = run[0][lane][k];
+  lost = run[1][lane][k];
 #pragma unroll
-  for (int m = 16; m > 0; m /= 2) x += __shfl_xor_sync(0xffffffffu, x, m);
+  for (int m = 16; m > 0; m /= 2) {
+    const float y = __shfl_xor_sync(0xffffffffu, x, m), l = __shfl_xor_sync(0xffffffffu, lost, m);
+    const float big = fmaxf(fabsf(x), fabsf(y)) == fabsf(x) ? x : y, small = big == x ? y : x;
+    const float s = x + y;
+    lost += l + (small - (s - big));
+    x = s;
+  }
   const int to = blockIdx.x * 32 + k;
-  if (lane == 0 && to < D) (blockIdx.y ? second : first)[to] = (float)x;
+  if (lane == 0 && to < D) (blockIdx.y ? second : first)[to] = x + lost;
 }
 
-constexpr int kMaxBlocks = 152 * 2;
+constexpr int kMaxBlocks = 152 * 4;
 
 // Sixteen-byte vectors want every row of every tensor on sixteen bytes, and groups of whole vectors.
 bool whole(const NormArgs &a) {
@@ -584,36 +718,68 @@ bool whole(const NormArgs &a) {
   return true;
 }
 
-template <bool kBack, typename TX, typename TR, int TPR, int N, bool kWhole>
-cudaError_t go(NormArgs a, cudaStream_t st) {
+// Bytes of shared memory that both rows of all of a block's inputs and the gains take in the
+// backward pass.
+template <typename TX, typename TR, int N>
+size_t staged_bytes(const NormArgs &a, int threads) {
   constexpr int V = 16 / sizeof(TX);
-  using T = Team<TPR, V, N, kWhole>;
-  const int n = a.groups ? a.D / a.groups : 1;
+  const size_t x = 2 * N * V * sizeof(TX) * threads, r = 2 * N * V * sizeof(TR) * threads;
+  const size_t gain = N * V * sizeof(float) * threads;
+  return x + (a.gate ? x : 0) + (a.dz ? r : 0) + (a.dy ? x : 0) + (a.next && a.residual ? r : 0) +
+         (a.gain ? gain : 0) + (a.next_gain ? gain : 0);
+}
+
+// fp32 rows beside bf16 ones: all of them on 32 bytes.
+bool wide(const NormArgs &a) {
+  const struct { const void *p; long long s; bool f32; } all[] = {
+      {a.residual, a.rs, a.r_f32}, {a.z, a.zs, a.r_f32}, {a.dz, a.dzs, a.r_f32}, {a.dres, a.drs, a.r_f32},
+      {a.gain, 0, true}, {a.next_gain, 0, true}};
+  for (const auto &t : all)
+    if (t.p && t.f32 && (reinterpret_cast<uintptr_t>(t.p) % 32 || t.s % 8)) return false;
+  return !a.x_f32;
+}
+
+template <bool kBack, typename TX, typename TR, int kTeam, int N, bool kWhole, bool kStaged>
+cudaError_t go(NormArgs a, int threads, cudaStream_t st) {
+  constexpr int V = 16 / sizeof(TX);
+  const int n = a.groups ? a.D / a.groups : 1, teams = kTeam ? 256 / kTeam : 1;
   a.per = kWhole ? n / V : n;
   a.inv_n = 1.f / (float)n;
   a.inv_D = 1.f / (float)a.D;
+  a.wide = kWhole && wide(a);
   a.mode = !a.groups ? kNone
            : a.groups == 1 ? kRow
-           : kWhole && a.per <= T::kLanes && (a.per & (a.per - 1)) == 0 ? kShuffle : kList;
-  a.list = a.mode == kList || (!kWhole && a.groups > 1) ? (kWhole ? a.D / V : a.D) + a.groups : 0;
-  const long long blocks = ((long long)a.M + T::kTeams - 1) / T::kTeams;
-  size_t smem = (size_t)T::kTeams * a.list * 4;
-  if (kBack && T::kTeams > 1 && smem < (size_t)a.D * 4) smem = (size_t)a.D * 4;
+           : kWhole && a.per <= (kTeam ? kTeam : 32) && (a.per & (a.per - 1)) == 0 ? kShuffle : kList;
+  a.list = a.mode == kList ? (kWhole ? a.D / V : a.D) + a.groups : 0;
+  size_t smem = (kBack && kStaged ? staged_bytes<TX, TR, N>(a, threads) : 0) + (size_t)teams * a.list * 4;
+  if (kBack && teams > 1 && smem < (size_t)a.D * 4) smem = (size_t)a.D * 4;
   void (*f)(NormArgs);
   if constexpr (kBack)
-    f = k15_norm_bwd_kernel<TX, TR, TPR, N, kWhole>;
+    f = k15_norm_bwd_kernel<TX, TR, kTeam, N, kWhole, kStaged>;
   else
-    f = k15_norm_kernel<TX, TR, TPR, N, kWhole>;
+    f = k15_norm_kernel<TX, TR, kTeam, N, kWhole>;
   cudaError_t e;
-  if (smem > 48 * 1024 &&
+  if (smem + 1024 > 48 * 1024 &&
       (e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess)
     return e;
+  const long long blocks = ((long long)a.M + teams - 1) / teams;
   if (!kBack) {
-    f<<<(unsigned)blocks, T::kThreads, smem, st>>>(a);
+    f<<<(unsigned)blocks, threads, smem, st>>>(a);
     return cudaGetLastError();
   }
-  const int grid = (int)(blocks < kMaxBlocks ? blocks : kMaxBlocks);
-  f<<<grid, T::kThreads, smem, st>>>(a);
+  // as many blocks as are resident at once: what shared memory and registers leave
+  static const int regs = [&] {
+    cudaFuncAttributes attr;
+    return cudaFuncGetAttributes(&attr, f) == cudaSuccess ? attr.numRegs : 128;
+  }();
+  int resident = 65536 / ((regs + 7) / 8 * 8 * threads);
+  const int by_smem = (int)(227 * 1024 / (smem + 1024)), by_threads = 2048 / threads;
+  resident = resident < by_smem ? resident : by_smem;
+  resident = resident < by_threads ? resident : by_threads;
+  int most = 152 * (resident < 1 ? 1 : resident);
+  if (most > kMaxBlocks) most = kMaxBlocks;
+  const int grid = (int)(blocks < most ? blocks : most);
+  f<<<grid, threads, smem, st>>>(a);
   e = cudaGetLastError();
   const int sums = (a.dgain ? 1 : 0) + (a.dnext ? 1 : 0);
   if (e != cudaSuccess || !sums) return e;
@@ -622,33 +788,33 @@ cudaError_t go(NormArgs a, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-// The smallest team whose threads hold the row, 16 elements each, 8 in the backward pass,
-// which has twice the values to hold (more for the widest rows).  Rows element by
-// element are no path to be quick on: fewer teams.
+// A thread's elements: 16 (forward) or 8 (backward, which has twice the values to hold), more
+// where the row is wider than 512 threads of them.  Rows of up to 512 elements go to
+// warps or parts of warps.  Rows are staged where both of all inputs leave room in an SM's
+// shared memory.  Rows element by element are no path to be quick on.
 template <bool kBack, typename TX, typename TR>
 cudaError_t pick(const NormArgs &a, cudaStream_t st) {
   constexpr int V = 16 / sizeof(TX), k8 = 8 / V, k16 = 16 / V, k32 = 32 / V;
   const int D = a.D;
+  auto threads = [&](int N) { return ((D + V - 1) / V + N * 32 - 1) / (N * 32) * 32; };
   if (!whole(a)) {
-    if (D <= 128) return go<kBack, TX, TR, 8, k16, false>(a, st);
-    if (D <= 2048) return go<kBack, TX, TR, 128, k16, false>(a, st);
-    return go<kBack, TX, TR, 512, k32, false>(a, st);
+    if (D <= 128) return go<kBack, TX, TR, 8, k16, false, false>(a, 256, st);
+    return go<kBack, TX, TR, 0, k32, false, false>(a, threads(k32), st);
   }
-  if (D <= 64) return go<kBack, TX, TR, 8, k8, true>(a, st);
-  if (D <= 256) return go<kBack, TX, TR, 32, k8, true>(a, st);
+  if (D <= 64) return go<kBack, TX, TR, 8, k8, true, true>(a, 256, st);
+  if (D <= 256) return go<kBack, TX, TR, 32, k8, true, true>(a, 256, st);
+  if (D <= 512) return go<kBack, TX, TR, 32, k16, true, true>(a, 256, st);
   if constexpr (kBack) {
-    if (D <= 512) return go<kBack, TX, TR, 64, k8, true>(a, st);
-    if (D <= 1024) return go<kBack, TX, TR, 128, k8, true>(a, st);
-    if (D <= 2048) return go<kBack, TX, TR, 256, k8, true>(a, st);
-    if (D <= 4096) return go<kBack, TX, TR, 512, k8, true>(a, st);
-  } else {
-    if (D <= 512) return go<kBack, TX, TR, 32, k16, true>(a, st);
-    if (D <= 1024) return go<kBack, TX, TR, 64, k16, true>(a, st);
-    if (D <= 2048) return go<kBack, TX, TR, 128, k16, true>(a, st);
-    if (D <= 4096) return go<kBack, TX, TR, 256, k16, true>(a, st);
+    if (D <= 4096) return go<kBack, TX, TR, 0, k8, true, true>(a, threads(k8), st);
   }
-  if (D <= 8192) return go<kBack, TX, TR, 512, k16, true>(a, st);
-  return go<kBack, TX, TR, 512, k32, true>(a, st);
+  if constexpr (kBack) {
+    const int n = threads(k16);
+    if (n <= 512 && staged_bytes<TX, TR, k16>(a, n) + (D / V + a.groups) * 4 <= 226 * 1024)
+      return go<kBack, TX, TR, 0, k16, true, true>(a, n, st);
+  } else {
+    if (D <= 8192) return go<kBack, TX, TR, 0, k16, true, true>(a, threads(k16), st);
+  }
+  return go<kBack, TX, TR, 0, k32, true, false>(a, threads(k32), st);
 }
 
 template <bool kBack>
