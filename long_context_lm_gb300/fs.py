@@ -1003,11 +1003,11 @@ def fs_linear_workspace(batch, H, Hkv, T, d, device, backward=False):
 
 
 def _linear_inputs(q, k, v, decay, count):
-    dev = _cuda(q, "q")
-    if q.dim() != 4:
+    dev, shape = _cuda(q, "q"), q.shape
+    if len(shape) != 4:
         raise ValueError("q must be [batch, H, T, d]")
-    B, H, T, d = q.shape
-    qp, qs = _rows(q, dev, "q", torch.bfloat16, q.shape)
+    B, H, T, d = shape
+    qp, qs = _rows(q, dev, "q", torch.bfloat16, shape)
     Hkv = k.shape[1] if isinstance(k, torch.Tensor) and k.dim() == 4 else 0
     shape = (B, Hkv, T, d)
     kp, ks = _rows(k, dev, "k", torch.bfloat16, shape)
@@ -1077,14 +1077,15 @@ def fs_linear_attn_bwd(q, k, v, decay, dout, state=None, dstate_out=None, count=
 
 def _matrix(t, dev, name, dtype, shape):
     """Pointer and row stride of a [..., D] tensor of ``shape`` whose rows lie evenly apart."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == dev \
+            and t.is_contiguous():
+        return t.data_ptr(), shape[-1]
     if not isinstance(t, torch.Tensor) or t.device != dev:
         raise ValueError(f"{name} must be a tensor on {dev}")
     if t.dtype != dtype:
         raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, not {list(t.shape)}")
-    if t.is_contiguous():
-        return t.data_ptr(), shape[-1]
     if t.stride(-1) != 1 and shape[-1] > 1:
         raise ValueError(f"{name}: the elements of a row must be contiguous")
     axes = [(n, s) for n, s in zip(t.shape[:-1], t.stride()[:-1]) if n > 1]
@@ -1094,12 +1095,20 @@ def _matrix(t, dev, name, dtype, shape):
     return t.data_ptr(), axes[-1][1] if axes else shape[-1]
 
 
-_NORM_DTYPES = (torch.bfloat16, torch.float32)
+_NORM_CODES = {torch.bfloat16: FS_BF16, torch.float32: FS_FP32}
+
+
+def _like(t, dtype, stream):
+    """A new contiguous tensor of t's shape."""
+    if stream is None and t.dtype is dtype and t.is_contiguous():
+        return torch.empty_like(t)
+    return _new(stream, lambda: torch.empty(t.shape, dtype=dtype, device=t.device))
 
 
 def _norm_inputs(x, gate, residual, gain, next_gain, groups, res_dtype):
     dev, dt = _cuda(x, "x"), x.dtype
-    if dt not in _NORM_DTYPES or res_dtype not in _NORM_DTYPES:
+    code, res_code = _NORM_CODES.get(dt), _NORM_CODES.get(res_dtype)
+    if code is None or res_code is None:
         raise ValueError(f"x has dtype {dt}, the residual {res_dtype}: expected bfloat16 or float32")
     shape = x.shape
     if not shape or shape[-1] < 1:
@@ -1113,8 +1122,7 @@ def _norm_inputs(x, gate, residual, gain, next_gain, groups, res_dtype):
     rp, rs = (None, 0) if residual is None else _matrix(residual, dev, "residual", res_dtype, shape)
     a = None if gain is None else _on(gain, dev, "gain", torch.float32, (D,))
     b = None if next_gain is None else _on(next_gain, dev, "next_gain", torch.float32, (D,))
-    return dev, (xp, xs, FS_BF16 if dt == torch.bfloat16 else FS_FP32, gp, gs, rp, rs,
-                 FS_BF16 if res_dtype == torch.bfloat16 else FS_FP32, a, b, M, D, int(groups))
+    return dev, (xp, xs, code, gp, gs, rp, rs, res_code, a, b, M, D, groups)
 
 
 def fs_block_norm(x, gate=None, residual=None, groups=0, gain=None, next_norm=False, next_gain=None,
@@ -1129,17 +1137,19 @@ def fs_block_norm(x, gate=None, residual=None, groups=0, gain=None, next_norm=Fa
     res_dtype = residual.dtype if residual is not None else z.dtype if z is not None else x.dtype
     dev, args = _norm_inputs(x, gate, residual, gain, next_gain, groups, res_dtype)
     if z is None:
-        z = _new(stream, lambda: torch.empty(x.shape, dtype=res_dtype, device=dev))
-    zp, zs = _matrix(z, dev, "z", res_dtype, x.shape)
+        z = _like(x if residual is None else residual, res_dtype, stream)
+        zp, zs = z.data_ptr(), args[11]
+    else:
+        zp, zs = _matrix(z, dev, "z", res_dtype, x.shape)
     yp, ys = None, 0
-    if next_norm and y is None:
-        y = _new(stream, lambda: torch.empty(x.shape, dtype=x.dtype, device=dev))
     if y is not None:
         yp, ys = _matrix(y, dev, "y", x.dtype, x.shape)
+    elif next_norm:
+        y = _like(x, x.dtype, stream)
+        yp, ys = y.data_ptr(), args[11]
     elif next_gain is not None:
         raise ValueError("next_gain without next_norm")
-    _launch(dev, stream, L.fs_block_norm, "fs_block_norm", *args, float(scale), float(eps), zp, zs, yp,
-            ys)
+    _launch(dev, stream, L.fs_block_norm, "fs_block_norm", *args, scale, eps, zp, zs, yp, ys)
     return z, y
 
 
@@ -1179,8 +1189,10 @@ def fs_block_norm_bwd(x, dz=None, dy=None, gate=None, residual=None, groups=0, g
             grads.append((None, None, 0))
             continue
         if t is None:
-            t = _new(stream, lambda: torch.empty(shape, dtype=dt, device=dev))
-        grads.append((t, *_matrix(t, dev, name, dt, shape)))
+            t = _like(of, dt, stream)
+            grads.append((t, t.data_ptr(), D))
+        else:
+            grads.append((t, *_matrix(t, dev, name, dt, shape)))
     sums = [None if t is None else
             _new(stream, lambda: torch.empty(D, dtype=torch.float32, device=dev))
             for t in (gain, next_gain)]
@@ -1189,8 +1201,8 @@ def fs_block_norm_bwd(x, dz=None, dy=None, gate=None, residual=None, groups=0, g
         if ws is None:
             ws = _new(stream, lambda: fs_block_norm_workspace(M, D, dev))
         wp, wn = _scratch(ws, dev)
-    _launch(dev, stream, L.fs_block_norm_bwd, "fs_block_norm_bwd", *args, float(scale), float(eps),
-            dzp, dzs, dyp, dys, *(x for _, p, s in grads for x in (p, s)),
+    _launch(dev, stream, L.fs_block_norm_bwd, "fs_block_norm_bwd", *args, scale, eps, dzp,
+            dzs, dyp, dys, *(x for _, p, s in grads for x in (p, s)),
             *(None if t is None else t.data_ptr() for t in sums), wp, wn)
     return {"x": grads[0][0], "gate": grads[1][0], "residual": grads[2][0], "gain": sums[0],
             "next_gain": sums[1]}
