@@ -16,12 +16,13 @@
 //
 // A block takes one (sequence, head), or one of `splits` stretches of it, chunk
 // after chunk; S never leaves it.  Warps:
-//   0-3       rows: scores to bf16 parts in their own TMEM columns, Q S times the row's
-//             power in place, the finished rows by way of the values' place in shared
-//             memory (a TMA store a warp: 32 rows written by their own threads would be
-//             32 places an instruction)
-//   4..       states (D / 16 warps): weighted values into a ring of two slabs; S in
-//             registers, its bf16 parts into shared memory for the next chunk
+//   0-7       rows, two warps to 32 of them, each with half of the columns: scores to bf16
+//             parts in their own TMEM columns, Q S times the row's power in place, the
+//             finished rows by way of the values' place in shared memory (a TMA store: rows
+//             written by their own threads would be 32 places an instruction)
+//   8..       states (D / 16 warps): weighted values into a slab, the next one's made in
+//             registers while it is multiplied; S in registers, its bf16 parts into
+//             shared memory for the next chunk
 //   last four one for TMA loads, one that issues the products of the rows, one that issues
 //             those of the slabs (issued by one thread, slabs waited behind the rows'
 //             products, a slab at a time, and took 7000 cycles a chunk in place of 3000)
@@ -65,10 +66,14 @@ template <int D>
 struct Cfg {
   static constexpr int kAtoms = D / 64;
   static constexpr int kStateWarps = D / 16;
-  static constexpr int kTma = 4 + kStateWarps, kMma = kTma + 1, kMmaU = kTma + 2;
+  static constexpr int kTma = 8 + kStateWarps, kMma = kTma + 1, kMmaU = kTma + 2;
   static constexpr int kThreads = 32 * (kTma + 4);
-  static constexpr int kSlab = D == 64 ? 32 : 16, kSlabs = kC / kSlab;  // tokens of a slab, slabs
-  static constexpr int kUnits = kSlab / 16;  // 16-byte pieces of a slab for a state thread
+  static constexpr int kSlab = 32, kSlabs = kC / kSlab;  // tokens of a slab, slabs
+  static constexpr int kUnits = 2;  // 16-byte pieces of a slab for a state thread
+  // registers a thread: at launch, then of the rows', states' and last four warps
+  static constexpr int kRegs = D == 64 ? 64 : 96, kRowRegs = D == 64 ? 64 : 80, kStateRegs = D == 64 ? 88 : 128,
+                       kLastRegs = 40;
+  static_assert(8 * kRowRegs + kStateWarps * kStateRegs + 4 * kLastRegs <= (12 + kStateWarps) * kRegs, "registers");
   static constexpr uint32_t kSlabAtom = kSlab * 128;
   static constexpr int kHalves = D / 64;  // groups of 16 rows that a state warp holds
   static constexpr int kValues = 2;                              // chunks of v held
@@ -76,20 +81,21 @@ struct Cfg {
   static constexpr uint32_t kPart = kAtoms * kSlabAtom;          // one part of a slab
   static constexpr uint32_t kSPart = kAtoms * D * 128;           // one part of S
   static constexpr uint32_t kQ = 0, kK = kTile, kV = kK + kTile, kS = kV + kValues * kTile,
-                            kSlab0 = kS + 2 * kSPart, kBytes = kSlab0 + 2 * 3 * kPart;
+                            kSlab0 = kS + 2 * kSPart, kBytes = kSlab0 + 3 * kPart;
   // TMEM columns: scores (then their parts), outputs, the chunk's addition to S
   static constexpr uint32_t kScores = 0, kOut = kC, kU = kC + D, kCols = D == 64 ? 256 : 512;
 };
 
 struct Shared {
   uint64_t qfull, qempty, kfull, kempty, vfull[2], vempty[2];
-  uint64_t slab_full[2], slab_empty[2];
+  uint64_t slab_full, slab_empty;
   uint64_t s_ready, s_free, scores, inter, parts, done, o_free, u_full, u_free, fin, fin_u;
   // values looked through: the states' warps may be a chunk ahead of the rows', not two
   uint64_t checked[2];
   uint32_t tmem;
   int odd[2];                 // a chunk's values are not all finite
   float power[kC + 4];        // lam^n
+  float scaled[kC + 4];       // scale lam^n
   alignas(16) float cols[3][32];  // see the rows' warps (read four at a time)
   int bad[2][128];            // per column: the first such token in the sweep's order
 };
@@ -121,7 +127,7 @@ __device__ __forceinline__ uint64_t desc_blocks(uint32_t at, uint32_t apart) {
 
 // 16 lanes x 64 columns, a warp's lane t holding of each eight columns 2 (t % 4) and the
 // next, in lanes t / 4 and t / 4 + 8.
-__device__ __forceinline__ void tmem_ld_16x64(uint32_t at, float (&r)[32]) {
+__device__ __forceinline__ void tmem_ld_16x64(uint32_t at, f2 (&r)[16]) {
   uint32_t u[32];
   asm volatile(
       "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
@@ -135,7 +141,7 @@ __device__ __forceinline__ void tmem_ld_16x64(uint32_t at, float (&r)[32]) {
       : "r"(at));
   tc::tmem_wait_ld();
 #pragma unroll
-  for (int i = 0; i < 32; ++i) r[i] = __uint_as_float(u[i]);
+  for (int i = 0; i < 16; ++i) r[i] = (f2)u[2 * i] | (f2)u[2 * i + 1] << 32;
 }
 
 // The 64 x 128 box of a map at token t of head h of sequence b.
@@ -196,12 +202,11 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, D == 64 ? 2 : 1)
       tc::mbar_init(x, 1);
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&s.vfull[i], 1);
-      tc::mbar_init(&s.vempty[i], kRows ? 4 : C::kStateWarps);
-      tc::mbar_init(&s.slab_full[i], C::kStateWarps);
-      tc::mbar_init(&s.slab_empty[i], 1);
+      tc::mbar_init(&s.vempty[i], kRows ? 8 : C::kStateWarps);
     }
-    for (uint64_t *x : {&s.s_ready, &s.u_free, &s.checked[0], &s.checked[1]}) tc::mbar_init(x, C::kStateWarps);
-    for (uint64_t *x : {&s.parts, &s.o_free}) tc::mbar_init(x, 4);
+    tc::mbar_init(&s.slab_empty, 1);
+    for (uint64_t *x : {&s.slab_full, &s.s_ready, &s.u_free, &s.checked[0], &s.checked[1]}) tc::mbar_init(x, C::kStateWarps);
+    for (uint64_t *x : {&s.parts, &s.o_free}) tc::mbar_init(x, 8);
     tc::mbar_init(&s.kempty, kRows ? 2 : 1);  // read by the scores' product and by the slabs'
     tc::mbar_init(&s.fin_u, 1);
     tc::mbar_fence_init();
@@ -210,6 +215,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, D == 64 ? 2 : 1)
   for (int i = threadIdx.x; i <= kC; i += C::kThreads) {
     const Factor f = decay_power(decay, i);
     s.power[i] = f.hi + f.lo;
+    s.scaled[i] = (f.hi + f.lo) * p.a.scale;
   }
   for (int i = threadIdx.x; i < 96; i += C::kThreads) {
     const Factor f = decay_power(decay, 32 * (i / 32 + 1) + (reverse ? i % 32 - 31 : -(i % 32)));
@@ -226,10 +232,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, D == 64 ? 2 : 1)
   const uint32_t tmem = s.tmem, base = smem_u32(smem);
   const uint32_t tu = tmem + (kRows ? C::kU : 0);
   const int chunks = st.to - st.from;
-  // Heads of 64: 80 registers a thread at launch, of which the last four warps need half:
-  // 96 + 104 + 40 = 3 x 80.
   if (warp >= C::kTma) {
-    if constexpr (D == 64) tc::regs_dec<40>();
+    tc::regs_dec<C::kLastRegs>();
   if (warp == C::kTma && lane == 0) {
     // ------------------------------------------------------------------ loads
     const int mq = p.map[blockIdx.z][0], mk = p.map[blockIdx.z][1], mv = p.map[blockIdx.z][2];
@@ -308,7 +312,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, D == 64 ? 2 : 1)
 #pragma unroll
       for (int k = 0; k < 2 * kC / 16; ++k) {
         const int kk = k % (kC / 16), part = k / (kC / 16);
-        tc::mma_ts(tmem + C::kOut, tmem + C::kScores + kk / 2 * 32 + part * 16 + kk % 2 * 8,
+        tc::mma_ts(tmem + C::kOut, tmem + C::kScores + kk * 16 + part * 8,
                    desc_blocks(values + kk * 2048, kAtom), kB, 1);
       }
       tc::mma_commit(&s.done);
@@ -324,17 +328,17 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, D == 64 ? 2 : 1)
       if (!tc::mbar_wait(&s.kfull, i & 1, p.err)) break;
       if (i && !tc::mbar_wait(&s.u_free, (i - 1) & 1, p.err)) break;
       for (int j = 0; j < C::kSlabs; ++j) {
-        const int at = i * C::kSlabs + j, slot = at & 1;
-        if (!(ok = tc::mbar_wait(&s.slab_full[slot], at >> 1 & 1, p.err))) break;
+        const int at = i * C::kSlabs + j;
+        if (!(ok = tc::mbar_wait(&s.slab_full, at & 1, p.err))) break;
         tc::fence_after_sync();
 #pragma unroll
         for (int k = 0; k < 3 * C::kUnits; ++k) {
           const int kk = k % C::kUnits, part = k / C::kUnits;
           tc::mma_ss(tu, desc_blocks(keys + j * C::kSlabAtom + kk * 2048, kAtom),
-                     desc_blocks(base + C::kSlab0 + (slot * 3 + part) * C::kPart + kk * 2048, C::kSlabAtom),
+                     desc_blocks(base + C::kSlab0 + part * C::kPart + kk * 2048, C::kSlabAtom),
                      kUD, j > 0 || k > 0);
         }
-        tc::mma_commit(&s.slab_empty[slot]);
+        tc::mma_commit(&s.slab_empty);
       }
       if (!ok) break;
       tc::mma_commit(&s.u_full);
@@ -343,23 +347,22 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, D == 64 ? 2 : 1)
     tc::mma_commit(&s.fin_u);
     tc::mbar_wait(&s.fin_u, 0, nullptr);
   }
-  } else if (warp >= 4) {
-    if constexpr (D == 64) tc::regs_inc<104>();
+  } else if (warp >= 8) {
+    tc::regs_inc<C::kStateRegs>();
     // ------------------------------------------------------------------ states
     constexpr int kT = 32 * C::kStateWarps;
-    const int sw = warp - 4, t = threadIdx.x - 128;
+    const int sw = warp - 8, t = threadIdx.x - 256;
     // this lane's places in S: rows row0 + 16 g (+ 8), columns col0 + 8 e (+ 1)
     const int row0 = (D == 64 ? sw * 16 : sw % 4 * 32) + lane / 4;
     const int col0 = (D == 64 ? 0 : sw / 4 * 64) + lane % 4 * 2;
     const uint32_t lanes = tu + ((uint32_t)(warp % 4 * 32) << 16) + (D == 64 ? 0 : sw / 4 * 64);
     const size_t bh = (size_t)blockIdx.z * gridDim.y + blockIdx.y;
-    float S[C::kHalves][32];
-    auto each = [&](auto f) {  // f(element, row, column)
+    f2 S[C::kHalves][16];
+    auto each = [&](auto f) {  // f(pair, row, column of its first)
 #pragma unroll
       for (int g = 0; g < C::kHalves; ++g)
 #pragma unroll
-        for (int e = 0; e < 32; ++e)
-          f(S[g][e], row0 + 16 * g + (e & 2) * 4, col0 + e / 4 * 8 + (e & 1));
+        for (int e = 0; e < 16; ++e) f(S[g][e], row0 + 16 * g + (e & 1) * 8, col0 + e / 2 * 8);
     };
     // between the passes states lie as the lanes hold them
     auto slot = [&](int i) { return p.states + (bh * p.splits + i) * (D * D) + t * 4; };
@@ -369,23 +372,25 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, D == 64 ? 2 : 1)
 #pragma unroll
       for (int g = 0; g < C::kHalves; ++g)
 #pragma unroll
-        for (int e = 0; e < 32; e += 4) {
-          const float4 x = *reinterpret_cast<const float4 *>(from + (g * 8 + e / 4) * kT * 4);
-          S[g][e] = x.x, S[g][e + 1] = x.y, S[g][e + 2] = x.z, S[g][e + 3] = x.w;
+        for (int e = 0; e < 16; e += 2) {
+          const ulonglong2 x = *reinterpret_cast<const ulonglong2 *>(from + (g * 8 + e / 2) * kT * 4);
+          S[g][e] = x.x, S[g][e + 1] = x.y;
         }
     } else if (given && r == 0) {
       const int sr = w.transposed ? 1 : D, sc = w.transposed ? D : 1;
-      each([&](float &x, int row, int col) { x = given[row * sr + col * sc] * w.state_mul; });
+      each([&](f2 &x, int row, int col) {
+        const float *at = given + row * sr + col * sc;
+        x = f2_bits(at[0] * w.state_mul, at[sc] * w.state_mul);
+      });
     } else {
-      each([&](float &x, int, int) { x = 0.f; });
+      each([&](f2 &x, int, int) { x = 0; });
     }
     auto save = [&](float *to) {
 #pragma unroll
       for (int g = 0; g < C::kHalves; ++g)
 #pragma unroll
-        for (int e = 0; e < 32; e += 4)
-          *reinterpret_cast<float4 *>(to + (g * 8 + e / 4) * kT * 4) =
-              make_float4(S[g][e], S[g][e + 1], S[g][e + 2], S[g][e + 3]);
+        for (int e = 0; e < 16; e += 2)
+          *reinterpret_cast<ulonglong2 *>(to + (g * 8 + e / 2) * kT * 4) = make_ulonglong2(S[g][e], S[g][e + 1]);
     };
     // S as the factor of the next product: two parts, [row][column] with the columns
     // swizzled.  A lane names the row that it is to fill of one of four 8 x 8 blocks:
@@ -395,15 +400,15 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, D == 64 ? 2 : 1)
 #pragma unroll
       for (int g = 0; g < C::kHalves; ++g)
 #pragma unroll
-        for (int e = 0; e < 32; e += 8) {
+        for (int e = 0; e < 16; e += 4) {
           uint32_t hi[4], lo[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            f2 x = f2_bits(S[g][e + 2 * k], S[g][e + 2 * k + 1]);
+            f2 x = S[g][e + k];
             hi[k] = split2(x);
             lo[k] = pack2(x);
           }
-          const uint32_t at = sat + g * 16 * 128 + (((e / 4 + lane / 16) ^ (lane % 8)) << 4);
+          const uint32_t at = sat + g * 16 * 128 + (((e / 2 + lane / 16) ^ (lane % 8)) << 4);
           stmatrix4(at, hi);
           stmatrix4(at + C::kSPart, lo);
         }
@@ -455,13 +460,13 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, D == 64 ? 2 : 1)
             some |= part[k][2][c];
           }
         }
-        const int at = i * C::kSlabs + j, slot = at & 1;
-        if (at > 1 && !(ok = WAIT(s.slab_empty[slot], (at >> 1) - 1))) break;
+        const int at = i * C::kSlabs + j;
+        if (at && !(ok = WAIT(s.slab_empty, at - 1))) break;
 #pragma unroll
         for (int k = 0; k < C::kUnits; ++k)
 #pragma unroll
           for (int q = 0; q < 3; ++q)
-            *reinterpret_cast<uint4 *>(to + (slot * 3 + q) * C::kPart + k * 2048) =
+            *reinterpret_cast<uint4 *>(to + q * C::kPart + k * 2048) =
                 make_uint4(part[k][q][0], part[k][q][1], part[k][q][2], part[k][q][3]);
         // A value that is not finite leaves NaN in the third part (and NaN in the state's column).
         // It leaves V before the scores' product, where scores of 0 would make NaN of the rows
@@ -481,7 +486,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, D == 64 ? 2 : 1)
         }
         tc::fence_async_smem();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&s.slab_full[slot]);
+        if (lane == 0) tc::mbar_arrive(&s.slab_full);
       }
       if (!ok) break;
       if (lane == 0) tc::mbar_arrive(kRows ? &s.checked[i & 1] : &s.vempty[i % C::kValues]);
@@ -491,7 +496,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, D == 64 ? 2 : 1)
       const f2 hi = f2_bits(f.hi, f.hi), lo = f2_bits(f.lo, f.lo);
 #pragma unroll
       for (int g = 0; g < C::kHalves; ++g) {
-        float u[32];
+        f2 u[16];
         tmem_ld_16x64(lanes + ((uint32_t)(16 * g) << 16), u);
         if (g == C::kHalves - 1) {
           tc::fence_before_sync();
@@ -499,12 +504,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, D == 64 ? 2 : 1)
           if (lane == 0) tc::mbar_arrive(&s.u_free);
         }
 #pragma unroll
-        for (int e = 0; e < 32; e += 2) {
-          const f2 x = f2_bits(S[g][e], S[g][e + 1]);
-          const f2 y = madd2(x, hi, madd2(x, lo, f2_bits(u[e], u[e + 1])));
-          S[g][e] = __uint_as_float((uint32_t)y);
-          S[g][e + 1] = __uint_as_float((uint32_t)(y >> 32));
-        }
+        for (int e = 0; e < 16; ++e) S[g][e] = madd2(S[g][e], hi, madd2(S[g][e], lo, u[e]));
       }
       if (kRows && i + 1 < chunks) {
         if (!WAIT(s.s_free, i)) break;
@@ -517,16 +517,22 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, D == 64 ? 2 : 1)
       float *out = w.state_out + (size_t)blockIdx.y * D * D;
       const int sr = w.transposed ? 1 : D, sc = w.transposed ? D : 1;
       const float mul = 1.f / w.state_mul;
-      each([&](float &x, int row, int col) { out[row * sr + col * sc] = x * mul; });
+      each([&](f2 &x, int row, int col) {
+        float *at = out + row * sr + col * sc;
+        at[0] = lo2(x) * mul;
+        at[sc] = hi2(x) * mul;
+      });
     }
-  } else if (kRows) {
-    if constexpr (D == 64) tc::regs_inc<96>();
+  } else {
+    // (without rows too: the states' share counts on it)
+    if constexpr (C::kRowRegs < C::kRegs) tc::regs_dec<C::kRowRegs>();
+    if constexpr (kRows) {
     // -------------------------------------------------------------------- rows
     // lam^|i - j| for 32 columns that all rows of the warp see is a factor of the row and
     // one of the column, counted from the warp's near edge, so that neither passes 1
-    const int row = warp * 32 + lane;
-    const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
-    const float rowf = s.power[reverse ? 31 - lane : lane];
+    const int quarter = warp % 4, half = warp / 4, row = quarter * 32 + lane;
+    const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
+    const float rowf = s.scaled[reverse ? 31 - lane : lane];
     const f2 rowff = f2_bits(rowf, rowf);
     const CUtensorMap *map = &maps.out[blockIdx.z];
     const int mh = h * p.out_axes[blockIdx.z][1], mb = b * p.out_axes[blockIdx.z][0];
@@ -535,47 +541,48 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, D == 64 ? 2 : 1)
       const int chunk = st.chunk(st.from + i, reverse), n = st.size(chunk);
       if (!WAIT(s.scores, i)) break;
       tc::fence_after_sync();
+      const uint32_t at = lanes + C::kScores + 16 * half;
 #pragma unroll 1
       for (int c = 0; c < 4; ++c) {
-        uint32_t hi[16], lo[16];
-        const int off = reverse ? c - warp : warp - c;
+        uint32_t parts[2][8];
+        const int off = reverse ? c - quarter : quarter - c;
         if (off < 0) {
 #pragma unroll
-          for (int e = 0; e < 16; ++e) hi[e] = lo[e] = 0;
+          for (int e = 0; e < 8; ++e) parts[0][e] = parts[1][e] = 0;
         } else {
-          uint32_t x[32];
-          tc::tmem_ld32(lanes + C::kScores + 32 * c, x);
+          uint32_t x[16];
+          tc::tmem_ld16(at + 32 * c, x);
           tc::tmem_wait_ld();
           if (off > 0 && (!reverse || 32 * c + 32 <= n)) {
-            const ulonglong2 *cw = reinterpret_cast<const ulonglong2 *>(s.cols[off - 1]);
+            const ulonglong2 *cw = reinterpret_cast<const ulonglong2 *>(s.cols[off - 1] + 16 * half);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
+            for (int e = 0; e < 4; ++e) {
               const ulonglong2 f = cw[e];
               f2 y = mul2(mul2((f2)x[4 * e] | (f2)x[4 * e + 1] << 32, f.x), rowff);
               f2 z = mul2(mul2((f2)x[4 * e + 2] | (f2)x[4 * e + 3] << 32, f.y), rowff);
-              hi[2 * e] = split2(y);
-              lo[2 * e] = pack2(y);
-              hi[2 * e + 1] = split2(z);
-              lo[2 * e + 1] = pack2(z);
+              parts[0][2 * e] = split2(y);
+              parts[1][2 * e] = pack2(y);
+              parts[0][2 * e + 1] = split2(z);
+              parts[1][2 * e + 1] = pack2(z);
             }
           } else {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
+            for (int e = 0; e < 8; ++e) {
               float v[2];
 #pragma unroll
               for (int k = 0; k < 2; ++k) {
-                const int j = 32 * c + 2 * e + k, lag = reverse ? j - row : row - j;
+                const int j = 32 * c + 16 * half + 2 * e + k, lag = reverse ? j - row : row - j;
                 const bool seen = lag >= 0 && (!reverse || j < n);
-                v[k] = seen ? __uint_as_float(x[2 * e + k]) * s.power[abs(lag)] : 0.f;
+                v[k] = seen ? __uint_as_float(x[2 * e + k]) * s.scaled[abs(lag)] : 0.f;
               }
               f2 y = f2_bits(v[0], v[1]);
-              hi[e] = split2(y);
-              lo[e] = pack2(y);
+              parts[0][e] = split2(y);
+              parts[1][e] = pack2(y);
             }
           }
         }
-        tc::tmem_st16(lanes + C::kScores + 32 * c, hi);
-        tc::tmem_st16(lanes + C::kScores + 32 * c + 16, lo);
+        tc::tmem_st8(at + 32 * c, parts[0]);
+        tc::tmem_st8(at + 32 * c + 8, parts[1]);
       }
       if (i && lane == 0) {  // the last chunk's rows are on their way
         if (storing) bulk_wait_read<0>();
@@ -584,21 +591,22 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, D == 64 ? 2 : 1)
       __syncwarp();
       if (!WAIT(s.inter, i)) break;
       tc::fence_after_sync();
+      const uint32_t out = lanes + C::kOut + half * (D / 2);
       {
-        const float f = s.power[reverse ? max(n - 1 - row, 0) : row + 1];
+        const float f = s.scaled[reverse ? max(n - 1 - row, 0) : row + 1];
         const f2 ff = f2_bits(f, f);
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
-          uint32_t x[32];
-          tc::tmem_ld32(lanes + C::kOut + 32 * c, x);
+          uint32_t x[16];
+          tc::tmem_ld16(out + 16 * c, x);
           tc::tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 32; e += 2) {
+          for (int e = 0; e < 16; e += 2) {
             const f2 y = mul2((f2)x[e] | (f2)x[e + 1] << 32, ff);
             x[e] = (uint32_t)y;
             x[e + 1] = (uint32_t)(y >> 32);
           }
-          tc::tmem_st32(lanes + C::kOut + 32 * c, x);
+          tc::tmem_st16(out + 16 * c, x);
         }
       }
       tc::tmem_wait_st();
@@ -608,80 +616,75 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, D == 64 ? 2 : 1)
       if (!WAIT(s.checked[i & 1], i >> 1) || !WAIT(s.done, i)) break;
       tc::fence_after_sync();
       const bool odd = s.odd[i & 1] != 0;
-      // whole warps of rows leave by TMA, 128 bytes of each at a time; the last ones of a
-      // sequence from their threads
-      const bool whole = 32 * warp + 32 <= n;
-      unsigned char *box = smem + C::kV + i % C::kValues * C::kTile + warp * 4096;
-      const long long at = b * w.os[0] + h * w.os[1] + (chunk * (long long)kC + row) * w.os[2];
-      storing = whole;
+      // whole warps of bf16 rows leave by TMA, 64 columns at a time; the last rows of a
+      // sequence, and fp32 parts, from their threads
+      const bool whole = 32 * quarter + 32 <= n && !w.out_f32;
+      unsigned char *box = smem + C::kV + i % C::kValues * C::kTile + (D == 64 ? 0 : half * kAtom) + quarter * 4096;
+      const long long to = b * w.os[0] + h * w.os[1] + (chunk * (long long)kC + row) * w.os[2] + half * (D / 2);
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
-        uint32_t x[32];
-        tc::tmem_ld32(lanes + C::kOut + 32 * c, x);
+        uint32_t x[16];
+        tc::tmem_ld16(out + 16 * c, x);
         tc::tmem_wait_ld();
         if (c == D / 32 - 1) {
           tc::fence_before_sync();
           __syncwarp();
           if (lane == 0) tc::mbar_arrive(&s.o_free);
         }
-        float y[32];
-#pragma unroll
-        for (int e = 0; e < 32; ++e) y[e] = __uint_as_float(x[e]) * p.a.scale;
         if (odd) {
+#pragma unroll 1
+          for (int e = 0; e < 16; ++e) {
+            const bool bad = s.bad[i & 1][half * (D / 2) + 16 * c + e] <= (reverse ? kC - 1 - row : row);
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (s.bad[i & 1][32 * c + e] <= (reverse ? kC - 1 - row : row)) y[e] = __uint_as_float(0x7fc00000u);
+            for (int k = 0; k < 16; ++k)
+              if (k == e && bad) x[k] = 0x7fc00000u;
+          }
         }
         if (w.out_f32) {
-          unsigned char *to = box + c % C::kAtoms * kAtom;
-          if (whole && c >= C::kAtoms) {  // the place is read before it is filled again
-            if (lane == 0) bulk_wait_read<C::kAtoms - 1>();
-            __syncwarp();
-          }
+          if (row < n)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float4 z = make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
-            if (whole)
-              *reinterpret_cast<float4 *>(to + swz128(lane, e)) = z;
-            else if (row < n)
-              *reinterpret_cast<float4 *>(static_cast<float *>(w.out) + at + 32 * c + 4 * e) = z;
-          }
-          if (whole) {
-            tc::fence_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              store_rows(to, map, 32 * c, chunk * kC + 32 * warp, mh, mb);
-              bulk_commit();
-            }
-          }
-        } else {
-          unsigned char *to = box + c / 2 * kAtom;
+            for (int e = 0; e < 16; e += 8)
+              asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
+                               static_cast<float *>(w.out) + to + 16 * c + e),
+                           "r"(x[e]), "r"(x[e + 1]), "r"(x[e + 2]), "r"(x[e + 3]), "r"(x[e + 4]), "r"(x[e + 5]),
+                           "r"(x[e + 6]), "r"(x[e + 7])
+                           : "memory");
+          continue;
+        }
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint4 z = make_uint4(pack_bf16(y[8 * e], y[8 * e + 1]), pack_bf16(y[8 * e + 2], y[8 * e + 3]),
-                                       pack_bf16(y[8 * e + 4], y[8 * e + 5]), pack_bf16(y[8 * e + 6], y[8 * e + 7]));
-            if (whole)
-              *reinterpret_cast<uint4 *>(to + swz128(lane, c % 2 * 4 + e)) = z;
-            else if (row < n)
-              *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(w.out) + at + 32 * c + 8 * e) = z;
-          }
-          if (whole && c % 2) {
-            tc::fence_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              store_rows(to, map, 64 * (c / 2), chunk * kC + 32 * warp, mh, mb);
-              bulk_commit();
-            }
-          }
+        for (int e = 0; e < 2; ++e) {
+          uint32_t y[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            y[k] = pack_bf16(__uint_as_float(x[8 * e + 2 * k]), __uint_as_float(x[8 * e + 2 * k + 1]));
+          const uint4 z = make_uint4(y[0], y[1], y[2], y[3]);
+          if (whole)
+            *reinterpret_cast<uint4 *>(box + swz128(lane, (D == 64 ? 4 * half : 0) + 2 * c + e)) = z;
+          else if (row < n)
+            *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(w.out) + to + 16 * c + 8 * e) = z;
+        }
+      }
+      storing = false;
+      if (whole) {
+        tc::fence_async_smem();
+        if (D == 64)  // two warps' halves of one box
+          asm volatile("bar.sync %0, 64;" ::"r"(3 + quarter) : "memory");
+        else
+          __syncwarp();
+        if (lane == 0 && (D == 128 || half == 0)) {
+          store_rows(box, map, D == 64 ? 0 : 64 * half, chunk * kC + 32 * quarter, mh, mb);
+          bulk_commit();
+          storing = true;
         }
       }
       if (odd) {  // clean for the chunk after the next
-        asm volatile("bar.sync 2, 128;" ::: "memory");
-        if (row < D) s.bad[i & 1][row] = kC;
-        if (row == 0) s.odd[i & 1] = 0;
+        asm volatile("bar.sync 2, 256;" ::: "memory");
+        if (warp < 4 && row < D) s.bad[i & 1][row] = kC;
+        if (warp == 0 && lane == 0) s.odd[i & 1] = 0;
       }
     }
     if (lane == 0) bulk_wait_read<0>();
+    }
   }
   tc::fence_before_sync();
   __syncthreads();
