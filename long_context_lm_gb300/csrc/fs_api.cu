@@ -1082,7 +1082,7 @@ LinearRows linear_rows(const void *x, const long long (&s)[3], int share) {
   return r;
 }
 
-// The workspace: the header with the error word, the states between stretches, the parts
+// The workspace: the header with the error word, the chunks' states, the parts
 // of shared heads' gradients.
 struct LinearLayout {
   size_t states, dk, dv, total;
@@ -1105,8 +1105,7 @@ LinearLayout linear_layout(int batch, int H, int Hkv, int T, int d, bool backwar
 int linear_sweeps(const LinearArgs &a, const LinearLayout &L, void *ws, cudaStream_t st) {
   if (a.T <= FS_LINEAR_STEPS) return status_of(launch_linear_recurrent(a, st));
   char *base = static_cast<char *>(ws);
-  return status_of(launch_linear_chunks(a, reinterpret_cast<float *>(base + L.states),
-                                        reinterpret_cast<int *>(base), st));
+  return status_of(launch_linear_chunks(a, base + L.states, reinterpret_cast<int *>(base), st));
 }
 
 }  // namespace

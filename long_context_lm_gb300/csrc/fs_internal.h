@@ -216,9 +216,9 @@ struct LinearArgs {
 };
 cudaError_t launch_linear_recurrent(const LinearArgs &a, cudaStream_t st);
 // The same in chunks of 128 tokens (k16_linear_tc.cu), with linear_chunk_bytes of
-// scratch for the states between stretches.
+// scratch for states.
 size_t linear_chunk_bytes(int sweeps, int batch, int H, int T, int d);
-cudaError_t launch_linear_chunks(const LinearArgs &a, float *states, int *err, cudaStream_t st);
+cudaError_t launch_linear_chunks(const LinearArgs &a, void *ws, int *err, cudaStream_t st);
 struct LinearSumArgs {
   const float *part;   // [batch, H, T, d]
   void *out;           // bf16 [batch, H / share, T, d]

@@ -12,27 +12,23 @@
 // Precision.  q, k and v are bf16 and go in as they are.  The scores times their
 // powers, and S as a factor, go in as a bf16 high and low part (2^-16 of
 // themselves); the weighted values, of which states are made, in three parts
-// (24 bits).  All sums are fp32; S itself is fp32, in registers.
+// (24 bits).  All sums are fp32; S itself is fp32.
 //
-// A block takes one (sequence, head), or one of `splits` stretches of it, chunk
-// after chunk; S never leaves it.  Warps:
-//   0-7       rows, two warps to 32 of them, each with half of the columns: scores to bf16
-//             parts in their own TMEM columns, Q S times the row's power in place, the
-//             finished rows by way of the values' place in shared memory (a TMA store: rows
-//             written by their own threads would be 32 places an instruction)
-//   8..       states (D / 16 warps): weighted values into a slab, the next one's made in
-//             registers while it is multiplied; S in registers, its bf16 parts into
-//             shared memory for the next chunk
-//   last four one for TMA loads, one that issues the products of the rows, one that issues
-//             those of the slabs (issued by one thread, slabs waited behind the rows'
-//             products, a slab at a time, and took 7000 cycles a chunk in place of 3000)
-// Values are loaded a chunk ahead.  Heads of 64 leave room for two blocks an SM, which
-// fill each other's waits; heads of 128 for one.
+// Two passes over the chunks, with a small kernel between them:
+//   states  every (sequence, head) is cut into stretches, as many as fill the GPU; a
+//           block goes through one with S in registers, from zeros, and leaves the
+//           state before each chunk and the one after the last in memory
+//   join    runs through the stretches: the state before each
+//   rows    all chunks by themselves, in equal runs: S = (the stretch's own) + lam^m (the state
+//           before it), then the three products of the outputs
+// One pass (states in registers, rows beside them) reads and writes less, but with few
+// heads needs the stretches' states beforehand, by a pass as long as the first here, and with
+// any number of heads leaves blocks without work: 65536 tokens x 16 heads XX us, now XX;
+// 5 ragged sequences of 8191 x 16 heads of 128 321, now XX.  The states between the passes
+// (16 KB a chunk of 64 KB of rows; heads of 128: 64 of 128) are kept to what the L2 holds
+// by going through long sequences in bands.
 //
-// With fewer (sequence, head) pairs than blocks fit, each is cut into stretches: a
-// first pass of the same kernel without rows makes the states of the stretches
-// alone (k and v are read twice then), a small kernel runs through them, and
-// the main pass starts each stretch from its own.
+// What bounds it: XX
 #include <cuda.h>
 #include <string.h>
 
@@ -45,15 +41,23 @@
 namespace fs {
 namespace {
 
-constexpr int kC = 128;       // tokens of a chunk
-constexpr uint32_t kAtom = kC * 128;       // 64 elements of a chunk's rows
+constexpr int kC = 128;               // tokens of a chunk
+constexpr uint32_t kAtom = kC * 128;  // bytes of 64 elements of a chunk's rows
 
+// A band: the chunks [c0, c1) of every sequence, in the sweep's order.
 struct Params {
   LinearArgs a;
-  int splits;
-  float *states;     // [sweep, batch H, splits, D D]: the state before each stretch
-  int map[3][3];     // which map holds q, k, v of a sweep
-  int axes[4][2];    // 0 where a map's sequences or heads are one
+  int c0, c1;
+  bool first, last;   // band
+  int splits;         // stretches of a band
+  float *local;       // [sweep, batch H, c1 - c0 - 1, D D]: the state before each chunk but the band's
+                      // first, of its stretch alone (none before a stretch's first)
+  float *slots;       // [sweep, batch H, splits, D D]: what each stretch adds; then the state before it
+  float *carry;       // [sweep, batch H, D D]: the state behind the band
+  uint8_t *odd;       // [sweep, batch H, c1 - c0, 8]: not all of the values that a warp of the states'
+                      // kernel saw of the chunk are finite
+  int map[3][3];      // which map holds q, k, v of a sweep
+  int axes[4][2];     // 0 where a map's sequences or heads are one
   int out_axes[3][2];
   int *err;
 };
@@ -62,62 +66,45 @@ struct Maps {
   CUtensorMap in[4], out[3];
 };
 
-template <int D>
-struct Cfg {
-  static constexpr int kAtoms = D / 64;
-  static constexpr int kStateWarps = D / 16;
-  static constexpr int kTma = 8 + kStateWarps, kMma = kTma + 1, kMmaU = kTma + 2;
-  static constexpr int kThreads = 32 * (kTma + 4);
-  static constexpr int kSlab = 32, kSlabs = kC / kSlab;  // tokens of a slab, slabs
-  static constexpr int kUnits = 2;  // 16-byte pieces of a slab for a state thread
-  // registers a thread: at launch, then of the rows', states' and last four warps
-  static constexpr int kRegs = D == 64 ? 64 : 96, kRowRegs = D == 64 ? 64 : 80, kStateRegs = D == 64 ? 88 : 128,
-                       kLastRegs = 40;
-  static_assert(8 * kRowRegs + kStateWarps * kStateRegs + 4 * kLastRegs <= (12 + kStateWarps) * kRegs, "registers");
-  static constexpr uint32_t kSlabAtom = kSlab * 128;
-  static constexpr int kHalves = D / 64;  // groups of 16 rows that a state warp holds
-  static constexpr int kValues = 2;                              // chunks of v held
-  static constexpr uint32_t kTile = kAtoms * kAtom;              // q, k or v
-  static constexpr uint32_t kPart = kAtoms * kSlabAtom;          // one part of a slab
-  static constexpr uint32_t kSPart = kAtoms * D * 128;           // one part of S
-  static constexpr uint32_t kQ = 0, kK = kTile, kV = kK + kTile, kS = kV + kValues * kTile,
-                            kSlab0 = kS + 2 * kSPart, kBytes = kSlab0 + 3 * kPart;
-  // TMEM columns: scores (then their parts), outputs, the chunk's addition to S
-  static constexpr uint32_t kScores = 0, kOut = kC, kU = kC + D, kCols = D == 64 ? 256 : 512;
-};
-
-struct Shared {
-  uint64_t qfull, qempty, kfull, kempty, vfull[2], vempty[2];
-  uint64_t slab_full, slab_empty;
-  uint64_t s_ready, s_free, scores, inter, parts, done, o_free, u_full, u_free, fin, fin_u;
-  // values looked through: the states' warps may be a chunk ahead of the rows', not two
-  uint64_t checked[2];
-  uint32_t tmem;
-  int odd[2];                 // a chunk's values are not all finite
-  float power[kC + 4];        // lam^n
-  float scaled[kC + 4];       // scale lam^n
-  alignas(16) float cols[3][32];  // see the rows' warps (read four at a time)
-  int bad[2][128];            // per column: the first such token in the sweep's order
-};
-
-// A stretch of a sweep: chunks [from, to) in the sweep's order of the `chunks` of a sequence of n tokens.
-struct Stretch {
-  int n, chunks, per, last, from, to;  // last: the last stretch with a token (0 if there is none)
-  __device__ __forceinline__ Stretch(const Params &p, int b, int r) {
+// A sequence's part of the band: chunks [lo, hi) of `chunks`, in stretches of `per`.
+struct Band {
+  int n, chunks, lo, hi, per, stretches;
+  __device__ __forceinline__ Band(const Params &p, int b) {
     n = p.a.count ? min(max(p.a.count[b], 0), p.a.T) : p.a.T;
     chunks = (n + kC - 1) / kC;
-    per = max((chunks + p.splits - 1) / p.splits, 1);
-    last = max((chunks + per - 1) / per - 1, 0);
-    from = min(r * per, chunks);
-    to = min(from + per, chunks);
+    lo = p.c0;
+    hi = max(min(p.c1, chunks), lo);
+    per = max((hi - lo + p.splits - 1) / p.splits, 1);
+    stretches = (hi - lo + per - 1) / per;
   }
   __device__ __forceinline__ int chunk(int i, bool reverse) const { return reverse ? chunks - 1 - i : i; }
   __device__ __forceinline__ int size(int chunk) const { return min(n - chunk * kC, kC); }
-  // tokens of the chunks [a, b) in the sweep's order
+  // tokens of the chunks [a, b) in the sweep's order: the sequence's last chunk may not be whole
   __device__ __forceinline__ int tokens(int a, int b, bool reverse) const {
-    const int whole = (b - a) * kC, odd = chunks * kC - n;  // the sequence's last chunk lacks `odd`
-    return whole - ((reverse ? a == 0 : b == chunks) && b > a ? odd : 0);
+    const int odd = chunks * kC - n;
+    return (b - a) * kC - (b > a && (reverse ? a == 0 : b == chunks) ? odd : 0);
   }
+  __device__ __forceinline__ int end(int r) const { return min(lo + (r + 1) * per, hi); }
+};
+// The last chunk of a sequence need not go into a state that nobody wants.
+__device__ __forceinline__ bool wants_last(const Params &p, const LinearSweep &w) {
+  return !p.last || w.state_out;
+}
+
+// How the states' warps hold a D x D matrix (and how it lies in memory between the passes): warp
+// w rows 16 (w % 4).. of 64 (32 (w % 4).. of 128) and columns 64 (w / 4).., a lane of each 8 x 8 block two
+// columns of one row.
+template <int D>
+struct Frags {
+  static constexpr int kWarps = D / 16, kThreads = 32 * kWarps;
+  static constexpr int kHalves = D / 64;  // groups of 16 rows that a warp holds
+  static __device__ __forceinline__ int row0(int t) { return (D == 64 ? t / 32 * 16 : t / 32 % 4 * 32) + t % 32 / 4; }
+  static __device__ __forceinline__ int col0(int t) { return (D == 64 ? 0 : t / 128 * 64) + t % 4 * 2; }
+  // pair e of group g: the row and the first column
+  static __device__ __forceinline__ int row(int t, int g, int e) { return row0(t) + 16 * g + e % 2 * 8; }
+  static __device__ __forceinline__ int col(int t, int e) { return col0(t) + e / 2 * 8; }
+  // floats from a matrix's start to pairs e and e + 1 (e even) of group g
+  static __device__ __forceinline__ int at(int t, int g, int e) { return ((g * 8 + e / 2) * kThreads + t) * 4; }
 };
 
 // tc::desc_sw128 for elements in several blocks of 64, `apart` bytes from one to the next.
@@ -178,149 +165,97 @@ __device__ __forceinline__ void stmatrix4(uint32_t at, const uint32_t (&r)[4]) {
 
 #define WAIT(bar, k) __all_sync(0xffffffffu, tc::mbar_wait(&(bar), (k) & 1, p.err))
 
-// kRows: the whole sweep; without, only the states of the stretches (into p.states).
-template <int D, bool kRows>
-__global__ void __launch_bounds__(Cfg<D>::kThreads, D == 64 ? 2 : 1)
-    k16_linear_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
-  using C = Cfg<D>;
+// ---------------------------------------------------------------------------
+// states
+// ---------------------------------------------------------------------------
+template <int D>
+struct StateCfg {
+  static constexpr int kAtoms = D / 64, kWarps = D / 16;
+  static constexpr int kTma = kWarps, kMma = kWarps + 1, kThreads = 32 * (kWarps + 4);
+  static constexpr int kSlab = 32, kSlabs = kC / kSlab;  // tokens of a slab of weighted values
+  static constexpr uint32_t kSlabAtom = kSlab * 128;
+  static constexpr uint32_t kTile = kAtoms * kAtom, kPart = kAtoms * kSlabAtom;
+  static constexpr uint32_t kK = 0, kV = kTile, kSlab0 = 3 * kTile, kBytes = kSlab0 + 3 * kPart;
+  static constexpr int kBlocks = D == 64 ? 3 : 1;  // of an SM
+};
+
+struct StateShared {
+  uint64_t kfull, kempty, vfull[2], vempty[2], slab_full, slab_empty, u_full, u_free, fin;
+  uint32_t tmem;
+  float power[kC + 4];  // lam^n
+};
+
+// Warps: D / 16 that make weighted values (the next slab's in registers while one is
+// multiplied) and hold S, then one for TMA loads (values a chunk ahead) and one that issues
+// the products.  A thread has 16 bytes of rows r and r + 16 of every slab.
+template <int D>
+__global__ void __launch_bounds__(StateCfg<D>::kThreads, StateCfg<D>::kBlocks)
+    k16_states_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
+  using C = StateCfg<D>;
+  using F = Frags<D>;
   extern __shared__ unsigned char smem_raw[];
   unsigned char *smem = reinterpret_cast<unsigned char *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  __shared__ Shared s;
+  __shared__ StateShared s;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const LinearSweep &w = p.a.sweep[blockIdx.z];
   const int b = blockIdx.y / p.a.H, h = blockIdx.y % p.a.H, r = blockIdx.x;
-  const Stretch st(p, b, r);
+  const Band band(p, b);
   const bool reverse = w.reverse;
-  // nothing for this block: no such stretch, or the last one, whose state nobody starts from
-  // (with one stretch the main pass reads the given state itself)
-  if (kRows ? r > st.last : r >= st.last) return;
+  if (r >= band.stretches) return;
+  const int from = band.lo + r * band.per, to = band.end(r);
+  const int chunks = to - from - (to == band.chunks && !wants_last(p, w) ? 1 : 0);
   const float decay = p.a.decay[h];
 
   if (threadIdx.x == 0) {
-    for (uint64_t *x : {&s.qfull, &s.qempty, &s.kfull, &s.s_free, &s.scores, &s.inter, &s.done, &s.u_full, &s.fin})
+    for (uint64_t *x : {&s.kfull, &s.kempty, &s.vfull[0], &s.vfull[1], &s.slab_empty, &s.u_full, &s.fin})
       tc::mbar_init(x, 1);
-    for (int i = 0; i < 2; ++i) {
-      tc::mbar_init(&s.vfull[i], 1);
-      tc::mbar_init(&s.vempty[i], kRows ? 8 : C::kStateWarps);
-    }
-    tc::mbar_init(&s.slab_empty, 1);
-    for (uint64_t *x : {&s.slab_full, &s.s_ready, &s.u_free, &s.checked[0], &s.checked[1]}) tc::mbar_init(x, C::kStateWarps);
-    for (uint64_t *x : {&s.parts, &s.o_free}) tc::mbar_init(x, 8);
-    tc::mbar_init(&s.kempty, kRows ? 2 : 1);  // read by the scores' product and by the slabs'
-    tc::mbar_init(&s.fin_u, 1);
+    for (uint64_t *x : {&s.vempty[0], &s.vempty[1], &s.slab_full, &s.u_free}) tc::mbar_init(x, C::kWarps);
     tc::mbar_fence_init();
-    s.odd[0] = s.odd[1] = 0;
   }
   for (int i = threadIdx.x; i <= kC; i += C::kThreads) {
     const Factor f = decay_power(decay, i);
     s.power[i] = f.hi + f.lo;
-    s.scaled[i] = (f.hi + f.lo) * p.a.scale;
   }
-  for (int i = threadIdx.x; i < 96; i += C::kThreads) {
-    const Factor f = decay_power(decay, 32 * (i / 32 + 1) + (reverse ? i % 32 - 31 : -(i % 32)));
-    s.cols[i / 32][i % 32] = f.hi + f.lo;
-  }
-  for (int i = threadIdx.x; i < 256; i += C::kThreads) s.bad[i / 128][i % 128] = kC;
   if (warp == C::kMma) {
-    tc::tmem_alloc(&s.tmem, kRows ? C::kCols : D);
+    tc::tmem_alloc(&s.tmem, D);
     tc::tmem_relinquish();
   }
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = s.tmem, base = smem_u32(smem);
-  const uint32_t tu = tmem + (kRows ? C::kU : 0);
-  const int chunks = st.to - st.from;
-  if (warp >= C::kTma) {
-    tc::regs_dec<C::kLastRegs>();
+
   if (warp == C::kTma && lane == 0) {
-    // ------------------------------------------------------------------ loads
-    const int mq = p.map[blockIdx.z][0], mk = p.map[blockIdx.z][1], mv = p.map[blockIdx.z][2];
+    const int mk = p.map[blockIdx.z][1], mv = p.map[blockIdx.z][2];
     auto load = [&](uint32_t at, int m, const LinearRows &x, uint64_t *bar, int i) {
-      const int t = st.chunk(st.from + i, reverse) * kC;
+      const int t = band.chunk(from + i, reverse) * kC;
       tc::mbar_arrive_expect_tx(bar, C::kTile);
       for (int k = 0; k < C::kAtoms; ++k)
         load_rows(smem + at + k * kAtom, &maps.in[m], bar, 64 * k, t, h / x.share * p.axes[m][1],
                   b * p.axes[m][0]);
     };
-    int nq = 0, nk = 0, nv = 0;  // loaded so far
+    int nk = 0, nv = 0;  // loaded so far
     bool ok = true;
-    auto load_q = [&]() {
-      if (!kRows || !ok || nq >= chunks) return;
-      if (nq && !(ok = tc::mbar_wait(&s.qempty, (nq - 1) & 1, p.err))) return;
-      load(C::kQ, mq, w.q, &s.qfull, nq);
-      ++nq;
-    };
-    auto load_k = [&]() {
-      if (!ok || nk >= chunks) return;
-      if (nk && !(ok = tc::mbar_wait(&s.kempty, (nk - 1) & 1, p.err))) return;
-      load(C::kK, mk, w.k, &s.kfull, nk);
-      ++nk;
-    };
-    auto load_v = [&]() {
-      const int at = nv % C::kValues;
-      if (!ok || nv >= chunks) return;
-      if (nv >= C::kValues && !(ok = tc::mbar_wait(&s.vempty[at], (nv / C::kValues - 1) & 1, p.err))) return;
-      load(C::kV + at * C::kTile, mv, w.v, &s.vfull[at], nv);
-      ++nv;
-    };
-    // in the order in which places become free
-    load_k();
-    load_q();
-    load_v();
-    load_v();
-    for (int i = 1; i < chunks && ok; ++i) {
-      load_q();
-      load_k();
-      load_v();
+    for (int i = -1; i < chunks && ok; ++i) {
+      if (i + 1 < chunks) {
+        if (nv > 1) ok = tc::mbar_wait(&s.vempty[nv & 1], (nv / 2 - 1) & 1, p.err);
+        if (!ok) break;
+        load(C::kV + (nv & 1) * C::kTile, mv, w.v, &s.vfull[nv & 1], nv);
+        ++nv;
+      }
+      const int k = i < 0 ? 0 : i;
+      if (nk == k && k < chunks) {
+        if (nk) ok = tc::mbar_wait(&s.kempty, (nk - 1) & 1, p.err);
+        if (!ok) break;
+        load(C::kK, mk, w.k, &s.kfull, nk);
+        ++nk;
+      }
     }
     // what is under way lands before the block ends
-    if (nq) tc::mbar_wait(&s.qfull, (nq - 1) & 1, nullptr);
     if (nk) tc::mbar_wait(&s.kfull, (nk - 1) & 1, nullptr);
-    for (int i = nv > C::kValues ? nv - C::kValues : 0; i < nv; ++i)
-      tc::mbar_wait(&s.vfull[i % C::kValues], i / C::kValues & 1, nullptr);
-  } else if (kRows && warp == C::kMma && lane == 0) {
-    // ----------------------------------------------------- products of the rows
-    constexpr uint32_t kQK = tc::idesc_bf16(128, 128, 0), kB = tc::idesc_bf16(128, D, 1);
-    const uint32_t keys = base + C::kK;
-    for (int i = 0; i < chunks; ++i) {
-      const uint32_t values = base + C::kV + i % C::kValues * C::kTile;
-      if (!tc::mbar_wait(&s.kfull, i & 1, p.err) || !tc::mbar_wait(&s.qfull, i & 1, p.err)) break;
-      tc::fence_after_sync();
-#pragma unroll
-      for (int k = 0; k < D / 16; ++k)
-        tc::mma_ss(tmem + C::kScores, tc::desc_sw128(base + C::kQ + k / 4 * kAtom + k % 4 * 32),
-                   tc::desc_sw128(keys + k / 4 * kAtom + k % 4 * 32), kQK, k > 0);
-      tc::mma_commit(&s.scores);
-      tc::mma_commit(&s.kempty);
-      if (!tc::mbar_wait(&s.s_ready, i & 1, p.err) ||
-          (i && !tc::mbar_wait(&s.o_free, (i - 1) & 1, p.err)))
-        break;
-      tc::fence_after_sync();
-#pragma unroll
-      for (int k = 0; k < 2 * D / 16; ++k) {
-        const int kk = k % (D / 16), part = k / (D / 16);
-        tc::mma_ss(tmem + C::kOut, tc::desc_sw128(base + C::kQ + kk / 4 * kAtom + kk % 4 * 32),
-                   desc_blocks(base + C::kS + part * C::kSPart + kk * 2048, D * 128), kB, k > 0);
-      }
-      tc::mma_commit(&s.inter);
-      tc::mma_commit(&s.s_free);
-      tc::mma_commit(&s.qempty);
-      if (!tc::mbar_wait(&s.parts, i & 1, p.err) || !tc::mbar_wait(&s.checked[i & 1], i >> 1 & 1, p.err)) break;
-      tc::fence_after_sync();
-#pragma unroll
-      for (int k = 0; k < 2 * kC / 16; ++k) {
-        const int kk = k % (kC / 16), part = k / (kC / 16);
-        tc::mma_ts(tmem + C::kOut, tmem + C::kScores + kk * 16 + part * 8,
-                   desc_blocks(values + kk * 2048, kAtom), kB, 1);
-      }
-      tc::mma_commit(&s.done);
-    }
-    tc::mma_commit(&s.fin);
-    tc::mbar_wait(&s.fin, 0, nullptr);
-  } else if (warp == C::kMmaU && lane == 0) {
-    // ---------------------------------------------------- products of the slabs
+    for (int i = nv > 2 ? nv - 2 : 0; i < nv; ++i) tc::mbar_wait(&s.vfull[i & 1], i / 2 & 1, nullptr);
+  } else if (warp == C::kMma && lane == 0) {
     constexpr uint32_t kUD = tc::idesc_bf16(D, D, 1) | 1u << 15;  // K^T: its rows run along M
     const uint32_t keys = base + C::kK;
     bool ok = true;
@@ -328,127 +263,71 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, D == 64 ? 2 : 1)
       if (!tc::mbar_wait(&s.kfull, i & 1, p.err)) break;
       if (i && !tc::mbar_wait(&s.u_free, (i - 1) & 1, p.err)) break;
       for (int j = 0; j < C::kSlabs; ++j) {
-        const int at = i * C::kSlabs + j;
-        if (!(ok = tc::mbar_wait(&s.slab_full, at & 1, p.err))) break;
+        if (!(ok = tc::mbar_wait(&s.slab_full, (i * C::kSlabs + j) & 1, p.err))) break;
         tc::fence_after_sync();
 #pragma unroll
-        for (int k = 0; k < 3 * C::kUnits; ++k) {
-          const int kk = k % C::kUnits, part = k / C::kUnits;
-          tc::mma_ss(tu, desc_blocks(keys + j * C::kSlabAtom + kk * 2048, kAtom),
-                     desc_blocks(base + C::kSlab0 + part * C::kPart + kk * 2048, C::kSlabAtom),
-                     kUD, j > 0 || k > 0);
-        }
+        for (int k = 0; k < 6; ++k)
+          tc::mma_ss(tmem, desc_blocks(keys + j * C::kSlabAtom + k % 2 * 2048, kAtom),
+                     desc_blocks(base + C::kSlab0 + k / 2 * C::kPart + k % 2 * 2048, C::kSlabAtom), kUD,
+                     j > 0 || k > 0);
         tc::mma_commit(&s.slab_empty);
       }
       if (!ok) break;
       tc::mma_commit(&s.u_full);
       tc::mma_commit(&s.kempty);
     }
-    tc::mma_commit(&s.fin_u);
-    tc::mbar_wait(&s.fin_u, 0, nullptr);
-  }
-  } else if (warp >= 8) {
-    tc::regs_inc<C::kStateRegs>();
-    // ------------------------------------------------------------------ states
-    constexpr int kT = 32 * C::kStateWarps;
-    const int sw = warp - 8, t = threadIdx.x - 256;
-    // this lane's places in S: rows row0 + 16 g (+ 8), columns col0 + 8 e (+ 1)
-    const int row0 = (D == 64 ? sw * 16 : sw % 4 * 32) + lane / 4;
-    const int col0 = (D == 64 ? 0 : sw / 4 * 64) + lane % 4 * 2;
-    const uint32_t lanes = tu + ((uint32_t)(warp % 4 * 32) << 16) + (D == 64 ? 0 : sw / 4 * 64);
+    tc::mma_commit(&s.fin);
+    tc::mbar_wait(&s.fin, 0, nullptr);
+  } else if (warp < C::kWarps) {
+    const int t = threadIdx.x;
+    const uint32_t lanes = tmem + ((uint32_t)(warp % 4 * 32) << 16) + (D == 64 ? 0 : warp / 4 * 64);
     const size_t bh = (size_t)blockIdx.z * gridDim.y + blockIdx.y;
-    f2 S[C::kHalves][16];
-    auto each = [&](auto f) {  // f(pair, row, column of its first)
+    f2 S[F::kHalves][16];
 #pragma unroll
-      for (int g = 0; g < C::kHalves; ++g)
+    for (int g = 0; g < F::kHalves; ++g)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) f(S[g][e], row0 + 16 * g + (e & 1) * 8, col0 + e / 2 * 8);
-    };
-    // between the passes states lie as the lanes hold them
-    auto slot = [&](int i) { return p.states + (bh * p.splits + i) * (D * D) + t * 4; };
-    const float *given = w.state ? w.state + (size_t)blockIdx.y * D * D : nullptr;
-    if (kRows && st.last > 0) {
-      const float *from = slot(r);
-#pragma unroll
-      for (int g = 0; g < C::kHalves; ++g)
-#pragma unroll
-        for (int e = 0; e < 16; e += 2) {
-          const ulonglong2 x = *reinterpret_cast<const ulonglong2 *>(from + (g * 8 + e / 2) * kT * 4);
-          S[g][e] = x.x, S[g][e + 1] = x.y;
-        }
-    } else if (given && r == 0) {
-      const int sr = w.transposed ? 1 : D, sc = w.transposed ? D : 1;
-      each([&](f2 &x, int row, int col) {
-        const float *at = given + row * sr + col * sc;
-        x = f2_bits(at[0] * w.state_mul, at[sc] * w.state_mul);
-      });
-    } else {
-      each([&](f2 &x, int, int) { x = 0; });
-    }
+      for (int e = 0; e < 16; ++e) S[g][e] = 0;
     auto save = [&](float *to) {
 #pragma unroll
-      for (int g = 0; g < C::kHalves; ++g)
+      for (int g = 0; g < F::kHalves; ++g)
 #pragma unroll
         for (int e = 0; e < 16; e += 2)
-          *reinterpret_cast<ulonglong2 *>(to + (g * 8 + e / 2) * kT * 4) = make_ulonglong2(S[g][e], S[g][e + 1]);
+          *reinterpret_cast<ulonglong2 *>(to + F::at(t, g, e)) = make_ulonglong2(S[g][e], S[g][e + 1]);
     };
-    // S as the factor of the next product: two parts, [row][column] with the columns
-    // swizzled.  A lane names the row that it is to fill of one of four 8 x 8 blocks:
-    // rows + 0 and + 8 of two neighbours among the blocks of columns.
-    const uint32_t sat = base + C::kS + col0 / 64 * (D * 128) + (row0 - lane / 4 + lane / 8 % 2 * 8 + lane % 8) * 128;
-    auto publish = [&]() {
-#pragma unroll
-      for (int g = 0; g < C::kHalves; ++g)
-#pragma unroll
-        for (int e = 0; e < 16; e += 4) {
-          uint32_t hi[4], lo[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            f2 x = S[g][e + k];
-            hi[k] = split2(x);
-            lo[k] = pack2(x);
-          }
-          const uint32_t at = sat + g * 16 * 128 + (((e / 2 + lane / 16) ^ (lane % 8)) << 4);
-          stmatrix4(at, hi);
-          stmatrix4(at + C::kSPart, lo);
-        }
-      tc::fence_async_smem();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&s.s_ready);
-    };
-    if (!kRows && r == 0) save(slot(0));
-    if (kRows && chunks) publish();
+    const size_t nb = p.c1 - p.c0;
+    // the matrix of the stretch's chunk i >= 1; the flag of chunk i
+    auto local = [&](int i) { return p.local + (bh * (nb - 1) + (from - p.c0 + i - 1)) * (D * D); };
+    auto flag = [&](int i) { return p.odd + (bh * nb + (from - p.c0 + i)) * 8 + warp; };
     const Factor whole = decay_power(decay, kC);
-    // this thread's sixteen bytes of a slab's row r16 (and r16 + 16)
     const int r16 = t % 128 / 8, ch = t % 8, atom = t / 128;
     const uint32_t in = swz128(r16, ch);
-    unsigned char *to = smem + C::kSlab0 + atom * C::kSlabAtom + in;
+    unsigned char *slab = smem + C::kSlab0 + atom * C::kSlabAtom + in;
+    bool ok = true;
     for (int i = 0; i < chunks; ++i) {
-      const int n = st.size(st.chunk(st.from + i, reverse));
-      unsigned char *values = smem + C::kV + i % C::kValues * C::kTile;
-      if (!WAIT(s.vfull[i % C::kValues], i / C::kValues)) break;
+      const int n = band.size(band.chunk(from + i, reverse));
+      unsigned char *values = smem + C::kV + (i & 1) * C::kTile;
+      if (!(ok = WAIT(s.vfull[i & 1], i / 2))) break;
+      if (i) save(local(i));
       if (n < kC) {
         // what lies behind the sequence takes no part, whatever it is
-        if (!WAIT(s.kfull, i)) break;
-        unsigned char *keys = smem + C::kK;
-        for (int u = t; u < (kC - n) * (D / 8); u += kT) {
+        if (!(ok = WAIT(s.kfull, i))) break;
+        for (int u = t; u < (kC - n) * (D / 8); u += F::kThreads) {
           const uint32_t at = u % (D / 8) / 8 * kAtom + swz128(n + u / (D / 8), u % 8);
-          *reinterpret_cast<uint4 *>(keys + at) = make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4 *>(smem + C::kK + at) = make_uint4(0, 0, 0, 0);
           *reinterpret_cast<uint4 *>(values + at) = make_uint4(0, 0, 0, 0);
         }
         tc::fence_async_smem();
-        asm volatile("bar.sync 1, %0;" ::"n"(32 * C::kStateWarps) : "memory");
+        asm volatile("bar.sync 1, %0;" ::"n"(F::kThreads) : "memory");
       }
-      unsigned char *from = values + atom * kAtom + in;
+      const unsigned char *source = values + atom * kAtom + in;
       uint32_t some = 0;  // the bits of all third parts
-      bool ok = true;
 #pragma unroll 1
       for (int j = 0; j < C::kSlabs; ++j) {
-        uint32_t part[C::kUnits][3][4];
+        uint32_t part[2][3][4];
 #pragma unroll
-        for (int k = 0; k < C::kUnits; ++k) {
+        for (int k = 0; k < 2; ++k) {
           const int row = j * C::kSlab + r16 + 16 * k;
-          const uint4 x = *reinterpret_cast<const uint4 *>(from + j * C::kSlabAtom + k * 2048);
+          const uint4 x = *reinterpret_cast<const uint4 *>(source + j * C::kSlabAtom + k * 2048);
           const float f = row < n ? s.power[reverse ? row + 1 : n - 1 - row] : 0.f;
           const uint32_t v[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
@@ -463,42 +342,26 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, D == 64 ? 2 : 1)
         const int at = i * C::kSlabs + j;
         if (at && !(ok = WAIT(s.slab_empty, at - 1))) break;
 #pragma unroll
-        for (int k = 0; k < C::kUnits; ++k)
+        for (int k = 0; k < 2; ++k)
 #pragma unroll
           for (int q = 0; q < 3; ++q)
-            *reinterpret_cast<uint4 *>(to + q * C::kPart + k * 2048) =
+            *reinterpret_cast<uint4 *>(slab + q * C::kPart + k * 2048) =
                 make_uint4(part[k][q][0], part[k][q][1], part[k][q][2], part[k][q][3]);
-        // A value that is not finite leaves NaN in the third part (and NaN in the state's column).
-        // It leaves V before the scores' product, where scores of 0 would make NaN of the rows
-        // before it as well; those after it get theirs at the end.
-        if (kRows && j + 1 == C::kSlabs &&
-            ((some & 0x7f80u) == 0x7f80u || (some & 0x7f800000u) == 0x7f800000u)) {
-          for (int u = 0; u < kC / 16; ++u) {
-            const int row = 16 * u + r16;
-            uint32_t *word = reinterpret_cast<uint32_t *>(from + u * 2048);
-            for (int c = 0; c < 8; ++c) {
-              if ((word[c / 2] >> c % 2 * 16 & 0x7f80u) != 0x7f80u) continue;
-              word[c / 2] &= c % 2 ? 0xffffu : 0xffff0000u;
-              atomicMin(&s.bad[i & 1][atom * 64 + ch * 8 + c], reverse ? kC - 1 - row : row);
-              s.odd[i & 1] = 1;
-            }
-          }
-        }
         tc::fence_async_smem();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&s.slab_full);
       }
       if (!ok) break;
-      if (lane == 0) tc::mbar_arrive(kRows ? &s.checked[i & 1] : &s.vempty[i % C::kValues]);
-      if (!WAIT(s.u_full, i)) break;
+      if (lane == 0) tc::mbar_arrive(&s.vempty[i & 1]);
+      if (!(ok = WAIT(s.u_full, i))) break;
       tc::fence_after_sync();
       const Factor f = n == kC ? whole : decay_power(decay, n);
       const f2 hi = f2_bits(f.hi, f.hi), lo = f2_bits(f.lo, f.lo);
 #pragma unroll
-      for (int g = 0; g < C::kHalves; ++g) {
+      for (int g = 0; g < F::kHalves; ++g) {
         f2 u[16];
         tmem_ld_16x64(lanes + ((uint32_t)(16 * g) << 16), u);
-        if (g == C::kHalves - 1) {
+        if (g == F::kHalves - 1) {
           tc::fence_before_sync();
           __syncwarp();
           if (lane == 0) tc::mbar_arrive(&s.u_free);
@@ -506,41 +369,454 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, D == 64 ? 2 : 1)
 #pragma unroll
         for (int e = 0; e < 16; ++e) S[g][e] = madd2(S[g][e], hi, madd2(S[g][e], lo, u[e]));
       }
-      if (kRows && i + 1 < chunks) {
-        if (!WAIT(s.s_free, i)) break;
-        publish();
-      }
+      // A value that is not finite leaves NaN in its third part (some large finite ones leave bits
+      // that look like it: the rows' pass looks again).
+      const bool odd = (some & 0x7f80u) == 0x7f80u || (some & 0x7f800000u) == 0x7f800000u;
+      const bool any = __any_sync(0xffffffffu, odd);
+      if (lane == 0) *flag(i) = any;
     }
-    if (!kRows) {
-      save(slot(r + 1));
-    } else if (r == st.last && w.state_out) {
-      float *out = w.state_out + (size_t)blockIdx.y * D * D;
-      const int sr = w.transposed ? 1 : D, sc = w.transposed ? D : 1;
-      const float mul = 1.f / w.state_mul;
-      each([&](f2 &x, int row, int col) {
-        float *at = out + row * sr + col * sc;
-        at[0] = lo2(x) * mul;
-        at[sc] = hi2(x) * mul;
-      });
+    if (ok && chunks < to - from) {  // the last chunk: only the state before it
+      if (chunks) save(local(chunks));
+      if (lane == 0) *flag(chunks) = 1;
+    } else if (ok) {
+      save(p.slots + (bh * p.splits + r) * (D * D));
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == C::kMma) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, D);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// join
+// ---------------------------------------------------------------------------
+// Runs through the stretches in the sweep's order: a slot, what its stretch adds, becomes the
+// state before the stretch.  Four floats of a matrix a thread.
+template <int D>
+__global__ void __launch_bounds__(256) k16_join_kernel(const __grid_constant__ Params p) {
+  using F = Frags<D>;
+  const LinearSweep &w = p.a.sweep[blockIdx.z];
+  const int b = blockIdx.y / p.a.H, h = blockIdx.y % p.a.H;
+  const Band band(p, b);
+  const float decay = p.a.decay[h];
+  const int i = blockIdx.x * 256 + threadIdx.x, t = i % F::kThreads, g = i / F::kThreads / 8,
+            e = i / F::kThreads % 8 * 2;
+  const int row = F::row(t, g, e), col = F::col(t, e);
+  const int sr = w.transposed ? 1 : D, sc = w.transposed ? D : 1;
+  const size_t bh = (size_t)blockIdx.z * gridDim.y + blockIdx.y;
+  float4 *carry = reinterpret_cast<float4 *>(p.carry + bh * (D * D)) + i;
+  float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (!p.first) {
+    x = *carry;
+  } else if (w.state) {
+    const float *from = w.state + (size_t)blockIdx.y * (D * D) + row * sr + col * sc;
+    x = make_float4(from[0] * w.state_mul, from[sc] * w.state_mul, from[8 * sr] * w.state_mul,
+                    from[8 * sr + sc] * w.state_mul);
+  }
+  float4 *at = reinterpret_cast<float4 *>(p.slots + bh * p.splits * (D * D)) + i;
+  const int adds = band.stretches - (band.stretches && band.hi == band.chunks && !wants_last(p, w) ? 1 : 0);
+  constexpr int kAhead = 8;
+  for (int r0 = 0; r0 < band.stretches; r0 += kAhead) {
+    float4 y[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+      if (r0 + k < adds) y[k] = at[(size_t)(r0 + k) * (D * D / 4)];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int r = r0 + k;
+      if (r >= band.stretches) break;
+      at[(size_t)r * (D * D / 4)] = x;
+      if (r >= adds) break;
+      const Factor f = decay_power(decay, band.tokens(band.lo + r * band.per, band.end(r), w.reverse));
+      x = make_float4(f.times(x.x, y[k].x), f.times(x.y, y[k].y), f.times(x.z, y[k].z), f.times(x.w, y[k].w));
+    }
+  }
+  if (!p.last) {
+    *carry = x;
+  } else if (w.state_out) {
+    const float mul = 1.f / w.state_mul;
+    float *to = w.state_out + (size_t)blockIdx.y * (D * D) + row * sr + col * sc;
+    to[0] = x.x * mul;
+    to[sc] = x.y * mul;
+    to[8 * sr] = x.z * mul;
+    to[8 * sr + sc] = x.w * mul;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// rows
+// ---------------------------------------------------------------------------
+template <int D>
+struct RowCfg {
+  static constexpr int kAtoms = D / 64, kStateWarps = D / 16;
+  static constexpr int kTma = 8 + kStateWarps, kMma = kTma + 1, kThreads = 32 * (kTma + 4);
+  // registers a thread: at launch, then of the rows', states' and last four warps
+  static constexpr int kRegs = D == 64 ? 64 : 96, kRowRegs = D == 64 ? 64 : 80, kStateRegs = D == 64 ? 88 : 128,
+                       kLastRegs = 40;
+  static_assert(8 * kRowRegs + kStateWarps * kStateRegs + 4 * kLastRegs <= (12 + kStateWarps) * kRegs, "registers");
+  static constexpr uint32_t kTile = kAtoms * kAtom, kSPart = kAtoms * D * 128;  // q, k or v; one part of S
+  static constexpr uint32_t kQ = 0, kK = kTile, kV = 2 * kTile, kS = 4 * kTile, kBytes = kS + 2 * kSPart;
+  static constexpr uint32_t kScores = 0, kOut = kC, kCols = 256;  // TMEM columns
+};
+
+// What the rows' warps need of a head: lam^n times the scale; columns' factors (see there).
+struct Tables {
+  float scaled[kC + 4];
+  alignas(16) float cols[3][32];
+};
+
+// A block's run of chunks in the order (sweep, sequence, head, the band's chunks from the last to the
+// first: those whose states were written last come first out of the L2).
+struct Start {
+  int left, z, b, h, ci;
+};
+// By one warp: chunks of all sequences, then the place of this block's first.
+__device__ __forceinline__ Start find_start(const Params &p, int lane) {
+  Start s{0, 0, 0, 0, -1};
+  const int H = p.a.H;
+  auto chunks = [&](int b) {
+    if (b >= p.a.batch) return 0;
+    const Band band(p, b);
+    return band.hi - band.lo;
+  };
+  auto sum = [](long long x) {
+#pragma unroll
+    for (int m = 16; m > 0; m /= 2) x += __shfl_xor_sync(0xffffffffu, x, m);
+    return x;
+  };
+  long long all = 0;
+  if (p.a.count) {
+    for (int b = lane; b < p.a.batch; b += 32) all += chunks(b);
+    all = sum(all);
+  } else {
+    all = (long long)chunks(0) * p.a.batch;
+  }
+  const long long total = all * H * p.a.sweeps;
+  long long at = total * blockIdx.x / gridDim.x;
+  s.left = (int)(total * (blockIdx.x + 1) / gridDim.x - at);
+  if (s.left <= 0) return s;
+  s.z = (int)(at / (all * H));
+  at -= s.z * all * H;
+  int n;
+  if (p.a.count) {
+    for (int b = 0;; b += 32) {  // (the place is in front of the last sequence's end)
+      const int mine = chunks(b + lane);
+      long long before = mine;
+#pragma unroll
+      for (int m = 1; m < 32; m *= 2) {
+        const long long x = __shfl_up_sync(0xffffffffu, before, m);
+        if (lane >= m) before += x;
+      }
+      const unsigned found = __ballot_sync(0xffffffffu, at < before * H);
+      if (found) {
+        const int k = __ffs(found) - 1;
+        n = __shfl_sync(0xffffffffu, mine, k);
+        at -= (__shfl_sync(0xffffffffu, before, k) - n) * H;
+        s.b = b + k;
+        break;
+      }
+      at -= __shfl_sync(0xffffffffu, before, 31) * H;
     }
   } else {
-    // (without rows too: the states' share counts on it)
+    n = chunks(0);
+    s.b = (int)(at / ((long long)n * H));
+    at -= (long long)s.b * n * H;
+  }
+  s.h = (int)(at / n);
+  s.ci = p.c0 + n - 1 - (int)(at % n);
+  return s;
+}
+
+struct Walk : Start {
+  const Params &p;
+  bool reverse;
+  __device__ __forceinline__ Walk(const Params &p_, const Start &s) : Start(s), p(p_), reverse(p_.a.sweep[s.z].reverse) {}
+  // the next chunk; whether its head is another
+  __device__ __forceinline__ bool next() {
+    if (--ci >= p.c0) return false;
+    if (++h == p.a.H) {
+      h = 0;
+      for (;;) {
+        if (++b == p.a.batch) b = 0, ++z;
+        if (z == p.a.sweeps) return true;  // (only behind the last chunk of all)
+        const Band band(p, b);
+        if (band.hi > band.lo) break;
+      }
+      reverse = p.a.sweep[z].reverse;
+    }
+    ci = Band(p, b).hi - 1;
+    return true;
+  }
+};
+
+struct RowShared {
+  uint64_t qfull, qempty, kfull, kempty, vfull[2], vempty[2];
+  uint64_t ready[2];  // S, tables and values: the states' warps may be a chunk ahead of the rows', not two
+  uint64_t s_free, scores, inter, parts, done, o_free, fin;
+  uint32_t tmem;
+  int odd[2];         // a chunk's values are not all finite
+  int bad[2][128];    // per column: the first such token in the sweep's order
+  Tables tables[2];
+  Start start;
+};
+
+// Warps:
+//   0-7       rows, two warps to 32 of them, each with half of the columns: scores to bf16
+//             parts in their own TMEM columns, Q S times the row's power in place, the
+//             finished rows by way of the values' place in shared memory (a TMA store: rows
+//             written by their own threads would be 32 places an instruction)
+//   8..       states (D / 16 warps): S from its two parts, split, into shared memory; the
+//             head's tables
+//   last four one for TMA loads (values a chunk ahead), one that issues the products
+// Heads of 64 leave room for two blocks an SM, which fill each other's waits; heads of 128
+// for one.
+template <int D>
+__global__ void __launch_bounds__(RowCfg<D>::kThreads, D == 64 ? 2 : 1)
+    k16_rows_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
+  using C = RowCfg<D>;
+  using F = Frags<D>;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char *smem = reinterpret_cast<unsigned char *>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ RowShared s;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+
+  if (threadIdx.x == 0) {
+    for (uint64_t *x : {&s.qfull, &s.qempty, &s.kfull, &s.kempty, &s.vfull[0], &s.vfull[1], &s.s_free,
+                        &s.scores, &s.inter, &s.done, &s.fin})
+      tc::mbar_init(x, 1);
+    for (uint64_t *x : {&s.ready[0], &s.ready[1]}) tc::mbar_init(x, C::kStateWarps);
+    for (uint64_t *x : {&s.vempty[0], &s.vempty[1], &s.parts, &s.o_free}) tc::mbar_init(x, 8);
+    tc::mbar_fence_init();
+    s.odd[0] = s.odd[1] = 0;
+  }
+  for (int i = threadIdx.x; i < 256; i += C::kThreads) s.bad[i / 128][i % 128] = kC;
+  if (warp == 0) {
+    const Start start = find_start(p, lane);
+    if (lane == 0) s.start = start;
+  }
+  if (warp == C::kMma) {
+    tc::tmem_alloc(&s.tmem, C::kCols);
+    tc::tmem_relinquish();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = s.tmem, base = smem_u32(smem);
+
+  if (warp >= C::kTma) {
+    tc::regs_dec<C::kLastRegs>();
+    if (warp == C::kTma && lane == 0) {
+      // ---------------------------------------------------------------- loads
+      Walk a(p, s.start), c(p, s.start);  // of q and k; of v, a chunk ahead
+      const int chunks = a.left;
+      auto load = [&](const Walk &u, uint32_t at, int which, uint64_t *bar) {
+        const LinearSweep &w = p.a.sweep[u.z];
+        const LinearRows &x = which == 0 ? w.q : which == 1 ? w.k : w.v;
+        const int m = p.map[u.z][which], t = Band(p, u.b).chunk(u.ci, u.reverse) * kC;
+        tc::mbar_arrive_expect_tx(bar, C::kTile);
+        for (int k = 0; k < C::kAtoms; ++k)
+          load_rows(smem + at + k * kAtom, &maps.in[m], bar, 64 * k, t, u.h / x.share * p.axes[m][1],
+                    u.b * p.axes[m][0]);
+      };
+      int nq = 0, nk = 0, nv = 0;  // loaded so far
+      bool ok = true;
+      auto load_v = [&]() {
+        if (!ok || nv >= chunks) return;
+        if (nv > 1 && !(ok = tc::mbar_wait(&s.vempty[nv & 1], (nv / 2 - 1) & 1, p.err))) return;
+        load(c, C::kV + (nv & 1) * C::kTile, 2, &s.vfull[nv & 1]);
+        ++nv;
+        c.next();
+      };
+      for (int i = 0; i < chunks && ok; ++i, a.next()) {
+        if (nk && !(ok = tc::mbar_wait(&s.kempty, (nk - 1) & 1, p.err))) break;
+        load(a, C::kK, 1, &s.kfull);
+        ++nk;
+        if (nq && !(ok = tc::mbar_wait(&s.qempty, (nq - 1) & 1, p.err))) break;
+        load(a, C::kQ, 0, &s.qfull);
+        ++nq;
+        if (i != 1) load_v();
+        if (i == 0) load_v();
+      }
+      // what is under way lands before the block ends
+      if (nq) tc::mbar_wait(&s.qfull, (nq - 1) & 1, nullptr);
+      if (nk) tc::mbar_wait(&s.kfull, (nk - 1) & 1, nullptr);
+      for (int i = nv > 2 ? nv - 2 : 0; i < nv; ++i) tc::mbar_wait(&s.vfull[i & 1], i / 2 & 1, nullptr);
+    } else if (warp == C::kMma && lane == 0) {
+      // ------------------------------------------------------------- products
+      constexpr uint32_t kQK = tc::idesc_bf16(128, 128, 0), kB = tc::idesc_bf16(128, D, 1);
+      const int chunks = s.start.left;
+      for (int i = 0; i < chunks; ++i) {
+        const uint32_t values = base + C::kV + (i & 1) * C::kTile;
+        if (!tc::mbar_wait(&s.kfull, i & 1, p.err) || !tc::mbar_wait(&s.qfull, i & 1, p.err)) break;
+        tc::fence_after_sync();
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+          tc::mma_ss(tmem + C::kScores, tc::desc_sw128(base + C::kQ + k / 4 * kAtom + k % 4 * 32),
+                     tc::desc_sw128(base + C::kK + k / 4 * kAtom + k % 4 * 32), kQK, k > 0);
+        tc::mma_commit(&s.scores);
+        tc::mma_commit(&s.kempty);
+        if (!tc::mbar_wait(&s.ready[i & 1], i >> 1 & 1, p.err) ||
+            (i && !tc::mbar_wait(&s.o_free, (i - 1) & 1, p.err)))
+          break;
+        tc::fence_after_sync();
+#pragma unroll
+        for (int k = 0; k < 2 * D / 16; ++k) {
+          const int kk = k % (D / 16), part = k / (D / 16);
+          tc::mma_ss(tmem + C::kOut, tc::desc_sw128(base + C::kQ + kk / 4 * kAtom + kk % 4 * 32),
+                     desc_blocks(base + C::kS + part * C::kSPart + kk * 2048, D * 128), kB, k > 0);
+        }
+        tc::mma_commit(&s.inter);
+        tc::mma_commit(&s.s_free);
+        tc::mma_commit(&s.qempty);
+        if (!tc::mbar_wait(&s.vfull[i & 1], i >> 1 & 1, p.err) || !tc::mbar_wait(&s.parts, i & 1, p.err)) break;
+        tc::fence_after_sync();
+#pragma unroll
+        for (int k = 0; k < 2 * kC / 16; ++k) {
+          const int kk = k % (kC / 16), part = k / (kC / 16);
+          tc::mma_ts(tmem + C::kOut, tmem + C::kScores + kk * 16 + part * 8, desc_blocks(values + kk * 2048, kAtom),
+                     kB, 1);
+        }
+        tc::mma_commit(&s.done);
+      }
+      tc::mma_commit(&s.fin);
+      tc::mbar_wait(&s.fin, 0, nullptr);
+    }
+  } else if (warp >= 8) {
+    tc::regs_inc<C::kStateRegs>();
+    // ------------------------------------------------------------------ states
+    const int t = threadIdx.x - 256;
+    // A lane names the row that it is to fill of one of four 8 x 8 blocks: rows + 0 and + 8 of
+    // two neighbours among the blocks of columns ([row][column], columns swizzled).
+    const uint32_t to = base + C::kS + F::col0(t) / 64 * (D * 128) +
+                        (F::row0(t) - lane / 4 + lane / 8 % 2 * 8 + lane % 8) * 128;
+    Walk u(p, s.start);
+    const int chunks = u.left;
+    int which = 0;             // of the tables
+    bool fresh = true;         // another head than the last chunk's
+    int stretch = -1;
+    f2 before[F::kHalves][16];  // the state before the stretch
+    for (int i = 0; i < chunks; ++i) {
+      const Band band(p, u.b);
+      const size_t bh = ((size_t)u.z * p.a.batch + u.b) * p.a.H + u.h;
+      const int r = (u.ci - band.lo) / band.per, from = band.lo + r * band.per;
+      const size_t nb = p.c1 - p.c0, place = u.ci - p.c0;
+      if (fresh || r != stretch) {
+        const float *at = p.slots + (bh * p.splits + r) * (D * D);
+#pragma unroll
+        for (int g = 0; g < F::kHalves; ++g)
+#pragma unroll
+          for (int e = 0; e < 16; e += 2) {
+            const ulonglong2 x = __ldg(reinterpret_cast<const ulonglong2 *>(at + F::at(t, g, e)));
+            before[g][e] = x.x, before[g][e + 1] = x.y;
+          }
+        stretch = r;
+      }
+      const bool own = u.ci > from;  // (the first chunk of a stretch has only the state before it)
+      const float *at = p.local + (bh * (nb - 1) + (own ? place - 1 : 0)) * (D * D);
+      ulonglong2 local[8];
+      auto fetch = [&](int g) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          local[e] = own ? __ldg(reinterpret_cast<const ulonglong2 *>(at + F::at(t, g, 2 * e))) : make_ulonglong2(0, 0);
+      };
+      fetch(0);
+      bool look;
+      if constexpr (D == 64) {
+        look = *reinterpret_cast<const uint32_t *>(p.odd + (bh * nb + place) * 8) != 0;
+      } else {
+        const uint2 x = *reinterpret_cast<const uint2 *>(p.odd + (bh * nb + place) * 8);
+        look = (x.x | x.y) != 0;
+      }
+      const float decay = p.a.decay[u.h];
+      const Factor f = decay_power(decay, band.tokens(from, u.ci, u.reverse));
+      const f2 hi = f2_bits(f.hi, f.hi), lo = f2_bits(f.lo, f.lo);
+      if (i && !WAIT(s.s_free, i - 1)) break;
+      if (fresh) {
+        which ^= 1;
+        Tables &tab = s.tables[which];
+        for (int k = t; k <= kC + 96; k += F::kThreads) {
+          const int n = k <= kC ? k : 32 * ((k - kC - 1) / 32 + 1) + (u.reverse ? (k - kC - 1) % 32 - 31 : -((k - kC - 1) % 32));
+          const Factor x = decay_power(decay, n);
+          if (k <= kC)
+            tab.scaled[k] = (x.hi + x.lo) * p.a.scale;
+          else
+            tab.cols[(k - kC - 1) / 32][(k - kC - 1) % 32] = x.hi + x.lo;
+        }
+      }
+#pragma unroll
+      for (int g = 0; g < F::kHalves; ++g) {
+        if (g) fetch(g);
+#pragma unroll
+        for (int e = 0; e < 16; e += 4) {
+          uint32_t a[4], c[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const f2 y = k % 2 ? local[e / 2 + k / 2].y : local[e / 2 + k / 2].x;
+            f2 x = madd2(before[g][e + k], hi, madd2(before[g][e + k], lo, y));
+            a[k] = split2(x);
+            c[k] = pack2(x);
+          }
+          const uint32_t spot = to + g * 16 * 128 + (((e / 2 + lane / 16) ^ (lane % 8)) << 4);
+          stmatrix4(spot, a);
+          stmatrix4(spot + C::kSPart, c);
+        }
+      }
+      const int n = band.size(band.chunk(u.ci, u.reverse));
+      if (n < kC || look) {
+        if (!WAIT(s.vfull[i & 1], i >> 1)) break;
+        unsigned char *values = smem + C::kV + (i & 1) * C::kTile;
+        for (int k = t; k < kC * (D / 8); k += F::kThreads) {
+          const int row = k / (D / 8), ch = k % (D / 8);
+          uint32_t *word = reinterpret_cast<uint32_t *>(values + ch / 8 * kAtom + swz128(row, ch % 8));
+          for (int j = 0; j < 4; ++j) {
+            if (row >= n) {  // what lies behind the sequence takes no part, whatever it is
+              word[j] = 0;
+              continue;
+            }
+            // A value that is not finite leaves the tile, where scores of 0 would make NaN of the rows
+            // before it as well; those after it get theirs at the end.
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+              if ((word[j] >> 16 * m & 0x7f80u) == 0x7f80u) {
+                word[j] &= m ? 0xffffu : 0xffff0000u;
+                atomicMin(&s.bad[i & 1][ch * 8 + 2 * j + m], u.reverse ? kC - 1 - row : row);
+                s.odd[i & 1] = 1;
+              }
+          }
+        }
+      }
+      tc::fence_async_smem();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&s.ready[i & 1]);
+      fresh = u.next();
+    }
+  } else {
     if constexpr (C::kRowRegs < C::kRegs) tc::regs_dec<C::kRowRegs>();
-    if constexpr (kRows) {
     // -------------------------------------------------------------------- rows
     // lam^|i - j| for 32 columns that all rows of the warp see is a factor of the row and
     // one of the column, counted from the warp's near edge, so that neither passes 1
     const int quarter = warp % 4, half = warp / 4, row = quarter * 32 + lane;
     const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
-    const float rowf = s.scaled[reverse ? 31 - lane : lane];
-    const f2 rowff = f2_bits(rowf, rowf);
-    const CUtensorMap *map = &maps.out[blockIdx.z];
-    const int mh = h * p.out_axes[blockIdx.z][1], mb = b * p.out_axes[blockIdx.z][0];
+    Walk u(p, s.start);
+    const int chunks = u.left;
+    int which = 0;
+    bool fresh = true;
     bool storing = false;  // (lane 0) a store may still read the values' place
     for (int i = 0; i < chunks; ++i) {
-      const int chunk = st.chunk(st.from + i, reverse), n = st.size(chunk);
-      if (!WAIT(s.scores, i)) break;
+      const Band band(p, u.b);
+      const LinearSweep &w = p.a.sweep[u.z];
+      const bool reverse = u.reverse;
+      const int chunk = band.chunk(u.ci, reverse), n = band.size(chunk);
+      if (fresh) which ^= 1;
+      if (!WAIT(s.ready[i & 1], i >> 1) || !WAIT(s.scores, i)) break;
       tc::fence_after_sync();
+      const Tables &tab = s.tables[which];
+      const float rowf = tab.scaled[reverse ? 31 - lane : lane];
+      const f2 rowff = f2_bits(rowf, rowf);
       const uint32_t at = lanes + C::kScores + 16 * half;
 #pragma unroll 1
       for (int c = 0; c < 4; ++c) {
@@ -554,7 +830,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, D == 64 ? 2 : 1)
           tc::tmem_ld16(at + 32 * c, x);
           tc::tmem_wait_ld();
           if (off > 0 && (!reverse || 32 * c + 32 <= n)) {
-            const ulonglong2 *cw = reinterpret_cast<const ulonglong2 *>(s.cols[off - 1] + 16 * half);
+            const ulonglong2 *cw = reinterpret_cast<const ulonglong2 *>(tab.cols[off - 1] + 16 * half);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const ulonglong2 f = cw[e];
@@ -573,7 +849,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, D == 64 ? 2 : 1)
               for (int k = 0; k < 2; ++k) {
                 const int j = 32 * c + 16 * half + 2 * e + k, lag = reverse ? j - row : row - j;
                 const bool seen = lag >= 0 && (!reverse || j < n);
-                v[k] = seen ? __uint_as_float(x[2 * e + k]) * s.scaled[abs(lag)] : 0.f;
+                v[k] = seen ? __uint_as_float(x[2 * e + k]) * tab.scaled[abs(lag)] : 0.f;
               }
               f2 y = f2_bits(v[0], v[1]);
               parts[0][e] = split2(y);
@@ -586,14 +862,14 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, D == 64 ? 2 : 1)
       }
       if (i && lane == 0) {  // the last chunk's rows are on their way
         if (storing) bulk_wait_read<0>();
-        tc::mbar_arrive(&s.vempty[(i - 1) % C::kValues]);
+        tc::mbar_arrive(&s.vempty[(i - 1) & 1]);
       }
       __syncwarp();
       if (!WAIT(s.inter, i)) break;
       tc::fence_after_sync();
       const uint32_t out = lanes + C::kOut + half * (D / 2);
       {
-        const float f = s.scaled[reverse ? max(n - 1 - row, 0) : row + 1];
+        const float f = tab.scaled[reverse ? max(n - 1 - row, 0) : row + 1];
         const f2 ff = f2_bits(f, f);
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
@@ -613,14 +889,14 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, D == 64 ? 2 : 1)
       tc::fence_before_sync();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&s.parts);
-      if (!WAIT(s.checked[i & 1], i >> 1) || !WAIT(s.done, i)) break;
+      if (!WAIT(s.done, i)) break;
       tc::fence_after_sync();
       const bool odd = s.odd[i & 1] != 0;
       // whole warps of bf16 rows leave by TMA, 64 columns at a time; the last rows of a
       // sequence, and fp32 parts, from their threads
       const bool whole = 32 * quarter + 32 <= n && !w.out_f32;
-      unsigned char *box = smem + C::kV + i % C::kValues * C::kTile + (D == 64 ? 0 : half * kAtom) + quarter * 4096;
-      const long long to = b * w.os[0] + h * w.os[1] + (chunk * (long long)kC + row) * w.os[2] + half * (D / 2);
+      unsigned char *box = smem + C::kV + (i & 1) * C::kTile + (D == 64 ? 0 : half * kAtom) + quarter * 4096;
+      const long long to = u.b * w.os[0] + u.h * w.os[1] + (chunk * (long long)kC + row) * w.os[2] + half * (D / 2);
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
         uint32_t x[16];
@@ -672,7 +948,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, D == 64 ? 2 : 1)
         else
           __syncwarp();
         if (lane == 0 && (D == 128 || half == 0)) {
-          store_rows(box, map, D == 64 ? 0 : 64 * half, chunk * kC + 32 * quarter, mh, mb);
+          store_rows(box, &maps.out[u.z], D == 64 ? 0 : 64 * half, chunk * kC + 32 * quarter,
+                     u.h * p.out_axes[u.z][1], u.b * p.out_axes[u.z][0]);
           bulk_commit();
           storing = true;
         }
@@ -682,44 +959,15 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, D == 64 ? 2 : 1)
         if (warp < 4 && row < D) s.bad[i & 1][row] = kC;
         if (warp == 0 && lane == 0) s.odd[i & 1] = 0;
       }
+      fresh = u.next();
     }
     if (lane == 0) bulk_wait_read<0>();
-    }
   }
   tc::fence_before_sync();
   __syncthreads();
   if (warp == C::kMma) {
     tc::fence_after_sync();
-    tc::tmem_dealloc(tmem, kRows ? C::kCols : D);
-  }
-}
-
-// Runs through the stretches' states in the sweep's order: slot r, the state that stretch r - 1
-// alone adds (the first: with the given one), becomes the state before stretch r.
-template <int D>
-__global__ void __launch_bounds__(256) k16_join_kernel(const __grid_constant__ Params p) {
-  const int b = blockIdx.y / p.a.H, h = blockIdx.y % p.a.H;
-  const Stretch st(p, b, 0);
-  const bool reverse = p.a.sweep[blockIdx.z].reverse;
-  float4 *at = reinterpret_cast<float4 *>(
-                   p.states + ((size_t)blockIdx.z * gridDim.y + blockIdx.y) * p.splits * (D * D)) +
-               blockIdx.x * 256 + threadIdx.x;
-  if (st.last < 2) return;
-  constexpr int kAhead = 8;
-  float4 x = at[D * D / 4];
-  for (int r0 = 2; r0 <= st.last; r0 += kAhead) {
-    float4 y[kAhead];
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k)
-      if (r0 + k <= st.last) y[k] = at[(size_t)(r0 + k) * (D * D / 4)];
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      const int r = r0 + k;
-      if (r > st.last) break;
-      const Factor f = decay_power(p.a.decay[h], st.tokens((r - 1) * st.per, min(r * st.per, st.chunks), reverse));
-      x = make_float4(f.times(x.x, y[k].x), f.times(x.y, y[k].y), f.times(x.z, y[k].z), f.times(x.w, y[k].w));
-      at[(size_t)r * (D * D / 4)] = x;
-    }
+    tc::tmem_dealloc(tmem, C::kCols);
   }
 }
 
@@ -761,48 +1009,76 @@ bool make_map(CUtensorMap *map, const void *x, const long long (&s)[3], bool f32
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Stretches of a sweep: as many as blocks fit at once, eight chunks each at least.  (Below that the
-// two further launches and the second read of k and v cost what the shorter way saves: 8 x 16
-// heads of 333 tokens 33 us in two stretches, 20 in one.)
-int splits_of(int sweeps, int pairs, int T, int d) {
-  const int blocks = 152 * (d == 64 ? 2 : 1), most = (T + kC - 1) / kC / 8;
-  const int n = blocks / (sweeps * pairs < blocks ? sweeps * pairs : blocks);
-  return n < most ? n : most < 1 ? 1 : most;
+// Chunks of a band, and the stretches that they are cut into.
+struct Plan {
+  int chunks, band, splits;
+  size_t local, slots, carry, odd, total;  // bytes
+};
+constexpr size_t kBandBytes = (size_t)160 << 20;
+Plan plan_of(int sweeps, int pairs, int T, int d) {
+  Plan q;
+  const size_t matrix = (size_t)d * d * 4, all = (size_t)sweeps * pairs;
+  q.chunks = (T + kC - 1) / kC;
+  // bands of equal length whose states stay within kBandBytes
+  size_t most = kBandBytes / (all * matrix);
+  if (most < 1) most = 1;
+  const size_t bands = (q.chunks + most - 1) / most;
+  q.band = (int)((q.chunks + bands - 1) / bands);
+  const int blocks = 152 * (d == 64 ? StateCfg<64>::kBlocks : StateCfg<128>::kBlocks);
+  int n = (int)(blocks / (all < (size_t)blocks ? all : blocks));
+  const int longest = (q.band + 3) / 4;  // four chunks a stretch at least
+  q.splits = n < longest ? n : longest;
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  q.local = all * (q.band - 1) * matrix;
+  q.slots = all * q.splits * matrix;
+  q.carry = bands > 1 ? all * matrix : 0;
+  q.odd = up(all * q.band * 8);
+  q.total = q.local + q.slots + q.carry + q.odd;
+  return q;
 }
 
 template <int D>
-cudaError_t run(const Params &p, const Maps &m, cudaStream_t st) {
-  constexpr int kSmem = Cfg<D>::kBytes + 1024;
+cudaError_t run(Params &p, const Maps &m, const Plan &q, cudaStream_t st) {
+  auto states = k16_states_kernel<D>;
+  auto rows = k16_rows_kernel<D>;
+  constexpr int kStates = StateCfg<D>::kBytes + 1024, kRows = RowCfg<D>::kBytes + 1024;
+  cudaError_t e = cudaFuncSetAttribute(states, cudaFuncAttributeMaxDynamicSharedMemorySize, kStates);
+  if (e != cudaSuccess) return e;
+  if ((e = cudaFuncSetAttribute(rows, cudaFuncAttributeMaxDynamicSharedMemorySize, kRows)) != cudaSuccess) return e;
   const int pairs = p.a.batch * p.a.H;
-  if (p.splits > 1) {
-    auto f = k16_linear_kernel<D, false>;
-    cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-    if (e != cudaSuccess) return e;
-    f<<<dim3(p.splits - 1, pairs, p.a.sweeps), Cfg<D>::kThreads, kSmem, st>>>(m, p);
+  for (int c = 0; c < q.chunks; c += q.band) {
+    p.c0 = c;
+    p.c1 = c + q.band < q.chunks ? c + q.band : q.chunks;
+    p.first = c == 0;
+    p.last = p.c1 == q.chunks;
+    states<<<dim3(p.splits, pairs, p.a.sweeps), StateCfg<D>::kThreads, kStates, st>>>(m, p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     k16_join_kernel<D><<<dim3(D * D / 1024, pairs, p.a.sweeps), 256, 0, st>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    const long long units = (long long)p.a.sweeps * pairs * (p.c1 - p.c0), blocks = 152 * (D == 64 ? 2 : 1);
+    rows<<<(unsigned)(units < blocks ? units : blocks), RowCfg<D>::kThreads, kRows, st>>>(m, p);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
-  auto f = k16_linear_kernel<D, true>;
-  const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-  if (e != cudaSuccess) return e;
-  f<<<dim3(p.splits, pairs, p.a.sweeps), Cfg<D>::kThreads, kSmem, st>>>(m, p);
-  return cudaGetLastError();
+  return cudaSuccess;
 }
 
 }  // namespace
 
 size_t linear_chunk_bytes(int sweeps, int batch, int H, int T, int d) {
-  const int n = splits_of(sweeps, batch * H, T, d);
-  return n > 1 ? (size_t)sweeps * batch * H * n * d * d * 4 : 0;
+  return plan_of(sweeps, batch * H, T, d).total;
 }
 
-cudaError_t launch_linear_chunks(const LinearArgs &a, float *states, int *err, cudaStream_t st) {
+cudaError_t launch_linear_chunks(const LinearArgs &a, void *ws, int *err, cudaStream_t st) {
+  const Plan q = plan_of(a.sweeps, a.batch * a.H, a.T, a.d);
   Params p;
   memset(&p, 0, sizeof(p));
   p.a = a;
-  p.splits = splits_of(a.sweeps, a.batch * a.H, a.T, a.d);
-  p.states = states;
+  p.splits = q.splits;
+  char *at = static_cast<char *>(ws);
+  p.local = reinterpret_cast<float *>(at);
+  p.slots = reinterpret_cast<float *>(at + q.local);
+  p.carry = reinterpret_cast<float *>(at + q.local + q.slots);
+  p.odd = reinterpret_cast<uint8_t *>(at + q.local + q.slots + q.carry);
   p.err = err;
   // one map a tensor: the sweeps share theirs
   Maps maps;
@@ -830,7 +1106,7 @@ cudaError_t launch_linear_chunks(const LinearArgs &a, float *states, int *err, c
                   p.out_axes[i]))
       return cudaErrorInvalidValue;
   }
-  return a.d == 64 ? run<64>(p, maps, st) : run<128>(p, maps, st);
+  return a.d == 64 ? run<64>(p, maps, q, st) : run<128>(p, maps, q, st);
 }
 
 }  // namespace fs
