@@ -29,141 +29,12 @@
 // by going through long sequences in bands.
 //
 // What bounds it: XX
-#include <cuda.h>
-#include <string.h>
-
-#include "fs_common.cuh"
-#include "fs_internal.h"
-#include "linear.cuh"
-#include "pairs.cuh"
-#include "tc05.cuh"
+#include "linear_tc.cuh"
 
 namespace fs {
 namespace {
 
-constexpr int kC = 128;               // tokens of a chunk
-constexpr uint32_t kAtom = kC * 128;  // bytes of 64 elements of a chunk's rows
-
-// A band: the chunks [c0, c1) of every sequence, in the sweep's order.
-struct Params {
-  LinearArgs a;
-  int c0, c1;
-  bool first, last;   // band
-  int splits;         // stretches of a band
-  float *local;       // [sweep, batch H, c1 - c0 - 1, D D]: the state before each chunk but the band's
-                      // first, of its stretch alone (none before a stretch's first)
-  float *slots;       // [sweep, batch H, splits, D D]: what each stretch adds; then the state before it
-  float *carry;       // [sweep, batch H, D D]: the state behind the band
-  uint8_t *odd;       // [sweep, batch H, c1 - c0, 8]: not all of the values that a warp of the states'
-                      // kernel saw of the chunk are finite
-  int map[3][3];      // which map holds q, k, v of a sweep
-  int axes[4][2];     // 0 where a map's sequences or heads are one
-  int out_axes[3][2];
-  int *err;
-};
-
-struct Maps {
-  CUtensorMap in[4], out[3];
-};
-
-// A sequence's part of the band: chunks [lo, hi) of `chunks`, in stretches of `per`.
-struct Band {
-  int n, chunks, lo, hi, per, stretches;
-  __device__ __forceinline__ Band(const Params &p, int b) {
-    n = p.a.count ? min(max(p.a.count[b], 0), p.a.T) : p.a.T;
-    chunks = (n + kC - 1) / kC;
-    lo = p.c0;
-    hi = max(min(p.c1, chunks), lo);
-    per = max((hi - lo + p.splits - 1) / p.splits, 1);
-    stretches = (hi - lo + per - 1) / per;
-  }
-  __device__ __forceinline__ int chunk(int i, bool reverse) const { return reverse ? chunks - 1 - i : i; }
-  __device__ __forceinline__ int size(int chunk) const { return min(n - chunk * kC, kC); }
-  // tokens of the chunks [a, b) in the sweep's order: the sequence's last chunk may not be whole
-  __device__ __forceinline__ int tokens(int a, int b, bool reverse) const {
-    const int odd = chunks * kC - n;
-    return (b - a) * kC - (b > a && (reverse ? a == 0 : b == chunks) ? odd : 0);
-  }
-  __device__ __forceinline__ int end(int r) const { return min(lo + (r + 1) * per, hi); }
-};
-// The last chunk of a sequence need not go into a state that nobody wants.
-__device__ __forceinline__ bool wants_last(const Params &p, const LinearSweep &w) {
-  return !p.last || w.state_out;
-}
-
-// How the states' warps hold a D x D matrix (and how it lies in memory between the passes): warp
-// w rows 16 (w % 4).. of 64 (32 (w % 4).. of 128) and columns 64 (w / 4).., a lane of each 8 x 8 block two
-// columns of one row.
-template <int D>
-struct Frags {
-  static constexpr int kWarps = D / 16, kThreads = 32 * kWarps;
-  static constexpr int kHalves = D / 64;  // groups of 16 rows that a warp holds
-  static __device__ __forceinline__ int row0(int t) { return (D == 64 ? t / 32 * 16 : t / 32 % 4 * 32) + t % 32 / 4; }
-  static __device__ __forceinline__ int col0(int t) { return (D == 64 ? 0 : t / 128 * 64) + t % 4 * 2; }
-  // pair e of group g: the row and the first column
-  static __device__ __forceinline__ int row(int t, int g, int e) { return row0(t) + 16 * g + e % 2 * 8; }
-  static __device__ __forceinline__ int col(int t, int e) { return col0(t) + e / 2 * 8; }
-  // floats from a matrix's start to pairs e and e + 1 (e even) of group g
-  static __device__ __forceinline__ int at(int t, int g, int e) { return ((g * 8 + e / 2) * kThreads + t) * 4; }
-};
-
-// tc::desc_sw128 for elements in several blocks of 64, `apart` bytes from one to the next.
-__device__ __forceinline__ uint64_t desc_blocks(uint32_t at, uint32_t apart) {
-  return (tc::desc_sw128(at) & ~(0x3fffull << 16)) | (uint64_t)(apart >> 4) << 16;
-}
-
-// 16 lanes x 64 columns, a warp's lane t holding of each eight columns 2 (t % 4) and the
-// next, in lanes t / 4 and t / 4 + 8.
-__device__ __forceinline__ void tmem_ld_16x64(uint32_t at, f2 (&r)[16]) {
-  uint32_t u[32];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
-      : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]),
-        "=r"(u[7]), "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]),
-        "=r"(u[14]), "=r"(u[15]), "=r"(u[16]), "=r"(u[17]), "=r"(u[18]), "=r"(u[19]),
-        "=r"(u[20]), "=r"(u[21]), "=r"(u[22]), "=r"(u[23]), "=r"(u[24]), "=r"(u[25]),
-        "=r"(u[26]), "=r"(u[27]), "=r"(u[28]), "=r"(u[29]), "=r"(u[30]), "=r"(u[31])
-      : "r"(at));
-  tc::tmem_wait_ld();
-#pragma unroll
-  for (int i = 0; i < 16; ++i) r[i] = (f2)u[2 * i] | (f2)u[2 * i + 1] << 32;
-}
-
-// The 64 x 128 box of a map at token t of head h of sequence b.
-__device__ __forceinline__ void load_rows(void *dst, const void *map, uint64_t *bar, int x, int t,
-                                          int h, int b) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, "
-      "{%3, %4, %5, %6}], [%2];\n" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(t), "r"(h), "r"(b)
-      : "memory");
-}
-
-// The other way, of `map`'s box size; for bulk_commit and bulk_wait_read of the same thread.
-__device__ __forceinline__ void store_rows(const void *src, const void *map, int x, int t, int h, int b) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%2, %3, %4, %5}], [%1];\n" ::"l"(
-          reinterpret_cast<uint64_t>(map)),
-      "r"(smem_u32(src)), "r"(x), "r"(t), "r"(h), "r"(b)
-      : "memory");
-}
-__device__ __forceinline__ void bulk_commit() {
-  asm volatile("cp.async.bulk.commit_group;\n" ::: "memory");
-}
-template <int N>
-__device__ __forceinline__ void bulk_wait_read() {
-  asm volatile("cp.async.bulk.wait_group.read %0;\n" ::"n"(N) : "memory");
-}
-
-__device__ __forceinline__ void stmatrix4(uint32_t at, const uint32_t (&r)[4]) {
-  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1,%2,%3,%4};\n" ::"r"(at), "r"(r[0]),
-               "r"(r[1]), "r"(r[2]), "r"(r[3])
-               : "memory");
-}
-
-#define WAIT(bar, k) __all_sync(0xffffffffu, tc::mbar_wait(&(bar), (k) & 1, p.err))
+using namespace lin;
 
 // ---------------------------------------------------------------------------
 // states
@@ -202,7 +73,8 @@ __global__ void __launch_bounds__(StateCfg<D>::kThreads, StateCfg<D>::kBlocks)
   const int b = blockIdx.y / p.a.H, h = blockIdx.y % p.a.H, r = blockIdx.x;
   const Band band(p, b);
   const bool reverse = w.reverse;
-  if (r >= band.stretches) return;
+  // (fused: nobody starts from the last stretch's)
+  if (r >= band.stretches - (p.fused ? 1 : 0)) return;
   const int from = band.lo + r * band.per, to = band.end(r);
   const int chunks = to - from - (to == band.chunks && !wants_last(p, w) ? 1 : 0);
   const float decay = p.a.decay[h];
@@ -307,7 +179,7 @@ __global__ void __launch_bounds__(StateCfg<D>::kThreads, StateCfg<D>::kBlocks)
       const int n = band.size(band.chunk(from + i, reverse));
       unsigned char *values = smem + C::kV + (i & 1) * C::kTile;
       if (!(ok = WAIT(s.vfull[i & 1], i / 2))) break;
-      if (i) save(local(i));
+      if (i && !p.fused) save(local(i));
       if (n < kC) {
         // what lies behind the sequence takes no part, whatever it is
         if (!(ok = WAIT(s.kfull, i))) break;
@@ -373,7 +245,7 @@ __global__ void __launch_bounds__(StateCfg<D>::kThreads, StateCfg<D>::kBlocks)
       // that look like it: the rows' pass looks again).
       const bool odd = (some & 0x7f80u) == 0x7f80u || (some & 0x7f800000u) == 0x7f800000u;
       const bool any = __any_sync(0xffffffffu, odd);
-      if (lane == 0) *flag(i) = any;
+      if (lane == 0 && !p.fused) *flag(i) = any;
     }
     if (ok && chunks < to - from) {  // the last chunk: only the state before it
       if (chunks) save(local(chunks));
@@ -417,6 +289,7 @@ __global__ void __launch_bounds__(256) k16_join_kernel(const __grid_constant__ P
                     from[8 * sr + sc] * w.state_mul);
   }
   float4 *at = reinterpret_cast<float4 *>(p.slots + bh * p.splits * (D * D)) + i;
+  // (the last stretch of a sequence: not where nobody wants the state behind it)
   const int adds = band.stretches - (band.stretches && band.hi == band.chunks && !wants_last(p, w) ? 1 : 0);
   constexpr int kAhead = 8;
   for (int r0 = 0; r0 < band.stretches; r0 += kAhead) {
@@ -436,7 +309,7 @@ __global__ void __launch_bounds__(256) k16_join_kernel(const __grid_constant__ P
   }
   if (!p.last) {
     *carry = x;
-  } else if (w.state_out) {
+  } else if (w.state_out && !p.fused) {
     const float mul = 1.f / w.state_mul;
     float *to = w.state_out + (size_t)blockIdx.y * (D * D) + row * sr + col * sc;
     to[0] = x.x * mul;
@@ -449,23 +322,15 @@ __global__ void __launch_bounds__(256) k16_join_kernel(const __grid_constant__ P
 // ---------------------------------------------------------------------------
 // rows
 // ---------------------------------------------------------------------------
-template <int D>
 struct RowCfg {
-  static constexpr int kAtoms = D / 64, kStateWarps = D / 16;
+  static constexpr int D = 64, kStateWarps = D / 16;
   static constexpr int kTma = 8 + kStateWarps, kMma = kTma + 1, kThreads = 32 * (kTma + 4);
-  // registers a thread: at launch, then of the rows', states' and last four warps
-  static constexpr int kRegs = D == 64 ? 64 : 96, kRowRegs = D == 64 ? 64 : 80, kStateRegs = D == 64 ? 88 : 128,
-                       kLastRegs = 40;
-  static_assert(8 * kRowRegs + kStateWarps * kStateRegs + 4 * kLastRegs <= (12 + kStateWarps) * kRegs, "registers");
-  static constexpr uint32_t kTile = kAtoms * kAtom, kSPart = kAtoms * D * 128;  // q, k or v; one part of S
+  // registers a thread: at launch and the rows', then the states' and the last four warps'
+  static constexpr int kRegs = 64, kStateRegs = 88, kLastRegs = 40;
+  static_assert(8 * kRegs + kStateWarps * kStateRegs + 4 * kLastRegs <= (12 + kStateWarps) * kRegs, "registers");
+  static constexpr uint32_t kTile = kAtom, kSPart = D * 128;  // q, k or v; one part of S
   static constexpr uint32_t kQ = 0, kK = kTile, kV = 2 * kTile, kS = 4 * kTile, kBytes = kS + 2 * kSPart;
   static constexpr uint32_t kScores = 0, kOut = kC, kCols = 256;  // TMEM columns
-};
-
-// What the rows' warps need of a head: lam^n times the scale; columns' factors (see there).
-struct Tables {
-  float scaled[kC + 4];
-  alignas(16) float cols[3][32];
 };
 
 // A block's run of chunks in the order (sweep, sequence, head, the band's chunks from the last to the
@@ -533,7 +398,9 @@ __device__ __forceinline__ Start find_start(const Params &p, int lane) {
 struct Walk : Start {
   const Params &p;
   bool reverse;
-  __device__ __forceinline__ Walk(const Params &p_, const Start &s) : Start(s), p(p_), reverse(p_.a.sweep[s.z].reverse) {}
+  Band band;
+  __device__ __forceinline__ Walk(const Params &p_, const Start &s)
+      : Start(s), p(p_), reverse(p_.a.sweep[s.z].reverse), band(p_, s.b) {}
   // the next chunk; whether its head is another
   __device__ __forceinline__ bool next() {
     if (--ci >= p.c0) return false;
@@ -542,12 +409,12 @@ struct Walk : Start {
       for (;;) {
         if (++b == p.a.batch) b = 0, ++z;
         if (z == p.a.sweeps) return true;  // (only behind the last chunk of all)
-        const Band band(p, b);
+        band = Band(p, b);
         if (band.hi > band.lo) break;
       }
       reverse = p.a.sweep[z].reverse;
     }
-    ci = Band(p, b).hi - 1;
+    ci = band.hi - 1;
     return true;
   }
 };
@@ -573,10 +440,10 @@ struct RowShared {
 //   last four one for TMA loads (values a chunk ahead), one that issues the products
 // Heads of 64 leave room for two blocks an SM, which fill each other's waits; heads of 128
 // for one.
-template <int D>
-__global__ void __launch_bounds__(RowCfg<D>::kThreads, D == 64 ? 2 : 1)
+__global__ void __launch_bounds__(RowCfg::kThreads, 2)
     k16_rows_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
-  using C = RowCfg<D>;
+  using C = RowCfg;
+  constexpr int D = C::D;
   using F = Frags<D>;
   extern __shared__ unsigned char smem_raw[];
   unsigned char *smem = reinterpret_cast<unsigned char *>(
@@ -611,35 +478,26 @@ __global__ void __launch_bounds__(RowCfg<D>::kThreads, D == 64 ? 2 : 1)
     tc::regs_dec<C::kLastRegs>();
     if (warp == C::kTma && lane == 0) {
       // ---------------------------------------------------------------- loads
-      Walk a(p, s.start), c(p, s.start);  // of q and k; of v, a chunk ahead
+      Walk a(p, s.start);
       const int chunks = a.left;
       auto load = [&](const Walk &u, uint32_t at, int which, uint64_t *bar) {
         const LinearSweep &w = p.a.sweep[u.z];
         const LinearRows &x = which == 0 ? w.q : which == 1 ? w.k : w.v;
-        const int m = p.map[u.z][which], t = Band(p, u.b).chunk(u.ci, u.reverse) * kC;
+        const int m = p.map[u.z][which], t = u.band.chunk(u.ci, u.reverse) * kC;
         tc::mbar_arrive_expect_tx(bar, C::kTile);
-        for (int k = 0; k < C::kAtoms; ++k)
-          load_rows(smem + at + k * kAtom, &maps.in[m], bar, 64 * k, t, u.h / x.share * p.axes[m][1],
-                    u.b * p.axes[m][0]);
+        load_rows(smem + at, &maps.in[m], bar, 0, t, u.h / x.share * p.axes[m][1], u.b * p.axes[m][0]);
       };
       int nq = 0, nk = 0, nv = 0;  // loaded so far
-      bool ok = true;
-      auto load_v = [&]() {
-        if (!ok || nv >= chunks) return;
-        if (nv > 1 && !(ok = tc::mbar_wait(&s.vempty[nv & 1], (nv / 2 - 1) & 1, p.err))) return;
-        load(c, C::kV + (nv & 1) * C::kTile, 2, &s.vfull[nv & 1]);
-        ++nv;
-        c.next();
-      };
-      for (int i = 0; i < chunks && ok; ++i, a.next()) {
-        if (nk && !(ok = tc::mbar_wait(&s.kempty, (nk - 1) & 1, p.err))) break;
+      for (; nv < chunks; a.next()) {
+        if (nk && !tc::mbar_wait(&s.kempty, (nk - 1) & 1, p.err)) break;
         load(a, C::kK, 1, &s.kfull);
         ++nk;
-        if (nq && !(ok = tc::mbar_wait(&s.qempty, (nq - 1) & 1, p.err))) break;
+        if (nq && !tc::mbar_wait(&s.qempty, (nq - 1) & 1, p.err)) break;
         load(a, C::kQ, 0, &s.qfull);
         ++nq;
-        if (i != 1) load_v();
-        if (i == 0) load_v();
+        if (nv > 1 && !tc::mbar_wait(&s.vempty[nv & 1], (nv / 2 - 1) & 1, p.err)) break;
+        load(a, C::kV + (nv & 1) * C::kTile, 2, &s.vfull[nv & 1]);
+        ++nv;
       }
       // what is under way lands before the block ends
       if (nq) tc::mbar_wait(&s.qfull, (nq - 1) & 1, nullptr);
@@ -689,81 +547,51 @@ __global__ void __launch_bounds__(RowCfg<D>::kThreads, D == 64 ? 2 : 1)
     tc::regs_inc<C::kStateRegs>();
     // ------------------------------------------------------------------ states
     const int t = threadIdx.x - 256;
-    // A lane names the row that it is to fill of one of four 8 x 8 blocks: rows + 0 and + 8 of
-    // two neighbours among the blocks of columns ([row][column], columns swizzled).
-    const uint32_t to = base + C::kS + F::col0(t) / 64 * (D * 128) +
-                        (F::row0(t) - lane / 4 + lane / 8 % 2 * 8 + lane % 8) * 128;
+    const Publisher<D> publisher(base + C::kS, t);
     Walk u(p, s.start);
     const int chunks = u.left;
     int which = 0;             // of the tables
     bool fresh = true;         // another head than the last chunk's
     int stretch = -1;
-    f2 before[F::kHalves][16];  // the state before the stretch
+    f2 before[16];             // the state before the stretch
     for (int i = 0; i < chunks; ++i) {
-      const Band band(p, u.b);
+      const Band &band = u.band;
       const size_t bh = ((size_t)u.z * p.a.batch + u.b) * p.a.H + u.h;
       const int r = (u.ci - band.lo) / band.per, from = band.lo + r * band.per;
       const size_t nb = p.c1 - p.c0, place = u.ci - p.c0;
       if (fresh || r != stretch) {
         const float *at = p.slots + (bh * p.splits + r) * (D * D);
 #pragma unroll
-        for (int g = 0; g < F::kHalves; ++g)
-#pragma unroll
-          for (int e = 0; e < 16; e += 2) {
-            const ulonglong2 x = __ldg(reinterpret_cast<const ulonglong2 *>(at + F::at(t, g, e)));
-            before[g][e] = x.x, before[g][e + 1] = x.y;
-          }
+        for (int e = 0; e < 16; e += 2) {
+          const ulonglong2 x = __ldg(reinterpret_cast<const ulonglong2 *>(at + F::at(t, 0, e)));
+          before[e] = x.x, before[e + 1] = x.y;
+        }
         stretch = r;
       }
       const bool own = u.ci > from;  // (the first chunk of a stretch has only the state before it)
       const float *at = p.local + (bh * (nb - 1) + (own ? place - 1 : 0)) * (D * D);
       ulonglong2 local[8];
-      auto fetch = [&](int g) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          local[e] = own ? __ldg(reinterpret_cast<const ulonglong2 *>(at + F::at(t, g, 2 * e))) : make_ulonglong2(0, 0);
-      };
-      fetch(0);
-      bool look;
-      if constexpr (D == 64) {
-        look = *reinterpret_cast<const uint32_t *>(p.odd + (bh * nb + place) * 8) != 0;
-      } else {
-        const uint2 x = *reinterpret_cast<const uint2 *>(p.odd + (bh * nb + place) * 8);
-        look = (x.x | x.y) != 0;
-      }
+      for (int e = 0; e < 8; ++e)
+        local[e] = own ? __ldg(reinterpret_cast<const ulonglong2 *>(at + F::at(t, 0, 2 * e))) : make_ulonglong2(0, 0);
+      const bool look = *reinterpret_cast<const uint32_t *>(p.odd + (bh * nb + place) * 8) != 0;
       const float decay = p.a.decay[u.h];
       const Factor f = decay_power(decay, band.tokens(from, u.ci, u.reverse));
       const f2 hi = f2_bits(f.hi, f.hi), lo = f2_bits(f.lo, f.lo);
       if (i && !WAIT(s.s_free, i - 1)) break;
       if (fresh) {
         which ^= 1;
-        Tables &tab = s.tables[which];
-        for (int k = t; k <= kC + 96; k += F::kThreads) {
-          const int n = k <= kC ? k : 32 * ((k - kC - 1) / 32 + 1) + (u.reverse ? (k - kC - 1) % 32 - 31 : -((k - kC - 1) % 32));
-          const Factor x = decay_power(decay, n);
-          if (k <= kC)
-            tab.scaled[k] = (x.hi + x.lo) * p.a.scale;
-          else
-            tab.cols[(k - kC - 1) / 32][(k - kC - 1) % 32] = x.hi + x.lo;
-        }
+        fill_tables(s.tables[which], decay, u.reverse, p.a.scale, t, F::kThreads);
       }
 #pragma unroll
-      for (int g = 0; g < F::kHalves; ++g) {
-        if (g) fetch(g);
+      for (int e = 0; e < 16; e += 4) {
+        f2 x[4];
 #pragma unroll
-        for (int e = 0; e < 16; e += 4) {
-          uint32_t a[4], c[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const f2 y = k % 2 ? local[e / 2 + k / 2].y : local[e / 2 + k / 2].x;
-            f2 x = madd2(before[g][e + k], hi, madd2(before[g][e + k], lo, y));
-            a[k] = split2(x);
-            c[k] = pack2(x);
-          }
-          const uint32_t spot = to + g * 16 * 128 + (((e / 2 + lane / 16) ^ (lane % 8)) << 4);
-          stmatrix4(spot, a);
-          stmatrix4(spot + C::kSPart, c);
+        for (int k = 0; k < 4; ++k) {
+          const f2 y = k % 2 ? local[e / 2 + k / 2].y : local[e / 2 + k / 2].x;
+          x[k] = madd2(before[e + k], hi, madd2(before[e + k], lo, y));
         }
+        publisher.put(0, e, x);
       }
       const int n = band.size(band.chunk(u.ci, u.reverse));
       if (n < kC || look) {
@@ -771,7 +599,7 @@ __global__ void __launch_bounds__(RowCfg<D>::kThreads, D == 64 ? 2 : 1)
         unsigned char *values = smem + C::kV + (i & 1) * C::kTile;
         for (int k = t; k < kC * (D / 8); k += F::kThreads) {
           const int row = k / (D / 8), ch = k % (D / 8);
-          uint32_t *word = reinterpret_cast<uint32_t *>(values + ch / 8 * kAtom + swz128(row, ch % 8));
+          uint32_t *word = reinterpret_cast<uint32_t *>(values + swz128(row, ch));
           for (int j = 0; j < 4; ++j) {
             if (row >= n) {  // what lies behind the sequence takes no part, whatever it is
               word[j] = 0;
@@ -795,71 +623,21 @@ __global__ void __launch_bounds__(RowCfg<D>::kThreads, D == 64 ? 2 : 1)
       fresh = u.next();
     }
   } else {
-    if constexpr (C::kRowRegs < C::kRegs) tc::regs_dec<C::kRowRegs>();
     // -------------------------------------------------------------------- rows
-    // lam^|i - j| for 32 columns that all rows of the warp see is a factor of the row and
-    // one of the column, counted from the warp's near edge, so that neither passes 1
-    const int quarter = warp % 4, half = warp / 4, row = quarter * 32 + lane;
-    const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
+    const RowWarp<D> rows(warp, lane, tmem + C::kScores, tmem + C::kOut);
     Walk u(p, s.start);
     const int chunks = u.left;
     int which = 0;
     bool fresh = true;
     bool storing = false;  // (lane 0) a store may still read the values' place
     for (int i = 0; i < chunks; ++i) {
-      const Band band(p, u.b);
-      const LinearSweep &w = p.a.sweep[u.z];
       const bool reverse = u.reverse;
-      const int chunk = band.chunk(u.ci, reverse), n = band.size(chunk);
+      const int chunk = u.band.chunk(u.ci, reverse), n = u.band.size(chunk);
       if (fresh) which ^= 1;
       if (!WAIT(s.ready[i & 1], i >> 1) || !WAIT(s.scores, i)) break;
       tc::fence_after_sync();
       const Tables &tab = s.tables[which];
-      const float rowf = tab.scaled[reverse ? 31 - lane : lane];
-      const f2 rowff = f2_bits(rowf, rowf);
-      const uint32_t at = lanes + C::kScores + 16 * half;
-#pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
-        uint32_t parts[2][8];
-        const int off = reverse ? c - quarter : quarter - c;
-        if (off < 0) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) parts[0][e] = parts[1][e] = 0;
-        } else {
-          uint32_t x[16];
-          tc::tmem_ld16(at + 32 * c, x);
-          tc::tmem_wait_ld();
-          if (off > 0 && (!reverse || 32 * c + 32 <= n)) {
-            const ulonglong2 *cw = reinterpret_cast<const ulonglong2 *>(tab.cols[off - 1] + 16 * half);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const ulonglong2 f = cw[e];
-              f2 y = mul2(mul2((f2)x[4 * e] | (f2)x[4 * e + 1] << 32, f.x), rowff);
-              f2 z = mul2(mul2((f2)x[4 * e + 2] | (f2)x[4 * e + 3] << 32, f.y), rowff);
-              parts[0][2 * e] = split2(y);
-              parts[1][2 * e] = pack2(y);
-              parts[0][2 * e + 1] = split2(z);
-              parts[1][2 * e + 1] = pack2(z);
-            }
-          } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              float v[2];
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                const int j = 32 * c + 16 * half + 2 * e + k, lag = reverse ? j - row : row - j;
-                const bool seen = lag >= 0 && (!reverse || j < n);
-                v[k] = seen ? __uint_as_float(x[2 * e + k]) * tab.scaled[abs(lag)] : 0.f;
-              }
-              f2 y = f2_bits(v[0], v[1]);
-              parts[0][e] = split2(y);
-              parts[1][e] = pack2(y);
-            }
-          }
-        }
-        tc::tmem_st8(at + 32 * c, parts[0]);
-        tc::tmem_st8(at + 32 * c + 8, parts[1]);
-      }
+      rows.parts(tab, reverse, n);
       if (i && lane == 0) {  // the last chunk's rows are on their way
         if (storing) bulk_wait_read<0>();
         tc::mbar_arrive(&s.vempty[(i - 1) & 1]);
@@ -867,96 +645,18 @@ __global__ void __launch_bounds__(RowCfg<D>::kThreads, D == 64 ? 2 : 1)
       __syncwarp();
       if (!WAIT(s.inter, i)) break;
       tc::fence_after_sync();
-      const uint32_t out = lanes + C::kOut + half * (D / 2);
-      {
-        const float f = tab.scaled[reverse ? max(n - 1 - row, 0) : row + 1];
-        const f2 ff = f2_bits(f, f);
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t x[16];
-          tc::tmem_ld16(out + 16 * c, x);
-          tc::tmem_wait_ld();
-#pragma unroll
-          for (int e = 0; e < 16; e += 2) {
-            const f2 y = mul2((f2)x[e] | (f2)x[e + 1] << 32, ff);
-            x[e] = (uint32_t)y;
-            x[e + 1] = (uint32_t)(y >> 32);
-          }
-          tc::tmem_st16(out + 16 * c, x);
-        }
-      }
-      tc::tmem_wait_st();
+      rows.weigh(tab, reverse, n);
       tc::fence_before_sync();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&s.parts);
       if (!WAIT(s.done, i)) break;
       tc::fence_after_sync();
       const bool odd = s.odd[i & 1] != 0;
-      // whole warps of bf16 rows leave by TMA, 64 columns at a time; the last rows of a
-      // sequence, and fp32 parts, from their threads
-      const bool whole = 32 * quarter + 32 <= n && !w.out_f32;
-      unsigned char *box = smem + C::kV + (i & 1) * C::kTile + (D == 64 ? 0 : half * kAtom) + quarter * 4096;
-      const long long to = u.b * w.os[0] + u.h * w.os[1] + (chunk * (long long)kC + row) * w.os[2] + half * (D / 2);
-#pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t x[16];
-        tc::tmem_ld16(out + 16 * c, x);
-        tc::tmem_wait_ld();
-        if (c == D / 32 - 1) {
-          tc::fence_before_sync();
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&s.o_free);
-        }
-        if (odd) {
-#pragma unroll 1
-          for (int e = 0; e < 16; ++e) {
-            const bool bad = s.bad[i & 1][half * (D / 2) + 16 * c + e] <= (reverse ? kC - 1 - row : row);
-#pragma unroll
-            for (int k = 0; k < 16; ++k)
-              if (k == e && bad) x[k] = 0x7fc00000u;
-          }
-        }
-        if (w.out_f32) {
-          if (row < n)
-#pragma unroll
-            for (int e = 0; e < 16; e += 8)
-              asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
-                               static_cast<float *>(w.out) + to + 16 * c + e),
-                           "r"(x[e]), "r"(x[e + 1]), "r"(x[e + 2]), "r"(x[e + 3]), "r"(x[e + 4]), "r"(x[e + 5]),
-                           "r"(x[e + 6]), "r"(x[e + 7])
-                           : "memory");
-          continue;
-        }
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          uint32_t y[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            y[k] = pack_bf16(__uint_as_float(x[8 * e + 2 * k]), __uint_as_float(x[8 * e + 2 * k + 1]));
-          const uint4 z = make_uint4(y[0], y[1], y[2], y[3]);
-          if (whole)
-            *reinterpret_cast<uint4 *>(box + swz128(lane, (D == 64 ? 4 * half : 0) + 2 * c + e)) = z;
-          else if (row < n)
-            *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(w.out) + to + 16 * c + 8 * e) = z;
-        }
-      }
-      storing = false;
-      if (whole) {
-        tc::fence_async_smem();
-        if (D == 64)  // two warps' halves of one box
-          asm volatile("bar.sync %0, 64;" ::"r"(3 + quarter) : "memory");
-        else
-          __syncwarp();
-        if (lane == 0 && (D == 128 || half == 0)) {
-          store_rows(box, &maps.out[u.z], D == 64 ? 0 : 64 * half, chunk * kC + 32 * quarter,
-                     u.h * p.out_axes[u.z][1], u.b * p.out_axes[u.z][0]);
-          bulk_commit();
-          storing = true;
-        }
-      }
+      storing = rows.store(p.a.sweep[u.z], &maps.out[u.z], p.out_axes[u.z], u.b, u.h, chunk, n, reverse,
+                           odd ? s.bad[i & 1] : nullptr, smem + C::kV + (i & 1) * C::kTile, &s.o_free);
       if (odd) {  // clean for the chunk after the next
         asm volatile("bar.sync 2, 256;" ::: "memory");
-        if (warp < 4 && row < D) s.bad[i & 1][row] = kC;
+        if (warp < 4 && rows.row < D) s.bad[i & 1][rows.row] = kC;
         if (warp == 0 && lane == 0) s.odd[i & 1] = 0;
       }
       fresh = u.next();
@@ -1009,30 +709,38 @@ bool make_map(CUtensorMap *map, const void *x, const long long (&s)[3], bool f32
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Chunks of a band, and the stretches that they are cut into.
+// Which way, chunks of a band, and the stretches that they are cut into.
 struct Plan {
+  bool fused;
   int chunks, band, splits;
   size_t local, slots, carry, odd, total;  // bytes
 };
 constexpr size_t kBandBytes = (size_t)160 << 20;
 Plan plan_of(int sweeps, int pairs, int T, int d) {
-  Plan q;
+  Plan q{};
   const size_t matrix = (size_t)d * d * 4, all = (size_t)sweeps * pairs;
-  q.chunks = (T + kC - 1) / kC;
+  q.chunks = q.band = (T + kC - 1) / kC;
+  const size_t resident = 152 * (d == 64 ? 2 : 1);  // blocks of the fused kernel
+  q.fused = d == 128 || q.chunks < 8 || all >= resident;
+  if (q.fused) {
+    // Stretches of eight chunks at least, some four blocks to a place, so that the long and the short
+    // even out.
+    const size_t n = all >= 2 * resident ? 1 : 4 * resident / all, most = q.chunks / 8;
+    q.splits = (int)(n < most ? n : most < 1 ? 1 : most);
+    q.slots = q.splits > 1 ? all * q.splits * matrix : 0;
+    q.total = q.slots;
+    return q;
+  }
   // bands of equal length whose states stay within kBandBytes
-  size_t most = kBandBytes / (all * matrix);
-  if (most < 1) most = 1;
+  const size_t most = kBandBytes / (all * matrix) > 1 ? kBandBytes / (all * matrix) : 1;
   const size_t bands = (q.chunks + most - 1) / most;
   q.band = (int)((q.chunks + bands - 1) / bands);
-  const int blocks = 152 * (d == 64 ? StateCfg<64>::kBlocks : StateCfg<128>::kBlocks);
-  int n = (int)(blocks / (all < (size_t)blocks ? all : blocks));
-  const int longest = (q.band + 3) / 4;  // four chunks a stretch at least
-  q.splits = n < longest ? n : longest;
-  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  const size_t n = 152 * StateCfg<64>::kBlocks / all, longest = (q.band + 3) / 4;  // four chunks a stretch at least
+  q.splits = (int)(n < longest ? n : longest);
   q.local = all * (q.band - 1) * matrix;
   q.slots = all * q.splits * matrix;
   q.carry = bands > 1 ? all * matrix : 0;
-  q.odd = up(all * q.band * 8);
+  q.odd = (all * q.band * 8 + 255) / 256 * 256;
   q.total = q.local + q.slots + q.carry + q.odd;
   return q;
 }
@@ -1040,23 +748,27 @@ Plan plan_of(int sweeps, int pairs, int T, int d) {
 template <int D>
 cudaError_t run(Params &p, const Maps &m, const Plan &q, cudaStream_t st) {
   auto states = k16_states_kernel<D>;
-  auto rows = k16_rows_kernel<D>;
-  constexpr int kStates = StateCfg<D>::kBytes + 1024, kRows = RowCfg<D>::kBytes + 1024;
+  constexpr int kStates = StateCfg<D>::kBytes + 1024, kRows = RowCfg::kBytes + 1024;
   cudaError_t e = cudaFuncSetAttribute(states, cudaFuncAttributeMaxDynamicSharedMemorySize, kStates);
   if (e != cudaSuccess) return e;
-  if ((e = cudaFuncSetAttribute(rows, cudaFuncAttributeMaxDynamicSharedMemorySize, kRows)) != cudaSuccess) return e;
+  if ((e = cudaFuncSetAttribute(k16_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRows)) != cudaSuccess)
+    return e;
   const int pairs = p.a.batch * p.a.H;
+  p.fused = q.fused;
   for (int c = 0; c < q.chunks; c += q.band) {
     p.c0 = c;
     p.c1 = c + q.band < q.chunks ? c + q.band : q.chunks;
     p.first = c == 0;
     p.last = p.c1 == q.chunks;
-    states<<<dim3(p.splits, pairs, p.a.sweeps), StateCfg<D>::kThreads, kStates, st>>>(m, p);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    k16_join_kernel<D><<<dim3(D * D / 1024, pairs, p.a.sweeps), 256, 0, st>>>(p);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    const long long units = (long long)p.a.sweeps * pairs * (p.c1 - p.c0), blocks = 152 * (D == 64 ? 2 : 1);
-    rows<<<(unsigned)(units < blocks ? units : blocks), RowCfg<D>::kThreads, kRows, st>>>(m, p);
+    if (!q.fused || p.splits > 1) {
+      states<<<dim3(q.fused ? p.splits - 1 : p.splits, pairs, p.a.sweeps), StateCfg<D>::kThreads, kStates, st>>>(m, p);
+      if ((e = cudaGetLastError()) != cudaSuccess) return e;
+      k16_join_kernel<D><<<dim3(D * D / 1024, pairs, p.a.sweeps), 256, 0, st>>>(p);
+      if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    }
+    if (q.fused) return lin::launch_fused(p, m, st);
+    const long long units = (long long)p.a.sweeps * pairs * (p.c1 - p.c0), blocks = 152 * 2;
+    k16_rows_kernel<<<(unsigned)(units < blocks ? units : blocks), RowCfg::kThreads, kRows, st>>>(m, p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   return cudaSuccess;

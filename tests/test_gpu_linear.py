@@ -81,7 +81,8 @@ def check_forward(q, k, v, decay, S0, count, **kw):
 SHAPES = [(1, 1, 1, 1, 64), (2, 3, 1, 1, 128), (1, 2, 2, 2, 64), (3, 4, 2, 16, 64), (2, 2, 2, 17, 64),
           (1, 8, 8, 31, 128), (2, 8, 4, 63, 64), (2, 2, 1, 64, 128), (3, 2, 2, 65, 64), (2, 8, 2, 127, 128),
           (1, 8, 8, 128, 64), (4, 2, 2, 129, 64), (2, 4, 4, 129, 128), (3, 4, 1, 255, 64), (2, 8, 8, 300, 128),
-          (5, 3, 3, 511, 64), (1, 2, 2, 1000, 64), (1, 2, 1, 1025, 128)]
+          (5, 3, 3, 511, 64), (1, 2, 2, 1000, 64), (1, 2, 1, 1025, 128), (3, 2, 2, 1153, 64), (70, 2, 1, 1100, 64),
+          (2, 3, 3, 2305, 128)]
 
 
 @pytest.mark.parametrize("shape", SHAPES)
@@ -288,7 +289,7 @@ def test_a_stream_argument_and_two_calls_at_once():
     assert all(torch.equal(o, want) for pair in outs for o in pair)
 
 
-@pytest.mark.parametrize("B,H,T,d", [(1, 2, 20000, 64), (1, 1, 12345, 128), (300, 2, 130, 64)])
+@pytest.mark.parametrize("B,H,T,d", [(1, 2, 20000, 64), (1, 1, 12345, 128), (300, 2, 130, 64), (4, 32, 12000, 64)])
 def test_long_sequences_and_large_batches(B, H, T, d):
     # against the same call in pieces of 1111 tokens, each of which the small tests cover: states
     # agree as pieces do with the statement, outputs to two roundings and both calls' sums
