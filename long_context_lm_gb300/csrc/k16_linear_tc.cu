@@ -39,15 +39,16 @@ using namespace lin;
 // ---------------------------------------------------------------------------
 // states
 // ---------------------------------------------------------------------------
+// Heads of 128 are taken by two blocks, 64 columns (of v) each.
 template <int D>
 struct StateCfg {
-  static constexpr int kAtoms = D / 64, kWarps = D / 16;
+  static constexpr int kAtoms = D / 64, kParts = D / 64, kWarps = D / 16, kStateThreads = 32 * kWarps;
   static constexpr int kTma = kWarps, kMma = kWarps + 1, kThreads = 32 * (kWarps + 4);
-  static constexpr int kSlab = 32, kSlabs = kC / kSlab;  // tokens of a slab of weighted values
-  static constexpr uint32_t kSlabAtom = kSlab * 128;
-  static constexpr uint32_t kTile = kAtoms * kAtom, kPart = kAtoms * kSlabAtom;
-  static constexpr uint32_t kK = 0, kV = kTile, kSlab0 = 3 * kTile, kBytes = kSlab0 + 3 * kPart;
-  static constexpr int kBlocks = D == 64 ? 3 : 1;  // of an SM
+  static constexpr int kRows = kStateThreads / 8;              // rows that the threads take at once
+  static constexpr int kSlab = 2 * kRows, kSlabs = kC / kSlab;  // tokens of a slab of weighted values
+  static constexpr uint32_t kTile = kAtoms * kAtom, kPart = kSlab * 128;
+  static constexpr uint32_t kK = 0, kV = kTile, kSlab0 = kV + 2 * kAtom, kBytes = kSlab0 + 3 * kPart;
+  static constexpr int kBlocks = D == 64 ? 3 : 2;  // of an SM
 };
 
 struct StateShared {
@@ -58,7 +59,8 @@ struct StateShared {
 
 // Warps: D / 16 that make weighted values (the next slab's in registers while one is
 // multiplied) and hold S, then one for TMA loads (values a chunk ahead) and one that issues
-// the products.  A thread has 16 bytes of rows r and r + 16 of every slab.
+// the products.  A thread has 16 bytes of two rows of every slab, and in a state of 128 x 64 one of the two
+// groups of 16 rows that Frags gives a warp.
 template <int D>
 __global__ void __launch_bounds__(StateCfg<D>::kThreads, StateCfg<D>::kBlocks)
     k16_states_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
@@ -70,7 +72,8 @@ __global__ void __launch_bounds__(StateCfg<D>::kThreads, StateCfg<D>::kBlocks)
   __shared__ StateShared s;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const LinearSweep &w = p.a.sweep[blockIdx.z];
-  const int b = blockIdx.y / p.a.H, h = blockIdx.y % p.a.H, r = blockIdx.x;
+  const int b = blockIdx.y / p.a.H, h = blockIdx.y % p.a.H;
+  const int r = blockIdx.x / C::kParts, part0 = blockIdx.x % C::kParts;
   const Band band(p, b);
   const bool reverse = w.reverse;
   // (fused: nobody starts from the last stretch's)
@@ -90,7 +93,7 @@ __global__ void __launch_bounds__(StateCfg<D>::kThreads, StateCfg<D>::kBlocks)
     s.power[i] = f.hi + f.lo;
   }
   if (warp == C::kMma) {
-    tc::tmem_alloc(&s.tmem, D);
+    tc::tmem_alloc(&s.tmem, 64);
     tc::tmem_relinquish();
   }
   tc::fence_before_sync();
@@ -100,11 +103,12 @@ __global__ void __launch_bounds__(StateCfg<D>::kThreads, StateCfg<D>::kBlocks)
 
   if (warp == C::kTma && lane == 0) {
     const int mk = p.map[blockIdx.z][1], mv = p.map[blockIdx.z][2];
-    auto load = [&](uint32_t at, int m, const LinearRows &x, uint64_t *bar, int i) {
+    // `atoms` times 64 columns from column x0 on
+    auto load = [&](uint32_t at, int m, const LinearRows &x, uint64_t *bar, int i, int x0, int atoms) {
       const int t = band.chunk(from + i, reverse) * kC;
-      tc::mbar_arrive_expect_tx(bar, C::kTile);
-      for (int k = 0; k < C::kAtoms; ++k)
-        load_rows(smem + at + k * kAtom, &maps.in[m], bar, 64 * k, t, h / x.share * p.axes[m][1],
+      tc::mbar_arrive_expect_tx(bar, atoms * kAtom);
+      for (int k = 0; k < atoms; ++k)
+        load_rows(smem + at + k * kAtom, &maps.in[m], bar, x0 + 64 * k, t, h / x.share * p.axes[m][1],
                   b * p.axes[m][0]);
     };
     int nk = 0, nv = 0;  // loaded so far
@@ -113,14 +117,14 @@ __global__ void __launch_bounds__(StateCfg<D>::kThreads, StateCfg<D>::kBlocks)
       if (i + 1 < chunks) {
         if (nv > 1) ok = tc::mbar_wait(&s.vempty[nv & 1], (nv / 2 - 1) & 1, p.err);
         if (!ok) break;
-        load(C::kV + (nv & 1) * C::kTile, mv, w.v, &s.vfull[nv & 1], nv);
+        load(C::kV + (nv & 1) * kAtom, mv, w.v, &s.vfull[nv & 1], nv, 64 * part0, 1);
         ++nv;
       }
       const int k = i < 0 ? 0 : i;
       if (nk == k && k < chunks) {
         if (nk) ok = tc::mbar_wait(&s.kempty, (nk - 1) & 1, p.err);
         if (!ok) break;
-        load(C::kK, mk, w.k, &s.kfull, nk);
+        load(C::kK, mk, w.k, &s.kfull, nk, 0, C::kAtoms);
         ++nk;
       }
     }
@@ -128,7 +132,7 @@ __global__ void __launch_bounds__(StateCfg<D>::kThreads, StateCfg<D>::kBlocks)
     if (nk) tc::mbar_wait(&s.kfull, (nk - 1) & 1, nullptr);
     for (int i = nv > 2 ? nv - 2 : 0; i < nv; ++i) tc::mbar_wait(&s.vfull[i & 1], i / 2 & 1, nullptr);
   } else if (warp == C::kMma && lane == 0) {
-    constexpr uint32_t kUD = tc::idesc_bf16(D, D, 1) | 1u << 15;  // K^T: its rows run along M
+    constexpr uint32_t kUD = tc::idesc_bf16(D, 64, 1) | 1u << 15;  // K^T: its rows run along M
     const uint32_t keys = base + C::kK;
     bool ok = true;
     for (int i = 0; i < chunks && ok; ++i) {
@@ -138,10 +142,11 @@ __global__ void __launch_bounds__(StateCfg<D>::kThreads, StateCfg<D>::kBlocks)
         if (!(ok = tc::mbar_wait(&s.slab_full, (i * C::kSlabs + j) & 1, p.err))) break;
         tc::fence_after_sync();
 #pragma unroll
-        for (int k = 0; k < 6; ++k)
-          tc::mma_ss(tmem, desc_blocks(keys + j * C::kSlabAtom + k % 2 * 2048, kAtom),
-                     desc_blocks(base + C::kSlab0 + k / 2 * C::kPart + k % 2 * 2048, C::kSlabAtom), kUD,
-                     j > 0 || k > 0);
+        for (int k = 0; k < 3 * C::kSlab / 16; ++k) {
+          const int kk = k % (C::kSlab / 16), part = k / (C::kSlab / 16);
+          tc::mma_ss(tmem, desc_blocks(keys + j * C::kPart + kk * 2048, kAtom),
+                     tc::desc_sw128(base + C::kSlab0 + part * C::kPart + kk * 2048), kUD, j > 0 || k > 0);
+        }
         tc::mma_commit(&s.slab_empty);
       }
       if (!ok) break;
@@ -152,54 +157,51 @@ __global__ void __launch_bounds__(StateCfg<D>::kThreads, StateCfg<D>::kBlocks)
     tc::mbar_wait(&s.fin, 0, nullptr);
   } else if (warp < C::kWarps) {
     const int t = threadIdx.x;
-    const uint32_t lanes = tmem + ((uint32_t)(warp % 4 * 32) << 16) + (D == 64 ? 0 : warp / 4 * 64);
+    const int group = D == 64 ? 0 : warp / 4, place = D == 64 ? t : part0 * 128 + t % 128;  // in Frags
+    const uint32_t lanes = tmem + ((uint32_t)(warp % 4 * 32 + 16 * group) << 16);
     const size_t bh = (size_t)blockIdx.z * gridDim.y + blockIdx.y;
-    f2 S[F::kHalves][16];
+    f2 S[16];
 #pragma unroll
-    for (int g = 0; g < F::kHalves; ++g)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) S[g][e] = 0;
+    for (int e = 0; e < 16; ++e) S[e] = 0;
     auto save = [&](float *to) {
 #pragma unroll
-      for (int g = 0; g < F::kHalves; ++g)
-#pragma unroll
-        for (int e = 0; e < 16; e += 2)
-          *reinterpret_cast<ulonglong2 *>(to + F::at(t, g, e)) = make_ulonglong2(S[g][e], S[g][e + 1]);
+      for (int e = 0; e < 16; e += 2)
+        *reinterpret_cast<ulonglong2 *>(to + F::at(place, group, e)) = make_ulonglong2(S[e], S[e + 1]);
     };
     const size_t nb = p.c1 - p.c0;
     // the matrix of the stretch's chunk i >= 1; the flag of chunk i
     auto local = [&](int i) { return p.local + (bh * (nb - 1) + (from - p.c0 + i - 1)) * (D * D); };
     auto flag = [&](int i) { return p.odd + (bh * nb + (from - p.c0 + i)) * 8 + warp; };
     const Factor whole = decay_power(decay, kC);
-    const int r16 = t % 128 / 8, ch = t % 8, atom = t / 128;
-    const uint32_t in = swz128(r16, ch);
-    unsigned char *slab = smem + C::kSlab0 + atom * C::kSlabAtom + in;
+    const int r0 = t / 8;
+    const uint32_t in = swz128(r0, t % 8);
+    unsigned char *slab = smem + C::kSlab0 + in;
     bool ok = true;
     for (int i = 0; i < chunks; ++i) {
       const int n = band.size(band.chunk(from + i, reverse));
-      unsigned char *values = smem + C::kV + (i & 1) * C::kTile;
+      unsigned char *values = smem + C::kV + (i & 1) * kAtom;
       if (!(ok = WAIT(s.vfull[i & 1], i / 2))) break;
       if (i && !p.fused) save(local(i));
       if (n < kC) {
         // what lies behind the sequence takes no part, whatever it is
         if (!(ok = WAIT(s.kfull, i))) break;
-        for (int u = t; u < (kC - n) * (D / 8); u += F::kThreads) {
-          const uint32_t at = u % (D / 8) / 8 * kAtom + swz128(n + u / (D / 8), u % 8);
-          *reinterpret_cast<uint4 *>(smem + C::kK + at) = make_uint4(0, 0, 0, 0);
-          *reinterpret_cast<uint4 *>(values + at) = make_uint4(0, 0, 0, 0);
+        for (int u = t; u < (kC - n) * (D / 8); u += C::kStateThreads) {
+          const uint32_t at = swz128(n + u / (D / 8), u % 8);
+          *reinterpret_cast<uint4 *>(smem + C::kK + u % (D / 8) / 8 * kAtom + at) = make_uint4(0, 0, 0, 0);
+          if (u % (D / 8) < 8) *reinterpret_cast<uint4 *>(values + at) = make_uint4(0, 0, 0, 0);
         }
         tc::fence_async_smem();
-        asm volatile("bar.sync 1, %0;" ::"n"(F::kThreads) : "memory");
+        asm volatile("bar.sync 1, %0;" ::"n"(C::kStateThreads) : "memory");
       }
-      const unsigned char *source = values + atom * kAtom + in;
+      const unsigned char *source = values + in;
       uint32_t some = 0;  // the bits of all third parts
 #pragma unroll 1
       for (int j = 0; j < C::kSlabs; ++j) {
         uint32_t part[2][3][4];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const int row = j * C::kSlab + r16 + 16 * k;
-          const uint4 x = *reinterpret_cast<const uint4 *>(source + j * C::kSlabAtom + k * 2048);
+          const int row = j * C::kSlab + r0 + C::kRows * k;
+          const uint4 x = *reinterpret_cast<const uint4 *>(source + j * C::kPart + k * C::kRows * 128);
           const float f = row < n ? s.power[reverse ? row + 1 : n - 1 - row] : 0.f;
           const uint32_t v[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
@@ -217,7 +219,7 @@ __global__ void __launch_bounds__(StateCfg<D>::kThreads, StateCfg<D>::kBlocks)
         for (int k = 0; k < 2; ++k)
 #pragma unroll
           for (int q = 0; q < 3; ++q)
-            *reinterpret_cast<uint4 *>(slab + q * C::kPart + k * 2048) =
+            *reinterpret_cast<uint4 *>(slab + q * C::kPart + k * C::kRows * 128) =
                 make_uint4(part[k][q][0], part[k][q][1], part[k][q][2], part[k][q][3]);
         tc::fence_async_smem();
         __syncwarp();
@@ -229,18 +231,13 @@ __global__ void __launch_bounds__(StateCfg<D>::kThreads, StateCfg<D>::kBlocks)
       tc::fence_after_sync();
       const Factor f = n == kC ? whole : decay_power(decay, n);
       const f2 hi = f2_bits(f.hi, f.hi), lo = f2_bits(f.lo, f.lo);
+      f2 u[16];
+      tmem_ld_16x64(lanes, u);
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&s.u_free);
 #pragma unroll
-      for (int g = 0; g < F::kHalves; ++g) {
-        f2 u[16];
-        tmem_ld_16x64(lanes + ((uint32_t)(16 * g) << 16), u);
-        if (g == F::kHalves - 1) {
-          tc::fence_before_sync();
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&s.u_free);
-        }
-#pragma unroll
-        for (int e = 0; e < 16; ++e) S[g][e] = madd2(S[g][e], hi, madd2(S[g][e], lo, u[e]));
-      }
+      for (int e = 0; e < 16; ++e) S[e] = madd2(S[e], hi, madd2(S[e], lo, u[e]));
       // A value that is not finite leaves NaN in its third part (some large finite ones leave bits
       // that look like it: the rows' pass looks again).
       const bool odd = (some & 0x7f80u) == 0x7f80u || (some & 0x7f800000u) == 0x7f800000u;
@@ -258,7 +255,7 @@ __global__ void __launch_bounds__(StateCfg<D>::kThreads, StateCfg<D>::kBlocks)
   __syncthreads();
   if (warp == C::kMma) {
     tc::fence_after_sync();
-    tc::tmem_dealloc(tmem, D);
+    tc::tmem_dealloc(tmem, 64);
   }
 }
 
@@ -291,7 +288,8 @@ __global__ void __launch_bounds__(256) k16_join_kernel(const __grid_constant__ P
   float4 *at = reinterpret_cast<float4 *>(p.slots + bh * p.splits * (D * D)) + i;
   // (the last stretch of a sequence: not where nobody wants the state behind it)
   const int adds = band.stretches - (band.stretches && band.hi == band.chunks && !wants_last(p, w) ? 1 : 0);
-  constexpr int kAhead = 8;
+  constexpr int kAhead = 4;
+  const Factor whole = decay_power(decay, band.per * kC);
   for (int r0 = 0; r0 < band.stretches; r0 += kAhead) {
     float4 y[kAhead];
 #pragma unroll
@@ -303,7 +301,8 @@ __global__ void __launch_bounds__(256) k16_join_kernel(const __grid_constant__ P
       if (r >= band.stretches) break;
       at[(size_t)r * (D * D / 4)] = x;
       if (r >= adds) break;
-      const Factor f = decay_power(decay, band.tokens(band.lo + r * band.per, band.end(r), w.reverse));
+      const int n = band.tokens(band.lo + r * band.per, band.end(r), w.reverse);
+      const Factor f = n == band.per * kC ? whole : decay_power(decay, n);
       x = make_float4(f.times(x.x, y[k].x), f.times(x.y, y[k].y), f.times(x.z, y[k].z), f.times(x.w, y[k].w));
     }
   }
@@ -761,7 +760,7 @@ cudaError_t run(Params &p, const Maps &m, const Plan &q, cudaStream_t st) {
     p.first = c == 0;
     p.last = p.c1 == q.chunks;
     if (!q.fused || p.splits > 1) {
-      states<<<dim3(q.fused ? p.splits - 1 : p.splits, pairs, p.a.sweeps), StateCfg<D>::kThreads, kStates, st>>>(m, p);
+      states<<<dim3((q.fused ? p.splits - 1 : p.splits) * StateCfg<D>::kParts, pairs, p.a.sweeps), StateCfg<D>::kThreads, kStates, st>>>(m, p);
       if ((e = cudaGetLastError()) != cudaSuccess) return e;
       k16_join_kernel<D><<<dim3(D * D / 1024, pairs, p.a.sweeps), 256, 0, st>>>(p);
       if ((e = cudaGetLastError()) != cudaSuccess) return e;
