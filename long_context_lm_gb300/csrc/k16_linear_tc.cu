@@ -21,14 +21,16 @@
 //   join    runs through the stretches: the state before each
 //   rows    all chunks by themselves, in equal runs: S = (the stretch's own) + lam^m (the state
 //           before it), then the three products of the outputs
-// One pass (states in registers, rows beside them) reads and writes less, but with few
-// heads needs the stretches' states beforehand, by a pass as long as the first here, and with
-// any number of heads leaves blocks without work: 65536 tokens x 16 heads XX us, now XX;
-// 5 ragged sequences of 8191 x 16 heads of 128 321, now XX.  The states between the passes
-// (16 KB a chunk of 64 KB of rows; heads of 128: 64 of 128) are kept to what the L2 holds
-// by going through long sequences in bands.
+// One pass (k17_linear_fused.cu: states in registers, rows beside them) reads and writes less,
+// but with few heads needs the stretches' states beforehand, by a pass as long as the first here,
+// and with any number of heads leaves blocks without work.  65536 tokens x 16 heads: 263 us in one
+// pass, 210 in two.  States of heads of 128 are half of a chunk's rows (64 KB of 128; of 64 a
+// quarter): 5 ragged sequences of 8191 x 16 heads of 128: 493 us in two passes, 296 in one.
 //
-// What bounds it: XX
+// What bounds it: 65536 tokens x 16 heads move 1.07 GB in two passes (537 MB in and out have to, the
+// keys and values go in twice, the states out and in), 158 us at the copy's rate; states 88 us, join
+// 13, rows 110 (a chunk's three waits of rows on products and of products on rows, by two blocks an
+// SM in turn).
 #include "linear_tc.cuh"
 
 namespace fs {
@@ -71,7 +73,8 @@ __global__ void __launch_bounds__(StateCfg<D>::kThreads, StateCfg<D>::kBlocks)
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ StateShared s;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const LinearSweep &w = p.a.sweep[blockIdx.z];
+  const int z = p.own[blockIdx.z];
+  const LinearSweep &w = p.a.sweep[z];
   const int b = blockIdx.y / p.a.H, h = blockIdx.y % p.a.H;
   const int r = blockIdx.x / C::kParts, part0 = blockIdx.x % C::kParts;
   const Band band(p, b);
@@ -102,7 +105,7 @@ __global__ void __launch_bounds__(StateCfg<D>::kThreads, StateCfg<D>::kBlocks)
   const uint32_t tmem = s.tmem, base = smem_u32(smem);
 
   if (warp == C::kTma && lane == 0) {
-    const int mk = p.map[blockIdx.z][1], mv = p.map[blockIdx.z][2];
+    const int mk = p.map[z][1], mv = p.map[z][2];
     // `atoms` times 64 columns from column x0 on
     auto load = [&](uint32_t at, int m, const LinearRows &x, uint64_t *bar, int i, int x0, int atoms) {
       const int t = band.chunk(from + i, reverse) * kC;
@@ -267,7 +270,7 @@ __global__ void __launch_bounds__(StateCfg<D>::kThreads, StateCfg<D>::kBlocks)
 template <int D>
 __global__ void __launch_bounds__(256) k16_join_kernel(const __grid_constant__ Params p) {
   using F = Frags<D>;
-  const LinearSweep &w = p.a.sweep[blockIdx.z];
+  const LinearSweep &w = p.a.sweep[p.own[blockIdx.z]];
   const int b = blockIdx.y / p.a.H, h = blockIdx.y % p.a.H;
   const Band band(p, b);
   const float decay = p.a.decay[h];
@@ -420,14 +423,41 @@ struct Walk : Start {
 
 struct RowShared {
   uint64_t qfull, qempty, kfull, kempty, vfull[2], vempty[2];
-  uint64_t ready[2];  // S, tables and values: the states' warps may be a chunk ahead of the rows', not two
+  // S and tables; values looked through: their warps may be a chunk ahead of the rows', not two
+  uint64_t ready[2], checked[2];
   uint64_t s_free, scores, inter, parts, done, o_free, fin;
   uint32_t tmem;
+  bool turned[2];     // S is another sweep's, transposed
   int odd[2];         // a chunk's values are not all finite
   int bad[2][128];    // per column: the first such token in the sweep's order
   Tables tables[2];
   Start start;
 };
+
+// A chunk's values: what lies behind the sequence takes no part, whatever it is.  A value that
+// is not finite leaves the tile, where scores of 0 would make NaN of the rows before it as well;
+// those after it get theirs at the end.
+__device__ __forceinline__ void look_through(RowShared &s, unsigned char *values, int i, int n, bool reverse, int t,
+                                             int threads) {
+  const int ch = t % 8;
+#pragma unroll 1
+  for (int row = t / 8; row < kC; row += threads / 8) {
+    uint4 *place = reinterpret_cast<uint4 *>(values + swz128(row, ch));
+    if (row >= n) {
+      *place = make_uint4(0, 0, 0, 0);
+      continue;
+    }
+    if (!not_finite(*place)) continue;
+    uint32_t *word = reinterpret_cast<uint32_t *>(place);
+    for (int j = 0; j < 8; ++j) {
+      if ((word[j / 2] >> j % 2 * 16 & 0x7f80u) != 0x7f80u) continue;
+      word[j / 2] &= j % 2 ? 0xffffu : 0xffff0000u;
+      atomicMin(&s.bad[i & 1][ch * 8 + j], reverse ? kC - 1 - row : row);
+      s.odd[i & 1] = 1;
+    }
+  }
+  tc::fence_async_smem();
+}
 
 // Warps:
 //   0-7       rows, two warps to 32 of them, each with half of the columns: scores to bf16
@@ -436,9 +466,15 @@ struct RowShared {
 //             written by their own threads would be 32 places an instruction)
 //   8..       states (D / 16 warps): S from its two parts, split, into shared memory; the
 //             head's tables
-//   last four one for TMA loads (values a chunk ahead), one that issues the products
+//   last four one for TMA loads (values a chunk ahead), one that issues the products, with
+//             kTurns two that look through values
 // Heads of 64 leave room for two blocks an SM, which fill each other's waits; heads of 128
 // for one.
+// kTurns: one of the sweeps borrows its states.  Then warps of their own look through the values
+// (by the states' warps gradients of 4 x 4096 tokens x 16 heads 174 us, so 159); else the states'
+// warps do, where the first pass has seen something (so 65536 tokens x 16 heads 210 us,
+// with warps of their own 216).
+template <bool kTurns>
 __global__ void __launch_bounds__(RowCfg::kThreads, 2)
     k16_rows_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
   using C = RowCfg;
@@ -455,6 +491,7 @@ __global__ void __launch_bounds__(RowCfg::kThreads, 2)
                         &s.scores, &s.inter, &s.done, &s.fin})
       tc::mbar_init(x, 1);
     for (uint64_t *x : {&s.ready[0], &s.ready[1]}) tc::mbar_init(x, C::kStateWarps);
+    for (uint64_t *x : {&s.checked[0], &s.checked[1]}) tc::mbar_init(x, 2);
     for (uint64_t *x : {&s.vempty[0], &s.vempty[1], &s.parts, &s.o_free}) tc::mbar_init(x, 8);
     tc::mbar_fence_init();
     s.odd[0] = s.odd[1] = 0;
@@ -505,31 +542,43 @@ __global__ void __launch_bounds__(RowCfg::kThreads, 2)
     } else if (warp == C::kMma && lane == 0) {
       // ------------------------------------------------------------- products
       constexpr uint32_t kQK = tc::idesc_bf16(128, 128, 0), kB = tc::idesc_bf16(128, D, 1);
+      constexpr uint32_t kBT = tc::idesc_bf16(128, D, 0);  // (S transposed: its columns along K)
       const int chunks = s.start.left;
       for (int i = 0; i < chunks; ++i) {
-        const uint32_t values = base + C::kV + (i & 1) * C::kTile;
+        // (kept from computing the descriptors beforehand, for which there are no registers)
+        uint32_t here = base;
+        asm volatile("" : "+r"(here));
+        const uint32_t values = here + C::kV + (i & 1) * C::kTile;
         if (!tc::mbar_wait(&s.kfull, i & 1, p.err) || !tc::mbar_wait(&s.qfull, i & 1, p.err)) break;
         tc::fence_after_sync();
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
-          tc::mma_ss(tmem + C::kScores, tc::desc_sw128(base + C::kQ + k / 4 * kAtom + k % 4 * 32),
-                     tc::desc_sw128(base + C::kK + k / 4 * kAtom + k % 4 * 32), kQK, k > 0);
+          tc::mma_ss(tmem + C::kScores, tc::desc_sw128(here + C::kQ + k / 4 * kAtom + k % 4 * 32),
+                     tc::desc_sw128(here + C::kK + k / 4 * kAtom + k % 4 * 32), kQK, k > 0);
         tc::mma_commit(&s.scores);
         tc::mma_commit(&s.kempty);
         if (!tc::mbar_wait(&s.ready[i & 1], i >> 1 & 1, p.err) ||
             (i && !tc::mbar_wait(&s.o_free, (i - 1) & 1, p.err)))
           break;
         tc::fence_after_sync();
+        const uint64_t sd = tc::desc_sw128(here + C::kS);
+        if (kTurns && s.turned[i & 1]) {
 #pragma unroll
-        for (int k = 0; k < 2 * D / 16; ++k) {
-          const int kk = k % (D / 16), part = k / (D / 16);
-          tc::mma_ss(tmem + C::kOut, tc::desc_sw128(base + C::kQ + kk / 4 * kAtom + kk % 4 * 32),
-                     desc_blocks(base + C::kS + part * C::kSPart + kk * 2048, D * 128), kB, k > 0);
+          for (int k = 0; k < 2 * D / 16; ++k)
+            tc::mma_ss(tmem + C::kOut, tc::desc_sw128(here + C::kQ + k % 4 * 32),
+                       sd + (k / 4 * C::kSPart + k % 4 * 32) / 16, kBT, k > 0);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 2 * D / 16; ++k)
+            tc::mma_ss(tmem + C::kOut, tc::desc_sw128(here + C::kQ + k % 4 * 32),
+                       sd + (k / 4 * C::kSPart + k % 4 * 2048) / 16, kB, k > 0);
         }
         tc::mma_commit(&s.inter);
         tc::mma_commit(&s.s_free);
         tc::mma_commit(&s.qempty);
-        if (!tc::mbar_wait(&s.vfull[i & 1], i >> 1 & 1, p.err) || !tc::mbar_wait(&s.parts, i & 1, p.err)) break;
+        if (!tc::mbar_wait(kTurns ? &s.checked[i & 1] : &s.vfull[i & 1], i >> 1 & 1, p.err) ||
+            !tc::mbar_wait(&s.parts, i & 1, p.err))
+          break;
         tc::fence_after_sync();
 #pragma unroll
         for (int k = 0; k < 2 * kC / 16; ++k) {
@@ -541,6 +590,22 @@ __global__ void __launch_bounds__(RowCfg::kThreads, 2)
       }
       tc::mma_commit(&s.fin);
       tc::mbar_wait(&s.fin, 0, nullptr);
+    } else if (kTurns && warp > C::kMma) {
+      // --------------------------------------------------------------- values
+      const int t = threadIdx.x - 32 * (C::kMma + 1);
+      Walk u(p, s.start);
+      const int chunks = u.left;
+      for (int i = 0; i < chunks; ++i, u.next()) {
+        const size_t bh = ((size_t)p.slot[u.z] * p.a.batch + u.b) * p.a.H + u.h;
+        const bool look =
+            *reinterpret_cast<const uint32_t *>(p.odd + (bh * (p.c1 - p.c0) + (u.ci - p.c0)) * 8) != 0;
+        const int n = u.band.size(u.band.chunk(u.ci, u.reverse));
+        if (!WAIT(s.vfull[i & 1], i >> 1)) break;
+        if (n < kC || look || u.z == p.borrows)  // (nobody has looked through a borrower's values)
+          look_through(s, smem + C::kV + (i & 1) * C::kTile, i, n, u.reverse, t, 64);
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&s.checked[i & 1]);
+      }
     }
   } else if (warp >= 8) {
     tc::regs_inc<C::kStateRegs>();
@@ -555,7 +620,7 @@ __global__ void __launch_bounds__(RowCfg::kThreads, 2)
     f2 before[16];             // the state before the stretch
     for (int i = 0; i < chunks; ++i) {
       const Band &band = u.band;
-      const size_t bh = ((size_t)u.z * p.a.batch + u.b) * p.a.H + u.h;
+      const size_t bh = ((size_t)p.slot[u.z] * p.a.batch + u.b) * p.a.H + u.h;
       const int r = (u.ci - band.lo) / band.per, from = band.lo + r * band.per;
       const size_t nb = p.c1 - p.c0, place = u.ci - p.c0;
       if (fresh || r != stretch) {
@@ -573,11 +638,12 @@ __global__ void __launch_bounds__(RowCfg::kThreads, 2)
 #pragma unroll
       for (int e = 0; e < 8; ++e)
         local[e] = own ? __ldg(reinterpret_cast<const ulonglong2 *>(at + F::at(t, 0, 2 * e))) : make_ulonglong2(0, 0);
-      const bool look = *reinterpret_cast<const uint32_t *>(p.odd + (bh * nb + place) * 8) != 0;
+      const bool look = !kTurns && *reinterpret_cast<const uint32_t *>(p.odd + (bh * nb + place) * 8) != 0;
       const float decay = p.a.decay[u.h];
       const Factor f = decay_power(decay, band.tokens(from, u.ci, u.reverse));
       const f2 hi = f2_bits(f.hi, f.hi), lo = f2_bits(f.lo, f.lo);
       if (i && !WAIT(s.s_free, i - 1)) break;
+      if (kTurns && t == 0) s.turned[i & 1] = u.z == p.borrows;
       if (fresh) {
         which ^= 1;
         fill_tables(s.tables[which], decay, u.reverse, p.a.scale, t, F::kThreads);
@@ -592,31 +658,14 @@ __global__ void __launch_bounds__(RowCfg::kThreads, 2)
         }
         publisher.put(0, e, x);
       }
-      const int n = band.size(band.chunk(u.ci, u.reverse));
-      if (n < kC || look) {
-        if (!WAIT(s.vfull[i & 1], i >> 1)) break;
-        unsigned char *values = smem + C::kV + (i & 1) * C::kTile;
-        for (int k = t; k < kC * (D / 8); k += F::kThreads) {
-          const int row = k / (D / 8), ch = k % (D / 8);
-          uint32_t *word = reinterpret_cast<uint32_t *>(values + swz128(row, ch));
-          for (int j = 0; j < 4; ++j) {
-            if (row >= n) {  // what lies behind the sequence takes no part, whatever it is
-              word[j] = 0;
-              continue;
-            }
-            // A value that is not finite leaves the tile, where scores of 0 would make NaN of the rows
-            // before it as well; those after it get theirs at the end.
-#pragma unroll
-            for (int m = 0; m < 2; ++m)
-              if ((word[j] >> 16 * m & 0x7f80u) == 0x7f80u) {
-                word[j] &= m ? 0xffffu : 0xffff0000u;
-                atomicMin(&s.bad[i & 1][ch * 8 + 2 * j + m], u.reverse ? kC - 1 - row : row);
-                s.odd[i & 1] = 1;
-              }
-          }
+      tc::fence_async_smem();
+      if (!kTurns) {
+        const int n = band.size(band.chunk(u.ci, u.reverse));
+        if (n < kC || look) {
+          if (!WAIT(s.vfull[i & 1], i >> 1)) break;
+          look_through(s, smem + C::kV + (i & 1) * C::kTile, i, n, u.reverse, t, F::kThreads);
         }
       }
-      tc::fence_async_smem();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&s.ready[i & 1]);
       fresh = u.next();
@@ -648,7 +697,7 @@ __global__ void __launch_bounds__(RowCfg::kThreads, 2)
       tc::fence_before_sync();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&s.parts);
-      if (!WAIT(s.done, i)) break;
+      if ((kTurns && !WAIT(s.checked[i & 1], i >> 1)) || !WAIT(s.done, i)) break;
       tc::fence_after_sync();
       const bool odd = s.odd[i & 1] != 0;
       storing = rows.store(p.a.sweep[u.z], &maps.out[u.z], p.out_axes[u.z], u.b, u.h, chunk, n, reverse,
@@ -714,32 +763,41 @@ struct Plan {
   int chunks, band, splits;
   size_t local, slots, carry, odd, total;  // bytes
 };
-constexpr size_t kBandBytes = (size_t)160 << 20;
+// (Bands small enough for the L2 to keep their states and keys between the passes cost more launches
+// than they save: 65536 tokens x 16 heads in bands of 40 MB 289 us, of 80 MB 245, in one 210.)
+constexpr size_t kBandBytes = (size_t)256 << 20;
 Plan plan_of(int sweeps, int pairs, int T, int d) {
   Plan q{};
-  const size_t matrix = (size_t)d * d * 4, all = (size_t)sweeps * pairs;
+  const size_t matrix = (size_t)d * d * 4;
+  const size_t all = (size_t)sweeps * pairs;
+  // Of the gradients' sweeps the second, over R^T, has the states of the third, over R.
+  const size_t own = sweeps == 3 ? (size_t)2 * pairs : all;
   q.chunks = q.band = (T + kC - 1) / kC;
   const size_t resident = 152 * (d == 64 ? 2 : 1);  // blocks of the fused kernel
   q.fused = d == 128 || q.chunks < 8 || all >= resident;
   if (q.fused) {
-    // Stretches of eight chunks at least, some four blocks to a place, so that the long and the short
-    // even out.
-    const size_t n = all >= 2 * resident ? 1 : 4 * resident / all, most = q.chunks / 8;
+    // Stretches of eight chunks at least: as many as fill the GPU once, if they nearly do (3 x 16 heads
+    // in three stretches 475 us, in six 497), else some three times (80 heads in one stretch
+    // 326 us, in three 313, in five 290, in seven 300).
+    size_t n = all < resident ? resident / all : 1;
+    if (all < 2 * resident && n * all < resident * 7 / 8) n = 3 * resident / all;
+    const size_t most = q.chunks / 8;
     q.splits = (int)(n < most ? n : most < 1 ? 1 : most);
-    q.slots = q.splits > 1 ? all * q.splits * matrix : 0;
+    q.slots = q.splits > 1 ? own * q.splits * matrix : 0;
     q.total = q.slots;
     return q;
   }
   // bands of equal length whose states stay within kBandBytes
-  const size_t most = kBandBytes / (all * matrix) > 1 ? kBandBytes / (all * matrix) : 1;
+  const size_t most = kBandBytes / (own * matrix) > 1 ? kBandBytes / (own * matrix) : 1;
   const size_t bands = (q.chunks + most - 1) / most;
   q.band = (int)((q.chunks + bands - 1) / bands);
-  const size_t n = 152 * StateCfg<64>::kBlocks / all, longest = (q.band + 3) / 4;  // four chunks a stretch at least
+  // four chunks a stretch at least
+  const size_t n = 152 * StateCfg<64>::kBlocks / own, longest = (q.band + 3) / 4;
   q.splits = (int)(n < longest ? n : longest);
-  q.local = all * (q.band - 1) * matrix;
-  q.slots = all * q.splits * matrix;
-  q.carry = bands > 1 ? all * matrix : 0;
-  q.odd = (all * q.band * 8 + 255) / 256 * 256;
+  q.local = own * (q.band - 1) * matrix;
+  q.slots = own * q.splits * matrix;
+  q.carry = bands > 1 ? own * matrix : 0;
+  q.odd = (own * q.band * 8 + 255) / 256 * 256;
   q.total = q.local + q.slots + q.carry + q.odd;
   return q;
 }
@@ -750,24 +808,32 @@ cudaError_t run(Params &p, const Maps &m, const Plan &q, cudaStream_t st) {
   constexpr int kStates = StateCfg<D>::kBytes + 1024, kRows = RowCfg::kBytes + 1024;
   cudaError_t e = cudaFuncSetAttribute(states, cudaFuncAttributeMaxDynamicSharedMemorySize, kStates);
   if (e != cudaSuccess) return e;
-  if ((e = cudaFuncSetAttribute(k16_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRows)) != cudaSuccess)
+  auto rows = p.a.sweeps == 3 ? k16_rows_kernel<true> : k16_rows_kernel<false>;
+  if ((e = cudaFuncSetAttribute(rows, cudaFuncAttributeMaxDynamicSharedMemorySize, kRows)) != cudaSuccess)
     return e;
   const int pairs = p.a.batch * p.a.H;
   p.fused = q.fused;
+  const bool borrow = p.a.sweeps == 3;
+  p.borrows = borrow ? 1 : -1;
+  int owners = 0;
+  for (int i = 0; i < p.a.sweeps; ++i)
+    if (i != p.borrows) p.slot[i] = owners, p.own[owners++] = i;
+  if (borrow) p.slot[1] = p.slot[2];
   for (int c = 0; c < q.chunks; c += q.band) {
     p.c0 = c;
     p.c1 = c + q.band < q.chunks ? c + q.band : q.chunks;
     p.first = c == 0;
     p.last = p.c1 == q.chunks;
     if (!q.fused || p.splits > 1) {
-      states<<<dim3((q.fused ? p.splits - 1 : p.splits) * StateCfg<D>::kParts, pairs, p.a.sweeps), StateCfg<D>::kThreads, kStates, st>>>(m, p);
+      const int stretches = q.fused ? p.splits - 1 : p.splits;
+      states<<<dim3(stretches * StateCfg<D>::kParts, pairs, owners), StateCfg<D>::kThreads, kStates, st>>>(m, p);
       if ((e = cudaGetLastError()) != cudaSuccess) return e;
-      k16_join_kernel<D><<<dim3(D * D / 1024, pairs, p.a.sweeps), 256, 0, st>>>(p);
+      k16_join_kernel<D><<<dim3(D * D / 1024, pairs, owners), 256, 0, st>>>(p);
       if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
     if (q.fused) return lin::launch_fused(p, m, st);
     const long long units = (long long)p.a.sweeps * pairs * (p.c1 - p.c0), blocks = 152 * 2;
-    k16_rows_kernel<<<(unsigned)(units < blocks ? units : blocks), RowCfg::kThreads, kRows, st>>>(m, p);
+    rows<<<(unsigned)(units < blocks ? units : blocks), RowCfg::kThreads, kRows, st>>>(m, p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   return cudaSuccess;

@@ -90,7 +90,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, D == 64 ? 2 : 1)
       tc::mbar_init(&s.vempty[i], 8);
     }
     tc::mbar_init(&s.slab_empty, 1);
-    for (uint64_t *x : {&s.slab_full, &s.s_ready, &s.u_free, &s.checked[0], &s.checked[1]}) tc::mbar_init(x, C::kStateWarps);
+    for (uint64_t *x : {&s.slab_full, &s.s_ready, &s.u_free, &s.checked[0], &s.checked[1]})
+      tc::mbar_init(x, C::kStateWarps);
     for (uint64_t *x : {&s.parts, &s.o_free}) tc::mbar_init(x, 8);
     tc::mbar_init(&s.kempty, 2);  // read by the scores' product and by the slabs'
     tc::mbar_init(&s.fin_u, 1);
@@ -233,18 +234,26 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, D == 64 ? 2 : 1)
     // ------------------------------------------------------------------ states
     const int t = threadIdx.x - 256;
     const uint32_t lanes = tu + ((uint32_t)(warp % 4 * 32) << 16) + (D == 64 ? 0 : t / 128 * 64);
-    const size_t bh = (size_t)blockIdx.z * gridDim.y + blockIdx.y;
     const int sr = w.transposed ? 1 : D, sc = w.transposed ? D : 1;
     f2 S[F::kHalves][16];
+    const size_t slot = (size_t)p.slot[blockIdx.z] * gridDim.y + blockIdx.y;
     const float *given = w.state ? w.state + (size_t)blockIdx.y * D * D : nullptr;
 #pragma unroll
     for (int g = 0; g < F::kHalves; ++g)
 #pragma unroll
       for (int e = 0; e < 16; e += 2) {
         if (st.stretches > 1) {
-          const float *at = p.slots + (bh * p.splits + r) * (D * D) + F::at(t, g, e);
-          const ulonglong2 x = *reinterpret_cast<const ulonglong2 *>(at);
-          S[g][e] = x.x, S[g][e + 1] = x.y;
+          const float *at = p.slots + (slot * p.splits + r) * (D * D);
+          if ((int)blockIdx.z == p.borrows) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const int row = F::row(t, g, e + k), col = F::col(t, e + k);
+              S[g][e + k] = f2_bits(at[F::index(col, row)], at[F::index(col + 1, row)]);
+            }
+          } else {
+            const ulonglong2 x = *reinterpret_cast<const ulonglong2 *>(at + F::at(t, g, e));
+            S[g][e] = x.x, S[g][e + 1] = x.y;
+          }
         } else if (given) {
 #pragma unroll
           for (int k = 0; k < 2; ++k) {

@@ -24,11 +24,14 @@ struct Params {
   bool first, last;   // band
   bool fused;         // the rows' pass makes states itself: only the stretches' own are wanted
   int splits;         // stretches of a band
-  float *local;       // [sweep, batch H, c1 - c0 - 1, D D]: the state before each chunk but the band's
+  // Sweeps with states of their own, where those of a sweep are, and the sweep (or -1) whose states
+  // are another's transposed.
+  int own[3], slot[3], borrows;
+  float *local;       // [own sweep, batch H, c1 - c0 - 1, D D]: the state before each chunk but the band's
                       // first, of its stretch alone (none before a stretch's first)
-  float *slots;       // [sweep, batch H, splits, D D]: what each stretch adds; then the state before it
-  float *carry;       // [sweep, batch H, D D]: the state behind the band
-  uint8_t *odd;       // [sweep, batch H, c1 - c0, 8]: not all of the values that a warp of the states'
+  float *slots;       // [own sweep, batch H, splits, D D]: what each stretch adds; then the state before it
+  float *carry;       // [own sweep, batch H, D D]: the state behind the band
+  uint8_t *odd;       // [own sweep, batch H, c1 - c0, 8]: not all of the values that a warp of the states'
                       // kernel saw of the chunk are finite
   int map[3][3];      // which map holds q, k, v of a sweep
   int axes[4][2];     // 0 where a map's sequences or heads are one
@@ -79,6 +82,11 @@ struct Frags {
   static __device__ __forceinline__ int col(int t, int e) { return col0(t) + e / 2 * 8; }
   // floats from a matrix's start to pairs e and e + 1 (e even) of group g
   static __device__ __forceinline__ int at(int t, int g, int e) { return ((g * 8 + e / 2) * kThreads + t) * 4; }
+  // and to an element
+  static __device__ __forceinline__ int index(int row, int col) {
+    const int warp = D == 64 ? row / 16 : row / 32 + col / 64 * 4, g = D == 64 ? 0 : row / 16 % 2;
+    return at(32 * warp + row % 8 * 4 + col % 8 / 2, g, col % 64 / 8 * 2) + row / 8 % 2 * 2 + col % 2;
+  }
 };
 
 // tc::desc_sw128 for elements in several blocks of 64, `apart` bytes from one to the next.
@@ -129,6 +137,17 @@ __device__ __forceinline__ void bulk_commit() {
 template <int N>
 __device__ __forceinline__ void bulk_wait_read() {
   asm volatile("cp.async.bulk.wait_group.read %0;\n" ::"n"(N) : "memory");
+}
+
+// Eight bf16 numbers, not all of them finite.
+__device__ __forceinline__ bool not_finite(const uint4 &u) {
+  auto biggest = [](uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a & 0x7fff7fffu), "r"(b & 0x7fff7fffu));
+    return r;
+  };
+  const uint32_t m = biggest(biggest(u.x, u.y), biggest(u.z, u.w)) & 0x7fff7fffu;
+  return (m & 0xffffu) >= 0x7f80u || (m >> 16) >= 0x7f80u;
 }
 
 __device__ __forceinline__ void stmatrix4(uint32_t at, const uint32_t (&r)[4]) {
