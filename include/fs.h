@@ -650,7 +650,9 @@ int fs_selftest_tree_wait(const void *q, const fs_cache *cache,
  *                 of Hkv, query head h reading kv head h / (H / Hkv).  Strides as
  *                 fs_rope's, multiples of 8 elements, pointers 16-byte aligned
  *                 (else FS_ERR_UNSUPPORTED); no negative ones, and 0 between tokens
- *                 only for T = 1 (FS_ERR_UNSUPPORTED).  out overlaps no input
+ *                 only for T = 1 (FS_ERR_UNSUPPORTED).  out overlaps no input, and its
+                 rows do not one another (each axis' stride passes what the axes of
+                 smaller strides take, else FS_ERR_INVALID_ARG)
  *   decay         [H] f32, the logarithm of the factor a token: 0 or below (-inf:
  *                 a token sees itself alone).  A constant of the model: there is no
  *                 gradient for it
@@ -716,7 +718,8 @@ int fs_linear_attn_bwd(const void *q, const void *k, const void *v, const long l
  *   gain, next_gain  [D] f32, or NULL: ones
  *   z, y          either may be NULL (not wanted; y NULL: no norm of z)
  * z may be x or residual and y may be x or gate, of the same type, with their
- * strides (in place); other overlaps give undefined results.  Computed in fp32,
+ * strides (in place).  Another output at an input's address, or two outputs at one:
+ * FS_ERR_INVALID_ARG; other overlaps give undefined results.  Computed in fp32,
  * y from z before its rounding; rounded once.  Squares and their sums are to fit fp32.
  * D <= 16384 (else FS_ERR_UNSUPPORTED), D a multiple of groups, eps >= 0.  One kernel. */
 int fs_block_norm(const void *x, long long x_stride, int dtype, const void *gate,
@@ -735,7 +738,7 @@ int fs_block_norm(const void *x, long long x_stride, int dtype, const void *gate
  *   ws            of fs_block_norm_workspace_bytes() bytes, for one call at a time; NULL
  *                 where neither dgain nor dnext_gain is wanted
  * dx may be x or dy, dgate may be gate, dresidual may be dz or residual, with their
- * strides; other overlaps give undefined results.  Sums over rows are fp32 within
+ * strides (else as above).  Sums over rows are fp32 within
  * a block's rows, then compensated in block order: deterministic.  One or two kernels. */
 size_t fs_block_norm_workspace_bytes(int M, int D);
 int fs_block_norm_bwd(const void *x, long long x_stride, int dtype, const void *gate,

@@ -1063,10 +1063,22 @@ int check_linear_rows(const void *p, const long long (&s)[3], int T) {
   return reinterpret_cast<uintptr_t>(p) % 16 ? FS_ERR_UNSUPPORTED : FS_OK;
 }
 
-int check_linear_out(const void *p, const long long (&s)[3], int batch, int H, int T) {
+// An output: its rows may not lie on one another (an axis' stride passes what the axes of smaller
+// strides take).
+int check_linear_out(const void *p, const long long (&s)[3], int batch, int H, int T, int d) {
   FS_TRY(check_linear_rows(p, s, T));
-  // (rows that lie on one another)
-  if ((batch > 1 && s[0] == 0) || (H > 1 && s[1] == 0)) return FS_ERR_INVALID_ARG;
+  const int n[3] = {batch, H, T};
+  bool done[3] = {};
+  long long span = d;
+  for (int i = 0; i < 3; ++i) {
+    int at = -1;
+    for (int j = 0; j < 3; ++j)
+      if (!done[j] && (at < 0 || s[j] < s[at])) at = j;
+    done[at] = true;
+    if (n[at] == 1) continue;
+    if (s[at] < span) return FS_ERR_INVALID_ARG;
+    span += s[at] * (n[at] - 1);
+  }
   return FS_OK;
 }
 
@@ -1131,7 +1143,7 @@ extern "C" int fs_linear_attn(const void *q, const void *k, const void *v, const
   FS_TRY(check_linear_rows(q, qs, T));
   FS_TRY(check_linear_rows(k, ks, T));
   FS_TRY(check_linear_rows(v, vs, T));
-  FS_TRY(check_linear_out(out, os, batch, H, T));
+  FS_TRY(check_linear_out(out, os, batch, H, T, d));
   if (out == q || out == k || out == v) return FS_ERR_INVALID_ARG;
   FS_TRY(check_states(state, state_out, true, (size_t)batch * H * d * d));
   const LinearLayout L = linear_layout(batch, H, Hkv, T, d, false);
@@ -1179,9 +1191,9 @@ extern "C" int fs_linear_attn_bwd(
   FS_TRY(check_linear_rows(k, ks, T));
   FS_TRY(check_linear_rows(v, vs, T));
   FS_TRY(check_linear_rows(dout, ds, T));
-  FS_TRY(check_linear_out(dq, gq, batch, H, T));
-  FS_TRY(check_linear_out(dk, gk, batch, Hkv, T));
-  FS_TRY(check_linear_out(dv, gv, batch, Hkv, T));
+  FS_TRY(check_linear_out(dq, gq, batch, H, T, d));
+  FS_TRY(check_linear_out(dk, gk, batch, Hkv, T, d));
+  FS_TRY(check_linear_out(dv, gv, batch, Hkv, T, d));
   for (const void *o : {dq, dk, dv})
     if (o == q || o == k || o == v || o == dout) return FS_ERR_INVALID_ARG;
   if (dq == dk || dq == dv || dk == dv) return FS_ERR_INVALID_ARG;
@@ -1272,6 +1284,26 @@ int check_norm(const NormArgs &a, int dtype, int res_dtype) {
   for (const void *p : {(const void *)a.gain, (const void *)a.next_gain, (const void *)a.dgain,
                         (const void *)a.dnext, (const void *)a.ws})
     if (reinterpret_cast<uintptr_t>(p) % 4) return FS_ERR_INVALID_ARG;
+  // In place: only where every row's inputs are read before its outputs are written, at the same
+  // places.
+  const struct { const void *p; long long s; bool r; } ins[] = {
+      {a.x, a.xs, false}, {a.gate, a.gs, false}, {a.residual, a.rs, true}, {a.dz, a.dzs, true}, {a.dy, a.dys, false}};
+  enum { kX = 1, kGate = 2, kResidual = 4, kDz = 8, kDy = 16 };
+  const int over[] = {kX | kResidual, kX | kGate, kX | kDy, kGate, kResidual | kDz};
+  const bool res[] = {true, false, false, false, true};
+  for (int i = 0; i < 5; ++i) {
+    if (!outs[i].p) continue;
+    for (int j = 0; j < i; ++j)
+      if (outs[i].p == outs[j].p) return FS_ERR_INVALID_ARG;
+    int same = 0;
+    for (int j = 0; j < 5; ++j) {
+      if (ins[j].p != outs[i].p) continue;
+      if ((ins[j].r ? r : x) != (res[i] ? r : x) || ins[j].s != outs[i].s) return FS_ERR_INVALID_ARG;
+      same |= 1 << j;
+    }
+    if (same && !(same & over[i])) return FS_ERR_INVALID_ARG;
+  }
+  if (a.dgain && a.dgain == a.dnext) return FS_ERR_INVALID_ARG;
   return FS_OK;
 }
 

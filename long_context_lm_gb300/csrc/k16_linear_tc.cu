@@ -188,13 +188,13 @@ __global__ void __launch_bounds__(StateCfg<D>::kThreads, StateCfg<D>::kBlocks)
       if (n < kC) {
         // what lies behind the sequence takes no part, whatever it is
         if (!(ok = WAIT(s.kfull, i))) break;
-        for (int u = t; u < (kC - n) * (D / 8); u += C::kStateThreads) {
-          const uint32_t at = swz128(n + u / (D / 8), u % 8);
-          *reinterpret_cast<uint4 *>(smem + C::kK + u % (D / 8) / 8 * kAtom + at) = make_uint4(0, 0, 0, 0);
-          if (u % (D / 8) < 8) *reinterpret_cast<uint4 *>(values + at) = make_uint4(0, 0, 0, 0);
-        }
-        tc::fence_async_smem();
-        asm volatile("bar.sync 1, %0;" ::"n"(C::kStateThreads) : "memory");
+        for (int u = t; u < (kC - n) * (D / 8); u += C::kStateThreads)
+          *reinterpret_cast<uint4 *>(smem + C::kK + u % (D / 8) / 8 * kAtom + swz128(n + u / (D / 8), u % 8)) =
+              make_uint4(0, 0, 0, 0);
+        // values: what this thread reads itself (the fence before the first slab's arrival is the keys')
+#pragma unroll 1
+        for (int row = r0; row < kC; row += C::kRows)
+          if (row >= n) *reinterpret_cast<uint4 *>(values + in + (row - r0) * 128) = make_uint4(0, 0, 0, 0);
       }
       const unsigned char *source = values + in;
       uint32_t some = 0;  // the bits of all third parts
@@ -426,10 +426,11 @@ struct RowShared {
   // S and tables; values looked through: their warps may be a chunk ahead of the rows', not two
   uint64_t ready[2], checked[2];
   uint64_t s_free, scores, inter, parts, done, o_free, fin;
+  uint64_t pairs[4];  // a chunk's rows of the second of two warps are in the values' place
   uint32_t tmem;
   bool turned[2];     // S is another sweep's, transposed
-  int odd[2];         // a chunk's values are not all finite
-  int bad[2][128];    // per column: the first such token in the sweep's order
+  int odd[2];         // i + 1: the values of the block's chunk i are not all finite
+  int bad[2][128];    // per column, as bad_mark
   Tables tables[2];
   Start start;
 };
@@ -452,8 +453,8 @@ __device__ __forceinline__ void look_through(RowShared &s, unsigned char *values
     for (int j = 0; j < 8; ++j) {
       if ((word[j / 2] >> j % 2 * 16 & 0x7f80u) != 0x7f80u) continue;
       word[j / 2] &= j % 2 ? 0xffffu : 0xffff0000u;
-      atomicMin(&s.bad[i & 1][ch * 8 + j], reverse ? kC - 1 - row : row);
-      s.odd[i & 1] = 1;
+      atomicMax(&s.bad[i & 1][ch * 8 + j], bad_mark(i, reverse ? kC - 1 - row : row));
+      s.odd[i & 1] = i + 1;
     }
   }
   tc::fence_async_smem();
@@ -490,13 +491,14 @@ __global__ void __launch_bounds__(RowCfg::kThreads, 2)
     for (uint64_t *x : {&s.qfull, &s.qempty, &s.kfull, &s.kempty, &s.vfull[0], &s.vfull[1], &s.s_free,
                         &s.scores, &s.inter, &s.done, &s.fin})
       tc::mbar_init(x, 1);
+    for (uint64_t &x : s.pairs) tc::mbar_init(&x, 1);
     for (uint64_t *x : {&s.ready[0], &s.ready[1]}) tc::mbar_init(x, C::kStateWarps);
     for (uint64_t *x : {&s.checked[0], &s.checked[1]}) tc::mbar_init(x, 2);
     for (uint64_t *x : {&s.vempty[0], &s.vempty[1], &s.parts, &s.o_free}) tc::mbar_init(x, 8);
     tc::mbar_fence_init();
     s.odd[0] = s.odd[1] = 0;
   }
-  for (int i = threadIdx.x; i < 256; i += C::kThreads) s.bad[i / 128][i % 128] = kC;
+  for (int i = threadIdx.x; i < 256; i += C::kThreads) s.bad[i / 128][i % 128] = 0;
   if (warp == 0) {
     const Start start = find_start(p, lane);
     if (lane == 0) s.start = start;
@@ -699,14 +701,9 @@ __global__ void __launch_bounds__(RowCfg::kThreads, 2)
       if (lane == 0) tc::mbar_arrive(&s.parts);
       if ((kTurns && !WAIT(s.checked[i & 1], i >> 1)) || !WAIT(s.done, i)) break;
       tc::fence_after_sync();
-      const bool odd = s.odd[i & 1] != 0;
-      storing = rows.store(p.a.sweep[u.z], &maps.out[u.z], p.out_axes[u.z], u.b, u.h, chunk, n, reverse,
-                           odd ? s.bad[i & 1] : nullptr, smem + C::kV + (i & 1) * C::kTile, &s.o_free);
-      if (odd) {  // clean for the chunk after the next
-        asm volatile("bar.sync 2, 256;" ::: "memory");
-        if (warp < 4 && rows.row < D) s.bad[i & 1][rows.row] = kC;
-        if (warp == 0 && lane == 0) s.odd[i & 1] = 0;
-      }
+      storing = rows.store(p.a.sweep[u.z], &maps.out[u.z], p.out_axes[u.z], u.b, u.h, chunk, n, i, reverse,
+                           s.odd[i & 1] == i + 1 ? s.bad[i & 1] : nullptr, smem + C::kV + (i & 1) * C::kTile,
+                           &s.o_free, s.pairs, p.err);
       fresh = u.next();
     }
     if (lane == 0) bulk_wait_read<0>();

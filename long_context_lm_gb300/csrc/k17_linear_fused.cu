@@ -56,11 +56,12 @@ struct Shared {
   uint64_t s_ready, s_free, scores, inter, parts, done, o_free, u_full, u_free, fin, fin_u;
   // values looked through: the states' warps may be a chunk ahead of the rows', not two
   uint64_t checked[2];
+  uint64_t pairs[4];  // a chunk's rows of the second of two warps are in the values' place
   uint32_t tmem;
-  int odd[2];                 // a chunk's values are not all finite
+  int odd[2];                 // i + 1: the values of the block's chunk i are not all finite
   float power[kC + 4];        // lam^n
   Tables tables;
-  int bad[2][128];            // per column: the first such token in the sweep's order
+  int bad[2][128];            // per column, as bad_mark
 };
 
 template <int D>
@@ -95,6 +96,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, D == 64 ? 2 : 1)
     for (uint64_t *x : {&s.parts, &s.o_free}) tc::mbar_init(x, 8);
     tc::mbar_init(&s.kempty, 2);  // read by the scores' product and by the slabs'
     tc::mbar_init(&s.fin_u, 1);
+    for (uint64_t &x : s.pairs) tc::mbar_init(&x, 1);
     tc::mbar_fence_init();
     s.odd[0] = s.odd[1] = 0;
   }
@@ -103,7 +105,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, D == 64 ? 2 : 1)
     s.power[i] = f.hi + f.lo;
   }
   fill_tables(s.tables, decay, reverse, p.a.scale, threadIdx.x, C::kThreads);
-  for (int i = threadIdx.x; i < 256; i += C::kThreads) s.bad[i / 128][i % 128] = kC;
+  for (int i = threadIdx.x; i < 256; i += C::kThreads) s.bad[i / 128][i % 128] = 0;
   if (warp == C::kMma) {
     tc::tmem_alloc(&s.tmem, C::kCols);
     tc::tmem_relinquish();
@@ -285,21 +287,21 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, D == 64 ? 2 : 1)
     unsigned char *slab = smem + C::kSlab0 + atom * C::kSlabAtom + in;
     for (int i = 0; i < chunks; ++i) {
       const int n = st.size(st.chunk(from + i, reverse));
-      unsigned char *values = smem + C::kV + i % C::kValues * C::kTile;
+      unsigned char *source = smem + C::kV + i % C::kValues * C::kTile + atom * kAtom + in;
       if (!WAIT(s.vfull[i % C::kValues], i / C::kValues)) break;
       if (n < kC) {
         // what lies behind the sequence takes no part, whatever it is
         if (!WAIT(s.kfull, i)) break;
         unsigned char *keys = smem + C::kK;
-        for (int u = t; u < (kC - n) * (D / 8); u += F::kThreads) {
-          const uint32_t at = u % (D / 8) / 8 * kAtom + swz128(n + u / (D / 8), u % 8);
-          *reinterpret_cast<uint4 *>(keys + at) = make_uint4(0, 0, 0, 0);
-          *reinterpret_cast<uint4 *>(values + at) = make_uint4(0, 0, 0, 0);
-        }
-        tc::fence_async_smem();
-        asm volatile("bar.sync 1, %0;" ::"n"(F::kThreads) : "memory");
+        for (int u = t; u < (kC - n) * (D / 8); u += F::kThreads)
+          *reinterpret_cast<uint4 *>(keys + u % (D / 8) / 8 * kAtom + swz128(n + u / (D / 8), u % 8)) =
+              make_uint4(0, 0, 0, 0);
+        // values: those that this thread reads itself (the fence before the first slab's arrival is
+        // for all of them)
+#pragma unroll 1
+        for (int row = r16; row < kC; row += 16)
+          if (row >= n) *reinterpret_cast<uint4 *>(source + (row - r16) * 128) = make_uint4(0, 0, 0, 0);
       }
-      unsigned char *source = values + atom * kAtom + in;
       uint32_t some = 0;  // the bits of all third parts
       bool ok = true;
 #pragma unroll 1
@@ -335,12 +337,13 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, D == 64 ? 2 : 1)
             ((some & 0x7f80u) == 0x7f80u || (some & 0x7f800000u) == 0x7f800000u)) {
           for (int u = 0; u < kC / 16; ++u) {
             const int row = 16 * u + r16;
+            if (row >= n) break;
             uint32_t *word = reinterpret_cast<uint32_t *>(source + u * 2048);
             for (int c = 0; c < 8; ++c) {
               if ((word[c / 2] >> c % 2 * 16 & 0x7f80u) != 0x7f80u) continue;
               word[c / 2] &= c % 2 ? 0xffffu : 0xffff0000u;
-              atomicMin(&s.bad[i & 1][atom * 64 + ch * 8 + c], reverse ? kC - 1 - row : row);
-              s.odd[i & 1] = 1;
+              atomicMax(&s.bad[i & 1][atom * 64 + ch * 8 + c], bad_mark(i, reverse ? kC - 1 - row : row));
+              s.odd[i & 1] = i + 1;
             }
           }
         }
@@ -406,14 +409,9 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, D == 64 ? 2 : 1)
       if (lane == 0) tc::mbar_arrive(&s.parts);
       if (!WAIT(s.checked[i & 1], i >> 1) || !WAIT(s.done, i)) break;
       tc::fence_after_sync();
-      const bool odd = s.odd[i & 1] != 0;
-      storing = rows.store(w, &maps.out[blockIdx.z], p.out_axes[blockIdx.z], b, h, chunk, n, reverse,
-                           odd ? s.bad[i & 1] : nullptr, smem + C::kV + (i & 1) * C::kTile, &s.o_free);
-      if (odd) {  // clean for the chunk after the next
-        asm volatile("bar.sync 2, 256;" ::: "memory");
-        if (warp < 4 && rows.row < D) s.bad[i & 1][rows.row] = kC;
-        if (warp == 0 && lane == 0) s.odd[i & 1] = 0;
-      }
+      storing = rows.store(w, &maps.out[blockIdx.z], p.out_axes[blockIdx.z], b, h, chunk, n, i, reverse,
+                           s.odd[i & 1] == i + 1 ? s.bad[i & 1] : nullptr, smem + C::kV + (i & 1) * C::kTile,
+                           &s.o_free, s.pairs, p.err);
     }
     if (lane == 0) bulk_wait_read<0>();
   }

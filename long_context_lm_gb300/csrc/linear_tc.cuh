@@ -203,6 +203,11 @@ struct Publisher {
   }
 };
 
+// Values that are not finite: per column the first such token of the block's chunk i, `at` tokens from
+// the chunk's start in the sweep's order.  Marks of later chunks are greater, those of earlier tokens
+// of one chunk too, so that nothing needs clearing: a row `at` is behind one if mark >= bad_mark(i, at).
+__device__ __forceinline__ int bad_mark(int i, int at) { return (i + 1) << 8 | (255 - at); }
+
 // A warp of the rows' eight: 32 rows, half of the columns.
 template <int D>
 struct RowWarp {
@@ -286,12 +291,12 @@ struct RowWarp {
   }
 
   // The finished rows.  Whole warps of bf16 rows leave by TMA by way of the values' place, 64 columns at
-  // a time; the last rows of a sequence, and fp32 parts, from their threads.  `bad` (or null):
-  // from which row on, in the sweep's order, a column is not finite.  Arrives on o_free
+  // a time; the last rows of a sequence, and fp32 parts, from their threads.  `i`: which chunk of
+  // the block's.  `bad` (or null): columns that are not finite, as bad_mark.  Arrives on o_free
   // when the accumulator is read.  True: the values' place is read until bulk_wait_read (lane 0).
   __device__ __forceinline__ bool store(const LinearSweep &w, const CUtensorMap *map, const int (&axes)[2], int b,
-                                        int h, int chunk, int n, bool reverse, const int *bad,
-                                        unsigned char *values, uint64_t *o_free) const {
+                                        int h, int chunk, int n, int i, bool reverse, const int *bad,
+                                        unsigned char *values, uint64_t *o_free, uint64_t *pairs, int *err) const {
     const bool whole = 32 * quarter + 32 <= n && !w.out_f32;
     unsigned char *box = values + (D == 64 ? 0 : half * kAtom) + quarter * 4096;
     const long long to = b * w.os[0] + h * w.os[1] + (chunk * (long long)kC + row) * w.os[2] + half * (D / 2);
@@ -308,7 +313,7 @@ struct RowWarp {
       if (bad) {
 #pragma unroll 1
         for (int e = 0; e < 16; ++e) {
-          const bool gone = bad[half * (D / 2) + 16 * c + e] <= (reverse ? kC - 1 - row : row);
+          const bool gone = bad[half * (D / 2) + 16 * c + e] >= bad_mark(i, reverse ? kC - 1 - row : row);
 #pragma unroll
           for (int k = 0; k < 16; ++k)
             if (k == e && gone) x[k] = 0x7fc00000u;
@@ -338,13 +343,11 @@ struct RowWarp {
           *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(w.out) + to + 16 * c + 8 * e) = z;
       }
     }
-    if (!whole) return false;
-    tc::fence_async_smem();
-    if (D == 64)  // two warps' halves of one box
-      asm volatile("bar.sync %0, 64;" ::"r"(3 + quarter) : "memory");
-    else
-      __syncwarp();
-    if (lane != 0 || (D == 64 && half != 0)) return false;
+    if (whole) tc::fence_async_smem();
+    __syncwarp();
+    if (D == 64 && half != 0 && lane == 0) tc::mbar_arrive(&pairs[quarter]);  // two warps' halves of one box
+    if (!whole || lane != 0 || (D == 64 && half != 0)) return false;
+    if (D == 64 && !tc::mbar_wait(&pairs[quarter], i & 1, err)) return false;
     store_rows(box, map, D == 64 ? 0 : 64 * half, chunk * kC + 32 * quarter, h * axes[1], b * axes[0]);
     bulk_commit();
     return true;

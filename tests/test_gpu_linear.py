@@ -303,3 +303,29 @@ def test_long_sequences_and_large_batches(B, H, T, d):
         got = fs.fs_linear_attn(q[:, :, cut], k[:, :, cut], v[:, :, cut], decay, state=state, state_out=state)
         near(out[:, :, cut], got.double(), 2.0 ** -7 * got.double().abs() + 2.0 ** -14 * M[:, :, cut].double())
     near(S1, state.double(), 2 * state_tol(MS.double(), T))
+
+
+@pytest.mark.parametrize("B,H,Hkv,T,d", [(2, 2, 1, 200, 64), (1, 2, 2, 2000, 64), (2, 4, 2, 2000, 128)])
+def test_an_error_word_that_is_set_ends_the_waits(B, H, Hkv, T, d):
+    """A call whose workspace holds an error gives its waits up early, wherever each one is, and ends;
+    the status is reported; with the word cleared the next call is whole again."""
+    q, k, v, dout, decay, S0, G, _ = inputs(B, H, Hkv, T, d, seed=7)
+    ws = fs.fs_linear_workspace(B, H, Hkv, T, d, q.device)
+    wb = fs.fs_linear_workspace(B, H, Hkv, T, d, q.device, backward=True)
+
+    def run():
+        return (fs.fs_linear_attn(q, k, v, decay, state=S0, ws=ws),
+                *fs.fs_linear_attn_bwd(q, k, v, decay, dout, state=S0, dstate_out=G, ws=wb))
+
+    want = run()
+    fs.fs_check_status(ws), fs.fs_check_status(wb)
+    for w in (ws, wb):
+        w[:4].view(torch.int32).fill_(fs.FS_ERR_TIMEOUT)
+    run()
+    for w in (ws, wb):
+        with pytest.raises(fs.FSError):
+            fs.fs_check_status(w)
+        w[:256].zero_()
+    for a, b in zip(run(), want):
+        assert torch.equal(a, b)
+    fs.fs_check_status(ws), fs.fs_check_status(wb)

@@ -81,7 +81,7 @@ def test_parts_missing(M, D, groups, dt, rdt, gate, residual, next, gains):
 @pytest.mark.parametrize("M,D", [(5000, 64), (20000, 40), (3001, 512), (2000, 1024), (1500, 2048), (700, 4096)])
 def test_many_rows(M, D):
     # sums over rows: a block's rows in fp32 (at most M / (4 x 152) of them to a team, each addition
-    # 2^-24 of the sum's magnitude), the blocks' in fp64
+    # 2^-24 of the sum's magnitude), the blocks' with their errors carried
     check(M, D, 1, BF, BF, True, True, True, seed=5)
 
 

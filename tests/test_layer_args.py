@@ -143,3 +143,38 @@ def test_binding_refuses_host_tensors_and_sizes_past_32_bits():
         fs.fs_block_norm_workspace(2 ** 32 + 4, 64, "cpu")
     with pytest.raises(ValueError):
         fs.fs_linear_workspace(1, 2, 2, 2 ** 32 + 1, 64, "cpu")
+
+
+@pytest.mark.parametrize("kw", [
+    dict(os=S(8192, 2048, 56)),              # tokens
+    dict(os=S(8192, 1984, 64)),              # heads
+    dict(os=S(4096, 2048, 64)),              # sequences
+])
+def test_linear_rows_that_lie_on_one_another(kw):
+    assert linear(**kw) == INVALID
+    assert linear_bwd(gq=kw["os"]) == INVALID
+
+
+@pytest.mark.parametrize("kw", [
+    dict(y=0x2000),                                    # both outputs at one place
+    dict(y=0x4000, res=0x4000),                        # y over the residual
+    dict(z=0x4000, gate=0x4000),                       # z over the gate
+    dict(z=0x1000, zs=128),                            # in place with other rows
+    dict(z=0x1000, rdtype=1),                          # in place with another type
+    dict(z=0x4000, res=0x4000, rs=128),
+])
+def test_norm_in_place_refusals(kw):
+    assert norm(**kw) == INVALID
+
+
+@pytest.mark.parametrize("kw", [
+    dict(dx=0x2000),                                   # dx over dz
+    dict(dx=0x4000, gate=0x4000),
+    dict(dx=0x1000, dxs=128),
+    dict(gate=0x4000, dgate=0x3000),                   # both outputs at one place
+    dict(gate=0x4000, dgate=0x2000),
+    dict(res=0x4000, dres=0x1000),
+    dict(dy=0x5000, gain=0x100, next=0x200, dgain=0x600, dnext=0x600, ws=256, n=1 << 40),
+])
+def test_norm_backward_in_place_refusals(kw):
+    assert norm_bwd(**kw) == INVALID
