@@ -14,9 +14,11 @@
 // Memory bounds both: every tensor is read or written once.  A team of threads takes a
 // row.  In the backward pass it takes one after another, each thread its own vectors, and the
 // next row is under way into shared memory (asynchronous copies that nobody else waits
-// for) while it works on this one: 16384 x 1024 gated heads in bf16 42 us instead of 65;
-// rows too wide for that, and rows off sixteen bytes, are read where they lie.  (The
-// forward pass gained nothing from it: 77 us against 71, and 464 against 272 where rows are
+// for) while it works on this one: 16384 x 1024 gated heads in bf16 42 us instead of 65.  Of what
+// is read to the row's end (x and the gate) there are always two rows, of the rest too (kTwice) or one,
+// fetched anew once it has been read: less shared memory and fewer registers for one more block
+// on the SM.  Rows too wide for that, and rows off sixteen bytes, are read where they lie.
+// (The forward pass gained nothing from it: 77 us against 71, and 464 against 272 where rows are
 // wide and one block had an SM to itself.)
 // A thread has read an element of an input for the last time before it writes the
 // output that may take its place.  Sums are fp32 in a fixed order.  The
@@ -119,7 +121,7 @@ __device__ __forceinline__ void store(T *p, int left, const f2 (&x)[V / 2], bool
   }
 }
 
-// A thread's vectors of one tensor's rows.  kStaged: this row and the next in shared memory, piece
+// A thread's vectors of one tensor's rows.  kStaged: one or two of them in shared memory, piece
 // after piece, threads side by side.
 template <bool kStaged, bool kWhole, typename T, int V, int N>
 struct Slot {
@@ -128,12 +130,12 @@ struct Slot {
   uint32_t stage; // bytes from a stage to the next
   const T *row;   // the next row to fetch (not kStaged: to read), at this thread's first element
   long long step; // elements to the team's row after it
-  __device__ __forceinline__ void init(uint32_t &free, const void *p, long long stride, long long first, int rows,
-                                       int e0) {
+  __device__ __forceinline__ void init(uint32_t &free, int stages, const void *p, long long stride, long long first,
+                                       int rows, int e0) {
     at = stage = 0;
     if constexpr (kStaged) {
       stage = N * kPieces * blockDim.x * 16;
-      if (p) at = free + threadIdx.x * 16, free += 2 * stage;
+      if (p) at = free + threadIdx.x * 16, free += stages * stage;
     }
     row = static_cast<const T *>(p) + first * stride + e0;
     step = rows * stride;
@@ -450,8 +452,8 @@ __global__ void __launch_bounds__(kTeam ? 256 : 512, sizeof(TX) == 4 || N * 8 > 
   }
 }
 
-template <typename TX, typename TR, int kTeam, int N, bool kWhole, bool kStaged>
-__global__ void __launch_bounds__(kTeam ? 256 : 512, 1) k15_norm_bwd_kernel(const __grid_constant__ NormArgs a) {
+template <typename TX, typename TR, int kTeam, int N, bool kWhole, bool kStaged, bool kTwice>
+__global__ void __maxnreg__(!kTwice ? 96 : kTeam ? 255 : 128) k15_norm_bwd_kernel(const __grid_constant__ NormArgs a) {
   constexpr int V = 16 / sizeof(TX);
   constexpr bool kExact = sizeof(TX) == 4;
   extern __shared__ uint4 slots[];
@@ -468,16 +470,15 @@ __global__ void __launch_bounds__(kTeam ? 256 : 512, 1) k15_norm_bwd_kernel(cons
   uint32_t free = smem_u32(slots);
   Slot<kStaged, kWhole, TX, V, N> x, gate, dy;
   Slot<kStaged, kWhole, TR, V, N> dz, res;
-  Slot<kStaged, kWhole, float, V, N> gain, next;  // (one row: stage 0)
-  x.init(free, a.x, a.xs, row, rows, e0);
-  gate.init(free, a.gate, a.gs, row, rows, e0);
-  dz.init(free, a.dz, a.dzs, row, rows, e0);
-  dy.init(free, a.dy, a.dys, row, rows, e0);
-  res.init(free, a.next ? a.residual : nullptr, a.rs, row, rows, e0);
-  gain.init(free, a.gain, 0, 0, 0, e0);
-  if (a.gain) free -= gain.stage;
-  next.init(free, a.next_gain, 0, 0, 0, e0);
-  if (a.next_gain) free -= next.stage;
+  Slot<kStaged, kWhole, float, V, N> gain, next;
+  constexpr int stages = kTwice ? 2 : 1;
+  x.init(free, 2, a.x, a.xs, row, rows, e0);
+  gate.init(free, 2, a.gate, a.gs, row, rows, e0);
+  dz.init(free, stages, a.dz, a.dzs, row, rows, e0);
+  dy.init(free, stages, a.dy, a.dys, row, rows, e0);
+  res.init(free, stages, a.next ? a.residual : nullptr, a.rs, row, rows, e0);
+  gain.init(free, 1, a.gain, 0, 0, 0, e0);
+  next.init(free, 1, a.next_gain, 0, 0, 0, e0);
   if constexpr (kStaged) gain.fill(a.D - e0, apart), next.fill(a.D - e0, apart);
   team.list = reinterpret_cast<float *>(slots) + (free - smem_u32(slots)) / 4 + team.team * a.list;
   TX *dxr = static_cast<TX *>(a.dx) + row * a.dxs + e0, *dgr = static_cast<TX *>(a.dgate) + row * a.dgs + e0;
@@ -486,21 +487,29 @@ __global__ void __launch_bounds__(kTeam ? 256 : 512, 1) k15_norm_bwd_kernel(cons
     const int left = have ? a.D - e0 : 0;
     x.fetch(which, left, apart);
     gate.fetch(which, left, apart);
+  };
+  auto fetch_rest = [&](int which, bool have) {
+    const int left = have ? a.D - e0 : 0;
     dz.fetch(which, left, apart);
     dy.fetch(which, left, apart);
     res.fetch(which, left, apart);
-    cp_async_commit();
   };
-  if constexpr (kStaged) fetch(0, row < a.M);
+  if constexpr (kStaged) {
+    fetch(0, row < a.M);
+    fetch_rest(0, row < a.M);
+    cp_async_commit();
+  }
   f2 dgain[N][V / 2] = {}, dnext[N][V / 2] = {};  // (zeros of a team without a row add nothing)
   const f2 scale = both(a.scale);
   int which = 0;
   for (; row - team.team < a.M; row += rows, which ^= 1) {
     if constexpr (kStaged) {
       fetch(which ^ 1, row + rows < a.M);
+      if constexpr (kTwice) fetch_rest(which ^ 1, row + rows < a.M);
+      cp_async_commit();
       cp_async_wait<1>();
     }
-    const int left = row < a.M ? a.D - e0 : 0;
+    const int left = row < a.M ? a.D - e0 : 0, rest = kTwice ? which : 0;
     PerGroup<kWhole, V> inv[N];
     team.factors(inv, a, [&](int i) { return x.get(which, i, left, apart); });
     f2 sig[N][V / 2], g[N][V / 2];  // g: the gradient that reaches z
@@ -512,7 +521,7 @@ __global__ void __launch_bounds__(kTeam ? 256 : 512, 1) k15_norm_bwd_kernel(cons
         for (int c = 0; c < V / 2; ++c) sig[i][c] = sigmoid2<kExact>(gv.get(c));
       }
       if (a.dz) {
-        const Raw<TR, V> dv = dz.get(which, i, left, apart);
+        const Raw<TR, V> dv = dz.get(rest, i, left, apart);
 #pragma unroll
         for (int c = 0; c < V / 2; ++c) g[i][c] = dv.get(c);
       } else {
@@ -538,14 +547,14 @@ __global__ void __launch_bounds__(kTeam ? 256 : 512, 1) k15_norm_bwd_kernel(cons
           for (int c = 0; c < V / 2; ++c) z[i][c] = mul2(z[i][c], mul2(gv.get(c), sig[i][c]));
         }
         if (a.residual) {
-          const Raw<TR, V> rv = res.get(which, i, left, apart);
+          const Raw<TR, V> rv = res.get(rest, i, left, apart);
 #pragma unroll
           for (int c = 0; c < V / 2; ++c) z[i][c] = madd2(scale, z[i][c], rv.get(c));
         } else {
 #pragma unroll
           for (int c = 0; c < V / 2; ++c) z[i][c] = mul2(scale, z[i][c]);
         }
-        const Raw<TX, V> dv = dy.get(which, i, left, apart);
+        const Raw<TX, V> dv = dy.get(rest, i, left, apart);
         if (a.next_gain) {
           const Raw<float, V> nv = next.get(0, i, a.D - e0, apart);
 #pragma unroll
@@ -563,7 +572,7 @@ __global__ void __launch_bounds__(kTeam ? 256 : 512, 1) k15_norm_bwd_kernel(cons
       const f2 rf = both(r), mc = both(-r * r * s[1] * a.inv_D);
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        const Raw<TX, V> dv = dy.get(which, i, left, apart);
+        const Raw<TX, V> dv = dy.get(rest, i, left, apart);
         f2 w[V / 2];
 #pragma unroll
         for (int c = 0; c < V / 2; ++c) {
@@ -578,6 +587,10 @@ __global__ void __launch_bounds__(kTeam ? 256 : 512, 1) k15_norm_bwd_kernel(cons
 #pragma unroll
         for (int c = 0; c < V / 2; ++c) g[i][c] = madd2(rf, madd2(mc, z[i][c], w[c]), g[i][c]);
       }
+    }
+    if constexpr (kStaged && !kTwice) {  // (these have been read)
+      fetch_rest(0, row + rows < a.M);
+      cp_async_commit();
     }
     if (a.dres) {
 #pragma unroll
@@ -614,7 +627,9 @@ __global__ void __launch_bounds__(kTeam ? 256 : 512, 1) k15_norm_bwd_kernel(cons
     dgr += rows * a.dgs;
     if (a.mode != kNone) {
       PerGroup<kWhole, V> p[N];
-      team.add_groups(p, a, [&](int i, int c) { return mul2(g[i][c], mul2(x.get(which, i, left, apart).get(c), inv[i].get(c))); });
+      team.add_groups(p, a, [&](int i, int c) {
+        return mul2(g[i][c], mul2(x.get(which, i, left, apart).get(c), inv[i].get(c)));
+      });
       const f2 mn = both(-a.inv_n);
 #pragma unroll
       for (int i = 0; i < N; ++i) {
@@ -718,14 +733,14 @@ bool whole(const NormArgs &a) {
   return true;
 }
 
-// Bytes of shared memory that both rows of all of a block's inputs and the gains take in the
-// backward pass.
-template <typename TX, typename TR, int N>
+// Bytes of shared memory that the rows of a block's inputs and the gains take in the backward pass.
+template <typename TX, typename TR, int N, bool kTwice>
 size_t staged_bytes(const NormArgs &a, int threads) {
   constexpr int V = 16 / sizeof(TX);
-  const size_t x = 2 * N * V * sizeof(TX) * threads, r = 2 * N * V * sizeof(TR) * threads;
+  const size_t x = N * V * sizeof(TX) * threads, r = N * V * sizeof(TR) * threads;
   const size_t gain = N * V * sizeof(float) * threads;
-  return x + (a.gate ? x : 0) + (a.dz ? r : 0) + (a.dy ? x : 0) + (a.next && a.residual ? r : 0) +
+  constexpr int k = kTwice ? 2 : 1;
+  return 2 * x + (a.gate ? 2 * x : 0) + k * ((a.dz ? r : 0) + (a.dy ? x : 0)) + (a.next && a.residual ? k * r : 0) +
          (a.gain ? gain : 0) + (a.next_gain ? gain : 0);
 }
 
@@ -739,7 +754,7 @@ bool wide(const NormArgs &a) {
   return !a.x_f32;
 }
 
-template <bool kBack, typename TX, typename TR, int kTeam, int N, bool kWhole, bool kStaged>
+template <bool kBack, typename TX, typename TR, int kTeam, int N, bool kWhole, bool kStaged, bool kTwice = true>
 cudaError_t go(NormArgs a, int threads, cudaStream_t st) {
   constexpr int V = 16 / sizeof(TX);
   const int n = a.groups ? a.D / a.groups : 1, teams = kTeam ? 256 / kTeam : 1;
@@ -751,13 +766,13 @@ cudaError_t go(NormArgs a, int threads, cudaStream_t st) {
            : a.groups == 1 ? kRow
            : kWhole && a.per <= (kTeam ? kTeam : 32) && (a.per & (a.per - 1)) == 0 ? kShuffle : kList;
   a.list = a.mode == kList ? (kWhole ? a.D / V : a.D) + a.groups : 0;
-  size_t smem = (kBack && kStaged ? staged_bytes<TX, TR, N>(a, threads) : 0) + (size_t)teams * a.list * 4;
-  if (kBack && teams > 1 && smem < (size_t)a.D * 4) smem = (size_t)a.D * 4;
   void (*f)(NormArgs);
   if constexpr (kBack)
-    f = k15_norm_bwd_kernel<TX, TR, kTeam, N, kWhole, kStaged>;
+    f = k15_norm_bwd_kernel<TX, TR, kTeam, N, kWhole, kStaged, kTwice>;
   else
     f = k15_norm_kernel<TX, TR, kTeam, N, kWhole>;
+  size_t smem = (kBack && kStaged ? staged_bytes<TX, TR, N, kTwice>(a, threads) : 0) + (size_t)teams * a.list * 4;
+  if (kBack && teams > 1 && smem < (size_t)a.D * 4) smem = (size_t)a.D * 4;
   cudaError_t e;
   if (smem + 1024 > 48 * 1024 &&
       (e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess)
@@ -767,17 +782,15 @@ cudaError_t go(NormArgs a, int threads, cudaStream_t st) {
     f<<<(unsigned)blocks, threads, smem, st>>>(a);
     return cudaGetLastError();
   }
-  // as many blocks as are resident at once: what shared memory and registers leave
+  // as many blocks as are resident at once: what registers, threads and shared memory leave
   static const int regs = [&] {
     cudaFuncAttributes attr;
-    return cudaFuncGetAttributes(&attr, f) == cudaSuccess ? attr.numRegs : 128;
+    return cudaFuncGetAttributes(&attr, f) == cudaSuccess ? attr.numRegs : 255;
   }();
-  int resident = 65536 / ((regs + 7) / 8 * 8 * threads);
-  const int by_smem = (int)(227 * 1024 / (smem + 1024)), by_threads = 2048 / threads;
-  resident = resident < by_smem ? resident : by_smem;
-  resident = resident < by_threads ? resident : by_threads;
-  int most = 152 * (resident < 1 ? 1 : resident);
-  if (most > kMaxBlocks) most = kMaxBlocks;
+  int resident = kMaxBlocks / 152;
+  for (int x : {65536 / ((regs + 7) / 8 * 8 * threads), 2048 / threads, (int)(227 * 1024 / (smem + 1024))})
+    resident = x < resident ? x : resident;
+  const int most = 152 * (resident < 1 ? 1 : resident);
   const int grid = (int)(blocks < most ? blocks : most);
   f<<<grid, threads, smem, st>>>(a);
   e = cudaGetLastError();
@@ -801,15 +814,21 @@ cudaError_t pick(const NormArgs &a, cudaStream_t st) {
     if (D <= 128) return go<kBack, TX, TR, 8, k16, false, false>(a, 256, st);
     return go<kBack, TX, TR, 0, k32, false, false>(a, threads(k32), st);
   }
-  if (D <= 64) return go<kBack, TX, TR, 8, k8, true, true>(a, 256, st);
-  if (D <= 256) return go<kBack, TX, TR, 32, k8, true, true>(a, 256, st);
+  if (D <= 64) return go<kBack, TX, TR, 8, k8, true, true, false>(a, 256, st);
+  if (D <= 256) return go<kBack, TX, TR, 32, k8, true, true, false>(a, 256, st);
   if (D <= 512) return go<kBack, TX, TR, 32, k16, true, true>(a, 256, st);
   if constexpr (kBack) {
-    if (D <= 4096) return go<kBack, TX, TR, 0, k8, true, true>(a, threads(k8), st);
+    // Eight elements a thread want 128 registers and two rows in shared memory and can do with 96
+    // and less (bf16 rows of 2048, two blocks an SM either way: 72 us and 78): where that makes
+    // room for another block (of 2560, one or two: 132 us and 99; 2500 in fp32: 170 and 135).
+    const int n = threads(k8), with96 = 65536 / 96 / n, with128 = 65536 / 128 / n;
+    if (D <= 4096 && with128 < with96 && with128 < kMaxBlocks / 152)
+      return go<kBack, TX, TR, 0, k8, true, true, false>(a, n, st);
+    if (D <= 4096) return go<kBack, TX, TR, 0, k8, true, true>(a, n, st);
   }
   if constexpr (kBack) {
     const int n = threads(k16);
-    if (n <= 512 && staged_bytes<TX, TR, k16>(a, n) + (D / V + a.groups) * 4 <= 226 * 1024)
+    if (n <= 512 && staged_bytes<TX, TR, k16, true>(a, n) + (D / V + a.groups) * 4 <= 226 * 1024)
       return go<kBack, TX, TR, 0, k16, true, true>(a, n, st);
   } else {
     if (D <= 8192) return go<kBack, TX, TR, 0, k16, true, true>(a, threads(k16), st);
