@@ -762,7 +762,7 @@ struct Plan {
 };
 // (Bands small enough for the L2 to keep their states and keys between the passes cost more launches
 // than they save: 65536 tokens x 16 heads in bands of 40 MB 289 us, of 80 MB 245, in one 210.)
-constexpr size_t kBandBytes = (size_t)256 << 20;
+constexpr size_t kBandBytes = (size_t)160 << 20;
 Plan plan_of(int sweeps, int pairs, int T, int d) {
   Plan q{};
   const size_t matrix = (size_t)d * d * 4;

@@ -329,3 +329,54 @@ def test_an_error_word_that_is_set_ends_the_waits(B, H, Hkv, T, d):
     for a, b in zip(run(), want):
         assert torch.equal(a, b)
     fs.fs_check_status(ws), fs.fs_check_status(wb)
+
+
+@pytest.mark.parametrize("B,H,Hkv,T,d", [(2, 4, 2, 1300, 64), (3, 6, 1, 1999, 64), (2, 6, 3, 1300, 128)])
+@pytest.mark.parametrize("state,ragged", [(True, False), (False, True), (True, True)])
+def test_shared_heads_of_longer_prompts(B, H, Hkv, T, d, state, ragged):
+    test_forward((B, H, Hkv, T, d), state, ragged)
+    test_backward((B, H, Hkv, T, d), state, ragged)
+
+
+@pytest.mark.parametrize("B,H,Hkv,T,d,counts", [(3, 33, 11, 7000, 64, (7000, 3000, 0)), (1, 100, 100, 7000, 64, None),
+                                                (2, 24, 8, 5000, 128, (4999, 1111))])
+def test_gradients_of_long_sequences(B, H, Hkv, T, d, counts):
+    # against the calls in pieces of 900 tokens, whose states and states' gradients chain them; tolerances
+    # as in the forward's test
+    q, k, v, dout, _, S0, G, _ = inputs(B, H, Hkv, T, d, seed=4)
+    count = None if counts is None else torch.tensor(counts, dtype=torch.int32, device="cuda")
+    decay = -torch.exp2(-torch.arange(H, device="cuda").float() % 12 - 3)
+    got = fs.fs_linear_attn_bwd(q, k, v, decay, dout, state=S0, dstate_out=G, count=count,
+                                dstate=(dS := torch.empty_like(S0)))
+    M = fs.fs_linear_attn_bwd(*(t.abs() for t in (q, k, v)), decay, dout.abs(), state=S0.abs(), dstate_out=G.abs(),
+                              count=count, dstate=(MS := torch.empty_like(S0)))
+    cuts = [slice(a, min(T, a + 900)) for a in range(0, T, 900)]
+    part = [None if count is None else (count - c.start).clamp(0, c.stop - c.start) for c in cuts]
+    states = [S0]
+    for c, n in zip(cuts[:-1], part):
+        states.append(torch.empty_like(S0))
+        fs.fs_linear_attn(q[:, :, c], k[:, :, c], v[:, :, c], decay, state=states[-2], state_out=states[-1], count=n)
+    for c, n, S in reversed(list(zip(cuts, part, states))):
+        want = fs.fs_linear_attn_bwd(q[:, :, c], k[:, :, c], v[:, :, c], decay, dout[:, :, c], state=S, dstate_out=G,
+                                     count=n, dstate=(back := torch.empty_like(S0)))
+        G = back
+        for x, w, m in zip(got, want, M):
+            near(x[:, :, c], w.double(), 2.0 ** -7 * w.double().abs() + 2.0 ** -14 * m[:, :, c].double())
+    near(dS, G.double(), 2 * state_tol(MS.double(), T))
+
+
+@pytest.mark.parametrize("which", range(4))
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("H,T,d", [(2, 9, 64), (2, 300, 64), (3, 1400, 64), (2, 1400, 128)])
+def test_gradients_where_an_input_is_not_finite(which, value, H, T, d):
+    # reach exactly the gradients that the definition's reach: of that token, of earlier and later ones
+    a = list(inputs(1, H, H, T, d, seed=T + which)[:4])
+    decay = torch.tensor([-0.01, -0.3, 0.0][:H], device="cuda")
+    M = ref.linear_grads(*(t.abs() for t in a[:3]), decay, a[3].abs())
+    a[which][0, 1, T // 2 + 1, 5] = value
+    got = fs.fs_linear_attn_bwd(*a[:3], decay, a[3])
+    want = ref.linear_grads(*a[:3], decay, a[3])
+    for x, w, m in zip(got, want, M):
+        fine = w.isfinite()
+        assert torch.equal(x.isfinite(), fine)
+        near(torch.where(fine, x, 0), torch.where(fine, w, 0), 2.0 ** -8 * w.abs().nan_to_num(0, 0, 0) + 2.0 ** -15 * m + 1e-30)
