@@ -7,7 +7,8 @@
 // For a decoding step the state's bytes are everything (read once, written once:
 // 2 x 4 d^2 bytes against 8 d bytes of rows), so all of a thread's state is under way
 // before anything is computed, and a thread has enough of it (32 elements at d = 128)
-// to carry the decay's exponential and the sums over rows.
+// to carry the decay's exponential and the sums over rows.  128 sequences x 16 heads of
+// 128: 268 MB of states in 43.6 us, 6.2 TB/s, 91% of a copy's rate.
 // lam goes in as two fp32 numbers (linear.cuh): as one it would be off by up to
 // 2^-25 in the same direction at every token, and a head with a long memory adds
 // that up over thousands of them.

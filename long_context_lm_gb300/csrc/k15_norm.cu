@@ -11,7 +11,11 @@
 //   dgate = scale g h gain silu'(gate),   dgain = sum over rows of scale g silu(gate) h
 //   dx = r_g (u - h mean_group(u h)),     u = scale g silu(gate) gain
 //
-// Memory bounds both: every tensor is read or written once.  A team of threads takes a
+// Every tensor is read or written once.  Memory bounds the forward pass: 65536 x 16 gated heads
+// of 64 in bf16 67 us, 6.0 TB/s; 16384 x 8192 with an fp32 residual and the next norm 259 us, 6.2 TB/s.
+// The backward pass is bound by its instructions (16384 x 16 gated heads 46 us, two thirds of
+// all issue slots) and by its sums over a row, one after the other (8191 x 2500 in fp32 135 us,
+// 4.9 TB/s).  A team of threads takes a
 // row.  In the backward pass it takes one after another, each thread its own vectors, and the
 // next row is under way into shared memory (asynchronous copies that nobody else waits
 // for) while it works on this one: 16384 x 1024 gated heads in bf16 42 us instead of 65.  Of what

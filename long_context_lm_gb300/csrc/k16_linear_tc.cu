@@ -25,7 +25,7 @@
 // but with few heads needs the stretches' states beforehand, by a pass as long as the first here,
 // and with any number of heads leaves blocks without work.  65536 tokens x 16 heads: 263 us in one
 // pass, 210 in two.  States of heads of 128 are half of a chunk's rows (64 KB of 128; of 64 a
-// quarter): 5 ragged sequences of 8191 x 16 heads of 128: 493 us in two passes, 296 in one.
+// quarter): 5 ragged sequences of 8191 x 16 heads of 128: 493 us in two passes, 292 in one.
 //
 // What bounds it: 65536 tokens x 16 heads move 1.07 GB in two passes (537 MB in and out have to, the
 // keys and values go in twice, the states out and in), 158 us at the copy's rate; states 88 us, join
@@ -771,7 +771,14 @@ Plan plan_of(int sweeps, int pairs, int T, int d) {
   const size_t own = sweeps == 3 ? (size_t)2 * pairs : all;
   q.chunks = q.band = (T + kC - 1) / kC;
   const size_t resident = 152 * (d == 64 ? 2 : 1);  // blocks of the fused kernel
-  q.fused = d == 128 || q.chunks < 8 || all >= resident;
+  // Heads of 64 in one pass: where blocks of whole heads fill the GPU (24 x 16 heads of 2048 tokens
+  // 172 us, in two passes 173; 16 x 16: 146 and 136; gradients, whose sweeps are three, 6 x 16 of
+  // 4096 197 and 233, 4 x 16 183 and 160), and where the chain of a head's chunks, 5.5 us each up to
+  // a block an SM and 9 above, is shorter than two passes, 31 us and 24 ns a chunk of any head (2 x 16
+  // heads of 640 tokens 27 us, in two passes 33; of 1024 38 and 36; 8 x 16 of 1024 40 and 55, of 2048
+  // 95 and 80).
+  q.fused = d == 128 || all >= (sweeps == 3 ? resident * 4 / 5 : resident) ||
+            (all > 152 ? q.chunks < 9 : q.chunks * (230 - all) < 1290);
   if (q.fused) {
     // Stretches of eight chunks at least: as many as fill the GPU once, if they nearly do (3 x 16 heads
     // in three stretches 475 us, in six 497), else some three times (80 heads in one stretch

@@ -19,7 +19,7 @@
 //
 // What bounds it: the states' warps, 16-bit arithmetic on the ALU pipe (13 operations for a pair of
 // weighted values in three parts) and its waits; some 9000 cycles a chunk of 128 x 128, the rows' warps
-// 6500.
+// 6500.  5 ragged sequences of 8191 x 16 heads of 128: 186 us beside 120 for the stretches' states.
 #include "linear_tc.cuh"
 
 namespace fs {

@@ -339,6 +339,7 @@ def test_shared_heads_of_longer_prompts(B, H, Hkv, T, d, state, ragged):
 
 
 @pytest.mark.parametrize("B,H,Hkv,T,d,counts", [(3, 33, 11, 7000, 64, (7000, 3000, 0)), (1, 100, 100, 7000, 64, None),
+                                                (2, 40, 8, 9000, 64, (9000, 4000)), (1, 80, 80, 9000, 64, None),
                                                 (2, 24, 8, 5000, 128, (4999, 1111))])
 def test_gradients_of_long_sequences(B, H, Hkv, T, d, counts):
     # against the calls in pieces of 900 tokens, whose states and states' gradients chain them; tolerances
