@@ -659,7 +659,7 @@ int fs_selftest_tree_wait(const void *q, const fs_cache *cache,
  *   count         [batch] int32 or NULL (all T): sequence b's tokens; rows
  *                 t >= count[b] of out are left as they were, those of q, k and v
  *                 may hold anything
- *   scale         finite, not 0
+ *   scale         of either sign, between 2^-64 and 2^64
  *   state         [batch, H, d, d] f32, 16-byte aligned, the state before the first
  *                 token, or NULL (zeros); state_out the one after the last, or NULL
  *                 (not written).  Both may be the same memory (in place); they do

@@ -1134,7 +1134,8 @@ extern "C" int fs_linear_attn(const void *q, const void *k, const void *v, const
                               float *state_out, void *out, const long long *out_strides, void *ws,
                               size_t ws_bytes, void *stream) {
   FS_TRY(check_linear(batch, H, Hkv, T, d));
-  if (!decay || !(scale - scale == 0.f) || scale == 0.f) return FS_ERR_INVALID_ARG;
+  // (gradients' states are held over the scale)
+  if (!decay || !(fabsf(scale) >= 0x1p-64f && fabsf(scale) <= 0x1p64f)) return FS_ERR_INVALID_ARG;
   long long qs[3], ks[3], vs[3], os[3];
   set_strides(qs, q_strides, batch, H, T, d);
   set_strides(ks, k_strides, batch, Hkv, T, d);
@@ -1178,7 +1179,8 @@ extern "C" int fs_linear_attn_bwd(
     const long long *dq_strides, const long long *dk_strides, const long long *dv_strides,
     float *dstate, void *ws, size_t ws_bytes, void *stream) {
   FS_TRY(check_linear(batch, H, Hkv, T, d));
-  if (!decay || !(scale - scale == 0.f) || scale == 0.f) return FS_ERR_INVALID_ARG;
+  // (gradients' states are held over the scale)
+  if (!decay || !(fabsf(scale) >= 0x1p-64f && fabsf(scale) <= 0x1p64f)) return FS_ERR_INVALID_ARG;
   long long qs[3], ks[3], vs[3], ds[3], gq[3], gk[3], gv[3];
   set_strides(qs, q_strides, batch, H, T, d);
   set_strides(ks, k_strides, batch, Hkv, T, d);

@@ -291,7 +291,7 @@ __global__ void __launch_bounds__(256) k16_join_kernel(const __grid_constant__ P
   float4 *at = reinterpret_cast<float4 *>(p.slots + bh * p.splits * (D * D)) + i;
   // (the last stretch of a sequence: not where nobody wants the state behind it)
   const int adds = band.stretches - (band.stretches && band.hi == band.chunks && !wants_last(p, w) ? 1 : 0);
-  constexpr int kAhead = 4;
+  constexpr int kAhead = 8;
   const Factor whole = decay_power(decay, band.per * kC);
   for (int r0 = 0; r0 < band.stretches; r0 += kAhead) {
     float4 y[kAhead];

@@ -178,3 +178,9 @@ def test_norm_in_place_refusals(kw):
 ])
 def test_norm_backward_in_place_refusals(kw):
     assert norm_bwd(**kw) == INVALID
+
+
+@pytest.mark.parametrize("scale", [1e-30, -1e-30, 1e-45, 1e30, -1e30])
+@pytest.mark.parametrize("call", [linear, linear_bwd])
+def test_linear_scales_that_states_cannot_be_held_over(call, scale):
+    assert call(scale=scale) == INVALID
