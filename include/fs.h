@@ -670,11 +670,11 @@ int fs_selftest_tree_wait(const void *q, const fs_cache *cache,
  * for states.  An element of v that is not finite makes its
  * column of that token's and all later outputs, and of the state, NaN or
  * infinite; one of k or q reaches what the definition says.
- *   ws            device workspace of fs_linear_workspace_bytes() bytes, for one
- *                 call at a time; its first int is an error word (fs_check_status(ws))
- *                 that the caller zeroes once: calls record FS_ERR_TIMEOUT there when
- *                 a bounded wait gives up, and none clears it.  May be NULL for
- *                 forward calls with T <= FS_LINEAR_STEPS
+ *   ws            device workspace of fs_linear_workspace_bytes() bytes, 16-byte aligned
+ *                 (else FS_ERR_UNSUPPORTED), for one call at a time; its first int is an
+ *                 error word (fs_check_status(ws)) that the caller zeroes once: calls
+ *                 record FS_ERR_TIMEOUT there when a bounded wait gives up, and none
+ *                 clears it.  May be NULL for forward calls with T <= FS_LINEAR_STEPS
  * d: 64 or 128; batch * H < 2^16, T < 2^30 (else FS_ERR_UNSUPPORTED).
  * Deterministic. */
 #define FS_LINEAR_STEPS 16
@@ -694,7 +694,8 @@ int fs_linear_attn(const void *q, const void *k, const void *v, const long long 
  *   dq, dk, dv    bf16, as q, k and v (written; rows t >= count[b] are left as they
  *                 were); dstate [batch, H, d, d] f32 or NULL.  They overlap neither an
  *                 input nor one another
- *   ws            of fs_linear_workspace_bytes(..., 1) bytes, never NULL
+ *   ws            of fs_linear_workspace_bytes(..., 1) bytes, never NULL; 32-byte aligned
+ *                 where H > Hkv and T > FS_LINEAR_STEPS (else FS_ERR_UNSUPPORTED)
  * The other arguments as the forward's.  Deterministic. */
 int fs_linear_attn_bwd(const void *q, const void *k, const void *v, const long long *q_strides,
                        const long long *k_strides, const long long *v_strides, const float *decay,

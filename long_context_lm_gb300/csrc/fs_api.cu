@@ -1204,7 +1204,8 @@ extern "C" int fs_linear_attn_bwd(
   FS_TRY(check_states(dstate_out, dstate, false, floats));
   const LinearLayout L = linear_layout(batch, H, Hkv, T, d, true);
   if (!ws || ws_bytes < L.total) return FS_ERR_INVALID_ARG;
-  if (reinterpret_cast<uintptr_t>(ws) % 16) return FS_ERR_UNSUPPORTED;
+  // (prompts' parts of shared heads' gradients are stored 32 bytes at a time)
+  if (reinterpret_cast<uintptr_t>(ws) % (H > Hkv && T > FS_LINEAR_STEPS ? 32 : 16)) return FS_ERR_UNSUPPORTED;
   const int share = H / Hkv;
   LinearArgs a{};
   a.sweeps = 3;
