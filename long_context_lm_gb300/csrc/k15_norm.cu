@@ -199,21 +199,25 @@ struct Slot {
 };
 
 // 1 / (1 + e^-x) by the special-function unit: 2^-20 of itself, enough for bf16 results.
-// kExact: with the exponent's rounding put back and a Newton step on the reciprocal, 2^-22.
+// kExact: by e^-|x|, which is in (0, 1] for any x and keeps what lies below fp32's normal range; with the
+// exponent's rounding put back and a Newton step on the reciprocal, 2^-22.
 template <bool kExact>
 __device__ __forceinline__ float sigmoid(float x) {
   constexpr float kL = -1.44269504f, kRest = -1.92596303e-8f;  // -log2 e, what it lacks
-  float t = x * kL, e, r;
-  if constexpr (kExact) t = fminf(t, 126.f);  // (past it the Newton step would meet an infinity)
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
+  float e, r;
   if constexpr (kExact) {
-    const float rest = fmaf(x, kL, -t) + x * kRest;
-    if (t < 126.f) e = fmaf(e, rest * 0.693147181f, e);
+    const float a = fabsf(x), t = a * kL;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(t));
+    if (t > -150.f) e = fmaf(e, (fmaf(a, kL, -t) + a * kRest) * 0.693147181f, e);  // (else e is 0, t may be infinite)
+    const float d = 1.f + e;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
+    r = fmaf(r, fmaf(-d, r, 1.f), r);
+    return x < 0.f ? e * r : r;
+  } else {
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * kL));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+    return r;
   }
-  const float d = 1.f + e;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
-  if constexpr (kExact) r = fmaf(r, fmaf(-d, r, 1.f), r);
-  return r;
 }
 template <bool kExact>
 __device__ __forceinline__ f2 sigmoid2(f2 x) {

@@ -26,3 +26,60 @@ def test_gradients_with_eps_0(M, D, groups, dt, rdt, next):
         assert (got[n] is None) == (n == "next_gain" and not next)
         if got[n] is not None:
             near(got[n], *want[n], 2 * loss(dt))
+
+
+# gates from next to nothing to the type's ends, both signs
+GATES = [1e-30, 1e-6, 0.1, 1.0, 5.0, 10.0, 17.0, 20.0, 40.0, 80.0, 86.0, 88.0, 89.0, 95.0, 100.0, 104.0, 1e3, 1e5, 3e7, 1e8,
+         1e20, 1e30, 1e37, 2.3e38, 2.5e38, 3.3e38]
+
+
+def gates(M, D, dt, bound=float("inf")):
+    g = torch.tensor([v for v in GATES if v <= bound], dtype=torch.float64)
+    ends = torch.tensor([torch.finfo(dt).max], dtype=torch.float64) if bound > 3.4e38 else g[:0]
+    g = torch.cat([g, -g, ends, -ends, torch.zeros(1, dtype=torch.float64)])
+    return g[torch.arange(M * D) * 7 % len(g)].reshape(M, D).to(dt).cuda()
+
+
+@pytest.mark.parametrize("D", [64, 1000, 1024, 4099])
+@pytest.mark.parametrize("dt,rdt", TYPES)
+@pytest.mark.parametrize("residual", [False, True])
+def test_gates_of_any_size(D, dt, rdt, residual):
+    # x within a half, so that the products with the type's largest numbers stay within it
+    form, _, dz, _ = make(6, D, dt, rdt, True, residual, False, seed=D)
+    form.update(x=(form["x"].float().sigmoid() - 0.5).to(dt), gate=gates(6, D, dt), scale=0.7)
+    z, _ = fs.fs_block_norm(z=torch.empty((6, D), dtype=rdt, device="cuda"), **form)
+    want, _ = ref.norm(**form)
+    size = want.abs() + (2 * form["residual"].double().abs() if residual else 0)
+    near(z, want, size, loss(dt))
+    if dt is FP and not residual:
+        # also where the sigmoid lies below fp32's normal range: steps of 2^-149 of it, times a gate
+        # of 104 at most and |x| of a half
+        assert ((z.double() - want).abs() <= 2.0 ** -19 * want.abs() + 104 * 2.0 ** -149).all()
+    dz = (dz.float().sigmoid() - 0.5).to(rdt)
+    got = fs.fs_block_norm_bwd(dz=dz, **form)
+    near(got["x"], *ref.norm_grads(dz=dz, **form)["x"], 2 * loss(dt))
+
+
+@pytest.mark.parametrize("dt,rdt", TYPES)
+def test_gates_of_any_size_before_a_second_norm(dt, rdt):
+    # squares of z fit fp32 for gates up to 1e16
+    form, next_gain, dz, dy = make(6, 1024, dt, rdt, True, True, True, seed=3)
+    form.update(gate=gates(6, 1024, dt, 1e16), groups=16, scale=0.7, eps=1e-6)
+    z, y = fs.fs_block_norm(next_norm=True, next_gain=next_gain, **form)
+    wz, wy = ref.norm(next_gain=next_gain, **form)
+    size = wz.abs() + 2 * form["residual"].double().abs()
+    near(z, wz, size, loss(dt))
+    near(y, wy, wy.abs() * (size / wz.abs().clamp(min=1e-30)), loss(dt))
+
+
+@pytest.mark.parametrize("dt", [BF, FP])
+def test_gates_that_are_not_finite(dt):
+    # +inf opens without a bound; -inf is 0 times infinity, as the formula has it; both in their elements alone
+    x = torch.randn((3, 256), device="cuda").to(dt)
+    gate = torch.randn((3, 256), device="cuda").to(dt)
+    want, _ = fs.fs_block_norm(x, gate=gate)
+    gate[0, 5], gate[1, 7], gate[2, 9] = float("inf"), float("-inf"), float("nan")
+    z, _ = fs.fs_block_norm(x, gate=gate)
+    assert z[0, 5] == x[0, 5] * float("inf") and z[1, 7].isnan() and z[2, 9].isnan()
+    z[0, 5], z[1, 7], z[2, 9] = want[0, 5], want[1, 7], want[2, 9]
+    assert torch.equal(z, want)
