@@ -621,8 +621,8 @@ __global__ void __maxnreg__(!kTwice ? 96 : kTeam ? 255 : 128) k15_norm_bwd_kerne
           f2 d = mul2(g[i][c], mul2(xv.get(c), inv[i].get(c)));
           if (a.gain) d = mul2(d, gn.get(c));
           const f2 sg = sig[i][c], silu = mul2(gv.get(c), sg);
-          // silu' = sig (1 + gate (1 - sig)) = sig + silu - silu sig
-          out[c] = mul2(d, sub2_bits(add2_bits(sg, silu), mul2(silu, sg)));
+          // silu' = sig + silu (1 - sig), the bracket first: past 17, where sig is 1, it is 0 whatever the gate
+          out[c] = mul2(d, madd2(silu, sub2_bits(both(1.f), sg), sg));
           g[i][c] = mul2(g[i][c], silu);
         }
         if (a.dgate) store<kWhole, TX, V>(dgr + i * apart, left - i * apart, out, a.wide);

@@ -57,7 +57,9 @@ def test_gates_of_any_size(D, dt, rdt, residual):
         assert ((z.double() - want).abs() <= 2.0 ** -19 * want.abs() + 104 * 2.0 ** -149).all()
     dz = (dz.float().sigmoid() - 0.5).to(rdt)
     got = fs.fs_block_norm_bwd(dz=dz, **form)
-    near(got["x"], *ref.norm_grads(dz=dz, **form)["x"], 2 * loss(dt))
+    want = ref.norm_grads(dz=dz, **form)
+    near(got["x"], *want["x"], 2 * loss(dt))
+    near(got["gate"], *want["gate"], 2 * loss(dt))   # (the slope past 17 is 1, not a difference of two gates)
 
 
 @pytest.mark.parametrize("dt,rdt", TYPES)
@@ -70,6 +72,10 @@ def test_gates_of_any_size_before_a_second_norm(dt, rdt):
     size = wz.abs() + 2 * form["residual"].double().abs()
     near(z, wz, size, loss(dt))
     near(y, wy, wy.abs() * (size / wz.abs().clamp(min=1e-30)), loss(dt))
+    got = fs.fs_block_norm_bwd(dz=dz, dy=dy, next_gain=next_gain, **form)
+    want = ref.norm_grads(dz=dz, dy=dy, next_gain=next_gain, **form)
+    for n in want:
+        near(got[n], *want[n], 2 * loss(dt))
 
 
 @pytest.mark.parametrize("dt", [BF, FP])
