@@ -340,9 +340,10 @@ struct Team {
 #pragma unroll
       for (int c = 0; c < (kWhole ? 1 : V / 2); ++c) p[i].x[c] = both(v[i]);
   }
-  // The factors that normalise the groups of x, D elements (ones where they are not to be); x(i): vector i.
+  // The factors that normalise x's groups (ones where they are not to be); x(i): vector i.  The row has `left`
+  // elements from the thread's first on, 0 without a row.
   template <typename F>
-  __device__ __forceinline__ void factors(PerGroup<kWhole, V> (&inv)[N], const NormArgs &a, int D, F x) {
+  __device__ __forceinline__ void factors(PerGroup<kWhole, V> (&inv)[N], const NormArgs &a, int left, F x) {
     if (a.mode == kNone) {
 #pragma unroll
       for (int i = 0; i < N; ++i)
@@ -359,9 +360,9 @@ struct Team {
 #pragma unroll
       for (int c = 0; c < (kWhole ? 1 : V / 2); ++c) {
         // (past the row, and in a team without one, 0: with eps 0 the factor there would be infinite)
-        const int e = (t + i * size) * V + 2 * c;
-        const float f = e < D ? rsqrtf(fmaf(lo2(inv[i].x[c]), a.inv_n, a.eps)) : 0.f;
-        const float g = kWhole ? f : e + 1 < D ? rsqrtf(fmaf(hi2(inv[i].x[c]), a.inv_n, a.eps)) : 0.f;
+        const int e = i * size * V + 2 * c;
+        const float f = e < left ? rsqrtf(fmaf(lo2(inv[i].x[c]), a.inv_n, a.eps)) : 0.f;
+        const float g = kWhole ? f : e + 1 < left ? rsqrtf(fmaf(hi2(inv[i].x[c]), a.inv_n, a.eps)) : 0.f;
         inv[i].x[c] = f2_bits(f, g);
       }
   }
@@ -404,7 +405,7 @@ __global__ void __launch_bounds__(kTeam ? 256 : 512, sizeof(TX) == 4 || N * 8 > 
   }
   const f2 scale = both(a.scale);
   PerGroup<kWhole, V> inv[N];
-  team.factors(inv, a, a.D, [&](int i) { return x[i]; });
+  team.factors(inv, a, left, [&](int i) { return x[i]; });
   f2 z[N][V / 2], ss = 0;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
@@ -517,10 +518,9 @@ __global__ void __maxnreg__(!kTwice ? 96 : kTeam ? 255 : 128) k15_norm_bwd_kerne
       cp_async_commit();
       cp_async_wait<1>();
     }
-    const bool have = row < a.M;
-    const int left = have ? a.D - e0 : 0, rest = kTwice ? which : 0;
+    const int left = row < a.M ? a.D - e0 : 0, rest = kTwice ? which : 0;
     PerGroup<kWhole, V> inv[N];
-    team.factors(inv, a, have ? a.D : 0, [&](int i) { return x.get(which, i, left, apart); });
+    team.factors(inv, a, left, [&](int i) { return x.get(which, i, left, apart); });
     f2 sig[N][V / 2], g[N][V / 2];  // g: the gradient that reaches z
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -577,7 +577,7 @@ __global__ void __maxnreg__(!kTwice ? 96 : kTeam ? 255 : 128) k15_norm_bwd_kerne
       }
       float s[2] = {lo2(s0) + hi2(s0), lo2(s1) + hi2(s1)};
       team.add(s);
-      const float r = have ? rsqrtf(fmaf(s[0], a.inv_D, a.eps)) : 0.f;
+      const float r = left > 0 ? rsqrtf(fmaf(s[0], a.inv_D, a.eps)) : 0.f;
       const f2 rf = both(r), mc = both(-r * r * s[1] * a.inv_D);
 #pragma unroll
       for (int i = 0; i < N; ++i) {
