@@ -89,3 +89,21 @@ def test_gates_that_are_not_finite(dt):
     assert z[0, 5] == x[0, 5] * float("inf") and z[1, 7].isnan() and z[2, 9].isnan()
     z[0, 5], z[1, 7], z[2, 9] = want[0, 5], want[1, 7], want[2, 9]
     assert torch.equal(z, want)
+
+
+@pytest.mark.parametrize("D", [64, 1024, 1001, 2500])
+@pytest.mark.parametrize("dt", [BF, FP])
+def test_gates_beside_an_fp32_residual_stream(D, dt):
+    # z and the gains' gradients are fp32 numbers there, whatever x is: an exponential of 2^-22 and no more
+    # than eight roundings of 2^-24 on the way to them
+    g = torch.Generator(device="cuda").manual_seed(D)
+    r = lambda *s: torch.randn(s, generator=g, device="cuda")  # noqa: E731
+    gate = (160 * torch.rand((1, D), generator=g, device="cuda") - 80).to(dt)
+    form = dict(x=r(1, D).to(dt), gate=gate, gain=1 + 0.3 * r(D), scale=0.7)
+    z, _ = fs.fs_block_norm(z=torch.empty((1, D), device="cuda"), **form)
+    want, _ = ref.norm(**form)
+    assert ((z.double() - want).abs() <= (2.0 ** -22 + 8 * 2.0 ** -24) * want.abs()).all()
+    dz = r(1, D)
+    got = fs.fs_block_norm_bwd(dz=dz, **form)["gain"]
+    want = ref.norm_grads(dz=dz, **form)["gain"][0]
+    assert ((got.double() - want).abs() <= (2.0 ** -22 + 8 * 2.0 ** -24) * want.abs()).all()
