@@ -674,7 +674,8 @@ int fs_selftest_tree_wait(const void *q, const fs_cache *cache,
  *                 (else FS_ERR_UNSUPPORTED), for one call at a time; its first int is an
  *                 error word (fs_check_status(ws)) that the caller zeroes once: calls
  *                 record FS_ERR_TIMEOUT there when a bounded wait gives up, and none
- *                 clears it.  May be NULL for forward calls with T <= FS_LINEAR_STEPS
+ *                 clears it.  May be NULL for forward calls with T <= FS_LINEAR_STEPS.
+ *                 The size for a batch and a T does for smaller ones of the same heads
  * d: 64 or 128; batch * H < 2^16, T < 2^30 (else FS_ERR_UNSUPPORTED).
  * Deterministic. */
 #define FS_LINEAR_STEPS 16

@@ -31,6 +31,8 @@
 // keys and values go in twice, the states out and in), 158 us at the copy's rate; states 88 us, join
 // 13, rows 110 (a chunk's three waits of rows on products and of products on rows, by two blocks an
 // SM in turn).
+#include <algorithm>
+
 #include "linear_tc.cuh"
 
 namespace fs {
@@ -763,6 +765,9 @@ struct Plan {
 // (Bands small enough for the L2 to keep their states and keys between the passes cost more launches
 // than they save: 65536 tokens x 16 heads in bands of 40 MB 289 us, of 80 MB 245, in one 210.)
 constexpr size_t kBandBytes = (size_t)160 << 20;
+constexpr size_t resident_of(int d) { return 152 * (d == 64 ? 2 : 1); }  // blocks of the fused kernel
+// heads (of all sweeps) whose blocks fill the GPU
+constexpr size_t filled_by(int sweeps, int d) { return sweeps == 3 ? resident_of(d) * 4 / 5 : resident_of(d); }
 Plan plan_of(int sweeps, int pairs, int T, int d) {
   Plan q{};
   const size_t matrix = (size_t)d * d * 4;
@@ -770,14 +775,14 @@ Plan plan_of(int sweeps, int pairs, int T, int d) {
   // Of the gradients' sweeps the second, over R^T, has the states of the third, over R.
   const size_t own = sweeps == 3 ? (size_t)2 * pairs : all;
   q.chunks = q.band = (T + kC - 1) / kC;
-  const size_t resident = 152 * (d == 64 ? 2 : 1);  // blocks of the fused kernel
+  const size_t resident = resident_of(d);
   // Heads of 64 in one pass: where blocks of whole heads fill the GPU (24 x 16 heads of 2048 tokens
   // 172 us, in two passes 173; 16 x 16: 146 and 136; gradients, whose sweeps are three, 6 x 16 of
   // 4096 197 and 233, 4 x 16 183 and 160), and where the chain of a head's chunks, 5.5 us each up to
   // a block an SM and 9 above, is shorter than two passes, 31 us and 24 ns a chunk of any head (2 x 16
   // heads of 640 tokens 27 us, in two passes 33; of 1024 38 and 36; 8 x 16 of 1024 40 and 55, of 2048
   // 95 and 80).
-  q.fused = d == 128 || all >= (sweeps == 3 ? resident * 4 / 5 : resident) ||
+  q.fused = d == 128 || all >= filled_by(sweeps, d) ||
             (all > 152 ? q.chunks < 9 : q.chunks * (230 - all) < 1290);
   if (q.fused) {
     // Stretches of eight chunks at least: as many as fill the GPU once, if they nearly do (3 x 16 heads
@@ -845,8 +850,25 @@ cudaError_t run(Params &p, const Maps &m, const Plan &q, cudaStream_t st) {
 
 }  // namespace
 
+// What plan_of wants for this shape and for any with fewer sequences or tokens: plans change from two
+// passes to one, and from one band to two, where the next larger shape wants less.
 size_t linear_chunk_bytes(int sweeps, int batch, int H, int T, int d) {
-  return plan_of(sweeps, batch * H, T, d).total;
+  const size_t matrix = (size_t)d * d * 4, chunks = (T + kC - 1) / kC;
+  const auto least = [](size_t a, size_t b) { return a < b ? a : b; };
+  const int owners = sweeps == 3 ? 2 : 1;
+  // One pass: two stretches or more of eight chunks or more, of which three times what is resident at most.
+  size_t one = 0;
+  if (chunks >= 16) one = least(3 * resident_of(d) * owners / sweeps, (size_t)owners * batch * H * (chunks / 8)) * matrix;
+  // Two passes: the largest batch that takes them.
+  size_t two = 0;
+  if (d == 64) {
+    const size_t own = owners * H * least(batch, (filled_by(sweeps, d) - 1) / ((size_t)sweeps * H));
+    const size_t states = own * chunks * matrix;
+    two = least(states, kBandBytes) + least(152 * StateCfg<64>::kBlocks, own * ((chunks + 3) / 4)) * matrix +
+          (states > kBandBytes ? own * matrix : 0) + (least(states, kBandBytes) / matrix * 8 + 255) / 256 * 256;
+  }
+  const size_t now = plan_of(sweeps, batch * H, T, d).total;
+  return std::max({one, two, now});
 }
 
 cudaError_t launch_linear_chunks(const LinearArgs &a, void *ws, int *err, cudaStream_t st) {

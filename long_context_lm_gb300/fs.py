@@ -990,8 +990,8 @@ def _scratch(ws, dev):
 
 
 def fs_linear_workspace(batch, H, Hkv, T, d, device, backward=False):
-    """A workspace for fs_linear_attn (or, ``backward``, fs_linear_attn_bwd) of this shape, one call
-    at a time; ``fs_check_status(ws)`` raises if a bounded wait of a call gave up."""
+    """A workspace for fs_linear_attn (or, ``backward``, fs_linear_attn_bwd) of this shape, or of a smaller
+    batch or T, one call at a time; ``fs_check_status(ws)`` raises if a bounded wait of a call gave up."""
     if max(batch, H, Hkv, T, d) > _INT_MAX:
         raise ValueError("a size does not fit 32 bits")
     n = load().fs_linear_workspace_bytes(batch, H, Hkv, T, d, 1 if backward else 0)

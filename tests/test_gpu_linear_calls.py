@@ -23,3 +23,18 @@ def test_a_workspace_cut_from_a_larger_buffer(H, Hkv, T, d, off):
     fs.fs_check_status(ws)
     assert all(torch.equal(a, b) for a, b in zip(got, want))
     assert (arena[:off] == 0).all() and (arena[off + n:] == 0).all()
+
+
+@pytest.mark.parametrize("B,H,T,d", [(3, 16, 2500, 64), (5, 16, 2500, 128), (1, 2, 90000, 64), (20, 8, 700, 64)])
+def test_one_workspace_for_the_largest_call_serves_all(B, H, T, d):
+    dev = torch.device("cuda", torch.cuda.current_device())
+    both = [fs.fs_linear_workspace(B, H, H, T, d, dev, backward=b) for b in (False, True)]
+    for b, t in ((B, T), (B, T // 3), (1, T), (1, T // 2 + 1), (max(1, B // 2), T // 5), (B, 17), (1, 3)):
+        q, k, v, dout, decay, S0, G, _ = inputs(b, H, H, t, d, seed=t)
+        want = (fs.fs_linear_attn(q, k, v, decay, state=S0),
+                *fs.fs_linear_attn_bwd(q, k, v, decay, dout, state=S0, dstate_out=G))
+        got = (fs.fs_linear_attn(q, k, v, decay, state=S0, ws=both[0]),
+               *fs.fs_linear_attn_bwd(q, k, v, decay, dout, state=S0, dstate_out=G, ws=both[1]))
+        assert all(torch.equal(x, y) for x, y in zip(got, want)), (b, t)
+    for ws in both:
+        fs.fs_check_status(ws)
