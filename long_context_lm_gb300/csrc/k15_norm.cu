@@ -727,7 +727,8 @@ __global__ void __launch_bounds__(1024) k15_gain_kernel(const float *part, int b
     x = s;
   }
   const int to = blockIdx.x * 32 + k;
-  if (lane == 0 && to < D) (blockIdx.y ? second : first)[to] = x + lost;
+  // (of a sum that is not finite nothing is lost: the difference of infinities would be NaN)
+  if (lane == 0 && to < D) (blockIdx.y ? second : first)[to] = fabsf(x) <= 0x1.fffffep127f ? x + lost : x;
 }
 
 constexpr int kMaxBlocks = 152 * 4;

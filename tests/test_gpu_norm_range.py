@@ -107,3 +107,22 @@ def test_gates_beside_an_fp32_residual_stream(D, dt):
     got = fs.fs_block_norm_bwd(dz=dz, **form)["gain"]
     want = ref.norm_grads(dz=dz, **form)["gain"][0]
     assert ((got.double() - want).abs() <= (2.0 ** -22 + 8 * 2.0 ** -24) * want.abs()).all()
+
+
+@pytest.mark.parametrize("M", [1, 40, 5000])
+@pytest.mark.parametrize("D", [64, 1024])
+def test_gains_gradients_that_are_not_finite(M, D):
+    # an infinite sum is infinite, of its sign; infinities of both signs make NaN; other columns keep theirs
+    g = torch.Generator(device="cuda").manual_seed(M)
+    x, dz = (torch.randn((M, D), generator=g, device="cuda") for _ in range(2))
+    x[:, 3:6] = x[:, 3:6].abs() + 0.1
+    gain = torch.ones(D, device="cuda")
+    want = fs.fs_block_norm_bwd(x, dz=dz, gain=gain)["gain"]
+    dz[M // 2, 3], dz[0, 4], dz[M - 1, 5] = float("inf"), float("-inf"), float("nan")
+    if M > 1:
+        dz[0, 6], dz[M - 1, 6] = float("inf"), float("-inf")
+        x[:, 6] = 1.0
+        want[6] = float("nan")
+    got = fs.fs_block_norm_bwd(x, dz=dz, gain=gain)["gain"]
+    want[3], want[4], want[5] = float("inf"), float("-inf"), float("nan")
+    assert torch.equal(got.isnan(), want.isnan()) and torch.equal(got.nan_to_num(0.5), want.nan_to_num(0.5))
