@@ -1009,6 +1009,8 @@ def _linear_inputs(q, k, v, decay, count):
     B, H, T, d = shape
     qp, qs = _rows(q, dev, "q", torch.bfloat16, shape)
     Hkv = k.shape[1] if isinstance(k, torch.Tensor) and k.dim() == 4 else 0
+    if max(B, H, Hkv, T) > _INT_MAX:  # (expanded axes; ctypes would take their low 32 bits)
+        raise ValueError("a size does not fit 32 bits")
     shape = (B, Hkv, T, d)
     kp, ks = _rows(k, dev, "k", torch.bfloat16, shape)
     vp, vs = _rows(v, dev, "v", torch.bfloat16, shape)

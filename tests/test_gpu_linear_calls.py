@@ -38,3 +38,17 @@ def test_one_workspace_for_the_largest_call_serves_all(B, H, T, d):
         assert all(torch.equal(x, y) for x, y in zip(got, want)), (b, t)
     for ws in both:
         fs.fs_check_status(ws)
+
+
+@pytest.mark.parametrize("axis", [0, 2])
+def test_sizes_past_32_bits_are_refused(axis):
+    # axes as long as that exist by expansion alone; their low 32 bits would be a call of one token
+    shape = [1, 1, 1, 64]
+    shape[axis] = 2 ** 32 + 1
+    x = torch.zeros((1, 1, 1, 64), device="cuda", dtype=torch.bfloat16).expand(shape)
+    decay = torch.zeros(1, device="cuda")
+    ws = fs.fs_linear_workspace(1, 1, 1, 1, 64, "cuda", backward=True)
+    with pytest.raises(ValueError):
+        fs.fs_linear_attn(x, x, x, decay, out=x, ws=ws)
+    with pytest.raises(ValueError):
+        fs.fs_linear_attn_bwd(x, x, x, decay, x, dq=x, dk=x, dv=x, ws=ws)
