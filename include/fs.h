@@ -648,11 +648,11 @@ int fs_selftest_tree_wait(const void *q, const fs_cache *cache,
  * tokens one after the other: a decoding step is T = 1.
  *   q, out        [batch, H, T, d] bf16; k, v [batch, Hkv, T, d] bf16; H a multiple
  *                 of Hkv, query head h reading kv head h / (H / Hkv).  Strides as
- *                 fs_rope's, multiples of 8 elements, pointers 16-byte aligned
- *                 (else FS_ERR_UNSUPPORTED); no negative ones, and 0 between tokens
- *                 only for T = 1 (FS_ERR_UNSUPPORTED).  out overlaps no input, and its
-                 rows do not one another (each axis' stride passes what the axes of
-                 smaller strides take, else FS_ERR_INVALID_ARG)
+ *                 fs_rope's: none negative (FS_ERR_INVALID_ARG), multiples of 8
+ *                 elements, 0 between tokens only for T = 1, pointers 16-byte aligned
+ *                 (else FS_ERR_UNSUPPORTED).  out overlaps no input, and its rows do
+ *                 not one another (each axis' stride passes what the axes of smaller
+ *                 strides take, else FS_ERR_INVALID_ARG)
  *   decay         [H] f32, the logarithm of the factor a token: 0 or below (-inf:
  *                 a token sees itself alone).  A constant of the model: there is no
  *                 gradient for it
