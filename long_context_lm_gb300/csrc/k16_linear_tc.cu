@@ -709,6 +709,8 @@ __global__ void __launch_bounds__(RowCfg::kThreads, 2)
       fresh = u.next();
     }
     if (lane == 0) bulk_wait_read<0>();
+    __syncwarp();
+    tc::tmem_wait_st();  // (a wait that gave up may have left parts on their way into columns that are given back)
   }
   tc::fence_before_sync();
   __syncthreads();
