@@ -707,6 +707,25 @@ int fs_linear_attn_bwd(const void *q, const void *k, const void *v, const long l
                        const long long *dv_strides, float *dstate, void *ws, size_t ws_bytes,
                        void *stream);
 
+/* The same calls with another limit for the waits of T > FS_LINEAR_STEPS tokens, 1 .. 4e9 SM cycles
+ * (the last is theirs): a test makes them give up.  The call then ends as it does after a stalled
+ * pipeline stage, with FS_ERR_TIMEOUT in the workspace's error word and outputs that are not valid. */
+int fs_selftest_linear_wait(const void *q, const void *k, const void *v, const long long *q_strides,
+                            const long long *k_strides, const long long *v_strides,
+                            const float *decay, int batch, int H, int Hkv, int T, int d,
+                            const int32_t *count, float scale, const float *state, float *state_out,
+                            void *out, const long long *out_strides, void *ws, size_t ws_bytes,
+                            long long cycles, void *stream);
+int fs_selftest_linear_wait_bwd(const void *q, const void *k, const void *v,
+                                const long long *q_strides, const long long *k_strides,
+                                const long long *v_strides, const float *decay, int batch, int H,
+                                int Hkv, int T, int d, const int32_t *count, float scale,
+                                const float *state, const void *dout, const long long *dout_strides,
+                                const float *dstate_out, void *dq, void *dk, void *dv,
+                                const long long *dq_strides, const long long *dk_strides,
+                                const long long *dv_strides, float *dstate, void *ws,
+                                size_t ws_bytes, long long cycles, void *stream);
+
 /* The norms after and before a block, its gate and its residual scale, for M rows
  * of D elements (a block's outputs, or the heads' outputs of M tokens side by side):
  *   a = x / sqrt(mean of x^2 over its group + eps)   (groups >= 1 groups of D / groups

@@ -1127,12 +1127,13 @@ extern "C" size_t fs_linear_workspace_bytes(int batch, int H, int Hkv, int T, in
   return linear_layout(batch, H, Hkv, T, d, backward != 0).total;
 }
 
-extern "C" int fs_linear_attn(const void *q, const void *k, const void *v, const long long *q_strides,
-                              const long long *k_strides, const long long *v_strides,
-                              const float *decay, int batch, int H, int Hkv, int T, int d,
-                              const int32_t *count, float scale, const float *state,
-                              float *state_out, void *out, const long long *out_strides, void *ws,
-                              size_t ws_bytes, void *stream) {
+namespace {
+
+int linear_attn(const void *q, const void *k, const void *v, const long long *q_strides,
+                const long long *k_strides, const long long *v_strides, const float *decay, int batch,
+                int H, int Hkv, int T, int d, const int32_t *count, float scale, const float *state,
+                float *state_out, void *out, const long long *out_strides, void *ws, size_t ws_bytes,
+                long long wait_cycles, void *stream) {
   FS_TRY(check_linear(batch, H, Hkv, T, d));
   // (gradients' states are held over the scale)
   if (!decay || !(fabsf(scale) >= 0x1p-64f && fabsf(scale) <= 0x1p64f)) return FS_ERR_INVALID_ARG;
@@ -1168,16 +1169,17 @@ extern "C" int fs_linear_attn(const void *q, const void *k, const void *v, const
   a.decay = decay;
   a.count = count;
   a.scale = scale;
+  a.wait_cycles = wait_cycles;
   return linear_sweeps(a, L, ws, static_cast<cudaStream_t>(stream));
 }
 
-extern "C" int fs_linear_attn_bwd(
-    const void *q, const void *k, const void *v, const long long *q_strides,
-    const long long *k_strides, const long long *v_strides, const float *decay, int batch, int H,
-    int Hkv, int T, int d, const int32_t *count, float scale, const float *state, const void *dout,
-    const long long *dout_strides, const float *dstate_out, void *dq, void *dk, void *dv,
-    const long long *dq_strides, const long long *dk_strides, const long long *dv_strides,
-    float *dstate, void *ws, size_t ws_bytes, void *stream) {
+int linear_attn_bwd(const void *q, const void *k, const void *v, const long long *q_strides,
+                    const long long *k_strides, const long long *v_strides, const float *decay, int batch,
+                    int H, int Hkv, int T, int d, const int32_t *count, float scale, const float *state,
+                    const void *dout, const long long *dout_strides, const float *dstate_out, void *dq,
+                    void *dk, void *dv, const long long *dq_strides, const long long *dk_strides,
+                    const long long *dv_strides, float *dstate, void *ws, size_t ws_bytes,
+                    long long wait_cycles, void *stream) {
   FS_TRY(check_linear(batch, H, Hkv, T, d));
   // (gradients' states are held over the scale)
   if (!decay || !(fabsf(scale) >= 0x1p-64f && fabsf(scale) <= 0x1p64f)) return FS_ERR_INVALID_ARG;
@@ -1244,6 +1246,7 @@ extern "C" int fs_linear_attn_bwd(
   a.decay = decay;
   a.count = count;
   a.scale = scale;
+  a.wait_cycles = wait_cycles;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   FS_TRY(linear_sweeps(a, L, ws, st));
   for (int i = 0; share > 1 && i < 2; ++i) {
@@ -1260,6 +1263,54 @@ extern "C" int fs_linear_attn_bwd(
     FS_TRY(status_of(launch_linear_sum(s, st)));
   }
   return FS_OK;
+}
+
+}  // namespace
+
+extern "C" int fs_linear_attn(const void *q, const void *k, const void *v, const long long *q_strides,
+                              const long long *k_strides, const long long *v_strides,
+                              const float *decay, int batch, int H, int Hkv, int T, int d,
+                              const int32_t *count, float scale, const float *state,
+                              float *state_out, void *out, const long long *out_strides, void *ws,
+                              size_t ws_bytes, void *stream) {
+  return linear_attn(q, k, v, q_strides, k_strides, v_strides, decay, batch, H, Hkv, T, d, count, scale, state,
+                     state_out, out, out_strides, ws, ws_bytes, tc::kWaitCycles, stream);
+}
+
+extern "C" int fs_linear_attn_bwd(
+    const void *q, const void *k, const void *v, const long long *q_strides,
+    const long long *k_strides, const long long *v_strides, const float *decay, int batch, int H,
+    int Hkv, int T, int d, const int32_t *count, float scale, const float *state, const void *dout,
+    const long long *dout_strides, const float *dstate_out, void *dq, void *dk, void *dv,
+    const long long *dq_strides, const long long *dk_strides, const long long *dv_strides,
+    float *dstate, void *ws, size_t ws_bytes, void *stream) {
+  return linear_attn_bwd(q, k, v, q_strides, k_strides, v_strides, decay, batch, H, Hkv, T, d, count, scale,
+                         state, dout, dout_strides, dstate_out, dq, dk, dv, dq_strides, dk_strides,
+                         dv_strides, dstate, ws, ws_bytes, tc::kWaitCycles, stream);
+}
+
+extern "C" int fs_selftest_linear_wait(
+    const void *q, const void *k, const void *v, const long long *q_strides,
+    const long long *k_strides, const long long *v_strides, const float *decay, int batch, int H,
+    int Hkv, int T, int d, const int32_t *count, float scale, const float *state, float *state_out,
+    void *out, const long long *out_strides, void *ws, size_t ws_bytes, long long cycles,
+    void *stream) {
+  if (cycles < 1 || cycles > tc::kWaitCycles) return FS_ERR_INVALID_ARG;
+  return linear_attn(q, k, v, q_strides, k_strides, v_strides, decay, batch, H, Hkv, T, d, count, scale, state,
+                     state_out, out, out_strides, ws, ws_bytes, cycles, stream);
+}
+
+extern "C" int fs_selftest_linear_wait_bwd(
+    const void *q, const void *k, const void *v, const long long *q_strides,
+    const long long *k_strides, const long long *v_strides, const float *decay, int batch, int H,
+    int Hkv, int T, int d, const int32_t *count, float scale, const float *state, const void *dout,
+    const long long *dout_strides, const float *dstate_out, void *dq, void *dk, void *dv,
+    const long long *dq_strides, const long long *dk_strides, const long long *dv_strides,
+    float *dstate, void *ws, size_t ws_bytes, long long cycles, void *stream) {
+  if (cycles < 1 || cycles > tc::kWaitCycles) return FS_ERR_INVALID_ARG;
+  return linear_attn_bwd(q, k, v, q_strides, k_strides, v_strides, decay, batch, H, Hkv, T, d, count, scale,
+                         state, dout, dout_strides, dstate_out, dq, dk, dv, dq_strides, dk_strides,
+                         dv_strides, dstate, ws, ws_bytes, cycles, stream);
 }
 
 namespace {

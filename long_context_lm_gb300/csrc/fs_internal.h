@@ -213,6 +213,7 @@ struct LinearArgs {
   const float *decay;
   const int32_t *count;
   float scale;
+  long long wait_cycles;  // after which a wait of the chunked kernels gives up
 };
 cudaError_t launch_linear_recurrent(const LinearArgs &a, cudaStream_t st);
 // The same in chunks of 128 tokens (k16_linear_tc.cu), with linear_chunk_bytes of

@@ -120,14 +120,14 @@ __global__ void __launch_bounds__(StateCfg<D>::kThreads, StateCfg<D>::kBlocks)
     bool ok = true;
     for (int i = -1; i < chunks && ok; ++i) {
       if (i + 1 < chunks) {
-        if (nv > 1) ok = tc::mbar_wait(&s.vempty[nv & 1], (nv / 2 - 1) & 1, p.err);
+        if (nv > 1) ok = wait_for(&s.vempty[nv & 1], (nv / 2 - 1) & 1, p);
         if (!ok) break;
         load(C::kV + (nv & 1) * kAtom, mv, w.v, &s.vfull[nv & 1], nv, 64 * part0, 1);
         ++nv;
       }
       const int k = i < 0 ? 0 : i;
       if (nk == k && k < chunks) {
-        if (nk) ok = tc::mbar_wait(&s.kempty, (nk - 1) & 1, p.err);
+        if (nk) ok = wait_for(&s.kempty, (nk - 1) & 1, p);
         if (!ok) break;
         load(C::kK, mk, w.k, &s.kfull, nk, 0, C::kAtoms);
         ++nk;
@@ -141,10 +141,10 @@ __global__ void __launch_bounds__(StateCfg<D>::kThreads, StateCfg<D>::kBlocks)
     const uint32_t keys = base + C::kK;
     bool ok = true;
     for (int i = 0; i < chunks && ok; ++i) {
-      if (!tc::mbar_wait(&s.kfull, i & 1, p.err)) break;
-      if (i && !tc::mbar_wait(&s.u_free, (i - 1) & 1, p.err)) break;
+      if (!wait_for(&s.kfull, i & 1, p)) break;
+      if (i && !wait_for(&s.u_free, (i - 1) & 1, p)) break;
       for (int j = 0; j < C::kSlabs; ++j) {
-        if (!(ok = tc::mbar_wait(&s.slab_full, (i * C::kSlabs + j) & 1, p.err))) break;
+        if (!(ok = wait_for(&s.slab_full, (i * C::kSlabs + j) & 1, p))) break;
         tc::fence_after_sync();
 #pragma unroll
         for (int k = 0; k < 3 * C::kSlab / 16; ++k) {
@@ -529,13 +529,13 @@ __global__ void __launch_bounds__(RowCfg::kThreads, 2)
       };
       int nq = 0, nk = 0, nv = 0;  // loaded so far
       for (; nv < chunks; a.next()) {
-        if (nk && !tc::mbar_wait(&s.kempty, (nk - 1) & 1, p.err)) break;
+        if (nk && !wait_for(&s.kempty, (nk - 1) & 1, p)) break;
         load(a, C::kK, 1, &s.kfull);
         ++nk;
-        if (nq && !tc::mbar_wait(&s.qempty, (nq - 1) & 1, p.err)) break;
+        if (nq && !wait_for(&s.qempty, (nq - 1) & 1, p)) break;
         load(a, C::kQ, 0, &s.qfull);
         ++nq;
-        if (nv > 1 && !tc::mbar_wait(&s.vempty[nv & 1], (nv / 2 - 1) & 1, p.err)) break;
+        if (nv > 1 && !wait_for(&s.vempty[nv & 1], (nv / 2 - 1) & 1, p)) break;
         load(a, C::kV + (nv & 1) * C::kTile, 2, &s.vfull[nv & 1]);
         ++nv;
       }
@@ -553,7 +553,7 @@ __global__ void __launch_bounds__(RowCfg::kThreads, 2)
         uint32_t here = base;
         asm volatile("" : "+r"(here));
         const uint32_t values = here + C::kV + (i & 1) * C::kTile;
-        if (!tc::mbar_wait(&s.kfull, i & 1, p.err) || !tc::mbar_wait(&s.qfull, i & 1, p.err)) break;
+        if (!wait_for(&s.kfull, i & 1, p) || !wait_for(&s.qfull, i & 1, p)) break;
         tc::fence_after_sync();
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
@@ -561,8 +561,8 @@ __global__ void __launch_bounds__(RowCfg::kThreads, 2)
                      tc::desc_sw128(here + C::kK + k / 4 * kAtom + k % 4 * 32), kQK, k > 0);
         tc::mma_commit(&s.scores);
         tc::mma_commit(&s.kempty);
-        if (!tc::mbar_wait(&s.ready[i & 1], i >> 1 & 1, p.err) ||
-            (i && !tc::mbar_wait(&s.o_free, (i - 1) & 1, p.err)))
+        if (!wait_for(&s.ready[i & 1], i >> 1 & 1, p) ||
+            (i && !wait_for(&s.o_free, (i - 1) & 1, p)))
           break;
         tc::fence_after_sync();
         const uint64_t sd = tc::desc_sw128(here + C::kS);
@@ -580,8 +580,8 @@ __global__ void __launch_bounds__(RowCfg::kThreads, 2)
         tc::mma_commit(&s.inter);
         tc::mma_commit(&s.s_free);
         tc::mma_commit(&s.qempty);
-        if (!tc::mbar_wait(kTurns ? &s.checked[i & 1] : &s.vfull[i & 1], i >> 1 & 1, p.err) ||
-            !tc::mbar_wait(&s.parts, i & 1, p.err))
+        if (!wait_for(kTurns ? &s.checked[i & 1] : &s.vfull[i & 1], i >> 1 & 1, p) ||
+            !wait_for(&s.parts, i & 1, p))
           break;
         tc::fence_after_sync();
 #pragma unroll
@@ -705,7 +705,7 @@ __global__ void __launch_bounds__(RowCfg::kThreads, 2)
       tc::fence_after_sync();
       storing = rows.store(p.a.sweep[u.z], &maps.out[u.z], p.out_axes[u.z], u.b, u.h, chunk, n, i, reverse,
                            s.odd[i & 1] == i + 1 ? s.bad[i & 1] : nullptr, smem + C::kV + (i & 1) * C::kTile,
-                           &s.o_free, s.pairs, p.err);
+                           &s.o_free, s.pairs, p);
       fresh = u.next();
     }
     if (lane == 0) bulk_wait_read<0>();
@@ -885,6 +885,7 @@ cudaError_t launch_linear_chunks(const LinearArgs &a, void *ws, int *err, cudaSt
   p.carry = reinterpret_cast<float *>(at + q.local + q.slots);
   p.odd = reinterpret_cast<uint8_t *>(at + q.local + q.slots + q.carry);
   p.err = err;
+  p.polls = a.wait_cycles < tc::kWaitCycles ? 0 : 255;
   // one map a tensor: the sweeps share theirs
   Maps maps;
   memset(&maps, 0, sizeof(maps));

@@ -132,20 +132,20 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, D == 64 ? 2 : 1)
     bool ok = true;
     auto load_q = [&]() {
       if (!ok || nq >= chunks) return;
-      if (nq && !(ok = tc::mbar_wait(&s.qempty, (nq - 1) & 1, p.err))) return;
+      if (nq && !(ok = wait_for(&s.qempty, (nq - 1) & 1, p))) return;
       load(C::kQ, mq, w.q, &s.qfull, nq);
       ++nq;
     };
     auto load_k = [&]() {
       if (!ok || nk >= chunks) return;
-      if (nk && !(ok = tc::mbar_wait(&s.kempty, (nk - 1) & 1, p.err))) return;
+      if (nk && !(ok = wait_for(&s.kempty, (nk - 1) & 1, p))) return;
       load(C::kK, mk, w.k, &s.kfull, nk);
       ++nk;
     };
     auto load_v = [&]() {
       const int at = nv % C::kValues;
       if (!ok || nv >= chunks) return;
-      if (nv >= C::kValues && !(ok = tc::mbar_wait(&s.vempty[at], (nv / C::kValues - 1) & 1, p.err))) return;
+      if (nv >= C::kValues && !(ok = wait_for(&s.vempty[at], (nv / C::kValues - 1) & 1, p))) return;
       load(C::kV + at * C::kTile, mv, w.v, &s.vfull[at], nv);
       ++nv;
     };
@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, D == 64 ? 2 : 1)
     const uint32_t keys = base + C::kK;
     for (int i = 0; i < chunks; ++i) {
       const uint32_t values = base + C::kV + i % C::kValues * C::kTile;
-      if (!tc::mbar_wait(&s.kfull, i & 1, p.err) || !tc::mbar_wait(&s.qfull, i & 1, p.err)) break;
+      if (!wait_for(&s.kfull, i & 1, p) || !wait_for(&s.qfull, i & 1, p)) break;
       tc::fence_after_sync();
 #pragma unroll
       for (int k = 0; k < D / 16; ++k)
@@ -178,8 +178,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, D == 64 ? 2 : 1)
                    tc::desc_sw128(keys + k / 4 * kAtom + k % 4 * 32), kQK, k > 0);
       tc::mma_commit(&s.scores);
       tc::mma_commit(&s.kempty);
-      if (!tc::mbar_wait(&s.s_ready, i & 1, p.err) ||
-          (i && !tc::mbar_wait(&s.o_free, (i - 1) & 1, p.err)))
+      if (!wait_for(&s.s_ready, i & 1, p) ||
+          (i && !wait_for(&s.o_free, (i - 1) & 1, p)))
         break;
       tc::fence_after_sync();
 #pragma unroll
@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, D == 64 ? 2 : 1)
       tc::mma_commit(&s.inter);
       tc::mma_commit(&s.s_free);
       tc::mma_commit(&s.qempty);
-      if (!tc::mbar_wait(&s.parts, i & 1, p.err) || !tc::mbar_wait(&s.checked[i & 1], i >> 1 & 1, p.err)) break;
+      if (!wait_for(&s.parts, i & 1, p) || !wait_for(&s.checked[i & 1], i >> 1 & 1, p)) break;
       tc::fence_after_sync();
 #pragma unroll
       for (int k = 0; k < 2 * kC / 16; ++k) {
@@ -209,11 +209,11 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, D == 64 ? 2 : 1)
     const uint32_t keys = base + C::kK;
     bool ok = true;
     for (int i = 0; i < chunks && ok; ++i) {
-      if (!tc::mbar_wait(&s.kfull, i & 1, p.err)) break;
-      if (i && !tc::mbar_wait(&s.u_free, (i - 1) & 1, p.err)) break;
+      if (!wait_for(&s.kfull, i & 1, p)) break;
+      if (i && !wait_for(&s.u_free, (i - 1) & 1, p)) break;
       for (int j = 0; j < C::kSlabs; ++j) {
         const int at = i * C::kSlabs + j;
-        if (!(ok = tc::mbar_wait(&s.slab_full, at & 1, p.err))) break;
+        if (!(ok = wait_for(&s.slab_full, at & 1, p))) break;
         tc::fence_after_sync();
 #pragma unroll
         for (int k = 0; k < 3 * C::kUnits; ++k) {
@@ -411,7 +411,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, D == 64 ? 2 : 1)
       tc::fence_after_sync();
       storing = rows.store(w, &maps.out[blockIdx.z], p.out_axes[blockIdx.z], b, h, chunk, n, i, reverse,
                            s.odd[i & 1] == i + 1 ? s.bad[i & 1] : nullptr, smem + C::kV + (i & 1) * C::kTile,
-                           &s.o_free, s.pairs, p.err);
+                           &s.o_free, s.pairs, p);
     }
     if (lane == 0) bulk_wait_read<0>();
     __syncwarp();

@@ -37,6 +37,7 @@ struct Params {
   int axes[4][2];     // 0 where a map's sequences or heads are one
   int out_axes[3][2];
   int *err;
+  uint32_t polls;     // between two looks at the clock, less one
 };
 
 struct Maps {
@@ -156,7 +157,21 @@ __device__ __forceinline__ void stmatrix4(uint32_t at, const uint32_t (&r)[4]) {
                : "memory");
 }
 
-#define WAIT(bar, k) __all_sync(0xffffffffu, tc::mbar_wait(&(bar), (k) & 1, p.err))
+// tc::mbar_wait with the call's own limit.
+__device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, const Params &p) {
+  if (tc::mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  for (uint32_t i = 1;; ++i) {
+    if (tc::mbar_try_wait(bar, parity)) return true;
+    if ((i & p.polls) == 0) {
+      if (clock64() - t0 > p.a.wait_cycles) break;
+      if (*reinterpret_cast<volatile int *>(p.err) != 0) return false;
+    }
+  }
+  tc::report_error(p.err, FS_ERR_TIMEOUT);
+  return false;
+}
+#define WAIT(bar, k) __all_sync(0xffffffffu, wait_for(&(bar), (k) & 1, p))
 
 // What the rows' warps need of a head: lam^n times the scale; columns' factors (see there).
 struct Tables {
@@ -296,7 +311,7 @@ struct RowWarp {
   // when the accumulator is read.  True: the values' place is read until bulk_wait_read (lane 0).
   __device__ __forceinline__ bool store(const LinearSweep &w, const CUtensorMap *map, const int (&axes)[2], int b,
                                         int h, int chunk, int n, int i, bool reverse, const int *bad,
-                                        unsigned char *values, uint64_t *o_free, uint64_t *pairs, int *err) const {
+                                        unsigned char *values, uint64_t *o_free, uint64_t *pairs, const Params &p) const {
     const bool whole = 32 * quarter + 32 <= n && !w.out_f32;
     unsigned char *box = values + (D == 64 ? 0 : half * kAtom) + quarter * 4096;
     const long long to = b * w.os[0] + h * w.os[1] + (chunk * (long long)kC + row) * w.os[2] + half * (D / 2);
@@ -347,7 +362,7 @@ struct RowWarp {
     __syncwarp();
     if (D == 64 && half != 0 && lane == 0) tc::mbar_arrive(&pairs[quarter]);  // two warps' halves of one box
     if (!whole || lane != 0 || (D == 64 && half != 0)) return false;
-    if (D == 64 && !tc::mbar_wait(&pairs[quarter], i & 1, err)) return false;
+    if (D == 64 && !wait_for(&pairs[quarter], i & 1, p)) return false;
     store_rows(box, map, D == 64 ? 0 : 64 * half, chunk * kC + 32 * quarter, h * axes[1], b * axes[0]);
     bulk_commit();
     return true;

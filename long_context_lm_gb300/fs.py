@@ -39,7 +39,7 @@ SYMBOLS = ["fs_default_params", "fs_status_string", "fs_last_cuda_error", "fs_wo
            "fs_rope_make_plan", "fs_rope", "fs_cache_row_bytes", "fs_cache_append",
            "fs_cache_read", "fs_cache_accept", "fs_tree_workspace_bytes", "fs_tree_attn",
            "fs_selftest_tree_wait", "fs_linear_workspace_bytes", "fs_linear_attn",
-           "fs_linear_attn_bwd", "fs_block_norm", "fs_block_norm_workspace_bytes",
+           "fs_linear_attn_bwd", "fs_selftest_linear_wait", "fs_selftest_linear_wait_bwd", "fs_block_norm", "fs_block_norm_workspace_bytes",
            "fs_block_norm_bwd"]
 FS_LINEAR_STEPS = 16
 FS_ROPE_LAYOUTS = {"half": 0, "pairs": 1}
@@ -174,6 +174,8 @@ def load(build_if_stale: bool = True):
         L.fs_linear_attn.argtypes = [P, P, P, S3, S3, S3, P, I, I, I, I, I, P, F, P, P, P, S3, P, Z, P]
         L.fs_linear_attn_bwd.argtypes = [P, P, P, S3, S3, S3, P, I, I, I, I, I, P, F, P, P, S3, P, P,
                                          P, P, S3, S3, S3, P, P, Z, P]
+        L.fs_selftest_linear_wait.argtypes = [*L.fs_linear_attn.argtypes[:-1], LL, P]
+        L.fs_selftest_linear_wait_bwd.argtypes = [*L.fs_linear_attn_bwd.argtypes[:-1], LL, P]
         L.fs_block_norm.argtypes = [P, LL, I, P, LL, P, LL, I, P, P, I, I, I, F, F, P, LL, P, LL, P]
         L.fs_block_norm_workspace_bytes.argtypes = [I, I]
         L.fs_block_norm_workspace_bytes.restype = Z
@@ -1028,7 +1030,18 @@ def fs_linear_attn(q, k, v, decay, state=None, state_out=None, count=None, scale
     ``count`` [batch]: tokens of each sequence (None: T); ``scale`` default d ** -0.5.  T = 1 is a
     decoding step.  Returns out [batch, H, T, d] bf16; rows past count[b] are left as they were (a
     new ``out`` starts as zeros when ``count`` is given)."""
-    L = _lib or load()
+    return _linear_attn((_lib or load()).fs_linear_attn, "fs_linear_attn", (), q, k, v, decay, state,
+                        state_out, count, scale, out, ws, stream)
+
+
+def fs_selftest_linear_wait(q, k, v, decay, cycles, state=None, state_out=None, count=None, scale=None,
+                            out=None, ws=None, stream=None):
+    """fs_linear_attn whose waits give up after ``cycles`` SM cycles (FS_ERR_TIMEOUT in ``ws``)."""
+    return _linear_attn((_lib or load()).fs_selftest_linear_wait, "fs_selftest_linear_wait", (int(cycles),),
+                        q, k, v, decay, state, state_out, count, scale, out, ws, stream)
+
+
+def _linear_attn(fn, where, more, q, k, v, decay, state, state_out, count, scale, out, ws, stream):
     dev, Hkv, args = _linear_inputs(q, k, v, decay, count)
     B, H, T, d = q.shape
     if out is None:
@@ -1043,8 +1056,8 @@ def fs_linear_attn(q, k, v, decay, state=None, state_out=None, count=None, scale
         ws = _new(stream, lambda: fs_linear_workspace(B, H, Hkv, T, d, dev))
     if ws is not None:
         wp, wn = _scratch(ws, dev)
-    _launch(dev, stream, L.fs_linear_attn, "fs_linear_attn", *args,
-            d ** -0.5 if scale is None else float(scale), sp, tp, op, os_, wp, wn)
+    _launch(dev, stream, fn, where, *args, d ** -0.5 if scale is None else float(scale), sp, tp, op, os_,
+            wp, wn, *more)
     return out
 
 
@@ -1054,7 +1067,20 @@ def fs_linear_attn_bwd(q, k, v, decay, dout, state=None, dstate_out=None, count=
     (bf16, as q, k and v), and the gradient of ``state`` into ``dstate`` [batch, H, d, d] fp32 where
     that is given.  Rows past count[b] are left as they were (new tensors start as zeros when
     ``count`` is given).  Returns (dq, dk, dv)."""
-    L = _lib or load()
+    return _linear_attn_bwd((_lib or load()).fs_linear_attn_bwd, "fs_linear_attn_bwd", (), q, k, v, decay, dout,
+                            state, dstate_out, count, scale, dq, dk, dv, dstate, ws, stream)
+
+
+def fs_selftest_linear_wait_bwd(q, k, v, decay, dout, cycles, state=None, dstate_out=None, count=None,
+                                scale=None, dq=None, dk=None, dv=None, dstate=None, ws=None, stream=None):
+    """fs_linear_attn_bwd whose waits give up after ``cycles`` SM cycles (FS_ERR_TIMEOUT in ``ws``)."""
+    return _linear_attn_bwd((_lib or load()).fs_selftest_linear_wait_bwd, "fs_selftest_linear_wait_bwd",
+                            (int(cycles),), q, k, v, decay, dout, state, dstate_out, count, scale, dq, dk, dv,
+                            dstate, ws, stream)
+
+
+def _linear_attn_bwd(fn, where, more, q, k, v, decay, dout, state, dstate_out, count, scale, dq, dk, dv,
+                     dstate, ws, stream):
     dev, Hkv, args = _linear_inputs(q, k, v, decay, count)
     B, H, T, d = q.shape
     dp, ds = _rows(dout, dev, "dout", torch.bfloat16, q.shape)
@@ -1072,8 +1098,8 @@ def fs_linear_attn_bwd(q, k, v, decay, dout, state=None, dstate_out=None, count=
     if ws is None:
         ws = _new(stream, lambda: fs_linear_workspace(B, H, Hkv, T, d, dev, backward=True))
     wp, wn = _scratch(ws, dev)
-    _launch(dev, stream, L.fs_linear_attn_bwd, "fs_linear_attn_bwd", *args,
-            d ** -0.5 if scale is None else float(scale), sp, dp, ds, gp, *ptrs, *strides, tp, wp, wn)
+    _launch(dev, stream, fn, where, *args, d ** -0.5 if scale is None else float(scale), sp, dp, ds, gp,
+            *ptrs, *strides, tp, wp, wn, *more)
     return tuple(grads)
 
 

@@ -52,3 +52,40 @@ def test_sizes_past_32_bits_are_refused(axis):
         fs.fs_linear_attn(x, x, x, decay, out=x, ws=ws)
     with pytest.raises(ValueError):
         fs.fs_linear_attn_bwd(x, x, x, decay, x, dq=x, dk=x, dv=x, ws=ws)
+
+
+@pytest.mark.parametrize("B,H,Hkv,T,d", [(2, 2, 1, 200, 64), (1, 2, 2, 5000, 64), (4, 80, 40, 1500, 64), (2, 4, 2, 3000, 128)])
+def test_waits_that_give_up(B, H, Hkv, T, d):
+    # The limit runs out in other places each time, with copies and products under way; the call ends
+    # with its status, written by the kernels, and the next one is right.  Values that are not finite,
+    # so that the roles that look for them have work, too.
+    q, k, v, dout, decay, S0, G, _ = inputs(B, H, Hkv, T, d, seed=7)
+    for t in (v, k):
+        t[0, 0, T // 2, 3] = float("inf")
+    ws = fs.fs_linear_workspace(B, H, Hkv, T, d, q.device)
+    wb = fs.fs_linear_workspace(B, H, Hkv, T, d, q.device, backward=True)
+    bits = lambda *ts: [t.view(torch.int16) for t in ts]  # noqa: E731
+    form, back = dict(state=S0, ws=ws), dict(state=S0, dstate_out=G, ws=wb)
+    want = bits(fs.fs_linear_attn(q, k, v, decay, **form)), bits(*fs.fs_linear_attn_bwd(q, k, v, decay, dout, **back))
+    fs.fs_check_status(ws), fs.fs_check_status(wb)
+    gave_up = [0, 0]
+    for cycles in (1, 100, 300, 1000, 2000, 4000, 8000, 16000, 32000, 64000, 10 ** 9):
+        for i, (w, call, again) in enumerate((
+                (ws, lambda: bits(fs.fs_selftest_linear_wait(q, k, v, decay, cycles, **form)),
+                 lambda: bits(fs.fs_linear_attn(q, k, v, decay, **form))),
+                (wb, lambda: bits(*fs.fs_selftest_linear_wait_bwd(q, k, v, decay, dout, cycles, **back)),
+                 lambda: bits(*fs.fs_linear_attn_bwd(q, k, v, decay, dout, **back))))):
+            got, status = call(), int(w[:4].view(torch.int32))
+            assert status in (0, fs.FS_ERR_TIMEOUT)
+            gave_up[i] += status != 0
+            if status == 0:
+                assert all(torch.equal(a, b) for a, b in zip(got, want[i]))
+            else:
+                with pytest.raises(fs.FSError):
+                    fs.fs_check_status(w)
+            w[:4].zero_()
+            assert all(torch.equal(a, b) for a, b in zip(again(), want[i]))
+            fs.fs_check_status(w)
+            if cycles == 10 ** 9:
+                assert status == 0
+    assert min(gave_up) > 0

@@ -27,3 +27,11 @@ def test_a_workspace_does_for_smaller_batches_and_lengths(H, Hkv, d, backward):
         assert all(x > 0 for x in row) and row == sorted(row), (T, row)
         assert all(x >= y for x, y in zip(row, last)), (T, row, last)
         last = row
+
+
+@pytest.mark.parametrize("cycles", [0, -1, 4 * 10 ** 9 + 1])
+def test_limits_of_waits_outside(cycles):
+    L, none = fs.load(), [None] * 7
+    assert L.fs_selftest_linear_wait(*none, 1, 1, 1, 32, 64, None, 1.0, None, None, None, None, None, 0, cycles,
+                                     None) == INVALID
+    assert L.fs_selftest_linear_wait_bwd(*none, 1, 1, 1, 32, 64, None, 1.0, *[None] * 12, 0, cycles, None) == INVALID
