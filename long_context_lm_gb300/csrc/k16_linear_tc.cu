@@ -787,11 +787,15 @@ Plan plan_of(int sweeps, int pairs, int T, int d) {
   q.fused = d == 128 || all >= filled_by(sweeps, d) ||
             (all > 152 ? q.chunks < 9 : q.chunks * (230 - all) < 1290);
   if (q.fused) {
-    // Stretches of eight chunks at least: as many as fill the GPU once, if they nearly do (3 x 16 heads
-    // in three stretches 475 us, in six 497), else some three times (80 heads in one stretch
-    // 326 us, in three 313, in five 290, in seven 300).
+    // Stretches of eight chunks at least, as many as fill the GPU once (heads of 128: 32 of 8191 tokens in
+    // four stretches 159 us, in fourteen 163; 64 in two 262, in seven 293, ragged 262 and 239; gradients of
+    // 16 three 241, six 255), and none where blocks of whole heads fill five eighths of it (128 heads of 4096
+    // one 172, three 286; 96 of 8191 321 and 384, ragged 321 and 303; 160 of 4096 one 331, two 372; 256 335
+    // and 489; gradients of 40 one 323, three 482).  Below that one stretch would leave too much empty, and
+    // two pay for a pass more: three times what is resident (80 ragged heads of 8191 one 319, five 292; even
+    // 319 and 347).
     size_t n = all < resident ? resident / all : 1;
-    if (all < 2 * resident && n * all < resident * 7 / 8) n = 3 * resident / all;
+    if (n == 1 && all < resident * 5 / 8) n = 3 * resident / all;
     const size_t most = q.chunks / 8;
     q.splits = (int)(n < most ? n : most < 1 ? 1 : most);
     q.slots = q.splits > 1 ? own * q.splits * matrix : 0;
