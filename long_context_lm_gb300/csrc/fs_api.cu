@@ -1114,6 +1114,11 @@ LinearLayout linear_layout(int batch, int H, int Hkv, int T, int d, bool backwar
   return L;
 }
 
+// Token by token up to FS_LINEAR_STEPS, else in chunks, which cost the same for 2 tokens as for 128
+// (us, token by token and in a chunk, inputs out of the L2): 16 heads of 64, 8 tokens 13 and 16, 16 20 and
+// 16, 24 25 and 16; 64 x 16 of them, 16 tokens 42 and 48, 24 59 and 48; their gradients 95 and 122, 136
+// and 121; 8 x 16 (4) heads of 128, 8 tokens 18 and 24, 16 26 and 23; 64 x 16 (4), 16 tokens 104 and 118, 24
+// 149 and 118.  The sides are even at 10 to 20 tokens, the fewer the heads the earlier.
 int linear_sweeps(const LinearArgs &a, const LinearLayout &L, void *ws, cudaStream_t st) {
   if (a.T <= FS_LINEAR_STEPS) return status_of(launch_linear_recurrent(a, st));
   char *base = static_cast<char *>(ws);

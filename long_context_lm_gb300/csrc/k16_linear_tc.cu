@@ -10,9 +10,13 @@
 // token) and a token's weight in it is one power higher.
 //
 // Precision.  q, k and v are bf16 and go in as they are.  The scores times their
-// powers, and S as a factor, go in as a bf16 high and low part (2^-16 of
-// themselves); the weighted values, of which states are made, in three parts
-// (24 bits).  All sums are fp32; S itself is fp32.
+// powers, and S as a factor, go in as a bf16 high and low part, off by 2^-18 of
+// themselves at most: 2^9 times less than what the rounding of q, k and v to bf16 may
+// have put into the same terms, so that no cancellation shows it before that.  (A third
+// part of the scores wants 64 TMEM columns more, where two blocks of one pass over heads
+// of 64 take all 512; one of S 32 KB of shared memory, where heads of 128 take 217 of 227.)
+// The weighted values, of which states are made, go in as three parts (24 bits), since a
+// state adds up over thousands of chunks.  All sums are fp32; S itself is fp32.
 //
 // Two passes over the chunks, with a small kernel between them:
 //   states  every (sequence, head) is cut into stretches, as many as fill the GPU; a
@@ -467,12 +471,10 @@ __device__ __forceinline__ void look_through(RowShared &s, unsigned char *values
 //             parts in their own TMEM columns, Q S times the row's power in place, the
 //             finished rows by way of the values' place in shared memory (a TMA store: rows
 //             written by their own threads would be 32 places an instruction)
-//   8..       states (D / 16 warps): S from its two parts, split, into shared memory; the
-//             head's tables
+//   8-11      states: S from its two parts, split, into shared memory; the head's tables
 //   last four one for TMA loads (values a chunk ahead), one that issues the products, with
 //             kTurns two that look through values
-// Heads of 64 leave room for two blocks an SM, which fill each other's waits; heads of 128
-// for one.
+// Heads of 64 alone, for which there is room for two blocks an SM that fill each other's waits.
 // kTurns: one of the sweeps borrows its states.  Then warps of their own look through the values
 // (by the states' warps gradients of 4 x 4096 tokens x 16 heads 174 us, so 159); else the states'
 // warps do, where the first pass has seen something (so 65536 tokens x 16 heads 210 us,
@@ -738,23 +740,21 @@ EncodeTiled encode_fn() {
   return fn;
 }
 
-// [batch, heads, T, D] rows in boxes of 128 bytes x `tokens`; an axis of stride 0 (one long, or the
+// [batch, heads, T, D] rows in boxes of 64 elements x `tokens`; an axis of stride 0 (one long, or the
 // same for all) is one long.
-bool make_map(CUtensorMap *map, const void *x, const long long (&s)[3], bool f32, int batch, int heads,
-              int T, int d, int tokens, int *axes) {
+bool make_map(CUtensorMap *map, const void *x, const long long (&s)[3], int batch, int heads, int T, int d,
+              int tokens, int *axes) {
   EncodeTiled fn = encode_fn();
   if (!fn) return false;
-  const cuuint64_t size = f32 ? 4 : 2;
   axes[0] = s[0] != 0;
   axes[1] = s[1] != 0;
   const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)T, (cuuint64_t)(axes[1] ? heads : 1),
                               (cuuint64_t)(axes[0] ? batch : 1)};
-  const cuuint64_t strides[3] = {(cuuint64_t)s[2] * size, (axes[1] ? (cuuint64_t)s[1] : d) * size,
-                                 (axes[0] ? (cuuint64_t)s[0] : d) * size};
-  const cuuint32_t box[4] = {(cuuint32_t)(128 / size), (cuuint32_t)tokens, 1, 1}, estr[4] = {1, 1, 1, 1};
-  return fn(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
-            const_cast<void *>(x), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  const cuuint64_t strides[3] = {(cuuint64_t)s[2] * 2, (cuuint64_t)(axes[1] ? s[1] : d) * 2,
+                                 (cuuint64_t)(axes[0] ? s[0] : d) * 2};
+  const cuuint32_t box[4] = {64, (cuuint32_t)tokens, 1, 1}, estr[4] = {1, 1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(x), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -906,14 +906,15 @@ cudaError_t launch_linear_chunks(const LinearArgs &a, void *ws, int *err, cudaSt
       if (m == n) {
         if (n == 4) return cudaErrorInvalidValue;
         seen[n++] = rows[j];
-        if (!make_map(&maps.in[m], rows[j]->x, rows[j]->s, false, a.batch, a.H / rows[j]->share, a.T, a.d, kC,
+        if (!make_map(&maps.in[m], rows[j]->x, rows[j]->s, a.batch, a.H / rows[j]->share, a.T, a.d, kC,
                       p.axes[m]))
           return cudaErrorInvalidValue;
       }
       p.map[i][j] = m;
     }
-    if (!make_map(&maps.out[i], a.sweep[i].out, a.sweep[i].os, a.sweep[i].out_f32, a.batch, a.H, a.T, a.d, 32,
-                  p.out_axes[i]))
+    // (fp32 parts leave from their threads)
+    if (!a.sweep[i].out_f32 &&
+        !make_map(&maps.out[i], a.sweep[i].out, a.sweep[i].os, a.batch, a.H, a.T, a.d, 32, p.out_axes[i]))
       return cudaErrorInvalidValue;
   }
   return a.d == 64 ? run<64>(p, maps, q, st) : run<128>(p, maps, q, st);
