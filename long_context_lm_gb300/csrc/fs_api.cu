@@ -1052,6 +1052,13 @@ int check_linear(int batch, int H, int Hkv, int T, int d) {
   return FS_OK;
 }
 
+int check_linear_plain(const float *decay, const int32_t *count, float scale) {
+  if (!decay || (reinterpret_cast<uintptr_t>(decay) | reinterpret_cast<uintptr_t>(count)) % 4)
+    return FS_ERR_INVALID_ARG;
+  // (gradients' states are held over the scale)
+  return fabsf(scale) >= 0x1p-64f && fabsf(scale) <= 0x1p64f ? FS_OK : FS_ERR_INVALID_ARG;
+}
+
 // One of the row tensors: 16-byte rows, no negative strides, tokens apart.
 int check_linear_rows(const void *p, const long long (&s)[3], int T) {
   if (!p) return FS_ERR_INVALID_ARG;
@@ -1140,8 +1147,7 @@ int linear_attn(const void *q, const void *k, const void *v, const long long *q_
                 float *state_out, void *out, const long long *out_strides, void *ws, size_t ws_bytes,
                 long long wait_cycles, void *stream) {
   FS_TRY(check_linear(batch, H, Hkv, T, d));
-  // (gradients' states are held over the scale)
-  if (!decay || !(fabsf(scale) >= 0x1p-64f && fabsf(scale) <= 0x1p64f)) return FS_ERR_INVALID_ARG;
+  FS_TRY(check_linear_plain(decay, count, scale));
   long long qs[3], ks[3], vs[3], os[3];
   set_strides(qs, q_strides, batch, H, T, d);
   set_strides(ks, k_strides, batch, Hkv, T, d);
@@ -1186,8 +1192,7 @@ int linear_attn_bwd(const void *q, const void *k, const void *v, const long long
                     const long long *dv_strides, float *dstate, void *ws, size_t ws_bytes,
                     long long wait_cycles, void *stream) {
   FS_TRY(check_linear(batch, H, Hkv, T, d));
-  // (gradients' states are held over the scale)
-  if (!decay || !(fabsf(scale) >= 0x1p-64f && fabsf(scale) <= 0x1p64f)) return FS_ERR_INVALID_ARG;
+  FS_TRY(check_linear_plain(decay, count, scale));
   long long qs[3], ks[3], vs[3], ds[3], gq[3], gk[3], gv[3];
   set_strides(qs, q_strides, batch, H, T, d);
   set_strides(ks, k_strides, batch, Hkv, T, d);

@@ -1,4 +1,5 @@
-"""Workspaces of fs_linear_attn and fs_linear_attn_bwd: alignment and sizes.  Runs without a GPU: every
+"""Workspaces of fs_linear_attn and fs_linear_attn_bwd, their alignment and sizes, and what else may lie off
+its place.  Runs without a GPU: every
 call here is refused."""
 import pytest
 
@@ -35,3 +36,9 @@ def test_limits_of_waits_outside(cycles):
     assert L.fs_selftest_linear_wait(*none, 1, 1, 1, 32, 64, None, 1.0, None, None, None, None, None, 0, cycles,
                                      None) == INVALID
     assert L.fs_selftest_linear_wait_bwd(*none, 1, 1, 1, 32, 64, None, 1.0, *[None] * 12, 0, cycles, None) == INVALID
+
+
+@pytest.mark.parametrize("kw", [dict(decay=258), dict(count=4097), dict(decay=257, T=4), dict(count=4098, T=4)])
+@pytest.mark.parametrize("call", [linear, linear_bwd])
+def test_numbers_off_their_size(call, kw):
+    assert call(**kw) == INVALID
