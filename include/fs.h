@@ -742,6 +742,8 @@ int fs_selftest_linear_wait_bwd(const void *q, const void *k, const void *v,
  * strides (in place).  Another output at an input's address, or two outputs at one:
  * FS_ERR_INVALID_ARG; other overlaps give undefined results.  Computed in fp32,
  * y from z before its rounding; rounded once.  Squares and their sums are to fit fp32.
+ * Gates may be of any size; where z is bf16 one below -87, whose factor is below
+ * 2^-126, counts as 0.
  * D <= 16384 (else FS_ERR_UNSUPPORTED), D a multiple of groups, eps >= 0.  One kernel. */
 int fs_block_norm(const void *x, long long x_stride, int dtype, const void *gate,
                   long long gate_stride, const void *residual, long long residual_stride,
