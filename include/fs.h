@@ -667,7 +667,7 @@ int fs_selftest_tree_wait(const void *q, const fs_cache *cache,
  * Products of bf16 numbers are summed in fp32; the factors of the tensor cores'
  * products that are not bf16 numbers themselves (scores, weighted values, states)
  * go in as sums of two or three bf16 parts, 17 bits or more for outputs and 24
- * for states.  An element of v that is not finite makes its
+ * for states (of terms above 2^-109).  An element of v that is not finite makes its
  * column of that token's and all later outputs, and of the state, NaN or
  * infinite; one of k or q reaches what the definition says.
  *   ws            device workspace of fs_linear_workspace_bytes() bytes, 16-byte aligned
