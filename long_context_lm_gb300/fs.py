@@ -39,8 +39,8 @@ SYMBOLS = ["fs_default_params", "fs_status_string", "fs_last_cuda_error", "fs_wo
            "fs_rope_make_plan", "fs_rope", "fs_cache_row_bytes", "fs_cache_append",
            "fs_cache_read", "fs_cache_accept", "fs_tree_workspace_bytes", "fs_tree_attn",
            "fs_selftest_tree_wait", "fs_linear_workspace_bytes", "fs_linear_attn",
-           "fs_linear_attn_bwd", "fs_selftest_linear_wait", "fs_selftest_linear_wait_bwd", "fs_block_norm", "fs_block_norm_workspace_bytes",
-           "fs_block_norm_bwd"]
+           "fs_linear_attn_bwd", "fs_selftest_linear_wait", "fs_selftest_linear_wait_bwd",
+           "fs_block_norm", "fs_block_norm_workspace_bytes", "fs_block_norm_bwd"]
 FS_LINEAR_STEPS = 16
 FS_ROPE_LAYOUTS = {"half": 0, "pairs": 1}
 FS_ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "ramp": 3}
